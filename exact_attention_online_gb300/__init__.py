@@ -35,7 +35,9 @@ __all__ = ["build", "lib", "LIB_PATH", "EXPORTS", "FAError", "fa_fwd", "fa_fwd_p
            "fa_fwd_decode_workspace_size", "fa_fwd_decode", "attention_decode",
            "fa_fwd_train", "fa_bwd_train", "fa_bwd_preprocess_train", "fa_exp2_check",
            "fa_ex2_rate",
-           "fa_fwd_window_train", "fa_bwd_window_train"]
+           "fa_fwd_window_train", "fa_bwd_window_train",
+           "fa_kv_append", "fa_kv_append_varlen", "fa_kv_gather", "fa_kv_gather_varlen",
+           "fa_fwd_decode_paged_workspace_size", "fa_fwd_decode_paged", "attention_decode_paged"]
 
 
 class FAError(RuntimeError):
@@ -482,6 +484,131 @@ def attention_decode(q, k, v, causal: bool = True, scale: float | None = None, s
     o = torch.empty_like(q)
     lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
     fa_fwd_decode(q, k, v, o, lse, work, causal, scale, stream)
+    return o, lse
+
+
+# ------------------------------------------------------------- paged cache
+def _cache(k_pages, v_pages, block_table, kv_scales, B):
+    """Pointers and sizes of a paged cache: k_pages, v_pages [n_pages, Hkv, page_size, d]
+    (bf16; torch.float8_e4m3fn with kv_scales fp32 [n_pages, Hkv, 2, page_size]),
+    block_table int32 [B, max_pages]."""
+    import torch
+    if k_pages.dim() != 4:
+        raise ValueError("k_pages must be 4-D [n_pages, Hkv, page_size, d]")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be 2-D [B, max_pages]")
+    n_pages, Hkv, ps, d = k_pages.shape
+    max_pages = block_table.shape[1]
+    if kv_scales is None:
+        dtype, sp = torch.bfloat16, None
+    else:
+        dtype, sp = torch.float8_e4m3fn, _f32(kv_scales, "kv_scales", (n_pages, Hkv, 2, ps))
+    return (_ptr(k_pages, "k_pages", dtype, None),
+            _ptr(v_pages, "v_pages", dtype, (n_pages, Hkv, ps, d)), sp,
+            _i32(block_table, "block_table", (B, max_pages)), n_pages, Hkv, ps, max_pages, d)
+
+
+def _rows_shape(k, k_pages, layout):
+    """k as [B, Hkv, N, d] or packed [Hkv, total, d], agreeing with the pages."""
+    if k_pages.dim() != 4:
+        raise ValueError("k_pages must be 4-D [n_pages, Hkv, page_size, d]")
+    if k.dim() != len(layout) or k.shape[-3] != k_pages.shape[1] or k.shape[-1] != k_pages.shape[3]:
+        raise ValueError(f"k has shape {tuple(k.shape)}, expected [{', '.join(layout)}] of "
+                         f"k_pages {tuple(k_pages.shape)}")
+    return tuple(k.shape)
+
+
+def fa_kv_append(k, v, k_pages, v_pages, block_table, starts, counts, kv_scales=None,
+                 stream=None) -> None:
+    """Rows i < counts[b] of k, v [B, Hkv, N, d] to positions starts[b] + i of sequence b;
+    quantised to e4m3 when kv_scales is given.  starts, counts: int32 [B]."""
+    B = block_table.shape[0]
+    shape = _rows_shape(k, k_pages, ("B", "Hkv", "N", "d"))
+    kp, vp, sp, tp, P, Hkv, ps, mp, d = _cache(k_pages, v_pages, block_table, kv_scales, B)
+    _check(lib().fa_kv_append(_bf16(k, "k", (B,) + shape[1:]), _bf16(v, "v", shape), kp, vp, sp,
+                              tp, _i32(starts, "starts", (B,)), _i32(counts, "counts", (B,)),
+                              B, Hkv, shape[2], P, ps, mp, d, _stream(stream)), "fa_kv_append")
+
+
+def fa_kv_append_varlen(k, v, k_pages, v_pages, block_table, starts, cu_seqlens, max_seqlen: int,
+                        kv_scales=None, stream=None) -> None:
+    """fa_kv_append from a packed batch: k, v [Hkv, total, d], cu_seqlens int32 [B + 1]."""
+    B = block_table.shape[0]
+    shape = _rows_shape(k, k_pages, ("Hkv", "total", "d"))
+    kp, vp, sp, tp, P, Hkv, ps, mp, d = _cache(k_pages, v_pages, block_table, kv_scales, B)
+    _check(lib().fa_kv_append_varlen(_bf16(k, "k"), _bf16(v, "v", shape), kp, vp, sp, tp,
+                                     _i32(starts, "starts", (B,)),
+                                     _i32(cu_seqlens, "cu_seqlens", (B + 1,)), B, int(max_seqlen),
+                                     shape[1], Hkv, P, ps, mp, d, _stream(stream)),
+           "fa_kv_append_varlen")
+
+
+def fa_kv_gather(k_pages, v_pages, k, v, block_table, starts, counts, kv_scales=None,
+                 stream=None) -> None:
+    """Positions starts[b] .. starts[b] + counts[b] - 1 of sequence b into rows 0 ..
+    counts[b] - 1 of bf16 k, v [B, Hkv, N, d]; the rows behind stay as they are."""
+    B = block_table.shape[0]
+    shape = _rows_shape(k, k_pages, ("B", "Hkv", "N", "d"))
+    kp, vp, sp, tp, P, Hkv, ps, mp, d = _cache(k_pages, v_pages, block_table, kv_scales, B)
+    _check(lib().fa_kv_gather(kp, vp, sp, _bf16(k, "k", (B,) + shape[1:]), _bf16(v, "v", shape),
+                              tp, _i32(starts, "starts", (B,)), _i32(counts, "counts", (B,)),
+                              B, Hkv, shape[2], P, ps, mp, d, _stream(stream)), "fa_kv_gather")
+
+
+def fa_kv_gather_varlen(k_pages, v_pages, k, v, block_table, starts, cu_seqlens, max_seqlen: int,
+                        kv_scales=None, stream=None) -> None:
+    """fa_kv_gather into a packed batch: k, v [Hkv, total, d], cu_seqlens int32 [B + 1]."""
+    B = block_table.shape[0]
+    shape = _rows_shape(k, k_pages, ("Hkv", "total", "d"))
+    kp, vp, sp, tp, P, Hkv, ps, mp, d = _cache(k_pages, v_pages, block_table, kv_scales, B)
+    _check(lib().fa_kv_gather_varlen(kp, vp, sp, _bf16(k, "k"), _bf16(v, "v", shape), tp,
+                                     _i32(starts, "starts", (B,)),
+                                     _i32(cu_seqlens, "cu_seqlens", (B + 1,)), B, int(max_seqlen),
+                                     shape[1], Hkv, P, ps, mp, d, _stream(stream)),
+           "fa_kv_gather_varlen")
+
+
+def fa_fwd_decode_paged_workspace_size(B: int, H: int, Hkv: int, Nq: int, d: int) -> int:
+    return int(lib().fa_fwd_decode_paged_workspace_size(B, H, Hkv, Nq, d))
+
+
+def fa_fwd_decode_paged(q, k_pages, v_pages, o, lse, block_table, seqlens, workspace,
+                        causal: bool, scale: float, kv_scales=None, stream=None) -> None:
+    """q, o: bf16 [B, H, Nq, d]; lse: fp32 [B, H, Nq]; seqlens: int32 [B], the cached
+    positions of each sequence, its Nq new ones included."""
+    B, H, Nq, d = _dims_of(q, "q")
+    kp, vp, sp, tp, P, Hkv, ps, mp, dk = _cache(k_pages, v_pages, block_table, kv_scales, B)
+    if dk != d:
+        raise ValueError(f"q {tuple(q.shape)} and k_pages {tuple(k_pages.shape)} disagree")
+    wp, wb = _ws(workspace)
+    _check(lib().fa_fwd_decode_paged(_bf16(q, "q"), kp, vp, sp, _bf16(o, "o", (B, H, Nq, d)),
+                                     _f32(lse, "lse", (B, H, Nq)), tp,
+                                     _i32(seqlens, "seqlens", (B,)), wp, wb, B, H, Hkv, Nq, P, ps,
+                                     mp, d, int(bool(causal)), float(scale), _stream(stream)),
+           "fa_fwd_decode_paged")
+
+
+def attention_decode_paged(q, k_pages, v_pages, block_table, seqlens, causal: bool = True,
+                           scale: float | None = None, kv_scales=None, workspace=None,
+                           stream=None):
+    """Decoding over a paged cache; allocates the output and LSE, and the workspace unless it
+    is given; returns (o, lse)."""
+    import torch
+    B, H, Nq, d = _dims_of(q, "q")
+    scale = d ** -0.5 if scale is None else scale
+    o = torch.empty_like(q, memory_format=torch.contiguous_format)
+    lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+    if workspace is None:
+        n = fa_fwd_decode_paged_workspace_size(B, H, k_pages.shape[1], Nq, d)
+        if n == 0:
+            raise FAError(FA_ERR_UNSUPPORTED, "fa_fwd_decode_paged_workspace_size")
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    fa_fwd_decode_paged(q, k_pages, v_pages, o, lse, block_table, seqlens, workspace, causal,
+                        scale, kv_scales, stream)
+    if stream is not None and hasattr(stream, "cuda_stream"):
+        # the allocator must not hand these out again before the call's stream has used them
+        for t in (o, lse, workspace):
+            t.record_stream(stream)
     return o, lse
 
 

@@ -20,7 +20,7 @@ OBJ_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(OUT_DIR, "libfa.so")
 
 SOURCES = ["api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_noalloc.cu", "fa_fp8.cu", "fa_decode.cu",
-           "fa_diag.cu"]
+           "fa_diag.cu", "fa_kvcache.cu", "fa_paged.cu"]
 HEADERS = ["sm103_ptx.cuh", "fa_internal.h", "exp2_poly.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
@@ -156,6 +156,18 @@ def _bind(L: ctypes.CDLL) -> ctypes.CDLL:
     L.fa_fwd_decode_workspace_size.restype = sz
     L.fa_fwd_decode.argtypes = [vp, vp, vp, vp, vp, vp, sz, i, i, i, i, i, i, i, f, vp]
     L.fa_fwd_decode.restype = i
+    L.fa_kv_append.argtypes = [vp] * 8 + [i] * 7 + [vp]
+    L.fa_kv_append.restype = i
+    L.fa_kv_append_varlen.argtypes = [vp] * 8 + [i] * 8 + [vp]
+    L.fa_kv_append_varlen.restype = i
+    L.fa_kv_gather.argtypes = [vp] * 8 + [i] * 7 + [vp]
+    L.fa_kv_gather.restype = i
+    L.fa_kv_gather_varlen.argtypes = [vp] * 8 + [i] * 8 + [vp]
+    L.fa_kv_gather_varlen.restype = i
+    L.fa_fwd_decode_paged_workspace_size.argtypes = [i, i, i, i, i]
+    L.fa_fwd_decode_paged_workspace_size.restype = sz
+    L.fa_fwd_decode_paged.argtypes = [vp] * 9 + [sz] + [i] * 9 + [f, vp]
+    L.fa_fwd_decode_paged.restype = i
     return L
 
 
@@ -183,4 +195,6 @@ EXPORTS = ["fa_fwd", "fa_fwd_precise", "fa_bwd_workspace_size", "fa_bwd", "fa_bw
            "fa_bwd_varlen", "fa_fwd_train", "fa_fwd_train_precise", "fa_bwd_train",
            "fa_bwd_train_precise", "fa_bwd_preprocess_train", "fa_bwd_preprocess_train_precise", "fa_exp2_check",
            "fa_ex2_rate",
-           "fa_fwd_window_train", "fa_bwd_window_train"]
+           "fa_fwd_window_train", "fa_bwd_window_train",
+           "fa_kv_append", "fa_kv_append_varlen", "fa_kv_gather", "fa_kv_gather_varlen",
+           "fa_fwd_decode_paged_workspace_size", "fa_fwd_decode_paged"]

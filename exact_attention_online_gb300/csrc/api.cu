@@ -663,4 +663,130 @@ fa_status fa_fwd_decode(const void* q, const void* k, const void* v, void* o, fl
                                        (cudaStream_t)stream));
 }
 
+// Paged cache: the shape of the pool and the table, then the pointers.
+static fa_status check_paged_shape(int B, int Hkv, long long n_pages, int page_size,
+                                   int max_pages, int d) {
+    if (B < 1 || Hkv < 1 || n_pages < 1 || page_size < 1 || max_pages < 1 || d < 1)
+        return FA_ERR_INVALID_ARG;
+    if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+    if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1)))
+        return FA_ERR_UNSUPPORTED;
+    const long long keys = (long long)max_pages * page_size;
+    if (keys >= (1LL << 30) || n_pages * Hkv >= (1LL << 31) ||
+        (long long)B * Hkv >= (1LL << 31) / (keys / 128 + 1))
+        return FA_ERR_UNSUPPORTED;
+    return FA_OK;
+}
+
+static fa_status check_ints(const int* p) {
+    if (!p) return FA_ERR_INVALID_ARG;
+    return reinterpret_cast<uintptr_t>(p) % alignof(int) ? FA_ERR_ALIGNMENT : FA_OK;
+}
+
+static fa_status check_scales(const float* p) {   // null: a bf16 cache
+    return p ? check_ptr(p) : FA_OK;
+}
+
+static PagedCache paged_cache(const void* k_pages, const void* v_pages, const float* kv_scales,
+                              const int* block_table, int Hkv, int n_pages, int page_size,
+                              int max_pages, int d) {
+    int shift = 0;
+    while ((1 << shift) < page_size) ++shift;
+    return PagedCache{k_pages, v_pages, kv_scales, block_table, Hkv, n_pages, shift, max_pages, d};
+}
+
+static fa_status check_paged_decode(int B, int H, int Hkv, int Nq, int n_pages, int page_size,
+                                    int max_pages, int d) {
+    if (H < 1 || Nq < 1 || Hkv < 1 || H % Hkv != 0) return FA_ERR_INVALID_ARG;
+    const fa_status st = check_paged_shape(B, Hkv, n_pages, page_size, max_pages, d);
+    if (st != FA_OK) return st;
+    if ((long long)(H / Hkv) * Nq > kPagedMaxRows) return FA_ERR_UNSUPPORTED;
+    if ((long long)B * H * Nq * d >= (1LL << 31)) return FA_ERR_UNSUPPORTED;
+    return FA_OK;
+}
+
+size_t fa_fwd_decode_paged_workspace_size(int B, int H, int Hkv, int Nq, int d) {
+    if (check_paged_decode(B, H, Hkv, Nq, 1, 16, 1, d) != FA_OK) return 0;
+    return paged_workspace_bytes(B, Hkv, H / Hkv * Nq, d);
+}
+
+fa_status fa_fwd_decode_paged(const void* q, const void* k_pages, const void* v_pages,
+                              const float* kv_scales, void* o, float* lse, const int* block_table,
+                              const int* seqlens, void* workspace, size_t workspace_bytes, int B,
+                              int H, int Hkv, int Nq, int n_pages, int page_size, int max_pages,
+                              int d, int causal, float scale, fa_stream_t stream) {
+    fa_status st = first_error(
+        {check_paged_decode(B, H, Hkv, Nq, n_pages, page_size, max_pages, d), check_scale(scale),
+         check_ptr(q), check_ptr(k_pages), check_ptr(v_pages), check_scales(kv_scales),
+         check_ptr(o), check_ptr(lse), check_ints(block_table), check_ints(seqlens)});
+    if (st != FA_OK) return st;
+    if (!workspace || workspace_bytes < paged_workspace_bytes(B, Hkv, H / Hkv * Nq, d))
+        return FA_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return FA_ERR_ALIGNMENT;
+    int dev;
+    if ((st = device_ready(&dev)) != FA_OK) return st;
+    return from_cuda(launch_fwd_decode_paged(
+        paged_cache(k_pages, v_pages, kv_scales, block_table, Hkv, n_pages, page_size, max_pages,
+                    d),
+        q, o, lse, seqlens, workspace, B, H, Nq, causal ? 1 : 0, scale, g_status_ptr[dev],
+        (cudaStream_t)stream));
+}
+
+// Shared body of the four entry points that move rows into or out of the
+// pages; counts is counts [B], or with packed cu_seqlens [B + 1].
+static fa_status kv_move(const void* k, const void* v, const void* k_pages, const void* v_pages,
+                         const float* kv_scales, const int* block_table, const int* starts,
+                         const int* counts, int B, int Hkv, int N, int total, bool packed,
+                         int n_pages, int page_size, int max_pages, int d, bool append,
+                         fa_stream_t stream) {
+    if (N < 1 || (packed && total < 1)) return FA_ERR_INVALID_ARG;
+    fa_status st = first_error({check_paged_shape(B, Hkv, n_pages, page_size, max_pages, d),
+                                check_ptr(k), check_ptr(v), check_ptr(k_pages), check_ptr(v_pages),
+                                check_scales(kv_scales), check_ints(block_table),
+                                check_ints(starts), check_ints(counts)});
+    if (st != FA_OK) return st;
+    if ((long long)B * Hkv >= (1LL << 31) / N) return FA_ERR_UNSUPPORTED;
+    int dev;
+    if ((st = device_ready(&dev)) != FA_OK) return st;
+    return from_cuda(launch_kv_move(
+        paged_cache(k_pages, v_pages, kv_scales, block_table, Hkv, n_pages, page_size, max_pages,
+                    d),
+        const_cast<void*>(k), const_cast<void*>(v), starts, counts, B, N, total, packed, append,
+        (cudaStream_t)stream));
+}
+
+fa_status fa_kv_append(const void* k, const void* v, void* k_pages, void* v_pages,
+                       float* kv_scales, const int* block_table, const int* starts,
+                       const int* counts, int B, int Hkv, int N, int n_pages, int page_size,
+                       int max_pages, int d, fa_stream_t stream) {
+    return kv_move(k, v, k_pages, v_pages, kv_scales, block_table, starts, counts, B, Hkv, N, 0,
+                   false, n_pages, page_size, max_pages, d, true, stream);
+}
+
+fa_status fa_kv_append_varlen(const void* k, const void* v, void* k_pages, void* v_pages,
+                              float* kv_scales, const int* block_table, const int* starts,
+                              const int* cu_seqlens, int B, int max_seqlen, int total, int Hkv,
+                              int n_pages, int page_size, int max_pages, int d,
+                              fa_stream_t stream) {
+    return kv_move(k, v, k_pages, v_pages, kv_scales, block_table, starts, cu_seqlens, B, Hkv,
+                   max_seqlen, total, true, n_pages, page_size, max_pages, d, true, stream);
+}
+
+fa_status fa_kv_gather(const void* k_pages, const void* v_pages, const float* kv_scales, void* k,
+                       void* v, const int* block_table, const int* starts, const int* counts,
+                       int B, int Hkv, int N, int n_pages, int page_size, int max_pages, int d,
+                       fa_stream_t stream) {
+    return kv_move(k, v, k_pages, v_pages, kv_scales, block_table, starts, counts, B, Hkv, N, 0,
+                   false, n_pages, page_size, max_pages, d, false, stream);
+}
+
+fa_status fa_kv_gather_varlen(const void* k_pages, const void* v_pages, const float* kv_scales,
+                              void* k, void* v, const int* block_table, const int* starts,
+                              const int* cu_seqlens, int B, int max_seqlen, int total, int Hkv,
+                              int n_pages, int page_size, int max_pages, int d,
+                              fa_stream_t stream) {
+    return kv_move(k, v, k_pages, v_pages, kv_scales, block_table, starts, cu_seqlens, B, Hkv,
+                   max_seqlen, total, true, n_pages, page_size, max_pages, d, false, stream);
+}
+
 }  // extern "C"

@@ -167,6 +167,30 @@ cudaError_t launch_fwd_decode(const void* q, const void* k, const void* v, void*
                               cudaStream_t stream);
 constexpr int kDecodeMaxRows = 16;   // (H / Hkv) * Nq rows per kv group
 
+// A paged key/value cache (fa_kvcache.cu, fa_paged.cu): pools [n_pages][Hkv]
+// [page_size][d], bf16 when scales is null, else e4m3 with scales fp32
+// [n_pages][Hkv][2][page_size]; table [B][max_pages] names each sequence's
+// pages.  page_size = 2^ps_shift.
+struct PagedCache {
+    const void* k_pages;
+    const void* v_pages;
+    const float* scales;
+    const int* table;
+    int Hkv, n_pages, ps_shift, max_pages, d;
+};
+constexpr int kPagedMaxRows = 32;    // (H / Hkv) * Nq rows per kv head
+constexpr int kPagedMaxCtas = 304;   // most CTAs of the split kernel: two an SM
+// Rows into the pages (append) or out of them; counts: rows per sequence
+// [B], or with packed the B + 1 row offsets.
+cudaError_t launch_kv_move(const PagedCache& c, void* k, void* v, const int* starts,
+                           const int* counts, int B, int N, int total, bool packed, bool append,
+                           cudaStream_t stream);
+size_t paged_workspace_bytes(int B, int Hkv, int R, int d);
+cudaError_t launch_fwd_decode_paged(const PagedCache& c, const void* q, void* o, float* lse,
+                                    const int* seqlens, void* workspace, int B, int H, int Nq,
+                                    int causal, float scale, DeviceStatus* status,
+                                    cudaStream_t stream);
+
 // Number of SMs of the current device (cached per device).
 int device_sm_count();
 

@@ -447,6 +447,17 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float
     return pack_e4m3x2(a, b) | (pack_e4m3x2(c, d) << 16);
 }
 
+// Four e4m3 codes (element i in byte i) as fp32 values (exact).
+__device__ __forceinline__ void unpack_e4m3x4(uint32_t w, float (&x)[4]) {
+    uint32_t lo, hi;
+    asm("{.reg .b16 l, h;\n\t"
+        "mov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, h;}" : "=r"(lo), "=r"(hi) : "r"(w));
+    unpack_f16x2(lo, x[0], x[1]);
+    unpack_f16x2(hi, x[2], x[3]);
+}
+
 // Paired fp32 arithmetic (one instruction for two lanes of a 64-bit register
 // pair) and the three-input max.
 __device__ __forceinline__ uint64_t f2(float lo, float hi) {

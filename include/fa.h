@@ -423,6 +423,112 @@ FA_API fa_status fa_fwd_decode(const void* q, const void* k, const void* v, void
                                fa_stream_t stream);
 
 /*
+ * Paged key/value cache (the cache of a server that decodes many sequences
+ * of different lengths; the pages describe decoding against a long cache, not
+ * its storage, so pages, block table and scales are this library's).
+ *
+ * The pool: k_pages, v_pages [n_pages][Hkv][page_size][d], both bf16
+ * (kv_scales NULL), or both e4m3 codes with kv_scales fp32
+ * [n_pages][Hkv][2][page_size], K's scales before V's: code c with scale s
+ * stands for c * s.  Position x of sequence b is row x % page_size of page
+ * block_table[b][x / page_size] (DEVICE int32 [B][max_pages]).  One page may
+ * stand in several tables (a shared prefix).  d in {64, 128}; page_size a
+ * power of two from 16 to 256; max_pages * page_size < 2^30; n_pages * Hkv <
+ * 2^31 (the pool itself may be larger than 2^31 elements).  FA_ERR_UNSUPPORTED
+ * past these.  Pointers to floats and rows 16-byte aligned, to ints 4-byte.
+ *
+ * Table entries and lengths are read by the kernels.  Entries outside
+ * [0, n_pages) that a call reaches give unspecified results (fa_fwd_decode_paged)
+ * or rows that are not moved (append, gather), and lengths are clamped to the
+ * table: whatever they hold, no access leaves the tensors.  Entries past a
+ * sequence's last page are not read.
+ */
+
+/*
+ * Writes new K and V rows into the pages: k, v bf16 [B][Hkv][N][d], row i of
+ * sequence b to position starts[b] + i for i < counts[b] (rows from counts[b]
+ * on are padding and are not written; a prompt batch padded to N has starts 0,
+ * a decoding step N = 1, starts = the lengths so far, counts 1, or 0 for an
+ * empty slot of the batch).  starts, counts: DEVICE int32 [B].  bf16 pages
+ * take the rows as they are.  For e4m3 pages each row of d values is
+ * quantised: amax = max |x|, scale = amax / 448, code = e4m3(x * (448 / amax)),
+ * both divisions in fp32, round to nearest even (scale 0 and codes 0 for a
+ * row of zeros; a nonzero amax below 2^-100 counts as 2^-100; a NaN stays a
+ * NaN, and a row with an infinity reads back as NaN).  Two rows for one place
+ * in one call leave either of them there.  Positions past the table are not
+ * written.  Errors as fa_fwd(), FA_ERR_UNSUPPORTED for B * Hkv * N >= 2^31.
+ * Asynchronous on `stream`; one launch.
+ */
+FA_API fa_status fa_kv_append(const void* k, const void* v, void* k_pages, void* v_pages,
+                              float* kv_scales, const int* block_table, const int* starts,
+                              const int* counts, int B, int Hkv, int N, int n_pages,
+                              int page_size, int max_pages, int d, fa_stream_t stream);
+
+/*
+ * The same from a packed batch (the layout of fa_fwd_varlen()): k, v bf16
+ * [Hkv][total][d], sequence b at rows cu_seqlens[b] .. cu_seqlens[b+1] - 1, its
+ * first row to position starts[b]; no sequence longer than max_seqlen (rows
+ * past it are not moved).
+ */
+FA_API fa_status fa_kv_append_varlen(const void* k, const void* v, void* k_pages, void* v_pages,
+                                     float* kv_scales, const int* block_table, const int* starts,
+                                     const int* cu_seqlens, int B, int max_seqlen, int total,
+                                     int Hkv, int n_pages, int page_size, int max_pages, int d,
+                                     fa_stream_t stream);
+
+/*
+ * Reads cached rows back: positions starts[b] .. starts[b] + counts[b] - 1 of
+ * sequence b into rows 0 .. counts[b] - 1 of bf16 k, v [B][Hkv][N][d] (at most
+ * N of them; the rows behind are left as they are).  e4m3 pages are
+ * dequantised: bf16(code * scale), the product in fp32.  Hands a cached prefix
+ * to the entry points that take contiguous K and V.  Errors and launches as
+ * fa_kv_append().
+ */
+FA_API fa_status fa_kv_gather(const void* k_pages, const void* v_pages, const float* kv_scales,
+                              void* k, void* v, const int* block_table, const int* starts,
+                              const int* counts, int B, int Hkv, int N, int n_pages,
+                              int page_size, int max_pages, int d, fa_stream_t stream);
+
+/* The same into a packed batch, bf16 k, v [Hkv][total][d]. */
+FA_API fa_status fa_kv_gather_varlen(const void* k_pages, const void* v_pages,
+                                     const float* kv_scales, void* k, void* v,
+                                     const int* block_table, const int* starts,
+                                     const int* cu_seqlens, int B, int max_seqlen, int total,
+                                     int Hkv, int n_pages, int page_size, int max_pages, int d,
+                                     fa_stream_t stream);
+
+/*
+ * Decoding attention over a paged cache: Nq new query rows of each sequence
+ * against its first seqlens[b] cached positions (DEVICE int32 [B]; the new
+ * tokens' own rows included, so append them first).  q, o bf16 [B][H][Nq][d],
+ * lse fp32 [B][H][Nq] (natural log).  The queries are the last Nq positions:
+ * with causal != 0 query row r sees positions j <= r + seqlens[b] - Nq, else
+ * every position below seqlens[b].  A row that sees nothing (an empty slot,
+ * seqlens[b] = 0; the first rows when seqlens[b] < Nq) gets O = 0 and LSE =
+ * -infinity.  Cache rows at positions >= seqlens[b] may hold anything.
+ * (H / Hkv) * Nq <= 32 (FA_ERR_UNSUPPORTED otherwise).
+ *
+ * The scores and P V run on the tensor core with fp32 accumulation.  bf16
+ * pages: P is rounded to bf16.  e4m3 pages: q and P enter as the sum of two
+ * e4m3 terms (8 significant bits, those of bf16), so that the codes are
+ * multiplied as they are and only the scales are applied in fp32.
+ *
+ * workspace: caller-owned device memory of
+ * fa_fwd_decode_paged_workspace_size() bytes, 256-byte aligned, contents on
+ * entry of no matter; calls that may overlap on the GPU (other streams, other
+ * graphs) need one each.  The result does not depend on the order in which
+ * the CTAs run: it is the same bit for bit on every call with the same inputs.
+ * Asynchronous on `stream`.
+ */
+FA_API size_t fa_fwd_decode_paged_workspace_size(int B, int H, int Hkv, int Nq, int d);
+FA_API fa_status fa_fwd_decode_paged(const void* q, const void* k_pages, const void* v_pages,
+                                     const float* kv_scales, void* o, float* lse,
+                                     const int* block_table, const int* seqlens, void* workspace,
+                                     size_t workspace_bytes, int B, int H, int Hkv, int Nq,
+                                     int n_pages, int page_size, int max_pages, int d, int causal,
+                                     float scale, fa_stream_t stream);
+
+/*
  * Synchronizes `stream`, then reads and clears the device status word of the
  * current device: FA_OK, or the first error a kernel recorded (for example
  * FA_ERR_TIMEOUT when a bounded wait ran out).  Returns FA_ERR_CUDA if the
