@@ -169,6 +169,23 @@ bool make_tmap_u8_3d(CUtensorMap* map, const void* base, int inner, int rows, in
     return r == CUDA_SUCCESS;
 }
 
+bool make_tmap_pages(CUtensorMap* map, const void* base, bool f8, int d, int rows,
+                     long long outer, int box_rows) {
+    if (!load_encode()) return false;
+    const int row_bytes = f8 ? d : 2 * d;
+    const int box_bytes = row_bytes < 128 ? row_bytes : 128;
+    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)rows, (cuuint64_t)outer};
+    cuuint64_t strides[2] = {(cuuint64_t)row_bytes, (cuuint64_t)row_bytes * (cuuint64_t)rows};
+    cuuint32_t box[3] = {(cuuint32_t)(f8 ? box_bytes : box_bytes / 2), (cuuint32_t)box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = g_encode(map, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                          3, const_cast<void*>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 size_t bwd_workspace_bytes(const Shape& s) {
     const size_t rows = (size_t)s.B * s.H * padded_rows(s.N);
     return align256(rows * kExtCols * 2) * 2 + align256(rows * (size_t)s.d * 4) + align256(4);

@@ -141,6 +141,12 @@ bool make_tmap_f32_2d(CUtensorMap* map, const void* base, int inner, long long r
 // 128-byte swizzle (inner and rows multiples of 128).
 bool make_tmap_u8_3d(CUtensorMap* map, const void* base, int inner, int rows, int outer);
 
+// 3-D map over a pool of cache pages [outer = page * Hkv + g][rows][d], bf16 or
+// one-byte codes, boxes of box_rows rows and 128 bytes (64 for one-byte rows of
+// 64), swizzled by that width.
+bool make_tmap_pages(CUtensorMap* map, const void* base, bool f8, int d, int rows,
+                     long long outer, int box_rows);
+
 // FP8 buffer: e4m3 codes of V transposed [B*Hkv][d][Np], then fp32 block
 // scales of V [B*Hkv][Np/128] and the largest V scale of each kv head
 // [B*Hkv]; each region 256-byte aligned.

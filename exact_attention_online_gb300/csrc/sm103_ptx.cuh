@@ -224,9 +224,10 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool a_mn, bo
 }
 
 // Instruction descriptor for kind::f8f6f4 with e4m3 A and B (type code 0 in
-// bits 7-9 and 10-12), fp32 D, both operands K-major.
-__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
-    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+// bits 7-9 and 10-12), fp32 D, B K-major, A K-major unless a_mn.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, bool a_mn = false) {
+    return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((uint32_t)(N >> 3) << 17) |
+           ((uint32_t)(M >> 4) << 24);
 }
 
 // Shared-memory matrix descriptor, 128-byte swizzle.
@@ -240,6 +241,11 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr, uint32_t lbo, ui
     d |= (uint64_t)1 << 46;
     d |= (uint64_t)2 << 61;
     return d;
+}
+
+// The same for 64-byte swizzle (layout type 4): rows of 64 bytes, 8-row groups of 512.
+__device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+    return (sdesc_sw128(saddr, lbo, sbo) & ~((uint64_t)7 << 61)) | ((uint64_t)4 << 61);
 }
 
 // Shared-memory matrix descriptor, no swizzle (layout type 0): 8-row x
@@ -383,6 +389,27 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
         FA_I32(r)
         : "memory");
 }
+// 16 columns into r[at .. at + 15]; wait with tmem_ld_fence before use.
+template <int N>
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[N], int at) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
+        "%10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[at]), "=r"(r[at + 1]), "=r"(r[at + 2]), "=r"(r[at + 3]), "=r"(r[at + 4]),
+          "=r"(r[at + 5]), "=r"(r[at + 6]), "=r"(r[at + 7]), "=r"(r[at + 8]), "=r"(r[at + 9]),
+          "=r"(r[at + 10]), "=r"(r[at + 11]), "=r"(r[at + 12]), "=r"(r[at + 13]),
+          "=r"(r[at + 14]), "=r"(r[at + 15])
+        : "r"(taddr));
+}
+// N columns (a multiple of 16), complete on return.
+template <int N>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[N]) {
+#pragma unroll
+    for (int c = 0; c < N; c += 16) tmem_ld16(taddr + c, r, c);
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int c = 0; c < N; ++c) asm volatile("" : "+r"(r[c]) : : "memory");
+}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, "
@@ -492,6 +519,15 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
+}
+
+// Programmatic dependent launch: let the next kernel's blocks come in / wait
+// until the kernel before has finished and its writes are visible.
+__device__ __forceinline__ void pdl_launch_dependents() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void pdl_wait() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 __device__ __forceinline__ float ex2(float x) {
