@@ -55,13 +55,24 @@ def _check(status: int, where: str) -> None:
         raise FAError(status, where)
 
 
+_cuda = None   # (current device, raw current stream of a device), once CUDA is up
+
+
+def _runtime():
+    global _cuda
+    if _cuda is None:
+        import torch
+        torch.cuda.current_device()   # raises without a CUDA runtime
+        _cuda = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    return _cuda
+
+
 def _current_index() -> int:
     """Index of the current CUDA device: every pointer the library receives
     must be memory of this device (its kernels and tensor maps are built
     there)."""
-    import torch
     try:
-        return torch.cuda.current_device()
+        return _runtime()[0]()
     except Exception:   # no CUDA runtime in this process: the library rejects the call
         return 0
 
@@ -75,13 +86,13 @@ def _on_current_device(t, name) -> None:
 
 
 def _stream(stream):
-    import torch
     if stream is None:
-        stream = torch.cuda.current_stream()
+        device, raw_stream = _runtime()
+        return raw_stream(device())
     if hasattr(stream, "cuda_stream"):
         _on_current_device(stream, "stream")
-        return ctypes.c_void_p(stream.cuda_stream)
-    return ctypes.c_void_p(int(stream))
+        return stream.cuda_stream
+    return int(stream)
 
 
 def _ptr(t, name, dtype, shape):
@@ -89,12 +100,12 @@ def _ptr(t, name, dtype, shape):
     only pointers, so a short buffer would be read or written past its end),
     dtype, contiguity and device: a CUDA tensor of the current device, so that
     every operand of a call shares one device."""
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA {str(dtype)[6:]} tensor")
     _on_current_device(t, name)
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _bf16(t, name, shape=None):
@@ -203,7 +214,7 @@ def _ws(workspace):
     if not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
     _on_current_device(workspace, "workspace")
-    return ctypes.c_void_p(workspace.data_ptr()), workspace.numel() * workspace.element_size()
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def fa_bwd(q, k, v, o, dout, lse, dq, dk, dv, workspace, causal: bool, scale: float,

@@ -174,6 +174,8 @@ def _bind(L: ctypes.CDLL) -> ctypes.CDLL:
 def lib() -> ctypes.CDLL:
     """The loaded libfa.so.  Raises if it was not built (call build())."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):

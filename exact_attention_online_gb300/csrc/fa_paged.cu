@@ -62,8 +62,8 @@ struct PagedParams {
     float* lse;
     float* part_o;                      // [slots][R][d]
     float* part_lse;                    // [slots][R], log2
-    int2* meta;                         // per pair: first slot, number of slots
     int B, Hkv, Nq, R, n_pages, ps_shift, max_pages, causal;
+    int ctas;                           // of the split kernel
     float scale_log2;
     DeviceStatus* status;
 };
@@ -128,6 +128,34 @@ struct Cursor {
     }
 };
 
+// Length of the list of tiles (returned) and the tiles of the sequences before
+// lane's first and up to its last one: a warp adds up B lengths, each lane
+// those of ceil(B / 32) neighbouring sequences b0 .. b1 - 1.
+__device__ __forceinline__ int list_length(const PagedParams& p, int lane, int& b0, int& b1,
+                                           int& before, int& upto) {
+    const int per = (p.B + 31) / 32;
+    b0 = min(p.B, lane * per);
+    b1 = min(p.B, b0 + per);
+    int mine = 0;
+#pragma unroll 4
+    for (int b = b0; b < b1; ++b) mine += tiles_of(clamped_len(p, b));
+    mine *= p.Hkv;
+    upto = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, off);
+        if (lane >= off) upto += y;
+    }
+    before = upto - mine;
+    return __shfl_sync(0xffffffffu, upto, 31);
+}
+
+// CTA c of nc holds tiles c T / nc .. (c + 1) T / nc - 1; the one that holds
+// tile t.  nc <= T, so that each one holds some and a pair's CTAs are neighbours.
+__device__ __forceinline__ int cta_of_tile(int t, int T, int nc) {
+    return (int)((((long long)t + 1) * nc + T - 1) / T) - 1;
+}
+
 // Monotone map of a float's order onto signed integers (its own inverse).
 __device__ __forceinline__ int ordered(float x) {
     const int i = __float_as_int(x);
@@ -186,7 +214,7 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
     __shared__ float4 row_part4[RP];              // [4 warps][RP]: maxima, then sums
     __shared__ float q_scale[2][RP];              // e4m3: score of one code product, log2 units
     __shared__ int row_query[RP];                 // r % Nq
-    __shared__ int start_sh[7];                    // b, g, tile, tiles of this CTA; T, CTAs, first tile
+    __shared__ int start_sh[4];                   // first pair and tile, tiles of this CTA
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_sh;
     float* row_part = reinterpret_cast<float*>(row_part4);
@@ -195,29 +223,12 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
 
     pdl_launch_dependents();
     if (warp == 0) {
-        // The list's length T and this CTA's share: each lane adds up the
-        // tiles of B / 32 neighbouring sequences.
-        const int per = (p.B + 31) / 32, b0 = min(p.B, lane * per), b1 = min(p.B, b0 + per);
-        int mine = 0;
-        for (int b = b0; b < b1; ++b) mine += tiles_of(clamped_len(p, b)) * p.Hkv;
-        int upto = mine;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, upto, off);
-            if (lane >= off) upto += y;
-        }
-        const int T = __shfl_sync(0xffffffffu, upto, 31);
-        // no more CTAs than tiles: each one holds some, so a pair's CTAs are neighbours
+        int b0, b1, at, upto;
+        const int T = list_length(p, lane, b0, b1, at, upto);
         const int nc = min((int)gridDim.x, T), c = min((int)blockIdx.x, nc);
         const int begin = nc ? (int)((long long)c * T / nc) : 0;
         const int end = c < nc ? (int)((long long)(c + 1) * T / nc) : begin;
-        int at = upto - mine;                     // first tile of this lane's sequences
-        if (lane == 0) {
-            start_sh[4] = T;
-            start_sh[5] = nc;
-            start_sh[6] = begin;
-            if (begin == end) start_sh[3] = 0;
-        }
+        if (lane == 0 && begin == end) start_sh[3] = 0;
         if (begin < end && at <= begin && begin < upto) {
             for (int b = b0; b < b1; ++b) {
                 const int tiles = tiles_of(clamped_len(p, b));
@@ -496,7 +507,6 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
         const int vs_at = ks_at + (1 << seg_shift);
         bool ok = true;
         int gt = 0;
-        int list_at = start_sh[6];                // tile gt in the list
         for (int n = 0; cur.left > 0; ++n) {
             const int tiles = cur.run();
             float m[RP], l[RP], qc[RP];
@@ -655,8 +665,7 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
             row_part[warp * RP + row] = total;            // several lanes, one value
             named_bar_sync(kSoftBar, 128);
             const int pair = cur.b * p.Hkv + cur.g;
-            const int pair_tiles = tiles_of(cur.len);
-            const bool whole = tiles == pair_tiles;
+            const bool whole = tiles == tiles_of(cur.len);
             const long long slot = (long long)blockIdx.x + pair;
             const long long out_row = whole ? (long long)pair * p.R : slot * p.R;
 #pragma unroll
@@ -681,16 +690,7 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                         p.part_lse[out_row + r] = lse2;
                 }
             }
-            if (j == 0 && cur.t == 0) {
-                int parts = 1;
-                if (!whole) {   // the CTA that holds the pair's last tile
-                    const long long T = start_sh[4], nc = start_sh[5];
-                    parts = (int)(((list_at + pair_tiles) * nc + T - 1) / T) - (int)blockIdx.x;
-                }
-                p.meta[pair] = make_int2((int)slot, parts);
-            }
             gt += tiles;
-            list_at += tiles;
             cur.skip(p, tiles);
         }
     }
@@ -704,54 +704,86 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
 
 // One warp per query row of the pairs that several CTAs share: the parts
 // weighted by exp(LSE_s - LSE), in slot order.  Rows of empty sequences are
-// written here.
+// written here.  Where a row's parts lie follows from the lengths alone and is
+// found while the split kernel still runs; after it, the parts' LSEs and the
+// first kPre parts of O come in one round trip.
 template <int D>
 __global__ void __launch_bounds__(256) fa_paged_combine_kernel(const PagedParams p, int rows) {
+    constexpr int E = D / 32, kPre = 8;
     const int row = (int)((blockIdx.x * 256 + threadIdx.x) >> 5), lane = threadIdx.x & 31;
-    if (row >= rows) return;
-    const int pair = row / p.R, r = row - pair * p.R;
+    const int pair = min(row, rows - 1) / p.R, r = row - pair * p.R;
+    const int b = pair / p.Hkv, g = pair - b * p.Hkv;
+    int b0, b1, at, upto;
+    const int T = list_length(p, lane, b0, b1, at, upto);
+    const int tiles = tiles_of(clamped_len(p, b));
+    for (int x = b0; x < b1 && x < b; ++x) at += tiles_of(clamped_len(p, x)) * p.Hkv;
+    // the lane whose sequences b is one of
+    const int first = __shfl_sync(0xffffffffu, at, b / ((p.B + 31) / 32)) + g * tiles;
+    const int nc = min(p.ctas, T);
+    const int c0 = tiles ? cta_of_tile(first, T, nc) : 0;
+    const int parts = tiles ? cta_of_tile(first + tiles - 1, T, nc) - c0 + 1 : 0;
+    // Every thread waits here, also those with nothing to join: this grid must
+    // not end before the split kernel, whose results the next one in the
+    // stream may read.
+    pdl_wait();
+    if (row >= rows || parts == 1) return;
     __nv_bfloat16* o = p.o + (long long)row * D + lane;
-    if (clamped_len(p, pair / p.Hkv) == 0) {
+    if (parts == 0) {
 #pragma unroll
-        for (int c = 0; c < D; c += 32) o[c] = __float2bfloat16_rn(0.0f);
+        for (int c = 0; c < E; ++c) o[32 * c] = __float2bfloat16_rn(0.0f);
         if (lane == 0) p.lse[row] = -CUDART_INF_F;
         return;
     }
-    pdl_wait();
-    const int2 mt = __ldcg(p.meta + pair);
-    if (mt.y <= 1) return;
-    const float* lp = p.part_lse + (long long)mt.x * p.R + r;
-    const float* op = p.part_o + ((long long)mt.x * p.R + r) * D + lane;
-    float mx = -CUDART_INF_F;
-    for (int s = lane; s < mt.y; s += 32) mx = fmaxf(mx, __ldcg(lp + (long long)s * p.R));
+    const long long slot = (long long)c0 + pair;
+    const float* lp = p.part_lse + slot * p.R + r;
+    const float* op = p.part_o + (slot * p.R + r) * D + lane;
+    const long long lstep = p.R, ostep = (long long)p.R * D;
+    const float l0 = lane < parts ? __ldcg(lp + lane * lstep) : -CUDART_INF_F;
+    float pre[kPre][E];
+#pragma unroll
+    for (int k = 0; k < kPre; ++k)
+#pragma unroll
+        for (int c = 0; c < E; ++c) pre[k][c] = k < parts ? __ldcg(op + k * ostep + 32 * c) : 0.0f;
+    float mx = l0;
+    for (int s = lane + 32; s < parts; s += 32) mx = fmaxf(mx, __ldcg(lp + s * lstep));
     mx = from_ordered(__reduce_max_sync(0xffffffffu, ordered(mx)));
     if (mx == -CUDART_INF_F) mx = 0.0f;
-    float acc[D / 32], sum = 0.0f;
+    float acc[E], sum = 0.0f;
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c) acc[c] = 0.0f;
-    for (int base = 0; base < mt.y; base += 32) {
+    for (int c = 0; c < E; ++c) acc[c] = 0.0f;
+    for (int base = 0; base < parts; base += 32) {
         const int s = base + lane;
-        const float w = s < mt.y ? ex2(__ldcg(lp + (long long)s * p.R) - mx) : 0.0f;
-        const int cnt = min(32, mt.y - base);
+        const float ls = base == 0 ? l0 : (s < parts ? __ldcg(lp + s * lstep) : -CUDART_INF_F);
+        const float w = ex2(ls - mx);
+        const int cnt = min(32, parts - base);
         sum += w;
+        int k = 0;
+        if (base == 0) {
+#pragma unroll
+            for (; k < kPre; ++k) {
+                const float wk = __shfl_sync(0xffffffffu, w, k);
+#pragma unroll
+                for (int c = 0; c < E; ++c) acc[c] = fmaf(wk, pre[k][c], acc[c]);
+            }
+        }
 #pragma unroll 8
-        for (int k = 0; k < cnt; ++k) {
+        for (; k < cnt; ++k) {
             const float wk = __shfl_sync(0xffffffffu, w, k);
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c)
-                acc[c] = fmaf(wk, __ldcg(op + (long long)(base + k) * p.R * D + 32 * c), acc[c]);
+            for (int c = 0; c < E; ++c)
+                acc[c] = fmaf(wk, __ldcg(op + (base + k) * ostep + 32 * c), acc[c]);
         }
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c)
+    for (int c = 0; c < E; ++c)
         o[32 * c] = __float2bfloat16_rn(sum == 0.0f ? 0.0f : acc[c] / sum);
     if (lane == 0) p.lse[row] = sum == 0.0f ? -CUDART_INF_F : (mx + log2f(sum)) * kLn2;
 }
 
 template <int D, bool F8, int RP>
-cudaError_t launch_split(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p,
+cudaError_t launch_split(const CUtensorMap& tk, const CUtensorMap& tv, PagedParams& p,
                          cudaStream_t stream) {
     using C = Cfg<D, F8, RP>;
     static_assert(C::kSmem + 2048 <= 227 * 1024, "shared memory of one CTA");
@@ -765,18 +797,19 @@ cudaError_t launch_split(const CUtensorMap& tk, const CUtensorMap& tv, const Pag
         if (e != cudaSuccess) return e;
         configured.fetch_or(1ull << dev, std::memory_order_release);
     }
-    // At most one tile list entry a CTA: no more CTAs than tiles can exist.
+    // no more CTAs than there can be tiles
     const long long most = (long long)p.B * p.Hkv * (((p.max_pages << p.ps_shift) + kTile - 1) / kTile);
     long long grid = (long long)(device_sm_count() > 0 ? device_sm_count() : 152) * C::kCtas;
     if (grid > kPagedMaxCtas) grid = kPagedMaxCtas;
     if (grid > most) grid = most;
+    p.ctas = (int)grid;
     count_launch();
     kern<<<(unsigned)grid, kThreads, C::kSmem, stream>>>(tk, tv, p);
     return cudaGetLastError();
 }
 
 template <int D, bool F8>
-cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p,
+cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, PagedParams& p,
                         cudaStream_t stream) {
     if (p.R <= 8) return launch_split<D, F8, 8>(tk, tv, p, stream);
     if (p.R <= 16) return launch_split<D, F8, 16>(tk, tv, p, stream);
@@ -806,7 +839,7 @@ size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 size_t paged_workspace_bytes(int B, int Hkv, int R, int d) {
     const size_t slots = (size_t)kPagedMaxCtas + (size_t)B * Hkv;
-    return align256(slots * R * d * 4) + align256(slots * R * 4) + (size_t)B * Hkv * 8;
+    return align256(slots * R * d * 4) + slots * R * 4;
 }
 
 cudaError_t launch_fwd_decode_paged(const PagedCache& c, const void* q, void* o, float* lse,
@@ -826,8 +859,6 @@ cudaError_t launch_fwd_decode_paged(const PagedCache& c, const void* q, void* o,
     p.part_o = reinterpret_cast<float*>(ws);
     ws += align256(slots * p.R * c.d * 4);
     p.part_lse = reinterpret_cast<float*>(ws);
-    ws += align256(slots * p.R * 4);
-    p.meta = reinterpret_cast<int2*>(ws);
     p.q = static_cast<const __nv_bfloat16*>(q);
     p.scales = c.scales;
     p.table = c.table;

@@ -102,12 +102,12 @@ def test_packed_moves_refuse_an_empty_batch(L, append):
 
 def test_workspace_size(L):
     # partial O fp32 [slots][R][d] and LSE fp32 [slots][R] for one slot a CTA (304 at most)
-    # and one a (sequence, kv head), then two ints a (sequence, kv head)
+    # and one a (sequence, kv head)
     r256 = lambda x: (x + 255) // 256 * 256
     B, H, Hkv, Nq, d = 3, 8, 2, 2, 64
     slots, R = 304 + B * Hkv, H // Hkv * Nq
     assert fa.fa_fwd_decode_paged_workspace_size(B, H, Hkv, Nq, d) == \
-        r256(slots * R * d * 4) + r256(slots * R * 4) + 8 * B * Hkv
+        r256(slots * R * d * 4) + slots * R * 4
     assert fa.fa_fwd_decode_paged_workspace_size(B, H, 3, Nq, d) == 0
     assert fa.fa_fwd_decode_paged_workspace_size(B, 66, 2, 1, d) == 0     # 33 rows
     assert fa.fa_fwd_decode_paged_workspace_size(B, H, Hkv, Nq, 96) == 0
