@@ -9,8 +9,8 @@
 //   O^T  += V_t^T P_t^T  A = V read transposed (MN-major), B = P_t, O^T in TMEM
 // With the keys on the MMA's M side a tile costs one read of K and V from
 // shared memory (N is 16 to 64 columns), each of the 128 softmax threads owns
-// one key and R scores, nothing is computed for absent query rows past the next
-// 8, 16 or 32, and no thread needs another's score: the running maximum m of a
+// one key and eight rows' scores, nothing is computed for absent query rows past the
+// next 8, 16 or 32, and no thread needs another's score: the running maximum m of a
 // row moves only when some key passes it by 2^kSlack (a vote of the four
 // warps), the row sums stay one partial per thread until the end, and the
 // rescale of O^T touches kN columns.
@@ -25,16 +25,17 @@
 // again; a row of zeros has scale 0 and weighs nothing.  No pass converts the
 // pages, and shared memory sees each of their bytes twice.
 //
-// Work: the tiles of all (sequence, kv head) pairs, in order, are one list of T
-// that the CTAs share evenly (CTA c of n takes tiles c T / n .. (c + 1) T / n),
-// found on the device from the lengths, so that ragged batches stay balanced and
-// a captured graph replays with other lengths.  A pair that one CTA holds whole
-// is finished there.  The others leave O / l and LSE of their part in slot c + i
-// (i the pair's index: along the list either c or i grows, so slots are unique),
-// and the combine kernel joins a pair's slots in order.
+// Work: the tiles of all (sequence, kv head) pairs, in order, are one list that
+// the CTAs share evenly (Plan), found on the device from the lengths, so that
+// ragged batches stay balanced and a captured graph replays with other lengths.
+// A pair that one CTA holds whole is finished there.  The others leave O / l and
+// LSE of their part in slot c + i (CTA c, pair i: along the list either c or i
+// grows, so slots are unique), and the combine kernel joins a pair's slots in
+// order.
 //
-// Warps: 0-3 softmax, 4 loads K, V and scales (a lane a page), 5 issues MMAs, 6
-// lays out the next pair's queries.
+// Warps: 0-3 (8-11, .., 16-19) softmax, four warps for each eight query rows, which
+// need nothing of one another; 4 loads K, 7 V and the scales, 5 issues MMAs, 6 lays
+// out the next pair's queries.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -47,11 +48,12 @@ namespace fa {
 namespace {
 
 constexpr int kTile = 128;              // keys per tile
-constexpr int kThreads = 224;
+constexpr int kRows = 8;                // query rows of a softmax group
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kMinLogScale = -60.0f;  // V scales below 2^-60 no longer move the reference
-constexpr int kSoftBar = 1;             // named barrier of the softmax warps
+constexpr float kNoMax = -3.402823466e38f;   // running maximum of a row that has seen no key
+constexpr int kSoftBar = 1;             // named barrier of softmax group 0
 
 struct PagedParams {
     const __nv_bfloat16* q;             // rows i * R .. of pair i = b * Hkv + g
@@ -63,14 +65,16 @@ struct PagedParams {
     float* part_o;                      // [slots][R][d]
     float* part_lse;                    // [slots][R], log2
     int B, Hkv, Nq, R, n_pages, ps_shift, max_pages, causal;
-    int ctas;                           // of the split kernel
+    int ctas;                           // resident CTAs of the split kernel
     float scale_log2;
     DeviceStatus* status;
 };
 
-// Sizes of one variant: head dimension, page type, query rows rounded up.
-template <int D, bool F8, int RP>
+// Sizes of one variant: head dimension, page type, groups of eight query rows.
+template <int D, bool F8, int G>
 struct Cfg {
+    static constexpr int RP = kRows * G;
+    static constexpr int kThreads = 128 + 128 * G;
     static constexpr int kN = F8 ? 2 * RP : (RP < 16 ? 16 : RP);   // MMA columns
     static constexpr int kRowBytes = F8 ? D : 2 * D;
     static constexpr int kSw = kRowBytes < 128 ? 64 : 128;         // swizzle = chunk width
@@ -80,12 +84,13 @@ struct Cfg {
     static constexpr int kPRow = F8 ? kTile : 2 * kTile;
     static constexpr int kPBytes = kN * kPRow;
     static constexpr int kScaleBytes = F8 ? 2 * kTile * 4 : 0;
-    // d = 128 fills an SM with one CTA; d = 64 runs two, so that one's
-    // softmax and epilogue hide behind the other's loads.
-    static constexpr int kCtas = (D == 64 && RP <= 16) ? 2 : 1;
-    static constexpr int kRing = (kCtas == 2 ? 96 : 192) * 1024;
-    static constexpr int kStages =
-        (kRing - (F8 && RP == 32 ? 16 * 1024 : 0)) / (2 * kTileBytes + kScaleBytes);
+    // bf16 rows of 128 fill an SM with one CTA.  Smaller ones leave less time a
+    // tile, and with up to 8 rows two CTAs fit, so that one's softmax and
+    // epilogue hide behind the other's.
+    static constexpr int kCtas = kRowBytes <= 128 && G == 1 ? 2 : 1;
+    static constexpr int kRing = (kCtas == 2 ? 113 : 227) * 1024 - 1024 - 2048 - 2 * kQBytes -
+                                 2 * kPBytes;
+    static constexpr int kStages = kRing / (2 * kTileBytes + kScaleBytes);
     static constexpr int kSmem =
         kStages * (2 * kTileBytes + kScaleBytes) + 2 * kQBytes + 2 * kPBytes + 1024;
     static constexpr int kTmemCols = 3 * kN <= 64 ? 64 : (3 * kN <= 128 ? 128 : 256);
@@ -100,60 +105,116 @@ __device__ __forceinline__ int clamped_len(const PagedParams& p, int b) {
 }
 __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
 
-// A CTA's place in the list of tiles: pair (b, g), tile t of it, and how many
-// tiles the CTA still has.
+// How the list is shared.  A pair counts its tiles and kPairUnits more units (its
+// queries, first maximum and epilogue); of the V units in all, CTA c holds c * size
+// .. (c + 1) * size - 1.  No CTA between two others is empty, so the CTAs of a pair
+// are neighbours.
+constexpr int kPairUnits = 1;
+struct Plan {
+    int V, size;
+    __device__ __forceinline__ Plan(int units, int ctas)
+        : V(units), size(max(1, (int)((unsigned)(units + ctas - 1) / (unsigned)ctas))) {}
+    __device__ __forceinline__ int begin(int c) const { return min(V, c * size); }
+    __device__ __forceinline__ int cta_of(int u) const {
+        return (int)((unsigned)u / (unsigned)size);
+    }
+};
+
+// The list as a warp sees it: lane l knows the units of ceil(B / 32)
+// neighbouring sequences b0 .. b1 - 1, which begin at unit `at`.
+struct List {
+    int b0, b1, at, upto, units;
+    __device__ __forceinline__ List(const PagedParams& p, int lane) {
+        const int per = (p.B + 31) / 32;
+        b0 = min(p.B, lane * per);
+        b1 = min(p.B, b0 + per);
+        int mine = 0;
+#pragma unroll 2
+        for (int b = b0; b < b1; ++b) mine += units_of(p, clamped_len(p, b));
+        upto = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, upto, off);
+            if (lane >= off) upto += y;
+        }
+        at = upto - mine;
+        units = __shfl_sync(0xffffffffu, upto, 31);
+    }
+    // units of one sequence: all its kv heads
+    static __device__ __forceinline__ int units_of(const PagedParams& p, int len) {
+        return len > 0 ? (tiles_of(len) + kPairUnits) * p.Hkv : 0;
+    }
+};
+
+// A CTA's place in the list: pair (b, g), tile t of it, and the units left.
 struct Cursor {
     int b, g, len, t, left;
+    // The place at unit `begin` of the list, for `units` units, found by a warp together.
+    __device__ __forceinline__ Cursor(const PagedParams& p, const List& list, int begin,
+                                      int units) {
+        b = g = len = t = 0;
+        left = units;
+        if (left <= 0) return;
+        const bool here = list.at <= begin && begin < list.upto;
+        const int owner = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+        if (owner < 0) {                // (lengths that somebody changes under the kernel)
+            left = 0;
+            return;
+        }
+        if (here) {
+            int at = list.at;
+#pragma unroll 1
+            for (b = list.b0; b < list.b1; ++b) {
+                len = clamped_len(p, b);
+                const int u = List::units_of(p, len);
+                if (begin < at + u) break;
+                at += u;
+            }
+            const int per = tiles_of(len) + kPairUnits;
+            g = (begin - at) / per;
+            t = (begin - at) - g * per - kPairUnits;   // below 0: the pair's extra units
+        }
+        b = __shfl_sync(0xffffffffu, b, owner);
+        g = __shfl_sync(0xffffffffu, g, owner);
+        t = __shfl_sync(0xffffffffu, t, owner);
+        len = __shfl_sync(0xffffffffu, len, owner);
+        if (b >= p.B || g < 0 || g >= p.Hkv || t >= tiles_of(len)) left = 0;
+        if (t < 0) {
+            left += t;
+            t = 0;
+        }
+    }
     // tiles of the current pair that belong to this CTA
     __device__ __forceinline__ int run() const { return min(tiles_of(len) - t, left); }
     // past `n` tiles of the current pair
     __device__ __forceinline__ void skip(const PagedParams& p, int n) {
         left -= n;
         t += n;
-        if (left > 0 && t == tiles_of(len)) {
-            t = 0;
-            if (++g == p.Hkv) {
-                g = 0;
-                // left > 0: a sequence with keys follows (the bound is for
-                // lengths that somebody changes under the kernel)
-                do {
-                    if (++b >= p.B) {
-                        left = 0;
-                        return;
-                    }
-                    len = clamped_len(p, b);
-                } while (len == 0);
+        if (left <= 0 || t < tiles_of(len)) return;
+        t = 0;
+        if ((left -= kPairUnits) <= 0) return;
+        if (++g < p.Hkv) return;
+        g = 0;
+        do {                            // left > 0: a sequence with keys follows
+            if (++b >= p.B) {
+                left = 0;
+                return;
             }
-        }
+            len = clamped_len(p, b);
+        } while (len == 0);
     }
 };
 
-// Length of the list of tiles (returned) and the tiles of the sequences before
-// lane's first and up to its last one: a warp adds up B lengths, each lane
-// those of ceil(B / 32) neighbouring sequences b0 .. b1 - 1.
-__device__ __forceinline__ int list_length(const PagedParams& p, int lane, int& b0, int& b1,
-                                           int& before, int& upto) {
-    const int per = (p.B + 31) / 32;
-    b0 = min(p.B, lane * per);
-    b1 = min(p.B, b0 + per);
-    int mine = 0;
-#pragma unroll 4
-    for (int b = b0; b < b1; ++b) mine += tiles_of(clamped_len(p, b));
-    mine *= p.Hkv;
-    upto = mine;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, upto, off);
-        if (lane >= off) upto += y;
-    }
-    before = upto - mine;
-    return __shfl_sync(0xffffffffu, upto, 31);
+// The library's bounded wait with only the first poll inlined.
+__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, int site, const WaitCtx& wc) {
+    return fa_wait(bar, parity, site, wc);
 }
-
-// CTA c of nc holds tiles c T / nc .. (c + 1) T / nc - 1; the one that holds
-// tile t.  nc <= T, so that each one holds some and a pair's CTAs are neighbours.
-__device__ __forceinline__ int cta_of_tile(int t, int T, int nc) {
-    return (int)((((long long)t + 1) * nc + T - 1) / T) - 1;
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int site, const WaitCtx& wc) {
+    return mbar_try_wait(smem_u32(bar), parity) || wait_on(bar, parity, site, wc);
+}
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int site,
+                                          const WaitCtx& wc) {
+    return __all_sync(0xffffffffu, wait(bar, parity, site, wc));
 }
 
 // Monotone map of a float's order onto signed integers (its own inverse).
@@ -163,6 +224,15 @@ __device__ __forceinline__ int ordered(float x) {
 }
 __device__ __forceinline__ float from_ordered(int i) {
     return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
+}
+
+// m + log2 l for l > 0.  The exponent of l is added to m first: the two cancel
+// where V's scales are small, and lg2.approx is off by 2^-22 absolutely only on
+// [1, 2).
+__device__ __forceinline__ float add_log2(float m, float l) {
+    const int i = __float_as_int(l), e = (i >> 23) - 127;
+    if (e == 128) return m + l;                   // infinity or NaN
+    return (m + (float)e) + lg2(__int_as_float((i & 0x7fffff) | 0x3f800000));
 }
 
 // Sums v[r] over the warp, all rows at once: halving exchanges leave each lane
@@ -191,73 +261,57 @@ __device__ __forceinline__ float warp_row_sums(float (&v)[RP], int lane, int& ro
     return v[0];
 }
 
-template <int D, bool F8, int RP>
-__global__ void __launch_bounds__(kThreads, (Cfg<D, F8, RP>::kCtas))
+template <int D, bool F8, int G>
+__global__ void __launch_bounds__((Cfg<D, F8, G>::kThreads), (Cfg<D, F8, G>::kCtas))
 fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
-                       const __grid_constant__ CUtensorMap tm_v, const PagedParams p) {
-    using C = Cfg<D, F8, RP>;
-    constexpr int S = C::kStages, N = C::kN, TB = C::kTileBytes;
+                       const __grid_constant__ CUtensorMap tm_v,
+                       const __grid_constant__ PagedParams p) {
+    using C = Cfg<D, F8, G>;
+    constexpr int S = C::kStages, N = C::kN, TB = C::kTileBytes, RP = C::RP;
     constexpr uint32_t kColO = 2 * N;             // S buffers at 0 and N
     extern __shared__ uint8_t dsm_raw[];
-    uint8_t* dsm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsm_raw) + 1023) &
-                                              ~static_cast<uintptr_t>(1023));
-    // Stage s: V, then K.  At d = 64 the MMA's 128 rows reach past V's 64
-    // columns: its second half reads K, into rows of O^T that nobody reads.
-    uint8_t* sKV = dsm;
-    uint8_t* sQ = sKV + S * 2 * TB;               // [2]
-    uint8_t* sP = sQ + 2 * C::kQBytes;            // [2]
-    float* sScale = reinterpret_cast<float*>(sP + 2 * C::kPBytes);   // [S][segment][K, V][rows]
+    // 32-bit shared addresses, 1024-byte aligned.  Stage s: V, then K.  At d = 64
+    // the MMA's 128 rows reach past V's 64 columns: its second half reads K, into
+    // rows of O^T that nobody reads.
+    const uint32_t sKV = (smem_u32(dsm_raw) + 1023) & ~1023u;
+    const uint32_t sQ = sKV + S * 2 * TB;         // [2]
+    const uint32_t sP = sQ + 2 * C::kQBytes;      // [2]
+    const uint32_t sScale = sP + 2 * C::kPBytes;  // [S][K, V][128] fp32
     __shared__ uint64_t bar_q[2], bar_q_free[2], bar_k[S], bar_k_empty[S], bar_v[S],
         bar_v_empty[S];
     // S_t, P_t and P_t V_t signal barrier t & 1 (t counts the CTA's tiles)
     __shared__ uint64_t bar_s[2], bar_p[2], bar_pv[2], bar_drain;
-    __shared__ float4 row_part4[RP];              // [4 warps][RP]: maxima, then sums
+    __shared__ float4 row_max[RP], row_sum[RP];   // a value a softmax warp
     __shared__ float q_scale[2][RP];              // e4m3: score of one code product, log2 units
     __shared__ int row_query[RP];                 // r % Nq
-    __shared__ int start_sh[4];                   // first pair and tile, tiles of this CTA
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_sh;
-    float* row_part = reinterpret_cast<float*>(row_part4);
-    const WaitCtx wc{p.status, &abort_sh};
+    const WaitCtx wc{p.status, &abort_sh}, dc{p.status, nullptr};   // dc: for drains
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     pdl_launch_dependents();
-    if (warp == 0) {
-        int b0, b1, at, upto;
-        const int T = list_length(p, lane, b0, b1, at, upto);
-        const int nc = min((int)gridDim.x, T), c = min((int)blockIdx.x, nc);
-        const int begin = nc ? (int)((long long)c * T / nc) : 0;
-        const int end = c < nc ? (int)((long long)(c + 1) * T / nc) : begin;
-        if (lane == 0 && begin == end) start_sh[3] = 0;
-        if (begin < end && at <= begin && begin < upto) {
-            for (int b = b0; b < b1; ++b) {
-                const int tiles = tiles_of(clamped_len(p, b));
-                if (begin < at + tiles * p.Hkv) {
-                    start_sh[0] = b;
-                    start_sh[1] = (begin - at) / tiles;
-                    start_sh[2] = (begin - at) % tiles;
-                    start_sh[3] = end - begin;
-                    break;
-                }
-                at += tiles * p.Hkv;
-            }
-        }
-    } else if (warp == 4) {
+    const List list(p, lane);
+    const Plan plan(list.units, p.ctas);
+    const int c = blockIdx.x, begin = plan.begin(c);
+    if (begin >= plan.V) return;
+
+    if (warp == 4) {
         if (lane == 0) {
             tma_prefetch_desc(&tm_k);
             tma_prefetch_desc(&tm_v);
             abort_sh = 0;
             for (int x = 0; x < 2; ++x) {
                 mbar_init(&bar_q[x], 32);
-                mbar_init(&bar_q_free[x], F8 ? 5 : 1);   // the last S MMA; the warps' scales
+                mbar_init(&bar_q_free[x], F8 ? 1 + 4 * G : 1);   // the last S MMA; scales read
                 mbar_init(&bar_s[x], 1);
-                mbar_init(&bar_p[x], 128);
+                mbar_init(&bar_p[x], 128 * G);
                 mbar_init(&bar_pv[x], 1);
             }
+#pragma unroll 1
             for (int s = 0; s < S; ++s) {
                 mbar_init(&bar_k[s], 1);
                 mbar_init(&bar_k_empty[s], 1);
-                mbar_init(&bar_v[s], 1);
+                mbar_init(&bar_v[s], F8 ? 33 : 1);       // the scales: a lane each
                 mbar_init(&bar_v_empty[s], 1);
             }
             mbar_init(&bar_drain, 1);
@@ -268,10 +322,12 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
         tmem_relinquish();
     } else {
         // Query rows past R and columns of P past RP stay zero.
-        const int x0 = (warp == 6 ? 3 : warp - 1) * 32 + lane;
-        for (int e = x0; e < (2 * C::kQBytes + 2 * C::kPBytes) / 16; e += 128)
-            reinterpret_cast<uint4*>(sQ)[e] = make_uint4(0u, 0u, 0u, 0u);
+        const int x0 = (warp < 4 ? warp : warp - 2) * 32 + lane;
+#pragma unroll 1
+        for (int e = x0; e < (2 * C::kQBytes + 2 * C::kPBytes) / 16; e += C::kThreads - 64)
+            sts_v4(sQ + e * 16, make_uint4(0u, 0u, 0u, 0u));
         if (warp == 6)
+#pragma unroll 1
             for (int r = lane; r < RP; r += 32) row_query[r] = r % p.Nq;
         fence_proxy_async_smem();
     }
@@ -279,415 +335,445 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base_sh;
-    Cursor cur{start_sh[0], start_sh[1], 0, start_sh[2], start_sh[3]};
-    if (cur.left > 0) cur.len = clamped_len(p, cur.b);
 
-    if (warp == 4) {
+    Cursor cur(p, list, begin, plan.begin(c + 1) - begin);
+
+    if (warp == 4 || warp == 7) {
         // ------------------------------------------------------- loads
-        // Lanes 0-15 load K, 16-31 V, one box of up to 128 keys of one page
-        // each; in e4m3 lanes 24-31 load the pages' scales instead.
+        // Boxes of up to 128 keys of one page.  Lane i holds segment i's place
+        // in the pool, one lane issues: a copy takes uniform registers, so
+        // copies from several lanes would be issued in a loop over the lanes.
+        const bool is_v = warp == 7;
+        const CUtensorMap* map = is_v ? &tm_v : &tm_k;
+        uint64_t* full = is_v ? bar_v : bar_k;
+        uint64_t* empty = is_v ? bar_v_empty : bar_k_empty;
         const int seg_shift = min(p.ps_shift, 7), seg = 1 << seg_shift;
-        const int n_seg = kTile >> seg_shift;
-        const bool is_scale = F8 && lane >= 24;
-        const int x = is_scale ? lane - 24 : lane & 15;
-        const int my_seg = is_scale ? x : x / C::kChunks, chunk = is_scale ? 0 : x % C::kChunks;
+        const int n_seg = kTile >> seg_shift, page_mask = (1 << p.ps_shift) - 1;
         const int seg_bytes = seg * C::kSw;
         auto page_of = [&](const Cursor& c) {
-            const int key = c.t * kTile + my_seg * seg;
-            return (my_seg < n_seg && key < c.len)
+            const int key = c.t * kTile + lane * seg;
+            return (c.left > 0 && lane < n_seg && key < c.len)
                        ? __ldg(p.table + (long long)c.b * p.max_pages + (key >> p.ps_shift))
                        : 0;
         };
         bool ok = true;
-        int gt = 0, vt = 0;                       // K and V tiles loaded so far
-        int page = cur.left > 0 ? page_of(cur) : 0;
+        int gt = 0;                               // tiles loaded so far
+        int page = page_of(cur);
+#pragma unroll 1
         while (ok && cur.left > 0) {
             const Cursor at = cur;
             cur.skip(p, 1);
-            const int page_next = cur.left > 0 ? page_of(cur) : 0;   // in flight during the waits
+            const int page_next = page_of(cur);              // in flight during the wait
             const int s = gt % S;
             const int have = min(n_seg, (at.len - at.t * kTile + seg - 1) >> seg_shift);
-            const bool mine = my_seg < have;
-            const int key = at.t * kTile + my_seg * seg;
-            const int row = key & ((1 << p.ps_shift) - 1);
             const bool known = (unsigned)page < (unsigned)p.n_pages;
             // a page outside the pool reads as zeros (past the map's last row)
             const int outer = (known ? page : p.n_pages) * p.Hkv + (known ? at.g : 0);
-            uint8_t* stage = sKV + s * 2 * TB;
-            if (gt >= S) ok = fa_wait_warp(&bar_k_empty[s], ((gt / S) - 1) & 1, 100, wc);
-            if (ok) {
-                if (lane == 0) mbar_arrive_expect_tx(&bar_k[s], have * seg_bytes * C::kChunks);
-                __syncwarp();
-                if (lane < 16 && mine)
-                    tma_load_3d(stage + TB + chunk * (kTile * C::kSw) + my_seg * seg_bytes, &tm_k,
-                                &bar_k[s], chunk * (F8 ? C::kSw : C::kSw / 2), row, outer);
-                ++gt;
-            }
-            if (ok && vt >= S) ok = fa_wait_warp(&bar_v_empty[s], ((vt / S) - 1) & 1, 101, wc);
-            if (ok) {
+            const int row = (at.t * kTile) & page_mask;      // of a page of 256; else 0
+            if (gt >= S)
+                ok = wait_warp(&empty[s], ((gt / S) - 1) & 1, is_v ? 101 : 100, wc);
+            if (!ok) break;
+            const uint32_t stage = sKV + s * 2 * TB + (is_v ? 0 : TB);
+            if (lane == 0) mbar_arrive_expect_tx(&full[s], have * seg_bytes * C::kChunks);
+            __syncwarp();
+#pragma unroll 2
+            for (int i = 0; i < have; ++i) {
+                const int at_row = __shfl_sync(0xffffffffu, outer, i);
                 if (lane == 0)
-                    mbar_arrive_expect_tx(&bar_v[s],
-                                          have * (seg_bytes * C::kChunks + (F8 ? 8 * seg : 0)));
-                __syncwarp();
-                if (lane >= 16 && mine && !is_scale)
-                    tma_load_3d(stage + chunk * (kTile * C::kSw) + my_seg * seg_bytes, &tm_v,
-                                &bar_v[s], chunk * (F8 ? C::kSw : C::kSw / 2), row, outer);
-                if (is_scale && mine) {
-                    const float* src =
-                        p.scales + (((long long)(known ? page : 0) * p.Hkv + at.g) << (p.ps_shift + 1)) +
-                        row;
-                    float* dst = sScale + s * 2 * kTile + my_seg * 2 * seg;
-                    if (p.ps_shift <= 7) {
-                        bulk_load(dst, src, 8 * seg, &bar_v[s]);      // K's, then V's
-                    } else {
-                        bulk_load(dst, src, 4 * seg, &bar_v[s]);
-                        bulk_load(dst + seg, src + (1 << p.ps_shift), 4 * seg, &bar_v[s]);
-                    }
-                }
+#pragma unroll
+                    for (int c = 0; c < C::kChunks; ++c)
+                        tma_load_3d_at(stage + c * (kTile * C::kSw) + i * seg_bytes, map,
+                                       &full[s], c * (F8 ? C::kSw : C::kSw / 2), row, at_row);
             }
-            if (ok) ++vt;
+            if (F8 && is_v) {
+                // 128 keys' scales, four bytes a lane and copy
+                const uint32_t dst = sScale + (s * 2 * kTile + lane) * 4;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int j = 32 * i + lane;
+                    const int pg = __shfl_sync(0xffffffffu, known ? page : 0, j >> seg_shift);
+                    const float* src = p.scales +
+                                       (((long long)pg * p.Hkv + at.g) << (p.ps_shift + 1)) +
+                                       ((at.t * kTile + j) & page_mask);
+                    cp_async4(dst + 128 * i, src);
+                    cp_async4(dst + kTile * 4 + 128 * i, src + (1 << p.ps_shift));
+                }
+                cp_async_arrive(&full[s]);
+            }
+            ++gt;
             page = page_next;
         }
-        // No copy may still be in flight when the CTA ends, whatever the
-        // other warps did.
-        const WaitCtx dc{p.status, nullptr};
-        for (int t = max(0, gt - S); t < gt; ++t) fa_wait(&bar_k[t % S], (t / S) & 1, 102, dc);
-        for (int t = max(0, vt - S); t < vt; ++t) fa_wait(&bar_v[t % S], (t / S) & 1, 103, dc);
+        // No copy may still be on its way when the CTA ends, whatever the other
+        // warps did.
+#pragma unroll 1
+        for (int t = max(0, gt - S); t < gt; ++t) wait(&full[t % S], (t / S) & 1, 102, dc);
         __syncwarp();
     } else if (warp == 5) {
         // ------------------------------------------------------- MMAs
-        if (lane == 0) {
-            constexpr uint32_t idesc_s =
-                F8 ? idesc_e4m3_f32(128, N) : idesc_bf16_f32(128, N, false, false);
-            constexpr uint32_t idesc_o =
-                F8 ? idesc_e4m3_f32(128, N, true) : idesc_bf16_f32(128, N, true, false);
-            constexpr uint32_t kGroup = 8 * C::kSw;                  // 8 rows of a chunk
-            const uint32_t skv = smem_u32(sKV), sq = smem_u32(sQ), sp = smem_u32(sP);
-            auto desc = [&](uint32_t a, uint32_t lbo) {
-                return C::kSw == 128 ? sdesc_sw128(a, lbo, kGroup) : sdesc_sw64(a, lbo, kGroup);
-            };
-            // O^T (+)= V_u^T P_u^T
-            auto pv = [&](int u, bool first) -> bool {
-                const int s = u % S;
-                if (!fa_wait(&bar_p[u & 1], (u >> 1) & 1, 104, wc) ||
-                    !fa_wait(&bar_v[s], (u / S) & 1, 105, wc))
-                    return false;
-                tc_fence_after();
-                // V transposed: 32 (e4m3) or 16 keys a step; the next chunk of
-                // columns (d = 64: K) is the leading-dimension stride
-                const uint64_t vd =
-                    desc(skv + s * 2 * TB, C::kChunks == 2 ? kTile * C::kSw : TB);
-                const uint64_t pd = sdesc_sw128(sp + (u & 1) * C::kPBytes, 16, 1024);
+        constexpr uint32_t idesc_s =
+            F8 ? idesc_e4m3_f32(128, N) : idesc_bf16_f32(128, N, false, false);
+        constexpr uint32_t idesc_o =
+            F8 ? idesc_e4m3_f32(128, N, true) : idesc_bf16_f32(128, N, true, false);
+        constexpr uint32_t kGroup = 8 * C::kSw;                      // 8 rows of a chunk
+        auto desc = [&](uint32_t a, uint32_t lbo) {
+            return C::kSw == 128 ? sdesc_sw128(a, lbo, kGroup) : sdesc_sw64(a, lbo, kGroup);
+        };
+        // O^T (+)= V_u^T P_u^T
+        auto pv = [&](int u, bool first) -> bool {
+            const int s = u % S;
+            if (!wait(&bar_p[u & 1], (u >> 1) & 1, 104, wc) ||
+                !wait(&bar_v[s], (u / S) & 1, 105, wc))
+                return false;
+            tc_fence_after();
+            // V transposed: 32 (e4m3) or 16 keys a step; the next chunk of
+            // columns (d = 64: K) is the leading-dimension stride
+            const uint64_t vd = desc(sKV + s * 2 * TB, C::kChunks == 2 ? kTile * C::kSw : TB);
+            const uint64_t pd = sdesc_sw128(sP + (u & 1) * C::kPBytes, 16, 1024);
 #pragma unroll
-                for (int kk = 0; kk < (F8 ? 4 : 8); ++kk) {
-                    const uint64_t a = vd + (uint64_t)(kk * (F8 ? 32 : 16) * C::kSw >> 4);
-                    const uint64_t b = pd + kmajor_step(kk, N * 128);
-                    if (F8) mma_ss_f8(tmem + kColO, a, b, idesc_o, !first || kk > 0);
-                    else mma_ss(tmem + kColO, a, b, idesc_o, !first || kk > 0);
-                }
-                mma_commit(&bar_pv[u & 1]);
-                mma_commit(&bar_v_empty[s]);
-                return true;
-            };
-            bool ok = true, first = false;        // first: tile gt - 1 begins its pair
-            int gt = 0;
-            for (int n = 0; ok && cur.left > 0; ++n) {
-                const int tiles = cur.run();
-                if (!fa_wait(&bar_q[n & 1], (n >> 1) & 1, 106, wc)) { ok = false; break; }
+            for (int kk = 0; kk < (F8 ? 4 : 8); ++kk) {
+                const uint64_t a = vd + (uint64_t)(kk * (F8 ? 32 : 16) * C::kSw >> 4);
+                const uint64_t b = pd + kmajor_step(kk, N * 128);
+                if (F8) mma_ss_f8(tmem + kColO, a, b, idesc_o, !first || kk > 0);
+                else mma_ss(tmem + kColO, a, b, idesc_o, !first || kk > 0);
+            }
+            mma_commit(&bar_pv[u & 1]);
+            mma_commit(&bar_v_empty[s]);
+            return true;
+        };
+        bool ok = true;
+        int gt = 0, pairs = 0;
+        bool behind = false, first = false;   // P V of tile gt - 1 to come; it begins its pair
+        for (; ok && cur.left > 0; ++pairs) {
+            const int tiles = cur.run();
+            cur.skip(p, tiles);
+            // after the last pair: its last P V
+            const int flush = cur.left <= 0;
+            if (lane == 0) {
+                ok = wait(&bar_q[pairs & 1], (pairs >> 1) & 1, 106, wc);
                 tc_fence_after();
-                const uint64_t qd = desc(sq + (n & 1) * C::kQBytes, 16);
-                for (int t = 0; t < tiles; ++t, ++gt) {
-                    const int s = gt % S;
-                    if (!fa_wait(&bar_k[s], (gt / S) & 1, 107, wc)) { ok = false; break; }
-                    tc_fence_after();
-                    // S_t's buffer was read before P_{t-2} was complete
-                    const uint64_t kd = desc(skv + s * 2 * TB + TB, 16);
+                const uint64_t qd = desc(sQ + (pairs & 1) * C::kQBytes, 16);
+#pragma unroll 1
+                for (int t = 0; ok && t < tiles + flush; ++t) {
+                    const int u = gt + t, s = u % S;
+                    if (t < tiles) {
+                        if (!(ok = wait(&bar_k[s], (u / S) & 1, 107, wc))) break;
+                        tc_fence_after();
+                        // S_u's buffer was read before P_{u-2} was complete
+                        const uint64_t kd = desc(sKV + s * 2 * TB + TB, 16);
 #pragma unroll
-                    for (int kk = 0; kk < C::kRowBytes / 32; ++kk) {
-                        const uint64_t a = kd + kmajor_step(kk, kTile * 128);
-                        const uint64_t b = qd + kmajor_step(kk, N * 128);
-                        if (F8) mma_ss_f8(tmem + (gt & 1) * N, a, b, idesc_s, kk > 0);
-                        else mma_ss(tmem + (gt & 1) * N, a, b, idesc_s, kk > 0);
+                        for (int kk = 0; kk < C::kRowBytes / 32; ++kk) {
+                            const uint64_t a = kd + kmajor_step(kk, kTile * 128);
+                            const uint64_t b = qd + kmajor_step(kk, N * 128);
+                            if (F8) mma_ss_f8(tmem + (u & 1) * N, a, b, idesc_s, kk > 0);
+                            else mma_ss(tmem + (u & 1) * N, a, b, idesc_s, kk > 0);
                     }
-                    mma_commit(&bar_s[gt & 1]);
-                    mma_commit(&bar_k_empty[s]);
-                    if (t + 1 == tiles) mma_commit(&bar_q_free[n & 1]);
-                    // P V one tile behind, across pairs: the softmax warps have
-                    // read a pair's O before they give the next pair's first P
-                    if (gt > 0 && !pv(gt - 1, first)) { ok = false; break; }
+                        mma_commit(&bar_s[u & 1]);
+                        mma_commit(&bar_k_empty[s]);
+                        if (t + 1 == tiles) mma_commit(&bar_q_free[pairs & 1]);
+                    }
+                    // P V one tile behind, across pairs: the softmax warps
+                    // have read a pair's O before they give the next
+                    // pair's first P
+                    if (behind) ok = pv(u - 1, first);
+                    behind = true;
                     first = t == 0;
                 }
-                cur.skip(p, tiles);
             }
-            if (ok && gt > 0) ok = pv(gt - 1, first);
-            if (!ok) {   // no MMA of this thread may still write TMEM at teardown
-                mma_commit(&bar_drain);
-                fa_wait(&bar_drain, 0, 108, WaitCtx{p.status, nullptr});
-            }
+            gt += tiles;
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+        }
+        if (lane == 0 && !ok) {   // no MMA of this thread may still write TMEM at teardown
+            mma_commit(&bar_drain);
+            wait(&bar_drain, 0, 108, dc);
         }
         __syncwarp();
     } else if (warp == 6) {
         // ---------------------------------------------------- query rows
         bool ok = true;
-        for (int n = 0; ok && cur.left > 0; ++n) {
-            if (n >= 2) ok = fa_wait_warp(&bar_q_free[n & 1], ((n >> 1) - 1) & 1, 109, wc);
+        int pairs = 0;
+        for (; cur.left > 0; ++pairs, cur.skip(p, cur.run())) {
+            if (pairs >= 2)
+                ok = wait_warp(&bar_q_free[pairs & 1], ((pairs >> 1) - 1) & 1, 109, wc);
             if (!ok) break;
-            uint8_t* dst = sQ + (n & 1) * C::kQBytes;
+            const uint32_t dst = sQ + (pairs & 1) * C::kQBytes;
             const __nv_bfloat16* src = p.q + ((long long)cur.b * p.Hkv + cur.g) * p.R * D;
             if constexpr (F8) {
-                constexpr int E = D / 32;         // entries of a row per lane
-                for (int r = 0; r < p.R; ++r) {
+                // eight lanes a row, D / 8 neighbouring entries each
+                constexpr int E = D / 8;
+                const int at = lane & 7;
+#pragma unroll 1
+                for (int r0 = 0; r0 < p.R; r0 += 4) {
+                    const int r = r0 + (lane >> 3);
+                    uint4 w[E / 8];
                     float x[E];
-                    float amax = 0.0f;
-                    const uint32_t* w = reinterpret_cast<const uint32_t*>(src + r * D) + lane * (E / 2);
+                    uint32_t amax = 0, c1[E / 4], c2[E / 4];
 #pragma unroll
-                    for (int e = 0; e < E / 2; ++e) {
-                        const uint32_t u = __ldg(w + e);
-                        x[2 * e] = __uint_as_float(u << 16);
-                        x[2 * e + 1] = __uint_as_float(u & 0xffff0000u);
+                    for (int e = 0; e < E / 8; ++e) {
+                        w[e] = make_uint4(0u, 0u, 0u, 0u);
+                        if (r < p.R)
+                            w[e] = __ldg(reinterpret_cast<const uint4*>(src + r * D + at * E) + e);
+                        const uint32_t u[4] = {w[e].x, w[e].y, w[e].z, w[e].w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            x[8 * e + 2 * i] = __uint_as_float(u[i] << 16);
+                            x[8 * e + 2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+                        }
                     }
+                    // magnitudes order like their bits; a NaN only shifts the scale
 #pragma unroll
-                    for (int e = 0; e < E; ++e) amax = fmaxf(amax, fabsf(x[e]));
-                    amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+                    for (int e = 0; e < E; ++e)
+                        amax = max(amax, __float_as_uint(x[e]) & 0x7fffffffu);
+#pragma unroll
+                    for (int off = 4; off > 0; off >>= 1)
+                        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
                     // 2^k amax in [2^7, 2^8); k <= 120 (smaller rows keep fewer bits)
-                    const int ex = (int)(__float_as_uint(amax) >> 23) - 127;
+                    const int ex = (int)(amax >> 23) - 127;
                     const int k = min(7 - ex, 120);
                     const float up = __uint_as_float((uint32_t)(127 + k) << 23);
-                    uint32_t c1 = 0, c2 = 0;
 #pragma unroll
-                    for (int e = 0; e < E; e += 2) {
-                        const float y0 = x[e] * up, y1 = x[e + 1] * up;
-                        const uint32_t h = pack_e4m3x2(y0, y1);
+                    for (int e = 0; e < E; e += 4) {
                         float v[4];
-                        unpack_e4m3x4(h, v);
-                        c1 |= h << (8 * e);
-                        c2 |= pack_e4m3x2(y0 - v[0], y1 - v[1]) << (8 * e);
+                        c1[e / 4] = pack_e4m3x4(x[e] * up, x[e + 1] * up, x[e + 2] * up,
+                                                x[e + 3] * up);
+                        unpack_e4m3x4(c1[e / 4], v);
+                        c2[e / 4] = pack_e4m3x4(fmaf(x[e], up, -v[0]), fmaf(x[e + 1], up, -v[1]),
+                                                fmaf(x[e + 2], up, -v[2]),
+                                                fmaf(x[e + 3], up, -v[3]));
                     }
-                    const int byte = lane * E, unit = byte >> 4;
-                    const int sw = C::kSw == 128 ? (r & 7) : ((r >> 1) & 3);
-                    uint8_t* to = dst + r * C::kSw + ((unit ^ sw) << 4) + (byte & 15);
-                    if (E == 4) {
-                        *reinterpret_cast<uint32_t*>(to) = c1;
-                        *reinterpret_cast<uint32_t*>(to + RP * C::kSw) = c2;
-                    } else {
-                        *reinterpret_cast<uint16_t*>(to) = (uint16_t)c1;
-                        *reinterpret_cast<uint16_t*>(to + RP * C::kSw) = (uint16_t)c2;
+                    if (r < p.R) {
+                        if constexpr (E == 16) {       // one 16-byte unit, swizzled by r & 7
+                            const uint32_t to = dst + r * 128 + ((at ^ (r & 7)) << 4);
+                            sts_v4(to, make_uint4(c1[0], c1[1], c1[2], c1[3]));
+                            sts_v4(to + RP * 128, make_uint4(c2[0], c2[1], c2[2], c2[3]));
+                        } else {                       // half of one, swizzled by r / 2 & 3
+                            const uint32_t to =
+                                dst + r * 64 + (((at >> 1) ^ ((r >> 1) & 3)) << 4) + (at & 1) * 8;
+                            sts_v2(to, c1[0], c1[1]);
+                            sts_v2(to + RP * 64, c2[0], c2[1]);
+                        }
                     }
                     // an infinite entry would saturate: the whole row becomes NaN
-                    if (lane == 0)
-                        q_scale[n & 1][r] =
+                    if (at == 0 && r < RP)
+                        q_scale[pairs & 1][r] =
                             ex == 128 ? CUDART_NAN_F
                                       : p.scale_log2 * __uint_as_float((uint32_t)(127 - k) << 23);
                 }
-                for (int r = p.R + lane; r < RP; r += 32) q_scale[n & 1][r] = 0.0f;
+#pragma unroll 1
+                for (int r = (p.R + 3) / 4 * 4 + lane; r < RP; r += 32) q_scale[pairs & 1][r] = 0.0f;
             } else {
-                constexpr int U = D / 8;          // 16-byte units of a row
+                constexpr int U = D / 8;      // 16-byte units of a row
+#pragma unroll 2
                 for (int e = lane; e < p.R * U; e += 32) {
                     const int r = e / U, u = e % U;
                     const uint4 w = __ldg(reinterpret_cast<const uint4*>(src) + e);
-                    *reinterpret_cast<uint4*>(dst + (u >> 3) * (N * 128) + r * 128 +
-                                              (((u & 7) ^ (r & 7)) << 4)) = w;
+                    sts_v4(dst + (u >> 3) * (N * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4), w);
                 }
             }
             fence_proxy_async_smem();
-            mbar_arrive(&bar_q[n & 1]);
-            cur.skip(p, cur.run());
+            mbar_arrive(&bar_q[pairs & 1]);
         }
         __syncwarp();
     } else {
         // ---------------------------------------------------- softmax
-        // Thread j holds key j of the tile.  A wait that gives up clears `ok`
-        // and skips the later waits, but every thread stays in step with the
-        // named barriers.
-        const int j = threadIdx.x;
-        const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-        const int seg_shift = min(p.ps_shift, 7);
-        // key j's scales in a stage: segment (j >> seg_shift), K's then V's
-        const int ks_at = ((j >> seg_shift) << (seg_shift + 1)) + (j & ((1 << seg_shift) - 1));
-        const int vs_at = ks_at + (1 << seg_shift);
+        // Thread j of a group holds key j of the tile and the group's eight
+        // rows.  A wait that gives up clears `ok` and skips the later waits, but
+        // every thread stays in step with the named barriers.
+        const int group = warp < 4 ? 0 : (warp >> 2) - 1, r0 = group * kRows;
+        const int quarter = warp & 3, j = quarter * 32 + lane;
+        const int bar_id = kSoftBar + group;
+        const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16) + r0;
+        const uint32_t max_w = smem_u32(row_max + r0) + quarter * 4;   // this warp's value, row r0
+        const uint32_t sum_w = smem_u32(row_sum + r0) + quarter * 4;
+        // where P's row r0 keeps key j, unswizzled
+        const uint32_t p_at = sP + r0 * 128 + (F8 ? j : (j >> 6) * (N * 128) + (j & 63) * 2);
         bool ok = true;
-        int gt = 0;
-        for (int n = 0; cur.left > 0; ++n) {
+        int gt = 0, pairs = 0;
+        for (; cur.left > 0; ++pairs) {
             const int tiles = cur.run();
-            float m[RP], l[RP], qc[RP];
+            float m[kRows], l[kRows], qc[kRows];
             if constexpr (F8) {
-                ok = ok && fa_wait_warp(&bar_q[n & 1], (n >> 1) & 1, 110, wc);
+                ok = ok && wait(&bar_q[pairs & 1], (pairs >> 1) & 1, 110, wc);
 #pragma unroll
-                for (int r = 0; r < RP; ++r) qc[r] = q_scale[n & 1][r];
+                for (int r = 0; r < kRows; ++r) qc[r] = q_scale[pairs & 1][r0 + r];
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar_q_free[n & 1]);
+                if (lane == 0) mbar_arrive(&bar_q_free[pairs & 1]);
             }
 #pragma unroll
-            for (int r = 0; r < RP; ++r) {
-                m[r] = -CUDART_INF_F;
+            for (int r = 0; r < kRows; ++r) {
+                m[r] = kNoMax;
                 l[r] = 0.0f;
             }
+#pragma unroll 1
             for (int t = 0; t < tiles; ++t) {
-                const int g_t = gt + t, s = g_t % S;
+                const int u = gt + t, s = u % S;
                 const int key = (cur.t + t) * kTile + j;
                 const int tile_end = (cur.t + t + 1) * kTile;
                 const bool tail = tile_end > cur.len;
-                uint32_t sr[N];
-                ok = ok && fa_wait_warp(&bar_s[g_t & 1], (g_t >> 1) & 1, 111, wc);
+                // S_u complete means P_{u-2} V_{u-2} complete too: a commit
+                // covers every MMA before it, and that one was issued before
+                // S_u, so P's buffer u & 1 may be written
+                ok = ok && wait(&bar_s[u & 1], (u >> 1) & 1, 111, wc);
+                if (F8 || tail) ok = ok && wait(&bar_v[s], (u / S) & 1, 112, wc);
+                __syncwarp();
                 tc_fence_after();
-                tmem_ld_cols<N>(tmem + lane_base + (g_t & 1) * N, sr);
-                if (F8 || tail) ok = ok && fa_wait_warp(&bar_v[s], (g_t / S) & 1, 112, wc);
+                uint32_t sa[8], sb[8];
+                tmem_ld8(lane_base + (u & 1) * N, sa);
+                if (F8) tmem_ld8(lane_base + (u & 1) * N + RP, sb);
+                tmem_ld_done8(sa);
+                if (F8) tmem_ld_done8(sb);
                 float ks = 1.0f, vs = 1.0f, lv = 0.0f;
                 if constexpr (F8) {
-                    ks = sScale[s * 2 * kTile + ks_at];
-                    vs = sScale[s * 2 * kTile + vs_at];
+                    ks = lds_f32(sScale + (s * 2 * kTile + j) * 4);
+                    vs = lds_f32(sScale + (s * 2 * kTile + kTile + j) * 4);
                     if (key >= cur.len) vs = 1.0f;          // may hold anything
-                    lv = fmaxf(__log2f(fabsf(vs)), kMinLogScale);
+                    lv = fmaxf(lg2(fabsf(vs)), kMinLogScale);
                 }
-                float x[RP];
+                float x[kRows];
 #pragma unroll
-                for (int r = 0; r < RP; ++r) {
+                for (int r = 0; r < kRows; ++r) {
                     if constexpr (F8)
-                        x[r] = (__uint_as_float(sr[r]) + __uint_as_float(sr[RP + r])) * (qc[r] * ks);
+                        x[r] = (__uint_as_float(sa[r]) + __uint_as_float(sb[r])) * (qc[r] * ks);
                     else
-                        x[r] = __uint_as_float(sr[r]) * p.scale_log2;
+                        x[r] = __uint_as_float(sa[r]) * p.scale_log2;
                 }
                 if (tile_end > cur.len - (p.causal ? p.Nq - 1 : 0)) {
 #pragma unroll
-                    for (int r = 0; r < RP; ++r) {
-                        const int end = p.causal ? cur.len - p.Nq + 1 + row_query[r] : cur.len;
+                    for (int r = 0; r < kRows; ++r) {
+                        const int end = p.causal ? cur.len - p.Nq + 1 + row_query[r0 + r] : cur.len;
                         if (key >= end) x[r] = -CUDART_INF_F;
                     }
                 }
                 // Does any score pass the running maximum by 2^kSlack?
+                const float slack = C::kSlack - lv;
                 bool need = false;
 #pragma unroll
-                for (int r = 0; r < RP; ++r) need |= x[r] > m[r] + (C::kSlack - lv);
-                if (named_bar_or(kSoftBar, 128, need)) {
+                for (int r = 0; r < kRows; ++r) need |= x[r] > m[r] + slack;
+                if (named_bar_or(bar_id, 128, need)) {
 #pragma unroll
-                    for (int r = 0; r < RP; ++r) {
+                    for (int r = 0; r < kRows; ++r) {
                         const int y = __reduce_max_sync(0xffffffffu, ordered(x[r] + lv));
-                        if (lane == r) row_part[warp * RP + r] = from_ordered(y);
+                        if (lane == r) sts_u32(max_w + r * 16, __float_as_uint(from_ordered(y)));
                     }
-                    named_bar_sync(kSoftBar, 128);
-                    float alpha[RP];
+                    named_bar_sync(bar_id, 128);
+                    float alpha[kRows];
 #pragma unroll
-                    for (int r = 0; r < RP; ++r) {
-                        const float mx = fmaxf(fmax3(row_part[r], row_part[RP + r],
-                                                     row_part[2 * RP + r]),
-                                               fmaxf(row_part[3 * RP + r], m[r]));
-                        alpha[r] = mx == m[r] ? 1.0f : ex2(m[r] - mx);
+                    for (int r = 0; r < kRows; ++r) {
+                        const float4 w4 = row_max[r0 + r];
+                        const float mx = fmaxf(fmax3(w4.x, w4.y, w4.z), fmaxf(w4.w, m[r]));
+                        alpha[r] = ex2(m[r] - mx);
                         m[r] = mx;
                         l[r] *= alpha[r];
                     }
                     if (t > 0) {
-                        ok = ok && fa_wait_warp(&bar_pv[(g_t - 1) & 1], ((g_t - 1) >> 1) & 1, 113,
-                                                wc);
+                        ok = ok && wait(&bar_pv[(u - 1) & 1], ((u - 1) >> 1) & 1, 113, wc);
+                        __syncwarp();
                         tc_fence_after();
-                        if (warp * 32 < D) {
-                            uint32_t ov[N];
-                            tmem_ld_cols<N>(tmem + lane_base + kColO, ov);
+                        if (quarter * 32 < D) {
+                            uint32_t oa[8], ob[8];
+                            tmem_ld8(lane_base + kColO, oa);
+                            if (F8) tmem_ld8(lane_base + kColO + RP, ob);
+                            tmem_ld_done8(oa);
+                            if (F8) tmem_ld_done8(ob);
 #pragma unroll
-                            for (int c = 0; c < N; ++c)
-                                if (c < RP || F8)
-                                    ov[c] = __float_as_uint(__uint_as_float(ov[c]) *
-                                                            alpha[c % RP]);
-#pragma unroll
-                            for (int c = 0; c < N; c += 16) {
-                                uint32_t part[16];
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) part[e] = ov[c + e];
-                                tmem_st16(tmem + lane_base + kColO + c, part);
+                            for (int r = 0; r < kRows; ++r) {
+                                oa[r] = __float_as_uint(__uint_as_float(oa[r]) * alpha[r]);
+                                if (F8) ob[r] = __float_as_uint(__uint_as_float(ob[r]) * alpha[r]);
                             }
+                            tmem_st8(lane_base + kColO, oa);
+                            if (F8) tmem_st8(lane_base + kColO + RP, ob);
                             tmem_st_wait();
                         }
                     }
                 }
-                // P's buffer: P_{t-2} V_{t-2} has read it
-                if (g_t >= 2)
-                    ok = ok && fa_wait_warp(&bar_pv[g_t & 1], ((g_t >> 1) - 1) & 1, 114, wc);
-                uint8_t* pb = sP + (g_t & 1) * C::kPBytes;
-                if constexpr (F8) {
-                    uint8_t* to = pb + (j & 15);
-                    const int unit = j >> 4;
-                    const float wv = vs * C::kPScale;
+                // P, at row r's swizzle (its 16-byte units exchanged by r & 7)
+                const uint32_t pw = p_at + (u & 1) * C::kPBytes;
+                const float wv = vs * C::kPScale;
 #pragma unroll
-                    for (int r = 0; r < RP; r += 2) {
-                        float w[2];
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const float mu = m[r + h] == -CUDART_INF_F ? 0.0f : m[r + h];
-                            const float e = ex2(x[r + h] - mu);
-                            l[r + h] += e;
-                            w[h] = e * wv;
-                        }
-                        const uint32_t h1 = pack_e4m3x2(w[0], w[1]);
+                for (int r = 0; r < kRows; r += 2) {
+                    const float e0 = ex2(x[r] - m[r]), e1 = ex2(x[r + 1] - m[r + 1]);
+                    l[r] += e0;
+                    l[r + 1] += e1;
+                    const uint32_t a0 = (pw ^ (r << 4)) + r * 128;
+                    const uint32_t a1 = (pw ^ ((r + 1) << 4)) + (r + 1) * 128;
+                    if constexpr (F8) {
+                        const float w0 = e0 * wv, w1 = e1 * wv;
+                        const uint32_t h1 = pack_e4m3x2(w0, w1);
                         float v[4];
                         unpack_e4m3x4(h1, v);
-                        const uint32_t h2 = pack_e4m3x2(w[0] - v[0], w[1] - v[1]);
-                        uint8_t* a0 = to + r * 128 + ((unit ^ (r & 7)) << 4);
-                        uint8_t* a1 = to + (r + 1) * 128 + ((unit ^ ((r + 1) & 7)) << 4);
-                        a0[0] = (uint8_t)h1;
-                        a1[0] = (uint8_t)(h1 >> 8);
-                        a0[RP * 128] = (uint8_t)h2;
-                        a1[RP * 128] = (uint8_t)(h2 >> 8);
-                    }
-                } else {
-                    uint8_t* to = pb + (j >> 6) * (N * 128) + (j & 7) * 2;
-                    const int unit = (j & 63) >> 3;
-#pragma unroll
-                    for (int r = 0; r < RP; ++r) {
-                        const float mu = m[r] == -CUDART_INF_F ? 0.0f : m[r];
-                        const float e = ex2(x[r] - mu);
-                        l[r] += e;
-                        *reinterpret_cast<__nv_bfloat16*>(to + r * 128 + ((unit ^ (r & 7)) << 4)) =
-                            __float2bfloat16_rn(e);
+                        const uint32_t h2 = pack_e4m3x2(w0 - v[0], w1 - v[1]);
+                        sts_u8(a0, h1);
+                        sts_u8(a1, h1 >> 8);
+                        sts_u8(a0 + RP * 128, h2);
+                        sts_u8(a1 + RP * 128, h2 >> 8);
+                    } else {
+                        const uint32_t h = pack_bf16x2(e0, e1);
+                        sts_u16(a0, (uint16_t)h);
+                        sts_u16(a1, (uint16_t)(h >> 16));
                     }
                 }
-                if (tail && key >= cur.len) {
-                    // V rows past the sequence may hold NaN, which a weight of
-                    // zero does not silence
-                    uint8_t* vrow = sKV + s * 2 * TB + j * C::kSw;
+                if (tail && group == 0 && key >= cur.len) {
+                    // V rows past the sequence may hold NaN, which a weight
+                    // of zero does not silence
+                    const uint32_t vrow = sKV + s * 2 * TB + j * C::kSw;
 #pragma unroll
-                    for (int c = 0; c < C::kChunks; ++c)
+                    for (int h = 0; h < C::kChunks; ++h)
 #pragma unroll
-                        for (int u = 0; u < C::kSw / 16; ++u)
-                            *reinterpret_cast<uint4*>(vrow + c * (kTile * C::kSw) + u * 16) =
-                                make_uint4(0u, 0u, 0u, 0u);
+                        for (int w = 0; w < C::kSw / 16; ++w)
+                            sts_v4(vrow + h * (kTile * C::kSw) + w * 16,
+                                   make_uint4(0u, 0u, 0u, 0u));
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
-                mbar_arrive(&bar_p[g_t & 1]);
+                mbar_arrive(&bar_p[u & 1]);
             }
             // The pair's part: O / l, and LSE (or O and LSE themselves).
-            const int g_last = gt + tiles - 1;
-            ok = ok && fa_wait_warp(&bar_pv[g_last & 1], (g_last >> 1) & 1, 115, wc);
-            tc_fence_after();
-            uint32_t ov[N];
-            tmem_ld_cols<N>(tmem + lane_base + kColO, ov);
             int row;
-            const float total = warp_row_sums<RP>(l, lane, row);
-            row_part[warp * RP + row] = total;            // several lanes, one value
-            named_bar_sync(kSoftBar, 128);
+            const float mine = warp_row_sums<kRows>(l, lane, row);
+            sts_u32(sum_w + row * 16, __float_as_uint(mine));    // several lanes, one value
+            named_bar_sync(bar_id, 128);
             const int pair = cur.b * p.Hkv + cur.g;
             const bool whole = tiles == tiles_of(cur.len);
-            const long long slot = (long long)blockIdx.x + pair;
-            const long long out_row = whole ? (long long)pair * p.R : slot * p.R;
+            const long long out_row = (long long)(whole ? pair : c + pair) * p.R + r0;
+            float inv[kRows], my_l = 0.0f, my_m = 0.0f;
 #pragma unroll
-            for (int r = 0; r < RP; ++r) {
-                if (r >= p.R) break;
-                const float lr = (row_part[r] + row_part[RP + r]) +
-                                 (row_part[2 * RP + r] + row_part[3 * RP + r]);
-                const float y = F8 ? __uint_as_float(ov[r]) + __uint_as_float(ov[(RP + r) % N])
-                                   : __uint_as_float(ov[r]);
-                const float out = lr == 0.0f ? 0.0f : y / (lr * C::kPScale);
-                if (warp * 32 < D) {
-                    if (whole)
-                        p.o[(out_row + r) * D + j] = __float2bfloat16_rn(out);
-                    else
-                        p.part_o[(out_row + r) * D + j] = out;
-                }
+            for (int r = 0; r < kRows; ++r) {
+                const float4 w4 = row_sum[r0 + r];
+                const float lr = (w4.x + w4.y) + (w4.z + w4.w);
                 if (j == r) {
-                    const float lse2 = lr == 0.0f ? -CUDART_INF_F : m[r] + log2f(lr);
-                    if (whole)
-                        p.lse[out_row + r] = lse2 * kLn2;
-                    else
-                        p.part_lse[out_row + r] = lse2;
+                    my_l = lr;
+                    my_m = m[r];
+                }
+                inv[r] = __fdividef(1.0f, lr * C::kPScale);
+                if (lr == 0.0f) inv[r] = -1.0f;                  // saw nothing
+            }
+            if (j < kRows && r0 + j < p.R) {
+                const float lse2 = my_l == 0.0f ? -CUDART_INF_F : add_log2(my_m, my_l);
+                if (whole)
+                    p.lse[out_row + j] = lse2 * kLn2;
+                else
+                    p.part_lse[out_row + j] = lse2;
+            }
+            const int last = gt + tiles - 1;
+            ok = ok && wait(&bar_pv[last & 1], (last >> 1) & 1, 115, wc);
+            __syncwarp();
+            tc_fence_after();
+            if (quarter * 32 < D) {
+                uint32_t oa[8], ob[8];
+                tmem_ld8(lane_base + kColO, oa);
+                if (F8) tmem_ld8(lane_base + kColO + RP, ob);
+                tmem_ld_done8(oa);
+                if (F8) tmem_ld_done8(ob);
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) {
+                    float y = __uint_as_float(oa[r]);
+                    if (F8) y += __uint_as_float(ob[r]);
+                    y = inv[r] < 0.0f ? 0.0f : y * inv[r];
+                    if (r0 + r < p.R) {
+                        if (whole)
+                            p.o[(out_row + r) * D + j] = __float2bfloat16_rn(y);
+                        else
+                            p.part_o[(out_row + r) * D + j] = y;
+                    }
                 }
             }
             gt += tiles;
@@ -708,20 +794,22 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
 // found while the split kernel still runs; after it, the parts' LSEs and the
 // first kPre parts of O come in one round trip.
 template <int D>
-__global__ void __launch_bounds__(256) fa_paged_combine_kernel(const PagedParams p, int rows) {
+__global__ void __launch_bounds__(256) fa_paged_combine_kernel(const __grid_constant__ PagedParams p, int rows) {
     constexpr int E = D / 32, kPre = 8;
     const int row = (int)((blockIdx.x * 256 + threadIdx.x) >> 5), lane = threadIdx.x & 31;
     const int pair = min(row, rows - 1) / p.R, r = row - pair * p.R;
     const int b = pair / p.Hkv, g = pair - b * p.Hkv;
-    int b0, b1, at, upto;
-    const int T = list_length(p, lane, b0, b1, at, upto);
+    const List list(p, lane);
+    const Plan plan(list.units, p.ctas);
     const int tiles = tiles_of(clamped_len(p, b));
-    for (int x = b0; x < b1 && x < b; ++x) at += tiles_of(clamped_len(p, x)) * p.Hkv;
-    // the lane whose sequences b is one of
-    const int first = __shfl_sync(0xffffffffu, at, b / ((p.B + 31) / 32)) + g * tiles;
-    const int nc = min(p.ctas, T);
-    const int c0 = tiles ? cta_of_tile(first, T, nc) : 0;
-    const int parts = tiles ? cta_of_tile(first + tiles - 1, T, nc) - c0 + 1 : 0;
+    int at = list.at;
+#pragma unroll 1
+    for (int x = list.b0; x < list.b1 && x < b; ++x) at += List::units_of(p, clamped_len(p, x));
+    // from the lane whose sequences b is one of; past the pair's extra units
+    const int first = __shfl_sync(0xffffffffu, at, b / ((p.B + 31) / 32)) +
+                      g * (tiles + kPairUnits) + kPairUnits;
+    const int c0 = tiles ? plan.cta_of(first) : 0;
+    const int parts = tiles ? plan.cta_of(first + tiles - 1) - c0 + 1 : 0;
     // Every thread waits here, also those with nothing to join: this grid must
     // not end before the split kernel, whose results the next one in the
     // stream may read.
@@ -745,12 +833,14 @@ __global__ void __launch_bounds__(256) fa_paged_combine_kernel(const PagedParams
 #pragma unroll
         for (int c = 0; c < E; ++c) pre[k][c] = k < parts ? __ldcg(op + k * ostep + 32 * c) : 0.0f;
     float mx = l0;
+#pragma unroll 1
     for (int s = lane + 32; s < parts; s += 32) mx = fmaxf(mx, __ldcg(lp + s * lstep));
     mx = from_ordered(__reduce_max_sync(0xffffffffu, ordered(mx)));
     if (mx == -CUDART_INF_F) mx = 0.0f;
     float acc[E], sum = 0.0f;
 #pragma unroll
     for (int c = 0; c < E; ++c) acc[c] = 0.0f;
+#pragma unroll 1
     for (int base = 0; base < parts; base += 32) {
         const int s = base + lane;
         const float ls = base == 0 ? l0 : (s < parts ? __ldcg(lp + s * lstep) : -CUDART_INF_F);
@@ -766,7 +856,7 @@ __global__ void __launch_bounds__(256) fa_paged_combine_kernel(const PagedParams
                 for (int c = 0; c < E; ++c) acc[c] = fmaf(wk, pre[k][c], acc[c]);
             }
         }
-#pragma unroll 8
+#pragma unroll 4
         for (; k < cnt; ++k) {
             const float wk = __shfl_sync(0xffffffffu, w, k);
 #pragma unroll
@@ -776,18 +866,19 @@ __global__ void __launch_bounds__(256) fa_paged_combine_kernel(const PagedParams
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    const float inv = __fdividef(1.0f, sum);
 #pragma unroll
     for (int c = 0; c < E; ++c)
-        o[32 * c] = __float2bfloat16_rn(sum == 0.0f ? 0.0f : acc[c] / sum);
-    if (lane == 0) p.lse[row] = sum == 0.0f ? -CUDART_INF_F : (mx + log2f(sum)) * kLn2;
+        o[32 * c] = __float2bfloat16_rn(sum == 0.0f ? 0.0f : acc[c] * inv);
+    if (lane == 0) p.lse[row] = sum == 0.0f ? -CUDART_INF_F : add_log2(mx, sum) * kLn2;
 }
 
-template <int D, bool F8, int RP>
+template <int D, bool F8, int G>
 cudaError_t launch_split(const CUtensorMap& tk, const CUtensorMap& tv, PagedParams& p,
                          cudaStream_t stream) {
-    using C = Cfg<D, F8, RP>;
+    using C = Cfg<D, F8, G>;
     static_assert(C::kSmem + 2048 <= 227 * 1024, "shared memory of one CTA");
-    auto kern = fa_decode_paged_kernel<D, F8, RP>;
+    auto kern = fa_decode_paged_kernel<D, F8, G>;
     static std::atomic<unsigned long long> configured{0};     // a bit a device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -804,16 +895,16 @@ cudaError_t launch_split(const CUtensorMap& tk, const CUtensorMap& tv, PagedPara
     if (grid > most) grid = most;
     p.ctas = (int)grid;
     count_launch();
-    kern<<<(unsigned)grid, kThreads, C::kSmem, stream>>>(tk, tv, p);
+    kern<<<(unsigned)grid, C::kThreads, C::kSmem, stream>>>(tk, tv, p);
     return cudaGetLastError();
 }
 
 template <int D, bool F8>
 cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, PagedParams& p,
                         cudaStream_t stream) {
-    if (p.R <= 8) return launch_split<D, F8, 8>(tk, tv, p, stream);
-    if (p.R <= 16) return launch_split<D, F8, 16>(tk, tv, p, stream);
-    return launch_split<D, F8, 32>(tk, tv, p, stream);
+    if (p.R <= 8) return launch_split<D, F8, 1>(tk, tv, p, stream);
+    if (p.R <= 16) return launch_split<D, F8, 2>(tk, tv, p, stream);
+    return launch_split<D, F8, 4>(tk, tv, p, stream);
 }
 
 template <int D>

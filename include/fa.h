@@ -434,8 +434,8 @@ FA_API fa_status fa_fwd_decode(const void* q, const void* k, const void* v, void
  * block_table[b][x / page_size] (DEVICE int32 [B][max_pages]).  One page may
  * stand in several tables (a shared prefix).  d in {64, 128}; page_size a
  * power of two from 16 to 256; max_pages * page_size < 2^30; n_pages * Hkv <
- * 2^31 (the pool itself may be larger than 2^31 elements).  FA_ERR_UNSUPPORTED
- * past these.  Pointers to floats and rows 16-byte aligned, to ints 4-byte.
+ * 2^31 (the pool itself may be larger than 2^31 elements); B * Hkv *
+ * (max_pages * page_size / 128 + 2) <= 2^30.  FA_ERR_UNSUPPORTED past these.  Pointers to floats and rows 16-byte aligned, to ints 4-byte.
  *
  * Table entries and lengths are read by the kernels.  Entries outside
  * [0, n_pages) that a call reaches give unspecified results (fa_fwd_decode_paged)
