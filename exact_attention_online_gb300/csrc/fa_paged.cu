@@ -34,8 +34,8 @@
 // order.
 //
 // Warps: 0-3 (8-11, .., 16-19) softmax, four warps for each eight query rows, which
-// need nothing of one another; 4 loads K, 7 V and the scales, 5 issues MMAs, 6 lays
-// out the next pair's queries.
+// need nothing of one another; 4 loads K, 7 V, 5 issues MMAs, 6 lays out the queries
+// of a pair and loads its scales.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -48,7 +48,7 @@ namespace fa {
 namespace {
 
 constexpr int kTile = 128;              // keys per tile
-constexpr int kRows = 8;                // query rows of a softmax group
+constexpr int kRows = 8;                // rows of Q, S and P a softmax group owns
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kMinLogScale = -60.0f;  // V scales below 2^-60 no longer move the reference
@@ -70,8 +70,9 @@ struct PagedParams {
     DeviceStatus* status;
 };
 
-// Sizes of one variant: head dimension, page type, groups of eight query rows.
-template <int D, bool F8, int G>
+// Sizes of one variant: head dimension, page type, groups of eight query rows, and
+// how many of its eight rows a group works on (the others are zero).
+template <int D, bool F8, int G, int W>
 struct Cfg {
     static constexpr int RP = kRows * G;
     static constexpr int kThreads = 128 + 128 * G;
@@ -91,6 +92,13 @@ struct Cfg {
     static constexpr int kRing = (kCtas == 2 ? 113 : 227) * 1024 - 1024 - 2048 - 2 * kQBytes -
                                  2 * kPBytes;
     static constexpr int kStages = kRing / (2 * kTileBytes + kScaleBytes);
+    // Tiles of K, and of V, in flight at once: about 112 KB an SM.  More of them
+    // slow the memory down: with all three stages in flight bf16 at d = 64 took
+    // 89.5 us instead of 84.6 (B16 H16, 8192 keys), at d = 128 162 instead of 157.
+    // Rows of 64 bytes are bound by the number of copies instead (103 us with this
+    // limit, 96 without: B16 H16, 16384 keys, pages of 16).
+    static constexpr int kAhead =
+        kRowBytes >= 128 ? (56 * 1024 / kCtas + kTileBytes / 2) / kTileBytes : kStages;
     static constexpr int kSmem =
         kStages * (2 * kTileBytes + kScaleBytes) + 2 * kQBytes + 2 * kPBytes + 1024;
     static constexpr int kTmemCols = 3 * kN <= 64 ? 64 : (3 * kN <= 128 ? 128 : 256);
@@ -261,12 +269,12 @@ __device__ __forceinline__ float warp_row_sums(float (&v)[RP], int lane, int& ro
     return v[0];
 }
 
-template <int D, bool F8, int G>
-__global__ void __launch_bounds__((Cfg<D, F8, G>::kThreads), (Cfg<D, F8, G>::kCtas))
+template <int D, bool F8, int G, int W>
+__global__ void __launch_bounds__((Cfg<D, F8, G, W>::kThreads), (Cfg<D, F8, G, W>::kCtas))
 fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v,
                        const __grid_constant__ PagedParams p) {
-    using C = Cfg<D, F8, G>;
+    using C = Cfg<D, F8, G, W>;
     constexpr int S = C::kStages, N = C::kN, TB = C::kTileBytes, RP = C::RP;
     constexpr uint32_t kColO = 2 * N;             // S buffers at 0 and N
     extern __shared__ uint8_t dsm_raw[];
@@ -311,7 +319,7 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
             for (int s = 0; s < S; ++s) {
                 mbar_init(&bar_k[s], 1);
                 mbar_init(&bar_k_empty[s], 1);
-                mbar_init(&bar_v[s], F8 ? 33 : 1);       // the scales: a lane each
+                mbar_init(&bar_v[s], F8 ? 33 : 1);       // and the scales: a lane each
                 mbar_init(&bar_v_empty[s], 1);
             }
             mbar_init(&bar_drain, 1);
@@ -338,6 +346,16 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
 
     Cursor cur(p, list, begin, plan.begin(c + 1) - begin);
 
+    const int seg_shift = min(p.ps_shift, 7), seg = 1 << seg_shift;
+    const int n_seg = kTile >> seg_shift, page_mask = (1 << p.ps_shift) - 1;
+    // The page of lane's segment of the cursor's tile (0 where there is none).
+    auto page_of = [&](const Cursor& at) {
+        const int key = at.t * kTile + lane * seg;
+        return (at.left > 0 && lane < n_seg && key < at.len)
+                   ? __ldg(p.table + (long long)at.b * p.max_pages + (key >> p.ps_shift))
+                   : 0;
+    };
+
     if (warp == 4 || warp == 7) {
         // ------------------------------------------------------- loads
         // Boxes of up to 128 keys of one page.  Lane i holds segment i's place
@@ -347,15 +365,9 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
         const CUtensorMap* map = is_v ? &tm_v : &tm_k;
         uint64_t* full = is_v ? bar_v : bar_k;
         uint64_t* empty = is_v ? bar_v_empty : bar_k_empty;
-        const int seg_shift = min(p.ps_shift, 7), seg = 1 << seg_shift;
-        const int n_seg = kTile >> seg_shift, page_mask = (1 << p.ps_shift) - 1;
         const int seg_bytes = seg * C::kSw;
-        auto page_of = [&](const Cursor& c) {
-            const int key = c.t * kTile + lane * seg;
-            return (c.left > 0 && lane < n_seg && key < c.len)
-                       ? __ldg(p.table + (long long)c.b * p.max_pages + (key >> p.ps_shift))
-                       : 0;
-        };
+        const uint64_t policy = l2_evict_first();
+        const int outside = p.n_pages * p.Hkv;
         bool ok = true;
         int gt = 0;                               // tiles loaded so far
         int page = page_of(cur);
@@ -368,10 +380,12 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
             const int have = min(n_seg, (at.len - at.t * kTile + seg - 1) >> seg_shift);
             const bool known = (unsigned)page < (unsigned)p.n_pages;
             // a page outside the pool reads as zeros (past the map's last row)
-            const int outer = (known ? page : p.n_pages) * p.Hkv + (known ? at.g : 0);
+            const int outer = known ? page * p.Hkv + at.g : outside;
             const int row = (at.t * kTile) & page_mask;      // of a page of 256; else 0
             if (gt >= S)
                 ok = wait_warp(&empty[s], ((gt / S) - 1) & 1, is_v ? 101 : 100, wc);
+            if (C::kAhead < S && gt >= C::kAhead)
+                ok = ok && wait_warp(&full[(gt - C::kAhead) % S], ((gt - C::kAhead) / S) & 1, 103, wc);
             if (!ok) break;
             const uint32_t stage = sKV + s * 2 * TB + (is_v ? 0 : TB);
             if (lane == 0) mbar_arrive_expect_tx(&full[s], have * seg_bytes * C::kChunks);
@@ -379,26 +393,12 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll 2
             for (int i = 0; i < have; ++i) {
                 const int at_row = __shfl_sync(0xffffffffu, outer, i);
-                if (lane == 0)
+                if (lane == 0) {
 #pragma unroll
-                    for (int c = 0; c < C::kChunks; ++c)
-                        tma_load_3d_at(stage + c * (kTile * C::kSw) + i * seg_bytes, map,
-                                       &full[s], c * (F8 ? C::kSw : C::kSw / 2), row, at_row);
-            }
-            if (F8 && is_v) {
-                // 128 keys' scales, four bytes a lane and copy
-                const uint32_t dst = sScale + (s * 2 * kTile + lane) * 4;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int j = 32 * i + lane;
-                    const int pg = __shfl_sync(0xffffffffu, known ? page : 0, j >> seg_shift);
-                    const float* src = p.scales +
-                                       (((long long)pg * p.Hkv + at.g) << (p.ps_shift + 1)) +
-                                       ((at.t * kTile + j) & page_mask);
-                    cp_async4(dst + 128 * i, src);
-                    cp_async4(dst + kTile * 4 + 128 * i, src + (1 << p.ps_shift));
+                    for (int h = 0; h < C::kChunks; ++h)
+                        tma_load_3d_at(stage + h * (kTile * C::kSw) + i * seg_bytes, map, &full[s],
+                                       h * (F8 ? C::kSw : C::kSw / 2), row, at_row, policy);
                 }
-                cp_async_arrive(&full[s]);
             }
             ++gt;
             page = page_next;
@@ -466,7 +466,7 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                             const uint64_t b = qd + kmajor_step(kk, N * 128);
                             if (F8) mma_ss_f8(tmem + (u & 1) * N, a, b, idesc_s, kk > 0);
                             else mma_ss(tmem + (u & 1) * N, a, b, idesc_s, kk > 0);
-                    }
+                        }
                         mma_commit(&bar_s[u & 1]);
                         mma_commit(&bar_k_empty[s]);
                         if (t + 1 == tiles) mma_commit(&bar_q_free[pairs & 1]);
@@ -488,10 +488,11 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
         }
         __syncwarp();
     } else if (warp == 6) {
-        // ---------------------------------------------------- query rows
+        // ---------------------------------- query rows, and e4m3's scales
         bool ok = true;
         int pairs = 0;
-        for (; cur.left > 0; ++pairs, cur.skip(p, cur.run())) {
+        int gt = 0;                               // tiles whose scales are loaded
+        while (cur.left > 0) {
             if (pairs >= 2)
                 ok = wait_warp(&bar_q_free[pairs & 1], ((pairs >> 1) - 1) & 1, 109, wc);
             if (!ok) break;
@@ -571,11 +572,40 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
             }
             fence_proxy_async_smem();
             mbar_arrive(&bar_q[pairs & 1]);
+            ++pairs;
+            if constexpr (F8) {
+                // 128 keys' scales a tile, four bytes a lane and copy
+                int page = page_of(cur);
+#pragma unroll 1
+                for (int t = cur.run(); ok && t > 0; --t, ++gt) {
+                    const Cursor at = cur;
+                    cur.skip(p, 1);
+                    const int page_next = page_of(cur);
+                    const int s = gt % S;
+                    if ((unsigned)page >= (unsigned)p.n_pages) page = 0;
+                    if (gt >= S) ok = wait_warp(&bar_v_empty[s], ((gt / S) - 1) & 1, 116, wc);
+                    const uint32_t dst = sScale + s * C::kScaleBytes + lane * 4;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int j = 32 * i + lane;
+                        const int pg = __shfl_sync(0xffffffffu, page, j >> seg_shift);
+                        const float* src = p.scales +
+                                           (((long long)pg * p.Hkv + at.g) << (p.ps_shift + 1)) +
+                                           ((at.t * kTile + j) & page_mask);
+                        cp_async4(dst + 128 * i, src);
+                        cp_async4(dst + kTile * 4 + 128 * i, src + (1 << p.ps_shift));
+                    }
+                    cp_async_arrive(&bar_v[s]);
+                    page = page_next;
+                }
+            } else {
+                cur.skip(p, cur.run());
+            }
         }
         __syncwarp();
     } else {
         // ---------------------------------------------------- softmax
-        // Thread j of a group holds key j of the tile and the group's eight
+        // Thread j of a group holds key j of the tile and the group's first W
         // rows.  A wait that gives up clears `ok` and skips the later waits, but
         // every thread stays in step with the named barriers.
         const int group = warp < 4 ? 0 : (warp >> 2) - 1, r0 = group * kRows;
@@ -590,16 +620,16 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
         int gt = 0, pairs = 0;
         for (; cur.left > 0; ++pairs) {
             const int tiles = cur.run();
-            float m[kRows], l[kRows], qc[kRows];
+            float m[W], l[W], qc[W];
             if constexpr (F8) {
                 ok = ok && wait(&bar_q[pairs & 1], (pairs >> 1) & 1, 110, wc);
 #pragma unroll
-                for (int r = 0; r < kRows; ++r) qc[r] = q_scale[pairs & 1][r0 + r];
+                for (int r = 0; r < W; ++r) qc[r] = q_scale[pairs & 1][r0 + r];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar_q_free[pairs & 1]);
             }
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) {
+            for (int r = 0; r < W; ++r) {
                 m[r] = kNoMax;
                 l[r] = 0.0f;
             }
@@ -616,21 +646,21 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                 if (F8 || tail) ok = ok && wait(&bar_v[s], (u / S) & 1, 112, wc);
                 __syncwarp();
                 tc_fence_after();
-                uint32_t sa[8], sb[8];
-                tmem_ld8(lane_base + (u & 1) * N, sa);
-                if (F8) tmem_ld8(lane_base + (u & 1) * N + RP, sb);
-                tmem_ld_done8(sa);
-                if (F8) tmem_ld_done8(sb);
+                uint32_t sa[W], sb[W];
+                tmem_ld(lane_base + (u & 1) * N, sa);
+                if (F8) tmem_ld(lane_base + (u & 1) * N + RP, sb);
+                tmem_ld_done(sa);
+                if (F8) tmem_ld_done(sb);
                 float ks = 1.0f, vs = 1.0f, lv = 0.0f;
                 if constexpr (F8) {
-                    ks = lds_f32(sScale + (s * 2 * kTile + j) * 4);
-                    vs = lds_f32(sScale + (s * 2 * kTile + kTile + j) * 4);
+                    ks = lds_f32(sScale + s * C::kScaleBytes + j * 4);
+                    vs = lds_f32(sScale + s * C::kScaleBytes + (kTile + j) * 4);
                     if (key >= cur.len) vs = 1.0f;          // may hold anything
                     lv = fmaxf(lg2(fabsf(vs)), kMinLogScale);
                 }
-                float x[kRows];
+                float x[W];
 #pragma unroll
-                for (int r = 0; r < kRows; ++r) {
+                for (int r = 0; r < W; ++r) {
                     if constexpr (F8)
                         x[r] = (__uint_as_float(sa[r]) + __uint_as_float(sb[r])) * (qc[r] * ks);
                     else
@@ -638,7 +668,7 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                 }
                 if (tile_end > cur.len - (p.causal ? p.Nq - 1 : 0)) {
 #pragma unroll
-                    for (int r = 0; r < kRows; ++r) {
+                    for (int r = 0; r < W; ++r) {
                         const int end = p.causal ? cur.len - p.Nq + 1 + row_query[r0 + r] : cur.len;
                         if (key >= end) x[r] = -CUDART_INF_F;
                     }
@@ -647,17 +677,17 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                 const float slack = C::kSlack - lv;
                 bool need = false;
 #pragma unroll
-                for (int r = 0; r < kRows; ++r) need |= x[r] > m[r] + slack;
+                for (int r = 0; r < W; ++r) need |= x[r] > m[r] + slack;
                 if (named_bar_or(bar_id, 128, need)) {
 #pragma unroll
-                    for (int r = 0; r < kRows; ++r) {
+                    for (int r = 0; r < W; ++r) {
                         const int y = __reduce_max_sync(0xffffffffu, ordered(x[r] + lv));
                         if (lane == r) sts_u32(max_w + r * 16, __float_as_uint(from_ordered(y)));
                     }
                     named_bar_sync(bar_id, 128);
-                    float alpha[kRows];
+                    float alpha[W];
 #pragma unroll
-                    for (int r = 0; r < kRows; ++r) {
+                    for (int r = 0; r < W; ++r) {
                         const float4 w4 = row_max[r0 + r];
                         const float mx = fmaxf(fmax3(w4.x, w4.y, w4.z), fmaxf(w4.w, m[r]));
                         alpha[r] = ex2(m[r] - mx);
@@ -669,18 +699,18 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                         __syncwarp();
                         tc_fence_after();
                         if (quarter * 32 < D) {
-                            uint32_t oa[8], ob[8];
-                            tmem_ld8(lane_base + kColO, oa);
-                            if (F8) tmem_ld8(lane_base + kColO + RP, ob);
-                            tmem_ld_done8(oa);
-                            if (F8) tmem_ld_done8(ob);
+                            uint32_t oa[W], ob[W];
+                            tmem_ld(lane_base + kColO, oa);
+                            if (F8) tmem_ld(lane_base + kColO + RP, ob);
+                            tmem_ld_done(oa);
+                            if (F8) tmem_ld_done(ob);
 #pragma unroll
-                            for (int r = 0; r < kRows; ++r) {
+                            for (int r = 0; r < W; ++r) {
                                 oa[r] = __float_as_uint(__uint_as_float(oa[r]) * alpha[r]);
                                 if (F8) ob[r] = __float_as_uint(__uint_as_float(ob[r]) * alpha[r]);
                             }
-                            tmem_st8(lane_base + kColO, oa);
-                            if (F8) tmem_st8(lane_base + kColO + RP, ob);
+                            tmem_st(lane_base + kColO, oa);
+                            if (F8) tmem_st(lane_base + kColO + RP, ob);
                             tmem_st_wait();
                         }
                     }
@@ -689,10 +719,14 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                 const uint32_t pw = p_at + (u & 1) * C::kPBytes;
                 const float wv = vs * C::kPScale;
 #pragma unroll
-                for (int r = 0; r < kRows; r += 2) {
-                    const float e0 = ex2(x[r] - m[r]), e1 = ex2(x[r + 1] - m[r + 1]);
+                for (int r = 0; r < W; r += 2) {
+                    const float e0 = ex2(x[r] - m[r]);
                     l[r] += e0;
-                    l[r + 1] += e1;
+                    float e1 = 0.0f;
+                    if (W > 1) {
+                        e1 = ex2(x[(r + 1) % W] - m[(r + 1) % W]);
+                        l[(r + 1) % W] += e1;
+                    }
                     const uint32_t a0 = (pw ^ (r << 4)) + r * 128;
                     const uint32_t a1 = (pw ^ ((r + 1) << 4)) + (r + 1) * 128;
                     if constexpr (F8) {
@@ -702,13 +736,15 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                         unpack_e4m3x4(h1, v);
                         const uint32_t h2 = pack_e4m3x2(w0 - v[0], w1 - v[1]);
                         sts_u8(a0, h1);
-                        sts_u8(a1, h1 >> 8);
                         sts_u8(a0 + RP * 128, h2);
-                        sts_u8(a1 + RP * 128, h2 >> 8);
+                        if (W > 1) {
+                            sts_u8(a1, h1 >> 8);
+                            sts_u8(a1 + RP * 128, h2 >> 8);
+                        }
                     } else {
                         const uint32_t h = pack_bf16x2(e0, e1);
                         sts_u16(a0, (uint16_t)h);
-                        sts_u16(a1, (uint16_t)(h >> 16));
+                        if (W > 1) sts_u16(a1, (uint16_t)(h >> 16));
                     }
                 }
                 if (tail && group == 0 && key >= cur.len) {
@@ -728,15 +764,15 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
             }
             // The pair's part: O / l, and LSE (or O and LSE themselves).
             int row;
-            const float mine = warp_row_sums<kRows>(l, lane, row);
+            const float mine = warp_row_sums<W>(l, lane, row);
             sts_u32(sum_w + row * 16, __float_as_uint(mine));    // several lanes, one value
             named_bar_sync(bar_id, 128);
             const int pair = cur.b * p.Hkv + cur.g;
             const bool whole = tiles == tiles_of(cur.len);
             const long long out_row = (long long)(whole ? pair : c + pair) * p.R + r0;
-            float inv[kRows], my_l = 0.0f, my_m = 0.0f;
+            float inv[W], my_l = 0.0f, my_m = 0.0f;
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) {
+            for (int r = 0; r < W; ++r) {
                 const float4 w4 = row_sum[r0 + r];
                 const float lr = (w4.x + w4.y) + (w4.z + w4.w);
                 if (j == r) {
@@ -746,7 +782,7 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                 inv[r] = __fdividef(1.0f, lr * C::kPScale);
                 if (lr == 0.0f) inv[r] = -1.0f;                  // saw nothing
             }
-            if (j < kRows && r0 + j < p.R) {
+            if (j < W && r0 + j < p.R) {
                 const float lse2 = my_l == 0.0f ? -CUDART_INF_F : add_log2(my_m, my_l);
                 if (whole)
                     p.lse[out_row + j] = lse2 * kLn2;
@@ -758,13 +794,13 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
             __syncwarp();
             tc_fence_after();
             if (quarter * 32 < D) {
-                uint32_t oa[8], ob[8];
-                tmem_ld8(lane_base + kColO, oa);
-                if (F8) tmem_ld8(lane_base + kColO + RP, ob);
-                tmem_ld_done8(oa);
-                if (F8) tmem_ld_done8(ob);
+                uint32_t oa[W], ob[W];
+                tmem_ld(lane_base + kColO, oa);
+                if (F8) tmem_ld(lane_base + kColO + RP, ob);
+                tmem_ld_done(oa);
+                if (F8) tmem_ld_done(ob);
 #pragma unroll
-                for (int r = 0; r < kRows; ++r) {
+                for (int r = 0; r < W; ++r) {
                     float y = __uint_as_float(oa[r]);
                     if (F8) y += __uint_as_float(ob[r]);
                     y = inv[r] < 0.0f ? 0.0f : y * inv[r];
@@ -873,12 +909,12 @@ __global__ void __launch_bounds__(256) fa_paged_combine_kernel(const __grid_cons
     if (lane == 0) p.lse[row] = sum == 0.0f ? -CUDART_INF_F : add_log2(mx, sum) * kLn2;
 }
 
-template <int D, bool F8, int G>
+template <int D, bool F8, int G, int W>
 cudaError_t launch_split(const CUtensorMap& tk, const CUtensorMap& tv, PagedParams& p,
                          cudaStream_t stream) {
-    using C = Cfg<D, F8, G>;
+    using C = Cfg<D, F8, G, W>;
     static_assert(C::kSmem + 2048 <= 227 * 1024, "shared memory of one CTA");
-    auto kern = fa_decode_paged_kernel<D, F8, G>;
+    auto kern = fa_decode_paged_kernel<D, F8, G, W>;
     static std::atomic<unsigned long long> configured{0};     // a bit a device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -902,9 +938,11 @@ cudaError_t launch_split(const CUtensorMap& tk, const CUtensorMap& tv, PagedPara
 template <int D, bool F8>
 cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, PagedParams& p,
                         cudaStream_t stream) {
-    if (p.R <= 8) return launch_split<D, F8, 1>(tk, tv, p, stream);
-    if (p.R <= 16) return launch_split<D, F8, 2>(tk, tv, p, stream);
-    return launch_split<D, F8, 4>(tk, tv, p, stream);
+    if (p.R == 1) return launch_split<D, F8, 1, 1>(tk, tv, p, stream);
+    if (p.R <= 4) return launch_split<D, F8, 1, 4>(tk, tv, p, stream);
+    if (p.R <= 8) return launch_split<D, F8, 1, 8>(tk, tv, p, stream);
+    if (p.R <= 16) return launch_split<D, F8, 2, 8>(tk, tv, p, stream);
+    return launch_split<D, F8, 4, 8>(tk, tv, p, stream);
 }
 
 template <int D>
