@@ -499,84 +499,93 @@ def attention_decode(q, k, v, causal: bool = True, scale: float | None = None, s
 
 
 # ------------------------------------------------------------- paged cache
-def _cache(k_pages, v_pages, block_table, kv_scales, B):
+# A decoding step makes these calls once a layer on little data, so their checks
+# (those of _ptr) ask for the current device once a call.
+def _arg(t, name, dtype, shape, cur):
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous() or t.get_device() != cur:
+        _ptr(t, name, dtype, shape)      # says what is wrong
+    return t.data_ptr()
+
+
+def _cache(k_pages, v_pages, block_table, kv_scales, cur):
     """Pointers and sizes of a paged cache: k_pages, v_pages [n_pages, Hkv, page_size, d]
     (bf16; torch.float8_e4m3fn with kv_scales fp32 [n_pages, Hkv, 2, page_size]),
     block_table int32 [B, max_pages]."""
     import torch
-    if k_pages.dim() != 4:
+    shape = k_pages.shape
+    if len(shape) != 4:
         raise ValueError("k_pages must be 4-D [n_pages, Hkv, page_size, d]")
-    if block_table.dim() != 2:
+    table = block_table.shape
+    if len(table) != 2:
         raise ValueError("block_table must be 2-D [B, max_pages]")
-    n_pages, Hkv, ps, d = k_pages.shape
-    max_pages = block_table.shape[1]
+    n_pages, Hkv, ps, d = shape
     if kv_scales is None:
         dtype, sp = torch.bfloat16, None
     else:
-        dtype, sp = torch.float8_e4m3fn, _f32(kv_scales, "kv_scales", (n_pages, Hkv, 2, ps))
-    return (_ptr(k_pages, "k_pages", dtype, None),
-            _ptr(v_pages, "v_pages", dtype, (n_pages, Hkv, ps, d)), sp,
-            _i32(block_table, "block_table", (B, max_pages)), n_pages, Hkv, ps, max_pages, d)
+        dtype = torch.float8_e4m3fn
+        sp = _arg(kv_scales, "kv_scales", torch.float32, (n_pages, Hkv, 2, ps), cur)
+    return (_arg(k_pages, "k_pages", dtype, shape, cur), _arg(v_pages, "v_pages", dtype, shape, cur),
+            sp, _arg(block_table, "block_table", torch.int32, table, cur), table[0], table[1],
+            n_pages, Hkv, ps, d)
 
 
-def _rows_shape(k, k_pages, layout):
-    """k as [B, Hkv, N, d] or packed [Hkv, total, d], agreeing with the pages."""
+def _move(name, rows_first, k, v, k_pages, v_pages, block_table, starts, counts, kv_scales,
+          stream, max_seqlen=None):
+    """fa_kv_append and fa_kv_gather, dense (k [B, Hkv, N, d], counts [B]) or, with max_seqlen,
+    packed (k [Hkv, total, d], counts = cu_seqlens [B + 1])."""
+    import torch
+    cur = _current_index()
+    packed = max_seqlen is not None
+    shape = k.shape
     if k_pages.dim() != 4:
         raise ValueError("k_pages must be 4-D [n_pages, Hkv, page_size, d]")
-    if k.dim() != len(layout) or k.shape[-3] != k_pages.shape[1] or k.shape[-1] != k_pages.shape[3]:
-        raise ValueError(f"k has shape {tuple(k.shape)}, expected [{', '.join(layout)}] of "
-                         f"k_pages {tuple(k_pages.shape)}")
-    return tuple(k.shape)
+    if len(shape) != (3 if packed else 4) or shape[-3] != k_pages.shape[1] or \
+            shape[-1] != k_pages.shape[3]:
+        raise ValueError(f"k has shape {tuple(shape)}, expected "
+                         f"{'[Hkv, total, d]' if packed else '[B, Hkv, N, d]'} of k_pages "
+                         f"{tuple(k_pages.shape)}")
+    kp, vp, sp, tp, B, mp, P, Hkv, ps, d = _cache(k_pages, v_pages, block_table, kv_scales, cur)
+    i32 = torch.int32
+    rows = (_arg(k, "k", torch.bfloat16, shape if packed else (B,) + shape[1:], cur),
+            _arg(v, "v", torch.bfloat16, shape, cur))
+    pages = (kp, vp, sp)
+    index = (tp, _arg(starts, "starts", i32, (B,), cur),
+             _arg(counts, "cu_seqlens", i32, (B + 1,), cur) if packed else
+             _arg(counts, "counts", i32, (B,), cur))
+    sizes = (B, int(max_seqlen), shape[1], Hkv) if packed else (B, Hkv, shape[2])
+    ends = (rows, pages) if rows_first else (pages, rows)
+    _check(getattr(lib(), name)(*ends[0], *ends[1], *index, *sizes, P, ps, mp, d,
+                                _stream(stream)), name)
 
 
 def fa_kv_append(k, v, k_pages, v_pages, block_table, starts, counts, kv_scales=None,
                  stream=None) -> None:
     """Rows i < counts[b] of k, v [B, Hkv, N, d] to positions starts[b] + i of sequence b;
     quantised to e4m3 when kv_scales is given.  starts, counts: int32 [B]."""
-    B = block_table.shape[0]
-    shape = _rows_shape(k, k_pages, ("B", "Hkv", "N", "d"))
-    kp, vp, sp, tp, P, Hkv, ps, mp, d = _cache(k_pages, v_pages, block_table, kv_scales, B)
-    _check(lib().fa_kv_append(_bf16(k, "k", (B,) + shape[1:]), _bf16(v, "v", shape), kp, vp, sp,
-                              tp, _i32(starts, "starts", (B,)), _i32(counts, "counts", (B,)),
-                              B, Hkv, shape[2], P, ps, mp, d, _stream(stream)), "fa_kv_append")
+    _move("fa_kv_append", True, k, v, k_pages, v_pages, block_table, starts, counts, kv_scales,
+          stream)
 
 
 def fa_kv_append_varlen(k, v, k_pages, v_pages, block_table, starts, cu_seqlens, max_seqlen: int,
                         kv_scales=None, stream=None) -> None:
     """fa_kv_append from a packed batch: k, v [Hkv, total, d], cu_seqlens int32 [B + 1]."""
-    B = block_table.shape[0]
-    shape = _rows_shape(k, k_pages, ("Hkv", "total", "d"))
-    kp, vp, sp, tp, P, Hkv, ps, mp, d = _cache(k_pages, v_pages, block_table, kv_scales, B)
-    _check(lib().fa_kv_append_varlen(_bf16(k, "k"), _bf16(v, "v", shape), kp, vp, sp, tp,
-                                     _i32(starts, "starts", (B,)),
-                                     _i32(cu_seqlens, "cu_seqlens", (B + 1,)), B, int(max_seqlen),
-                                     shape[1], Hkv, P, ps, mp, d, _stream(stream)),
-           "fa_kv_append_varlen")
+    _move("fa_kv_append_varlen", True, k, v, k_pages, v_pages, block_table, starts, cu_seqlens,
+          kv_scales, stream, int(max_seqlen))
 
 
 def fa_kv_gather(k_pages, v_pages, k, v, block_table, starts, counts, kv_scales=None,
                  stream=None) -> None:
     """Positions starts[b] .. starts[b] + counts[b] - 1 of sequence b into rows 0 ..
     counts[b] - 1 of bf16 k, v [B, Hkv, N, d]; the rows behind stay as they are."""
-    B = block_table.shape[0]
-    shape = _rows_shape(k, k_pages, ("B", "Hkv", "N", "d"))
-    kp, vp, sp, tp, P, Hkv, ps, mp, d = _cache(k_pages, v_pages, block_table, kv_scales, B)
-    _check(lib().fa_kv_gather(kp, vp, sp, _bf16(k, "k", (B,) + shape[1:]), _bf16(v, "v", shape),
-                              tp, _i32(starts, "starts", (B,)), _i32(counts, "counts", (B,)),
-                              B, Hkv, shape[2], P, ps, mp, d, _stream(stream)), "fa_kv_gather")
+    _move("fa_kv_gather", False, k, v, k_pages, v_pages, block_table, starts, counts, kv_scales,
+          stream)
 
 
 def fa_kv_gather_varlen(k_pages, v_pages, k, v, block_table, starts, cu_seqlens, max_seqlen: int,
                         kv_scales=None, stream=None) -> None:
     """fa_kv_gather into a packed batch: k, v [Hkv, total, d], cu_seqlens int32 [B + 1]."""
-    B = block_table.shape[0]
-    shape = _rows_shape(k, k_pages, ("Hkv", "total", "d"))
-    kp, vp, sp, tp, P, Hkv, ps, mp, d = _cache(k_pages, v_pages, block_table, kv_scales, B)
-    _check(lib().fa_kv_gather_varlen(kp, vp, sp, _bf16(k, "k"), _bf16(v, "v", shape), tp,
-                                     _i32(starts, "starts", (B,)),
-                                     _i32(cu_seqlens, "cu_seqlens", (B + 1,)), B, int(max_seqlen),
-                                     shape[1], Hkv, P, ps, mp, d, _stream(stream)),
-           "fa_kv_gather_varlen")
+    _move("fa_kv_gather_varlen", False, k, v, k_pages, v_pages, block_table, starts, cu_seqlens,
+          kv_scales, stream, int(max_seqlen))
 
 
 def fa_fwd_decode_paged_workspace_size(B: int, H: int, Hkv: int, Nq: int, d: int) -> int:
@@ -587,15 +596,21 @@ def fa_fwd_decode_paged(q, k_pages, v_pages, o, lse, block_table, seqlens, works
                         causal: bool, scale: float, kv_scales=None, stream=None) -> None:
     """q, o: bf16 [B, H, Nq, d]; lse: fp32 [B, H, Nq]; seqlens: int32 [B], the cached
     positions of each sequence, its Nq new ones included."""
-    B, H, Nq, d = _dims_of(q, "q")
-    kp, vp, sp, tp, P, Hkv, ps, mp, dk = _cache(k_pages, v_pages, block_table, kv_scales, B)
-    if dk != d:
-        raise ValueError(f"q {tuple(q.shape)} and k_pages {tuple(k_pages.shape)} disagree")
+    import torch
+    cur = _current_index()
+    qs = _dims_of(q, "q")
+    B, H, Nq, d = qs
+    kp, vp, sp, tp, tB, mp, P, Hkv, ps, dk = _cache(k_pages, v_pages, block_table, kv_scales, cur)
+    if dk != d or tB != B:
+        raise ValueError(f"q {tuple(q.shape)}, k_pages {tuple(k_pages.shape)} and block_table "
+                         f"{tuple(block_table.shape)} disagree")
     wp, wb = _ws(workspace)
-    _check(lib().fa_fwd_decode_paged(_bf16(q, "q"), kp, vp, sp, _bf16(o, "o", (B, H, Nq, d)),
-                                     _f32(lse, "lse", (B, H, Nq)), tp,
-                                     _i32(seqlens, "seqlens", (B,)), wp, wb, B, H, Hkv, Nq, P, ps,
-                                     mp, d, int(bool(causal)), float(scale), _stream(stream)),
+    bf, f32 = torch.bfloat16, torch.float32
+    _check(lib().fa_fwd_decode_paged(_arg(q, "q", bf, qs, cur), kp, vp, sp,
+                                     _arg(o, "o", bf, qs, cur), _arg(lse, "lse", f32, qs[:3], cur),
+                                     tp, _arg(seqlens, "seqlens", torch.int32, (B,), cur), wp, wb,
+                                     B, H, Hkv, Nq, P, ps, mp, d, 1 if causal else 0,
+                                     float(scale), _stream(stream)),
            "fa_fwd_decode_paged")
 
 
@@ -616,8 +631,10 @@ def attention_decode_paged(q, k_pages, v_pages, block_table, seqlens, causal: bo
         workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
     fa_fwd_decode_paged(q, k_pages, v_pages, o, lse, block_table, seqlens, workspace, causal,
                         scale, kv_scales, stream)
-    if stream is not None and hasattr(stream, "cuda_stream"):
+    if stream is not None and _stream(stream) != _stream(None):
         # the allocator must not hand these out again before the call's stream has used them
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream))
         for t in (o, lse, workspace):
             t.record_stream(stream)
     return o, lse

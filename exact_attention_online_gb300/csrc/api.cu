@@ -762,7 +762,8 @@ static fa_status kv_move(const void* k, const void* v, const void* k_pages, cons
                                 check_scales(kv_scales), check_ints(block_table),
                                 check_ints(starts), check_ints(counts)});
     if (st != FA_OK) return st;
-    if ((long long)B * Hkv >= (1LL << 31) / N) return FA_ERR_UNSUPPORTED;
+    if ((packed ? (long long)Hkv * total : (long long)B * Hkv * N) >= (1LL << 31))
+        return FA_ERR_UNSUPPORTED;
     int dev;
     if ((st = device_ready(&dev)) != FA_OK) return st;
     return from_cuda(launch_kv_move(

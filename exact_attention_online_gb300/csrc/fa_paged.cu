@@ -26,7 +26,7 @@
 // pages, and shared memory sees each of their bytes twice.
 //
 // Work: the tiles of all (sequence, kv head) pairs, in order, are one list that
-// the CTAs share evenly (Plan), found on the device from the lengths, so that
+// the CTAs share evenly (List), found on the device from the lengths, so that
 // ragged batches stay balanced and a captured graph replays with other lengths.
 // A pair that one CTA holds whole is finished there.  The others leave O / l and
 // LSE of their part in slot c + i (CTA c, pair i: along the list either c or i
@@ -113,32 +113,27 @@ __device__ __forceinline__ int clamped_len(const PagedParams& p, int b) {
 }
 __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
 
-// How the list is shared.  A pair counts its tiles and kPairUnits more units (its
-// queries, first maximum and epilogue); of the V units in all, CTA c holds c * size
-// .. (c + 1) * size - 1.  No CTA between two others is empty, so the CTAs of a pair
-// are neighbours.
-constexpr int kPairUnits = 1;
-struct Plan {
-    int V, size;
-    __device__ __forceinline__ Plan(int units, int ctas)
-        : V(units), size(max(1, (int)((unsigned)(units + ctas - 1) / (unsigned)ctas))) {}
-    __device__ __forceinline__ int begin(int c) const { return min(V, c * size); }
-    __device__ __forceinline__ int cta_of(int u) const {
-        return (int)((unsigned)u / (unsigned)size);
-    }
-};
-
-// The list as a warp sees it: lane l knows the units of ceil(B / 32)
-// neighbouring sequences b0 .. b1 - 1, which begin at unit `at`.
+// The list and how it is shared, as a warp sees it.  A pair counts its tiles and
+// `extra` units more (its queries, first maximum and epilogue; none where there is
+// a CTA for every tile); of the V units in all, CTA c holds c * size .. (c + 1) *
+// size - 1.  No CTA between two others is empty, so the CTAs of a pair are
+// neighbours.  Lane l knows the units of ceil(B / 32) neighbouring sequences b0 ..
+// b1 - 1, which begin at unit `at` and end at `upto`.
 struct List {
-    int b0, b1, at, upto, units;
+    int b0, b1, at, upto, V, size, extra;
     __device__ __forceinline__ List(const PagedParams& p, int lane) {
         const int per = (p.B + 31) / 32;
         b0 = min(p.B, lane * per);
         b1 = min(p.B, b0 + per);
-        int mine = 0;
+        int tiles = 0, seqs = 0;
 #pragma unroll 2
-        for (int b = b0; b < b1; ++b) mine += units_of(p, clamped_len(p, b));
+        for (int b = b0; b < b1; ++b) {
+            const int t = tiles_of(clamped_len(p, b));
+            tiles += t;
+            seqs += t > 0;
+        }
+        extra = __reduce_add_sync(0xffffffffu, tiles) * p.Hkv > p.ctas;
+        const int mine = (tiles + extra * seqs) * p.Hkv;
         upto = mine;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -146,22 +141,28 @@ struct List {
             if (lane >= off) upto += y;
         }
         at = upto - mine;
-        units = __shfl_sync(0xffffffffu, upto, 31);
+        V = __shfl_sync(0xffffffffu, upto, 31);
+        size = max(1, (int)((unsigned)(V + p.ctas - 1) / (unsigned)p.ctas));
     }
     // units of one sequence: all its kv heads
-    static __device__ __forceinline__ int units_of(const PagedParams& p, int len) {
-        return len > 0 ? (tiles_of(len) + kPairUnits) * p.Hkv : 0;
+    __device__ __forceinline__ int units_of(const PagedParams& p, int len) const {
+        return len > 0 ? (tiles_of(len) + extra) * p.Hkv : 0;
+    }
+    __device__ __forceinline__ int begin(int c) const { return min(V, c * size); }
+    __device__ __forceinline__ int cta_of(int u) const {
+        return (int)((unsigned)u / (unsigned)size);
     }
 };
 
 // A CTA's place in the list: pair (b, g), tile t of it, and the units left.
 struct Cursor {
-    int b, g, len, t, left;
-    // The place at unit `begin` of the list, for `units` units, found by a warp together.
-    __device__ __forceinline__ Cursor(const PagedParams& p, const List& list, int begin,
-                                      int units) {
+    int b, g, len, t, left, extra;
+    // The place of CTA c, found by a warp together.
+    __device__ __forceinline__ Cursor(const PagedParams& p, const List& list, int c) {
+        const int begin = list.begin(c);
         b = g = len = t = 0;
-        left = units;
+        extra = list.extra;
+        left = list.begin(c + 1) - begin;
         if (left <= 0) return;
         const bool here = list.at <= begin && begin < list.upto;
         const int owner = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
@@ -174,13 +175,13 @@ struct Cursor {
 #pragma unroll 1
             for (b = list.b0; b < list.b1; ++b) {
                 len = clamped_len(p, b);
-                const int u = List::units_of(p, len);
+                const int u = list.units_of(p, len);
                 if (begin < at + u) break;
                 at += u;
             }
-            const int per = tiles_of(len) + kPairUnits;
+            const int per = tiles_of(len) + extra;
             g = (begin - at) / per;
-            t = (begin - at) - g * per - kPairUnits;   // below 0: the pair's extra units
+            t = (begin - at) - g * per - extra;        // -1: the pair's extra unit
         }
         b = __shfl_sync(0xffffffffu, b, owner);
         g = __shfl_sync(0xffffffffu, g, owner);
@@ -200,7 +201,7 @@ struct Cursor {
         t += n;
         if (left <= 0 || t < tiles_of(len)) return;
         t = 0;
-        if ((left -= kPairUnits) <= 0) return;
+        if ((left -= extra) <= 0) return;
         if (++g < p.Hkv) return;
         g = 0;
         do {                            // left > 0: a sequence with keys follows
@@ -299,9 +300,8 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
 
     pdl_launch_dependents();
     const List list(p, lane);
-    const Plan plan(list.units, p.ctas);
-    const int c = blockIdx.x, begin = plan.begin(c);
-    if (begin >= plan.V) return;
+    const int c = blockIdx.x;
+    if (list.begin(c) >= list.V) return;
 
     if (warp == 4) {
         if (lane == 0) {
@@ -344,7 +344,7 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
     tc_fence_after();
     const uint32_t tmem = tmem_base_sh;
 
-    Cursor cur(p, list, begin, plan.begin(c + 1) - begin);
+    Cursor cur(p, list, c);
 
     const int seg_shift = min(p.ps_shift, 7), seg = 1 << seg_shift;
     const int n_seg = kTile >> seg_shift, page_mask = (1 << p.ps_shift) - 1;
@@ -836,16 +836,15 @@ __global__ void __launch_bounds__(256) fa_paged_combine_kernel(const __grid_cons
     const int pair = min(row, rows - 1) / p.R, r = row - pair * p.R;
     const int b = pair / p.Hkv, g = pair - b * p.Hkv;
     const List list(p, lane);
-    const Plan plan(list.units, p.ctas);
     const int tiles = tiles_of(clamped_len(p, b));
     int at = list.at;
 #pragma unroll 1
-    for (int x = list.b0; x < list.b1 && x < b; ++x) at += List::units_of(p, clamped_len(p, x));
-    // from the lane whose sequences b is one of; past the pair's extra units
+    for (int x = list.b0; x < list.b1 && x < b; ++x) at += list.units_of(p, clamped_len(p, x));
+    // from the lane whose sequences b is one of; past the pair's extra unit
     const int first = __shfl_sync(0xffffffffu, at, b / ((p.B + 31) / 32)) +
-                      g * (tiles + kPairUnits) + kPairUnits;
-    const int c0 = tiles ? plan.cta_of(first) : 0;
-    const int parts = tiles ? plan.cta_of(first + tiles - 1) - c0 + 1 : 0;
+                      g * (tiles + list.extra) + list.extra;
+    const int c0 = tiles ? list.cta_of(first) : 0;
+    const int parts = tiles ? list.cta_of(first + tiles - 1) - c0 + 1 : 0;
     // Every thread waits here, also those with nothing to join: this grid must
     // not end before the split kernel, whose results the next one in the
     // stream may read.

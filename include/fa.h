@@ -468,7 +468,7 @@ FA_API fa_status fa_kv_append(const void* k, const void* v, void* k_pages, void*
  * The same from a packed batch (the layout of fa_fwd_varlen()): k, v bf16
  * [Hkv][total][d], sequence b at rows cu_seqlens[b] .. cu_seqlens[b+1] - 1, its
  * first row to position starts[b]; no sequence longer than max_seqlen (rows
- * past it are not moved).
+ * past it are not moved, nor rows in no sequence).  Hkv * total < 2^31.
  */
 FA_API fa_status fa_kv_append_varlen(const void* k, const void* v, void* k_pages, void* v_pages,
                                      float* kv_scales, const int* block_table, const int* starts,

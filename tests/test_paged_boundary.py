@@ -83,7 +83,7 @@ def move(L, append, varlen, k=A, v=A, kp=A, vp=A, sc=None, table=A, starts=A, co
     (dict(ps=0), fa.FA_ERR_INVALID_ARG),
     (dict(ps=48), fa.FA_ERR_UNSUPPORTED),
     (dict(d=32), fa.FA_ERR_UNSUPPORTED),
-    (dict(B=1 << 15, Hkv=1 << 6, N=1 << 10), fa.FA_ERR_UNSUPPORTED),   # 2^31 rows
+    (dict(B=1 << 15, Hkv=1 << 6, N=1 << 10, total=1 << 25), fa.FA_ERR_UNSUPPORTED),  # 2^31 rows
     (dict(v=MIS), fa.FA_ERR_ALIGNMENT),
     (dict(kp=MIS), fa.FA_ERR_ALIGNMENT),
     (dict(sc=MIS), fa.FA_ERR_ALIGNMENT),
