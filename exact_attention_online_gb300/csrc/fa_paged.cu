@@ -94,9 +94,9 @@ struct Cfg {
     static constexpr int kStages = kRing / (2 * kTileBytes + kScaleBytes);
     // Tiles of K, and of V, in flight at once: about 112 KB an SM.  More of them
     // slow the memory down: with all three stages in flight bf16 at d = 64 took
-    // 89.5 us instead of 84.6 (B16 H16, 8192 keys), at d = 128 162 instead of 157.
-    // Rows of 64 bytes are bound by the number of copies instead (103 us with this
-    // limit, 96 without: B16 H16, 16384 keys, pages of 16).
+    // 84.1 us instead of 80.0 (B16 H16, 8192 keys), at d = 128 155.5 instead of 153.2
+    // (B8 Hkv8, 32768 keys).  Rows of 64 bytes are bound by the number of copies
+    // instead (103 us with this limit, 96 without: B16 H16, 16384 keys, pages of 16).
     static constexpr int kAhead =
         kRowBytes >= 128 ? (56 * 1024 / kCtas + kTileBytes / 2) / kTileBytes : kStages;
     static constexpr int kSmem =
@@ -104,8 +104,8 @@ struct Cfg {
     static constexpr int kTmemCols = 3 * kN <= 64 ? 64 : (3 * kN <= 128 ? 128 : 256);
     // How far a score may pass the running maximum before O is rescaled (log2):
     // bf16 P keeps its precision at any magnitude; e4m3 P ends at 448.
-    static constexpr float kSlack = F8 ? 2.0f : 8.0f;
-    static constexpr float kPScale = F8 ? 112.0f : 1.0f;           // 2^kSlack * kPScale = 448
+    static constexpr float kSlack = F8 ? 3.0f : 8.0f;
+    static constexpr float kPScale = F8 ? 56.0f : 1.0f;            // 2^kSlack * kPScale = 448
 };
 
 __device__ __forceinline__ int clamped_len(const PagedParams& p, int b) {
@@ -286,10 +286,10 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
     const uint32_t sQ = sKV + S * 2 * TB;         // [2]
     const uint32_t sP = sQ + 2 * C::kQBytes;      // [2]
     const uint32_t sScale = sP + 2 * C::kPBytes;  // [S][K, V][128] fp32
-    __shared__ uint64_t bar_q[2], bar_q_free[2], bar_k[S], bar_k_empty[S], bar_v[S],
-        bar_v_empty[S];
-    // S_t, P_t and P_t V_t signal barrier t & 1 (t counts the CTA's tiles)
-    __shared__ uint64_t bar_s[2], bar_p[2], bar_pv[2], bar_drain;
+    // per stage: K, V and e4m3's scales are there; S and P V of the stage's tile are
+    // complete, which also frees its K, and its V and scales
+    __shared__ uint64_t bar_k[S], bar_v[S], bar_x[S], bar_s[S], bar_pv[S];
+    __shared__ uint64_t bar_q[2], bar_q_free[2], bar_p[2], bar_drain;   // by pair; P by tile
     __shared__ float4 row_max[RP], row_sum[RP];   // a value a softmax warp
     __shared__ float q_scale[2][RP];              // e4m3: score of one code product, log2 units
     __shared__ int row_query[RP];                 // r % Nq
@@ -311,16 +311,15 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
             for (int x = 0; x < 2; ++x) {
                 mbar_init(&bar_q[x], 32);
                 mbar_init(&bar_q_free[x], F8 ? 1 + 4 * G : 1);   // the last S MMA; scales read
-                mbar_init(&bar_s[x], 1);
                 mbar_init(&bar_p[x], 128 * G);
-                mbar_init(&bar_pv[x], 1);
             }
 #pragma unroll 1
             for (int s = 0; s < S; ++s) {
                 mbar_init(&bar_k[s], 1);
-                mbar_init(&bar_k_empty[s], 1);
-                mbar_init(&bar_v[s], F8 ? 33 : 1);       // and the scales: a lane each
-                mbar_init(&bar_v_empty[s], 1);
+                mbar_init(&bar_v[s], 1);
+                mbar_init(&bar_x[s], 32);
+                mbar_init(&bar_s[s], 1);
+                mbar_init(&bar_pv[s], 1);
             }
             mbar_init(&bar_drain, 1);
             fence_mbar_init();
@@ -359,14 +358,15 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
     if (warp == 4 || warp == 7) {
         // ------------------------------------------------------- loads
         // Boxes of up to 128 keys of one page.  Lane i holds segment i's place
-        // in the pool, one lane issues: a copy takes uniform registers, so
-        // copies from several lanes would be issued in a loop over the lanes.
+        // in the pool; one elected lane issues, because a copy takes uniform
+        // registers.
         const bool is_v = warp == 7;
         const CUtensorMap* map = is_v ? &tm_v : &tm_k;
         uint64_t* full = is_v ? bar_v : bar_k;
-        uint64_t* empty = is_v ? bar_v_empty : bar_k_empty;
+        uint64_t* empty = is_v ? bar_pv : bar_s;
         const int seg_bytes = seg * C::kSw;
         const uint64_t policy = l2_evict_first();
+        const bool leader = elect_one();
         const int outside = p.n_pages * p.Hkv;
         bool ok = true;
         int gt = 0;                               // tiles loaded so far
@@ -388,12 +388,12 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                 ok = ok && wait_warp(&full[(gt - C::kAhead) % S], ((gt - C::kAhead) / S) & 1, 103, wc);
             if (!ok) break;
             const uint32_t stage = sKV + s * 2 * TB + (is_v ? 0 : TB);
-            if (lane == 0) mbar_arrive_expect_tx(&full[s], have * seg_bytes * C::kChunks);
+            if (leader) mbar_arrive_expect_tx(&full[s], have * seg_bytes * C::kChunks);
             __syncwarp();
 #pragma unroll 2
             for (int i = 0; i < have; ++i) {
                 const int at_row = __shfl_sync(0xffffffffu, outer, i);
-                if (lane == 0) {
+                if (leader) {
 #pragma unroll
                     for (int h = 0; h < C::kChunks; ++h)
                         tma_load_3d_at(stage + h * (kTile * C::kSw) + i * seg_bytes, map, &full[s],
@@ -418,26 +418,32 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
         auto desc = [&](uint32_t a, uint32_t lbo) {
             return C::kSw == 128 ? sdesc_sw128(a, lbo, kGroup) : sdesc_sw64(a, lbo, kGroup);
         };
+        // The warp stays together and one elected lane issues: descriptors then
+        // travel in uniform registers (a branch on lane == 0 cost 12 us of 49 with
+        // 16 rows an e4m3 cache: B8, four tokens, 8K to 16K keys).
+        const bool leader = elect_one();
         // O^T (+)= V_u^T P_u^T
         auto pv = [&](int u, bool first) -> bool {
             const int s = u % S;
-            if (!wait(&bar_p[u & 1], (u >> 1) & 1, 104, wc) ||
-                !wait(&bar_v[s], (u / S) & 1, 105, wc))
+            if (!wait_warp(&bar_p[u & 1], (u >> 1) & 1, 104, wc) ||
+                !wait_warp(&bar_v[s], (u / S) & 1, 105, wc))
                 return false;
             tc_fence_after();
             // V transposed: 32 (e4m3) or 16 keys a step; the next chunk of
             // columns (d = 64: K) is the leading-dimension stride
             const uint64_t vd = desc(sKV + s * 2 * TB, C::kChunks == 2 ? kTile * C::kSw : TB);
             const uint64_t pd = sdesc_sw128(sP + (u & 1) * C::kPBytes, 16, 1024);
+            if (leader) {
 #pragma unroll
-            for (int kk = 0; kk < (F8 ? 4 : 8); ++kk) {
-                const uint64_t a = vd + (uint64_t)(kk * (F8 ? 32 : 16) * C::kSw >> 4);
-                const uint64_t b = pd + kmajor_step(kk, N * 128);
-                if (F8) mma_ss_f8(tmem + kColO, a, b, idesc_o, !first || kk > 0);
-                else mma_ss(tmem + kColO, a, b, idesc_o, !first || kk > 0);
+                for (int kk = 0; kk < (F8 ? 4 : 8); ++kk) {
+                    const uint64_t a = vd + (uint64_t)(kk * (F8 ? 32 : 16) * C::kSw >> 4);
+                    const uint64_t b = pd + kmajor_step(kk, N * 128);
+                    if (F8) mma_ss_f8(tmem + kColO, a, b, idesc_o, !first || kk > 0);
+                    else mma_ss(tmem + kColO, a, b, idesc_o, !first || kk > 0);
+                }
+                mma_commit(&bar_pv[s]);
             }
-            mma_commit(&bar_pv[u & 1]);
-            mma_commit(&bar_v_empty[s]);
+            __syncwarp();
             return true;
         };
         bool ok = true;
@@ -448,18 +454,18 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
             cur.skip(p, tiles);
             // after the last pair: its last P V
             const int flush = cur.left <= 0;
-            if (lane == 0) {
-                ok = wait(&bar_q[pairs & 1], (pairs >> 1) & 1, 106, wc);
-                tc_fence_after();
-                const uint64_t qd = desc(sQ + (pairs & 1) * C::kQBytes, 16);
+            ok = wait_warp(&bar_q[pairs & 1], (pairs >> 1) & 1, 106, wc);
+            tc_fence_after();
+            const uint64_t qd = desc(sQ + (pairs & 1) * C::kQBytes, 16);
 #pragma unroll 1
-                for (int t = 0; ok && t < tiles + flush; ++t) {
-                    const int u = gt + t, s = u % S;
-                    if (t < tiles) {
-                        if (!(ok = wait(&bar_k[s], (u / S) & 1, 107, wc))) break;
-                        tc_fence_after();
-                        // S_u's buffer was read before P_{u-2} was complete
-                        const uint64_t kd = desc(sKV + s * 2 * TB + TB, 16);
+            for (int t = 0; ok && t < tiles + flush; ++t) {
+                const int u = gt + t, s = u % S;
+                if (t < tiles) {
+                    if (!(ok = wait_warp(&bar_k[s], (u / S) & 1, 107, wc))) break;
+                    tc_fence_after();
+                    // S_u's buffer was read before P_{u-2} was complete
+                    const uint64_t kd = desc(sKV + s * 2 * TB + TB, 16);
+                    if (leader) {
 #pragma unroll
                         for (int kk = 0; kk < C::kRowBytes / 32; ++kk) {
                             const uint64_t a = kd + kmajor_step(kk, kTile * 128);
@@ -467,22 +473,20 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                             if (F8) mma_ss_f8(tmem + (u & 1) * N, a, b, idesc_s, kk > 0);
                             else mma_ss(tmem + (u & 1) * N, a, b, idesc_s, kk > 0);
                         }
-                        mma_commit(&bar_s[u & 1]);
-                        mma_commit(&bar_k_empty[s]);
+                        mma_commit(&bar_s[s]);
                         if (t + 1 == tiles) mma_commit(&bar_q_free[pairs & 1]);
                     }
-                    // P V one tile behind, across pairs: the softmax warps
-                    // have read a pair's O before they give the next
-                    // pair's first P
-                    if (behind) ok = pv(u - 1, first);
-                    behind = true;
-                    first = t == 0;
+                    __syncwarp();
                 }
+                // P V one tile behind, across pairs: the softmax warps have read
+                // a pair's O before they give the next pair's first P
+                if (behind) ok = pv(u - 1, first);
+                behind = true;
+                first = t == 0;
             }
             gt += tiles;
-            ok = __shfl_sync(0xffffffffu, ok, 0);
         }
-        if (lane == 0 && !ok) {   // no MMA of this thread may still write TMEM at teardown
+        if (leader && !ok) {   // no MMA of this thread may still write TMEM at teardown
             mma_commit(&bar_drain);
             wait(&bar_drain, 0, 108, dc);
         }
@@ -583,7 +587,7 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                     const int page_next = page_of(cur);
                     const int s = gt % S;
                     if ((unsigned)page >= (unsigned)p.n_pages) page = 0;
-                    if (gt >= S) ok = wait_warp(&bar_v_empty[s], ((gt / S) - 1) & 1, 116, wc);
+                    if (gt >= S) ok = wait_warp(&bar_pv[s], ((gt / S) - 1) & 1, 116, wc);
                     const uint32_t dst = sScale + s * C::kScaleBytes + lane * 4;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -595,13 +599,14 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                         cp_async4(dst + 128 * i, src);
                         cp_async4(dst + kTile * 4 + 128 * i, src + (1 << p.ps_shift));
                     }
-                    cp_async_arrive(&bar_v[s]);
+                    cp_async_arrive(&bar_x[s]);
                     page = page_next;
                 }
             } else {
                 cur.skip(p, cur.run());
             }
         }
+        if (F8) cp_async_wait_all();
         __syncwarp();
     } else {
         // ---------------------------------------------------- softmax
@@ -642,8 +647,8 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                 // S_u complete means P_{u-2} V_{u-2} complete too: a commit
                 // covers every MMA before it, and that one was issued before
                 // S_u, so P's buffer u & 1 may be written
-                ok = ok && wait(&bar_s[u & 1], (u >> 1) & 1, 111, wc);
-                if (F8 || tail) ok = ok && wait(&bar_v[s], (u / S) & 1, 112, wc);
+                ok = ok && wait(&bar_s[s], (u / S) & 1, 111, wc);
+                if (F8) ok = ok && wait(&bar_x[s], (u / S) & 1, 112, wc);
                 __syncwarp();
                 tc_fence_after();
                 uint32_t sa[W], sb[W];
@@ -695,7 +700,7 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                         l[r] *= alpha[r];
                     }
                     if (t > 0) {
-                        ok = ok && wait(&bar_pv[(u - 1) & 1], ((u - 1) >> 1) & 1, 113, wc);
+                        ok = ok && wait(&bar_pv[(u - 1) % S], ((u - 1) / S) & 1, 113, wc);
                         __syncwarp();
                         tc_fence_after();
                         if (quarter * 32 < D) {
@@ -730,11 +735,9 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                     const uint32_t a0 = (pw ^ (r << 4)) + r * 128;
                     const uint32_t a1 = (pw ^ ((r + 1) << 4)) + (r + 1) * 128;
                     if constexpr (F8) {
-                        const float w0 = e0 * wv, w1 = e1 * wv;
-                        const uint32_t h1 = pack_e4m3x2(w0, w1);
-                        float v[4];
-                        unpack_e4m3x4(h1, v);
-                        const uint32_t h2 = pack_e4m3x2(w0 - v[0], w1 - v[1]);
+                        // by way of fp16, whose 11 bits hold both terms' 8
+                        uint32_t h1, h2;
+                        split_e4m3x2(pack_f16x2(e0 * wv, e1 * wv), h1, h2);
                         sts_u8(a0, h1);
                         sts_u8(a0 + RP * 128, h2);
                         if (W > 1) {
@@ -747,12 +750,13 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                         if (W > 1) sts_u16(a1, (uint16_t)(h >> 16));
                     }
                 }
-                if (tail && group == 0 && key >= cur.len) {
+                if (tail && group == 0) {
                     // V rows past the sequence may hold NaN, which a weight
                     // of zero does not silence
+                    ok = ok && wait(&bar_v[s], (u / S) & 1, 117, wc);
                     const uint32_t vrow = sKV + s * 2 * TB + j * C::kSw;
 #pragma unroll
-                    for (int h = 0; h < C::kChunks; ++h)
+                    for (int h = 0; h < C::kChunks && key >= cur.len; ++h)
 #pragma unroll
                         for (int w = 0; w < C::kSw / 16; ++w)
                             sts_v4(vrow + h * (kTile * C::kSw) + w * 16,
@@ -790,7 +794,7 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                     p.part_lse[out_row + j] = lse2;
             }
             const int last = gt + tiles - 1;
-            ok = ok && wait(&bar_pv[last & 1], (last >> 1) & 1, 115, wc);
+            ok = ok && wait(&bar_pv[last % S], (last / S) & 1, 115, wc);
             __syncwarp();
             tc_fence_after();
             if (quarter * 32 < D) {

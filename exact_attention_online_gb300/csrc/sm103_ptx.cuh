@@ -184,6 +184,10 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
                  : "memory");
 }
 
+__device__ __forceinline__ void cp_async_wait_all() {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
 // Bulk reduction shared -> global, fp32 add (16-byte aligned, size % 16 == 0).
 __device__ __forceinline__ void bulk_reduce_add_f32(float* dst, const void* src, uint32_t bytes) {
     asm volatile(
@@ -541,6 +545,18 @@ __device__ __forceinline__ void unpack_e4m3x4(uint32_t w, float (&x)[4]) {
         "cvt.rn.f16x2.e4m3x2 %1, h;}" : "=r"(lo), "=r"(hi) : "r"(w));
     unpack_f16x2(lo, x[0], x[1]);
     unpack_f16x2(hi, x[2], x[3]);
+}
+
+// Two fp16 values of magnitude up to 448 as the sums of two e4m3 numbers each:
+// `hi` the nearest codes, `lo` the nearest of what is left (in bits 0-15).
+__device__ __forceinline__ void split_e4m3x2(uint32_t w, uint32_t& hi, uint32_t& lo) {
+    asm("{.reg .b16 h, l;\n\t.reg .b32 v, r;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 h, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 v, h;\n\t"
+        "sub.rn.f16x2 r, %2, v;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 l, r;\n\t"
+        "cvt.u32.u16 %0, h;\n\t"
+        "cvt.u32.u16 %1, l;}" : "=r"(hi), "=r"(lo) : "r"(w));
 }
 
 // Paired fp32 arithmetic (one instruction for two lanes of a 64-bit register
