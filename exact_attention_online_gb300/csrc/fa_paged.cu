@@ -299,10 +299,6 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     pdl_launch_dependents();
-    const List list(p, lane);
-    const int c = blockIdx.x;
-    if (list.begin(c) >= list.V) return;
-
     if (warp == 4) {
         if (lane == 0) {
             tma_prefetch_desc(&tm_k);
@@ -342,8 +338,11 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base_sh;
-
-    Cursor cur(p, list, c);
+    // Up to here nothing is read that an earlier kernel may have written: it may
+    // still run.
+    pdl_wait();
+    const int c = blockIdx.x;
+    Cursor cur(p, List(p, lane), c);
 
     const int seg_shift = min(p.ps_shift, 7), seg = 1 << seg_shift;
     const int n_seg = kTile >> seg_shift, page_mask = (1 << p.ps_shift) - 1;
@@ -836,6 +835,7 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
 template <int D>
 __global__ void __launch_bounds__(256) fa_paged_combine_kernel(const __grid_constant__ PagedParams p, int rows) {
     constexpr int E = D / 32, kPre = 8;
+    pdl_launch_dependents();
     const int row = (int)((blockIdx.x * 256 + threadIdx.x) >> 5), lane = threadIdx.x & 31;
     const int pair = min(row, rows - 1) / p.R, r = row - pair * p.R;
     const int b = pair / p.Hkv, g = pair - b * p.Hkv;
@@ -912,6 +912,25 @@ __global__ void __launch_bounds__(256) fa_paged_combine_kernel(const __grid_cons
     if (lane == 0) p.lse[row] = sum == 0.0f ? -CUDART_INF_F : add_log2(mx, sum) * kLn2;
 }
 
+// A launch whose blocks may come in while the kernel before in the stream still
+// runs; they wait for it (pdl_wait) before they read what it wrote.
+template <typename... Params, typename... Args>
+cudaError_t launch_pdl(void (*kern)(Params...), unsigned grid, unsigned threads, size_t smem,
+                       cudaStream_t stream, const Args&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    count_launch();
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 template <int D, bool F8, int G, int W>
 cudaError_t launch_split(const CUtensorMap& tk, const CUtensorMap& tv, PagedParams& p,
                          cudaStream_t stream) {
@@ -933,9 +952,7 @@ cudaError_t launch_split(const CUtensorMap& tk, const CUtensorMap& tv, PagedPara
     if (grid > kPagedMaxCtas) grid = kPagedMaxCtas;
     if (grid > most) grid = most;
     p.ctas = (int)grid;
-    count_launch();
-    kern<<<(unsigned)grid, C::kThreads, C::kSmem, stream>>>(tk, tv, p);
-    return cudaGetLastError();
+    return launch_pdl(kern, (unsigned)grid, C::kThreads, C::kSmem, stream, tk, tv, p);
 }
 
 template <int D, bool F8>
@@ -951,18 +968,8 @@ cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, PagedParam
 template <int D>
 cudaError_t launch_combine(const PagedParams& p, cudaStream_t stream) {
     const int rows = p.B * p.Hkv * p.R;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((rows + 7) / 8));
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
-    // its blocks come in while the split kernel still runs and wait for it
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    count_launch();
-    return cudaLaunchKernelEx(&cfg, fa_paged_combine_kernel<D>, p, rows);
+    return launch_pdl(fa_paged_combine_kernel<D>, (unsigned)((rows + 7) / 8), 256, 0, stream, p,
+                      rows);
 }
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
