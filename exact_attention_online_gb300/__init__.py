@@ -499,12 +499,12 @@ def attention_decode(q, k, v, causal: bool = True, scale: float | None = None, s
 
 
 # ------------------------------------------------------------- paged cache
-# A decoding step makes these calls once a layer on little data, so their checks
-# (those of _ptr) ask for the current device once a call.
+# A decoding step makes these calls once a layer on little data: their checks are
+# those of _ptr, with the current device asked for once a call.
 def _arg(t, name, dtype, shape, cur):
-    if t.shape != shape or t.dtype != dtype or not t.is_contiguous() or t.get_device() != cur:
-        _ptr(t, name, dtype, shape)      # says what is wrong
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.get_device() == cur and t.is_contiguous():
+        return t.data_ptr()
+    return _ptr(t, name, dtype, shape)   # says what is wrong
 
 
 def _cache(k_pages, v_pages, block_table, kv_scales, cur):
@@ -512,80 +512,79 @@ def _cache(k_pages, v_pages, block_table, kv_scales, cur):
     (bf16; torch.float8_e4m3fn with kv_scales fp32 [n_pages, Hkv, 2, page_size]),
     block_table int32 [B, max_pages]."""
     import torch
-    shape = k_pages.shape
+    shape, table = k_pages.shape, block_table.shape
     if len(shape) != 4:
         raise ValueError("k_pages must be 4-D [n_pages, Hkv, page_size, d]")
-    table = block_table.shape
     if len(table) != 2:
         raise ValueError("block_table must be 2-D [B, max_pages]")
-    n_pages, Hkv, ps, d = shape
     if kv_scales is None:
         dtype, sp = torch.bfloat16, None
     else:
         dtype = torch.float8_e4m3fn
-        sp = _arg(kv_scales, "kv_scales", torch.float32, (n_pages, Hkv, 2, ps), cur)
+        sp = _arg(kv_scales, "kv_scales", torch.float32, (shape[0], shape[1], 2, shape[2]), cur)
     return (_arg(k_pages, "k_pages", dtype, shape, cur), _arg(v_pages, "v_pages", dtype, shape, cur),
-            sp, _arg(block_table, "block_table", torch.int32, table, cur), table[0], table[1],
-            n_pages, Hkv, ps, d)
+            sp, _arg(block_table, "block_table", torch.int32, table, cur))
 
 
-def _move(name, rows_first, k, v, k_pages, v_pages, block_table, starts, counts, kv_scales,
-          stream, max_seqlen=None):
+def _move(call, append, k, v, k_pages, v_pages, block_table, starts, counts, kv_scales, stream,
+          max_seqlen=None):
     """fa_kv_append and fa_kv_gather, dense (k [B, Hkv, N, d], counts [B]) or, with max_seqlen,
     packed (k [Hkv, total, d], counts = cu_seqlens [B + 1])."""
     import torch
+    bf, i32 = torch.bfloat16, torch.int32
     cur = _current_index()
+    shape, pool, table = k.shape, k_pages.shape, block_table.shape
+    B = table[0]
     packed = max_seqlen is not None
-    shape = k.shape
-    if k_pages.dim() != 4:
-        raise ValueError("k_pages must be 4-D [n_pages, Hkv, page_size, d]")
-    if len(shape) != (3 if packed else 4) or shape[-3] != k_pages.shape[1] or \
-            shape[-1] != k_pages.shape[3]:
+    if len(pool) == 4 and (len(shape) != (3 if packed else 4) or shape[-1] != pool[3] or
+                           shape[-3] != pool[1] or not packed and shape[0] != B):
         raise ValueError(f"k has shape {tuple(shape)}, expected "
                          f"{'[Hkv, total, d]' if packed else '[B, Hkv, N, d]'} of k_pages "
-                         f"{tuple(k_pages.shape)}")
-    kp, vp, sp, tp, B, mp, P, Hkv, ps, d = _cache(k_pages, v_pages, block_table, kv_scales, cur)
-    i32 = torch.int32
-    rows = (_arg(k, "k", torch.bfloat16, shape if packed else (B,) + shape[1:], cur),
-            _arg(v, "v", torch.bfloat16, shape, cur))
-    pages = (kp, vp, sp)
-    index = (tp, _arg(starts, "starts", i32, (B,), cur),
-             _arg(counts, "cu_seqlens", i32, (B + 1,), cur) if packed else
-             _arg(counts, "counts", i32, (B,), cur))
-    sizes = (B, int(max_seqlen), shape[1], Hkv) if packed else (B, Hkv, shape[2])
-    ends = (rows, pages) if rows_first else (pages, rows)
-    _check(getattr(lib(), name)(*ends[0], *ends[1], *index, *sizes, P, ps, mp, d,
-                                _stream(stream)), name)
+                         f"{tuple(pool)} and block_table {tuple(table)}")
+    kp, vp, sp, tp = _cache(k_pages, v_pages, block_table, kv_scales, cur)
+    rk, rv = _arg(k, "k", bf, shape, cur), _arg(v, "v", bf, shape, cur)
+    st = _arg(starts, "starts", i32, (B,), cur)
+    if packed:
+        ct = _arg(counts, "cu_seqlens", i32, (B + 1,), cur)
+        sizes = (B, max_seqlen, shape[1], pool[1])
+    else:
+        ct = _arg(counts, "counts", i32, (B,), cur)
+        sizes = (B, pool[1], shape[2])
+    if append:
+        return call(rk, rv, kp, vp, sp, tp, st, ct, *sizes, pool[0], pool[2], table[1], pool[3],
+                    _stream(stream))
+    return call(kp, vp, sp, rk, rv, tp, st, ct, *sizes, pool[0], pool[2], table[1], pool[3],
+                _stream(stream))
 
 
 def fa_kv_append(k, v, k_pages, v_pages, block_table, starts, counts, kv_scales=None,
                  stream=None) -> None:
     """Rows i < counts[b] of k, v [B, Hkv, N, d] to positions starts[b] + i of sequence b;
     quantised to e4m3 when kv_scales is given.  starts, counts: int32 [B]."""
-    _move("fa_kv_append", True, k, v, k_pages, v_pages, block_table, starts, counts, kv_scales,
-          stream)
+    _check(_move(lib().fa_kv_append, True, k, v, k_pages, v_pages, block_table, starts, counts,
+                 kv_scales, stream), "fa_kv_append")
 
 
 def fa_kv_append_varlen(k, v, k_pages, v_pages, block_table, starts, cu_seqlens, max_seqlen: int,
                         kv_scales=None, stream=None) -> None:
     """fa_kv_append from a packed batch: k, v [Hkv, total, d], cu_seqlens int32 [B + 1]."""
-    _move("fa_kv_append_varlen", True, k, v, k_pages, v_pages, block_table, starts, cu_seqlens,
-          kv_scales, stream, int(max_seqlen))
+    _check(_move(lib().fa_kv_append_varlen, True, k, v, k_pages, v_pages, block_table, starts,
+                 cu_seqlens, kv_scales, stream, int(max_seqlen)), "fa_kv_append_varlen")
 
 
 def fa_kv_gather(k_pages, v_pages, k, v, block_table, starts, counts, kv_scales=None,
                  stream=None) -> None:
     """Positions starts[b] .. starts[b] + counts[b] - 1 of sequence b into rows 0 ..
     counts[b] - 1 of bf16 k, v [B, Hkv, N, d]; the rows behind stay as they are."""
-    _move("fa_kv_gather", False, k, v, k_pages, v_pages, block_table, starts, counts, kv_scales,
-          stream)
+    _check(_move(lib().fa_kv_gather, False, k, v, k_pages, v_pages, block_table, starts, counts,
+                 kv_scales, stream), "fa_kv_gather")
 
 
 def fa_kv_gather_varlen(k_pages, v_pages, k, v, block_table, starts, cu_seqlens, max_seqlen: int,
                         kv_scales=None, stream=None) -> None:
     """fa_kv_gather into a packed batch: k, v [Hkv, total, d], cu_seqlens int32 [B + 1]."""
-    _move("fa_kv_gather_varlen", False, k, v, k_pages, v_pages, block_table, starts, cu_seqlens,
-          kv_scales, stream, int(max_seqlen))
+    _check(_move(lib().fa_kv_gather_varlen, False, k, v, k_pages, v_pages, block_table, starts,
+                 cu_seqlens, kv_scales, stream, int(max_seqlen)), "fa_kv_gather_varlen")
 
 
 def fa_fwd_decode_paged_workspace_size(B: int, H: int, Hkv: int, Nq: int, d: int) -> int:
@@ -597,20 +596,23 @@ def fa_fwd_decode_paged(q, k_pages, v_pages, o, lse, block_table, seqlens, works
     """q, o: bf16 [B, H, Nq, d]; lse: fp32 [B, H, Nq]; seqlens: int32 [B], the cached
     positions of each sequence, its Nq new ones included."""
     import torch
+    bf, pool, table = torch.bfloat16, k_pages.shape, block_table.shape
     cur = _current_index()
-    qs = _dims_of(q, "q")
+    qs = q.shape
+    if len(qs) != 4:
+        raise ValueError("q must be 4-D [B, H, Nq, d]")
+    kp, vp, sp, tp = _cache(k_pages, v_pages, block_table, kv_scales, cur)
     B, H, Nq, d = qs
-    kp, vp, sp, tp, tB, mp, P, Hkv, ps, dk = _cache(k_pages, v_pages, block_table, kv_scales, cur)
-    if dk != d or tB != B:
-        raise ValueError(f"q {tuple(q.shape)}, k_pages {tuple(k_pages.shape)} and block_table "
-                         f"{tuple(block_table.shape)} disagree")
+    if pool[3] != d or table[0] != B:
+        raise ValueError(f"q {tuple(qs)}, k_pages {tuple(pool)} and block_table {tuple(table)} "
+                         "disagree")
     wp, wb = _ws(workspace)
-    bf, f32 = torch.bfloat16, torch.float32
     _check(lib().fa_fwd_decode_paged(_arg(q, "q", bf, qs, cur), kp, vp, sp,
-                                     _arg(o, "o", bf, qs, cur), _arg(lse, "lse", f32, qs[:3], cur),
-                                     tp, _arg(seqlens, "seqlens", torch.int32, (B,), cur), wp, wb,
-                                     B, H, Hkv, Nq, P, ps, mp, d, 1 if causal else 0,
-                                     float(scale), _stream(stream)),
+                                     _arg(o, "o", bf, qs, cur),
+                                     _arg(lse, "lse", torch.float32, qs[:3], cur), tp,
+                                     _arg(seqlens, "seqlens", torch.int32, (B,), cur), wp, wb, B,
+                                     H, pool[1], Nq, pool[0], pool[2], table[1], d,
+                                     1 if causal else 0, float(scale), _stream(stream)),
            "fa_fwd_decode_paged")
 
 

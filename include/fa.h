@@ -454,9 +454,9 @@ FA_API fa_status fa_fwd_decode(const void* q, const void* k, const void* v, void
  * quantised: amax = max |x|, scale = amax / 448, code = e4m3(x * (448 / amax)),
  * both divisions in fp32, round to nearest even (scale 0 and codes 0 for a
  * row of zeros; a nonzero amax below 2^-100 counts as 2^-100; a NaN stays a
- * NaN, and a row with an infinity reads back as NaN).  Two rows for one place
- * in one call leave either of them there.  Positions past the table are not
- * written.  Errors as fa_fwd(), FA_ERR_UNSUPPORTED for B * Hkv * N >= 2^31.
+ * NaN, and a row with an infinity reads back as NaN).  Different rows for one
+ * place in one call (a page that two sequences write) leave that place
+ * unspecified.  Positions past the table are not written.  Errors as fa_fwd(), FA_ERR_UNSUPPORTED for B * Hkv * N >= 2^31.
  * Asynchronous on `stream`; one launch.
  */
 FA_API fa_status fa_kv_append(const void* k, const void* v, void* k_pages, void* v_pages,
@@ -505,7 +505,9 @@ FA_API fa_status fa_kv_gather_varlen(const void* k_pages, const void* v_pages,
  * with causal != 0 query row r sees positions j <= r + seqlens[b] - Nq, else
  * every position below seqlens[b].  A row that sees nothing (an empty slot,
  * seqlens[b] = 0; the first rows when seqlens[b] < Nq) gets O = 0 and LSE =
- * -infinity.  Cache rows at positions >= seqlens[b] may hold anything.
+ * -infinity.  Cache rows at positions >= seqlens[b] may hold anything; a NaN
+ * or an infinity at a position below it reaches every one of the sequence's Nq
+ * rows of that kv head, as a weight of zero does not silence it in P V.
  * (H / Hkv) * Nq <= 32 (FA_ERR_UNSUPPORTED otherwise).
  *
  * The scores and P V run on the tensor core with fp32 accumulation.  bf16
@@ -518,7 +520,10 @@ FA_API fa_status fa_kv_gather_varlen(const void* k_pages, const void* v_pages,
  * entry of no matter; calls that may overlap on the GPU (other streams, other
  * graphs) need one each.  The result does not depend on the order in which
  * the CTAs run: it is the same bit for bit on every call with the same inputs.
- * Asynchronous on `stream`.
+ * Lengths and tables are read on the device, so a captured call may be replayed
+ * with other contents of the same tensors.  Asynchronous on `stream`; two
+ * launches, each of which may begin (not read anything) while the kernel before
+ * it on the stream still runs.
  */
 FA_API size_t fa_fwd_decode_paged_workspace_size(int B, int H, int Hkv, int Nq, int d);
 FA_API fa_status fa_fwd_decode_paged(const void* q, const void* k_pages, const void* v_pages,
