@@ -109,7 +109,7 @@ struct Cfg {
 };
 
 __device__ __forceinline__ int clamped_len(const PagedParams& p, int b) {
-    return min(max(__ldg(p.seqlens + b), 0), p.max_pages << p.ps_shift);
+    return min(max(p.seqlens[b], 0), p.max_pages << p.ps_shift);
 }
 __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
 
@@ -298,7 +298,6 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
     const WaitCtx wc{p.status, &abort_sh}, dc{p.status, nullptr};   // dc: for drains
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    pdl_launch_dependents();
     if (warp == 4) {
         if (lane == 0) {
             tma_prefetch_desc(&tm_k);
@@ -339,8 +338,11 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
     tc_fence_after();
     const uint32_t tmem = tmem_base_sh;
     // Up to here nothing is read that an earlier kernel may have written: it may
-    // still run.
+    // still run.  Loads from here on are not ld.global.nc, whose data has to be
+    // constant from the launch on.  The combine kernel may come in only now: it
+    // reads the lengths before it waits for this one.
     pdl_wait();
+    pdl_launch_dependents();
     const int c = blockIdx.x;
     Cursor cur(p, List(p, lane), c);
 
@@ -350,7 +352,7 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
     auto page_of = [&](const Cursor& at) {
         const int key = at.t * kTile + lane * seg;
         return (at.left > 0 && lane < n_seg && key < at.len)
-                   ? __ldg(p.table + (long long)at.b * p.max_pages + (key >> p.ps_shift))
+                   ? p.table[(long long)at.b * p.max_pages + (key >> p.ps_shift)]
                    : 0;
     };
 
@@ -515,7 +517,7 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                     for (int e = 0; e < E / 8; ++e) {
                         w[e] = make_uint4(0u, 0u, 0u, 0u);
                         if (r < p.R)
-                            w[e] = __ldg(reinterpret_cast<const uint4*>(src + r * D + at * E) + e);
+                            w[e] = reinterpret_cast<const uint4*>(src + r * D + at * E)[e];
                         const uint32_t u[4] = {w[e].x, w[e].y, w[e].z, w[e].w};
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -569,7 +571,7 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll 2
                 for (int e = lane; e < p.R * U; e += 32) {
                     const int r = e / U, u = e % U;
-                    const uint4 w = __ldg(reinterpret_cast<const uint4*>(src) + e);
+                    const uint4 w = reinterpret_cast<const uint4*>(src)[e];
                     sts_v4(dst + (u >> 3) * (N * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4), w);
                 }
             }
@@ -833,7 +835,8 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
 // found while the split kernel still runs; after it, the parts' LSEs and the
 // first kPre parts of O come in one round trip.
 template <int D>
-__global__ void __launch_bounds__(256) fa_paged_combine_kernel(const __grid_constant__ PagedParams p, int rows) {
+__global__ void __launch_bounds__(256)
+fa_paged_combine_kernel(const __grid_constant__ PagedParams p, int rows) {
     constexpr int E = D / 32, kPre = 8;
     pdl_launch_dependents();
     const int row = (int)((blockIdx.x * 256 + threadIdx.x) >> 5), lane = threadIdx.x & 31;

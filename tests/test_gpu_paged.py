@@ -278,6 +278,52 @@ def test_other_stream_and_graph_replay():
             check_attend(q, cache, new, ob.cpu(), lb.cpu(), True, 0.125)
 
 
+@pytest.mark.parametrize("graph", [False, True], ids=["eager", "graph"])
+def test_lengths_written_just_before_the_call(graph):
+    """The call's set-up may overlap the kernel (or copy) before it: it must see the lengths
+    that one writes.  With queries of zero every weight is equal and LSE = ln(length)."""
+    cache = Cache([700, 300, 1], 2, 64, 16, "bf16", seed=40, max_pages=80)
+    kp, vp, _, _ = cache.cuda()
+    table = torch.zeros((3, 80), dtype=torch.int32, device="cuda")
+    q = torch.zeros(3, 4, 1, 64, dtype=torch.bfloat16, device="cuda")
+    o, lse = torch.empty_like(q), torch.empty(3, 4, 1, device="cuda")
+    ws = torch.empty(fa.fa_fwd_decode_paged_workspace_size(3, 4, 2, 1, 64), dtype=torch.uint8,
+                     device="cuda")
+    start = [700, 300, 0]
+    steps = 120
+    lens, src, seen = i32(start), i32(start), torch.zeros(2 * steps, 3, device="cuda")
+    at = torch.zeros(1, dtype=torch.long, device="cuda")
+
+    def step():
+        lens.add_(1)                                   # a kernel, then the call
+        fa.fa_fwd_decode_paged(q, kp, vp, o, lse, table, lens, ws, True, 0.125)
+        seen.index_copy_(0, at, lse[:, 0, 0][None])
+        at.add_(1)
+        src.add_(1)
+        lens.copy_(src)                                # a copy, then the call
+        fa.fa_fwd_decode_paged(q, kp, vp, o, lse, table, lens, ws, True, 0.125)
+        seen.index_copy_(0, at, lse[:, 0, 0][None])
+        at.add_(1)
+
+    if graph:
+        step()
+        torch.cuda.synchronize()
+        for t, v in ((lens, i32(start)), (src, i32(start)), (at, torch.zeros_like(at))):
+            t.copy_(v)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step()
+        for _ in range(steps):
+            g.replay()
+    else:
+        for _ in range(steps):
+            step()
+    ok()
+    want = torch.tensor([[math.log(n + i // 2 + 1) for n in start] for i in range(2 * steps)],
+                        dtype=torch.float64)
+    assert (seen.cpu().double() - want).abs().max() <= 2.0 ** -19
+
+
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 def test_pool_past_2_to_the_31_elements(kv):
     """Pages whose offsets need more than 32 bits, written, attended to and read back."""
