@@ -499,31 +499,37 @@ def attention_decode(q, k, v, causal: bool = True, scale: float | None = None, s
 
 
 # ------------------------------------------------------------- paged cache
-# A decoding step makes these calls once a layer on little data: their checks are
-# those of _ptr, with the current device asked for once a call.
-def _arg(t, name, dtype, shape, cur):
-    if t.dtype is dtype and t.shape == shape and t.get_device() == cur and t.is_contiguous():
-        return t.data_ptr()
-    return _ptr(t, name, dtype, shape)   # says what is wrong
+# A decoding step makes these calls once a layer on little data, so their checks,
+# those of _ptr, are spelled out in one expression a call (a function call a tensor
+# was a quarter of a small call's time); _explain finds what is wrong.
+def _explain(*args):
+    for t, name, dtype, shape in args:
+        _ptr(t, name, dtype, shape)
+    raise ValueError("tensors disagree")
 
 
-def _cache(k_pages, v_pages, block_table, kv_scales, cur):
-    """Pointers and sizes of a paged cache: k_pages, v_pages [n_pages, Hkv, page_size, d]
-    (bf16; torch.float8_e4m3fn with kv_scales fp32 [n_pages, Hkv, 2, page_size]),
-    block_table int32 [B, max_pages]."""
+def _pool(k_pages, block_table, kv_scales):
+    """Shapes of a paged cache and the type of its pages: k_pages, v_pages [n_pages, Hkv,
+    page_size, d] (bf16; torch.float8_e4m3fn with kv_scales fp32 [n_pages, Hkv, 2,
+    page_size]), block_table int32 [B, max_pages]."""
     import torch
-    shape, table = k_pages.shape, block_table.shape
-    if len(shape) != 4:
+    pool, table = k_pages.shape, block_table.shape
+    if len(pool) != 4:
         raise ValueError("k_pages must be 4-D [n_pages, Hkv, page_size, d]")
     if len(table) != 2:
         raise ValueError("block_table must be 2-D [B, max_pages]")
+    return pool, table, torch.bfloat16 if kv_scales is None else torch.float8_e4m3fn
+
+
+def _scales(kv_scales, pool, cur):
+    import torch
     if kv_scales is None:
-        dtype, sp = torch.bfloat16, None
-    else:
-        dtype = torch.float8_e4m3fn
-        sp = _arg(kv_scales, "kv_scales", torch.float32, (shape[0], shape[1], 2, shape[2]), cur)
-    return (_arg(k_pages, "k_pages", dtype, shape, cur), _arg(v_pages, "v_pages", dtype, shape, cur),
-            sp, _arg(block_table, "block_table", torch.int32, table, cur))
+        return None
+    shape = (pool[0], pool[1], 2, pool[2])
+    if kv_scales.dtype is torch.float32 and kv_scales.shape == shape and \
+            kv_scales.get_device() == cur and kv_scales.is_contiguous():
+        return kv_scales.data_ptr()
+    return _ptr(kv_scales, "kv_scales", torch.float32, shape)
 
 
 def _move(call, append, k, v, k_pages, v_pages, block_table, starts, counts, kv_scales, stream,
@@ -532,29 +538,37 @@ def _move(call, append, k, v, k_pages, v_pages, block_table, starts, counts, kv_
     packed (k [Hkv, total, d], counts = cu_seqlens [B + 1])."""
     import torch
     bf, i32 = torch.bfloat16, torch.int32
+    pool, table, kd = _pool(k_pages, block_table, kv_scales)
     cur = _current_index()
-    shape, pool, table = k.shape, k_pages.shape, block_table.shape
+    shape = k.shape
     B = table[0]
-    packed = max_seqlen is not None
-    if len(pool) == 4 and (len(shape) != (3 if packed else 4) or shape[-1] != pool[3] or
-                           shape[-3] != pool[1] or not packed and shape[0] != B):
-        raise ValueError(f"k has shape {tuple(shape)}, expected "
-                         f"{'[Hkv, total, d]' if packed else '[B, Hkv, N, d]'} of k_pages "
-                         f"{tuple(pool)} and block_table {tuple(table)}")
-    kp, vp, sp, tp = _cache(k_pages, v_pages, block_table, kv_scales, cur)
-    rk, rv = _arg(k, "k", bf, shape, cur), _arg(v, "v", bf, shape, cur)
-    st = _arg(starts, "starts", i32, (B,), cur)
-    if packed:
-        ct = _arg(counts, "cu_seqlens", i32, (B + 1,), cur)
-        sizes = (B, max_seqlen, shape[1], pool[1])
+    if max_seqlen is None:
+        n, good = B, len(shape) == 4 and shape[0] == B
     else:
-        ct = _arg(counts, "counts", i32, (B,), cur)
-        sizes = (B, pool[1], shape[2])
-    if append:
-        return call(rk, rv, kp, vp, sp, tp, st, ct, *sizes, pool[0], pool[2], table[1], pool[3],
-                    _stream(stream))
-    return call(kp, vp, sp, rk, rv, tp, st, ct, *sizes, pool[0], pool[2], table[1], pool[3],
-                _stream(stream))
+        n, good = B + 1, len(shape) == 3
+    if not good or shape[-3] != pool[1] or shape[-1] != pool[3]:
+        raise ValueError(f"k has shape {tuple(shape)}, expected "
+                         f"{'[B, Hkv, N, d]' if max_seqlen is None else '[Hkv, total, d]'} of "
+                         f"k_pages {tuple(pool)} and block_table {tuple(table)}")
+    if not (k.dtype is bf and v.dtype is bf and v.shape == shape and k_pages.dtype is kd and
+            v_pages.dtype is kd and v_pages.shape == pool and block_table.dtype is i32 and
+            starts.dtype is i32 and starts.shape == (B,) and counts.dtype is i32 and
+            counts.shape == (n,) and k.get_device() == cur and v.get_device() == cur and
+            k_pages.get_device() == cur and v_pages.get_device() == cur and
+            block_table.get_device() == cur and starts.get_device() == cur and
+            counts.get_device() == cur and k.is_contiguous() and v.is_contiguous() and
+            k_pages.is_contiguous() and v_pages.is_contiguous() and
+            block_table.is_contiguous() and starts.is_contiguous() and counts.is_contiguous()):
+        _explain((k, "k", bf, shape), (v, "v", bf, shape), (k_pages, "k_pages", kd, pool),
+                 (v_pages, "v_pages", kd, pool), (block_table, "block_table", i32, table),
+                 (starts, "starts", i32, (B,)),
+                 (counts, "counts" if max_seqlen is None else "cu_seqlens", i32, (n,)))
+    sp = _scales(kv_scales, pool, cur)
+    rows, pages = (k.data_ptr(), v.data_ptr()), (k_pages.data_ptr(), v_pages.data_ptr(), sp)
+    sizes = (B, pool[1], shape[2]) if max_seqlen is None else (B, max_seqlen, shape[1], pool[1])
+    first, then = (rows, pages) if append else (pages, rows)
+    return call(*first, *then, block_table.data_ptr(), starts.data_ptr(), counts.data_ptr(),
+                *sizes, pool[0], pool[2], table[1], pool[3], _stream(stream))
 
 
 def fa_kv_append(k, v, k_pages, v_pages, block_table, starts, counts, kv_scales=None,
@@ -596,24 +610,38 @@ def fa_fwd_decode_paged(q, k_pages, v_pages, o, lse, block_table, seqlens, works
     """q, o: bf16 [B, H, Nq, d]; lse: fp32 [B, H, Nq]; seqlens: int32 [B], the cached
     positions of each sequence, its Nq new ones included."""
     import torch
-    bf, pool, table = torch.bfloat16, k_pages.shape, block_table.shape
+    bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    pool, table, kd = _pool(k_pages, block_table, kv_scales)
     cur = _current_index()
     qs = q.shape
     if len(qs) != 4:
         raise ValueError("q must be 4-D [B, H, Nq, d]")
-    kp, vp, sp, tp = _cache(k_pages, v_pages, block_table, kv_scales, cur)
     B, H, Nq, d = qs
     if pool[3] != d or table[0] != B:
         raise ValueError(f"q {tuple(qs)}, k_pages {tuple(pool)} and block_table {tuple(table)} "
                          "disagree")
-    wp, wb = _ws(workspace)
-    _check(lib().fa_fwd_decode_paged(_arg(q, "q", bf, qs, cur), kp, vp, sp,
-                                     _arg(o, "o", bf, qs, cur),
-                                     _arg(lse, "lse", torch.float32, qs[:3], cur), tp,
-                                     _arg(seqlens, "seqlens", torch.int32, (B,), cur), wp, wb, B,
-                                     H, pool[1], Nq, pool[0], pool[2], table[1], d,
-                                     1 if causal else 0, float(scale), _stream(stream)),
-           "fa_fwd_decode_paged")
+    if not (q.dtype is bf and o.dtype is bf and o.shape == qs and lse.dtype is f32 and
+            lse.shape == (B, H, Nq) and k_pages.dtype is kd and v_pages.dtype is kd and
+            v_pages.shape == pool and block_table.dtype is i32 and seqlens.dtype is i32 and
+            seqlens.shape == (B,) and q.get_device() == cur and o.get_device() == cur and
+            lse.get_device() == cur and k_pages.get_device() == cur and
+            v_pages.get_device() == cur and block_table.get_device() == cur and
+            seqlens.get_device() == cur and q.is_contiguous() and o.is_contiguous() and
+            lse.is_contiguous() and k_pages.is_contiguous() and v_pages.is_contiguous() and
+            block_table.is_contiguous() and seqlens.is_contiguous()):
+        _explain((q, "q", bf, qs), (k_pages, "k_pages", kd, pool), (v_pages, "v_pages", kd, pool),
+                 (o, "o", bf, qs), (lse, "lse", f32, (B, H, Nq)),
+                 (block_table, "block_table", i32, table), (seqlens, "seqlens", i32, (B,)))
+    sp = _scales(kv_scales, pool, cur)
+    if workspace.get_device() == cur and workspace.is_contiguous():
+        wp, wb = workspace.data_ptr(), workspace.nbytes
+    else:
+        wp, wb = _ws(workspace)
+    _check(lib().fa_fwd_decode_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), sp,
+                                     o.data_ptr(), lse.data_ptr(), block_table.data_ptr(),
+                                     seqlens.data_ptr(), wp, wb, B, H, pool[1], Nq, pool[0],
+                                     pool[2], table[1], d, 1 if causal else 0, float(scale),
+                                     _stream(stream)), "fa_fwd_decode_paged")
 
 
 def attention_decode_paged(q, k_pages, v_pages, block_table, seqlens, causal: bool = True,

@@ -13,7 +13,7 @@
 // next 8, 16 or 32, and no thread needs another's score: the running maximum m of a
 // row moves only when some key passes it by 2^kSlack (a vote of the four
 // warps), the row sums stay one partial per thread until the end, and the
-// rescale of O^T touches kN columns.
+// rescale of O^T touches few columns.
 //
 // e4m3 pages are multiplied as they are.  A bf16 query row, times the power of
 // two that brings its largest entry into [2^7, 2^8), is the sum of two e4m3
@@ -76,21 +76,26 @@ template <int D, bool F8, int G, int W>
 struct Cfg {
     static constexpr int RP = kRows * G;
     static constexpr int kThreads = 128 + 128 * G;
-    static constexpr int kN = F8 ? 2 * RP : (RP < 16 ? 16 : RP);   // MMA columns
+    static constexpr int kN = F8 ? 2 * RP : (RP < 16 ? 16 : RP);   // columns of S, rows of Q
+    // P enters as the sum of two terms of its type, so that its rounding does not
+    // show beside the output's (with one bf16 term the output's error was 1.4
+    // times its rounding).
+    static constexpr int kNP = 2 * RP;                             // columns of O, rows of P
     static constexpr int kRowBytes = F8 ? D : 2 * D;
     static constexpr int kSw = kRowBytes < 128 ? 64 : 128;         // swizzle = chunk width
     static constexpr int kChunks = kRowBytes / kSw;
     static constexpr int kTileBytes = kTile * kRowBytes;
     static constexpr int kQBytes = kN * kRowBytes;
     static constexpr int kPRow = F8 ? kTile : 2 * kTile;
-    static constexpr int kPBytes = kN * kPRow;
+    static constexpr int kPBytes = kNP * kPRow;
+    static constexpr int kPBufs = !F8 && D == 128 && G == 4 ? 1 : 2;   // no room for two there
     static constexpr int kScaleBytes = F8 ? 2 * kTile * 4 : 0;
     // bf16 rows of 128 fill an SM with one CTA.  Smaller ones leave less time a
     // tile, and with up to 8 rows two CTAs fit, so that one's softmax and
     // epilogue hide behind the other's.
     static constexpr int kCtas = kRowBytes <= 128 && G == 1 ? 2 : 1;
     static constexpr int kRing = (kCtas == 2 ? 113 : 227) * 1024 - 1024 - 2048 - 2 * kQBytes -
-                                 2 * kPBytes;
+                                 kPBufs * kPBytes;
     static constexpr int kStages = kRing / (2 * kTileBytes + kScaleBytes);
     // Tiles of K, and of V, in flight at once: about 112 KB an SM.  More of them
     // slow the memory down: with all three stages in flight bf16 at d = 64 took
@@ -100,8 +105,9 @@ struct Cfg {
     static constexpr int kAhead =
         kRowBytes >= 128 ? (56 * 1024 / kCtas + kTileBytes / 2) / kTileBytes : kStages;
     static constexpr int kSmem =
-        kStages * (2 * kTileBytes + kScaleBytes) + 2 * kQBytes + 2 * kPBytes + 1024;
-    static constexpr int kTmemCols = 3 * kN <= 64 ? 64 : (3 * kN <= 128 ? 128 : 256);
+        kStages * (2 * kTileBytes + kScaleBytes) + 2 * kQBytes + kPBufs * kPBytes + 1024;
+    static constexpr int kCols = 2 * kN + kNP;
+    static constexpr int kTmemCols = kCols <= 64 ? 64 : (kCols <= 128 ? 128 : 256);
     // How far a score may pass the running maximum before O is rescaled (log2):
     // bf16 P keeps its precision at any magnitude; e4m3 P ends at 448.
     static constexpr float kSlack = F8 ? 3.0f : 8.0f;
@@ -276,7 +282,7 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v,
                        const __grid_constant__ PagedParams p) {
     using C = Cfg<D, F8, G, W>;
-    constexpr int S = C::kStages, N = C::kN, TB = C::kTileBytes, RP = C::RP;
+    constexpr int S = C::kStages, N = C::kN, NP = C::kNP, TB = C::kTileBytes, RP = C::RP;
     constexpr uint32_t kColO = 2 * N;             // S buffers at 0 and N
     extern __shared__ uint8_t dsm_raw[];
     // 32-bit shared addresses, 1024-byte aligned.  Stage s: V, then K.  At d = 64
@@ -284,8 +290,8 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
     // rows of O^T that nobody reads.
     const uint32_t sKV = (smem_u32(dsm_raw) + 1023) & ~1023u;
     const uint32_t sQ = sKV + S * 2 * TB;         // [2]
-    const uint32_t sP = sQ + 2 * C::kQBytes;      // [2]
-    const uint32_t sScale = sP + 2 * C::kPBytes;  // [S][K, V][128] fp32
+    const uint32_t sP = sQ + 2 * C::kQBytes;      // [kPBufs]
+    const uint32_t sScale = sP + C::kPBufs * C::kPBytes;  // [S][K, V][128] fp32
     // per stage: K, V and e4m3's scales are there; S and P V of the stage's tile are
     // complete, which also frees its K, and its V and scales
     __shared__ uint64_t bar_k[S], bar_v[S], bar_x[S], bar_s[S], bar_pv[S];
@@ -326,7 +332,7 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
         // Query rows past R and columns of P past RP stay zero.
         const int x0 = (warp < 4 ? warp : warp - 2) * 32 + lane;
 #pragma unroll 1
-        for (int e = x0; e < (2 * C::kQBytes + 2 * C::kPBytes) / 16; e += C::kThreads - 64)
+        for (int e = x0; e < (2 * C::kQBytes + C::kPBufs * C::kPBytes) / 16; e += C::kThreads - 64)
             sts_v4(sQ + e * 16, make_uint4(0u, 0u, 0u, 0u));
         if (warp == 6)
 #pragma unroll 1
@@ -414,7 +420,7 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
         constexpr uint32_t idesc_s =
             F8 ? idesc_e4m3_f32(128, N) : idesc_bf16_f32(128, N, false, false);
         constexpr uint32_t idesc_o =
-            F8 ? idesc_e4m3_f32(128, N, true) : idesc_bf16_f32(128, N, true, false);
+            F8 ? idesc_e4m3_f32(128, NP, true) : idesc_bf16_f32(128, NP, true, false);
         constexpr uint32_t kGroup = 8 * C::kSw;                      // 8 rows of a chunk
         auto desc = [&](uint32_t a, uint32_t lbo) {
             return C::kSw == 128 ? sdesc_sw128(a, lbo, kGroup) : sdesc_sw64(a, lbo, kGroup);
@@ -433,12 +439,12 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
             // V transposed: 32 (e4m3) or 16 keys a step; the next chunk of
             // columns (d = 64: K) is the leading-dimension stride
             const uint64_t vd = desc(sKV + s * 2 * TB, C::kChunks == 2 ? kTile * C::kSw : TB);
-            const uint64_t pd = sdesc_sw128(sP + (u & 1) * C::kPBytes, 16, 1024);
+            const uint64_t pd = sdesc_sw128(sP + u % C::kPBufs * C::kPBytes, 16, 1024);
             if (leader) {
 #pragma unroll
                 for (int kk = 0; kk < (F8 ? 4 : 8); ++kk) {
                     const uint64_t a = vd + (uint64_t)(kk * (F8 ? 32 : 16) * C::kSw >> 4);
-                    const uint64_t b = pd + kmajor_step(kk, N * 128);
+                    const uint64_t b = pd + kmajor_step(kk, NP * 128);
                     if (F8) mma_ss_f8(tmem + kColO, a, b, idesc_o, !first || kk > 0);
                     else mma_ss(tmem + kColO, a, b, idesc_o, !first || kk > 0);
                 }
@@ -621,7 +627,7 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
         const uint32_t max_w = smem_u32(row_max + r0) + quarter * 4;   // this warp's value, row r0
         const uint32_t sum_w = smem_u32(row_sum + r0) + quarter * 4;
         // where P's row r0 keeps key j, unswizzled
-        const uint32_t p_at = sP + r0 * 128 + (F8 ? j : (j >> 6) * (N * 128) + (j & 63) * 2);
+        const uint32_t p_at = sP + r0 * 128 + (F8 ? j : (j >> 6) * (NP * 128) + (j & 63) * 2);
         bool ok = true;
         int gt = 0, pairs = 0;
         for (; cur.left > 0; ++pairs) {
@@ -647,7 +653,7 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                 const bool tail = tile_end > cur.len;
                 // S_u complete means P_{u-2} V_{u-2} complete too: a commit
                 // covers every MMA before it, and that one was issued before
-                // S_u, so P's buffer u & 1 may be written
+                // S_u, so with two buffers P_u's may be written
                 ok = ok && wait(&bar_s[s], (u / S) & 1, 111, wc);
                 if (F8) ok = ok && wait(&bar_x[s], (u / S) & 1, 112, wc);
                 __syncwarp();
@@ -707,22 +713,24 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                         if (quarter * 32 < D) {
                             uint32_t oa[W], ob[W];
                             tmem_ld(lane_base + kColO, oa);
-                            if (F8) tmem_ld(lane_base + kColO + RP, ob);
+                            tmem_ld(lane_base + kColO + RP, ob);
                             tmem_ld_done(oa);
-                            if (F8) tmem_ld_done(ob);
+                            tmem_ld_done(ob);
 #pragma unroll
                             for (int r = 0; r < W; ++r) {
                                 oa[r] = __float_as_uint(__uint_as_float(oa[r]) * alpha[r]);
-                                if (F8) ob[r] = __float_as_uint(__uint_as_float(ob[r]) * alpha[r]);
+                                ob[r] = __float_as_uint(__uint_as_float(ob[r]) * alpha[r]);
                             }
                             tmem_st(lane_base + kColO, oa);
-                            if (F8) tmem_st(lane_base + kColO + RP, ob);
+                            tmem_st(lane_base + kColO + RP, ob);
                             tmem_st_wait();
                         }
                     }
                 }
                 // P, at row r's swizzle (its 16-byte units exchanged by r & 7)
-                const uint32_t pw = p_at + (u & 1) * C::kPBytes;
+                const uint32_t pw = p_at + u % C::kPBufs * C::kPBytes;
+                if (C::kPBufs == 1 && u > 0)
+                    ok = ok && wait(&bar_pv[(u - 1) % S], ((u - 1) / S) & 1, 118, wc);
                 const float wv = vs * C::kPScale;
 #pragma unroll
                 for (int r = 0; r < W; r += 2) {
@@ -746,9 +754,15 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                             sts_u8(a1 + RP * 128, h2 >> 8);
                         }
                     } else {
-                        const uint32_t h = pack_bf16x2(e0, e1);
-                        sts_u16(a0, (uint16_t)h);
-                        if (W > 1) sts_u16(a1, (uint16_t)(h >> 16));
+                        const uint32_t h1 = pack_bf16x2(e0, e1);
+                        const uint32_t h2 = pack_bf16x2(e0 - __uint_as_float(h1 << 16),
+                                                        e1 - __uint_as_float(h1 & 0xffff0000u));
+                        sts_u16(a0, (uint16_t)h1);
+                        sts_u16(a0 + RP * 128, (uint16_t)h2);
+                        if (W > 1) {
+                            sts_u16(a1, (uint16_t)(h1 >> 16));
+                            sts_u16(a1 + RP * 128, (uint16_t)(h2 >> 16));
+                        }
                     }
                 }
                 if (tail && group == 0) {
@@ -801,13 +815,13 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
             if (quarter * 32 < D) {
                 uint32_t oa[W], ob[W];
                 tmem_ld(lane_base + kColO, oa);
-                if (F8) tmem_ld(lane_base + kColO + RP, ob);
+                tmem_ld(lane_base + kColO + RP, ob);
                 tmem_ld_done(oa);
-                if (F8) tmem_ld_done(ob);
+                tmem_ld_done(ob);
 #pragma unroll
                 for (int r = 0; r < W; ++r) {
                     float y = __uint_as_float(oa[r]);
-                    if (F8) y += __uint_as_float(ob[r]);
+                    y += __uint_as_float(ob[r]);
                     y = inv[r] < 0.0f ? 0.0f : y * inv[r];
                     if (r0 + r < p.R) {
                         if (whole)

@@ -511,9 +511,10 @@ FA_API fa_status fa_kv_gather_varlen(const void* k_pages, const void* v_pages,
  * (H / Hkv) * Nq <= 32 (FA_ERR_UNSUPPORTED otherwise).
  *
  * The scores and P V run on the tensor core with fp32 accumulation.  bf16
- * pages: P is rounded to bf16.  e4m3 pages: q and P enter as the sum of two
- * e4m3 terms (8 significant bits, those of bf16), so that the codes are
- * multiplied as they are and only the scales are applied in fp32.
+ * pages: P enters as the sum of two bf16 terms (16 significant bits).  e4m3
+ * pages: q and P enter as the sum of two e4m3 terms (8 significant bits, those
+ * of bf16), so that the codes are multiplied as they are and only the scales
+ * are applied in fp32.
  *
  * workspace: caller-owned device memory of
  * fa_fwd_decode_paged_workspace_size() bytes, 256-byte aligned, contents on

@@ -30,17 +30,18 @@ def bounds(q, k, v, vs, o, w, scale, e4m3):
     """Elementwise bound of |O - o| and |LSE - lse| of one (kv head, query row): q [d],
     k, v [n, d], vs [n] (V's row scales), o [d], w [n] softmax weights.
 
-    O: each weight is rounded to 8 significant bits (relative 2^-8 at most: bf16 by half a
-    step; two e4m3 terms leave 2^-4 of 2^-4, after fp16's 2^-11) and O to bf16 (2^-8 |O|).  In
-    e4m3 the second term's smallest step is 2^-9 where the largest weight times scale is at
-    least 56, so that each product code * weight is off by at most 2^-10 / 56 of the largest
-    such product's scale.  fp32 accumulation: n + 8 roundings of 2^-24 of the absolute sum,
-    doubled for the exponential's 2^-22 and the sum of weights.
+    O: bf16 weights are two terms of 8 significant bits, off by at most 2^-17; e4m3 weights
+    have 8 significant bits in two terms (2^-4 of 2^-4, after fp16's 2^-11) and, as the second
+    term's smallest step is 2^-9 where the largest weight times scale is at least 56, each
+    product code * weight is off by at most 2^-10 / 56 of the largest such product's scale.  O
+    is rounded to bf16 (2^-8 |O|).  fp32 accumulation: n + 8 roundings of 2^-24 of the absolute
+    sum, doubled for the exponential's 2^-22 and the sum of weights.
     LSE: the scores' fp32 accumulation over d, the exponential and the logarithm; in e4m3 the
     query's second term ends at 2^-10 where its largest entry is at least 2^7."""
     n, d = k.shape
     absum = w @ np.abs(v)
-    bo = 2.0 ** -8 * (absum * (1.15 if e4m3 else 1.02) + np.abs(o)) + (2 * n + 64) * 2.0 ** -24 * absum + 1e-30
+    weight = 2.0 ** -8 * 1.15 if e4m3 else 2.0 ** -16
+    bo = 2.0 ** -8 * np.abs(o) + (weight + (2 * n + 64) * 2.0 ** -24) * absum + 1e-30
     s_abs = scale * (np.abs(k) @ np.abs(q)).max()
     bl = 2 * (d + 16) * 2.0 ** -24 * s_abs + 2.0 ** -19
     if e4m3:
