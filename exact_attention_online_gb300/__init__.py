@@ -651,11 +651,12 @@ def attention_decode_paged(q, k_pages, v_pages, block_table, seqlens, causal: bo
     is given; returns (o, lse)."""
     import torch
     B, H, Nq, d = _dims_of(q, "q")
+    pool, _, _ = _pool(k_pages, block_table, kv_scales)
     scale = d ** -0.5 if scale is None else scale
     o = torch.empty_like(q, memory_format=torch.contiguous_format)
     lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
     if workspace is None:
-        n = fa_fwd_decode_paged_workspace_size(B, H, k_pages.shape[1], Nq, d)
+        n = fa_fwd_decode_paged_workspace_size(B, H, pool[1], Nq, d)
         if n == 0:
             raise FAError(FA_ERR_UNSUPPORTED, "fa_fwd_decode_paged_workspace_size")
         workspace = torch.empty(n, dtype=torch.uint8, device=q.device)

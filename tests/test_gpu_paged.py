@@ -279,6 +279,73 @@ def test_other_stream_and_graph_replay():
             check_attend(q, cache, new, ob.cpu(), lb.cpu(), True, 0.125)
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")], ids=["nan", "inf"])
+def test_a_bad_query_row_stays_alone(kv, bad):
+    cache = Cache([300], 2, 64, 16, kv, seed=41)
+    q = randn(42, 1, 12, 3, 64)
+    good, good_lse = run_attend(q, cache, [300], True, 0.125)
+    q2 = q.clone()
+    q2[0, 4, 1, 7] = bad
+    o, lse = run_attend(q2, cache, [300], True, 0.125)
+    assert torch.isnan(o[0, 4, 1].float()).all() and torch.isnan(lse[0, 4, 1])
+    o[0, 4, 1], lse[0, 4, 1] = good[0, 4, 1], good_lse[0, 4, 1]
+    assert torch.equal(o, good) and torch.equal(lse, good_lse)
+
+
+def test_one_workspace_for_two_graphs_in_turn():
+    """Two shapes captured with the same workspace and replayed one after the other."""
+    ws = torch.full((fa.fa_fwd_decode_paged_workspace_size(3, 8, 2, 2, 128),), 255,
+                    dtype=torch.uint8, device="cuda")
+    runs = []
+    for d, lens, seed in ((128, [2000, 5, 900], 43), (64, [100, 3000, 1], 44)):
+        cache = Cache(lens, 2, d, 16, "bf16", seed=seed)
+        kp, vp, table, _ = cache.cuda()
+        q, ld = randn(seed, 3, 8, 2, d).cuda(), i32(lens)
+        o, lse = torch.empty_like(q), torch.empty(3, 8, 2, device="cuda")
+        args = (q, kp, vp, o, lse, table, ld, ws, True, 0.1)
+        fa.fa_fwd_decode_paged(*args)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            fa.fa_fwd_decode_paged(*args)
+        runs.append((g, cache, lens, args))
+    for _ in range(3):
+        for g, _, _, args in runs:
+            args[3].zero_()
+            g.replay()
+    ok()
+    for _, cache, lens, args in runs:
+        check_attend(args[0].cpu(), cache, lens, args[3].cpu(), args[4].cpu(), True, 0.1)
+
+
+def test_two_threads():
+    """Calls from two threads, each on its own stream with its own buffers."""
+    import threading
+    failed = []
+
+    def work(seed):
+        try:
+            lens = [50 * seed, 700]
+            cache = Cache(lens, 1, 128, 16, "e4m3", seed=seed)
+            with torch.cuda.stream(torch.cuda.Stream()):
+                kp, vp, table, scales = cache.cuda()
+                q, ld = randn(seed, 2, 4, 1, 128).cuda(), i32(lens)
+                for _ in range(50):
+                    o, lse = fa.attention_decode_paged(q, kp, vp, table, ld, kv_scales=scales)
+                torch.cuda.current_stream().synchronize()
+            check_attend(q.cpu(), cache, lens, o.cpu(), lse.cpu(), True, 128 ** -0.5)
+        except BaseException as e:                       # noqa: BLE001 (told by the main thread)
+            failed.append(e)
+    threads = [threading.Thread(target=work, args=(s,)) for s in (3, 8)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+    ok()
+
+
 @pytest.mark.parametrize("graph", [False, True], ids=["eager", "graph"])
 def test_lengths_written_just_before_the_call(graph):
     """The call's set-up may overlap the kernel (or copy) before it: it must see the lengths
