@@ -120,8 +120,9 @@ __device__ __forceinline__ uint4 decode8(const uint2& c, float scale) {
     float x[4], y[4];
     unpack_e4m3x4(c.x, x);
     unpack_e4m3x4(c.y, y);
-    return make_uint4(pack_bf16x2(x[0] * scale, x[1] * scale), pack_bf16x2(x[2] * scale, x[3] * scale),
-                      pack_bf16x2(y[0] * scale, y[1] * scale), pack_bf16x2(y[2] * scale, y[3] * scale));
+    return make_uint4(
+        pack_bf16x2(x[0] * scale, x[1] * scale), pack_bf16x2(x[2] * scale, x[3] * scale),
+        pack_bf16x2(y[0] * scale, y[1] * scale), pack_bf16x2(y[2] * scale, y[3] * scale));
 }
 
 // Passes whose loads are in flight together, and rounds of them: a warp moves
@@ -248,6 +249,15 @@ cudaError_t launch_rows(const MoveParams& p, cudaStream_t stream) {
     return launch<D, F8, APPEND, 4, F8 && APPEND ? 2 : 1>(p, stream);
 }
 
+template <int D>
+cudaError_t launch_type(const MoveParams& p, bool append, cudaStream_t stream) {
+    if (append)
+        return p.scales ? launch_rows<D, true, true>(p, stream)
+                        : launch_rows<D, false, true>(p, stream);
+    return p.scales ? launch_rows<D, true, false>(p, stream)
+                    : launch_rows<D, false, false>(p, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_kv_move(const PagedCache& c, void* k, void* v, const int* starts,
@@ -273,13 +283,8 @@ cudaError_t launch_kv_move(const PagedCache& c, void* k, void* v, const int* sta
                  Divider(run),
                  Divider((unsigned)c.Hkv),
                  (unsigned)((packed ? 1LL : (long long)B) * c.Hkv * run)};
-    const bool f8 = c.scales != nullptr;
-    if (c.d == 128) {
-        if (append) return f8 ? launch_rows<128, true, true>(p, stream) : launch_rows<128, false, true>(p, stream);
-        return f8 ? launch_rows<128, true, false>(p, stream) : launch_rows<128, false, false>(p, stream);
-    }
-    if (append) return f8 ? launch_rows<64, true, true>(p, stream) : launch_rows<64, false, true>(p, stream);
-    return f8 ? launch_rows<64, true, false>(p, stream) : launch_rows<64, false, false>(p, stream);
+    if (c.d == 128) return launch_type<128>(p, append, stream);
+    return launch_type<64>(p, append, stream);
 }
 
 }  // namespace fa

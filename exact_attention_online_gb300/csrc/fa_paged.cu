@@ -392,7 +392,8 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
             if (gt >= S)
                 ok = wait_warp(&empty[s], ((gt / S) - 1) & 1, is_v ? 101 : 100, wc);
             if (C::kAhead < S && gt >= C::kAhead)
-                ok = ok && wait_warp(&full[(gt - C::kAhead) % S], ((gt - C::kAhead) / S) & 1, 103, wc);
+                ok = ok &&
+                     wait_warp(&full[(gt - C::kAhead) % S], ((gt - C::kAhead) / S) & 1, 103, wc);
             if (!ok) break;
             const uint32_t stage = sKV + s * 2 * TB + (is_v ? 0 : TB);
             if (leader) mbar_arrive_expect_tx(&full[s], have * seg_bytes * C::kChunks);
@@ -571,7 +572,8 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                                       : p.scale_log2 * __uint_as_float((uint32_t)(127 - k) << 23);
                 }
 #pragma unroll 1
-                for (int r = (p.R + 3) / 4 * 4 + lane; r < RP; r += 32) q_scale[pairs & 1][r] = 0.0f;
+                for (int r = (p.R + 3) / 4 * 4 + lane; r < RP; r += 32)
+                    q_scale[pairs & 1][r] = 0.0f;
             } else {
                 constexpr int U = D / 8;      // 16-byte units of a row
 #pragma unroll 2
@@ -964,7 +966,8 @@ cudaError_t launch_split(const CUtensorMap& tk, const CUtensorMap& tv, PagedPara
         configured.fetch_or(1ull << dev, std::memory_order_release);
     }
     // no more CTAs than there can be tiles
-    const long long most = (long long)p.B * p.Hkv * (((p.max_pages << p.ps_shift) + kTile - 1) / kTile);
+    const int longest = p.max_pages << p.ps_shift;
+    const long long most = (long long)p.B * p.Hkv * ((longest + kTile - 1) / kTile);
     long long grid = (long long)(device_sm_count() > 0 ? device_sm_count() : 152) * C::kCtas;
     if (grid > kPagedMaxCtas) grid = kPagedMaxCtas;
     if (grid > most) grid = most;
@@ -1030,11 +1033,10 @@ cudaError_t launch_fwd_decode_paged(const PagedCache& c, const void* q, void* o,
     p.causal = causal;
     p.scale_log2 = scale * kLog2e;
     p.status = status;
-    cudaError_t e;
-    if (c.d == 128)
-        e = f8 ? launch_rows<128, true>(tk, tv, p, stream) : launch_rows<128, false>(tk, tv, p, stream);
-    else
-        e = f8 ? launch_rows<64, true>(tk, tv, p, stream) : launch_rows<64, false>(tk, tv, p, stream);
+    const cudaError_t e = c.d == 128 ? (f8 ? launch_rows<128, true>(tk, tv, p, stream)
+                                           : launch_rows<128, false>(tk, tv, p, stream))
+                                     : (f8 ? launch_rows<64, true>(tk, tv, p, stream)
+                                           : launch_rows<64, false>(tk, tv, p, stream));
     if (e != cudaSuccess) return e;
     return c.d == 128 ? launch_combine<128>(p, stream) : launch_combine<64>(p, stream);
 }
