@@ -31,7 +31,8 @@
 // A pair that one CTA holds whole is finished there.  The others leave O / l and
 // LSE of their part in slot c + i (CTA c, pair i: along the list either c or i
 // grows, so slots are unique), and the combine kernel joins a pair's slots in
-// order.
+// order.  A small call (short table, few pairs) takes no list and no second kernel:
+// a cluster of CTAs shares a pair, and joins its parts through their shared memory.
 //
 // Warps: 0-3 (8-11, .., 16-19) softmax, four warps for each eight query rows, which
 // need nothing of one another; 4 loads K, 7 V, 5 issues MMAs, 6 lays out the queries
@@ -54,6 +55,7 @@ constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kMinLogScale = -60.0f;  // V scales below 2^-60 no longer move the reference
 constexpr float kNoMax = -3.402823466e38f;   // running maximum of a row that has seen no key
 constexpr int kSoftBar = 1;             // named barrier of softmax group 0
+constexpr int kMaxCluster = 8;          // most CTAs that share a pair without a list
 
 struct PagedParams {
     const __nv_bfloat16* q;             // rows i * R .. of pair i = b * Hkv + g
@@ -65,7 +67,7 @@ struct PagedParams {
     float* part_o;                      // [slots][R][d]
     float* part_lse;                    // [slots][R], log2
     int B, Hkv, Nq, R, n_pages, ps_shift, max_pages, causal;
-    int ctas;                           // resident CTAs of the split kernel
+    int ctas;                           // of the split kernel; in clusters: of a pair
     float scale_log2;
     DeviceStatus* status;
 };
@@ -108,6 +110,11 @@ struct Cfg {
         kStages * (2 * kTileBytes + kScaleBytes) + 2 * kQBytes + kPBufs * kPBytes + 1024;
     static constexpr int kCols = 2 * kN + kNP;
     static constexpr int kTmemCols = kCols <= 64 ? 64 : (kCols <= 128 ? 128 : 256);
+    // The longest table, in tiles, for which clusters of eight share a pair.  One
+    // sequence of 8 kv heads, with clusters and with the list: 1000 keys 5.4 and 6.4
+    // us, 2000 5.9 and 6.8; 4000 keys 7.9 and 7.6 in bf16 at d = 128, 7.1 and 8.4 in
+    // e4m3, 7.0 and 7.6 at d = 64; 8000 keys 9.2 and 7.8 at d = 64.
+    static constexpr int kClusterTiles = kRowBytes <= 128 ? 32 : 16;
     // How far a score may pass the running maximum before O is rescaled (log2):
     // bf16 P keeps its precision at any magnitude; e4m3 P ends at 448.
     static constexpr float kSlack = F8 ? 3.0f : 8.0f;
@@ -199,6 +206,16 @@ struct Cursor {
             t = 0;
         }
     }
+    // Without a list: CTA `rank` of the `ctas` that share a pair.
+    __device__ __forceinline__ Cursor(const PagedParams& p, int pair, int rank) {
+        b = pair / p.Hkv;
+        g = pair - b * p.Hkv;
+        extra = 0;
+        len = clamped_len(p, b);
+        const int tiles = tiles_of(len), per = (tiles + p.ctas - 1) / p.ctas;
+        t = rank * per;
+        left = max(0, min(per, tiles - t));
+    }
     // tiles of the current pair that belong to this CTA
     __device__ __forceinline__ int run() const { return min(tiles_of(len) - t, left); }
     // past `n` tiles of the current pair
@@ -276,7 +293,7 @@ __device__ __forceinline__ float warp_row_sums(float (&v)[RP], int lane, int& ro
     return v[0];
 }
 
-template <int D, bool F8, int G, int W>
+template <int D, bool F8, int G, int W, bool CLUSTER>
 __global__ void __launch_bounds__((Cfg<D, F8, G, W>::kThreads), (Cfg<D, F8, G, W>::kCtas))
 fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v,
@@ -299,6 +316,7 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
     __shared__ float4 row_max[RP], row_sum[RP];   // a value a softmax warp
     __shared__ float q_scale[2][RP];              // e4m3: score of one code product, log2 units
     __shared__ int row_query[RP];                 // r % Nq
+    __shared__ float cta_lse[RP];                 // in clusters: of this CTA's part, log2
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_sh;
     const WaitCtx wc{p.status, &abort_sh}, dc{p.status, nullptr};   // dc: for drains
@@ -336,7 +354,10 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
             sts_v4(sQ + e * 16, make_uint4(0u, 0u, 0u, 0u));
         if (warp == 6)
 #pragma unroll 1
-            for (int r = lane; r < RP; r += 32) row_query[r] = r % p.Nq;
+            for (int r = lane; r < RP; r += 32) {
+                row_query[r] = r % p.Nq;
+                cta_lse[r] = -CUDART_INF_F;       // a CTA without tiles
+            }
         fence_proxy_async_smem();
     }
     tc_fence_before();
@@ -349,8 +370,9 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
     // reads the lengths before it waits for this one.
     pdl_wait();
     pdl_launch_dependents();
-    const int c = blockIdx.x;
-    Cursor cur(p, List(p, lane), c);
+    // CTA c of the list; in clusters pair c
+    const int c = CLUSTER ? blockIdx.x / p.ctas : blockIdx.x;
+    Cursor cur = CLUSTER ? Cursor(p, c, cluster_rank()) : Cursor(p, List(p, lane), c);
 
     const int seg_shift = min(p.ps_shift, 7), seg = 1 << seg_shift;
     const int n_seg = kTile >> seg_shift, page_mask = (1 << p.ps_shift) - 1;
@@ -789,7 +811,7 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
             sts_u32(sum_w + row * 16, __float_as_uint(mine));    // several lanes, one value
             named_bar_sync(bar_id, 128);
             const int pair = cur.b * p.Hkv + cur.g;
-            const bool whole = tiles == tiles_of(cur.len);
+            const bool whole = !CLUSTER && tiles == tiles_of(cur.len);
             const long long out_row = (long long)(whole ? pair : c + pair) * p.R + r0;
             float inv[W], my_l = 0.0f, my_m = 0.0f;
 #pragma unroll
@@ -805,7 +827,9 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
             }
             if (j < W && r0 + j < p.R) {
                 const float lse2 = my_l == 0.0f ? -CUDART_INF_F : add_log2(my_m, my_l);
-                if (whole)
+                if (CLUSTER)
+                    cta_lse[r0 + j] = lse2;
+                else if (whole)
                     p.lse[out_row + j] = lse2 * kLn2;
                 else
                     p.part_lse[out_row + j] = lse2;
@@ -826,7 +850,9 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                     y += __uint_as_float(ob[r]);
                     y = inv[r] < 0.0f ? 0.0f : y * inv[r];
                     if (r0 + r < p.R) {
-                        if (whole)
+                        if (CLUSTER)              // P's buffers have been read
+                            sts_u32(sP + ((r0 + r) * D + j) * 4, __float_as_uint(y));
+                        else if (whole)
                             p.o[(out_row + r) * D + j] = __float2bfloat16_rn(y);
                         else
                             p.part_o[(out_row + r) * D + j] = y;
@@ -843,20 +869,56 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
         tc_fence_after();
         tmem_dealloc(tmem, C::kTmemCols);
     }
+    if constexpr (CLUSTER) {
+        static_assert(RP * D * 4 <= C::kPBufs * C::kPBytes, "a CTA's part of O in P's buffers");
+        // Thread j joins column j of rows rank, rank + ctas, ..: every part's LSE and
+        // O in one round trip.
+        cluster_sync();
+        const int j = threadIdx.x;
+        if (j < D) {
+#pragma unroll 1
+            for (int r = cluster_rank(); r < p.R; r += p.ctas) {
+                float ls[kMaxCluster], y[kMaxCluster], mx = -CUDART_INF_F;
+#pragma unroll
+                for (int s = 0; s < kMaxCluster; ++s) {
+                    ls[s] = -CUDART_INF_F;
+                    if (s < p.ctas) {
+                        ls[s] = ld_cluster_f32(smem_u32(cta_lse + r), s);
+                        y[s] = ld_cluster_f32(sP + (r * D + j) * 4, s);
+                    }
+                }
+#pragma unroll
+                for (int s = 0; s < kMaxCluster; ++s) mx = fmaxf(mx, ls[s]);
+                if (mx == -CUDART_INF_F) mx = 0.0f;
+                float sum = 0.0f, acc = 0.0f;
+#pragma unroll
+                for (int s = 0; s < kMaxCluster; ++s) {
+                    const float w = ex2(ls[s] - mx);
+                    sum += w;
+                    if (w != 0.0f) acc = fmaf(w, y[s], acc);   // a CTA without tiles left no O
+                }
+                const long long row = (long long)c * p.R + r;
+                p.o[row * D + j] = __float2bfloat16_rn(sum == 0.0f ? 0.0f : __fdividef(acc, sum));
+                if (j == 0) p.lse[row] = sum == 0.0f ? -CUDART_INF_F : add_log2(mx, sum) * kLn2;
+            }
+        }
+        cluster_sync();                           // nobody leaves while its part is read
+    }
 }
 
-// One warp per query row of the pairs that several CTAs share: the parts
-// weighted by exp(LSE_s - LSE), in slot order.  Rows of empty sequences are
-// written here.  Where a row's parts lie follows from the lengths alone and is
-// found while the split kernel still runs; after it, the parts' LSEs and the
-// first kPre parts of O come in one round trip.
+// One warp per query row and 32 columns, for the pairs that several CTAs share:
+// the parts weighted by exp(LSE_s - LSE), in slot order.  Rows of empty sequences
+// are written here.  Where a row's parts lie follows from the lengths alone and is
+// found while the split kernel still runs; after it, the LSEs and the columns of
+// 32 parts come in one round trip.
 template <int D>
 __global__ void __launch_bounds__(256)
 fa_paged_combine_kernel(const __grid_constant__ PagedParams p, int rows) {
-    constexpr int E = D / 32, kPre = 8;
+    constexpr int E = D / 32;                     // warps a row
     pdl_launch_dependents();
-    const int row = (int)((blockIdx.x * 256 + threadIdx.x) >> 5), lane = threadIdx.x & 31;
-    const int pair = min(row, rows - 1) / p.R, r = row - pair * p.R;
+    const int at_warp = (int)((blockIdx.x * 256 + threadIdx.x) >> 5), lane = threadIdx.x & 31;
+    const int row = min(at_warp / E, rows - 1), col = at_warp % E * 32 + lane;
+    const int pair = row / p.R, r = row - pair * p.R;
     const int b = pair / p.Hkv, g = pair - b * p.Hkv;
     const List list(p, lane);
     const int tiles = tiles_of(clamped_len(p, b));
@@ -872,124 +934,154 @@ fa_paged_combine_kernel(const __grid_constant__ PagedParams p, int rows) {
     // not end before the split kernel, whose results the next one in the
     // stream may read.
     pdl_wait();
-    if (row >= rows || parts == 1) return;
-    __nv_bfloat16* o = p.o + (long long)row * D + lane;
-    if (parts == 0) {
-#pragma unroll
-        for (int c = 0; c < E; ++c) o[32 * c] = __float2bfloat16_rn(0.0f);
-        if (lane == 0) p.lse[row] = -CUDART_INF_F;
-        return;
-    }
+    if (at_warp / E >= rows || parts == 1) return;
     const long long slot = (long long)c0 + pair;
     const float* lp = p.part_lse + slot * p.R + r;
-    const float* op = p.part_o + (slot * p.R + r) * D + lane;
+    const float* op = p.part_o + (slot * p.R + r) * D + col;
     const long long lstep = p.R, ostep = (long long)p.R * D;
-    const float l0 = lane < parts ? __ldcg(lp + lane * lstep) : -CUDART_INF_F;
-    float pre[kPre][E];
-#pragma unroll
-    for (int k = 0; k < kPre; ++k)
-#pragma unroll
-        for (int c = 0; c < E; ++c) pre[k][c] = k < parts ? __ldcg(op + k * ostep + 32 * c) : 0.0f;
-    float mx = l0;
-#pragma unroll 1
-    for (int s = lane + 32; s < parts; s += 32) mx = fmaxf(mx, __ldcg(lp + s * lstep));
-    mx = from_ordered(__reduce_max_sync(0xffffffffu, ordered(mx)));
-    if (mx == -CUDART_INF_F) mx = 0.0f;
-    float acc[E], sum = 0.0f;
-#pragma unroll
-    for (int c = 0; c < E; ++c) acc[c] = 0.0f;
+    float mx = -CUDART_INF_F, acc = 0.0f, sum = 0.0f;
 #pragma unroll 1
     for (int base = 0; base < parts; base += 32) {
-        const int s = base + lane;
-        const float ls = base == 0 ? l0 : (s < parts ? __ldcg(lp + s * lstep) : -CUDART_INF_F);
-        const float w = ex2(ls - mx);
-        const int cnt = min(32, parts - base);
-        sum += w;
-        int k = 0;
-        if (base == 0) {
+        // this round's parts: LSE of one a lane, its column of each
+        const float ls = base + lane < parts ? __ldcg(lp + (base + lane) * lstep) : -CUDART_INF_F;
+        float y[32];
 #pragma unroll
-            for (; k < kPre; ++k) {
-                const float wk = __shfl_sync(0xffffffffu, w, k);
+        for (int k = 0; k < 32; ++k) y[k] = 0.0f;
 #pragma unroll
-                for (int c = 0; c < E; ++c) acc[c] = fmaf(wk, pre[k][c], acc[c]);
-            }
-        }
-#pragma unroll 4
-        for (; k < cnt; ++k) {
-            const float wk = __shfl_sync(0xffffffffu, w, k);
+        for (int k = 0; k < 32; k += 8)
+            if (base + k < parts)
 #pragma unroll
-            for (int c = 0; c < E; ++c)
-                acc[c] = fmaf(wk, __ldcg(op + (base + k) * ostep + 32 * c), acc[c]);
-        }
+                for (int i = k; i < k + 8; ++i)
+                    if (base + i < parts) y[i] = __ldcg(op + (base + i) * ostep);
+        const float top = from_ordered(__reduce_max_sync(0xffffffffu, ordered(ls)));
+        const float m = fmaxf(mx, top);
+        const float ref = m == -CUDART_INF_F ? 0.0f : m;
+        const float old = ex2(mx - ref), w = ex2(ls - ref);
+        acc *= old;
+        sum = sum * old + w;                      // this lane's parts
+#pragma unroll
+        for (int k = 0; k < 32; ++k) acc = fmaf(__shfl_sync(0xffffffffu, w, k), y[k], acc);
+        mx = m;
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    const float inv = __fdividef(1.0f, sum);
-#pragma unroll
-    for (int c = 0; c < E; ++c)
-        o[32 * c] = __float2bfloat16_rn(sum == 0.0f ? 0.0f : acc[c] * inv);
-    if (lane == 0) p.lse[row] = sum == 0.0f ? -CUDART_INF_F : add_log2(mx, sum) * kLn2;
+    p.o[(long long)row * D + col] =
+        __float2bfloat16_rn(sum == 0.0f ? 0.0f : __fdividef(acc, sum));
+    if (col == 0)
+        p.lse[row] = sum == 0.0f ? -CUDART_INF_F : add_log2(mx, sum) * kLn2;
 }
 
-// A launch whose blocks may come in while the kernel before in the stream still
-// runs; they wait for it (pdl_wait) before they read what it wrote.
+// A launch (in clusters of `cluster` blocks) whose blocks may come in while the
+// kernel before in the stream still runs; they wait for it (pdl_wait) before they read what it wrote.
 template <typename... Params, typename... Args>
 cudaError_t launch_pdl(void (*kern)(Params...), unsigned grid, unsigned threads, size_t smem,
-                       cudaStream_t stream, const Args&... args) {
+                       int cluster, cudaStream_t stream, const Args&... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     count_launch();
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-template <int D, bool F8, int G, int W>
-cudaError_t launch_split(const CUtensorMap& tk, const CUtensorMap& tv, PagedParams& p,
-                         cudaStream_t stream) {
-    using C = Cfg<D, F8, G, W>;
-    static_assert(C::kSmem + 2048 <= 227 * 1024, "shared memory of one CTA");
-    auto kern = fa_decode_paged_kernel<D, F8, G, W>;
+// Once a device and kernel: the shared memory it may use.
+template <int D, bool F8, int G, int W, bool CLUSTER>
+cudaError_t configure(int dev) {
     static std::atomic<unsigned long long> configured{0};     // a bit a device
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (!((configured.load(std::memory_order_acquire) >> dev) & 1)) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-        if (e != cudaSuccess) return e;
-        configured.fetch_or(1ull << dev, std::memory_order_release);
-    }
-    // no more CTAs than there can be tiles
-    const int longest = p.max_pages << p.ps_shift;
-    const long long most = (long long)p.B * p.Hkv * ((longest + kTile - 1) / kTile);
-    long long grid = (long long)(device_sm_count() > 0 ? device_sm_count() : 152) * C::kCtas;
-    if (grid > kPagedMaxCtas) grid = kPagedMaxCtas;
-    if (grid > most) grid = most;
-    p.ctas = (int)grid;
-    return launch_pdl(kern, (unsigned)grid, C::kThreads, C::kSmem, stream, tk, tv, p);
+    if ((configured.load(std::memory_order_acquire) >> dev) & 1) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(fa_decode_paged_kernel<D, F8, G, W, CLUSTER>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               Cfg<D, F8, G, W>::kSmem);
+    if (e == cudaSuccess) configured.fetch_or(1ull << dev, std::memory_order_release);
+    return e;
 }
 
-template <int D, bool F8>
-cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, PagedParams& p,
-                        cudaStream_t stream) {
-    if (p.R == 1) return launch_split<D, F8, 1, 1>(tk, tv, p, stream);
-    if (p.R <= 4) return launch_split<D, F8, 1, 4>(tk, tv, p, stream);
-    if (p.R <= 8) return launch_split<D, F8, 1, 8>(tk, tv, p, stream);
-    if (p.R <= 16) return launch_split<D, F8, 2, 8>(tk, tv, p, stream);
-    return launch_split<D, F8, 4, 8>(tk, tv, p, stream);
+// Clusters of 2^log CTAs that the device runs at once (found once a device and
+// kernel; 0 where it cannot say).  The SMs of a GPU come in groups that a cluster
+// does not cross, so this is less than SMs / size.
+template <int D, bool F8, int G, int W>
+int clusters_at_once(int dev, int log) {
+    using C = Cfg<D, F8, G, W>;
+    static std::atomic<int> known[64][4];                     // 1 + the number
+    std::atomic<int>& n = known[dev][log];
+    if (int k = n.load(std::memory_order_relaxed)) return k - 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1u << log);
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1u << log;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int k = 0;
+    if (cudaOccupancyMaxActiveClusters(&k, fa_decode_paged_kernel<D, F8, G, W, true>, &cfg) !=
+        cudaSuccess)
+        k = 0;
+    n.store(k + 1, std::memory_order_relaxed);
+    return k;
 }
 
 template <int D>
 cudaError_t launch_combine(const PagedParams& p, cudaStream_t stream) {
     const int rows = p.B * p.Hkv * p.R;
-    return launch_pdl(fa_paged_combine_kernel<D>, (unsigned)((rows + 7) / 8), 256, 0, stream, p,
-                      rows);
+    const long long warps = (long long)rows * (D / 32);
+    return launch_pdl(fa_paged_combine_kernel<D>, (unsigned)((warps + 7) / 8), 256, 0, 1, stream,
+                      p, rows);
+}
+
+template <int D, bool F8, int G, int W>
+cudaError_t launch_attend(const CUtensorMap& tk, const CUtensorMap& tv, PagedParams& p,
+                          cudaStream_t stream) {
+    using C = Cfg<D, F8, G, W>;
+    static_assert(C::kSmem + 2048 <= 227 * 1024, "shared memory of one CTA");
+    const int longest = ((p.max_pages << p.ps_shift) + kTile - 1) / kTile;    // tiles of a pair
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if constexpr (G == 1) {
+        int log = 0;
+        while ((1 << log) < longest && (1 << log) < kMaxCluster) ++log;
+        if (longest <= C::kClusterTiles) {
+            if ((e = configure<D, F8, G, W, true>(dev)) != cudaSuccess) return e;
+            if ((long long)p.B * p.Hkv <= clusters_at_once<D, F8, G, W>(dev, log)) {
+                p.ctas = 1 << log;
+                return launch_pdl(fa_decode_paged_kernel<D, F8, G, W, true>,
+                                  (unsigned)(p.B * p.Hkv) << log, C::kThreads, C::kSmem, p.ctas,
+                                  stream, tk, tv, p);
+            }
+        }
+    }
+    if ((e = configure<D, F8, G, W, false>(dev)) != cudaSuccess) return e;
+    // no more CTAs than there can be tiles
+    const long long most = (long long)p.B * p.Hkv * longest;
+    long long grid = (long long)(device_sm_count() > 0 ? device_sm_count() : 152) * C::kCtas;
+    if (grid > kPagedMaxCtas) grid = kPagedMaxCtas;
+    if (grid > most) grid = most;
+    p.ctas = (int)grid;
+    e = launch_pdl(fa_decode_paged_kernel<D, F8, G, W, false>, (unsigned)grid, C::kThreads,
+                   C::kSmem, 1, stream, tk, tv, p);
+    return e == cudaSuccess ? launch_combine<D>(p, stream) : e;
+}
+
+template <int D, bool F8>
+cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, PagedParams& p,
+                        cudaStream_t stream) {
+    if (p.R == 1) return launch_attend<D, F8, 1, 1>(tk, tv, p, stream);
+    if (p.R <= 4) return launch_attend<D, F8, 1, 4>(tk, tv, p, stream);
+    if (p.R <= 8) return launch_attend<D, F8, 1, 8>(tk, tv, p, stream);
+    if (p.R <= 16) return launch_attend<D, F8, 2, 8>(tk, tv, p, stream);
+    return launch_attend<D, F8, 4, 8>(tk, tv, p, stream);
 }
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
@@ -1033,12 +1125,11 @@ cudaError_t launch_fwd_decode_paged(const PagedCache& c, const void* q, void* o,
     p.causal = causal;
     p.scale_log2 = scale * kLog2e;
     p.status = status;
-    const cudaError_t e = c.d == 128 ? (f8 ? launch_rows<128, true>(tk, tv, p, stream)
-                                           : launch_rows<128, false>(tk, tv, p, stream))
-                                     : (f8 ? launch_rows<64, true>(tk, tv, p, stream)
-                                           : launch_rows<64, false>(tk, tv, p, stream));
-    if (e != cudaSuccess) return e;
-    return c.d == 128 ? launch_combine<128>(p, stream) : launch_combine<64>(p, stream);
+    if (c.d == 128)
+        return f8 ? launch_rows<128, true>(tk, tv, p, stream)
+                  : launch_rows<128, false>(tk, tv, p, stream);
+    return f8 ? launch_rows<64, true>(tk, tv, p, stream)
+              : launch_rows<64, false>(tk, tv, p, stream);
 }
 
 }  // namespace fa

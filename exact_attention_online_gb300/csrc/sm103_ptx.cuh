@@ -625,6 +625,27 @@ __device__ __forceinline__ float lds_f32(uint32_t a) {
     return v;
 }
 
+// Thread-block clusters: this block's rank, the barrier of all the cluster's
+// threads (shared memory written before it may be read after it), and a float of
+// another block's shared memory.
+__device__ __forceinline__ int cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return (int)r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t a, int rank) {
+    float v;
+    asm volatile(
+        "{.reg .b32 r;\n\t"
+        "mapa.shared::cluster.u32 r, %1, %2;\n\t"
+        "ld.shared::cluster.f32 %0, [r];}" : "=f"(v) : "r"(a), "r"(rank) : "memory");
+    return v;
+}
+
 // Programmatic dependent launch: let the next kernel's blocks come in / wait
 // until the kernel before has finished and its writes are visible.
 __device__ __forceinline__ void pdl_launch_dependents() {

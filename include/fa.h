@@ -522,9 +522,9 @@ FA_API fa_status fa_kv_gather_varlen(const void* k_pages, const void* v_pages,
  * graphs) need one each.  The result does not depend on the order in which
  * the CTAs run: it is the same bit for bit on every call with the same inputs.
  * Lengths and tables are read on the device, so a captured call may be replayed
- * with other contents of the same tensors.  Asynchronous on `stream`; two
- * launches, each of which may begin (not read anything) while the kernel before
- * it on the stream still runs.
+ * with other contents of the same tensors.  Asynchronous on `stream`; one
+ * launch (short tables and few sequences) or two, each of which may begin (not
+ * read anything) while the kernel before it on the stream still runs.
  */
 FA_API size_t fa_fwd_decode_paged_workspace_size(int B, int H, int Hkv, int Nq, int d);
 FA_API fa_status fa_fwd_decode_paged(const void* q, const void* k_pages, const void* v_pages,

@@ -101,12 +101,16 @@ SHAPES = {
 
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 @pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
+@pytest.mark.parametrize("wide", [False, True], ids=["narrow", "wide"])
 @pytest.mark.parametrize("name", sorted(SHAPES))
-def test_attend(name, causal, kv):
-    """Rows past each sequence's length hold NaN, and so do the pages of no sequence."""
+def test_attend(name, wide, causal, kv):
+    """Rows past each sequence's length hold NaN, and so do the pages of no sequence.  A table
+    of no more pages than are needed, or of 8192 positions (few pairs and a short table are
+    shared by clusters, other calls by a list of tiles)."""
     H, Hkv, Nq, d, ps, lens = SHAPES[name]
-    src = Cache(lens, Hkv, d, ps, kv, seed=len(name))
-    cache = Cache(lens, Hkv, d, ps, kv, seed=len(name), fill="nan")
+    most = max(8192 // ps, -(-max(lens) // ps)) if wide else None
+    src = Cache(lens, Hkv, d, ps, kv, seed=len(name), max_pages=most)
+    cache = Cache(lens, Hkv, d, ps, kv, seed=len(name), fill="nan", max_pages=most)
     raw = lambda t: t.view(torch.uint8) if kv == "e4m3" else t
     for b, n in enumerate(lens):
         page, r = src._at(b, 0, n)
