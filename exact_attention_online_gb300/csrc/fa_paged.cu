@@ -110,11 +110,11 @@ struct Cfg {
         kStages * (2 * kTileBytes + kScaleBytes) + 2 * kQBytes + kPBufs * kPBytes + 1024;
     static constexpr int kCols = 2 * kN + kNP;
     static constexpr int kTmemCols = kCols <= 64 ? 64 : (kCols <= 128 ? 128 : 256);
-    // The longest table, in tiles, for which clusters of eight share a pair.  One
-    // sequence of 8 kv heads, with clusters and with the list: 1000 keys 5.4 and 6.4
-    // us, 2000 5.9 and 6.8; 4000 keys 7.9 and 7.6 in bf16 at d = 128, 7.1 and 8.4 in
-    // e4m3, 7.0 and 7.6 at d = 64; 8000 keys 9.2 and 7.8 at d = 64.
-    static constexpr int kClusterTiles = kRowBytes <= 128 ? 32 : 16;
+    // Most tiles of a CTA where clusters share the pairs.  One sequence of 8 kv
+    // heads, with clusters (of eight) and with the list: 1000 keys 5.4 and 6.4 us,
+    // 2000 5.9 and 6.8; 4000 keys (four tiles a CTA) 7.9 and 7.6 in bf16 at d = 128,
+    // 7.1 and 8.4 in e4m3, 7.0 and 7.6 at d = 64; 8000 keys 9.2 and 7.8 at d = 64.
+    static constexpr int kClusterTiles = kRowBytes <= 128 ? 4 : 2;
     // How far a score may pass the running maximum before O is rescaled (log2):
     // bf16 P keeps its precision at any magnitude; e4m3 P ends at 448.
     static constexpr float kSlack = F8 ? 3.0f : 8.0f;
@@ -871,36 +871,35 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
     }
     if constexpr (CLUSTER) {
         static_assert(RP * D * 4 <= C::kPBufs * C::kPBytes, "a CTA's part of O in P's buffers");
-        // Thread j joins column j of rows rank, rank + ctas, ..: every part's LSE and
-        // O in one round trip.
+        // The CTAs deal the rows out among them, D threads a row, one column a
+        // thread: every part's LSE and O in one round trip.
         cluster_sync();
-        const int j = threadIdx.x;
-        if (j < D) {
+        const int j = threadIdx.x % D;
 #pragma unroll 1
-            for (int r = cluster_rank(); r < p.R; r += p.ctas) {
-                float ls[kMaxCluster], y[kMaxCluster], mx = -CUDART_INF_F;
+        for (int r = threadIdx.x / D * p.ctas + cluster_rank(); r < p.R;
+             r += C::kThreads / D * p.ctas) {
+            float ls[kMaxCluster], y[kMaxCluster], mx = -CUDART_INF_F;
 #pragma unroll
-                for (int s = 0; s < kMaxCluster; ++s) {
-                    ls[s] = -CUDART_INF_F;
-                    if (s < p.ctas) {
-                        ls[s] = ld_cluster_f32(smem_u32(cta_lse + r), s);
-                        y[s] = ld_cluster_f32(sP + (r * D + j) * 4, s);
-                    }
+            for (int s = 0; s < kMaxCluster; ++s) {
+                ls[s] = -CUDART_INF_F;
+                if (s < p.ctas) {
+                    ls[s] = ld_cluster_f32(smem_u32(cta_lse + r), s);
+                    y[s] = ld_cluster_f32(sP + (r * D + j) * 4, s);
                 }
-#pragma unroll
-                for (int s = 0; s < kMaxCluster; ++s) mx = fmaxf(mx, ls[s]);
-                if (mx == -CUDART_INF_F) mx = 0.0f;
-                float sum = 0.0f, acc = 0.0f;
-#pragma unroll
-                for (int s = 0; s < kMaxCluster; ++s) {
-                    const float w = ex2(ls[s] - mx);
-                    sum += w;
-                    if (w != 0.0f) acc = fmaf(w, y[s], acc);   // a CTA without tiles left no O
-                }
-                const long long row = (long long)c * p.R + r;
-                p.o[row * D + j] = __float2bfloat16_rn(sum == 0.0f ? 0.0f : __fdividef(acc, sum));
-                if (j == 0) p.lse[row] = sum == 0.0f ? -CUDART_INF_F : add_log2(mx, sum) * kLn2;
             }
+#pragma unroll
+            for (int s = 0; s < kMaxCluster; ++s) mx = fmaxf(mx, ls[s]);
+            if (mx == -CUDART_INF_F) mx = 0.0f;
+            float sum = 0.0f, acc = 0.0f;
+#pragma unroll
+            for (int s = 0; s < kMaxCluster; ++s) {
+                const float w = ex2(ls[s] - mx);
+                sum += w;
+                if (w != 0.0f) acc = fmaf(w, y[s], acc);   // a CTA without tiles left no O
+            }
+            const long long row = (long long)c * p.R + r;
+            p.o[row * D + j] = __float2bfloat16_rn(sum == 0.0f ? 0.0f : __fdividef(acc, sum));
+            if (j == 0) p.lse[row] = sum == 0.0f ? -CUDART_INF_F : add_log2(mx, sum) * kLn2;
         }
         cluster_sync();                           // nobody leaves while its part is read
     }
@@ -972,7 +971,8 @@ fa_paged_combine_kernel(const __grid_constant__ PagedParams p, int rows) {
 }
 
 // A launch (in clusters of `cluster` blocks) whose blocks may come in while the
-// kernel before in the stream still runs; they wait for it (pdl_wait) before they read what it wrote.
+// kernel before in the stream still runs; they wait for it (pdl_wait) before they
+// read what it wrote.
 template <typename... Params, typename... Args>
 cudaError_t launch_pdl(void (*kern)(Params...), unsigned grid, unsigned threads, size_t smem,
                        int cluster, cudaStream_t stream, const Args&... args) {
@@ -1049,17 +1049,21 @@ cudaError_t launch_attend(const CUtensorMap& tk, const CUtensorMap& tv, PagedPar
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if constexpr (G == 1) {
+    // Clusters, one a pair, where all of them run at once and leave few tiles to a
+    // CTA: the largest size that fits, up to a CTA a tile, or one for every four
+    // rows to join (32 rows of 250 keys: 8.1 us with 8 CTAs, 9.0 with a CTA a tile).
+    // Smaller ones than eight beat the list too: 16 sequences of 8 kv heads and 250
+    // keys 5.5 and 6.3 us, 8 of 1000 keys in e4m3 7.0 and 7.9.
+    if (longest <= kMaxCluster * C::kClusterTiles) {
+        if ((e = configure<D, F8, G, W, true>(dev)) != cudaSuccess) return e;
         int log = 0;
-        while ((1 << log) < longest && (1 << log) < kMaxCluster) ++log;
-        if (longest <= C::kClusterTiles) {
-            if ((e = configure<D, F8, G, W, true>(dev)) != cudaSuccess) return e;
-            if ((long long)p.B * p.Hkv <= clusters_at_once<D, F8, G, W>(dev, log)) {
-                p.ctas = 1 << log;
-                return launch_pdl(fa_decode_paged_kernel<D, F8, G, W, true>,
-                                  (unsigned)(p.B * p.Hkv) << log, C::kThreads, C::kSmem, p.ctas,
-                                  stream, tk, tv, p);
-            }
+        while ((1 << log) < max(longest, p.R / 4) && (1 << log) < kMaxCluster) ++log;
+        for (; log >= 0 && longest <= C::kClusterTiles << log; --log) {
+            if ((long long)p.B * p.Hkv > clusters_at_once<D, F8, G, W>(dev, log)) continue;
+            p.ctas = 1 << log;
+            return launch_pdl(fa_decode_paged_kernel<D, F8, G, W, true>,
+                              (unsigned)(p.B * p.Hkv) << log, C::kThreads, C::kSmem, p.ctas,
+                              stream, tk, tv, p);
         }
     }
     if ((e = configure<D, F8, G, W, false>(dev)) != cudaSuccess) return e;

@@ -95,6 +95,8 @@ SHAPES = {
     "many_empty": (2, 1, 1, 128, 16, [0, 0, 40, 0, 0, 0, 9, 0]),
     "all_empty": (2, 2, 1, 64, 16, [0, 0]),
     "batch70": (2, 2, 1, 64, 16, [(37 * b) % 150 for b in range(70)]),
+    "batch20_rows24": (48, 2, 1, 128, 16, [(61 * b) % 513 for b in range(20)]),
+    "batch9_rows12": (12, 4, 4, 64, 32, [(97 * b) % 600 for b in range(9)]),
     "long": (2, 1, 1, 128, 16, [20000]),
 }
 
