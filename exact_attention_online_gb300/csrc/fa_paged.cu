@@ -246,7 +246,9 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int site, c
 }
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int site,
                                           const WaitCtx& wc) {
-    return __all_sync(0xffffffffu, wait(bar, parity, site, wc));
+    // a vote before the branch keeps the warp together where the phase is complete
+    if (__all_sync(0xffffffffu, mbar_try_wait(smem_u32(bar), parity))) return true;
+    return __all_sync(0xffffffffu, wait_on(bar, parity, site, wc));
 }
 
 // Monotone map of a float's order onto signed integers (its own inverse).
@@ -448,9 +450,11 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
         auto desc = [&](uint32_t a, uint32_t lbo) {
             return C::kSw == 128 ? sdesc_sw128(a, lbo, kGroup) : sdesc_sw64(a, lbo, kGroup);
         };
-        // The warp stays together and one elected lane issues: descriptors then
-        // travel in uniform registers (a branch on lane == 0 cost 12 us of 49 with
-        // 16 rows an e4m3 cache: B8, four tokens, 8K to 16K keys).
+        // The warp stays together and one elected lane issues, by a predicate:
+        // descriptors then travel in uniform registers (a branch on lane == 0 cost
+        // 12 us of 49 with 16 rows an e4m3 cache: B8, four tokens, 8K to 16K keys).
+        // A second warp for P V, so that S never queues behind it, gave nothing
+        // (41.2 and 40.8 us there) and takes registers (8 rows: 37.4 and 39.2).
         const bool leader = elect_one();
         // O^T (+)= V_u^T P_u^T
         auto pv = [&](int u, bool first) -> bool {
@@ -463,17 +467,14 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
             // columns (d = 64: K) is the leading-dimension stride
             const uint64_t vd = desc(sKV + s * 2 * TB, C::kChunks == 2 ? kTile * C::kSw : TB);
             const uint64_t pd = sdesc_sw128(sP + u % C::kPBufs * C::kPBytes, 16, 1024);
-            if (leader) {
 #pragma unroll
-                for (int kk = 0; kk < (F8 ? 4 : 8); ++kk) {
-                    const uint64_t a = vd + (uint64_t)(kk * (F8 ? 32 : 16) * C::kSw >> 4);
-                    const uint64_t b = pd + kmajor_step(kk, NP * 128);
-                    if (F8) mma_ss_f8(tmem + kColO, a, b, idesc_o, !first || kk > 0);
-                    else mma_ss(tmem + kColO, a, b, idesc_o, !first || kk > 0);
-                }
-                mma_commit(&bar_pv[s]);
+            for (int kk = 0; kk < (F8 ? 4 : 8); ++kk) {
+                const uint64_t a = vd + (uint64_t)(kk * (F8 ? 32 : 16) * C::kSw >> 4);
+                const uint64_t b = pd + kmajor_step(kk, NP * 128);
+                if (F8) mma_ss_f8_if(leader, tmem + kColO, a, b, idesc_o, !first || kk > 0);
+                else mma_ss_if(leader, tmem + kColO, a, b, idesc_o, !first || kk > 0);
             }
-            __syncwarp();
+            mma_commit_if(leader, &bar_pv[s]);
             return true;
         };
         bool ok = true;
@@ -495,18 +496,15 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                     tc_fence_after();
                     // S_u's buffer was read before P_{u-2} was complete
                     const uint64_t kd = desc(sKV + s * 2 * TB + TB, 16);
-                    if (leader) {
 #pragma unroll
-                        for (int kk = 0; kk < C::kRowBytes / 32; ++kk) {
-                            const uint64_t a = kd + kmajor_step(kk, kTile * 128);
-                            const uint64_t b = qd + kmajor_step(kk, N * 128);
-                            if (F8) mma_ss_f8(tmem + (u & 1) * N, a, b, idesc_s, kk > 0);
-                            else mma_ss(tmem + (u & 1) * N, a, b, idesc_s, kk > 0);
-                        }
-                        mma_commit(&bar_s[s]);
-                        if (t + 1 == tiles) mma_commit(&bar_q_free[pairs & 1]);
+                    for (int kk = 0; kk < C::kRowBytes / 32; ++kk) {
+                        const uint64_t a = kd + kmajor_step(kk, kTile * 128);
+                        const uint64_t b = qd + kmajor_step(kk, N * 128);
+                        if (F8) mma_ss_f8_if(leader, tmem + (u & 1) * N, a, b, idesc_s, kk > 0);
+                        else mma_ss_if(leader, tmem + (u & 1) * N, a, b, idesc_s, kk > 0);
                     }
-                    __syncwarp();
+                    mma_commit_if(leader, &bar_s[s]);
+                    mma_commit_if(leader && t + 1 == tiles, &bar_q_free[pairs & 1]);
                 }
                 // P V one tile behind, across pairs: the softmax warps have read
                 // a pair's O before they give the next pair's first P
