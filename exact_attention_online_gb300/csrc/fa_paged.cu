@@ -8,12 +8,12 @@
 //   S_t^T = K_t Q^T      A = the tile's 128 keys, B = the query rows (N = 16 ..)
 //   O^T  += V_t^T P_t^T  A = V read transposed (MN-major), B = P_t, O^T in TMEM
 // With the keys on the MMA's M side a tile costs one read of K and V from
-// shared memory (N is 16 to 64 columns), each of the 128 softmax threads owns
-// one key and eight rows' scores, nothing is computed for absent query rows past the
-// next 8, 16 or 32, and no thread needs another's score: the running maximum m of a
-// row moves only when some key passes it by 2^kSlack (a vote of the four
-// warps), the row sums stay one partial per thread until the end, and the
-// rescale of O^T touches few columns.
+// shared memory (N is 16 to 64 columns), a softmax thread owns one key and up to
+// sixteen rows' scores, nothing is computed for absent query rows past the next 1,
+// 4, 8, 16 or 32, and no thread needs another's score: the running maximum m of a
+// row moves only when some key passes it by 2^kSlack (a vote of the four warps),
+// the row sums stay one partial per thread until the end, and the rescale of O^T
+// touches few columns.  Neighbouring rows go through the fp32 units in pairs.
 //
 // e4m3 pages are multiplied as they are.  A bf16 query row, times the power of
 // two that brings its largest entry into [2^7, 2^8), is the sum of two e4m3
@@ -34,8 +34,8 @@
 // order.  A small call (short table, few pairs) takes no list and no second kernel:
 // a cluster of CTAs shares a pair, and joins its parts through their shared memory.
 //
-// Warps: 0-3 (8-11, .., 16-19) softmax, four warps for each eight query rows, which
-// need nothing of one another; 4 loads K, 7 V, 5 issues MMAs, 6 lays out the queries
+// Warps: 0-3 (and 8-11) softmax, four warps for a group of query rows, which need
+// nothing of one another; 4 loads K, 7 V, 5 issues MMAs, 6 lays out the queries
 // of a pair and loads its scales.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -49,7 +49,6 @@ namespace fa {
 namespace {
 
 constexpr int kTile = 128;              // keys per tile
-constexpr int kRows = 8;                // rows of Q, S and P a softmax group owns
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kMinLogScale = -60.0f;  // V scales below 2^-60 no longer move the reference
@@ -72,10 +71,11 @@ struct PagedParams {
     DeviceStatus* status;
 };
 
-// Sizes of one variant: head dimension, page type, groups of eight query rows, and
-// how many of its eight rows a group works on (the others are zero).
+// Sizes of one variant: head dimension, page type, groups of query rows, and how many
+// rows a group works on (of at least eight; the others are zero).
 template <int D, bool F8, int G, int W>
 struct Cfg {
+    static constexpr int kRows = W > 8 ? W : 8;    // of Q, S and P that a softmax group owns
     static constexpr int RP = kRows * G;
     static constexpr int kThreads = 128 + 128 * G;
     static constexpr int kN = F8 ? 2 * RP : (RP < 16 ? 16 : RP);   // columns of S, rows of Q
@@ -90,12 +90,12 @@ struct Cfg {
     static constexpr int kQBytes = kN * kRowBytes;
     static constexpr int kPRow = F8 ? kTile : 2 * kTile;
     static constexpr int kPBytes = kNP * kPRow;
-    static constexpr int kPBufs = !F8 && D == 128 && G == 4 ? 1 : 2;   // no room for two there
+    static constexpr int kPBufs = !F8 && D == 128 && RP == 32 ? 1 : 2;   // no room for two there
     static constexpr int kScaleBytes = F8 ? 2 * kTile * 4 : 0;
     // bf16 rows of 128 fill an SM with one CTA.  Smaller ones leave less time a
     // tile, and with up to 8 rows two CTAs fit, so that one's softmax and
     // epilogue hide behind the other's.
-    static constexpr int kCtas = kRowBytes <= 128 && G == 1 ? 2 : 1;
+    static constexpr int kCtas = kRowBytes <= 128 && RP == 8 ? 2 : 1;
     static constexpr int kRing = (kCtas == 2 ? 113 : 227) * 1024 - 1024 - 2048 - 2 * kQBytes -
                                  kPBufs * kPBytes;
     static constexpr int kStages = kRing / (2 * kTileBytes + kScaleBytes);
@@ -244,6 +244,15 @@ __device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, int site, c
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int site, const WaitCtx& wc) {
     return mbar_try_wait(smem_u32(bar), parity) || wait_on(bar, parity, site, wc);
 }
+// Two barriers' phases, both tried before either answer is needed (16 rows of e4m3,
+// d = 64: 35.8 us instead of 37.2 with one after the other).
+__device__ __forceinline__ bool wait_both(uint64_t* a, uint64_t* b, uint32_t parity, int site,
+                                          const WaitCtx& wc) {
+    const bool there = mbar_try_wait(smem_u32(a), parity);
+    const bool too = mbar_try_wait(smem_u32(b), parity);
+    return (there && too) ||
+           (wait_on(a, parity, site, wc) && wait_on(b, parity, site + 1, wc));
+}
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int site,
                                           const WaitCtx& wc) {
     // a vote before the branch keeps the warp together where the phase is complete
@@ -258,6 +267,22 @@ __device__ __forceinline__ int ordered(float x) {
 }
 __device__ __forceinline__ float from_ordered(int i) {
     return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
+}
+
+// Rows r and r + 1 of a thread's W as a pair (with one row: and zero).
+template <int W>
+__device__ __forceinline__ uint64_t pair(const float (&x)[W], int r) {
+    return f2(x[r], W > 1 ? x[(r + 1) % W] : 0.0f);
+}
+template <int W>
+__device__ __forceinline__ uint64_t pair(const uint32_t (&x)[W], int r) {
+    return f2(__uint_as_float(x[r]), W > 1 ? __uint_as_float(x[(r + 1) % W]) : 0.0f);
+}
+template <int W>
+__device__ __forceinline__ void put(float (&x)[W], int r, uint64_t v) {
+    float hi;
+    f2_split(v, x[r], hi);
+    if (W > 1) x[(r + 1) % W] = hi;
 }
 
 // m + log2 l for l > 0.  The exponent of l is added to m first: the two cancel
@@ -642,7 +667,7 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
         // Thread j of a group holds key j of the tile and the group's first W
         // rows.  A wait that gives up clears `ok` and skips the later waits, but
         // every thread stays in step with the named barriers.
-        const int group = warp < 4 ? 0 : (warp >> 2) - 1, r0 = group * kRows;
+        const int group = warp < 4 ? 0 : (warp >> 2) - 1, r0 = group * C::kRows;
         const int quarter = warp & 3, j = quarter * 32 + lane;
         const int bar_id = kSoftBar + group;
         const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16) + r0;
@@ -676,8 +701,8 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                 // S_u complete means P_{u-2} V_{u-2} complete too: a commit
                 // covers every MMA before it, and that one was issued before
                 // S_u, so with two buffers P_u's may be written
-                ok = ok && wait(&bar_s[s], (u / S) & 1, 111, wc);
-                if (F8) ok = ok && wait(&bar_x[s], (u / S) & 1, 112, wc);
+                ok = ok && (F8 ? wait_both(&bar_s[s], &bar_x[s], (u / S) & 1, 111, wc)
+                               : wait(&bar_s[s], (u / S) & 1, 111, wc));
                 __syncwarp();
                 tc_fence_after();
                 uint32_t sa[W], sb[W];
@@ -694,11 +719,12 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                 }
                 float x[W];
 #pragma unroll
-                for (int r = 0; r < W; ++r) {
+                for (int r = 0; r < W; r += 2) {
+                    const uint64_t a = pair(sa, r);
                     if constexpr (F8)
-                        x[r] = (__uint_as_float(sa[r]) + __uint_as_float(sb[r])) * (qc[r] * ks);
+                        put(x, r, f2_mul(f2_add(a, pair(sb, r)), f2_mul(pair(qc, r), f2(ks, ks))));
                     else
-                        x[r] = __uint_as_float(sa[r]) * p.scale_log2;
+                        put(x, r, f2_mul(a, f2(p.scale_log2, p.scale_log2)));
                 }
                 if (tile_end > cur.len - (p.causal ? p.Nq - 1 : 0)) {
 #pragma unroll
@@ -708,11 +734,14 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                     }
                 }
                 // Does any score pass the running maximum by 2^kSlack?
-                const float slack = C::kSlack - lv;
-                bool need = false;
+                float top = -CUDART_INF_F;
 #pragma unroll
-                for (int r = 0; r < W; ++r) need |= x[r] > m[r] + slack;
-                if (named_bar_or(bar_id, 128, need)) {
+                for (int r = 0; r < W; r += 2) {
+                    float lo, hi;
+                    f2_split(f2_sub(pair(x, r), pair(m, r)), lo, hi);
+                    top = W > 1 ? fmax3(top, lo, hi) : lo;
+                }
+                if (named_bar_or(bar_id, 128, top > C::kSlack - lv)) {
 #pragma unroll
                     for (int r = 0; r < W; ++r) {
                         const int y = __reduce_max_sync(0xffffffffu, ordered(x[r] + lv));
@@ -756,19 +785,18 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                 const float wv = vs * C::kPScale;
 #pragma unroll
                 for (int r = 0; r < W; r += 2) {
-                    const float e0 = ex2(x[r] - m[r]);
-                    l[r] += e0;
-                    float e1 = 0.0f;
-                    if (W > 1) {
-                        e1 = ex2(x[(r + 1) % W] - m[(r + 1) % W]);
-                        l[(r + 1) % W] += e1;
-                    }
-                    const uint32_t a0 = (pw ^ (r << 4)) + r * 128;
-                    const uint32_t a1 = (pw ^ ((r + 1) << 4)) + (r + 1) * 128;
+                    float e0, e1;
+                    f2_split(f2_sub(pair(x, r), pair(m, r)), e0, e1);
+                    e0 = ex2(e0);
+                    e1 = W > 1 ? ex2(e1) : 0.0f;
+                    put(l, r, f2_add(pair(l, r), f2(e0, e1)));
+                    const uint32_t a0 = (pw ^ ((r & 7) << 4)) + r * 128;
+                    const uint32_t a1 = (pw ^ (((r + 1) & 7) << 4)) + (r + 1) * 128;
                     if constexpr (F8) {
                         // by way of fp16, whose 11 bits hold both terms' 8
                         uint32_t h1, h2;
-                        split_e4m3x2(pack_f16x2(e0 * wv, e1 * wv), h1, h2);
+                        f2_split(f2_mul(f2(e0, e1), f2(wv, wv)), e0, e1);
+                        split_e4m3x2(pack_f16x2(e0, e1), h1, h2);
                         sts_u8(a0, h1);
                         sts_u8(a0 + RP * 128, h2);
                         if (W > 1) {
@@ -777,8 +805,10 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                         }
                     } else {
                         const uint32_t h1 = pack_bf16x2(e0, e1);
-                        const uint32_t h2 = pack_bf16x2(e0 - __uint_as_float(h1 << 16),
-                                                        e1 - __uint_as_float(h1 & 0xffff0000u));
+                        f2_split(f2_sub(f2(e0, e1), f2(__uint_as_float(h1 << 16),
+                                                       __uint_as_float(h1 & 0xffff0000u))),
+                                 e0, e1);
+                        const uint32_t h2 = pack_bf16x2(e0, e1);
                         sts_u16(a0, (uint16_t)h1);
                         sts_u16(a0 + RP * 128, (uint16_t)h2);
                         if (W > 1) {
@@ -1082,8 +1112,10 @@ cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, PagedParam
     if (p.R == 1) return launch_attend<D, F8, 1, 1>(tk, tv, p, stream);
     if (p.R <= 4) return launch_attend<D, F8, 1, 4>(tk, tv, p, stream);
     if (p.R <= 8) return launch_attend<D, F8, 1, 8>(tk, tv, p, stream);
+    // Two groups of 8 rows rather than one of 16 (e4m3 at d = 128, B8, four tokens, 8K
+    // to 16K keys: 41.2 and 50.0 us), two of 16 rather than four of 8 (53.2 and 54.5).
     if (p.R <= 16) return launch_attend<D, F8, 2, 8>(tk, tv, p, stream);
-    return launch_attend<D, F8, 4, 8>(tk, tv, p, stream);
+    return launch_attend<D, F8, 2, 16>(tk, tv, p, stream);
 }
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }

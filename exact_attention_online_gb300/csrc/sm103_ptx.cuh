@@ -449,17 +449,25 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
         FA_I32(r)
         : "memory");
 }
-// W columns (1, 4 or 8), to be used after tmem_ld_done, which waits for this
+// W columns (1, 4, 8 or 16), to be used after tmem_ld_done, which waits for this
 // thread's TMEM loads and names the result of one.
 template <int W>
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[W]) {
-    static_assert(W == 1 || W == 4 || W == 8, "tcgen05.ld shapes");
+    static_assert(W == 1 || W == 4 || W == 8 || W == 16, "tcgen05.ld shapes");
     if constexpr (W == 1)
         asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r[0]) : "r"(taddr));
     else if constexpr (W == 4)
         asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                      : "r"(taddr));
+    else if constexpr (W == 16)
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+            "%11, %12, %13, %14, %15}, [%16];"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+              "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+              "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+            : "r"(taddr));
     else
         asm volatile(
             "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -474,6 +482,13 @@ __device__ __forceinline__ void tmem_ld_done(uint32_t (&a)[W]) {
     else if constexpr (W == 4)
         asm volatile("tcgen05.wait::ld.sync.aligned;"
                      : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3])
+                     :
+                     : "memory");
+    else if constexpr (W == 16)
+        asm volatile("tcgen05.wait::ld.sync.aligned;"
+                     : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]),
+                       "+r"(a[6]), "+r"(a[7]), "+r"(a[8]), "+r"(a[9]), "+r"(a[10]), "+r"(a[11]),
+                       "+r"(a[12]), "+r"(a[13]), "+r"(a[14]), "+r"(a[15])
                      :
                      : "memory");
     else
@@ -492,6 +507,14 @@ __device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[W]) 
         asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr),
                      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
                      : "memory");
+    else if constexpr (W == 16)
+        asm volatile(
+            "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+            "%11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+            "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+            "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+            "r"(r[15])
+            : "memory");
     else
         asm volatile(
             "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
