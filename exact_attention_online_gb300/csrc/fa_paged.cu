@@ -11,8 +11,8 @@
 // shared memory (N is 16 to 64 columns), a softmax thread owns one key and up to
 // sixteen rows' scores, nothing is computed for absent query rows past the next 1,
 // 4, 8, 16 or 32, and no thread needs another's score: the running maximum m of a
-// row moves only when some key passes it by 2^kSlack (a vote of the four warps),
-// the row sums stay one partial per thread until the end, and the rescale of O^T
+// row (the reference) moves only when some key passes it by 2^kSlack (a vote of the
+// four warps) or, in an e4m3 cache, at every 32nd tile, the row sums stay one partial per thread until the end, and the rescale of O^T
 // touches few columns.  Neighbouring rows go through the fp32 units in pairs.
 //
 // e4m3 pages are multiplied as they are.  A bf16 query row, times the power of
@@ -21,9 +21,13 @@
 // B holds the rows' first terms and, RP columns on, their second terms, and
 // the two scores are added in fp32.  K's scale is the softmax thread's own
 // (one thread, one key).  V's scale vs goes into P: w = 2^(x - m) vs kPScale with
-// m the running maximum of x + log2 vs, so that w <= 448, as two e4m3 terms
-// again; a row of zeros has scale 0 and weighs nothing.  No pass converts the
-// pages, and shared memory sees each of their bytes twice.
+// m the reference of x + log2 vs, so that w <= 448, as two e4m3 terms again, the
+// second times 28 and with columns of O^T of its own.  These end at 2^-20.6 of the
+// reference while the row sum counts every weight, so one early key must not set the
+// reference of a long tail: every 32 tiles it is taken from the tile at hand, and O
+// and the row sum, which are fp32, are scaled up to it.  A row of zeros has scale 0
+// and weighs nothing.  No pass converts the pages, and shared memory sees each of
+// their bytes twice.
 //
 // Work: the tiles of all (sequence, kv head) pairs, in order, are one list that
 // the CTAs share evenly (List), found on the device from the lengths, so that
@@ -96,7 +100,8 @@ struct Cfg {
     // tile, and with up to 8 rows two CTAs fit, so that one's softmax and
     // epilogue hide behind the other's.
     static constexpr int kCtas = kRowBytes <= 128 && RP == 8 ? 2 : 1;
-    static constexpr int kRing = (kCtas == 2 ? 113 : 227) * 1024 - 1024 - 2048 - 2 * kQBytes -
+    static constexpr int kStatic = F8 ? 2304 : 2048;   // shared memory beside the tiles
+    static constexpr int kRing = (kCtas == 2 ? 113 : 227) * 1024 - 1024 - kStatic - 2 * kQBytes -
                                  kPBufs * kPBytes;
     static constexpr int kStages = kRing / (2 * kTileBytes + kScaleBytes);
     // Tiles of K, and of V, in flight at once: about 112 KB an SM.  More of them
@@ -115,10 +120,23 @@ struct Cfg {
     // 2000 5.9 and 6.8; 4000 keys (four tiles a CTA) 7.9 and 7.6 in bf16 at d = 128,
     // 7.1 and 8.4 in e4m3, 7.0 and 7.6 at d = 64; 8000 keys 9.2 and 7.8 at d = 64.
     static constexpr int kClusterTiles = kRowBytes <= 128 ? 4 : 2;
-    // How far a score may pass the running maximum before O is rescaled (log2):
-    // bf16 P keeps its precision at any magnitude; e4m3 P ends at 448.
+    // How far a score may pass the reference before O is rescaled (log2): bf16 P
+    // keeps its precision at any magnitude; e4m3 P ends at 448.
     static constexpr float kSlack = F8 ? 3.0f : 8.0f;
     static constexpr float kPScale = F8 ? 56.0f : 1.0f;            // 2^kSlack * kPScale = 448
+    // e4m3's second term of P is stored times this, and its columns of O count that
+    // much less: what a first term of up to 448 leaves is at most 16.
+    static constexpr float kTerm2 = F8 ? kE4m3Term2 : 1.0f;
+    // Every kRefTiles tiles e4m3's reference is taken anew, and may fall, but not by
+    // more than kRefDrop (log2) below the largest so far.  A term's last half step is
+    // 2^-10 / 28, so weights end at 2^-10 / 28 / 56 = 2^-20.6 of the reference: of the
+    // 4096 keys that share one, at most 2^-8.6 of the largest product is lost, however
+    // long the cache.  (With one reference for a whole pair, 4096 keys a stretch turn
+    // into n.)  Four tokens a sequence, B8, 8 kv heads, 8K to 16K keys, without this,
+    // every 32 and every 16 tiles: 16 rows of d = 128 40.8, 41.1 and 41.3 us, 32 rows
+    // 52.6, 54.5 and 55.7; 16 rows of d = 64 36.0, 37.3 and 38.0.
+    static constexpr int kRefTiles = F8 ? 32 : 0;
+    static constexpr float kRefDrop = 24.0f;
 };
 
 __device__ __forceinline__ int clamped_len(const PagedParams& p, int b) {
@@ -343,6 +361,9 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
     __shared__ float4 row_max[RP], row_sum[RP];   // a value a softmax warp
     __shared__ float q_scale[2][RP];              // e4m3: score of one code product, log2 units
     __shared__ int row_query[RP];                 // r % Nq
+    // e4m3: a row's largest reference before the last time that it could fall (by
+    // turns: one is read while the other is written)
+    __shared__ float row_top[2][RP];
     __shared__ float cta_lse[RP];                 // in clusters: of this CTA's part, log2
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_sh;
@@ -733,7 +754,7 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                         if (key >= end) x[r] = -CUDART_INF_F;
                     }
                 }
-                // Does any score pass the running maximum by 2^kSlack?
+                // Does any score pass the reference by 2^kSlack, or may that fall?
                 float top = -CUDART_INF_F;
 #pragma unroll
                 for (int r = 0; r < W; r += 2) {
@@ -741,7 +762,9 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                     f2_split(f2_sub(pair(x, r), pair(m, r)), lo, hi);
                     top = W > 1 ? fmax3(top, lo, hi) : lo;
                 }
-                if (named_bar_or(bar_id, 128, top > C::kSlack - lv)) {
+                constexpr int kTurn = C::kRefTiles > 0 ? C::kRefTiles : 1;
+                const bool fall = C::kRefTiles > 0 && t > 0 && t % kTurn == 0;
+                if (named_bar_or(bar_id, 128, fall || top > C::kSlack - lv)) {
 #pragma unroll
                     for (int r = 0; r < W; ++r) {
                         const int y = __reduce_max_sync(0xffffffffu, ordered(x[r] + lv));
@@ -752,7 +775,14 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
                     for (int r = 0; r < W; ++r) {
                         const float4 w4 = row_max[r0 + r];
-                        const float mx = fmaxf(fmax3(w4.x, w4.y, w4.z), fmaxf(w4.w, m[r]));
+                        float least = m[r];
+                        if (fall) {
+                            const int turn = t / kTurn;
+                            if (turn > 1) least = fmaxf(least, row_top[turn & 1][r0 + r]);
+                            if (j == r) row_top[(turn + 1) & 1][r0 + r] = least;
+                            least -= C::kRefDrop;
+                        }
+                        const float mx = fmaxf(fmax3(w4.x, w4.y, w4.z), fmaxf(w4.w, least));
                         alpha[r] = ex2(m[r] - mx);
                         m[r] = mx;
                         l[r] *= alpha[r];
@@ -874,8 +904,7 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                 tmem_ld_done(ob);
 #pragma unroll
                 for (int r = 0; r < W; ++r) {
-                    float y = __uint_as_float(oa[r]);
-                    y += __uint_as_float(ob[r]);
+                    float y = fmaf(__uint_as_float(ob[r]), 1.0f / C::kTerm2, __uint_as_float(oa[r]));
                     y = inv[r] < 0.0f ? 0.0f : y * inv[r];
                     if (r0 + r < p.R) {
                         if (CLUSTER)              // P's buffers have been read
@@ -1072,7 +1101,7 @@ template <int D, bool F8, int G, int W>
 cudaError_t launch_attend(const CUtensorMap& tk, const CUtensorMap& tv, PagedParams& p,
                           cudaStream_t stream) {
     using C = Cfg<D, F8, G, W>;
-    static_assert(C::kSmem + 2048 <= 227 * 1024, "shared memory of one CTA");
+    static_assert(C::kSmem + C::kStatic <= 227 * 1024, "shared memory of one CTA");
     const int longest = ((p.max_pages << p.ps_shift) + kTile - 1) / kTile;    // tiles of a pair
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);

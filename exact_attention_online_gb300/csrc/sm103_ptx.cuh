@@ -597,16 +597,20 @@ __device__ __forceinline__ void unpack_e4m3x4(uint32_t w, float (&x)[4]) {
     unpack_f16x2(hi, x[2], x[3]);
 }
 
-// Two fp16 values of magnitude up to 448 as the sums of two e4m3 numbers each:
-// `hi` the nearest codes, `lo` the nearest of what is left (in bits 0-15).
+// Two fp16 values of magnitude up to 448 as e4m3 numbers hi + lo / kE4m3Term2 each:
+// `hi` the nearest codes, `lo` the nearest of kE4m3Term2 times what is left (in bits
+// 0-15).  That is at most 16 (half a step at 448), so 28 times it still is a number of
+// the format, and reaches 28 times further down.
+constexpr float kE4m3Term2 = 28.0f;
 __device__ __forceinline__ void split_e4m3x2(uint32_t w, uint32_t& hi, uint32_t& lo) {
     asm("{.reg .b16 h, l;\n\t.reg .b32 v, r;\n\t"
         "cvt.rn.satfinite.e4m3x2.f16x2 h, %2;\n\t"
         "cvt.rn.f16x2.e4m3x2 v, h;\n\t"
         "sub.rn.f16x2 r, %2, v;\n\t"
+        "mul.rn.f16x2 r, r, %3;\n\t"
         "cvt.rn.satfinite.e4m3x2.f16x2 l, r;\n\t"
         "cvt.u32.u16 %0, h;\n\t"
-        "cvt.u32.u16 %1, l;}" : "=r"(hi), "=r"(lo) : "r"(w));
+        "cvt.u32.u16 %1, l;}" : "=r"(hi), "=r"(lo) : "r"(w), "r"(0x4f004f00u));
 }
 
 // Paired fp32 arithmetic (one instruction for two lanes of a 64-bit register
