@@ -16,9 +16,10 @@
 // touches few columns.  Neighbouring rows go through the fp32 units in pairs.
 //
 // e4m3 pages are multiplied as they are.  A bf16 query row, times the power of
-// two that brings its largest entry into [2^7, 2^8), is the sum of two e4m3
-// numbers (8 significant bits = 4 + 4, exact down to e4m3's smallest step, 2^-9), so
-// B holds the rows' first terms and, RP columns on, their second terms, and
+// two that brings its largest entry into [2^7, 2^8), is a + b / 32 with e4m3
+// numbers a and b (8 significant bits = 4 + 4; what a leaves is at most 8), exact
+// where an entry is at least 2^-14 of the largest and off by at most 2^-22 of that
+// below.  B holds the rows' first terms and, RP columns on, their second terms, and
 // the two scores are added in fp32.  K's scale is the softmax thread's own
 // (one thread, one key).  V's scale vs goes into P: w = 2^(x - m) vs kPScale with
 // m the reference of x + log2 vs, so that w <= 448, as two e4m3 terms again, the
@@ -124,6 +125,8 @@ struct Cfg {
     // keeps its precision at any magnitude; e4m3 P ends at 448.
     static constexpr float kSlack = F8 ? 3.0f : 8.0f;
     static constexpr float kPScale = F8 ? 56.0f : 1.0f;            // 2^kSlack * kPScale = 448
+    // The second term of an e4m3 query is stored times this.
+    static constexpr float kQTerm2 = 32.0f;
     // e4m3's second term of P is stored times this, and its columns of O count that
     // much less: what a first term of up to 448 leaves is at most 16.
     static constexpr float kTerm2 = F8 ? kE4m3Term2 : 1.0f;
@@ -615,9 +618,12 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                         c1[e / 4] = pack_e4m3x4(x[e] * up, x[e + 1] * up, x[e + 2] * up,
                                                 x[e + 3] * up);
                         unpack_e4m3x4(c1[e / 4], v);
-                        c2[e / 4] = pack_e4m3x4(fmaf(x[e], up, -v[0]), fmaf(x[e + 1], up, -v[1]),
-                                                fmaf(x[e + 2], up, -v[2]),
-                                                fmaf(x[e + 3], up, -v[3]));
+                        // (x up - v) kQTerm2; all of it exact
+                        const float up2 = up * C::kQTerm2;
+                        c2[e / 4] = pack_e4m3x4(fmaf(x[e], up2, -C::kQTerm2 * v[0]),
+                                                fmaf(x[e + 1], up2, -C::kQTerm2 * v[1]),
+                                                fmaf(x[e + 2], up2, -C::kQTerm2 * v[2]),
+                                                fmaf(x[e + 3], up2, -C::kQTerm2 * v[3]));
                     }
                     if (r < p.R) {
                         if constexpr (E == 16) {       // one 16-byte unit, swizzled by r & 7
@@ -743,7 +749,8 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                 for (int r = 0; r < W; r += 2) {
                     const uint64_t a = pair(sa, r);
                     if constexpr (F8)
-                        put(x, r, f2_mul(f2_add(a, pair(sb, r)), f2_mul(pair(qc, r), f2(ks, ks))));
+                        put(x, r, f2_mul(f2_fma(pair(sb, r), f2(1.0f / C::kQTerm2, 1.0f / C::kQTerm2), a),
+                                         f2_mul(pair(qc, r), f2(ks, ks))));
                     else
                         put(x, r, f2_mul(a, f2(p.scale_log2, p.scale_log2)));
                 }

@@ -514,7 +514,8 @@ FA_API fa_status fa_kv_gather_varlen(const void* k_pages, const void* v_pages,
  * pages: P enters as the sum of two bf16 terms (16 significant bits).  e4m3
  * pages: q and P enter as the sum of two e4m3 terms (8 significant bits, those
  * of bf16), so that the codes are multiplied as they are and only the scales
- * are applied in fp32.  A weight times its V scale keeps 8 bits down to 2^-12
+ * are applied in fp32.  A query's entry is exact down to 2^-14 of the row's
+ * largest and off by at most 2^-22 of that below.  A weight times its V scale keeps 8 bits down to 2^-12
  * of the largest such product among up to 4096 neighbouring keys, and is off
  * by at most 2^-20.6 of that below: all of them by 2^-8.6, whatever the
  * cache's length, while LSE counts every weight in full.

@@ -102,3 +102,34 @@ def test_leading_key_over_a_long_tail(d, rows, B, place, values):
                                               (off / ref[:m * R].abs()).max().item())
         dl = (lse[first:first + m].reshape(-1).double() - ref_lse[:m * R]).abs()
         assert (dl <= score + 2.0 ** -19).all(), dl.max().item()
+
+
+@pytest.mark.parametrize("rows", [(1, 1), (4, 1), (8, 1), (8, 2), (8, 4)], ids=lambda r: f"{r[0]}x{r[1]}")
+@pytest.mark.parametrize("d", [64, 128])
+def test_query_with_a_large_entry(d, rows):
+    """One entry of each query is 2^11, where every key is zero; the others, N(0, 1), make the
+    scores.  With one key LSE is its score, off by fp32's roundings, 2 (d + 16) of 2^-24 of the
+    absolute sum, the logarithm (2^-19) and the query's second term: 2^-22 of the largest entry
+    for each entry below 2^-14 of it."""
+    H, Nq = rows
+    B, scale, big = 24, 0.125, 2.0 ** 11
+    gen = torch.Generator(device="cuda").manual_seed(d + H + Nq)
+    k, v = (torch.randn((B, 1, 1, d), generator=gen, device="cuda").bfloat16() for _ in range(2))
+    k[..., 0] = 0
+    kp, vp = (torch.zeros((B, 1, 16, d), device="cuda").to(torch.float8_e4m3fn) for _ in range(2))
+    sc = torch.zeros((B, 1, 2, 16), device="cuda")
+    table, zero, one = torch.arange(B, dtype=torch.int32, device="cuda")[:, None], i32([0] * B), i32([1] * B)
+    fa.fa_kv_append(k, v, kp, vp, table, zero, one, kv_scales=sc)
+    q = torch.randn((B, H, Nq, d), generator=gen, device="cuda").bfloat16()
+    q[..., 0] = big
+    _, lse = fa.attention_decode_paged(q, kp, vp, table, one, False, scale, kv_scales=sc)
+    torch.cuda.synchronize()
+    assert fa.fa_device_status() == fa.FA_OK
+    kd = (kp[:, :, 0].double() * sc[:, :, 0, 0].double()[..., None])[:, :, None]     # [B, 1, 1, d]
+    q = q.double()
+    ref, absum = scale * (q * kd).sum(-1), scale * (q * kd).abs().sum(-1)
+    small = q.abs() < 2.0 ** -14 * big
+    bound = 2 * (d + 16) * 2.0 ** -24 * absum + 2.0 ** -19 + \
+        scale * 2.0 ** -22 * big * (small * kd.abs()).sum(-1)
+    off = (lse.double() - ref).abs()
+    assert (off <= bound).all(), ((off / bound).max().item(), off.max().item())
