@@ -690,7 +690,7 @@ static fa_status check_paged_shape(int B, int Hkv, long long n_pages, int page_s
         return FA_ERR_UNSUPPORTED;
     const long long keys = (long long)max_pages * page_size;
     if (keys >= (1LL << 30) || n_pages * Hkv >= (1LL << 31) ||
-        (long long)B * Hkv >= (1LL << 30) / (keys / 128 + 2))
+        (long long)B * Hkv > (1LL << 30) / (keys / 128 + 2))
         return FA_ERR_UNSUPPORTED;
     return FA_OK;
 }
