@@ -420,6 +420,38 @@ def fa_watchdog_selftest(timeout_ns: int, stream=None) -> None:
 
 # Convenience wrappers that allocate outputs with PyTorch (the library itself
 # never allocates).
+class _Outputs:
+    """Context in which a wrapper allocates for a call on `stream`: memory of that stream, so
+    that nothing the current stream still has to do can touch it, and a workspace that the
+    wrapper drops is handed out again behind the call.  What it returns goes through `out`:
+    the current stream, where the caller may use it, is told to the allocator too."""
+
+    def __init__(self, stream):
+        import torch
+        self.side = self.ctx = None
+        if stream is not None and _stream(stream) != _stream(None):
+            self.side = stream if isinstance(stream, torch.cuda.Stream) else \
+                torch.cuda.ExternalStream(_stream(stream))
+
+    def __enter__(self):
+        import torch
+        if self.side is not None:
+            self.ctx = torch.cuda.stream(self.side)
+            self.ctx.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+    def out(self, *tensors):
+        import torch
+        if self.side is not None:
+            for t in tensors:
+                t.record_stream(torch.cuda.current_stream())
+        return tensors
+
+
 def fa_fp8_buffer_size(B: int, H: int, Hkv: int, N: int, d: int) -> int:
     return int(lib().fa_fp8_buffer_size(B, H, Hkv, N, d))
 
@@ -454,12 +486,13 @@ def attention_fp8(q, k, v, causal: bool = False, scale: float | None = None, str
     n = fa_fp8_buffer_size(B, H, Hkv, N, d)
     if n == 0:
         raise FAError(FA_ERR_UNSUPPORTED, "fa_fp8_buffer_size")
-    buf = torch.empty(n, dtype=torch.uint8, device=q.device)
-    o = torch.empty_like(q)
-    lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
+    with _Outputs(stream) as on:
+        buf = torch.empty(n, dtype=torch.uint8, device=q.device)
+        o = torch.empty_like(q)
+        lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
     fa_fp8_quantize(v, buf, H, stream)
     fa_fwd_fp8(q, k, buf, o, lse, causal, scale, stream)
-    return o, lse, buf
+    return on.out(o, lse, buf)
 
 
 def fa_fwd_decode_workspace_size(B: int, H: int, Hkv: int, Nq: int, Nk: int, d: int) -> int:
@@ -491,11 +524,12 @@ def attention_decode(q, k, v, causal: bool = True, scale: float | None = None, s
     n = fa_fwd_decode_workspace_size(B, H, Hkv, Nq, Nk, d)
     if n == 0:
         raise FAError(FA_ERR_UNSUPPORTED, "fa_fwd_decode_workspace_size")
-    work = torch.empty(n, dtype=torch.uint8, device=q.device)
-    o = torch.empty_like(q)
-    lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+    with _Outputs(stream) as on:
+        work = torch.empty(n, dtype=torch.uint8, device=q.device)
+        o = torch.empty_like(q)
+        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
     fa_fwd_decode(q, k, v, o, lse, work, causal, scale, stream)
-    return o, lse
+    return on.out(o, lse)
 
 
 # ------------------------------------------------------------- paged cache
@@ -653,22 +687,19 @@ def attention_decode_paged(q, k_pages, v_pages, block_table, seqlens, causal: bo
     B, H, Nq, d = _dims_of(q, "q")
     pool, _, _ = _pool(k_pages, block_table, kv_scales)
     scale = d ** -0.5 if scale is None else scale
-    o = torch.empty_like(q, memory_format=torch.contiguous_format)
-    lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
-    if workspace is None:
-        n = fa_fwd_decode_paged_workspace_size(B, H, pool[1], Nq, d)
-        if n == 0:
-            raise FAError(FA_ERR_UNSUPPORTED, "fa_fwd_decode_paged_workspace_size")
-        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    with _Outputs(stream) as on:
+        o = torch.empty_like(q, memory_format=torch.contiguous_format)
+        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+        if workspace is None:
+            n = fa_fwd_decode_paged_workspace_size(B, H, pool[1], Nq, d)
+            if n == 0:
+                raise FAError(FA_ERR_UNSUPPORTED, "fa_fwd_decode_paged_workspace_size")
+            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
     fa_fwd_decode_paged(q, k_pages, v_pages, o, lse, block_table, seqlens, workspace, causal,
                         scale, kv_scales, stream)
-    if stream is not None and _stream(stream) != _stream(None):
-        # the allocator must not hand these out again before the call's stream has used them
-        if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream))
-        for t in (o, lse, workspace):
-            t.record_stream(stream)
-    return o, lse
+    if on.side is not None:
+        workspace.record_stream(on.side)       # the caller's, if it is given
+    return on.out(o, lse)
 
 
 def attention(q, k, v, causal: bool = False, scale: float | None = None, stream=None,
@@ -678,14 +709,12 @@ def attention(q, k, v, causal: bool = False, scale: float | None = None, stream=
     import torch
     d = q.shape[-1]
     scale = d ** -0.5 if scale is None else scale
-    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
-    if precise:
-        o = torch.empty(q.shape, dtype=torch.float32, device=q.device)
-        fa_fwd_precise(q, k, v, o, lse, causal, scale, stream)
-    else:
-        o = torch.empty_like(q)
-        fa_fwd(q, k, v, o, lse, causal, scale, stream)
-    return o, lse
+    with _Outputs(stream) as on:
+        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+        o = torch.empty(q.shape, dtype=torch.float32, device=q.device) if precise else \
+            torch.empty_like(q)
+    (fa_fwd_precise if precise else fa_fwd)(q, k, v, o, lse, causal, scale, stream)
+    return on.out(o, lse)
 
 
 def attention_window(q, k, v, window: int, scale: float | None = None, stream=None):
@@ -693,10 +722,11 @@ def attention_window(q, k, v, window: int, scale: float | None = None, stream=No
     returns (o, lse)."""
     import torch
     scale = q.shape[-1] ** -0.5 if scale is None else scale
-    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
-    o = torch.empty_like(q)
+    with _Outputs(stream) as on:
+        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+        o = torch.empty_like(q)
     fa_fwd_window(q, k, v, o, lse, window, scale, stream)
-    return o, lse
+    return on.out(o, lse)
 
 
 def attention_window_backward(q, k, v, o, lse, dout, window: int, scale: float | None = None,
@@ -705,12 +735,13 @@ def attention_window_backward(q, k, v, o, lse, dout, window: int, scale: float |
     import torch
     B, H, Hkv, N, d = _dims(q, k)
     scale = d ** -0.5 if scale is None else scale
-    if workspace is None:
-        workspace = torch.empty(fa_bwd_workspace_size(B, H, Hkv, N, d), dtype=torch.uint8,
-                                device=q.device)
-    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    with _Outputs(stream) as on:
+        if workspace is None:
+            workspace = torch.empty(fa_bwd_workspace_size(B, H, Hkv, N, d), dtype=torch.uint8,
+                                    device=q.device)
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     fa_bwd_window(q, k, v, o, dout, lse, dq, dk, dv, workspace, window, scale, stream)
-    return dq, dk, dv
+    return on.out(dq, dk, dv)
 
 
 def attention_varlen(q, k, v, cu_seqlens, max_seqlen: int, causal: bool = False,
@@ -718,10 +749,11 @@ def attention_varlen(q, k, v, cu_seqlens, max_seqlen: int, causal: bool = False,
     """Packed variable-length sequences; returns (o [H, total, d], lse [H, total])."""
     import torch
     scale = q.shape[-1] ** -0.5 if scale is None else scale
-    o = torch.empty_like(q)
-    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    with _Outputs(stream) as on:
+        o = torch.empty_like(q)
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
     fa_fwd_varlen(q, k, v, o, lse, cu_seqlens, max_seqlen, causal, scale, stream)
-    return o, lse
+    return on.out(o, lse)
 
 
 def attention_varlen_backward(q, k, v, o, lse, dout, cu_seqlens, max_seqlen: int,
@@ -731,13 +763,14 @@ def attention_varlen_backward(q, k, v, o, lse, dout, cu_seqlens, max_seqlen: int
     import torch
     B, H, Hkv, total, d = _varlen_dims(q, k, cu_seqlens)
     scale = d ** -0.5 if scale is None else scale
-    if workspace is None:
-        workspace = torch.empty(fa_bwd_varlen_workspace_size(B, H, Hkv, max_seqlen, d),
-                                dtype=torch.uint8, device=q.device)
-    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    with _Outputs(stream) as on:
+        if workspace is None:
+            workspace = torch.empty(fa_bwd_varlen_workspace_size(B, H, Hkv, max_seqlen, d),
+                                    dtype=torch.uint8, device=q.device)
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     fa_bwd_varlen(q, k, v, o, dout, lse, dq, dk, dv, workspace, cu_seqlens, max_seqlen, causal,
                   scale, stream)
-    return dq, dk, dv
+    return on.out(dq, dk, dv)
 
 
 def attention_backward(q, k, v, o, lse, dout, causal: bool = False, scale: float | None = None,
@@ -746,12 +779,13 @@ def attention_backward(q, k, v, o, lse, dout, causal: bool = False, scale: float
     import torch
     B, H, Hkv, N, d = _dims(q, k)
     scale = d ** -0.5 if scale is None else scale
-    if workspace is None:
-        workspace = torch.empty(fa_bwd_workspace_size(B, H, Hkv, N, d), dtype=torch.uint8,
-                                device=q.device)
-    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    with _Outputs(stream) as on:
+        if workspace is None:
+            workspace = torch.empty(fa_bwd_workspace_size(B, H, Hkv, N, d), dtype=torch.uint8,
+                                    device=q.device)
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     if o.dtype == torch.float32:
         fa_bwd_precise(q, k, v, o, dout, lse, dq, dk, dv, workspace, causal, scale, stream)
     else:
         fa_bwd(q, k, v, o, dout, lse, dq, dk, dv, workspace, causal, scale, stream)
-    return dq, dk, dv
+    return on.out(dq, dk, dv)
