@@ -59,11 +59,15 @@ _cuda = None   # (current device, raw current stream of a device), once CUDA is 
 
 
 def _runtime():
+    """torch's short forms of the two where it has them, as a small call's time is the host's; they
+    are not part of its public interface, which answers else."""
     global _cuda
     if _cuda is None:
         import torch
         torch.cuda.current_device()   # raises without a CUDA runtime
-        _cuda = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+        _cuda = (getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device,
+                 getattr(torch._C, "_cuda_getCurrentRawStream", None) or
+                 (lambda device: torch.cuda.current_stream(device).cuda_stream))
     return _cuda
 
 
