@@ -27,10 +27,20 @@ namespace fa {
 namespace {
 
 constexpr int kThreads = 256;
-// Up to here a warp takes one pass of rows: the rows spread over more SMs and
-// none waits for a second batch (8192 rows of d = 128: append to e4m3 4.6 us with
-// four passes, 3.3 with one; from 65536 rows on the longer form is ahead).
-constexpr unsigned kFewRows = 16384;
+// Up to here a warp takes one pass of rows (the short form): they spread over more
+// SMs, and none waits for a second batch.  Both forms, short and long, us in a graph of
+// calls on inputs larger than L2 (rows of K, and of V; pages of 16):
+//                          8192         16384        32768        49152        65536
+//   e4m3 append   d = 128  4.55  6.43   5.49  6.85   7.85  8.26   10.3  10.0   12.5  11.7
+//                 d = 64   3.02  4.74   4.54  6.34   5.44  6.76   6.95  7.81   7.92  8.18
+//   bf16 append   d = 128  4.30  4.33   5.78  5.85   8.05  8.00   10.8  10.6   13.1  13.1
+//                 d = 64   3.64  3.90   4.62  4.71   5.70  5.82   7.20  7.07   8.08  7.97
+//   bf16 gather   d = 128  4.62  4.75   5.78  5.83   8.19  8.07   10.9  10.5   13.5  13.2
+//                 d = 64   3.55  3.80   4.62  4.77   5.67  5.85   7.27  7.13   8.20  7.99
+//   e4m3 gather   d = 128  4.37  4.47   5.31  5.27   7.47  6.97   9.79  8.56   12.0  10.3
+//                 d = 64   2.95  3.30   4.33  4.54   5.25  5.30   6.65  6.24   7.56  7.08
+template <bool F8, bool APPEND>
+constexpr unsigned kFewRows = F8 && APPEND ? 49152 : 16384;
 
 // n / d for 31-bit n: q = floor(n * floor(2^32 / d) / 2^32) is the quotient or
 // one less.
@@ -126,7 +136,8 @@ __device__ __forceinline__ uint4 decode8(const uint2& c, float scale) {
 }
 
 // Passes whose loads are in flight together, and rounds of them: a warp moves
-// kRounds * kBatch * 256 / D rows, 32 in the long form.
+// kRounds * kBatch * 256 / D rows of K and of V (the long form: 8 rows of d = 128 and 16
+// of d = 64, twice as many where it quantises).
 template <int D, bool F8, bool APPEND, int kBatch, int kRounds>
 __global__ void __launch_bounds__(kThreads)
 fa_kv_move_kernel(const __grid_constant__ MoveParams p) {
@@ -245,7 +256,7 @@ cudaError_t launch(const MoveParams& p, cudaStream_t stream) {
 // four).
 template <int D, bool F8, bool APPEND>
 cudaError_t launch_rows(const MoveParams& p, cudaStream_t stream) {
-    if (p.rows <= kFewRows) return launch<D, F8, APPEND, 1, 1>(p, stream);
+    if (p.rows <= kFewRows<F8, APPEND>) return launch<D, F8, APPEND, 1, 1>(p, stream);
     return launch<D, F8, APPEND, 4, F8 && APPEND ? 2 : 1>(p, stream);
 }
 
