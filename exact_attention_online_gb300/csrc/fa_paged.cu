@@ -946,6 +946,7 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
             for (int s = 0; s < kMaxCluster; ++s) {
                 ls[s] = -CUDART_INF_F;
+                y[s] = 0.0f;
                 if (s < p.ctas) {
                     ls[s] = ld_cluster_f32(smem_u32(cta_lse + r), s);
                     y[s] = ld_cluster_f32(sP + (r * D + j) * 4, s);
@@ -959,7 +960,7 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
             for (int s = 0; s < kMaxCluster; ++s) {
                 const float w = ex2(ls[s] - mx);
                 sum += w;
-                if (w != 0.0f) acc = fmaf(w, y[s], acc);   // a CTA without tiles left no O
+                acc = fmaf(w, y[s], acc);         // (s >= p.ctas, or no tiles: w and y are 0)
             }
             const long long row = (long long)c * p.R + r;
             p.o[row * D + j] = __float2bfloat16_rn(sum == 0.0f ? 0.0f : __fdividef(acc, sum));

@@ -506,8 +506,10 @@ FA_API fa_status fa_kv_gather_varlen(const void* k_pages, const void* v_pages,
  * every position below seqlens[b].  A row that sees nothing (an empty slot,
  * seqlens[b] = 0; the first rows when seqlens[b] < Nq) gets O = 0 and LSE =
  * -infinity.  Cache rows at positions >= seqlens[b] may hold anything; a NaN
- * or an infinity at a position below it reaches every one of the sequence's Nq
- * rows of that kv head, as a weight of zero does not silence it in P V.
+ * or an infinity in V at a position below it reaches every row that gives that
+ * position weight (O is then NaN or infinite) and may reach the sequence's
+ * other rows of that kv head, as a weight of zero does not always silence it
+ * in P V; a NaN in K reaches the rows that see it.  No other row is affected.
  * (H / Hkv) * Nq <= 32 (FA_ERR_UNSUPPORTED otherwise).
  *
  * The scores and P V run on the tensor core with fp32 accumulation.  bf16
