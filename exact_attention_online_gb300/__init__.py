@@ -112,6 +112,18 @@ def _ptr(t, name, dtype, shape):
     return t.data_ptr()
 
 
+def _c_int(x, name) -> int:
+    """x for a C int argument, which would take the lower 32 bits of a larger one."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} = {x} is out of range")
+    return x
+
+
+def _bytes(size_of, *sizes) -> int:
+    return int(size_of(*(_c_int(x, "a size") for x in sizes)))
+
+
 def _bf16(t, name, shape=None):
     import torch
     return _ptr(t, name, torch.bfloat16, shape)
@@ -157,9 +169,10 @@ def fa_fwd_precise(q, k, v, o, lse, causal: bool, scale: float, stream=None) -> 
 def fa_fwd_window(q, k, v, o, lse, window: int, scale: float, stream=None) -> None:
     """Causal sliding window: query i attends to keys i - window < j <= i."""
     B, H, Hkv, N, d = _dims(q, k)
+    window = _c_int(window, "window")
     qs, ks, ls = _shapes(B, H, Hkv, N, d)
     _check(lib().fa_fwd_window(_bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v", ks), _bf16(o, "o", qs),
-                               _f32(lse, "lse", ls), B, H, Hkv, N, d, int(window), float(scale),
+                               _f32(lse, "lse", ls), B, H, Hkv, N, d, window, float(scale),
                                _stream(stream)), "fa_fwd_window")
 
 
@@ -184,33 +197,35 @@ def fa_fwd_varlen(q, k, v, o, lse, cu_seqlens, max_seqlen: int, causal: bool, sc
     """Packed sequences: q, o [H, total, d], k, v [Hkv, total, d], lse [H, total],
     cu_seqlens int32 [B + 1] on the device."""
     B, H, Hkv, total, d = _varlen_dims(q, k, cu_seqlens)
+    max_seqlen = _c_int(max_seqlen, "max_seqlen")
     qs, ks = (H, total, d), (Hkv, total, d)
     _check(lib().fa_fwd_varlen(_bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v", ks), _bf16(o, "o", qs),
                                _f32(lse, "lse", (H, total)), _i32(cu_seqlens, "cu_seqlens"), B,
-                               int(max_seqlen), total, H, Hkv, d, int(bool(causal)),
+                               max_seqlen, total, H, Hkv, d, int(bool(causal)),
                                float(scale), _stream(stream)), "fa_fwd_varlen")
 
 
 def fa_bwd_varlen_workspace_size(B: int, H: int, Hkv: int, max_seqlen: int, d: int) -> int:
-    return int(lib().fa_bwd_varlen_workspace_size(B, H, Hkv, max_seqlen, d))
+    return _bytes(lib().fa_bwd_varlen_workspace_size, B, H, Hkv, max_seqlen, d)
 
 
 def fa_bwd_varlen(q, k, v, o, dout, lse, dq, dk, dv, workspace, cu_seqlens, max_seqlen: int,
                   causal: bool, scale: float, stream=None) -> None:
     B, H, Hkv, total, d = _varlen_dims(q, k, cu_seqlens)
+    max_seqlen = _c_int(max_seqlen, "max_seqlen")
     qs, ks = (H, total, d), (Hkv, total, d)
     wp, wb = _ws(workspace)
     _check(lib().fa_bwd_varlen(_bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v", ks), _bf16(o, "o", qs),
                                _bf16(dout, "dout", qs), _f32(lse, "lse", (H, total)),
                                _bf16(dq, "dq", qs), _bf16(dk, "dk", ks), _bf16(dv, "dv", ks),
                                wp, wb,
-                               _i32(cu_seqlens, "cu_seqlens"), B, int(max_seqlen), total, H, Hkv,
+                               _i32(cu_seqlens, "cu_seqlens"), B, max_seqlen, total, H, Hkv,
                                d, int(bool(causal)), float(scale), _stream(stream)),
            "fa_bwd_varlen")
 
 
 def fa_bwd_workspace_size(B: int, H: int, Hkv: int, N: int, d: int) -> int:
-    return int(lib().fa_bwd_workspace_size(B, H, Hkv, N, d))
+    return _bytes(lib().fa_bwd_workspace_size, B, H, Hkv, N, d)
 
 
 def _ws(workspace):
@@ -316,12 +331,13 @@ def fa_bwd_window(q, k, v, o, dout, lse, dq, dk, dv, workspace, window: int, sca
                   stream=None) -> None:
     """Backward of fa_fwd_window."""
     B, H, Hkv, N, d = _dims(q, k)
+    window = _c_int(window, "window")
     qs, ks, ls = _shapes(B, H, Hkv, N, d)
     wp, wb = _ws(workspace)
     _check(lib().fa_bwd_window(_bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v", ks), _bf16(o, "o", qs),
                                _bf16(dout, "dout", qs), _f32(lse, "lse", ls), _bf16(dq, "dq", qs),
                                _bf16(dk, "dk", ks), _bf16(dv, "dv", ks), wp, wb, B, H, Hkv, N, d,
-                               int(window), float(scale), _stream(stream)), "fa_bwd_window")
+                               window, float(scale), _stream(stream)), "fa_bwd_window")
 
 
 def fa_fwd_window_train(q, k, v, o, lse, workspace, window: int, scale: float,
@@ -329,11 +345,12 @@ def fa_fwd_window_train(q, k, v, o, lse, workspace, window: int, scale: float,
     """fa_fwd_window, plus the backward's workspace prepared for
     fa_bwd_window_train."""
     B, H, Hkv, N, d = _dims(q, k)
+    window = _c_int(window, "window")
     qs, ks, ls = _shapes(B, H, Hkv, N, d)
     wp, wb = _ws(workspace)
     _check(lib().fa_fwd_window_train(_bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v", ks),
                                      _bf16(o, "o", qs), _f32(lse, "lse", ls), wp, wb, B, H, Hkv,
-                                     N, d, int(window), float(scale), _stream(stream)),
+                                     N, d, window, float(scale), _stream(stream)),
            "fa_fwd_window_train")
 
 
@@ -341,12 +358,13 @@ def fa_bwd_window_train(q, k, v, o, dout, dq, dk, dv, workspace, window: int, sc
                         stream=None) -> None:
     """The backward of fa_fwd_window_train, on the workspace it prepared."""
     B, H, Hkv, N, d = _dims(q, k)
+    window = _c_int(window, "window")
     qs, ks, ls = _shapes(B, H, Hkv, N, d)
     wp, wb = _ws(workspace)
     _check(lib().fa_bwd_window_train(_bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v", ks),
                                      _bf16(o, "o", qs), _bf16(dout, "dout", qs),
                                      _bf16(dq, "dq", qs), _bf16(dk, "dk", ks), _bf16(dv, "dv", ks),
-                                     wp, wb, B, H, Hkv, N, d, int(window), float(scale),
+                                     wp, wb, B, H, Hkv, N, d, window, float(scale),
                                      _stream(stream)), "fa_bwd_window_train")
 
 
@@ -388,12 +406,13 @@ def fa_bwd_dkdv(q, k, v, dout, dk, dv, workspace, causal: bool, scale: float,
 def fa_bwd_dkdv_window(q, k, v, dout, dk, dv, workspace, window: int, scale: float,
                        stream=None) -> None:
     B, H, Hkv, N, d = _dims(q, k)
+    window = _c_int(window, "window")
     qs, ks, _ = _shapes(B, H, Hkv, N, d)
     wp, wb = _ws(workspace)
     _check(lib().fa_bwd_dkdv_window(_bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v", ks),
                                     _bf16(dout, "dout", qs), _bf16(dk, "dk", ks),
                                     _bf16(dv, "dv", ks), wp, wb,
-                                    B, H, Hkv, N, d, int(window), float(scale), _stream(stream)),
+                                    B, H, Hkv, N, d, window, float(scale), _stream(stream)),
            "fa_bwd_dkdv_window")
 
 
@@ -457,7 +476,7 @@ class _Outputs:
 
 
 def fa_fp8_buffer_size(B: int, H: int, Hkv: int, N: int, d: int) -> int:
-    return int(lib().fa_fp8_buffer_size(B, H, Hkv, N, d))
+    return _bytes(lib().fa_fp8_buffer_size, B, H, Hkv, N, d)
 
 
 def fa_fp8_quantize(v, fp8_buf, H: int, stream=None) -> None:
@@ -500,7 +519,7 @@ def attention_fp8(q, k, v, causal: bool = False, scale: float | None = None, str
 
 
 def fa_fwd_decode_workspace_size(B: int, H: int, Hkv: int, Nq: int, Nk: int, d: int) -> int:
-    return int(lib().fa_fwd_decode_workspace_size(B, H, Hkv, Nq, Nk, d))
+    return _bytes(lib().fa_fwd_decode_workspace_size, B, H, Hkv, Nq, Nk, d)
 
 
 def fa_fwd_decode(q, k, v, o, lse, workspace, causal: bool, scale: float, stream=None) -> None:
@@ -621,7 +640,8 @@ def fa_kv_append_varlen(k, v, k_pages, v_pages, block_table, starts, cu_seqlens,
                         kv_scales=None, stream=None) -> None:
     """fa_kv_append from a packed batch: k, v [Hkv, total, d], cu_seqlens int32 [B + 1]."""
     _check(_move(lib().fa_kv_append_varlen, True, k, v, k_pages, v_pages, block_table, starts,
-                 cu_seqlens, kv_scales, stream, int(max_seqlen)), "fa_kv_append_varlen")
+                 cu_seqlens, kv_scales, stream, _c_int(max_seqlen, "max_seqlen")),
+           "fa_kv_append_varlen")
 
 
 def fa_kv_gather(k_pages, v_pages, k, v, block_table, starts, counts, kv_scales=None,
@@ -636,11 +656,12 @@ def fa_kv_gather_varlen(k_pages, v_pages, k, v, block_table, starts, cu_seqlens,
                         kv_scales=None, stream=None) -> None:
     """fa_kv_gather into a packed batch: k, v [Hkv, total, d], cu_seqlens int32 [B + 1]."""
     _check(_move(lib().fa_kv_gather_varlen, False, k, v, k_pages, v_pages, block_table, starts,
-                 cu_seqlens, kv_scales, stream, int(max_seqlen)), "fa_kv_gather_varlen")
+                 cu_seqlens, kv_scales, stream, _c_int(max_seqlen, "max_seqlen")),
+           "fa_kv_gather_varlen")
 
 
 def fa_fwd_decode_paged_workspace_size(B: int, H: int, Hkv: int, Nq: int, d: int) -> int:
-    return int(lib().fa_fwd_decode_paged_workspace_size(B, H, Hkv, Nq, d))
+    return _bytes(lib().fa_fwd_decode_paged_workspace_size, B, H, Hkv, Nq, d)
 
 
 def fa_fwd_decode_paged(q, k_pages, v_pages, o, lse, block_table, seqlens, workspace,
