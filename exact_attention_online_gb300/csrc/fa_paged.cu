@@ -56,7 +56,8 @@ namespace {
 constexpr int kTile = 128;              // keys per tile
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
-constexpr float kMinLogScale = -60.0f;  // V scales below 2^-60 no longer move the reference
+constexpr float kMinLogScale = -60.0f;  // V scales below 2^-60 no longer move the reference,
+                                        // whose sum of weights would leave fp32's range
 constexpr float kNoMax = -3.402823466e38f;   // running maximum of a row that has seen no key
 constexpr int kSoftBar = 1;             // named barrier of softmax group 0
 constexpr int kMaxCluster = 8;          // most CTAs that share a pair without a list
@@ -137,7 +138,7 @@ struct Cfg {
     // long the cache.  (With one reference for a whole pair, 4096 keys a stretch turn
     // into n.)  Four tokens a sequence, B8, 8 kv heads, 8K to 16K keys, without this,
     // every 32 and every 16 tiles: 16 rows of d = 128 40.8, 41.1 and 41.3 us, 32 rows
-    // 52.6, 54.5 and 55.7; 16 rows of d = 64 36.0, 37.3 and 38.0.
+    // 52.6, 54.6 and 55.7; 16 rows of d = 64 36.0, 37.4 and 38.0; 8 rows alike.
     static constexpr int kRefTiles = F8 ? 32 : 0;
     static constexpr float kRefDrop = 24.0f;
 };
@@ -266,7 +267,7 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int site, c
     return mbar_try_wait(smem_u32(bar), parity) || wait_on(bar, parity, site, wc);
 }
 // Two barriers' phases, both tried before either answer is needed (16 rows of e4m3,
-// d = 64: 35.8 us instead of 37.2 with one after the other).
+// d = 64: 37.5 us instead of 38.6 with one after the other).
 __device__ __forceinline__ bool wait_both(uint64_t* a, uint64_t* b, uint32_t parity, int site,
                                           const WaitCtx& wc) {
     const bool there = mbar_try_wait(smem_u32(a), parity);
@@ -1150,7 +1151,7 @@ cudaError_t launch_rows(const CUtensorMap& tk, const CUtensorMap& tv, PagedParam
     if (p.R <= 4) return launch_attend<D, F8, 1, 4>(tk, tv, p, stream);
     if (p.R <= 8) return launch_attend<D, F8, 1, 8>(tk, tv, p, stream);
     // Two groups of 8 rows rather than one of 16 (e4m3 at d = 128, B8, four tokens, 8K
-    // to 16K keys: 41.2 and 50.0 us), two of 16 rather than four of 8 (53.2 and 54.5).
+    // to 16K keys: 41.0 and 42.5 us), two of 16 rather than four of 8 (54.7 and 56.5).
     if (p.R <= 16) return launch_attend<D, F8, 2, 8>(tk, tv, p, stream);
     return launch_attend<D, F8, 2, 16>(tk, tv, p, stream);
 }

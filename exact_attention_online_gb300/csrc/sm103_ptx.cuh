@@ -358,8 +358,9 @@ __device__ __forceinline__ void mma_ts_f8(uint32_t d_tmem, uint32_t a_tmem, uint
 }
 
 // D[tmem] (+)= A[smem] * B[smem] where `issue` is set, for a converged warp of which
-// one thread issues: a predicate instead of a branch (four e4m3 MMAs and their commit
-// keep the warp 66 cycles instead of 195).
+// one thread issues: a predicate instead of a branch (paged decoding of B8, four tokens,
+// 8K to 16K keys, 32 rows of a bf16 cache at d = 64: 41.5 us instead of 43.7; e4m3 rows
+// and d = 128: 0 to 1 % less).
 __device__ __forceinline__ void mma_ss_if(bool issue, uint32_t d_tmem, uint64_t adesc,
                                           uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
     asm volatile(

@@ -435,7 +435,8 @@ FA_API fa_status fa_fwd_decode(const void* q, const void* k, const void* v, void
  * stand in several tables (a shared prefix).  d in {64, 128}; page_size a
  * power of two from 16 to 256; max_pages * page_size < 2^30; n_pages * Hkv <
  * 2^31 (the pool itself may be larger than 2^31 elements); B * Hkv *
- * (max_pages * page_size / 128 + 2) <= 2^30.  FA_ERR_UNSUPPORTED past these.  Pointers to floats and rows 16-byte aligned, to ints 4-byte.
+ * (max_pages * page_size / 128 + 2) <= 2^30.  FA_ERR_UNSUPPORTED past these.
+ * Pointers to floats and rows 16-byte aligned, to ints 4-byte.
  *
  * Table entries and lengths are read by the kernels.  Entries outside
  * [0, n_pages) that a call reaches give unspecified results (fa_fwd_decode_paged)
@@ -456,8 +457,9 @@ FA_API fa_status fa_fwd_decode(const void* q, const void* k, const void* v, void
  * row of zeros; a nonzero amax below 2^-100 counts as 2^-100; a NaN stays a
  * NaN, and a row with an infinity reads back as NaN).  Different rows for one
  * place in one call (a page that two sequences write) leave that place
- * unspecified.  Positions past the table are not written.  Errors as fa_fwd(), FA_ERR_UNSUPPORTED for B * Hkv * N >= 2^31.
- * Asynchronous on `stream`; one launch.
+ * unspecified.  Positions past the table are not written.  Errors as fa_fwd(),
+ * FA_ERR_UNSUPPORTED for B * Hkv * N >= 2^31.  Asynchronous on `stream`; one
+ * launch.
  */
 FA_API fa_status fa_kv_append(const void* k, const void* v, void* k_pages, void* v_pages,
                               float* kv_scales, const int* block_table, const int* starts,
@@ -517,10 +519,13 @@ FA_API fa_status fa_kv_gather_varlen(const void* k_pages, const void* v_pages,
  * pages: q and P enter as the sum of two e4m3 terms (8 significant bits, those
  * of bf16), so that the codes are multiplied as they are and only the scales
  * are applied in fp32.  A query's entry is exact down to 2^-14 of the row's
- * largest and off by at most 2^-22 of that below.  A weight times its V scale keeps 8 bits down to 2^-12
- * of the largest such product among up to 4096 neighbouring keys, and is off
- * by at most 2^-20.6 of that below: all of them by 2^-8.6, whatever the
- * cache's length, while LSE counts every weight in full.
+ * largest and off by at most 2^-22 of that below.  A weight times its V scale
+ * keeps 8 bits down to 2^-12 of the largest such product among the 4096 keys
+ * around it and is off by at most 2^-20.6 of that below, so that all products
+ * below are off by at most 2^-8.6 of the sum of all, whatever the cache's
+ * length; LSE counts every weight in full.  V scales below 2^-60 (rows of
+ * magnitudes below 2^-51) keep fewer bits where no larger one is
+ * near, and vanish below 2^-80.
  *
  * workspace: caller-owned device memory of
  * fa_fwd_decode_paged_workspace_size() bytes, 256-byte aligned, contents on

@@ -133,3 +133,33 @@ def test_query_with_a_large_entry(d, rows):
         scale * 2.0 ** -22 * big * (small * kd.abs()).sum(-1)
     off = (lse.double() - ref).abs()
     assert (off <= bound).all(), ((off / bound).max().item(), off.max().item())
+
+
+@pytest.mark.parametrize("size", [2.0 ** 60, 1.0, 2.0 ** -45, 2.0 ** -51], ids=["2^60", "1", "2^-45", "2^-51"])
+@pytest.mark.parametrize("rows", [(1, 1), (8, 2), (8, 4)], ids=lambda r: f"{r[0]}x{r[1]}")
+@pytest.mark.parametrize("d", [64, 128])
+def test_values_of_any_size_under_a_falling_reference(d, rows, size):
+    """The first 4000 keys lead the other 16000 by 0 to 60 nats; V is 1.5 * size throughout, so
+    that O is too, whatever the weights: sums of weights stay inside fp32's range while the
+    reference falls.  The bound is the one above, relative; V's scales are size * 1.5 / 448, at
+    least 2^-60."""
+    n, first, scale, B = 20000, 4000, 0.125, 200
+    H, Nq = rows
+    gen = torch.Generator(device="cuda").manual_seed(d + H)
+    k = torch.randn((1, n, d), generator=gen, device="cuda").bfloat16()
+    k[:, :, 0] = 0
+    k[:, :first, 0] = 1
+    v = torch.full((1, n, d), 1.5 * size, device="cuda").bfloat16()
+    kp, vp, sc, table = filled(k, v, 64, seed=d)
+    q = (torch.randint(0, 2, (B, H, Nq, d), generator=gen, device="cuda") - 0.5).bfloat16()
+    lead = torch.tensor([0.0, 12.0, 30.0, 60.0], device="cuda")
+    q[..., 0] = (8 * lead.repeat(B * H * Nq // 4)[:B * H * Nq].view(B, H, Nq)).bfloat16()
+    o, lse = fa.attention_decode_paged(q, kp, vp, table.expand(B, -1).contiguous(), i32([n] * B),
+                                       False, scale, kv_scales=sc)
+    torch.cuda.synchronize()
+    assert fa.fa_device_status() == fa.FA_OK
+    off = (o.double() / (1.5 * size) - 1).abs().max().item()
+    assert off <= 2.0 ** -8 * 2.13 + 2 * n * 2.0 ** -23 + FLOOR * REACH * 2, off
+    x = scale * q[:2].reshape(-1, d).double() @ rows64(kp, sc, 0, table, n)[0][0].T
+    dl = (lse[:2].reshape(-1).double() - torch.logsumexp(x, -1)).abs().max().item()
+    assert dl <= 2 * (d + 16) * 2.0 ** -24 * 70 + 2.0 ** -19 + 2.0 ** -22 * 80, dl
