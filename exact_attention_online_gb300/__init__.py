@@ -37,7 +37,9 @@ __all__ = ["build", "lib", "LIB_PATH", "EXPORTS", "FAError", "fa_fwd", "fa_fwd_p
            "fa_ex2_rate",
            "fa_fwd_window_train", "fa_bwd_window_train",
            "fa_kv_append", "fa_kv_append_varlen", "fa_kv_gather", "fa_kv_gather_varlen",
-           "fa_fwd_decode_paged_workspace_size", "fa_fwd_decode_paged", "attention_decode_paged"]
+           "fa_fwd_decode_paged_workspace_size", "fa_fwd_decode_paged", "attention_decode_paged",
+           "fa_kv_reserve", "fa_kv_release", "fa_kv_slots", "fa_kv_slots_varlen",
+           "rope_frequencies", "fa_rope", "rope", "fa_rope_append"]
 
 
 class FAError(RuntimeError):
@@ -725,6 +727,239 @@ def attention_decode_paged(q, k_pages, v_pages, block_table, seqlens, causal: bo
     if on.side is not None:
         workspace.record_stream(on.side)       # the caller's, if it is given
     return on.out(o, lse)
+
+
+# --------------------------------------------- block tables and slot maps
+def _all_i32(cur, shapes):
+    """Pointers of contiguous int32 tensors of the current device, (tensor, name, shape) each."""
+    import torch
+    i32 = torch.int32
+    for t, _, shape in shapes:
+        if not (t.dtype is i32 and t.shape == shape and t.get_device() == cur and
+                t.is_contiguous()):
+            _explain(*((t, name, i32, shape) for t, name, shape in shapes))
+    return [t.data_ptr() for t, _, _ in shapes]
+
+
+def _map(positions, slots, shape, cur):
+    import torch
+    if not (positions.dtype is torch.int32 and slots.dtype is torch.int64 and
+            positions.shape == shape and slots.shape == shape and
+            positions.get_device() == cur and slots.get_device() == cur and
+            positions.is_contiguous() and slots.is_contiguous()):
+        _explain((positions, "positions", torch.int32, shape), (slots, "slots", torch.int64, shape))
+    return positions.data_ptr(), slots.data_ptr()
+
+
+def _table(block_table):
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be 2-D [B, max_pages]")
+    return block_table.shape
+
+
+def fa_kv_reserve(block_table, seqlens, free_pages, n_free, new_tokens, starts, counts,
+                  cu_seqlens, page_size: int, positions=None, slots=None, stream=None) -> None:
+    """Room for new_tokens [B] more tokens a sequence: block_table [B, max_pages], seqlens [B],
+    free_pages [n_pages] and n_free [1] in place; starts, counts [B] and cu_seqlens [B + 1]
+    written; positions, slots (int64) [B, N] or packed [total]: the new tokens' map.  All
+    int32 but slots."""
+    B, mp = table = _table(block_table)
+    cur = _current_index()
+    one = (B,)
+    n_pages = free_pages.numel()
+    ptrs = _all_i32(cur, ((block_table, "block_table", table), (seqlens, "seqlens", one),
+                          (free_pages, "free_pages", (n_pages,)), (n_free, "n_free", (1,)),
+                          (new_tokens, "new_tokens", one), (starts, "starts", one),
+                          (counts, "counts", one), (cu_seqlens, "cu_seqlens", (B + 1,))))
+    N, total, at = 0, 0, (None, None)
+    if positions is not None or slots is not None:
+        if positions is None or slots is None:
+            raise ValueError("positions and slots come together")
+        shape = slots.shape
+        if len(shape) == 2:
+            N, shape = shape[1], (B, shape[1])
+            if N < 1:
+                raise ValueError("slots has no rows")
+        else:
+            total, shape = slots.numel(), (slots.numel(),)
+        at = _map(positions, slots, shape, cur)
+    _check(lib().fa_kv_reserve(*ptrs, *at, B, N, total, n_pages, _c_int(page_size, "page_size"),
+                               mp, _stream(stream)), "fa_kv_reserve")
+
+
+def fa_kv_release(block_table, seqlens, free_pages, n_free, keep, page_size: int, pinned=None,
+                  stream=None) -> None:
+    """Every sequence cut back to its first keep [B] tokens, the pages behind them free again
+    (but for the first pinned [B] pages of each, if given)."""
+    B, mp = table = _table(block_table)
+    cur = _current_index()
+    one = (B,)
+    n_pages = free_pages.numel()
+    ptrs = _all_i32(cur, ((block_table, "block_table", table), (seqlens, "seqlens", one),
+                          (free_pages, "free_pages", (n_pages,)), (n_free, "n_free", (1,)),
+                          (keep, "keep", one)) +
+                    (() if pinned is None else ((pinned, "pinned", one),)))
+    if pinned is None:
+        ptrs.append(None)
+    _check(lib().fa_kv_release(*ptrs, B, n_pages, _c_int(page_size, "page_size"), mp,
+                               _stream(stream)), "fa_kv_release")
+
+
+def fa_kv_slots(block_table, starts, counts, positions, slots, page_size: int,
+                stream=None) -> None:
+    """Positions and slots [B, N] of rows i < counts[b] at positions starts[b] + i."""
+    B, mp = table = _table(block_table)
+    cur = _current_index()
+    ptrs = _all_i32(cur, ((block_table, "block_table", table), (starts, "starts", (B,)),
+                          (counts, "counts", (B,))))
+    if slots.dim() != 2:
+        raise ValueError("slots must be 2-D [B, N]")
+    N = slots.shape[1]
+    at = _map(positions, slots, (B, N), cur)
+    _check(lib().fa_kv_slots(*ptrs, *at, B, N, _c_int(page_size, "page_size"), mp,
+                             _stream(stream)), "fa_kv_slots")
+
+
+def fa_kv_slots_varlen(block_table, starts, cu_seqlens, positions, slots, page_size: int,
+                       stream=None) -> None:
+    """The same of a packed batch: positions, slots [total], cu_seqlens [B + 1]."""
+    B, mp = table = _table(block_table)
+    cur = _current_index()
+    ptrs = _all_i32(cur, ((block_table, "block_table", table), (starts, "starts", (B,)),
+                          (cu_seqlens, "cu_seqlens", (B + 1,))))
+    if slots.dim() != 1:
+        raise ValueError("slots must be 1-D [total]")
+    at = _map(positions, slots, slots.shape, cur)
+    _check(lib().fa_kv_slots_varlen(*ptrs, *at, B, slots.numel(), _c_int(page_size, "page_size"),
+                                    mp, _stream(stream)), "fa_kv_slots_varlen")
+
+
+# ------------------------------------------------------- rotary positions
+_SCALINGS = {None: 0, "none": 0, "linear": 1, "ntk": 2, "parts": 3}
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, scaling: str | None = None,
+                     factor: float = 1.0, original_length: int = 0, beta_fast: float = 32.0,
+                     beta_slow: float = 1.0, device=None):
+    """(freqs, amplitude) for fa_rope and fa_rope_append: an int64 tensor [rot / 2] on `device`
+    (default: the current CUDA device) and a number, from fa_rope_freqs.  scaling: "linear",
+    "ntk" or "parts"."""
+    import torch
+    if scaling not in _SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(k for k in _SCALINGS if k)}")
+    rot = _c_int(rot, "rot")
+    freqs = torch.zeros(max(rot // 2, 1), dtype=torch.int64)
+    amplitude = ctypes.c_float()
+    _check(lib().fa_rope_freqs(freqs.data_ptr(), ctypes.byref(amplitude), rot, float(base),
+                               _SCALINGS[scaling], float(factor),
+                               _c_int(original_length, "original_length"), float(beta_fast),
+                               float(beta_slow)), "fa_rope_freqs")
+    return freqs.to("cuda" if device is None else device), amplitude.value
+
+
+_STRIDES = ctypes.c_longlong * 12
+
+
+def _rows_ok(t, shape, cur):
+    import torch
+    return (t.dtype is torch.bfloat16 and t.shape == shape and t.get_device() == cur and
+            t.stride(3) == 1)
+
+
+def _explain_rows(*args):
+    import torch
+    for t, name, shape in args:
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if t.dtype != torch.bfloat16 or not t.is_cuda or t.stride(3) != 1:
+            raise ValueError(f"{name} must be a CUDA bfloat16 tensor with contiguous rows")
+        _on_current_device(t, name)
+    raise ValueError("tensors disagree")
+
+
+def _rope_args(qs, positions, freqs, cur):
+    """B, H, N, d, rot of a call, and the pointers of positions and freqs."""
+    import torch
+    if len(qs) != 4:
+        raise ValueError("q must be 4-D [B, H, N, d]")
+    B, H, N, d = qs
+    if not (positions.dtype is torch.int32 and positions.shape == (B, N) and
+            positions.get_device() == cur and positions.is_contiguous() and
+            freqs.dtype is torch.int64 and freqs.get_device() == cur and freqs.is_contiguous() and
+            len(freqs.shape) == 1):
+        _explain((positions, "positions", torch.int32, (B, N)),
+                 (freqs, "freqs", torch.int64, (freqs.numel(),)))
+    return B, H, N, d, 2 * freqs.numel(), positions.data_ptr(), freqs.data_ptr()
+
+
+def fa_rope(q, k, q_out, k_out, positions, freqs, interleaved: bool = False,
+            inverse: bool = False, amplitude: float = 1.0, stream=None) -> None:
+    """q [B, H, N, d] and k [B, Hkv, N, d] (or None, with k_out) turned by their positions
+    int32 [B, N] into q_out and k_out; any strides over B, H and N.  freqs, amplitude: from
+    rope_frequencies; inverse: for gradients."""
+    cur = _current_index()
+    B, H, N, d, rot, pp, fp = _rope_args(q.shape, positions, freqs, cur)
+    if (k is None) != (k_out is None):
+        raise ValueError("k and k_out come together")
+    if k is None:
+        Hkv, kp, ks, kop, kos = 0, None, (0, 0, 0, 0), None, (0, 0, 0, 0)
+    else:
+        Hkv = k.shape[1] if k.dim() == 4 else 0
+        kp, ks, kop, kos = k.data_ptr(), k.stride(), k_out.data_ptr(), k_out.stride()
+    shape = (B, Hkv, N, d)
+    if not (_rows_ok(q, q.shape, cur) and _rows_ok(q_out, q.shape, cur) and
+            (k is None or (_rows_ok(k, shape, cur) and _rows_ok(k_out, shape, cur)))):
+        _explain_rows((q, "q", q.shape), (q_out, "q_out", q.shape),
+                      *(() if k is None else ((k, "k", shape), (k_out, "k_out", shape))))
+    strides = _STRIDES(*q.stride()[:3], *ks[:3], *q_out.stride()[:3], *kos[:3])
+    _check(lib().fa_rope(q.data_ptr(), kp, q_out.data_ptr(), kop, pp, fp, strides, B, H, Hkv, N, d,
+                         rot, 1 if interleaved else 0, 1 if inverse else 0, float(amplitude),
+                         _stream(stream)), "fa_rope")
+
+
+def rope(q, k, positions, freqs, interleaved: bool = False, inverse: bool = False,
+         amplitude: float = 1.0, stream=None):
+    """fa_rope into new contiguous tensors; returns (q_out, k_out)."""
+    import torch
+    with _Outputs(stream) as on:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        k_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    fa_rope(q, k, q_out, k_out, positions, freqs, interleaved, inverse, amplitude, stream)
+    on.out(*(t for t in (q_out, k_out) if t is not None))
+    return q_out, k_out
+
+
+def fa_rope_append(q, k, v, q_out, k_pages, v_pages, positions, slots, freqs,
+                   interleaved: bool = False, amplitude: float = 1.0, kv_scales=None,
+                   stream=None) -> None:
+    """q [B, H, N, d] turned into q_out; k [B, Hkv, N, d] turned, and v, into the pages at
+    slots int64 [B, N] (negative: not written); a packed batch is B = 1.  Any strides over
+    B, H and N of q, k, v and q_out."""
+    import torch
+    cur = _current_index()
+    B, H, N, d, rot, pp, fp = _rope_args(q.shape, positions, freqs, cur)
+    pool = k_pages.shape
+    if len(pool) != 4 or pool[3] != d:
+        raise ValueError(f"k_pages must be 4-D [n_pages, Hkv, page_size, {d}]")
+    kd = torch.bfloat16 if kv_scales is None else torch.float8_e4m3fn
+    shape = (B, pool[1], N, d)
+    if not (_rows_ok(q, q.shape, cur) and _rows_ok(q_out, q.shape, cur) and
+            _rows_ok(k, shape, cur) and _rows_ok(v, shape, cur)):
+        _explain_rows((q, "q", q.shape), (q_out, "q_out", q.shape), (k, "k", shape),
+                      (v, "v", shape))
+    if not (k_pages.dtype is kd and v_pages.dtype is kd and v_pages.shape == pool and
+            k_pages.get_device() == cur and v_pages.get_device() == cur and
+            k_pages.is_contiguous() and v_pages.is_contiguous() and
+            slots.dtype is torch.int64 and slots.shape == (B, N) and slots.get_device() == cur and
+            slots.is_contiguous()):
+        _explain((k_pages, "k_pages", kd, pool), (v_pages, "v_pages", kd, pool),
+                 (slots, "slots", torch.int64, (B, N)))
+    strides = _STRIDES(*q.stride()[:3], *k.stride()[:3], *v.stride()[:3], *q_out.stride()[:3])
+    _check(lib().fa_rope_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(),
+                                k_pages.data_ptr(), v_pages.data_ptr(),
+                                _scales(kv_scales, pool, cur), pp, slots.data_ptr(), fp, strides, B,
+                                H, pool[1], N, pool[0], pool[2], d, rot, 1 if interleaved else 0,
+                                float(amplitude), _stream(stream)), "fa_rope_append")
 
 
 def attention(q, k, v, causal: bool = False, scale: float | None = None, stream=None,

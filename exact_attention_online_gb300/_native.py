@@ -20,7 +20,7 @@ OBJ_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(OUT_DIR, "libfa.so")
 
 SOURCES = ["api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_noalloc.cu", "fa_fp8.cu", "fa_decode.cu",
-           "fa_diag.cu", "fa_kvcache.cu", "fa_paged.cu"]
+           "fa_diag.cu", "fa_kvcache.cu", "fa_paged.cu", "fa_tables.cu", "fa_rope.cu"]
 HEADERS = ["sm103_ptx.cuh", "fa_internal.h", "exp2_poly.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
@@ -168,6 +168,21 @@ def _bind(L: ctypes.CDLL) -> ctypes.CDLL:
     L.fa_fwd_decode_paged_workspace_size.restype = sz
     L.fa_fwd_decode_paged.argtypes = [vp] * 9 + [sz] + [i] * 9 + [f, vp]
     L.fa_fwd_decode_paged.restype = i
+    L.fa_kv_reserve.argtypes = [vp] * 10 + [i] * 6 + [vp]
+    L.fa_kv_reserve.restype = i
+    L.fa_kv_release.argtypes = [vp] * 6 + [i] * 4 + [vp]
+    L.fa_kv_release.restype = i
+    L.fa_kv_slots.argtypes = [vp] * 5 + [i] * 4 + [vp]
+    L.fa_kv_slots.restype = i
+    L.fa_kv_slots_varlen.argtypes = [vp] * 5 + [i] * 4 + [vp]
+    L.fa_kv_slots_varlen.restype = i
+    L.fa_rope_freqs.argtypes = [vp, ctypes.POINTER(f), i, ctypes.c_double, i, ctypes.c_double, i,
+                                ctypes.c_double, ctypes.c_double]
+    L.fa_rope_freqs.restype = i
+    L.fa_rope.argtypes = [vp] * 7 + [i] * 8 + [f, vp]
+    L.fa_rope.restype = i
+    L.fa_rope_append.argtypes = [vp] * 11 + [i] * 9 + [f, vp]
+    L.fa_rope_append.restype = i
     return L
 
 
@@ -199,4 +214,6 @@ EXPORTS = ["fa_fwd", "fa_fwd_precise", "fa_bwd_workspace_size", "fa_bwd", "fa_bw
            "fa_ex2_rate",
            "fa_fwd_window_train", "fa_bwd_window_train",
            "fa_kv_append", "fa_kv_append_varlen", "fa_kv_gather", "fa_kv_gather_varlen",
-           "fa_fwd_decode_paged_workspace_size", "fa_fwd_decode_paged"]
+           "fa_fwd_decode_paged_workspace_size", "fa_fwd_decode_paged",
+           "fa_kv_reserve", "fa_kv_release", "fa_kv_slots", "fa_kv_slots_varlen",
+           "fa_rope_freqs", "fa_rope", "fa_rope_append"]

@@ -203,6 +203,35 @@ int device_sm_count();
 // Counts one kernel launch for fa_kernel_launches().
 void count_launch();
 
+// A device pointer of the caller's: not null, aligned.
+inline fa_status check_pointer(const void* p, size_t align) {
+    if (!p) return FA_ERR_INVALID_ARG;
+    return reinterpret_cast<uintptr_t>(p) % align ? FA_ERR_ALIGNMENT : FA_OK;
+}
+
+// A launch (in clusters of `cluster` blocks) whose blocks may come in while the
+// kernel before in the stream still runs; they wait for it (pdl_wait) before they
+// read what it wrote.
+template <typename... Params, typename... Args>
+cudaError_t launch_pdl(void (*kern)(Params...), dim3 grid, unsigned threads, size_t smem,
+                       int cluster, cudaStream_t stream, const Args&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    count_launch();
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Argument checks of fa_bwd() (without the workspace) and the per-device
 // set-up (sm_103 check, status word), for entry points in other files.
 fa_status validate_bwd_args(const void* q, const void* k, const void* v, const void* o,

@@ -1036,29 +1036,6 @@ fa_paged_combine_kernel(const __grid_constant__ PagedParams p, int rows) {
         p.lse[row] = sum == 0.0f ? -CUDART_INF_F : add_log2(mx, sum) * kLn2;
 }
 
-// A launch (in clusters of `cluster` blocks) whose blocks may come in while the
-// kernel before in the stream still runs; they wait for it (pdl_wait) before they
-// read what it wrote.
-template <typename... Params, typename... Args>
-cudaError_t launch_pdl(void (*kern)(Params...), unsigned grid, unsigned threads, size_t smem,
-                       int cluster, cudaStream_t stream, const Args&... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)cluster;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.numAttrs = cluster > 1 ? 2 : 1;
-    count_launch();
-    return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
 // Once a device and kernel: the shared memory it may use.
 template <int D, bool F8, int G, int W, bool CLUSTER>
 cudaError_t configure(int dev) {

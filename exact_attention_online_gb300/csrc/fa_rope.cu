@@ -1,0 +1,391 @@
+// Rotary positions: pair i of a row at position x turns by the angle x * f_i,
+//     (a, b) -> amplitude * (a cos - b sin, b cos + a sin),
+// the pairs being (i, i + rot / 2) or, interleaved, (2 i, 2 i + 1); values from rot
+// on stay.  The gradient is the same with the angle negated.  The append form turns
+// q, and turns K on its way into the pages of a paged cache (bf16, or quantised to
+// e4m3 as fa_kv_append does) beside V.
+//
+// Angles: f_i comes as a 64-bit fraction of a full turn per token, so x * f_i modulo
+// one turn is a 64-bit integer product, exact whatever the position; its upper 32
+// bits go through sincospif.  (An fp32 angle is off by 2^-24 of itself: 0.03 rad at
+// position 10^6.)
+//
+// The work is a copy with a few operations a value: bound by HBM.  D / 16 lanes
+// share a row, 16 values a lane: the two 8-value pieces that are each other's
+// partners (half layout), or 16 neighbours (interleaved), so no value crosses lanes.
+// A thread keeps one token's sines and cosines in registers and goes over its heads,
+// whose loads are in flight together.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "fa_internal.h"
+
+namespace fa {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kBatch = 4;             // heads whose loads are in flight together
+
+// A tensor [B][heads][N][D] of any strides (in elements; rows contiguous).
+struct Rows {
+    const void* p;
+    long long sb, sh, sn;
+};
+
+struct RopeParams {
+    Rows q, k, v, q_out, k_out;       // k_out: contiguous side only
+    void* k_pages;
+    void* v_pages;
+    float* scales;
+    const int* positions;             // [B][N]
+    const long long* slots;           // [B][N]: page * page_size + row, or negative
+    const unsigned long long* freqs;  // [rot / 2]
+    long long n_slots;
+    int B, H, Hkv, N, T, rot, inverse, ps_shift, heads_each;
+    float amplitude;
+};
+
+enum { kPlain, kAppend, kAppendF8 };
+
+__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// The eight pairs of a lane, and back.
+template <bool INTER>
+__device__ __forceinline__ void unpack_pairs(const uint4 (&w)[2], float (&a)[8], float (&b)[8]) {
+    const uint32_t u[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (INTER) {
+            a[i] = lo_f(u[i]);
+            b[i] = hi_f(u[i]);
+        } else {
+            a[i] = i & 1 ? hi_f(u[i / 2]) : lo_f(u[i / 2]);
+            b[i] = i & 1 ? hi_f(u[4 + i / 2]) : lo_f(u[4 + i / 2]);
+        }
+    }
+}
+template <bool INTER>
+__device__ __forceinline__ void pack_pairs(const float (&a)[8], const float (&b)[8], uint4 (&w)[2]) {
+    uint32_t u[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (INTER) {
+            u[2 * i] = pack_bf16x2(a[2 * i], b[2 * i]);
+            u[2 * i + 1] = pack_bf16x2(a[2 * i + 1], b[2 * i + 1]);
+        } else {
+            u[i] = pack_bf16x2(a[2 * i], a[2 * i + 1]);
+            u[4 + i] = pack_bf16x2(b[2 * i], b[2 * i + 1]);
+        }
+    }
+    w[0] = make_uint4(u[0], u[1], u[2], u[3]);
+    w[1] = make_uint4(u[4], u[5], u[6], u[7]);
+}
+// Codes of the same two pieces.
+template <bool INTER>
+__device__ __forceinline__ void encode_pairs(const float (&a)[8], const float (&b)[8], float inv,
+                                             uint2 (&c)[2]) {
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        x[INTER ? 2 * i : i] = a[i] * inv;
+        x[INTER ? 2 * i + 1 : 8 + i] = b[i] * inv;
+    }
+    c[0] = make_uint2(pack_e4m3x4(x[0], x[1], x[2], x[3]), pack_e4m3x4(x[4], x[5], x[6], x[7]));
+    c[1] = make_uint2(pack_e4m3x4(x[8], x[9], x[10], x[11]),
+                      pack_e4m3x4(x[12], x[13], x[14], x[15]));
+}
+
+template <int D, bool INTER, int MODE>
+__global__ void __launch_bounds__(kThreads)
+fa_rope_kernel(const __grid_constant__ RopeParams p) {
+    constexpr int LPR = D / 16;                   // lanes a row
+    const int c = threadIdx.x % LPR;
+    const int t = blockIdx.x * (kThreads / LPR) + threadIdx.x / LPR;
+    const bool live = t < p.T;
+    const int b = live ? t / p.N : 0, n = live ? t - b * p.N : 0;
+    const bool turns = c < p.rot / 16;
+    // this lane's two pieces of 8 values
+    const int o0 = turns && !INTER ? 8 * c : 16 * c;
+    const int o1 = turns && !INTER ? p.rot / 2 + 8 * c : 16 * c + 8;
+    const int heads = p.H + p.Hkv * (MODE == kPlain ? 1 : 2);
+    const int first = blockIdx.y * p.heads_each, last = min(heads, first + p.heads_each);
+    pdl_wait();
+    pdl_launch_dependents();
+
+    float co[8], si[8];
+    if (turns && live && first < p.H + p.Hkv) {
+        const long long pos = p.positions[t];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            // half turns in [-1, 1)
+            const unsigned long long phase = (unsigned long long)pos * p.freqs[8 * c + i];
+            const float x = (float)(int)(phase >> 32) * 0x1p-31f;
+            sincospif(x, &si[i], &co[i]);
+            co[i] *= p.amplitude;
+            si[i] *= p.inverse ? -p.amplitude : p.amplitude;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) co[i] = si[i] = 0.0f;
+    }
+    long long place = -1;                         // of the new rows, kv head 0's, in rows
+    if (MODE != kPlain && live) {
+        const long long slot = p.slots[t];
+        if (slot >= 0 && slot < p.n_slots)
+            place = (((slot >> p.ps_shift) * p.Hkv) << p.ps_shift) +
+                    (slot & ((1 << p.ps_shift) - 1));
+    }
+    const __nv_bfloat16* const qs =
+        static_cast<const __nv_bfloat16*>(p.q.p) + b * p.q.sb + n * p.q.sn;
+    const __nv_bfloat16* const ks =
+        static_cast<const __nv_bfloat16*>(p.k.p) + b * p.k.sb + n * p.k.sn;
+    const __nv_bfloat16* const vs =
+        static_cast<const __nv_bfloat16*>(p.v.p) + b * p.v.sb + n * p.v.sn;
+#pragma unroll 1
+    for (int h0 = first; h0 < last; h0 += kBatch) {
+        uint4 w[kBatch][2];
+        bool ok[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int h = h0 + i;
+            ok[i] = live && h < last && (MODE == kPlain || h < p.H || place >= 0);
+            w[i][0] = w[i][1] = make_uint4(0u, 0u, 0u, 0u);
+            if (!ok[i]) continue;
+            const __nv_bfloat16* src = h < p.H           ? qs + h * p.q.sh
+                                       : h < p.H + p.Hkv ? ks + (h - p.H) * p.k.sh
+                                                         : vs + (h - p.H - p.Hkv) * p.v.sh;
+            w[i][0] = *reinterpret_cast<const uint4*>(src + o0);
+            w[i][1] = *reinterpret_cast<const uint4*>(src + o1);
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int h = h0 + i;
+            if (h >= last) break;
+            const bool is_v = MODE != kPlain && h >= p.H + p.Hkv;
+            const bool paged = MODE != kPlain && h >= p.H;
+            float x[8], y[8];
+            unpack_pairs<INTER>(w[i], x, y);
+            if (turns && !is_v) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float r = x[e] * co[e] - y[e] * si[e];
+                    y[e] = y[e] * co[e] + x[e] * si[e];
+                    x[e] = r;
+                }
+                if (MODE != kAppendF8 || !paged) pack_pairs<INTER>(x, y, w[i]);
+            }
+            if (MODE == kAppendF8 && paged) {
+                const int g = h - (is_v ? p.H + p.Hkv : p.H);
+                float amax = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fmaxf(fabsf(x[e]), fabsf(y[e])));
+#pragma unroll
+                for (int off = LPR / 2; off > 0; off >>= 1)
+                    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+                const bool zero = amax == 0.0f;
+                amax = fmaxf(amax, 0x1p-100f);
+                const float inv = zero ? 0.0f : 448.0f / amax;
+                if (!ok[i]) continue;
+                uint2 code[2];
+                encode_pairs<INTER>(x, y, inv, code);
+                const long long row = place + ((long long)g << p.ps_shift);
+                uint8_t* dst = static_cast<uint8_t*>(is_v ? p.v_pages : p.k_pages) + row * D;
+                *reinterpret_cast<uint2*>(dst + o0) = code[0];
+                *reinterpret_cast<uint2*>(dst + o1) = code[1];
+                if (c == 0) {
+                    // scales [page][Hkv][2][page_size]: row of (page * Hkv + g) * 2 (+ 1 for V)
+                    const int mask = (1 << p.ps_shift) - 1;
+                    p.scales[((row >> p.ps_shift) << (p.ps_shift + 1)) + (row & mask) +
+                             (is_v ? 1 << p.ps_shift : 0)] = zero ? 0.0f : amax / 448.0f;
+                }
+                continue;
+            }
+            if (!ok[i]) continue;
+            __nv_bfloat16* dst;
+            if (paged) {
+                const int g = h - (is_v ? p.H + p.Hkv : p.H);
+                dst = static_cast<__nv_bfloat16*>(is_v ? p.v_pages : p.k_pages) +
+                      (place + ((long long)g << p.ps_shift)) * D;
+            } else {
+                const bool is_k = h >= p.H;
+                const Rows& r = is_k ? p.k_out : p.q_out;
+                dst = static_cast<__nv_bfloat16*>(const_cast<void*>(r.p)) + b * r.sb + n * r.sn +
+                      (h - (is_k ? p.H : 0)) * r.sh;
+            }
+            *reinterpret_cast<uint4*>(dst + o0) = w[i][0];
+            *reinterpret_cast<uint4*>(dst + o1) = w[i][1];
+        }
+    }
+}
+
+template <int D, int MODE>
+cudaError_t launch(RopeParams& p, bool interleaved, cudaStream_t stream) {
+    constexpr int kRows = kThreads / (D / 16);    // tokens a block
+    const int heads = p.H + p.Hkv * (MODE == kPlain ? 1 : 2);
+    const unsigned tokens = (unsigned)((p.T + (long long)kRows - 1) / kRows);
+    // heads a thread: as many as leave blocks for every SM
+    const long long sms = device_sm_count() > 0 ? device_sm_count() : 152;
+    int each = 16;
+    while (each > 1 && (long long)tokens * ((heads + each - 1) / each) < 4 * sms) each /= 2;
+    p.heads_each = each;
+    const dim3 grid(tokens, (unsigned)((heads + each - 1) / each));
+    return interleaved ? launch_pdl(fa_rope_kernel<D, true, MODE>, grid, kThreads, 0, 1, stream, p)
+                       : launch_pdl(fa_rope_kernel<D, false, MODE>, grid, kThreads, 0, 1, stream, p);
+}
+
+template <int MODE>
+fa_status run(RopeParams& p, int d, bool interleaved, fa_stream_t stream) {
+    int dev;
+    DeviceStatus* status;
+    const fa_status st = ready_device(&dev, &status);
+    if (st != FA_OK) return st;
+    const cudaError_t e = d == 128 ? launch<128, MODE>(p, interleaved, (cudaStream_t)stream)
+                                   : launch<64, MODE>(p, interleaved, (cudaStream_t)stream);
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status check_rope(int B, int H, int Hkv, int N, int d, int rot, float amplitude,
+                     const int* positions, const unsigned long long* freqs) {
+    if (B < 1 || H < 1 || Hkv < 0 || N < 1 || d < 1 || rot < 1 || !std::isfinite(amplitude))
+        return FA_ERR_INVALID_ARG;
+    if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+    if (rot > d) return FA_ERR_INVALID_ARG;
+    if (rot % 16) return FA_ERR_UNSUPPORTED;
+    if ((long long)B * N >= (1LL << 31) - 256 || (long long)H + 2LL * Hkv >= 1 << 16)
+        return FA_ERR_UNSUPPORTED;
+    fa_status st = check_pointer(positions, alignof(int));
+    return st == FA_OK ? check_pointer(freqs, alignof(unsigned long long)) : st;
+}
+
+// A tensor of the call: its strides from the caller (b, h, n), or contiguous.
+fa_status rows_of(const void* p, const long long* strides, int B, int heads, int N, int d, bool out,
+                  Rows* r) {
+    const fa_status st = check_pointer(p, 16);
+    if (st != FA_OK) return st;
+    const int size[3] = {B, heads, N};
+    long long s[3] = {(long long)heads * N * d, (long long)N * d, d};
+    if (strides)
+        for (int i = 0; i < 3; ++i) {
+            s[i] = size[i] == 1 ? 0 : strides[i];
+            if (s[i] % 8) return FA_ERR_ALIGNMENT;
+            if (out && size[i] > 1 && s[i] == 0) return FA_ERR_INVALID_ARG;
+        }
+    *r = Rows{p, s[0], s[1], s[2]};
+    return FA_OK;
+}
+
+}  // namespace
+}  // namespace fa
+
+using namespace fa;
+
+extern "C" {
+
+fa_status fa_rope_freqs(unsigned long long* freqs, float* amplitude, int rot, double base,
+                        int scaling, double factor, int original_length, double beta_fast,
+                        double beta_slow) {
+    if (!freqs || !amplitude || rot < 2 || rot % 2 || !std::isfinite(base) || base <= 1.0)
+        return FA_ERR_INVALID_ARG;
+    if (scaling < FA_ROPE_NONE || scaling > FA_ROPE_PARTS) return FA_ERR_INVALID_ARG;
+    if (scaling != FA_ROPE_NONE && (!std::isfinite(factor) || factor < 1.0))
+        return FA_ERR_INVALID_ARG;
+    constexpr double kTurn = 6.283185307179586476925286766559;
+    double low = 0.0, high = 0.0;
+    *amplitude = 1.0f;
+    if (scaling == FA_ROPE_NTK && rot > 2) base *= std::pow(factor, rot / (rot - 2.0));
+    if (scaling == FA_ROPE_PARTS) {
+        if (original_length < 1 || !std::isfinite(beta_fast) || !std::isfinite(beta_slow) ||
+            beta_slow <= 0.0 || beta_fast < beta_slow)
+            return FA_ERR_INVALID_ARG;
+        // the pair that makes `turns` full turns over the original length
+        auto pair_of = [&](double turns) {
+            return rot * std::log(original_length / (turns * kTurn)) / (2.0 * std::log(base));
+        };
+        low = std::fmax(std::floor(pair_of(beta_fast)), 0.0);
+        high = std::fmin(std::ceil(pair_of(beta_slow)), rot - 1.0);
+        *amplitude = (float)(0.1 * std::log(factor) + 1.0);
+    }
+    for (int i = 0; i < rot / 2; ++i) {
+        double f = std::exp(-2.0 * i / rot * std::log(base));
+        if (scaling == FA_ROPE_LINEAR) f /= factor;
+        if (scaling == FA_ROPE_PARTS) {
+            const double ramp = std::fmin(std::fmax((i - low) / std::fmax(high - low, 0.001), 0.0), 1.0);
+            f = f * (1.0 - ramp) + f / factor * ramp;
+        }
+        freqs[i] = (unsigned long long)std::ldexp(f / kTurn, 64);   // f <= 1: below one turn
+    }
+    return FA_OK;
+}
+
+fa_status fa_rope(const void* q, const void* k, void* q_out, void* k_out, const int* positions,
+                  const unsigned long long* freqs, const long long* strides, int B, int H, int Hkv,
+                  int N, int d, int rot, int interleaved, int inverse, float amplitude,
+                  fa_stream_t stream) {
+    RopeParams p = {};
+    fa_status st = check_rope(B, H, Hkv, N, d, rot, amplitude, positions, freqs);
+    if (st == FA_OK) st = rows_of(q, strides, B, H, N, d, false, &p.q);
+    if (st == FA_OK) st = rows_of(q_out, strides ? strides + 6 : nullptr, B, H, N, d, true, &p.q_out);
+    if (st == FA_OK && Hkv) {
+        st = rows_of(k, strides ? strides + 3 : nullptr, B, Hkv, N, d, false, &p.k);
+        if (st == FA_OK)
+            st = rows_of(k_out, strides ? strides + 9 : nullptr, B, Hkv, N, d, true, &p.k_out);
+    }
+    if (st != FA_OK) return st;
+    p.positions = positions;
+    p.freqs = freqs;
+    p.B = B;
+    p.H = H;
+    p.Hkv = Hkv;
+    p.N = N;
+    p.T = B * N;
+    p.rot = rot;
+    p.inverse = inverse;
+    p.amplitude = amplitude;
+    return run<kPlain>(p, d, interleaved != 0, stream);
+}
+
+fa_status fa_rope_append(const void* q, const void* k, const void* v, void* q_out, void* k_pages,
+                         void* v_pages, float* kv_scales, const int* positions,
+                         const long long* slots, const unsigned long long* freqs,
+                         const long long* strides, int B, int H, int Hkv, int N, int n_pages,
+                         int page_size, int d, int rot, int interleaved, float amplitude,
+                         fa_stream_t stream) {
+    RopeParams p = {};
+    if (Hkv < 1 || n_pages < 1 || page_size < 1) return FA_ERR_INVALID_ARG;
+    fa_status st = check_rope(B, H, Hkv, N, d, rot, amplitude, positions, freqs);
+    if (st != FA_OK) return st;
+    if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1)) ||
+        (long long)n_pages * Hkv >= (1LL << 31))
+        return FA_ERR_UNSUPPORTED;
+    st = rows_of(q, strides, B, H, N, d, false, &p.q);
+    if (st == FA_OK) st = rows_of(k, strides ? strides + 3 : nullptr, B, Hkv, N, d, false, &p.k);
+    if (st == FA_OK) st = rows_of(v, strides ? strides + 6 : nullptr, B, Hkv, N, d, false, &p.v);
+    if (st == FA_OK) st = rows_of(q_out, strides ? strides + 9 : nullptr, B, H, N, d, true, &p.q_out);
+    if (st == FA_OK) st = check_pointer(k_pages, 16);
+    if (st == FA_OK) st = check_pointer(v_pages, 16);
+    if (st == FA_OK && kv_scales) st = check_pointer(kv_scales, 16);
+    if (st == FA_OK) st = check_pointer(slots, alignof(long long));
+    if (st != FA_OK) return st;
+    p.k_pages = k_pages;
+    p.v_pages = v_pages;
+    p.scales = kv_scales;
+    p.positions = positions;
+    p.slots = slots;
+    p.freqs = freqs;
+    p.n_slots = (long long)n_pages * page_size;
+    p.B = B;
+    p.H = H;
+    p.Hkv = Hkv;
+    p.N = N;
+    p.T = B * N;
+    p.rot = rot;
+    p.amplitude = amplitude;
+    while ((1 << p.ps_shift) < page_size) ++p.ps_shift;
+    return kv_scales ? run<kAppendF8>(p, d, interleaved != 0, stream)
+                     : run<kAppend>(p, d, interleaved != 0, stream);
+}
+
+}  // extern "C"

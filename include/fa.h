@@ -546,6 +546,126 @@ FA_API fa_status fa_fwd_decode_paged(const void* q, const void* k_pages, const v
                                      float scale, fa_stream_t stream);
 
 /*
+ * Block tables and slot maps on the GPU (this library's, like the cache itself).
+ * State of a pool, all DEVICE memory of the caller: block_table [B][max_pages],
+ * seqlens [B] (tokens of each sequence in the cache), and the free pages as a
+ * stack, free_pages [n_pages] of which the first *n_free are free.  A caller that
+ * keeps these fills the stack with 0 .. n_pages - 1 once; every step is a call on
+ * the GPU without a copy to the host.  B <= 4096, page_size a power of two from
+ * 16 to 256, max_pages * page_size < 2^30, B * max_pages < 2^30,
+ * (n_pages + B) * page_size < 2^31 (FA_ERR_UNSUPPORTED past these).  Lengths and
+ * n_free outside their ranges are clamped; whatever the entries hold, no access
+ * leaves the tensors.
+ *
+ * fa_kv_reserve makes room for new_tokens[b] more tokens of every sequence
+ * (negative counts as 0).  Sequence b needs the pages of its new length that its
+ * table does not have yet, and is served iff the table's max_pages hold them and
+ * it needs none, or the needs of sequences 0 .. b together (those whose table is
+ * too short left out) are at most n_free: in their order, until the pages run out.
+ * A served sequence gets counts[b] = max(new_tokens[b], 0), its pages from the
+ * stack's end, in order, and seqlens[b] += counts[b]; another one counts[b] = 0 and
+ * nothing else.  starts[b] = the tokens before the call; cu_seqlens [B + 1] = the
+ * running sums of counts.  These are what fa_kv_append and fa_kv_append_varlen
+ * take.
+ * positions, slots (both or neither null): the map of the new tokens, position
+ * starts[b] + i and slot page * page_size + row of the pool, as fa_rope_append
+ * takes them.  N >= 1: [B][N], row i of sequence b at b * N + i (rows past counts[b],
+ * which may be larger than N, get position 0 and slot -1; total is not used).  N = 0:
+ * packed [total], row i at cu_seqlens[b] + i (rows in no sequence get 0 and -1).
+ * One launch, two for maps of more than 65536 rows.
+ */
+FA_API fa_status fa_kv_reserve(int* block_table, int* seqlens, int* free_pages, int* n_free,
+                               const int* new_tokens, int* starts, int* counts, int* cu_seqlens,
+                               int* positions, long long* slots, int B, int N, int total,
+                               int n_pages, int page_size, int max_pages, fa_stream_t stream);
+
+/*
+ * Cuts every sequence back to its first keep[b] tokens (0: a finished one; fewer
+ * than there are: drafted tokens that were rejected; not fewer: nothing happens):
+ * the pages behind them go back to the stack, in the order of the sequences and of
+ * their pages, their entries become -1, and seqlens[b] = min(seqlens[b], keep[b]).
+ * pinned (may be null, DEVICE int32 [B]): the first pinned[b] pages of a sequence
+ * are not given back, only taken out of its table (a prefix that other tables
+ * hold too: a page that two tables give back would be handed out twice).  Errors
+ * as fa_kv_reserve().  One launch.
+ */
+FA_API fa_status fa_kv_release(int* block_table, int* seqlens, int* free_pages, int* n_free,
+                               const int* keep, const int* pinned, int B, int n_pages,
+                               int page_size, int max_pages, fa_stream_t stream);
+
+/*
+ * The map alone, of any table: rows i < counts[b] of sequence b at positions
+ * starts[b] + i into positions, slots [B][N]; rows behind them, and those whose
+ * position or page is outside the table, get position 0 or slot -1.  One launch.
+ */
+FA_API fa_status fa_kv_slots(const int* block_table, const int* starts, const int* counts,
+                             int* positions, long long* slots, int B, int N, int page_size,
+                             int max_pages, fa_stream_t stream);
+/* The same of a packed batch, [total] rows, sequence b at cu_seqlens[b]. */
+FA_API fa_status fa_kv_slots_varlen(const int* block_table, const int* starts,
+                                    const int* cu_seqlens, int* positions, long long* slots, int B,
+                                    int total, int page_size, int max_pages, fa_stream_t stream);
+
+/*
+ * Rotary positions (of q and k before the attention; the pages do not describe
+ * them, so all of this is the library's).  A row at position x has its pairs
+ * turned by the angle x * f_i: (a, b) -> amplitude * (a cos - b sin, b cos + a sin).
+ * Pair i is values i and i + rot / 2 of a row, or 2 i and 2 i + 1 where interleaved
+ * != 0; values from rot on are copied as they are.  rot is a multiple of 16 (up to
+ * d; FA_ERR_UNSUPPORTED otherwise).
+ *
+ * fa_rope_freqs fills the HOST array freqs [rot / 2] with f_i as fractions of a
+ * full turn in units of 2^-64 (so that a product with a position is exact modulo a
+ * turn; keep a DEVICE copy for the calls), and the amplitude that belongs to the
+ * scaling.  f_i = base^(-2 i / rot) radians a token, and for contexts `factor` >= 1
+ * times as long as the original_length that the model was trained on:
+ *   FA_ROPE_LINEAR  f_i / factor
+ *   FA_ROPE_NTK     base * factor^(rot / (rot - 2)) in the place of base
+ *   FA_ROPE_PARTS   f_i (1 - r_i) + f_i / factor r_i with the ramp r_i = clamp((i -
+ *                   lo) / (hi - lo), 0, 1) from lo = floor(i(beta_fast)) to hi =
+ *                   ceil(i(beta_slow)), i(n) = rot log(original_length / (2 pi n)) /
+ *                   (2 log base) the pair that makes n turns over the original
+ *                   length; amplitude 0.1 log(factor) + 1 (else 1)
+ * Reads and launches nothing on the GPU.
+ */
+enum { FA_ROPE_NONE = 0, FA_ROPE_LINEAR = 1, FA_ROPE_NTK = 2, FA_ROPE_PARTS = 3 };
+FA_API fa_status fa_rope_freqs(unsigned long long* freqs, float* amplitude, int rot, double base,
+                               int scaling, double factor, int original_length, double beta_fast,
+                               double beta_slow);
+
+/*
+ * q [B][H][N][d] and k [B][Hkv][N][d] (Hkv = 0: none) turned into q_out and k_out,
+ * bf16, computed in fp32; positions DEVICE int32 [B][N], any value.  inverse != 0
+ * turns the other way: with the gradients of q_out and k_out in the place of q and
+ * k the outputs are those of q and k.  A packed batch is B = 1, N = total.
+ * strides: HOST [12], the steps in elements along B, H and N of q, k, q_out, k_out,
+ * multiples of 8 (FA_ERR_ALIGNMENT otherwise; those along sizes of 1 are not used),
+ * rows themselves contiguous, as a projection's token-major output has them; null:
+ * all contiguous.  An output may be its input (with its strides).  B * N < 2^31 -
+ * 256, H + 2 Hkv < 2^16; d in {64, 128}.  One launch.
+ */
+FA_API fa_status fa_rope(const void* q, const void* k, void* q_out, void* k_out,
+                         const int* positions, const unsigned long long* freqs,
+                         const long long* strides, int B, int H, int Hkv, int N, int d, int rot,
+                         int interleaved, int inverse, float amplitude, fa_stream_t stream);
+
+/*
+ * A layer's new rows on their way into a paged cache: q turned into q_out, k turned
+ * into k_pages and v into v_pages, row (b, n) at slots[b][n] = page * page_size + row
+ * of the pool (DEVICE int64 [B][N], as fa_kv_reserve and fa_kv_slots write them;
+ * outside the pool: k and v are not written).  The pages as in fa_kv_append(); e4m3
+ * pages take the turned K unrounded (the row's scale and codes from its fp32
+ * values).  strides: HOST [12], of q, k, v, q_out, as in fa_rope().  q_out may be q.
+ * Different rows for one slot leave that place unspecified.  One launch.
+ */
+FA_API fa_status fa_rope_append(const void* q, const void* k, const void* v, void* q_out,
+                                void* k_pages, void* v_pages, float* kv_scales,
+                                const int* positions, const long long* slots,
+                                const unsigned long long* freqs, const long long* strides, int B,
+                                int H, int Hkv, int N, int n_pages, int page_size, int d, int rot,
+                                int interleaved, float amplitude, fa_stream_t stream);
+
+/*
  * Synchronizes `stream`, then reads and clears the device status word of the
  * current device: FA_OK, or the first error a kernel recorded (for example
  * FA_ERR_TIMEOUT when a bounded wait ran out).  Returns FA_ERR_CUDA if the
