@@ -39,7 +39,12 @@ __all__ = ["build", "lib", "LIB_PATH", "EXPORTS", "FAError", "fa_fwd", "fa_fwd_p
            "fa_kv_append", "fa_kv_append_varlen", "fa_kv_gather", "fa_kv_gather_varlen",
            "fa_fwd_decode_paged_workspace_size", "fa_fwd_decode_paged", "attention_decode_paged",
            "fa_kv_reserve", "fa_kv_release", "fa_kv_slots", "fa_kv_slots_varlen",
-           "rope_frequencies", "fa_rope", "rope", "fa_rope_append"]
+           "rope_frequencies", "fa_rope", "rope", "fa_rope_append",
+           "fa_fwd_cross_workspace_size", "fa_fwd_cross", "fa_fwd_cross_varlen",
+           "fa_bwd_cross_workspace_size", "fa_bwd_cross", "fa_bwd_cross_varlen",
+           "fa_fwd_cross_decode_workspace_size", "fa_fwd_cross_decode", "attention_cross",
+           "attention_cross_backward", "attention_cross_varlen",
+           "attention_cross_varlen_backward", "attention_cross_decode"]
 
 
 class FAError(RuntimeError):
@@ -468,6 +473,11 @@ class _Outputs:
     def __exit__(self, *exc):
         if self.ctx is not None:
             self.ctx.__exit__(*exc)
+
+    def kept(self, workspace):
+        """A workspace that may be the caller's: the call's stream is told to the allocator."""
+        if self.side is not None:
+            workspace.record_stream(self.side)
 
     def out(self, *tensors):
         import torch
@@ -960,6 +970,225 @@ def fa_rope_append(q, k, v, q_out, k_pages, v_pages, positions, slots, freqs,
                                 _scales(kv_scales, pool, cur), pp, slots.data_ptr(), fp, strides, B,
                                 H, pool[1], N, pool[0], pool[2], d, rot, 1 if interleaved else 0,
                                 float(amplitude), _stream(stream)), "fa_rope_append")
+
+
+# --------------------------------------- queries and keys of two lengths
+def fa_fwd_cross_workspace_size(B: int, H: int, Hkv: int, Nq: int, Nk: int, d: int) -> int:
+    return _bytes(lib().fa_fwd_cross_workspace_size, B, H, Hkv, Nq, Nk, d)
+
+
+def fa_bwd_cross_workspace_size(B: int, H: int, Hkv: int, Nq: int, Nk: int, d: int) -> int:
+    return _bytes(lib().fa_bwd_cross_workspace_size, B, H, Hkv, Nq, Nk, d)
+
+
+def fa_fwd_cross_decode_workspace_size(B: int, H: int, Hkv: int, Nq: int, Nk: int, d: int) -> int:
+    return _bytes(lib().fa_fwd_cross_decode_workspace_size, B, H, Hkv, Nq, Nk, d)
+
+
+def _cross_dims(q, k, kv_lens):
+    """Shapes of the query side, the key side and lse; B, H, Hkv, Nq, Nk, d; kv_lens' pointer."""
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q and k must be 4-D [B, H(kv), N, d]")
+    B, H, Nq, d = q.shape
+    Hkv, Nk = k.shape[1], k.shape[2]
+    if k.shape[0] != B or k.shape[3] != d:
+        raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)} disagree")
+    lens = None if kv_lens is None else _i32(kv_lens, "kv_lens", (B,))
+    return (B, H, Nq, d), (B, Hkv, Nk, d), (B, H, Nq), (B, H, Hkv, Nq, Nk, d), lens
+
+
+def _cross_varlen_dims(q, k, cu_q, cu_k, max_q, max_k):
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("packed q and k must be 3-D [H(kv), total, d]")
+    if cu_q.dim() != 1 or cu_k.shape != cu_q.shape:
+        raise ValueError("cu_q and cu_k must be 1-D [B + 1]")
+    H, total_q, d = q.shape
+    Hkv, total_k, dk = k.shape
+    if dk != d:
+        raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)} disagree")
+    sizes = (cu_q.numel() - 1, _c_int(max_q, "max_q"), _c_int(max_k, "max_k"), total_q, total_k, H,
+             Hkv, d)
+    return (H, total_q, d), (Hkv, total_k, d), (H, total_q), sizes, \
+        (_i32(cu_q, "cu_q"), _i32(cu_k, "cu_k"))
+
+
+def fa_fwd_cross(q, k, v, o, lse, workspace, causal: bool, scale: float, kv_lens=None,
+                 stream=None) -> None:
+    """q, o: bf16 [B, H, Nq, d]; k, v: bf16 [B, Hkv, Nk, d]; lse: fp32 [B, H, Nq]; kv_lens:
+    int32 [B], the keys of each sequence (default: Nk)."""
+    qs, ks, ls, sizes, lens = _cross_dims(q, k, kv_lens)
+    wp, wb = _ws(workspace)
+    _check(lib().fa_fwd_cross(_bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v", ks), _bf16(o, "o", qs),
+                              _f32(lse, "lse", ls), lens, wp, wb, *sizes, int(bool(causal)),
+                              float(scale), _stream(stream)), "fa_fwd_cross")
+
+
+def fa_bwd_cross(q, k, v, o, dout, lse, dq, dk, dv, workspace, causal: bool, scale: float,
+                 kv_lens=None, stream=None) -> None:
+    """The gradients of fa_fwd_cross."""
+    qs, ks, ls, sizes, lens = _cross_dims(q, k, kv_lens)
+    wp, wb = _ws(workspace)
+    _check(lib().fa_bwd_cross(_bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v", ks), _bf16(o, "o", qs),
+                              _bf16(dout, "dout", qs), _f32(lse, "lse", ls), _bf16(dq, "dq", qs),
+                              _bf16(dk, "dk", ks), _bf16(dv, "dv", ks), lens, wp, wb, *sizes,
+                              int(bool(causal)), float(scale), _stream(stream)), "fa_bwd_cross")
+
+
+def fa_fwd_cross_varlen(q, k, v, o, lse, workspace, cu_q, cu_k, max_q: int, max_k: int,
+                        causal: bool, scale: float, stream=None) -> None:
+    """Packed: q, o [H, total_q, d], k, v [Hkv, total_k, d], lse [H, total_q]; cu_q, cu_k int32
+    [B + 1]."""
+    qs, ks, ls, sizes, cu = _cross_varlen_dims(q, k, cu_q, cu_k, max_q, max_k)
+    wp, wb = _ws(workspace)
+    _check(lib().fa_fwd_cross_varlen(_bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v", ks),
+                                     _bf16(o, "o", qs), _f32(lse, "lse", ls), *cu, wp, wb, *sizes,
+                                     int(bool(causal)), float(scale), _stream(stream)),
+           "fa_fwd_cross_varlen")
+
+
+def fa_bwd_cross_varlen(q, k, v, o, dout, lse, dq, dk, dv, workspace, cu_q, cu_k, max_q: int,
+                        max_k: int, causal: bool, scale: float, stream=None) -> None:
+    """The gradients of fa_fwd_cross_varlen."""
+    qs, ks, ls, sizes, cu = _cross_varlen_dims(q, k, cu_q, cu_k, max_q, max_k)
+    wp, wb = _ws(workspace)
+    _check(lib().fa_bwd_cross_varlen(_bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v", ks),
+                                     _bf16(o, "o", qs), _bf16(dout, "dout", qs),
+                                     _f32(lse, "lse", ls), _bf16(dq, "dq", qs),
+                                     _bf16(dk, "dk", ks), _bf16(dv, "dv", ks), *cu, wp, wb, *sizes,
+                                     int(bool(causal)), float(scale), _stream(stream)),
+           "fa_bwd_cross_varlen")
+
+
+def fa_fwd_cross_decode(q, k, v, o, lse, workspace, causal: bool, scale: float, kv_lens=None,
+                        stream=None) -> None:
+    """fa_fwd_cross for a few queries a sequence, (H / Hkv) * Nq <= 32."""
+    import torch
+    bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    cur = _current_index()
+    qs, ks = q.shape, k.shape
+    if len(qs) != 4 or len(ks) != 4:
+        raise ValueError("q and k must be 4-D [B, H(kv), N, d]")
+    B, H, Nq, d = qs
+    if ks[0] != B or ks[3] != d:
+        raise ValueError(f"q {tuple(qs)} and k {tuple(ks)} disagree")
+    if not (q.dtype is bf and k.dtype is bf and v.dtype is bf and v.shape == ks and
+            o.dtype is bf and o.shape == qs and lse.dtype is f32 and lse.shape == (B, H, Nq) and
+            q.get_device() == cur and k.get_device() == cur and v.get_device() == cur and
+            o.get_device() == cur and lse.get_device() == cur and q.is_contiguous() and
+            k.is_contiguous() and v.is_contiguous() and o.is_contiguous() and
+            lse.is_contiguous() and
+            (kv_lens is None or (kv_lens.dtype is i32 and kv_lens.shape == (B,) and
+                                 kv_lens.get_device() == cur and kv_lens.is_contiguous()))):
+        _explain((q, "q", bf, qs), (k, "k", bf, ks), (v, "v", bf, ks), (o, "o", bf, qs),
+                 (lse, "lse", f32, (B, H, Nq)),
+                 *(() if kv_lens is None else ((kv_lens, "kv_lens", i32, (B,)),)))
+    if workspace.get_device() == cur and workspace.is_contiguous():
+        wp, wb = workspace.data_ptr(), workspace.nbytes
+    else:
+        wp, wb = _ws(workspace)
+    _check(lib().fa_fwd_cross_decode(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+                                     lse.data_ptr(),
+                                     None if kv_lens is None else kv_lens.data_ptr(), wp, wb, B, H,
+                                     ks[1], Nq, ks[2], d, 1 if causal else 0, float(scale),
+                                     _stream(stream)), "fa_fwd_cross_decode")
+
+
+def _workspace_of(size_of, where, *sizes):
+    import torch
+    n = size_of(*sizes)
+    if n == 0:
+        raise FAError(FA_ERR_UNSUPPORTED, where)
+    return torch.empty(n, dtype=torch.uint8, device="cuda")
+
+
+def attention_cross(q, k, v, kv_lens=None, causal: bool = False, scale: float | None = None,
+                    workspace=None, stream=None):
+    """Attention of q [B, H, Nq, d] to k, v [B, Hkv, Nk, d]; returns (o, lse)."""
+    import torch
+    B, H, Nq, d = _dims_of(q, "q")
+    _, Hkv, Nk, _ = _dims_of(k, "k")
+    scale = d ** -0.5 if scale is None else scale
+    with _Outputs(stream) as on:
+        o = torch.empty_like(q, memory_format=torch.contiguous_format)
+        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+        if workspace is None:
+            workspace = _workspace_of(fa_fwd_cross_workspace_size, "fa_fwd_cross_workspace_size",
+                                      B, H, Hkv, Nq, Nk, d)
+    fa_fwd_cross(q, k, v, o, lse, workspace, causal, scale, kv_lens, stream)
+    on.kept(workspace)
+    return on.out(o, lse)
+
+
+def attention_cross_backward(q, k, v, o, lse, dout, kv_lens=None, causal: bool = False,
+                             scale: float | None = None, workspace=None, stream=None):
+    """Returns (dq, dk, dv) for attention_cross."""
+    import torch
+    B, H, Nq, d = _dims_of(q, "q")
+    _, Hkv, Nk, _ = _dims_of(k, "k")
+    scale = d ** -0.5 if scale is None else scale
+    with _Outputs(stream) as on:
+        if workspace is None:
+            workspace = _workspace_of(fa_bwd_cross_workspace_size, "fa_bwd_cross_workspace_size",
+                                      B, H, Hkv, Nq, Nk, d)
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    fa_bwd_cross(q, k, v, o, dout, lse, dq, dk, dv, workspace, causal, scale, kv_lens, stream)
+    on.kept(workspace)
+    return on.out(dq, dk, dv)
+
+
+def attention_cross_varlen(q, k, v, cu_q, cu_k, max_q: int, max_k: int, causal: bool = False,
+                           scale: float | None = None, workspace=None, stream=None):
+    """Packed: q [H, total_q, d], k, v [Hkv, total_k, d]; returns (o, lse [H, total_q])."""
+    import torch
+    _, _, _, sizes, _ = _cross_varlen_dims(q, k, cu_q, cu_k, max_q, max_k)
+    B, mq, mk, _, _, H, Hkv, d = sizes
+    scale = d ** -0.5 if scale is None else scale
+    with _Outputs(stream) as on:
+        o = torch.empty_like(q, memory_format=torch.contiguous_format)
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        if workspace is None:
+            workspace = _workspace_of(fa_fwd_cross_workspace_size, "fa_fwd_cross_workspace_size",
+                                      B, H, Hkv, mq, mk, d)
+    fa_fwd_cross_varlen(q, k, v, o, lse, workspace, cu_q, cu_k, max_q, max_k, causal, scale, stream)
+    on.kept(workspace)
+    return on.out(o, lse)
+
+
+def attention_cross_varlen_backward(q, k, v, o, lse, dout, cu_q, cu_k, max_q: int, max_k: int,
+                                    causal: bool = False, scale: float | None = None,
+                                    workspace=None, stream=None):
+    """Returns (dq, dk, dv) for attention_cross_varlen."""
+    import torch
+    _, _, _, sizes, _ = _cross_varlen_dims(q, k, cu_q, cu_k, max_q, max_k)
+    B, mq, mk, _, _, H, Hkv, d = sizes
+    scale = d ** -0.5 if scale is None else scale
+    with _Outputs(stream) as on:
+        if workspace is None:
+            workspace = _workspace_of(fa_bwd_cross_workspace_size, "fa_bwd_cross_workspace_size",
+                                      B, H, Hkv, mq, mk, d)
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    fa_bwd_cross_varlen(q, k, v, o, dout, lse, dq, dk, dv, workspace, cu_q, cu_k, max_q, max_k,
+                        causal, scale, stream)
+    on.kept(workspace)
+    return on.out(dq, dk, dv)
+
+
+def attention_cross_decode(q, k, v, kv_lens=None, causal: bool = False, scale: float | None = None,
+                           workspace=None, stream=None):
+    """attention_cross for a few queries a sequence; returns (o, lse)."""
+    import torch
+    B, H, Nq, d = _dims_of(q, "q")
+    _, Hkv, Nk, _ = _dims_of(k, "k")
+    scale = d ** -0.5 if scale is None else scale
+    with _Outputs(stream) as on:
+        o = torch.empty_like(q, memory_format=torch.contiguous_format)
+        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+        if workspace is None:
+            workspace = _workspace_of(fa_fwd_cross_decode_workspace_size,
+                                      "fa_fwd_cross_decode_workspace_size", B, H, Hkv, Nq, Nk, d)
+    fa_fwd_cross_decode(q, k, v, o, lse, workspace, causal, scale, kv_lens, stream)
+    on.kept(workspace)
+    return on.out(o, lse)
 
 
 def attention(q, k, v, causal: bool = False, scale: float | None = None, stream=None,

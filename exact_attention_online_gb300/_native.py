@@ -20,7 +20,8 @@ OBJ_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(OUT_DIR, "libfa.so")
 
 SOURCES = ["api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_noalloc.cu", "fa_fp8.cu", "fa_decode.cu",
-           "fa_diag.cu", "fa_kvcache.cu", "fa_paged.cu", "fa_tables.cu", "fa_rope.cu"]
+           "fa_diag.cu", "fa_kvcache.cu", "fa_paged.cu", "fa_tables.cu", "fa_rope.cu",
+           "fa_cross.cu"]
 HEADERS = ["sm103_ptx.cuh", "fa_internal.h", "exp2_poly.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
@@ -183,6 +184,19 @@ def _bind(L: ctypes.CDLL) -> ctypes.CDLL:
     L.fa_rope.restype = i
     L.fa_rope_append.argtypes = [vp] * 11 + [i] * 9 + [f, vp]
     L.fa_rope_append.restype = i
+    for name in ("fa_fwd_cross", "fa_bwd_cross", "fa_fwd_cross_decode"):
+        size = getattr(L, name + "_workspace_size")
+        size.argtypes, size.restype = [i] * 6, sz
+    L.fa_fwd_cross.argtypes = [vp] * 7 + [sz] + [i] * 7 + [f, vp]
+    L.fa_fwd_cross.restype = i
+    L.fa_bwd_cross.argtypes = [vp] * 11 + [sz] + [i] * 7 + [f, vp]
+    L.fa_bwd_cross.restype = i
+    L.fa_fwd_cross_varlen.argtypes = [vp] * 8 + [sz] + [i] * 9 + [f, vp]
+    L.fa_fwd_cross_varlen.restype = i
+    L.fa_bwd_cross_varlen.argtypes = [vp] * 12 + [sz] + [i] * 9 + [f, vp]
+    L.fa_bwd_cross_varlen.restype = i
+    L.fa_fwd_cross_decode.argtypes = [vp] * 7 + [sz] + [i] * 7 + [f, vp]
+    L.fa_fwd_cross_decode.restype = i
     return L
 
 
@@ -216,4 +230,7 @@ EXPORTS = ["fa_fwd", "fa_fwd_precise", "fa_bwd_workspace_size", "fa_bwd", "fa_bw
            "fa_kv_append", "fa_kv_append_varlen", "fa_kv_gather", "fa_kv_gather_varlen",
            "fa_fwd_decode_paged_workspace_size", "fa_fwd_decode_paged",
            "fa_kv_reserve", "fa_kv_release", "fa_kv_slots", "fa_kv_slots_varlen",
-           "fa_rope_freqs", "fa_rope", "fa_rope_append"]
+           "fa_rope_freqs", "fa_rope", "fa_rope_append",
+           "fa_fwd_cross_workspace_size", "fa_fwd_cross", "fa_fwd_cross_varlen",
+           "fa_bwd_cross_workspace_size", "fa_bwd_cross", "fa_bwd_cross_varlen",
+           "fa_fwd_cross_decode_workspace_size", "fa_fwd_cross_decode"]

@@ -111,6 +111,13 @@ struct BwdParams {
     // cu_seqlens[b+1] - 1 of every head; N is then the longest sequence and
     // the workspace keeps N-row (padded) regions per (batch, head).
     const int* cu_seqlens;
+    // Keys of their own (CROSS): N, rows and cu_seqlens are the queries'; at most Nk
+    // keys a sequence, krows rows a head of k, v, dk, dv.  Padded batches: kv_lens[b]
+    // keys, or Nk (null); packed ones: rows cu_k[b] .. cu_k[b+1] - 1.  Otherwise Nk
+    // and krows are N and rows.
+    int Nk, krows;
+    const int* kv_lens;
+    const int* cu_k;
     float scale, scale_log2;
     const uint16_t* lse_ext;          // workspace tables (fa_internal.h)
     const uint16_t* d_ext;
@@ -137,14 +144,17 @@ struct BwdParams {
 // chunks of p.chunk heads at a time, sized so that a chunk's Q, dO and dQ
 // accumulator stay in L2 while its key blocks re-read them.
 struct BwdCta {
-    int jblk, b, g, bg, tok0, seq_len, z_kv, i_start, n_i, n_it;
-    bool idle;   // a key block past its packed sequence's end: nothing to do
+    int jblk, b, g, bg, z_kv, i_start, n_i, n_it;
+    int tok0, q_len;     // first query row of the sequence in its head, and their number
+    int ktok0, seq_len;  // the same of its keys
+    int off;             // query i sees keys j <= i + off under the causal mask
+    bool idle;   // a key block past its sequence's end: nothing to do
 };
-template <bool CAUSAL, bool WINDOW, bool VARLEN>
+template <bool CAUSAL, bool WINDOW, bool VARLEN, bool CROSS>
 __device__ __forceinline__ BwdCta bwd_cta(const BwdParams& p, int br, int item) {
     BwdCta c;
     constexpr bool kKeyMajor = CAUSAL && !VARLEN;
-    const int n_kblk = (p.N + kBN - 1) / kBN;
+    const int n_kblk = (p.Nk + kBN - 1) / kBN;
     const int n_bg = p.n_bg;                      // B * Hkv
     if (kKeyMajor) {
         const int chunk = item / (p.chunk * n_kblk), loc = item % (p.chunk * n_kblk);
@@ -160,11 +170,27 @@ __device__ __forceinline__ BwdCta bwd_cta(const BwdParams& p, int br, int item) 
     // The sequence: its first row in the tensors and its length.  Dense
     // batches address rows of head b*H(kv) + h; packed ones rows tok0 + i of
     // head h.
+    const bool packed = VARLEN || (CROSS && p.cu_seqlens);
     c.tok0 = 0;
-    c.seq_len = VARLEN ? packed_seq(p.cu_seqlens, c.b, p.N, p.rows, c.tok0) : p.N;
-    c.idle = VARLEN && c.jblk * kBN >= c.seq_len;
-    c.z_kv = VARLEN ? c.g : c.bg;
-    const int n_qblk = (c.seq_len + br - 1) / br;
+    c.q_len = packed ? packed_seq(p.cu_seqlens, c.b, p.N, p.rows, c.tok0) : p.N;
+    c.ktok0 = c.tok0;
+    c.seq_len = c.q_len;
+    if (CROSS) {
+        c.ktok0 = 0;
+        c.seq_len = packed      ? packed_seq(p.cu_k, c.b, p.Nk, p.krows, c.ktok0)
+                    : p.kv_lens ? min(max(__ldg(p.kv_lens + c.b), 0), p.Nk)
+                                : p.Nk;
+    }
+    c.off = CROSS ? c.seq_len - c.q_len : 0;
+    c.idle = (VARLEN || CROSS) && c.jblk * kBN >= c.seq_len;
+    c.z_kv = packed ? c.g : c.bg;
+    const int n_qblk = (c.q_len + br - 1) / br;
+    if (CROSS) {
+        c.i_start = p.causal ? max(0, c.jblk * kBN - c.off) / br : 0;
+        c.n_i = max(0, n_qblk - c.i_start);
+        c.n_it = p.G * c.n_i;
+        return c;
+    }
     // Query blocks that see some key of the block: rows 128 j .. 128 j + 127
     // + W - 1 under the causal (windowed) mask.
     c.i_start = CAUSAL ? (c.jblk * kBN) / br : 0;
@@ -203,9 +229,41 @@ __device__ __forceinline__ void bwd_fill_ones(uint8_t* sOnes, float scale_log2) 
     }
 }
 
+// Clears rows [from, rows) of a tile of `chunks` 128-byte-wide swizzled chunks, one row
+// a thread and turn, threads t of n.
+__device__ __forceinline__ void clear_rows(uint8_t* tile, int chunks, int rows, int from, int t,
+                                           int n) {
+    for (int r = max(from, 0) + t; r < rows; r += n)
+        for (int c = 0; c < chunks; ++c)
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                *reinterpret_cast<uint4*>(tile + c * (rows * 128) + r * 128 + u * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
+}
+
+// Zeros in dK and dV (columns [c_lo, c_hi) of this thread's key row) of a key block that
+// no query sees or that lies past a padded sequence's keys.
+template <int D>
+__device__ __forceinline__ void zero_grads(const BwdParams& p, const BwdCta& c, int key, int c_lo,
+                                           int c_hi, bool dk, bool dv) {
+    if (key >= (p.cu_seqlens ? c.seq_len : p.Nk)) return;
+    const size_t row = ((size_t)c.z_kv * p.krows + c.ktok0 + key) * D;
+    for (int e = c_lo; e < c_hi; e += 8) {
+        if (dk) *reinterpret_cast<uint4*>(p.dk + row + e) = make_uint4(0u, 0u, 0u, 0u);
+        if (dv) *reinterpret_cast<uint4*>(p.dv + row + e) = make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
 // WINDOW (with CAUSAL): the causal sliding window of p.window keys.
 // VARLEN: packed variable-length sequences (p.cu_seqlens).
-template <int D, bool CAUSAL, bool WINDOW, bool VARLEN>
+// CROSS: keys of another length than the queries (p.Nk, p.kv_lens, p.cu_k), padded or
+// packed, the causal mask by p.causal and counted from the last key.  Rows behind a
+// sequence may hold anything, and a weight of zero would not silence a NaN: K_j's
+// and V_j's rows past the keys are cleared by the compute warps before the item's
+// first MMA, Q_i's and dO_i's past a packed sequence's queries by warp 11 before the
+// MMAs learn that the step has landed.  Key rows that no query sees, and those of a
+// padded batch past its keys, get zeros in dK and dV.
+template <int D, bool CAUSAL, bool WINDOW, bool VARLEN, bool CROSS>
 __global__ void __launch_bounds__(kThreads, 1)
 fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -230,12 +288,17 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     // tensor memory (bar_acc_free) before the next item's MMAs overwrite them.
     __shared__ uint64_t bar_item_full[2], bar_item_empty[2], bar_acc_free;
     __shared__ int item_sh[2];
-    constexpr int kItemConsumers = kComputeWarps + 4 + (kTwoIssuers ? 2 : 1);
+    const int kItemConsumers =
+        kComputeWarps + 4 + (kTwoIssuers ? 2 : 1) + (CROSS && p.cu_seqlens ? 1 : 0);
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_sh;
     const WaitCtx wc{p.status, &abort_sh};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
+    const bool causal = CAUSAL || (CROSS && p.causal);
+    // CROSS, packed: a step's Q_i, dO_i have landed and their rows past the queries are
+    // cleared; the MMA issuers wait for these in the place of bar_full
+    __shared__ uint64_t bar_tail[2];
+    uint64_t* const bar_ready = CROSS && p.cu_seqlens ? bar_tail : bar_full;
 
     uint8_t* sK = smem + Cfg::kOffK;
     uint8_t* sV = smem + Cfg::kOffV;
@@ -257,6 +320,7 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         for (int s = 0; s < 2; ++s) {
             mbar_init(&bar_full[s], 1);
             mbar_init(&bar_empty[s], kTwoIssuers ? 2 : 1);   // every MMA issuer lets go of the stage
+            mbar_init(&bar_tail[s], 1);
         }
         mbar_init(&bar_s, 1);
         mbar_init(&bar_dp, 1);
@@ -316,11 +380,26 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         for (int n = 0; ok; ++n) {
             int item;
             if (!next_item_warp(n, item) || item < 0) break;
-            const BwdCta cta = bwd_cta<CAUSAL, WINDOW, VARLEN>(p, BR, item);
+            const BwdCta cta = bwd_cta<CAUSAL, WINDOW, VARLEN, CROSS>(p, BR, item);
+            if (CROSS && (cta.idle || cta.n_it == 0))
+                zero_grads<D>(p, cta, cta.jblk * kBN + rl, hf * (D / 2), (hf + 1) * (D / 2), true,
+                              true);
             if (cta.idle || cta.n_it == 0) continue;
-            const int jblk = cta.jblk, tok0 = cta.tok0, seq_len = cta.seq_len, z_kv = cta.z_kv;
+            const int jblk = cta.jblk, seq_len = cta.seq_len, z_kv = cta.z_kv;
             const int i_start = cta.i_start, n_i = cta.n_i, n_it = cta.n_it;
             const int key = jblk * kBN + rl;
+            if (CROSS) {   // bar_ktm: K_j's and V_j's rows past the keys are cleared
+                if (jblk * kBN + kBN > seq_len) {
+                    if (!fa_wait_warp(&bar_kv[nb % KVS], (nb / KVS) & 1, 64, wc)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* tile = (hf ? sV : sK) + (nb % KVS) * Cfg::kKVSlotBytes;
+                    clear_rows(tile, D / 64, kBN, seq_len - jblk * kBN, rl, kBN);
+                    fence_proxy_async_smem();
+                }
+                mbar_arrive(&bar_ktm);
+            }
             if (Cfg::kKInTmem) {
                 // K_j -> tensor memory: this thread's key row, the 64 head-dim
                 // columns of its half (one 128-byte swizzled row of chunk hf),
@@ -353,11 +432,11 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (!fa_wait_warp(&bar_s, git & 1, 61, wc)) { ok = false; break; }
                 tc_fence_after();
                 const int q0 = i * BR;
-                const bool need_mask = (CAUSAL && (q0 < jblk * kBN + kBN - 1 ||
+                const bool need_mask = (causal && (q0 + cta.off < jblk * kBN + kBN - 1 ||
                                                    (WINDOW && q0 + BR - 1 > jblk * kBN + p.window - 1))) ||
                                        (jblk * kBN + kBN > seq_len);
                 // column e visible iff key_lim <= e <= key_hi
-                const int key_lim = CAUSAL ? key - q0 : -1;
+                const int key_lim = causal ? key - cta.off - q0 : -1;
                 const int key_hi = WINDOW ? key + p.window - 1 - q0 : BR;
                 const bool key_valid = key < seq_len;
                 // P^T = 2^(S'^T c) with S'^T = S^T - LSE log2(e) / c from the
@@ -429,8 +508,9 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             // ---------------------------------------------------- dK, dV epilogue
             if (ok && fa_wait_warp(&bar_done, nb & 1, 63, wc)) {
                 tc_fence_after();
-                const bool valid = key < seq_len;
-                const size_t row = ((size_t)z_kv * p.rows + tok0 + (valid ? key : 0)) * D;
+                const bool there = key < seq_len;
+                const bool valid = there || (CROSS && !p.cu_seqlens && key < p.Nk);
+                const size_t row = ((size_t)z_kv * p.krows + cta.ktok0 + (valid ? key : 0)) * D;
                 const int c_lo = hf * (D / 2);
 #pragma unroll
                 for (int which = 0; which < 2; ++which) {
@@ -442,6 +522,9 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         uint32_t r[32];
                         tmem_ld32(lane_addr + col + c0, r);
                         tmem_ld_wait(r);
+                        if (CROSS && !there)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) r[e] = 0u;
                         if (valid) {
                             uint4* d4 = reinterpret_cast<uint4*>(dst + c0);
 #pragma unroll
@@ -483,7 +566,7 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         for (int n = 0; ok; ++n) {
             int item;
             if (!next_item_warp(n, item) || item < 0) break;
-            const BwdCta cta = bwd_cta<CAUSAL, WINDOW, VARLEN>(p, BR, item);
+            const BwdCta cta = bwd_cta<CAUSAL, WINDOW, VARLEN, CROSS>(p, BR, item);
             if (cta.idle || cta.n_it == 0) continue;
             const int b = cta.b, g = cta.g, i_start = cta.i_start, n_i = cta.n_i, n_it = cta.n_it;
             for (int it = 0; ok && it < n_it; ++it) {
@@ -567,7 +650,7 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         item_sh[slot] = item;
                         mbar_arrive(&bar_item_full[slot]);
                         if (item < 0) break;
-                        const BwdCta cta = bwd_cta<CAUSAL, WINDOW, VARLEN>(p, BR, item);
+                        const BwdCta cta = bwd_cta<CAUSAL, WINDOW, VARLEN, CROSS>(p, BR, item);
                         if (cta.idle || cta.n_it == 0) continue;
                         const int jblk = cta.jblk, b = cta.b, g = cta.g, tok0 = cta.tok0;
                         const int z_kv = cta.z_kv, i_start = cta.i_start, n_i = cta.n_i;
@@ -584,9 +667,9 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         mbar_arrive_expect_tx(&bar_kv[kvs], 2 * Cfg::kKVBytes);
                         for (int c = 0; c < D / 64; ++c) {
                             tma_load_3d(sk_ + c * (kBN * 128), &tm_k, &bar_kv[kvs], c * 64,
-                                        tok0 + jblk * kBN, z_kv);
+                                        cta.ktok0 + jblk * kBN, z_kv);
                             tma_load_3d(sv_ + c * (kBN * 128), &tm_v, &bar_kv[kvs], c * 64,
-                                        tok0 + jblk * kBN, z_kv);
+                                        cta.ktok0 + jblk * kBN, z_kv);
                         }
                         ++kv_issued;
                         for (int it = 0; it < n_it; ++it) {
@@ -599,7 +682,7 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             const int hq = g * p.G + it / n_i;
                             const int i = i_start + it % n_i;
                             const int bh = b * p.H + hq;
-                            const int z_q = VARLEN ? hq : bh;
+                            const int z_q = VARLEN || (CROSS && p.cu_seqlens) ? hq : bh;
                             mbar_arrive_expect_tx(&bar_full[st], Cfg::kStageBytes);
                             for (int c = 0; c < D / 64; ++c) {
                                 tma_load_3d(sQ + st * Cfg::kQBytes + c * (BR * 128), &tm_q,
@@ -672,7 +755,7 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     int item;
                     if (!next_item_thread(n, item)) { ok = false; break; }
                     if (item < 0) break;
-                    const BwdCta cta = bwd_cta<CAUSAL, WINDOW, VARLEN>(p, BR, item);
+                    const BwdCta cta = bwd_cta<CAUSAL, WINDOW, VARLEN, CROSS>(p, BR, item);
                     if (cta.idle || cta.n_it == 0) continue;
                     const int n_it = cta.n_it;
                     // K_j, V_j (and K_j in tensor memory) of this item, its first
@@ -806,7 +889,7 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 int item;
                 if (!next_item_thread(n, item)) { ok = false; break; }
                 if (item < 0) break;
-                const BwdCta cta = bwd_cta<CAUSAL, WINDOW, VARLEN>(p, BR, item);
+                const BwdCta cta = bwd_cta<CAUSAL, WINDOW, VARLEN, CROSS>(p, BR, item);
                 if (cta.idle || cta.n_it == 0) continue;
                 const int n_it = cta.n_it;
                 // K_j, V_j (and for half A K_j in tensor memory) of this item, its
@@ -816,8 +899,9 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 kd = sdesc_sw128(sk, 16, 1024);
                 vd = sdesc_sw128(smem_u32(sV) + kvs * Cfg::kKVSlotBytes, 16, 1024);
                 ok = fa_wait(&bar_kv[kvs], (nb / KVS) & 1, 50, wc) &&
-                     fa_wait(&bar_full[gi & 1], (gi >> 1) & 1, 51, wc) &&
-                     (!(Cfg::kKInTmem && half_a) || fa_wait(&bar_ktm, nb & 1, 57, wc)) &&
+                     fa_wait(&bar_ready[gi & 1], (gi >> 1) & 1, 51, wc) &&
+                     (!(CROSS || (Cfg::kKInTmem && half_a)) ||
+                      fa_wait(&bar_ktm, nb & 1, 57, wc)) &&
                      (nb == 0 || fa_wait(&bar_acc_free, (nb - 1) & 1, 58, wc));
                 if (ok) {
                     tc_fence_after();
@@ -843,7 +927,7 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         }
                         mma_commit(&bar_empty[st]);      // half A is done with Q_i, dO_i
                         if (next) {
-                            if (!fa_wait(&bar_full[st1], ((git + 1) >> 1) & 1, 54, wc)) { ok = false; break; }
+                            if (!fa_wait(&bar_ready[st1], ((git + 1) >> 1) & 1, 54, wc)) { ok = false; break; }
                             tc_fence_after();
                             issue_s(st1);
                         }
@@ -872,7 +956,7 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                                    id_dq, kk > 0);
                         mma_commit(&bar_dq_full);
                         if (next) {
-                            if (!fa_wait(&bar_full[st1], ((git + 1) >> 1) & 1, 56, wc)) { ok = false; break; }
+                            if (!fa_wait(&bar_ready[st1], ((git + 1) >> 1) & 1, 56, wc)) { ok = false; break; }
                             tc_fence_after();
                             issue_dp(st1);
                         }
@@ -896,6 +980,30 @@ fa_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
           }
           __syncwarp();   // reconverge before the block-wide barrier below
+        } else if (CROSS && warp == 11 && p.cu_seqlens) {
+            // --------------------- Q_i, dO_i rows past a packed sequence's queries
+            bool ok = true;
+            int gi = 0;
+            for (int n = 0; ok; ++n) {
+                int item;
+                if (!next_item_warp(n, item) || item < 0) break;
+                const BwdCta cta = bwd_cta<CAUSAL, WINDOW, VARLEN, CROSS>(p, BR, item);
+                if (cta.idle || cta.n_it == 0) continue;
+                for (int it = 0; it < cta.n_it; ++it) {
+                    const int git = gi + it;
+                    const int st = git & 1;
+                    if (!fa_wait_warp(&bar_full[st], (git >> 1) & 1, 67, wc)) { ok = false; break; }
+                    const int left = cta.q_len - (cta.i_start + it % cta.n_i) * BR;
+                    if (left < BR) {
+                        clear_rows(sQ + st * Cfg::kQBytes, D / 64, BR, left, lane, 32);
+                        clear_rows(sDO + st * Cfg::kQBytes, D / 64, BR, left, lane, 32);
+                        fence_proxy_async_smem();
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar_tail[st]);
+                }
+                gi += cta.n_it;
+            }
         }
     }
 
@@ -965,6 +1073,8 @@ fa_bwd_pre_kernel(const OT* __restrict__ o, const __nv_bfloat16* __restrict__ do
         const bool used = in && i < (len + kRowPad - 1) / kRowPad * kRowPad;
         float x = -1e30f;
         if (FULL && valid) x = -lse[base + i] * 1.4426950408889634f;
+        // a row that sees no key (LSE = -infinity): P = 0 like a padded one
+        if (x == CUDART_INF_F) x = -1e30f;
         float acc = 0.0f;
         if (valid) {
             const long long src = (base + i) * D + sl * 8;
@@ -1102,11 +1212,11 @@ int grid_for(long long work_items, int per_block) {
     return (int)blocks;
 }
 
-template <int D, bool CAUSAL, bool WINDOW = false, bool VARLEN = false>
+template <int D, bool CAUSAL, bool WINDOW = false, bool VARLEN = false, bool CROSS = false>
 cudaError_t launch_dkdv_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                           const CUtensorMap& tdo, const CUtensorMap& tdq, const BwdParams& p,
                           int grid, cudaStream_t stream) {
-    auto kern = fa_bwd_dkdv_kernel<D, CAUSAL, WINDOW, VARLEN>;
+    auto kern = fa_bwd_dkdv_kernel<D, CAUSAL, WINDOW, VARLEN, CROSS>;
     using Cfg = BwdCfg<D, (D == 64 && CAUSAL)>;
     static int configured_device = -1;
     int dev = 0;
@@ -1186,7 +1296,7 @@ struct Bwd2Cfg {
 };
 static_assert(Bwd2Cfg::kSmemAlloc <= 227 * 1024 - 1024, "shared memory of the two-pipeline kernel");
 
-template <bool CAUSAL, bool WINDOW, bool VARLEN>
+template <bool CAUSAL, bool WINDOW, bool VARLEN, bool CROSS>
 __global__ void __launch_bounds__(kThreads, 1)
 fa_bwd_dkdv2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -1206,11 +1316,15 @@ fa_bwd_dkdv2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     __shared__ uint64_t bar_dv_turn, bar_dk_turn;
     __shared__ uint64_t bar_item_full[2], bar_item_empty[2];
     __shared__ int item_sh[2];
-    constexpr int kItemConsumers = kComputeWarps + 4 + 2;
+    const int kItemConsumers = kComputeWarps + 4 + 2 + (CROSS && p.cu_seqlens ? 1 : 0);
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_sh;
     const WaitCtx wc{p.status, &abort_sh};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool causal = CAUSAL || (CROSS && p.causal);
+    // as in the kernel above
+    __shared__ uint64_t bar_tail[2 * NS];
+    uint64_t* const bar_ready = CROSS && p.cu_seqlens ? bar_tail : bar_full;
 
     uint8_t* sK = smem + Cfg::kOffK;
     uint8_t* sV = smem + Cfg::kOffV;
@@ -1227,7 +1341,10 @@ fa_bwd_dkdv2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         abort_sh = 0;
         mbar_init(&bar_kv, 1);
         mbar_init(&bar_kv_free, 2);                  // one commit per MMA issuer
-        for (int s = 0; s < 2 * NS; ++s) mbar_init(&bar_full[s], 1);
+        for (int s = 0; s < 2 * NS; ++s) {
+            mbar_init(&bar_full[s], 1);
+            mbar_init(&bar_tail[s], 1);
+        }
         for (int s = 0; s < NS; ++s) mbar_init(&bar_empty[s], 1);   // the step's MMA issuer
         for (int q = 0; q < 2; ++q) {
             mbar_init(&bar_s[q], 1);
@@ -1286,11 +1403,19 @@ fa_bwd_dkdv2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         for (int n = 0; ok; ++n) {
             int item;
             if (!next_item_warp(n, item) || item < 0) break;
-            const BwdCta cta = bwd_cta<CAUSAL, WINDOW, VARLEN>(p, BR, item);
+            const BwdCta cta = bwd_cta<CAUSAL, WINDOW, VARLEN, CROSS>(p, BR, item);
+            if (CROSS && (cta.idle || cta.n_it == 0))
+                zero_grads<D>(p, cta, cta.jblk * kBN + rl, 0, D, !cp, cp);
             if (cta.idle || cta.n_it == 0) continue;
-            const int jblk = cta.jblk, tok0 = cta.tok0, seq_len = cta.seq_len, z_kv = cta.z_kv;
+            const int jblk = cta.jblk, seq_len = cta.seq_len, z_kv = cta.z_kv;
             const int i_start = cta.i_start, n_i = cta.n_i, n_it = cta.n_it;
             const int key = jblk * kBN + rl;
+            if (CROSS && jblk * kBN + kBN > seq_len) {
+                // K_j's (V_j's) rows past the keys: cleared before bar_acc_free
+                if (!fa_wait_warp(&bar_kv, nb & 1, 64, wc)) { ok = false; break; }
+                clear_rows(cp ? sV : sK, D / 64, kBN, seq_len - jblk * kBN, rl, kBN);
+                fence_proxy_async_smem();
+            }
             // dK (pipeline 0's warps) and dV (pipeline 1's) of this item start
             // from zero; the previous item's were read out below
             {
@@ -1311,10 +1436,10 @@ fa_bwd_dkdv2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 if (!fa_wait_warp(&bar_s[cp], k & 1, 61, wc)) { ok = false; break; }
                 tc_fence_after();
                 const int q0 = i * BR;
-                const bool need_mask = (CAUSAL && (q0 < jblk * kBN + kBN - 1 ||
+                const bool need_mask = (causal && (q0 + cta.off < jblk * kBN + kBN - 1 ||
                                                    (WINDOW && q0 + BR - 1 > jblk * kBN + p.window - 1))) ||
                                        (jblk * kBN + kBN > seq_len);
-                const int key_lim = CAUSAL ? key - q0 : -1;
+                const int key_lim = causal ? key - cta.off - q0 : -1;
                 const int key_hi = WINDOW ? key + p.window - 1 - q0 : BR;
                 const bool key_valid = key < seq_len;
                 // P^T = 2^(S'^T c), S'^T = S^T - LSE log2(e) / c from the tensor
@@ -1386,8 +1511,9 @@ fa_bwd_dkdv2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             // ---------------------------------------------------- dK, dV epilogue
             if (ok && fa_wait_warp(&bar_done, nb & 1, 63, wc)) {
                 tc_fence_after();
-                const bool valid = key < seq_len;
-                const size_t row = ((size_t)z_kv * p.rows + tok0 + (valid ? key : 0)) * D;
+                const bool there = key < seq_len;
+                const bool valid = there || (CROSS && !p.cu_seqlens && key < p.Nk);
+                const size_t row = ((size_t)z_kv * p.krows + cta.ktok0 + (valid ? key : 0)) * D;
                 const uint32_t col = cp ? Cfg::kColDV : Cfg::kColDK;
                 const float mul = cp ? 1.0f : p.scale;
                 __nv_bfloat16* dst = (cp ? p.dv : p.dk) + row;
@@ -1396,6 +1522,9 @@ fa_bwd_dkdv2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     uint32_t r[32];
                     tmem_ld32(lane_addr + col + c0, r);
                     tmem_ld_wait(r);
+                    if (CROSS && !there)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) r[e] = 0u;
                     if (valid) {
                         uint4* d4 = reinterpret_cast<uint4*>(dst + c0);
 #pragma unroll
@@ -1433,7 +1562,7 @@ fa_bwd_dkdv2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         for (int n = 0; ok; ++n) {
             int item;
             if (!next_item_warp(n, item) || item < 0) break;
-            const BwdCta cta = bwd_cta<CAUSAL, WINDOW, VARLEN>(p, BR, item);
+            const BwdCta cta = bwd_cta<CAUSAL, WINDOW, VARLEN, CROSS>(p, BR, item);
             if (cta.idle || cta.n_it == 0) continue;
             const int b = cta.b, g = cta.g, i_start = cta.i_start, n_i = cta.n_i, n_it = cta.n_it;
             for (int it = 0; ok && it < n_it; ++it) {
@@ -1495,7 +1624,7 @@ fa_bwd_dkdv2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     item_sh[slot] = item;
                     mbar_arrive(&bar_item_full[slot]);
                     if (item < 0) break;
-                    const BwdCta cta = bwd_cta<CAUSAL, WINDOW, VARLEN>(p, BR, item);
+                    const BwdCta cta = bwd_cta<CAUSAL, WINDOW, VARLEN, CROSS>(p, BR, item);
                     if (cta.idle || cta.n_it == 0) continue;
                     const int jblk = cta.jblk, b = cta.b, g = cta.g, tok0 = cta.tok0;
                     const int z_kv = cta.z_kv, i_start = cta.i_start, n_i = cta.n_i;
@@ -1504,10 +1633,10 @@ fa_bwd_dkdv2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     if (nb > 0 && !fa_wait(&bar_kv_free, (nb - 1) & 1, 42, wc)) break;
                     mbar_arrive_expect_tx(&bar_kv, 2 * Cfg::kKVBytes);
                     for (int c = 0; c < D / 64; ++c) {
-                        tma_load_3d(sK + c * (kBN * 128), &tm_k, &bar_kv, c * 64, tok0 + jblk * kBN,
-                                    z_kv);
-                        tma_load_3d(sV + c * (kBN * 128), &tm_v, &bar_kv, c * 64, tok0 + jblk * kBN,
-                                    z_kv);
+                        tma_load_3d(sK + c * (kBN * 128), &tm_k, &bar_kv, c * 64,
+                                    cta.ktok0 + jblk * kBN, z_kv);
+                        tma_load_3d(sV + c * (kBN * 128), &tm_v, &bar_kv, c * 64,
+                                    cta.ktok0 + jblk * kBN, z_kv);
                     }
                     ++kv_issued;
                     for (int it = 0; it < n_it; ++it) {
@@ -1520,7 +1649,7 @@ fa_bwd_dkdv2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                         const int hq = g * p.G + it / n_i;
                         const int i = i_start + it % n_i;
                         const int bh = b * p.H + hq;
-                        const int z_q = VARLEN ? hq : bh;
+                        const int z_q = VARLEN || (CROSS && p.cu_seqlens) ? hq : bh;
                         uint64_t* full = &bar_full[git % (2 * NS)];
                         mbar_arrive_expect_tx(full, Cfg::kStepBytes);
                         for (int c = 0; c < D / 64; ++c) {
@@ -1571,7 +1700,7 @@ fa_bwd_dkdv2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     int item;
                     if (!next_item_thread(n, item)) { ok = false; break; }
                     if (item < 0) break;
-                    const BwdCta cta = bwd_cta<CAUSAL, WINDOW, VARLEN>(p, BR, item);
+                    const BwdCta cta = bwd_cta<CAUSAL, WINDOW, VARLEN, CROSS>(p, BR, item);
                     if (cta.idle || cta.n_it == 0) continue;
                     const int n_it = cta.n_it;
                     // Every per-item phase is waited on by both issuers, whether
@@ -1582,7 +1711,7 @@ fa_bwd_dkdv2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                         const int git = gi + it;
                         const uint32_t k = (uint32_t)git >> 1;
                         const int st = git % NS;
-                        if (!fa_wait(&bar_full[git % (2 * NS)], (git / (2 * NS)) & 1, 51, wc)) {
+                        if (!fa_wait(&bar_ready[git % (2 * NS)], (git / (2 * NS)) & 1, 51, wc)) {
                             ok = false;
                             break;
                         }
@@ -1671,6 +1800,33 @@ fa_bwd_dkdv2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 }
             }
             __syncwarp();
+        } else if (CROSS && warp == 11 && p.cu_seqlens) {
+            // --------------------- Q_i, dO_i rows past a packed sequence's queries
+            bool ok = true;
+            int gi = 0;
+            for (int n = 0; ok; ++n) {
+                int item;
+                if (!next_item_warp(n, item) || item < 0) break;
+                const BwdCta cta = bwd_cta<CAUSAL, WINDOW, VARLEN, CROSS>(p, BR, item);
+                if (cta.idle || cta.n_it == 0) continue;
+                for (int it = 0; it < cta.n_it; ++it) {
+                    const int git = gi + it;
+                    const int st = git % NS;
+                    if (!fa_wait_warp(&bar_full[git % (2 * NS)], (git / (2 * NS)) & 1, 67, wc)) {
+                        ok = false;
+                        break;
+                    }
+                    const int left = cta.q_len - (cta.i_start + it % cta.n_i) * BR;
+                    if (left < BR) {
+                        clear_rows(sQ + st * Cfg::kQBytes, D / 64, BR, left, lane, 32);
+                        clear_rows(sDO + st * Cfg::kQBytes, D / 64, BR, left, lane, 32);
+                        fence_proxy_async_smem();
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar_tail[git % (2 * NS)]);
+                }
+                gi += cta.n_it;
+            }
         }
     }
 
@@ -1682,11 +1838,11 @@ fa_bwd_dkdv2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     }
 }
 
-template <bool CAUSAL, bool WINDOW = false, bool VARLEN = false>
+template <bool CAUSAL, bool WINDOW = false, bool VARLEN = false, bool CROSS = false>
 cudaError_t launch_dkdv2_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                            const CUtensorMap& tdo, const BwdParams& p, int grid,
                            cudaStream_t stream) {
-    auto kern = fa_bwd_dkdv2_kernel<CAUSAL, WINDOW, VARLEN>;
+    auto kern = fa_bwd_dkdv2_kernel<CAUSAL, WINDOW, VARLEN, CROSS>;
     static int configured_device = -1;
     int dev = 0;
     cudaGetDevice(&dev);
@@ -1743,12 +1899,14 @@ cudaError_t launch_bwd_dkdv(const Shape& s, const void* q, const void* k, const 
     const int br = (s.d == 128) ? BwdCfg<128>::kBR : BwdCfg<64>::kBR;
     const bool varlen = s.cu_seqlens != nullptr;
     const int rows = varlen ? s.total : s.N;
+    const bool cross = s.Nk > 0;
+    const int krows = !cross ? rows : varlen ? s.total_k : s.Nk;
     const int zq = varlen ? s.H : s.B * s.H, zkv = varlen ? s.Hkv : s.B * s.Hkv;
     CUtensorMap tq, tk, tv, tdo, tdq;
     if (!make_tmap_bf16_3d(&tq, q, s.d, rows, zq, br) ||
         !make_tmap_bf16_3d(&tdo, dout, s.d, rows, zq, br) ||
-        !make_tmap_bf16_3d(&tk, k, s.d, rows, zkv, kBN) ||
-        !make_tmap_bf16_3d(&tv, v, s.d, rows, zkv, kBN) ||
+        !make_tmap_bf16_3d(&tk, k, s.d, krows, zkv, kBN) ||
+        !make_tmap_bf16_3d(&tv, v, s.d, krows, zkv, kBN) ||
         !make_tmap_f32_2d(&tdq, ws.dq_acc, s.d, (long long)s.B * s.H * padded_rows(s.N), 32, br))
         return cudaErrorInvalidValue;
     BwdParams p;
@@ -1758,6 +1916,10 @@ cudaError_t launch_bwd_dkdv(const Shape& s, const void* q, const void* k, const 
     p.Np = padded_rows(s.N);
     p.rows = rows;
     p.cu_seqlens = s.cu_seqlens;
+    p.Nk = cross ? s.Nk : s.N;
+    p.krows = krows;
+    p.kv_lens = s.kv_lens;
+    p.cu_k = s.cu_k;
     p.G = s.H / s.Hkv;
     // Chunk size: what fits a 64 MB L2 budget of Q, dO (bf16) and dQ
     // accumulator (fp32) rows, 8 G N d bytes per key/value head, but at least
@@ -1785,7 +1947,7 @@ cudaError_t launch_bwd_dkdv(const Shape& s, const void* q, const void* k, const 
     p.dv = static_cast<__nv_bfloat16*>(dv);
     p.status = status;
     p.work = ws.work;
-    const int n_kblk = (s.N + kBN - 1) / kBN;
+    const int n_kblk = (p.Nk + kBN - 1) / kBN;
     p.n_bg = s.B * s.Hkv;
     p.n_items = n_kblk * s.B * s.Hkv;
     // Persistent: one CTA per SM (fewer when there are fewer work items),
@@ -1793,6 +1955,12 @@ cudaError_t launch_bwd_dkdv(const Shape& s, const void* q, const void* k, const 
     const int sms = device_sm_count() > 0 ? device_sm_count() : 148;
     const int grid = p.n_items < sms ? p.n_items : sms;
     count_launch();
+    if (cross) {   // keys of another length (no window)
+        if (s.window > 0) return cudaErrorInvalidValue;
+        return s.d == 128 ? launch_dkdv2_t<false, false, false, true>(tq, tk, tv, tdo, p, grid, stream)
+                          : launch_dkdv_t<64, false, false, false, true>(tq, tk, tv, tdo, tdq, p,
+                                                                         grid, stream);
+    }
     if (varlen) {   // packed variable-length sequences (no window)
         if (s.window > 0) return cudaErrorInvalidValue;
         if (s.d == 128)

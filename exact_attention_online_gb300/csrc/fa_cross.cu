@@ -1,0 +1,217 @@
+// Entry points of attention to keys of another length than the queries (declared in
+// include/fa.h): argument checks and the launches of the forward, backward and
+// decoding kernels in their forms for two lengths.
+#include <cmath>
+
+#include "fa_internal.h"
+
+namespace fa {
+namespace {
+
+constexpr long long kMost = 1LL << 31;
+
+fa_status check_cross_shape(int B, int H, int Hkv, int Nq, int Nk, int d) {
+    if (B < 1 || H < 1 || Hkv < 1 || Nq < 1 || Nk < 1 || d < 1 || H % Hkv != 0)
+        return FA_ERR_INVALID_ARG;
+    if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+    // (sizes are below 2^31: three of them need a look at every product)
+    const long long q = (long long)B * H, k = (long long)B * Hkv;
+    const long long nq = (Nq + 127LL) / 128 * 128, nk = (Nk + 127LL) / 128 * 128;
+    if (q >= kMost || q * nq >= kMost || q * nq * d >= kMost || k * nk >= kMost)
+        return FA_ERR_UNSUPPORTED;
+    return FA_OK;
+}
+
+// Rows of k and v in all, of a padded or a packed batch.
+fa_status check_rows(long long heads, long long rows, int d) {
+    return heads * rows >= kMost || heads * rows * d >= kMost ? FA_ERR_UNSUPPORTED : FA_OK;
+}
+
+fa_status check_all(std::initializer_list<const void*> tensors) {
+    for (const void* t : tensors) {
+        const fa_status st = check_pointer(t, 16);
+        if (st != FA_OK) return st;
+    }
+    return FA_OK;
+}
+
+fa_status check_workspace(const void* ws, size_t bytes, size_t need) {
+    if (!ws) return FA_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(ws) % 256 != 0) return FA_ERR_ALIGNMENT;
+    return bytes < need ? FA_ERR_WORKSPACE : FA_OK;
+}
+
+bool bad_scale(float scale) { return !std::isfinite(scale) || scale <= 0.0f; }
+
+// What the padded and the packed calls share once their sizes are in `s`.
+fa_status forward(const Shape& s, const void* q, const void* k, const void* v, void* o, float* lse,
+                  void* workspace, size_t workspace_bytes, fa_stream_t stream) {
+    fa_status st = check_all({q, k, v, o, lse});
+    if (st != FA_OK) return st;
+    if (bad_scale(s.scale)) return FA_ERR_INVALID_ARG;
+    if ((st = check_workspace(workspace, workspace_bytes, cross_fwd_workspace_bytes(s))) != FA_OK)
+        return st;
+    int dev;
+    DeviceStatus* status;
+    if ((st = ready_device(&dev, &status)) != FA_OK) return st;
+    return launch_fwd(s, q, k, v, o, lse, false, status, (cudaStream_t)stream) == cudaSuccess
+               ? FA_OK
+               : FA_ERR_CUDA;
+}
+
+fa_status backward(const Shape& s, const void* q, const void* k, const void* v, const void* o,
+                   const void* dout, const float* lse, void* dq, void* dk, void* dv,
+                   void* workspace, size_t workspace_bytes, fa_stream_t stream) {
+    fa_status st = check_all({q, k, v, o, dout, lse, dq, dk, dv});
+    if (st != FA_OK) return st;
+    if (bad_scale(s.scale)) return FA_ERR_INVALID_ARG;
+    if ((st = check_workspace(workspace, workspace_bytes, bwd_workspace_bytes(s))) != FA_OK)
+        return st;
+    int dev;
+    DeviceStatus* status;
+    if ((st = ready_device(&dev, &status)) != FA_OK) return st;
+    const BwdWorkspace ws = bwd_workspace_carve(workspace, s);
+    cudaStream_t cs = (cudaStream_t)stream;
+    cudaError_t e = launch_bwd_preprocess(s, o, false, dout, lse, ws, status, cs);
+    if (e == cudaSuccess) e = launch_bwd_dkdv(s, q, k, v, dout, dk, dv, ws, status, cs);
+    if (e == cudaSuccess) e = launch_bwd_dq_convert(s, ws, dq, cs);
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status padded(Shape* s, const int* kv_lens, int B, int H, int Hkv, int Nq, int Nk, int d,
+                 int causal, float scale) {
+    fa_status st = check_cross_shape(B, H, Hkv, Nq, Nk, d);
+    if (st == FA_OK) st = check_rows((long long)B * Hkv, Nk, d);
+    if (st == FA_OK && kv_lens) st = check_pointer(kv_lens, alignof(int));
+    if (st != FA_OK) return st;
+    *s = Shape{B, H, Hkv, Nq, d, causal ? 1 : 0, scale};
+    s->Nk = Nk;
+    s->kv_lens = kv_lens;
+    return FA_OK;
+}
+
+fa_status packed(Shape* s, const int* cu_q, const int* cu_k, int B, int max_q, int max_k,
+                 int total_q, int total_k, int H, int Hkv, int d, int causal, float scale) {
+    fa_status st = check_cross_shape(B, H, Hkv, max_q, max_k, d);
+    if (st != FA_OK) return st;
+    if (total_q < 1 || total_k < 1) return FA_ERR_INVALID_ARG;
+    if ((st = check_rows(H, total_q, d)) != FA_OK || (st = check_rows(Hkv, total_k, d)) != FA_OK ||
+        (st = check_pointer(cu_q, alignof(int))) != FA_OK ||
+        (st = check_pointer(cu_k, alignof(int))) != FA_OK)
+        return st;
+    *s = Shape{B, H, Hkv, max_q, d, causal ? 1 : 0, scale};
+    s->cu_seqlens = cu_q;
+    s->total = total_q;
+    s->Nk = max_k;
+    s->cu_k = cu_k;
+    s->total_k = total_k;
+    return FA_OK;
+}
+
+fa_status check_decode(int B, int H, int Hkv, int Nq, int Nk, int d) {
+    const fa_status st = check_cross_shape(B, H, Hkv, Nq, Nk, d);
+    if (st != FA_OK) return st;
+    if ((long long)(H / Hkv) * Nq > kPagedMaxRows || Nk >= 1 << 30 ||
+        (long long)B * Hkv * (Nk / 128 + 2) > 1LL << 30)
+        return FA_ERR_UNSUPPORTED;
+    return FA_OK;
+}
+
+}  // namespace
+
+size_t cross_fwd_workspace_bytes(const Shape&) { return 256; }
+
+}  // namespace fa
+
+using namespace fa;
+
+extern "C" {
+
+size_t fa_fwd_cross_workspace_size(int B, int H, int Hkv, int Nq, int Nk, int d) {
+    if (check_cross_shape(B, H, Hkv, Nq, Nk, d) != FA_OK) return 0;
+    Shape s{B, H, Hkv, Nq, d, 0, 1.0f};
+    s.Nk = Nk;
+    return cross_fwd_workspace_bytes(s);
+}
+
+fa_status fa_fwd_cross(const void* q, const void* k, const void* v, void* o, float* lse,
+                       const int* kv_lens, void* workspace, size_t workspace_bytes, int B, int H,
+                       int Hkv, int Nq, int Nk, int d, int causal, float scale,
+                       fa_stream_t stream) {
+    Shape s;
+    const fa_status st = padded(&s, kv_lens, B, H, Hkv, Nq, Nk, d, causal, scale);
+    return st == FA_OK ? forward(s, q, k, v, o, lse, workspace, workspace_bytes, stream) : st;
+}
+
+fa_status fa_fwd_cross_varlen(const void* q, const void* k, const void* v, void* o, float* lse,
+                              const int* cu_q, const int* cu_k, void* workspace,
+                              size_t workspace_bytes, int B, int max_q, int max_k, int total_q,
+                              int total_k, int H, int Hkv, int d, int causal, float scale,
+                              fa_stream_t stream) {
+    Shape s;
+    const fa_status st = packed(&s, cu_q, cu_k, B, max_q, max_k, total_q, total_k, H, Hkv, d,
+                                causal, scale);
+    return st == FA_OK ? forward(s, q, k, v, o, lse, workspace, workspace_bytes, stream) : st;
+}
+
+size_t fa_bwd_cross_workspace_size(int B, int H, int Hkv, int Nq, int Nk, int d) {
+    if (check_cross_shape(B, H, Hkv, Nq, Nk, d) != FA_OK) return 0;
+    Shape s{B, H, Hkv, Nq, d, 0, 1.0f};
+    s.Nk = Nk;
+    return bwd_workspace_bytes(s);
+}
+
+fa_status fa_bwd_cross(const void* q, const void* k, const void* v, const void* o,
+                       const void* dout, const float* lse, void* dq, void* dk, void* dv,
+                       const int* kv_lens, void* workspace, size_t workspace_bytes, int B, int H,
+                       int Hkv, int Nq, int Nk, int d, int causal, float scale,
+                       fa_stream_t stream) {
+    Shape s;
+    const fa_status st = padded(&s, kv_lens, B, H, Hkv, Nq, Nk, d, causal, scale);
+    return st == FA_OK ? backward(s, q, k, v, o, dout, lse, dq, dk, dv, workspace, workspace_bytes,
+                                  stream)
+                       : st;
+}
+
+fa_status fa_bwd_cross_varlen(const void* q, const void* k, const void* v, const void* o,
+                              const void* dout, const float* lse, void* dq, void* dk, void* dv,
+                              const int* cu_q, const int* cu_k, void* workspace,
+                              size_t workspace_bytes, int B, int max_q, int max_k, int total_q,
+                              int total_k, int H, int Hkv, int d, int causal, float scale,
+                              fa_stream_t stream) {
+    Shape s;
+    const fa_status st = packed(&s, cu_q, cu_k, B, max_q, max_k, total_q, total_k, H, Hkv, d,
+                                causal, scale);
+    return st == FA_OK ? backward(s, q, k, v, o, dout, lse, dq, dk, dv, workspace, workspace_bytes,
+                                  stream)
+                       : st;
+}
+
+size_t fa_fwd_cross_decode_workspace_size(int B, int H, int Hkv, int Nq, int Nk, int d) {
+    if (check_decode(B, H, Hkv, Nq, Nk, d) != FA_OK) return 0;
+    return paged_workspace_bytes(B, Hkv, H / Hkv * Nq, d);
+}
+
+fa_status fa_fwd_cross_decode(const void* q, const void* k, const void* v, void* o, float* lse,
+                              const int* kv_lens, void* workspace, size_t workspace_bytes, int B,
+                              int H, int Hkv, int Nq, int Nk, int d, int causal, float scale,
+                              fa_stream_t stream) {
+    fa_status st = check_decode(B, H, Hkv, Nq, Nk, d);
+    if (st == FA_OK) st = check_all({q, k, v, o, lse});
+    if (st == FA_OK && kv_lens) st = check_pointer(kv_lens, alignof(int));
+    if (st != FA_OK) return st;
+    if (bad_scale(scale)) return FA_ERR_INVALID_ARG;
+    if ((st = check_workspace(workspace, workspace_bytes,
+                              paged_workspace_bytes(B, Hkv, H / Hkv * Nq, d))) != FA_OK)
+        return st;
+    int dev;
+    DeviceStatus* status;
+    if ((st = ready_device(&dev, &status)) != FA_OK) return st;
+    return launch_fwd_cross_decode(q, k, v, o, lse, kv_lens, workspace, B, H, Hkv, Nq, Nk, d,
+                                   causal ? 1 : 0, scale, status,
+                                   (cudaStream_t)stream) == cudaSuccess
+               ? FA_OK
+               : FA_ERR_CUDA;
+}
+
+}  // extern "C"

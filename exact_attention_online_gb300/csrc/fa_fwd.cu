@@ -121,6 +121,12 @@ struct FwdParams {
     // longest sequence.  Dense batches: rows = N, cu_seqlens unused.
     int rows;
     const int* cu_seqlens;
+    // Keys of their own (CROSS): at most Nk of them a sequence, krows rows a head of
+    // k and v.  Padded batches: kv_lens[b] of them, or Nk (null).  Packed ones: rows
+    // cu_k[b] .. cu_k[b+1] - 1.
+    int Nk, krows;
+    const int* kv_lens;
+    const int* cu_k;
     float scale_log2;                 // scale * log2(e)
     void* o;                          // bf16, or fp32 in the precise variant
     float* lse;
@@ -140,9 +146,18 @@ struct FwdTile {
     int bh, row_base;
     int q_z, kv_z;             // head coordinate of the Q / O and K / V tensor maps
     int tok0, len;             // first row of the sequence in its head, its length
+    int ktok0, klen;           // the same of its keys
+    int off;                   // query i sees keys j <= i + off under the causal mask
     int lo[kTiles];            // first key block each query tile needs
     int n_kv[kTiles];          // one past its last key block
 };
+
+// The keys of sequence b (CROSS): how many, and the first one's row in its head.
+__device__ __forceinline__ int key_rows(const FwdParams& p, int b, int& ktok0) {
+    if (p.cu_k) return packed_seq(p.cu_k, b, p.Nk, p.krows, ktok0);
+    ktok0 = 0;
+    return p.kv_lens ? min(max(__ldg(p.kv_lens + b), 0), p.Nk) : p.Nk;
+}
 
 __device__ __forceinline__ int fwd_m_blk(int item, const FwdParams& p, bool causal) {
     const int mb_rank = item / p.BH;
@@ -157,7 +172,7 @@ __device__ __forceinline__ int fwd_m_blk(int item, const FwdParams& p, bool caus
 // plain round robin).  With variable lengths the ranks count only the items
 // that have rows (query-block pairs past a sequence's end are passed over):
 // a cursor walks the (level, sequence) list forward, ranks only grow.
-template <bool VARLEN>
+template <bool VARLEN, bool CROSS>
 struct FwdSched {
     int round = 0;
     int mb = 0, b = 0, base = 0;   // cursor: level, sequence, rank of (b, head 0)
@@ -166,7 +181,7 @@ struct FwdSched {
         const int G = gridDim.x, c = blockIdx.x;
         const int t = round * G + ((round & 1) ? G - 1 - c : c);   // rank
         ++round;
-        if (!VARLEN) return t < p.n_items ? t : p.n_items;
+        if (!VARLEN && !(CROSS && p.cu_seqlens)) return t < p.n_items ? t : p.n_items;
         const int B = p.BH / p.H;
         while (mb < p.n_mblk) {
             if (b >= B) {
@@ -186,13 +201,13 @@ struct FwdSched {
     }
 };
 
-template <bool WINDOW, bool VARLEN>
+template <bool WINDOW, bool VARLEN, bool CROSS>
 __device__ __forceinline__ FwdTile fwd_tile(int item, const FwdParams& p, bool causal) {
     FwdTile w;
     w.bh = item % p.BH;
     const int m_blk = fwd_m_blk(item, p, causal);
     const int b = w.bh / p.H, h = w.bh % p.H;
-    if (VARLEN) {
+    if (VARLEN || (CROSS && p.cu_seqlens)) {
         w.len = packed_seq(p.cu_seqlens, b, p.N, p.rows, w.tok0);
         w.q_z = h;
         w.kv_z = h / (p.H / p.Hkv);
@@ -202,8 +217,26 @@ __device__ __forceinline__ FwdTile fwd_tile(int item, const FwdParams& p, bool c
         w.q_z = w.bh;
         w.kv_z = b * p.Hkv + h / (p.H / p.Hkv);
     }
+    w.ktok0 = w.tok0;
+    w.klen = w.len;
+    w.off = 0;
+    if (CROSS) {
+        w.klen = key_rows(p, b, w.ktok0);
+        w.off = w.klen - w.len;
+    }
     w.row_base = m_blk * (kTiles * kBM);
-    const int n_kv_all = (w.len + kBN - 1) / kBN;
+    const int n_kv_all = (w.klen + kBN - 1) / kBN;
+    if (CROSS) {
+        // The tile's last row sees keys up to its own index + off.  A tile that
+        // sees nothing keeps one block, which the masks empty.
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+            const int end = w.row_base + (t + 1) * kBM + w.off;
+            w.n_kv[t] = max(1, causal ? min(n_kv_all, (max(end, 0) + kBN - 1) / kBN) : n_kv_all);
+            w.lo[t] = 0;
+        }
+        return w;
+    }
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
         w.n_kv[t] = causal ? min(n_kv_all, 2 * m_blk + t + 1) : n_kv_all;
@@ -244,7 +277,11 @@ __device__ __forceinline__ bool convert_v_half(uint8_t* sV, uint64_t* bar_v, uin
     return true;
 }
 
-template <int D, bool CAUSAL, bool PRECISE, bool WINDOW, bool VARLEN>
+// CROSS: queries against keys of another length (p.Nk, p.kv_lens, p.cu_k), padded or
+// packed (p.cu_seqlens), the causal mask by p.causal and counted from the last key.
+// Rows past a sequence's keys may hold anything: their scores are masked, and the
+// softmax of query tile 0 (of tile 1 where only that sees the block) clears V's rows.
+template <int D, bool CAUSAL, bool PRECISE, bool WINDOW, bool VARLEN, bool CROSS>
 __global__ void __launch_bounds__(kThreads, 1)
 fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
               const __grid_constant__ CUtensorMap tm_v, const FwdParams p) {
@@ -265,6 +302,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     __shared__ int abort_sh;
     const WaitCtx wc{p.status, &abort_sh};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool causal = CAUSAL || (CROSS && p.causal);
 
     if (threadIdx.x == 0) {
         abort_sh = 0;
@@ -316,12 +354,13 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         const float c = p.scale_log2;
         uint32_t cs = 0;                         // S_t completions seen so far
         uint32_t cpv = 0;                        // P_t V completions seen (separate P)
+        uint32_t gv = 0;                         // V blocks of the items before (CROSS)
         bool ok = true;
         int lt = 0;
-        FwdSched<VARLEN> sch;
-        for (int item = sch.next(p, CAUSAL); ok && item < p.n_items;
-             item = sch.next(p, CAUSAL), ++lt) {
-            const FwdTile wt = fwd_tile<WINDOW, VARLEN>(item, p, CAUSAL);
+        FwdSched<VARLEN, CROSS> sch;
+        for (int item = sch.next(p, causal); ok && item < p.n_items;
+             item = sch.next(p, causal), ++lt) {
+            const FwdTile wt = fwd_tile<WINDOW, VARLEN, CROSS>(item, p, causal);
             const int row0 = wt.row_base + t * kBM;
             const int row = row0 + rl;
             // (selects, not a run-time index: the arrays stay in registers)
@@ -356,12 +395,12 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 for (int e = 0; e < kBN; ++e) sv[e] = __uint_as_float(r[e >> 5][e & 31]);
 
                 const int col0 = j * kBN;
-                const bool need_mask = (CAUSAL && (col0 + kBN - 1 > row0 ||
+                const bool need_mask = (causal && (col0 + kBN - 1 > row0 + wt.off ||
                                                    (WINDOW && col0 < row0 + kBM - p.window))) ||
-                                       (col0 + kBN > wt.len);
+                                       (col0 + kBN > wt.klen);
                 if (need_mask) {
-                    const int lim_causal = CAUSAL ? row - col0 : kBN;   // keep e <= row - col0
-                    const int lim_n = wt.len - col0;                     // keep e < N - col0
+                    const int lim_causal = causal ? row + wt.off - col0 : kBN;   // keep e <= this
+                    const int lim_n = wt.klen - col0;                    // keep e < N - col0
                     const int lim_lo = WINDOW ? row - p.window + 1 - col0 : 0;  // keep e >= this
 #pragma unroll
                     for (int e = 0; e < kBN; ++e)
@@ -453,11 +492,26 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                     f2_split(f2_add(f2_add(acc2[0], acc2[1]), f2_add(acc2[2], acc2[3])), a0, a1);
                     l += a0 + a1;
                 }
+                if (CROSS && col0 + kBN > wt.klen && (t == 0 || j >= wt.n_kv[0])) {
+                    // V_j's rows past the keys: a weight of zero would not silence a
+                    // NaN.  (Its stage is not used again before this tile's P V.)
+                    const uint32_t gj = gv + (uint32_t)j, vs = gj % SV;
+                    if (!fa_wait_warp(&bar_v[vs], (gj / SV) & 1, 38 + t, wc)) { ok = false; break; }
+                    if (col0 + rl >= wt.klen) {
+                        const uint32_t vrow = smem_u32(sV) + vs * Cfg::kTileBytes + rl * 128;
+#pragma unroll
+                        for (int u = 0; u < Cfg::kChunks * 8; ++u)
+                            sts_v4(vrow + (u >> 3) * Cfg::kChunkBytes + (u & 7) * 16,
+                                   make_uint4(0u, 0u, 0u, 0u));
+                    }
+                    fence_proxy_async_smem();
+                }
                 tmem_st_wait();
                 tc_fence_before();
                 mbar_arrive(&bar_p[t]);
             }
             if (!ok) break;
+            if (CROSS) gv += wt.n_kv[kTiles - 1];
 
             // ------------------------------------------------------- epilogue
             // O row -> registers, release the O columns to the next item's
@@ -479,6 +533,14 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             tc_fence_before();
             mbar_arrive(&bar_o_free[t]);
             const bool valid = row < wt.len;
+            // a row that sees no key (the exponentials of the FMA pipe are not quite 0)
+            if (CROSS && m2 == -CUDART_INF_F) {
+                l = 0.0f;
+#pragma unroll
+                for (int c0 = 0; c0 < D / 32; ++c0)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) ov[c0][e] = 0u;
+            }
             const float l_o = PRECISE ? l + lc : l;
             const float inv_l = (l_o > 0.0f) ? 1.0f / l_o : 0.0f;
             const size_t orow = ((size_t)wt.q_z * p.rows + wt.tok0 + (valid ? row : 0)) * D;
@@ -540,10 +602,10 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             tma_prefetch_desc(&tm_k);
             uint32_t g = 0;              // K blocks loaded so far (ring position)
             bool ok = true;
-            FwdSched<VARLEN> sch;
-            for (int item = sch.next(p, CAUSAL); ok && item < p.n_items;
-                 item = sch.next(p, CAUSAL)) {
-                const FwdTile wt = fwd_tile<WINDOW, VARLEN>(item, p, CAUSAL);
+            FwdSched<VARLEN, CROSS> sch;
+            for (int item = sch.next(p, causal); ok && item < p.n_items;
+                 item = sch.next(p, causal)) {
+                const FwdTile wt = fwd_tile<WINDOW, VARLEN, CROSS>(item, p, causal);
                 for (int j = wt.lo[0]; j < wt.n_kv[kTiles - 1]; ++j, ++g) {
                     const int s = g % SK;
                     if (g >= (uint32_t)SK && !fa_wait(&bar_k_empty[s], ((g / SK) - 1) & 1, 10, wc)) {
@@ -553,7 +615,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                     mbar_arrive_expect_tx(&bar_k[s], Cfg::kTileBytes);
                     for (int c = 0; c < Cfg::kChunks; ++c)
                         tma_load_3d(sK + s * Cfg::kTileBytes + c * Cfg::kChunkBytes, &tm_k, &bar_k[s],
-                                    c * 64, wt.tok0 + j * kBN, wt.kv_z);
+                                    c * 64, wt.ktok0 + j * kBN, wt.kv_z);
                 }
             }
             if (abort_sh) {   // drain the copies still in flight (bounded)
@@ -570,10 +632,10 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             uint32_t g = 0;
             int lt = 0, q_loaded = -1;
             bool ok = true;
-            FwdSched<VARLEN> sch;
-            for (int item = sch.next(p, CAUSAL); ok && item < p.n_items;
-                 item = sch.next(p, CAUSAL), ++lt) {
-                const FwdTile wt = fwd_tile<WINDOW, VARLEN>(item, p, CAUSAL);
+            FwdSched<VARLEN, CROSS> sch;
+            for (int item = sch.next(p, causal); ok && item < p.n_items;
+                 item = sch.next(p, causal), ++lt) {
+                const FwdTile wt = fwd_tile<WINDOW, VARLEN, CROSS>(item, p, causal);
                 for (int t = 0; t < kTiles; ++t) {
                     if (lt > 0 && !fa_wait(&bar_q_free[t], (lt - 1) & 1, 12, wc)) { ok = false; break; }
                     mbar_arrive_expect_tx(&bar_q[t], Cfg::kTileBytes);
@@ -592,7 +654,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                     mbar_arrive_expect_tx(&bar_v[s], Cfg::kTileBytes);
                     for (int c = 0; c < Cfg::kChunks; ++c)
                         tma_load_3d(sV + s * Cfg::kTileBytes + c * Cfg::kChunkBytes, &tm_v, &bar_v[s],
-                                    c * 64, wt.tok0 + j * kBN, wt.kv_z);
+                                    c * 64, wt.ktok0 + j * kBN, wt.kv_z);
                 }
             }
             if (abort_sh) {   // drain the copies still in flight (bounded)
@@ -617,10 +679,10 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             if (leader) tma_prefetch_desc(&tm_k);
             uint32_t g = 0, gc = 0;      // K blocks loaded (ring position); V halves converted
             bool ok = true;
-            FwdSched<VARLEN> sch;
-            for (int item = sch.next(p, CAUSAL); ok && item < p.n_items;
-                 item = sch.next(p, CAUSAL)) {
-                const FwdTile wt = fwd_tile<WINDOW, VARLEN>(item, p, CAUSAL);
+            FwdSched<VARLEN, CROSS> sch;
+            for (int item = sch.next(p, causal); ok && item < p.n_items;
+                 item = sch.next(p, causal)) {
+                const FwdTile wt = fwd_tile<WINDOW, VARLEN, CROSS>(item, p, causal);
                 for (int j = wt.lo[0]; j < wt.n_kv[kTiles - 1]; ++j, ++g) {
                     if (PRECISE && gc + 2 <= g) {
                         if (!convert_v_half<SV, Cfg::kTileBytes>(sV, bar_v, bar_v_cvt, gc, 1, lane, wc)) {
@@ -668,10 +730,10 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             uint32_t g = 0;   // V blocks issued (and their first halves converted)
             int lt = 0, q_loaded = -1;
             bool ok = true;
-            FwdSched<VARLEN> sch;
-            for (int item = sch.next(p, CAUSAL); ok && item < p.n_items;
-                 item = sch.next(p, CAUSAL), ++lt) {
-                const FwdTile wt = fwd_tile<WINDOW, VARLEN>(item, p, CAUSAL);
+            FwdSched<VARLEN, CROSS> sch;
+            for (int item = sch.next(p, causal); ok && item < p.n_items;
+                 item = sch.next(p, causal), ++lt) {
+                const FwdTile wt = fwd_tile<WINDOW, VARLEN, CROSS>(item, p, causal);
                 const int jb = wt.lo[0], je = wt.n_kv[kTiles - 1];
                 auto issue_v = [&](int j) -> bool {   // V_j into the ring
                     const int s = g % SV;
@@ -744,10 +806,10 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 mma_commit(&bar_pv[T]);
                 return true;
             };
-            FwdSched<VARLEN> sch;
-            for (int item = sch.next(p, CAUSAL); ok && item < p.n_items;
-                 item = sch.next(p, CAUSAL), ++lt) {
-                const FwdTile wt = fwd_tile<WINDOW, VARLEN>(item, p, CAUSAL);
+            FwdSched<VARLEN, CROSS> sch;
+            for (int item = sch.next(p, causal); ok && item < p.n_items;
+                 item = sch.next(p, causal), ++lt) {
+                const FwdTile wt = fwd_tile<WINDOW, VARLEN, CROSS>(item, p, causal);
                 // Key blocks [lo0, n0) for tile 0, [lo1, n1) for tile 1, with
                 // lo0 <= lo1 and n0 <= n1; V_j streams for j in [lo0, n1).
                 const int lo0 = wt.lo[0], lo1 = wt.lo[1], n0 = wt.n_kv[0], n1 = wt.n_kv[1];
@@ -809,10 +871,10 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 mma_commit(&bar_s[T]);
                 return true;
             };
-            FwdSched<VARLEN> sch;
-            for (int item = sch.next(p, CAUSAL); ok && item < p.n_items;
-                 item = sch.next(p, CAUSAL), ++lt) {
-                const FwdTile wt = fwd_tile<WINDOW, VARLEN>(item, p, CAUSAL);
+            FwdSched<VARLEN, CROSS> sch;
+            for (int item = sch.next(p, causal); ok && item < p.n_items;
+                 item = sch.next(p, causal), ++lt) {
+                const FwdTile wt = fwd_tile<WINDOW, VARLEN, CROSS>(item, p, causal);
                 const int lo0 = wt.lo[0], lo1 = wt.lo[1], n0 = wt.n_kv[0], n1 = wt.n_kv[1];
                 if (!fa_wait(&bar_q[0], lt & 1, 20, wc) || !fa_wait(&bar_q[1], lt & 1, 20, wc)) {
                     ok = false;
@@ -852,11 +914,12 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     }
 }
 
-template <int D, bool CAUSAL, bool PRECISE, bool WINDOW = false, bool VARLEN = false>
+template <int D, bool CAUSAL, bool PRECISE, bool WINDOW = false, bool VARLEN = false,
+          bool CROSS = false>
 cudaError_t launch_fwd_t(const Shape& s, const CUtensorMap& tq, const CUtensorMap& tk,
                          const CUtensorMap& tv, const FwdParams& p, int grid,
                          cudaStream_t stream) {
-    auto kern = fa_fwd_kernel<D, CAUSAL, PRECISE, WINDOW, VARLEN>;
+    auto kern = fa_fwd_kernel<D, CAUSAL, PRECISE, WINDOW, VARLEN, CROSS>;
     static int configured_device = -1;   // attribute is per device; cheap to repeat
     int dev = 0;
     cudaGetDevice(&dev);
@@ -883,14 +946,19 @@ cudaError_t launch_fwd(const Shape& s, const void* q, const void* k, const void*
                        const BwdWorkspace* train_ws) {
     // Dense: maps {d, N, B*H(kv)}.  Packed variable lengths: {d, total, H(kv)},
     // a sequence's rows addressed from its first row.
-    const bool varlen = s.cu_seqlens != nullptr;
+    const bool varlen = s.cu_seqlens != nullptr, cross = s.Nk > 0;
     const int rows = varlen ? s.total : s.N;
+    const int krows = !cross ? rows : varlen ? s.total_k : s.Nk;
     CUtensorMap tq, tk, tv;
     if (!make_tmap_bf16_3d(&tq, q, s.d, rows, varlen ? s.H : s.B * s.H, kBM) ||
-        !make_tmap_bf16_3d(&tk, k, s.d, rows, varlen ? s.Hkv : s.B * s.Hkv, kBN) ||
-        !make_tmap_bf16_3d(&tv, v, s.d, rows, varlen ? s.Hkv : s.B * s.Hkv, kBN))
+        !make_tmap_bf16_3d(&tk, k, s.d, krows, varlen ? s.Hkv : s.B * s.Hkv, kBN) ||
+        !make_tmap_bf16_3d(&tv, v, s.d, krows, varlen ? s.Hkv : s.B * s.Hkv, kBN))
         return cudaErrorInvalidValue;
     FwdParams p;
+    p.Nk = s.Nk;
+    p.krows = krows;
+    p.kv_lens = s.kv_lens;
+    p.cu_k = s.cu_k;
     p.H = s.H;
     p.Hkv = s.Hkv;
     p.N = s.N;
@@ -919,6 +987,12 @@ cudaError_t launch_fwd(const Shape& s, const void* q, const void* k, const void*
     const int grid = p.n_items < sms ? p.n_items : sms;
     count_launch();
     const bool c = s.causal != 0;
+    if (cross) {   // keys of another length (bf16 output, no window, no training form)
+        if (precise || s.window > 0 || train_ws) return cudaErrorInvalidValue;
+        return s.d == 128
+                   ? launch_fwd_t<128, false, false, false, false, true>(s, tq, tk, tv, p, grid, stream)
+                   : launch_fwd_t<64, false, false, false, false, true>(s, tq, tk, tv, p, grid, stream);
+    }
     if (varlen) {   // packed variable-length sequences (bf16 output, no window)
         if (precise || s.window > 0) return cudaErrorInvalidValue;
         if (s.d == 128)

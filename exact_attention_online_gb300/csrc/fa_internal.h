@@ -21,6 +21,13 @@ struct Shape {
     // the total row count; N is then the longest sequence.  nullptr = dense.
     const int* cu_seqlens = nullptr;
     int total = 0;
+    // Keys of their own, Nk > 0: N, cu_seqlens and total are the queries', and the
+    // keys Nk rows a sequence (kv_lens[b] of them valid, or all with null), or
+    // packed with row offsets cu_k and total_k rows (the longest then Nk).
+    int Nk = 0;
+    const int* kv_lens = nullptr;
+    const int* cu_k = nullptr;
+    int total_k = 0;
 };
 
 // Rows [t0, t0 + len) of sequence b of a packed variable-length batch (cu =
@@ -196,6 +203,13 @@ cudaError_t launch_fwd_decode_paged(const PagedCache& c, const void* q, void* o,
                                     const int* seqlens, void* workspace, int B, int H, int Nq,
                                     int causal, float scale, DeviceStatus* status,
                                     cudaStream_t stream);
+// Workspace of a forward with keys of their own (fa_cross.cu).
+size_t cross_fwd_workspace_bytes(const Shape& s);
+// Paged decoding over contiguous K and V [B][Hkv][Nk][d], kv_lens[b] keys a sequence (null: Nk).
+cudaError_t launch_fwd_cross_decode(const void* q, const void* k, const void* v, void* o,
+                                    float* lse, const int* kv_lens, void* workspace, int B, int H,
+                                    int Hkv, int Nq, int Nk, int d, int causal, float scale,
+                                    DeviceStatus* status, cudaStream_t stream);
 
 // Number of SMs of the current device (cached per device).
 int device_sm_count();

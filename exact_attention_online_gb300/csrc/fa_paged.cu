@@ -39,6 +39,9 @@
 // order.  A small call (short table, few pairs) takes no list and no second kernel:
 // a cluster of CTAs shares a pair, and joins its parts through their shared memory.
 //
+// A contiguous K and V [B][Hkv][Nk][d] is a pool of one page a sequence without a table,
+// and goes through the same kernels.
+//
 // Warps: 0-3 (and 8-11) softmax, four warps for a group of query rows, which need
 // nothing of one another; 4 loads K, 7 V, 5 issues MMAs, 6 lays out the queries
 // of a pair and loads its scales.
@@ -65,13 +68,14 @@ constexpr int kMaxCluster = 8;          // most CTAs that share a pair without a
 struct PagedParams {
     const __nv_bfloat16* q;             // rows i * R .. of pair i = b * Hkv + g
     const float* scales;
-    const int* table;
-    const int* seqlens;
+    const int* table;                   // null: page b is sequence b's
+    const int* seqlens;                 // null: all `limit`
     __nv_bfloat16* o;
     float* lse;
     float* part_o;                      // [slots][R][d]
     float* part_lse;                    // [slots][R], log2
     int B, Hkv, Nq, R, n_pages, ps_shift, max_pages, causal;
+    int limit;                          // most keys of a sequence
     int ctas;                           // of the split kernel; in clusters: of a pair
     float scale_log2;
     DeviceStatus* status;
@@ -144,7 +148,7 @@ struct Cfg {
 };
 
 __device__ __forceinline__ int clamped_len(const PagedParams& p, int b) {
-    return min(max(p.seqlens[b], 0), p.max_pages << p.ps_shift);
+    return p.seqlens ? min(max(p.seqlens[b], 0), p.limit) : p.limit;
 }
 __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
 
@@ -431,9 +435,8 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
     // The page of lane's segment of the cursor's tile (0 where there is none).
     auto page_of = [&](const Cursor& at) {
         const int key = at.t * kTile + lane * seg;
-        return (at.left > 0 && lane < n_seg && key < at.len)
-                   ? p.table[(long long)at.b * p.max_pages + (key >> p.ps_shift)]
-                   : 0;
+        if (at.left <= 0 || lane >= n_seg || key >= at.len) return 0;
+        return p.table ? p.table[(long long)at.b * p.max_pages + (key >> p.ps_shift)] : at.b;
     };
 
     if (warp == 4 || warp == 7) {
@@ -1088,7 +1091,7 @@ cudaError_t launch_attend(const CUtensorMap& tk, const CUtensorMap& tv, PagedPar
                           cudaStream_t stream) {
     using C = Cfg<D, F8, G, W>;
     static_assert(C::kSmem + C::kStatic <= 227 * 1024, "shared memory of one CTA");
-    const int longest = ((p.max_pages << p.ps_shift) + kTile - 1) / kTile;    // tiles of a pair
+    const int longest = (p.limit + kTile - 1) / kTile;         // tiles of a pair
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -1142,6 +1145,37 @@ size_t paged_workspace_bytes(int B, int Hkv, int R, int d) {
     return align256(slots * R * d * 4) + slots * R * 4;
 }
 
+namespace {
+
+// The calls' common part: what a pool, with or without a table, leaves to be filled in.
+cudaError_t launch_pool(const CUtensorMap& tk, const CUtensorMap& tv, PagedParams& p, bool f8,
+                        int d, const void* q, void* o, float* lse, void* workspace, int B, int H,
+                        int Hkv, int Nq, int causal, float scale, DeviceStatus* status,
+                        cudaStream_t stream) {
+    p.R = H / Hkv * Nq;
+    const size_t slots = (size_t)kPagedMaxCtas + (size_t)B * Hkv;
+    char* ws = static_cast<char*>(workspace);
+    p.part_o = reinterpret_cast<float*>(ws);
+    ws += align256(slots * p.R * d * 4);
+    p.part_lse = reinterpret_cast<float*>(ws);
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.o = static_cast<__nv_bfloat16*>(o);
+    p.lse = lse;
+    p.B = B;
+    p.Hkv = Hkv;
+    p.Nq = Nq;
+    p.causal = causal;
+    p.scale_log2 = scale * kLog2e;
+    p.status = status;
+    if (d == 128)
+        return f8 ? launch_rows<128, true>(tk, tv, p, stream)
+                  : launch_rows<128, false>(tk, tv, p, stream);
+    return f8 ? launch_rows<64, true>(tk, tv, p, stream)
+              : launch_rows<64, false>(tk, tv, p, stream);
+}
+
+}  // namespace
+
 cudaError_t launch_fwd_decode_paged(const PagedCache& c, const void* q, void* o, float* lse,
                                     const int* seqlens, void* workspace, int B, int H, int Nq,
                                     int causal, float scale, DeviceStatus* status,
@@ -1153,32 +1187,35 @@ cudaError_t launch_fwd_decode_paged(const PagedCache& c, const void* q, void* o,
         !make_tmap_pages(&tv, c.v_pages, f8, c.d, ps, (long long)c.n_pages * c.Hkv, box))
         return cudaErrorInvalidValue;
     PagedParams p;
-    p.R = H / c.Hkv * Nq;
-    const size_t slots = (size_t)kPagedMaxCtas + (size_t)B * c.Hkv;
-    char* ws = static_cast<char*>(workspace);
-    p.part_o = reinterpret_cast<float*>(ws);
-    ws += align256(slots * p.R * c.d * 4);
-    p.part_lse = reinterpret_cast<float*>(ws);
-    p.q = static_cast<const __nv_bfloat16*>(q);
     p.scales = c.scales;
     p.table = c.table;
     p.seqlens = seqlens;
-    p.o = static_cast<__nv_bfloat16*>(o);
-    p.lse = lse;
-    p.B = B;
-    p.Hkv = c.Hkv;
-    p.Nq = Nq;
     p.n_pages = c.n_pages;
     p.ps_shift = c.ps_shift;
     p.max_pages = c.max_pages;
-    p.causal = causal;
-    p.scale_log2 = scale * kLog2e;
-    p.status = status;
-    if (c.d == 128)
-        return f8 ? launch_rows<128, true>(tk, tv, p, stream)
-                  : launch_rows<128, false>(tk, tv, p, stream);
-    return f8 ? launch_rows<64, true>(tk, tv, p, stream)
-              : launch_rows<64, false>(tk, tv, p, stream);
+    p.limit = c.max_pages << c.ps_shift;
+    return launch_pool(tk, tv, p, f8, c.d, q, o, lse, workspace, B, H, c.Hkv, Nq, causal, scale,
+                       status, stream);
+}
+
+cudaError_t launch_fwd_cross_decode(const void* q, const void* k, const void* v, void* o,
+                                    float* lse, const int* kv_lens, void* workspace, int B, int H,
+                                    int Hkv, int Nq, int Nk, int d, int causal, float scale,
+                                    DeviceStatus* status, cudaStream_t stream) {
+    CUtensorMap tk, tv;
+    if (!make_tmap_pages(&tk, k, false, d, Nk, (long long)B * Hkv, kTile) ||
+        !make_tmap_pages(&tv, v, false, d, Nk, (long long)B * Hkv, kTile))
+        return cudaErrorInvalidValue;
+    PagedParams p;
+    p.scales = nullptr;
+    p.table = nullptr;
+    p.seqlens = kv_lens;
+    p.n_pages = B;
+    p.ps_shift = 30;                              // every key is on the sequence's one page
+    p.max_pages = 1;
+    p.limit = Nk;
+    return launch_pool(tk, tv, p, false, d, q, o, lse, workspace, B, H, Hkv, Nq, causal, scale,
+                       status, stream);
 }
 
 }  // namespace fa

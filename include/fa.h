@@ -666,6 +666,73 @@ FA_API fa_status fa_rope_append(const void* q, const void* k, const void* v, voi
                                 int interleaved, float amplitude, fa_stream_t stream);
 
 /*
+ * Attention to keys of another length than the queries (the states of an encoder;
+ * a prompt's next rows against all rows so far, as fa_kv_gather hands them out; the
+ * pages describe equal lengths, FlashAttention blog, so these forms are the
+ * library's).  q, o, dout, dq bf16 [B][H][Nq][d], k, v, dk, dv bf16 [B][Hkv][Nk][d],
+ * lse fp32 [B][H][Nq].  kv_lens (DEVICE int32 [B], or null: all Nk) gives each
+ * sequence's number of keys, clamped to [0, Nk]; rows of k and v behind them may hold
+ * anything.  With causal != 0 the queries are the last Nq positions: query i of a
+ * sequence of n keys sees keys j <= i + n - Nq (fa_fwd()'s rule when n = Nq).  A query
+ * that sees no key (no keys, or i + n < Nq) gets O = 0, LSE = -infinity and a dQ of 0;
+ * a key that no query sees gets dK = dV = 0, and so do the rows behind kv_lens.  A NaN
+ * or an infinity among a sequence's keys may reach all of its queries.
+ * d in {64, 128}; H % Hkv == 0; B * H * Nq * d, with Nq rounded up to 128, B * Hkv * Nk
+ * * d and B * Hkv * Nk rounded up to 128 below 2^31 (FA_ERR_UNSUPPORTED).  Errors
+ * otherwise as fa_fwd() and fa_bwd(); workspace: caller-owned, of the size that the
+ * function beside each gives, 256-byte aligned, contents on entry of no matter, one for
+ * each call that may overlap on the GPU (FA_ERR_WORKSPACE, FA_ERR_ALIGNMENT).
+ */
+FA_API size_t fa_fwd_cross_workspace_size(int B, int H, int Hkv, int Nq, int Nk, int d);
+FA_API fa_status fa_fwd_cross(const void* q, const void* k, const void* v, void* o, float* lse,
+                              const int* kv_lens, void* workspace, size_t workspace_bytes, int B,
+                              int H, int Hkv, int Nq, int Nk, int d, int causal, float scale,
+                              fa_stream_t stream);
+
+/*
+ * Its gradients, from o and lse as fa_fwd_cross() wrote them.  dk and dv are the same
+ * bit for bit on every call, dq as in fa_bwd().  Three launches.
+ */
+FA_API size_t fa_bwd_cross_workspace_size(int B, int H, int Hkv, int Nq, int Nk, int d);
+FA_API fa_status fa_bwd_cross(const void* q, const void* k, const void* v, const void* o,
+                              const void* dout, const float* lse, void* dq, void* dk, void* dv,
+                              const int* kv_lens, void* workspace, size_t workspace_bytes, int B,
+                              int H, int Hkv, int Nq, int Nk, int d, int causal, float scale,
+                              fa_stream_t stream);
+
+/*
+ * The same of packed batches (the layout of fa_fwd_varlen() on both sides): q, o, dout,
+ * dq [H][total_q][d], lse [H][total_q], k, v, dk, dv [Hkv][total_k][d]; sequence b's
+ * queries at rows cu_q[b] .. cu_q[b+1] - 1, its keys at cu_k[b] .. cu_k[b+1] - 1 (DEVICE
+ * int32 [B + 1] each; a length may be 0), none longer than max_q and max_k, which take
+ * the place of Nq and Nk in the sizes and limits.  Rows in no sequence may hold anything
+ * and are left as they are in o, lse, dq, dk and dv.  Offsets outside these rules give
+ * unspecified results but no access outside the tensors.
+ */
+FA_API fa_status fa_fwd_cross_varlen(const void* q, const void* k, const void* v, void* o,
+                                     float* lse, const int* cu_q, const int* cu_k, void* workspace,
+                                     size_t workspace_bytes, int B, int max_q, int max_k,
+                                     int total_q, int total_k, int H, int Hkv, int d, int causal,
+                                     float scale, fa_stream_t stream);
+FA_API fa_status fa_bwd_cross_varlen(const void* q, const void* k, const void* v, const void* o,
+                                     const void* dout, const float* lse, void* dq, void* dk,
+                                     void* dv, const int* cu_q, const int* cu_k, void* workspace,
+                                     size_t workspace_bytes, int B, int max_q, int max_k,
+                                     int total_q, int total_k, int H, int Hkv, int d, int causal,
+                                     float scale, fa_stream_t stream);
+
+/*
+ * fa_fwd_cross() for a few queries a sequence, (H / Hkv) * Nq <= 32 (FA_ERR_UNSUPPORTED
+ * otherwise), the keys split over the GPU as in fa_fwd_decode_paged(), whose notes on
+ * precision (bf16 pages), NaN, launches, replay and workspaces hold here too.
+ */
+FA_API size_t fa_fwd_cross_decode_workspace_size(int B, int H, int Hkv, int Nq, int Nk, int d);
+FA_API fa_status fa_fwd_cross_decode(const void* q, const void* k, const void* v, void* o,
+                                     float* lse, const int* kv_lens, void* workspace,
+                                     size_t workspace_bytes, int B, int H, int Hkv, int Nq, int Nk,
+                                     int d, int causal, float scale, fa_stream_t stream);
+
+/*
  * Synchronizes `stream`, then reads and clears the device status word of the
  * current device: FA_OK, or the first error a kernel recorded (for example
  * FA_ERR_TIMEOUT when a bounded wait ran out).  Returns FA_ERR_CUDA if the
