@@ -724,7 +724,8 @@ FA_API fa_status fa_bwd_cross_varlen(const void* q, const void* k, const void* v
 /*
  * fa_fwd_cross() for a few queries a sequence, (H / Hkv) * Nq <= 32 (FA_ERR_UNSUPPORTED
  * otherwise), the keys split over the GPU as in fa_fwd_decode_paged(), whose notes on
- * precision (bf16 pages), NaN, launches, replay and workspaces hold here too.
+ * precision (bf16 pages), NaN, launches, replay and workspaces hold here too.  k and v
+ * may have more than 2^31 elements; B * Hkv * (Nk / 128 + 2) <= 2^30, Nk < 2^30.
  */
 FA_API size_t fa_fwd_cross_decode_workspace_size(int B, int H, int Hkv, int Nq, int Nk, int d);
 FA_API fa_status fa_fwd_cross_decode(const void* q, const void* k, const void* v, void* o,
