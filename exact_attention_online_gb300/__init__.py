@@ -13,7 +13,7 @@ from __future__ import annotations
 
 import ctypes
 
-from ._native import EXPORTS, LIB_PATH, build, lib
+from ._native import EXPORTS, LIB_PATH, binding, build, lib
 
 FA_OK = 0
 FA_ERR_INVALID_ARG = -1
@@ -86,6 +86,25 @@ def _current_index() -> int:
         return _runtime()[0]()
     except Exception:   # no CUDA runtime in this process: the library rejects the call
         return 0
+
+
+# What a function of binding() returns for arguments that are not exactly what the call takes:
+# the wrapper's own checks then find what is wrong with them, or nothing (a size that is no int).
+_EXPLAIN = 1
+
+
+def _done(status: int, where: str) -> bool:
+    """Whether binding() has made the call; raises where the library refused it."""
+    if status == _EXPLAIN:
+        return False
+    if status != FA_OK:
+        raise FAError(status, where)
+    return True
+
+
+def _handle(stream):
+    """A stream for binding(): None is the current one."""
+    return None if stream is None else _stream(stream)
 
 
 def _on_current_device(t, name) -> None:
@@ -740,25 +759,14 @@ def attention_decode_paged(q, k_pages, v_pages, block_table, seqlens, causal: bo
 
 
 # --------------------------------------------- block tables and slot maps
-def _all_i32(cur, shapes):
-    """Pointers of contiguous int32 tensors of the current device, (tensor, name, shape) each."""
-    import torch
-    i32 = torch.int32
-    for t, _, shape in shapes:
-        if not (t.dtype is i32 and t.shape == shape and t.get_device() == cur and
-                t.is_contiguous()):
-            _explain(*((t, name, i32, shape) for t, name, shape in shapes))
-    return [t.data_ptr() for t, _, _ in shapes]
+def _all_i32(*args):
+    """Pointers of int32 tensors, (tensor, name, shape) each."""
+    return [_i32(t, name, shape) for t, name, shape in args]
 
 
-def _map(positions, slots, shape, cur):
+def _map(positions, slots, shape):
     import torch
-    if not (positions.dtype is torch.int32 and slots.dtype is torch.int64 and
-            positions.shape == shape and slots.shape == shape and
-            positions.get_device() == cur and slots.get_device() == cur and
-            positions.is_contiguous() and slots.is_contiguous()):
-        _explain((positions, "positions", torch.int32, shape), (slots, "slots", torch.int64, shape))
-    return positions.data_ptr(), slots.data_ptr()
+    return _i32(positions, "positions", shape), _ptr(slots, "slots", torch.int64, shape)
 
 
 def _table(block_table):
@@ -773,14 +781,17 @@ def fa_kv_reserve(block_table, seqlens, free_pages, n_free, new_tokens, starts, 
     free_pages [n_pages] and n_free [1] in place; starts, counts [B] and cu_seqlens [B + 1]
     written; positions, slots (int64) [B, N] or packed [total]: the new tokens' map.  All
     int32 but slots."""
+    if _done(binding().kv_reserve(block_table, seqlens, free_pages, n_free, new_tokens, starts,
+                                  counts, cu_seqlens, positions, slots, page_size,
+                                  _handle(stream)), "fa_kv_reserve"):
+        return
     B, mp = table = _table(block_table)
-    cur = _current_index()
     one = (B,)
     n_pages = free_pages.numel()
-    ptrs = _all_i32(cur, ((block_table, "block_table", table), (seqlens, "seqlens", one),
+    ptrs = _all_i32((block_table, "block_table", table), (seqlens, "seqlens", one),
                           (free_pages, "free_pages", (n_pages,)), (n_free, "n_free", (1,)),
                           (new_tokens, "new_tokens", one), (starts, "starts", one),
-                          (counts, "counts", one), (cu_seqlens, "cu_seqlens", (B + 1,))))
+                          (counts, "counts", one), (cu_seqlens, "cu_seqlens", (B + 1,)))
     N, total, at = 0, 0, (None, None)
     if positions is not None or slots is not None:
         if positions is None or slots is None:
@@ -792,7 +803,7 @@ def fa_kv_reserve(block_table, seqlens, free_pages, n_free, new_tokens, starts, 
                 raise ValueError("slots has no rows")
         else:
             total, shape = slots.numel(), (slots.numel(),)
-        at = _map(positions, slots, shape, cur)
+        at = _map(positions, slots, shape)
     _check(lib().fa_kv_reserve(*ptrs, *at, B, N, total, n_pages, _c_int(page_size, "page_size"),
                                mp, _stream(stream)), "fa_kv_reserve")
 
@@ -801,14 +812,16 @@ def fa_kv_release(block_table, seqlens, free_pages, n_free, keep, page_size: int
                   stream=None) -> None:
     """Every sequence cut back to its first keep [B] tokens, the pages behind them free again
     (but for the first pinned [B] pages of each, if given)."""
+    if _done(binding().kv_release(block_table, seqlens, free_pages, n_free, keep, pinned, page_size,
+                                  _handle(stream)), "fa_kv_release"):
+        return
     B, mp = table = _table(block_table)
-    cur = _current_index()
     one = (B,)
     n_pages = free_pages.numel()
-    ptrs = _all_i32(cur, ((block_table, "block_table", table), (seqlens, "seqlens", one),
+    ptrs = _all_i32((block_table, "block_table", table), (seqlens, "seqlens", one),
                           (free_pages, "free_pages", (n_pages,)), (n_free, "n_free", (1,)),
-                          (keep, "keep", one)) +
-                    (() if pinned is None else ((pinned, "pinned", one),)))
+                          (keep, "keep", one),
+                    *(() if pinned is None else ((pinned, "pinned", one),)))
     if pinned is None:
         ptrs.append(None)
     _check(lib().fa_kv_release(*ptrs, B, n_pages, _c_int(page_size, "page_size"), mp,
@@ -819,13 +832,12 @@ def fa_kv_slots(block_table, starts, counts, positions, slots, page_size: int,
                 stream=None) -> None:
     """Positions and slots [B, N] of rows i < counts[b] at positions starts[b] + i."""
     B, mp = table = _table(block_table)
-    cur = _current_index()
-    ptrs = _all_i32(cur, ((block_table, "block_table", table), (starts, "starts", (B,)),
-                          (counts, "counts", (B,))))
+    ptrs = _all_i32((block_table, "block_table", table), (starts, "starts", (B,)),
+                    (counts, "counts", (B,)))
     if slots.dim() != 2:
         raise ValueError("slots must be 2-D [B, N]")
     N = slots.shape[1]
-    at = _map(positions, slots, (B, N), cur)
+    at = _map(positions, slots, (B, N))
     _check(lib().fa_kv_slots(*ptrs, *at, B, N, _c_int(page_size, "page_size"), mp,
                              _stream(stream)), "fa_kv_slots")
 
@@ -834,12 +846,11 @@ def fa_kv_slots_varlen(block_table, starts, cu_seqlens, positions, slots, page_s
                        stream=None) -> None:
     """The same of a packed batch: positions, slots [total], cu_seqlens [B + 1]."""
     B, mp = table = _table(block_table)
-    cur = _current_index()
-    ptrs = _all_i32(cur, ((block_table, "block_table", table), (starts, "starts", (B,)),
-                          (cu_seqlens, "cu_seqlens", (B + 1,))))
+    ptrs = _all_i32((block_table, "block_table", table), (starts, "starts", (B,)),
+                    (cu_seqlens, "cu_seqlens", (B + 1,)))
     if slots.dim() != 1:
         raise ValueError("slots must be 1-D [total]")
-    at = _map(positions, slots, slots.shape, cur)
+    at = _map(positions, slots, slots.shape)
     _check(lib().fa_kv_slots_varlen(*ptrs, *at, B, slots.numel(), _c_int(page_size, "page_size"),
                                     mp, _stream(stream)), "fa_kv_slots_varlen")
 
@@ -870,36 +881,23 @@ def rope_frequencies(rot: int, base: float = 10000.0, scaling: str | None = None
 _STRIDES = ctypes.c_longlong * 12
 
 
-def _rows_ok(t, shape, cur):
+def _rows(t, name, shape):
+    """Device pointer and strides of rows t, contiguous each."""
     import torch
-    return (t.dtype is torch.bfloat16 and t.shape == shape and t.get_device() == cur and
-            t.stride(3) == 1)
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != torch.bfloat16 or not t.is_cuda or t.stride(3) != 1:
+        raise ValueError(f"{name} must be a CUDA bfloat16 tensor with contiguous rows")
+    _on_current_device(t, name)
+    return t.data_ptr(), t.stride()[:3]
 
 
-def _explain_rows(*args):
-    import torch
-    for t, name, shape in args:
-        if t.shape != shape:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-        if t.dtype != torch.bfloat16 or not t.is_cuda or t.stride(3) != 1:
-            raise ValueError(f"{name} must be a CUDA bfloat16 tensor with contiguous rows")
-        _on_current_device(t, name)
-    raise ValueError("tensors disagree")
-
-
-def _rope_args(qs, positions, freqs, cur):
+def _rope_args(q, positions, freqs):
     """B, H, N, d, rot of a call, and the pointers of positions and freqs."""
     import torch
-    if len(qs) != 4:
-        raise ValueError("q must be 4-D [B, H, N, d]")
-    B, H, N, d = qs
-    if not (positions.dtype is torch.int32 and positions.shape == (B, N) and
-            positions.get_device() == cur and positions.is_contiguous() and
-            freqs.dtype is torch.int64 and freqs.get_device() == cur and freqs.is_contiguous() and
-            len(freqs.shape) == 1):
-        _explain((positions, "positions", torch.int32, (B, N)),
-                 (freqs, "freqs", torch.int64, (freqs.numel(),)))
-    return B, H, N, d, 2 * freqs.numel(), positions.data_ptr(), freqs.data_ptr()
+    B, H, N, d = _dims_of(q, "q")
+    return (B, H, N, d, 2 * freqs.numel(), _i32(positions, "positions", (B, N)),
+            _ptr(freqs, "freqs", torch.int64, (freqs.numel(),)))
 
 
 def fa_rope(q, k, q_out, k_out, positions, freqs, interleaved: bool = False,
@@ -907,23 +905,20 @@ def fa_rope(q, k, q_out, k_out, positions, freqs, interleaved: bool = False,
     """q [B, H, N, d] and k [B, Hkv, N, d] (or None, with k_out) turned by their positions
     int32 [B, N] into q_out and k_out; any strides over B, H and N.  freqs, amplitude: from
     rope_frequencies; inverse: for gradients."""
-    cur = _current_index()
-    B, H, N, d, rot, pp, fp = _rope_args(q.shape, positions, freqs, cur)
+    if _done(binding().rope(q, k, q_out, k_out, positions, freqs, interleaved, inverse, amplitude,
+                            _handle(stream)), "fa_rope"):
+        return
+    B, H, N, d, rot, pp, fp = _rope_args(q, positions, freqs)
     if (k is None) != (k_out is None):
         raise ValueError("k and k_out come together")
-    if k is None:
-        Hkv, kp, ks, kop, kos = 0, None, (0, 0, 0, 0), None, (0, 0, 0, 0)
-    else:
-        Hkv = k.shape[1] if k.dim() == 4 else 0
-        kp, ks, kop, kos = k.data_ptr(), k.stride(), k_out.data_ptr(), k_out.stride()
-    shape = (B, Hkv, N, d)
-    if not (_rows_ok(q, q.shape, cur) and _rows_ok(q_out, q.shape, cur) and
-            (k is None or (_rows_ok(k, shape, cur) and _rows_ok(k_out, shape, cur)))):
-        _explain_rows((q, "q", q.shape), (q_out, "q_out", q.shape),
-                      *(() if k is None else ((k, "k", shape), (k_out, "k_out", shape))))
-    strides = _STRIDES(*q.stride()[:3], *ks[:3], *q_out.stride()[:3], *kos[:3])
-    _check(lib().fa_rope(q.data_ptr(), kp, q_out.data_ptr(), kop, pp, fp, strides, B, H, Hkv, N, d,
-                         rot, 1 if interleaved else 0, 1 if inverse else 0, float(amplitude),
+    (qp, qs), (qop, qos) = _rows(q, "q", q.shape), _rows(q_out, "q_out", q.shape)
+    Hkv, kp, kop, ks, kos = 0, None, None, (0, 0, 0), (0, 0, 0)
+    if k is not None:
+        Hkv = _dims_of(k, "k")[1]
+        (kp, ks), (kop, kos) = (_rows(t, n, (B, Hkv, N, d)) for t, n in ((k, "k"), (k_out, "k_out")))
+    strides = _STRIDES(*qs, *ks, *qos, *kos)
+    _check(lib().fa_rope(qp, kp, qop, kop, pp, fp, strides, B, H, Hkv, N, d, rot,
+                         1 if interleaved else 0, 1 if inverse else 0, float(amplitude),
                          _stream(stream)), "fa_rope")
 
 
@@ -945,30 +940,25 @@ def fa_rope_append(q, k, v, q_out, k_pages, v_pages, positions, slots, freqs,
     """q [B, H, N, d] turned into q_out; k [B, Hkv, N, d] turned, and v, into the pages at
     slots int64 [B, N] (negative: not written); a packed batch is B = 1.  Any strides over
     B, H and N of q, k, v and q_out."""
+    if _done(binding().rope_append(q, k, v, q_out, k_pages, v_pages, positions, slots, freqs,
+                                   interleaved, amplitude, kv_scales, _handle(stream)),
+             "fa_rope_append"):
+        return
     import torch
-    cur = _current_index()
-    B, H, N, d, rot, pp, fp = _rope_args(q.shape, positions, freqs, cur)
+    B, H, N, d, rot, pp, fp = _rope_args(q, positions, freqs)
     pool = k_pages.shape
     if len(pool) != 4 or pool[3] != d:
         raise ValueError(f"k_pages must be 4-D [n_pages, Hkv, page_size, {d}]")
     kd = torch.bfloat16 if kv_scales is None else torch.float8_e4m3fn
-    shape = (B, pool[1], N, d)
-    if not (_rows_ok(q, q.shape, cur) and _rows_ok(q_out, q.shape, cur) and
-            _rows_ok(k, shape, cur) and _rows_ok(v, shape, cur)):
-        _explain_rows((q, "q", q.shape), (q_out, "q_out", q.shape), (k, "k", shape),
-                      (v, "v", shape))
-    if not (k_pages.dtype is kd and v_pages.dtype is kd and v_pages.shape == pool and
-            k_pages.get_device() == cur and v_pages.get_device() == cur and
-            k_pages.is_contiguous() and v_pages.is_contiguous() and
-            slots.dtype is torch.int64 and slots.shape == (B, N) and slots.get_device() == cur and
-            slots.is_contiguous()):
-        _explain((k_pages, "k_pages", kd, pool), (v_pages, "v_pages", kd, pool),
-                 (slots, "slots", torch.int64, (B, N)))
-    strides = _STRIDES(*q.stride()[:3], *k.stride()[:3], *v.stride()[:3], *q_out.stride()[:3])
-    _check(lib().fa_rope_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(),
-                                k_pages.data_ptr(), v_pages.data_ptr(),
-                                _scales(kv_scales, pool, cur), pp, slots.data_ptr(), fp, strides, B,
-                                H, pool[1], N, pool[0], pool[2], d, rot, 1 if interleaved else 0,
+    kv = (B, pool[1], N, d)
+    rows = [_rows(*x) for x in ((q, "q", q.shape), (k, "k", kv), (v, "v", kv),
+                                (q_out, "q_out", q.shape))]
+    strides = _STRIDES(*(x for _, s in rows for x in s))
+    _check(lib().fa_rope_append(*(x for x, _ in rows), _ptr(k_pages, "k_pages", kd, pool),
+                                _ptr(v_pages, "v_pages", kd, pool),
+                                _scales(kv_scales, pool, _current_index()), pp,
+                                _ptr(slots, "slots", torch.int64, (B, N)), fp, strides, B, H,
+                                pool[1], N, pool[0], pool[2], d, rot, 1 if interleaved else 0,
                                 float(amplitude), _stream(stream)), "fa_rope_append")
 
 
@@ -1062,35 +1052,15 @@ def fa_bwd_cross_varlen(q, k, v, o, dout, lse, dq, dk, dv, workspace, cu_q, cu_k
 def fa_fwd_cross_decode(q, k, v, o, lse, workspace, causal: bool, scale: float, kv_lens=None,
                         stream=None) -> None:
     """fa_fwd_cross for a few queries a sequence, (H / Hkv) * Nq <= 32."""
-    import torch
-    bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
-    cur = _current_index()
-    qs, ks = q.shape, k.shape
-    if len(qs) != 4 or len(ks) != 4:
-        raise ValueError("q and k must be 4-D [B, H(kv), N, d]")
-    B, H, Nq, d = qs
-    if ks[0] != B or ks[3] != d:
-        raise ValueError(f"q {tuple(qs)} and k {tuple(ks)} disagree")
-    if not (q.dtype is bf and k.dtype is bf and v.dtype is bf and v.shape == ks and
-            o.dtype is bf and o.shape == qs and lse.dtype is f32 and lse.shape == (B, H, Nq) and
-            q.get_device() == cur and k.get_device() == cur and v.get_device() == cur and
-            o.get_device() == cur and lse.get_device() == cur and q.is_contiguous() and
-            k.is_contiguous() and v.is_contiguous() and o.is_contiguous() and
-            lse.is_contiguous() and
-            (kv_lens is None or (kv_lens.dtype is i32 and kv_lens.shape == (B,) and
-                                 kv_lens.get_device() == cur and kv_lens.is_contiguous()))):
-        _explain((q, "q", bf, qs), (k, "k", bf, ks), (v, "v", bf, ks), (o, "o", bf, qs),
-                 (lse, "lse", f32, (B, H, Nq)),
-                 *(() if kv_lens is None else ((kv_lens, "kv_lens", i32, (B,)),)))
-    if workspace.get_device() == cur and workspace.is_contiguous():
-        wp, wb = workspace.data_ptr(), workspace.nbytes
-    else:
-        wp, wb = _ws(workspace)
-    _check(lib().fa_fwd_cross_decode(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-                                     lse.data_ptr(),
-                                     None if kv_lens is None else kv_lens.data_ptr(), wp, wb, B, H,
-                                     ks[1], Nq, ks[2], d, 1 if causal else 0, float(scale),
-                                     _stream(stream)), "fa_fwd_cross_decode")
+    if _done(binding().cross_decode(q, k, v, o, lse, workspace, causal, scale, kv_lens,
+                                    _handle(stream)), "fa_fwd_cross_decode"):
+        return
+    qs, ks, ls, sizes, lens = _cross_dims(q, k, kv_lens)
+    wp, wb = _ws(workspace)
+    _check(lib().fa_fwd_cross_decode(_bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v", ks),
+                                     _bf16(o, "o", qs), _f32(lse, "lse", ls), lens, wp, wb, *sizes,
+                                     int(bool(causal)), float(scale), _stream(stream)),
+           "fa_fwd_cross_decode")
 
 
 def _workspace_of(size_of, where, *sizes):

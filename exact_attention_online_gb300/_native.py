@@ -1,14 +1,18 @@
 """Build and load libfa.so, the sm_103a CUDA library behind the C ABI in
-include/fa.h.  The library is built in-tree (``_lib/libfa.so``) with nvcc;
-nothing here falls back to any other implementation: if the library is missing
-or cannot be loaded, ``lib()`` raises."""
+include/fa.h, and fa_binding.so, the compiled part of the Python binding.  Both
+are built in-tree (``_lib/``), with nvcc and g++; nothing here falls back to any
+other implementation: if one is missing or cannot be loaded, ``lib()`` or
+``binding()`` raises."""
 from __future__ import annotations
 
 import concurrent.futures as cf
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 import threading
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +22,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_lib")
 OBJ_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(OUT_DIR, "libfa.so")
+BINDING_PATH = os.path.join(OUT_DIR, "fa_binding.so")
 
 SOURCES = ["api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_noalloc.cu", "fa_fp8.cu", "fa_decode.cu",
            "fa_diag.cu", "fa_kvcache.cu", "fa_paged.cu", "fa_tables.cu", "fa_rope.cu",
@@ -29,6 +34,7 @@ NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
 
 _lock = threading.Lock()
 _lib = None
+_binding = None
 
 
 def nvcc() -> str:
@@ -45,8 +51,31 @@ def _stale(target: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _binding_commands():
+    """(compile, link) of fa_binding.so, which looks into torch's tensors: g++ with torch's
+    headers and libraries, and libfa.so beside it."""
+    import torch
+    cxx = shutil.which("g++")
+    if not cxx:
+        raise RuntimeError("g++ not found: it is needed to build fa_binding.so")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    obj = os.path.join(OBJ_DIR, "binding.o")
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    heads = os.path.join(os.path.dirname(torch.__file__), "include")
+    inc = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(cuda, "include"), heads,
+           os.path.join(heads, "torch", "csrc", "api", "include")]
+    compile_ = [cxx, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-c",
+                os.path.join(CSRC, "binding.cpp"), "-o", obj]
+    for d in inc:
+        compile_ += ["-isystem" if d != INCLUDE else "-I", d]
+    link = [cxx, "-shared", obj, "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10",
+            "-lc10_cuda", "-L", OUT_DIR, "-l:libfa.so", "-Wl,-rpath,$ORIGIN",
+            "-Wl,-rpath," + libs]
+    return compile_, link
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile every .cu for sm_103a (in parallel) and link libfa.so."""
+    """Compile every .cu for sm_103a (in parallel) and link libfa.so; then the binding."""
     os.makedirs(OUT_DIR, exist_ok=True)
     os.makedirs(OBJ_DIR, exist_ok=True)
     hdrs = [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(INCLUDE, "fa.h")]
@@ -59,11 +88,16 @@ def build(force: bool = False, verbose: bool = False) -> str:
         objs.append(op)
         if force or _stale(op, [sp] + hdrs):
             jobs.append([cc] + NVCC_FLAGS + ["-c", sp, "-o", op])
+    compile_, link = _binding_commands()
+    obj = os.path.join(OBJ_DIR, "binding.o")
+    if force or _stale(obj, [os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "fa.h")]):
+        jobs.append(compile_)
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"{os.path.basename(cmd[0])} failed:\n{' '.join(cmd)}\n{r.stdout}\n"
+                               f"{r.stderr}")
         if verbose:
             print(r.stdout + r.stderr)
 
@@ -73,6 +107,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
         tmp = f"{LIB_PATH}.{os.getpid()}.tmp"
         run([cc] + ARCH + ["-shared", "-o", tmp] + objs)
         os.replace(tmp, LIB_PATH)
+    if force or jobs or _stale(BINDING_PATH, [obj]):
+        tmp = f"{BINDING_PATH}.{os.getpid()}.tmp"
+        run(link + ["-o", tmp])
+        os.replace(tmp, BINDING_PATH)
     return LIB_PATH
 
 
@@ -213,6 +251,26 @@ def lib() -> ctypes.CDLL:
                     "exact_attention_online_gb300.build() (nvcc, sm_103a)")
             _lib = _bind(ctypes.CDLL(LIB_PATH))
         return _lib
+
+
+def binding():
+    """The loaded fa_binding.so.  Raises if it was not built (call build())."""
+    global _binding
+    if _binding is not None:
+        return _binding
+    lib()
+    import torch  # noqa: F401  (its libraries have to be there first)
+    with _lock:
+        if _binding is None:
+            if not os.path.exists(BINDING_PATH):
+                raise RuntimeError(f"{BINDING_PATH} is missing: build it with "
+                                   "exact_attention_online_gb300.build()")
+            loader = importlib.machinery.ExtensionFileLoader("fa_binding", BINDING_PATH)
+            spec = importlib.util.spec_from_file_location("fa_binding", BINDING_PATH, loader=loader)
+            module = importlib.util.module_from_spec(spec)
+            loader.exec_module(module)
+            _binding = module
+        return _binding
 
 
 # Every symbol include/fa.h declares.
