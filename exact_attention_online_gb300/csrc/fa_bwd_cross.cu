@@ -1,0 +1,778 @@
+// dK/dV kernel of the backward for d = 64 and keys of another length than the
+// queries.  The mathematics, the work items (one 128-key block of one kv head) and
+// the tables are those of fa_bwd.cu:
+//   S^T  = K_j Q_i^T,  dP^T = V_j dO_i^T,  P^T = 2^(S^T c - lse2),
+//   dS^T = P^T o (dP^T - D),  dV += P^T dO_i,  dK += dS^T Q_i,  dQ_i = dS K_j
+// with 128 queries a step.  The kernel there keeps one step in flight at d = 64, and
+// its tensor pipe waits for the hand-offs most of the time (22 % of its cycles busy on
+// 400 queries to up to 1500 keys).  Here:
+//   - S^T has two buffers.  S^T of the next step is issued as soon as P^T of this one
+//     has been taken, across work items too, so the compute warps go from dS^T of one
+//     step to P^T of the next without waiting for the MMAs between.
+//   - dQ_i takes the half of its step's S^T buffer that P^T (bf16, half as wide) leaves
+//     free, which is what makes room for the second buffer:
+//       TMEM  dK 0-63 | dV 64-127 | S^T_0 128-255 | S^T_1 256-383 | dP^T 384-511
+//   - K_j and V_j have two slots, and an item's dK and dV are read out between P^T and
+//     dS^T of the next item's first step, when their last MMAs have long completed.
+//     Short queries make short items (four steps here), whose ends would otherwise
+//     stand beside each other.
+//   - Q and dO stream through rings of their own, as Q is needed a step earlier.
+//   - Sixteen compute warps instead of eight, which wait for one another's latencies
+//     less (171 us with eight, 164.5 with sixteen, on the shape above), and arrive on a
+//     barrier by one lane.
+// On that shape the backward takes 157 us, 198 with the kernel of fa_bwd.cu.  A step takes
+// about 4000 cycles.  Its MMAs alone take 1710 (an SS MMA of 128 x 64 x 16 reads 6 KB of
+// shared memory and takes 54 cycles, not 32); the rest is the chain dS^T -> dK, dQ -> dP^T ->
+// dS^T, whose first products wait behind S and dV in the tensor pipe's queue.  dP before
+// dK and dQ, with the dS^T tile guarded by dQ's barrier, measured 3 % slower.
+//
+// Order on the tensor pipe, by two issuing threads:
+//   A:  S(k+1) once dQ(k-1) has been read out of its buffer, then dV(k)
+//   B:  dK(k), dQ(k), then dP(k+1): its completion also frees the dS^T tile
+//
+// Warps: 0-15 compute (one key row per thread, four warps a row), 16 loads, 17 issuer
+// A, 18 issuer B, 19 clears the rows behind a sequence, 20-23 read dQ out.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+
+#include "bwd_parts.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int D = 64;
+constexpr int BR = 128;               // queries a step
+constexpr int kBN = kBwdKeys;
+constexpr int kThreads = 768;
+constexpr int kComputeWarps = 16;
+// Register split (setmaxnreg) of the launch's 768 x 80:
+// 512 x 88 + 128 x 64 + 128 x 64 = 61440.
+constexpr int kRegsCompute = 88, kRegsReadout = 64, kRegsControl = 64;
+constexpr int kRegsNeeded = 512 * kRegsCompute + 128 * kRegsReadout + 128 * kRegsControl;
+
+constexpr int kListSeqs = 512;                    // sequences whose key blocks are listed
+constexpr int NQ = 3, NO = 3;                     // stages of Q, of dO
+constexpr int kTile = 128 * D * 2;                // K_j, V_j, Q_i or dO_i
+constexpr int kExt = BR * 32;                     // a step's -LSE or -D table
+constexpr int kOffKV = 0;                         // two slots of K_j, V_j
+constexpr int kOffQ = kOffKV + 4 * kTile;
+constexpr int kOffO = kOffQ + NQ * kTile;
+constexpr int kOffDS = kOffO + NO * kTile;        // [2 chunks of 64 queries][128 keys]
+constexpr int kOffOnes = kOffDS + 2 * kTile;
+constexpr int kOffLse = kOffOnes + kBN * 32;      // NQ tables
+constexpr int kOffD = kOffLse + NQ * kExt;        // NO tables
+constexpr int kSmem = kOffD + NO * kExt + 1024;
+static_assert(kSmem <= 226 * 1024, "shared memory of one CTA");
+
+constexpr uint32_t kColDK = 0, kColDV = 64, kColDP = 384;
+__device__ __forceinline__ uint32_t col_s(uint32_t k) { return 128 + 128 * (k & 1); }
+
+// A bounded wait in few instructions, as the roles' code already misses the instruction
+// caches (400 queries to up to 1500 keys: 178.7 us with the library's waits, 168.1 with
+// these).  The first that gives up leaves its number in `abort`, which stops the others
+// and is reported at the end.  A poll ends after a microsecond, so that the limit is at
+// most about two seconds.
+constexpr uint32_t kMostPolls = 1u << 21;
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int site,
+                                     volatile int* abort) {
+    const uint32_t a = smem_u32(bar);
+#pragma unroll 1
+    for (uint32_t n = 0; !mbar_try_wait_us(a, parity); ++n)
+        if (n >= kMostPolls || ((n & 63) == 63 && *abort)) {
+            if (!*abort) *abort = site;
+            return false;
+        }
+    return true;
+}
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int site,
+                                          volatile int* abort) {
+    return __all_sync(0xffffffffu, wait(bar, parity, site, abort));
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+fa_bwd_cross64_kernel(const __grid_constant__ CUtensorMap tm_q,
+                      const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v,
+                      const __grid_constant__ CUtensorMap tm_do, const BwdParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    // Barriers, by what completes a phase (k: step, nb: item).  Where the next phase but
+    // one may complete before a waiter has looked, there are two in turn.
+    __shared__ uint64_t bar_kv[2], bar_kv_free[2];        // K_j, V_j landed; no longer read
+    __shared__ uint64_t bar_kv_ready[2];                  // ... and rows past the keys cleared
+    __shared__ uint64_t bar_q[NQ], bar_q_free[NQ], bar_o[NO], bar_o_free[NO];
+    __shared__ uint64_t bar_qt[NQ], bar_ot[NO];           // packed: landed and cleared
+    __shared__ uint64_t bar_s[2], bar_dp, bar_p, bar_ds, bar_dq[2], bar_dq_free[2];
+    __shared__ uint64_t bar_done, bar_acc_free;           // an item's MMAs; dK, dV read out
+    __shared__ uint64_t bar_item[2], bar_item_free[2], bar_drain[2];
+    __shared__ BwdCta item_sh[2];                         // n_it < 0: no more work
+    __shared__ uint32_t tmem_base_sh;
+    __shared__ int abort_sh, drain_sh;                    // drain_sh: for waits that run to their limit
+    __shared__ int list_sh[kListSeqs + 1];                // key blocks of the sequences before
+    constexpr int kConsumers = 16 + 4 + 2 + 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool packed = p.cu_seqlens != nullptr, causal = p.causal != 0;
+
+    bwd_fill_ones(smem + kOffOnes, p.scale_log2);
+    if (threadIdx.x == 0) {
+        abort_sh = drain_sh = 0;
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&bar_kv[s], 1);
+            mbar_init(&bar_kv_free[s], 2);
+            mbar_init(&bar_kv_ready[s], 1);
+            mbar_init(&bar_s[s], 1);
+            mbar_init(&bar_dq[s], 1);
+            mbar_init(&bar_dq_free[s], 4);
+            mbar_init(&bar_item[s], 1);
+            mbar_init(&bar_item_free[s], kConsumers);
+            mbar_init(&bar_drain[s], 1);
+        }
+        for (int s = 0; s < NQ; ++s) {
+            mbar_init(&bar_q[s], 1);
+            mbar_init(&bar_q_free[s], 1);
+            mbar_init(&bar_qt[s], 1);
+        }
+        for (int s = 0; s < NO; ++s) {
+            mbar_init(&bar_o[s], 1);
+            mbar_init(&bar_o_free[s], 2);
+            mbar_init(&bar_ot[s], 1);
+        }
+        mbar_init(&bar_dp, 1);
+        // a warp arrives by one lane: 512 arrivals on one word take their turns
+        mbar_init(&bar_p, kComputeWarps);
+        mbar_init(&bar_ds, kComputeWarps);
+        mbar_init(&bar_done, 2);
+        mbar_init(&bar_acc_free, kComputeWarps);
+        fence_mbar_init();
+    }
+    if (warp == 17) {
+        tmem_alloc(&tmem_base_sh, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base_sh;
+
+    // The item of rank n, taken apart by the producer, for a converged warp: false if the
+    // wait gave up or there is no more work.
+    auto next_item = [&](int n, BwdCta& cta) -> bool {
+        cta.n_it = 0;
+        if (!wait_warp(&bar_item[n & 1], (n >> 1) & 1, 120, &abort_sh)) return false;
+        cta = item_sh[n & 1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_item_free[n & 1]);
+        return cta.n_it > 0;
+    };
+
+    auto arrive_warp = [&](uint64_t* bar) {      // all lanes have fenced what they wrote
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+    };
+
+    if (warp < 16) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsCompute));
+        // ------------------------------------------------------------ compute
+        // warp w: TMEM lane quarter w % 4 (32 key rows), query columns 32 (w / 4) ..
+        const int quarter = warp & 3, cg = warp >> 2;
+        const int rl = quarter * 32 + lane;
+        const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
+        const float c = p.scale_log2;
+        uint8_t* const ds_row = smem + kOffDS + (cg >> 1) * kTile + rl * 128;
+        const int u0 = (cg & 1) * 4;                 // first 16-byte unit of the row
+        bool ok = true;
+        // The item whose dK (groups 0, 1) or dV (2, 3) is to be read out: its first row in
+        // this warp, how many of the 32 are in the tensor, and how many of those are keys'
+        bool pending = false;
+        uint4* rows_of = nullptr;
+        int rows_in = 0, rows_there = 0;
+        uint32_t k = 0;                              // steps so far
+        int nb = 0;                                  // working items so far
+        uint32_t acc[16];                            // its bf16 values, 32 columns of a row
+        auto read_out = [&](int nb_) -> bool {
+            if (!wait_warp(&bar_done, nb_ & 1, 121, &abort_sh)) return false;
+            tc_fence_after();
+            const float mul = cg > 1 ? 1.0f : p.scale;
+            uint32_t r[32];
+            tmem_ld32(lane_addr + cg * 32, r);                      // dK 0-63 | dV 64-127
+            tmem_ld_wait(r);
+            tc_fence_before();
+            arrive_warp(&bar_acc_free);
+            const bool there = lane < rows_there;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                acc[e] = there ? pack_bf16x2(__uint_as_float(r[2 * e]) * mul,
+                                             __uint_as_float(r[2 * e + 1]) * mul)
+                               : 0u;
+            return true;
+        };
+        // Four lanes exchange their rows' 16-byte units, so that they store a row's 64 bytes
+        // together (a row a thread took 3200 cycles an item).
+        auto store_rows = [&]() {
+#pragma unroll
+            for (int x = 1; x < 4; x <<= 1)
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    if (!(u & x))
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t &a = acc[u * 4 + e], &b = acc[(u | x) * 4 + e];
+                            const uint32_t give = lane & x ? a : b;
+                            const uint32_t got = __shfl_xor_sync(0xffffffffu, give, x);
+                            if (lane & x) a = got;
+                            else b = got;
+                        }
+            // unit j now is unit lane % 4 of row lane / 4 * 4 + j
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int row = (lane & ~3) + j;
+                if (row < rows_in)
+                    rows_of[row * (D / 8) + u0 + (lane & 3)] =
+                        make_uint4(acc[4 * j], acc[4 * j + 1], acc[4 * j + 2], acc[4 * j + 3]);
+            }
+        };
+        for (int n = 0; ok; ++n) {
+            BwdCta cta;
+            if (!next_item(n, cta)) break;
+            const int key = cta.jblk * kBN + rl;
+            const bool key_valid = key < cta.seq_len;
+            const int q_end = (cta.i_start + cta.n_i) * BR;
+            int q0 = cta.i_start * BR;                   // of the step; every head in turn
+#pragma unroll 1
+            for (int it = 0; it < cta.n_it; ++it, ++k) {
+                const bool need_mask = (causal && q0 + cta.off < cta.jblk * kBN + kBN - 1) ||
+                                       cta.jblk * kBN + kBN > cta.seq_len;
+                const int key_lim = causal ? key - cta.off - q0 : -1;   // visible: e >= key_lim
+                const uint32_t s_addr = lane_addr + col_s(k);
+                if (!wait_warp(&bar_s[k & 1], (k >> 1) & 1, 122, &abort_sh)) { ok = false; break; }
+                tc_fence_after();
+                // P^T = 2^(S'^T c), S'^T = S^T - LSE log2(e) / c from the tensor core: fp32
+                // kept for dS^T, bf16 into the first half of the buffer, which is the
+                // other warps' S^T too: all of it is read before any is written.
+                uint32_t sr[32];
+                tmem_ld32(s_addr + cg * 32, sr);
+                tmem_ld_wait(sr);
+                tc_fence_before();
+                named_bar_sync(2 + quarter, 128);
+                tc_fence_after();
+                if (need_mask) {   // masked here, so that there is one copy of the long loop
+                    const int lim = key_valid ? key_lim - cg * 32 : BR;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (e < lim) sr[e] = 0xff800000u;
+                }
+                float pf[32];
+                const uint64_t c2 = f2(c, c);
+                uint32_t pk[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    float x0, x1;
+                    f2_split(f2_mul(f2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])),
+                                    c2), x0, x1);
+                    pf[2 * e] = ex2(x0);
+                    pf[2 * e + 1] = ex2(x1);
+                    pk[e] = pack_bf16x2(pf[2 * e], pf[2 * e + 1]);
+                }
+                tmem_st16(s_addr + cg * 16, pk);
+                tmem_st_wait();
+                tc_fence_before();
+                arrive_warp(&bar_p);
+                // The item before: its dK, dV are taken out of tensor memory here, so that
+                // its successor's may follow, and stored after dS^T, which others wait for.
+                if (pending && !(ok = read_out(nb - 1))) break;
+                // dS^T = P^T o (dP^T - D) -> bf16, swizzled [key][query] tile; dP^T - D comes
+                // from the tensor core, and its completion means that the step before's
+                // dK and dQ MMAs have read the tile
+                if (!wait_warp(&bar_dp, k & 1, 123, &abort_sh)) { ok = false; break; }
+                tc_fence_after();
+                uint32_t dsk[16];
+#pragma unroll
+                for (int ch = 0; ch < 2; ++ch) {
+                    uint32_t dpr[16];
+                    tmem_ld(lane_addr + kColDP + cg * 32 + ch * 16, dpr);
+                    tmem_ld_done(dpr);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        float d0, d1;
+                        f2_split(f2_mul(f2(pf[ch * 16 + 2 * e], pf[ch * 16 + 2 * e + 1]),
+                                        f2(__uint_as_float(dpr[2 * e]),
+                                           __uint_as_float(dpr[2 * e + 1]))), d0, d1);
+                        dsk[ch * 8 + e] = pack_bf16x2(d0, d1);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    *reinterpret_cast<uint4*>(ds_row + (((u0 + u) ^ (rl & 7)) * 16)) =
+                        make_uint4(dsk[u * 4 + 0], dsk[u * 4 + 1], dsk[u * 4 + 2], dsk[u * 4 + 3]);
+                tc_fence_before();   // the dP^T reads precede the next dP^T MMA
+                fence_proxy_async_smem();
+                arrive_warp(&bar_ds);
+                if (pending) store_rows();
+                pending = false;
+                if ((q0 += BR) == q_end) q0 = cta.i_start * BR;
+            }
+            const int key0 = key - lane;
+            rows_there = min(32, cta.seq_len - key0);
+            rows_in = packed ? rows_there : min(32, p.Nk - key0);
+            rows_of = reinterpret_cast<uint4*>(
+                (cg > 1 ? p.dv : p.dk) + ((size_t)cta.z_kv * p.krows + cta.ktok0 + key0) * D);
+            pending = true;
+            ++nb;
+        }
+        if (ok && pending && read_out(nb - 1)) store_rows();
+    } else if (warp >= 20) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsReadout));
+        // ------------------------------------------------------- dQ read-out
+        // Added to the accumulator from registers: a copy that adds takes some 1500 cycles
+        // until it has read its 4 KB of shared memory, and the pieces of a step waited for
+        // one another (3300 cycles a step).  A thread holds
+        // 2 + 2 columns of 16 of a row, and the accumulator keeps these 16 in the order of
+        // the threads, so that each adds four neighbours and four threads 64 bytes.
+        const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        bool ok = true;
+        uint32_t k = 0;
+        for (int n = 0; ok; ++n) {
+            BwdCta cta;
+            if (!next_item(n, cta)) break;
+            const int i_end = cta.i_start + cta.n_i;
+            int i = cta.i_start;                         // of the step; every head in turn
+            float* head = p.dq_acc +
+                          ((size_t)(cta.b * p.H + cta.g * p.G) * p.Np + (warp & 3) * 32 + lane / 4) * D +
+                          lane % 4 * 4;
+#pragma unroll 1
+            for (int it = 0; it < cta.n_it; ++it, ++k) {
+                float* const to = head + (size_t)i * (BR * D);
+                if (++i == i_end) {
+                    i = cta.i_start;
+                    head += (size_t)p.Np * D;
+                }
+                if (!wait_warp(&bar_dq[k & 1], (k >> 1) & 1, 124, &abort_sh)) { ok = false; break; }
+                tc_fence_after();
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t r[32];
+                    tmem_ld16x64(lane_addr + ((uint32_t)(16 * h) << 16) + col_s(k) + 64, r);
+                    tmem_ld_wait(r);
+                    if (h) {
+                        tc_fence_before();
+                        arrive_warp(&bar_dq_free[k & 1]);
+                    }
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int x = 0; x < 4; x += 2)           // rows lane / 4, and 8 further
+                            red_add_f32x4(to + (h * 16 + x * 4) * D + c * 16, r[8 * c + x],
+                                          r[8 * c + x + 1], r[8 * c + 4 + x], r[8 * c + 5 + x]);
+                }
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
+        if (warp == 16) {
+            // ------------------------------------------------------ loads
+            // Work items: the key blocks that have keys and queries, listed by sequence
+            // (in a batch too large for the list, all of them, and the empty ones are
+            // passed over).  A CTA asks for the next number an item ahead.
+            const int n_kblk = (p.Nk + kBN - 1) / kBN, B = p.n_bg / p.Hkv;
+            const bool listed = B <= kListSeqs;
+            int n_work = p.n_items;
+            if (listed) {
+                const int per = (B + 31) / 32, b0 = lane * per, b1 = min(B, b0 + per);
+                int mine = 0;
+#pragma unroll 1
+                for (int b = b0; b < b1; ++b) {
+                    const BwdCta c = bwd_cta_cross(p, BR, b * p.Hkv, 0);
+                    if (c.q_len > 0) mine += (c.seq_len + kBN - 1) / kBN * p.Hkv;
+                    list_sh[b + 1] = mine;
+                }
+                int upto = mine;
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, upto, off);
+                    if (lane >= off) upto += y;
+                }
+#pragma unroll 1
+                for (int b = b0; b < b1; ++b) list_sh[b + 1] += upto - mine;
+                if (lane == 0) list_sh[0] = 0;
+                n_work = __shfl_sync(0xffffffffu, upto, 31);
+                __syncwarp();
+            }
+            if (lane == 0) {
+                tma_prefetch_desc(&tm_q);
+                tma_prefetch_desc(&tm_do);
+                // The next item is named to the others and its K_j, V_j asked for before
+                // this one's third step, whose stage comes free when the item before has
+                // ended, as the slot does.
+                int k = 0, nb = 0;             // steps loaded; items named
+                bool ok = true;
+                BwdCta cta;
+                int ahead = atomicAdd(p.work, 1);
+                auto take = [&](BwdCta& to) -> bool {
+                    if (nb >= 2 && !wait(&bar_item_free[nb & 1], ((nb >> 1) - 1) & 1, 125, &abort_sh))
+                        return false;
+                    do {
+                        const int old = ahead;
+                        ahead = atomicAdd(p.work, 1);
+                        if (old >= n_work) {
+                            // Every CTA asks twice too often; who asked last leaves the
+                            // counter zero for the next launch.
+                            if (ahead == n_work + 2 * (int)gridDim.x - 1) *p.work = 0;
+                            to.n_it = -1;
+                            break;
+                        }
+                        if (listed) {
+                            int lo = 0, hi = B - 1;              // its sequence
+                            while (lo < hi) {
+                                const int mid = (lo + hi + 1) >> 1;
+                                if (list_sh[mid] <= old) lo = mid;
+                                else hi = mid - 1;
+                            }
+                            const int blocks = (list_sh[lo + 1] - list_sh[lo]) / p.Hkv;
+                            const int at = old - list_sh[lo], g = at / blocks;
+                            to = bwd_cta_cross(p, BR, lo * p.Hkv + g, at - g * blocks);
+                        } else {
+                            to = bwd_cta_cross(p, BR, old / n_kblk, old % n_kblk);
+                        }
+                    } while (to.idle || to.n_it == 0);
+                    item_sh[nb & 1] = to;
+                    mbar_arrive(&bar_item[nb & 1]);
+                    if (to.n_it < 0) return true;
+                    const int slot = nb & 1;
+                    if (nb >= 2 && !wait(&bar_kv_free[slot], ((nb >> 1) - 1) & 1, 126, &abort_sh))
+                        return false;
+                    uint8_t* const kv = smem + kOffKV + slot * 2 * kTile;
+                    mbar_arrive_expect_tx(&bar_kv[slot], 2 * kTile);
+                    tma_load_3d(kv, &tm_k, &bar_kv[slot], 0, to.ktok0 + to.jblk * kBN, to.z_kv);
+                    tma_load_3d(kv + kTile, &tm_v, &bar_kv[slot], 0, to.ktok0 + to.jblk * kBN,
+                                to.z_kv);
+                    ++nb;
+                    return true;
+                };
+                ok = take(cta);
+                while (ok && cta.n_it > 0) {
+                    BwdCta then;
+                    int hq = cta.g * p.G, i = cta.i_start;   // of the step
+        #pragma unroll 1
+            for (int it = 0; it < cta.n_it; ++it, ++k) {
+                        if (it == 2 && !(ok = take(then))) break;
+                        const int sq = k % NQ, so = k % NO;
+                        const int bh = cta.b * p.H + hq;
+                        const size_t xrow = ((size_t)bh * p.Np + (size_t)i * BR) * kExtCols;
+                        if (k >= NQ && !wait(&bar_q_free[sq], (k / NQ - 1) & 1, 127, &abort_sh)) {
+                            ok = false;
+                            break;
+                        }
+                        mbar_arrive_expect_tx(&bar_q[sq], kTile + kExt);
+                        tma_load_3d(smem + kOffQ + sq * kTile, &tm_q, &bar_q[sq], 0,
+                                    cta.tok0 + i * BR, packed ? hq : bh);
+                        bulk_load(smem + kOffLse + sq * kExt, p.lse_ext + xrow, kExt, &bar_q[sq]);
+                        if (k >= NO && !wait(&bar_o_free[so], (k / NO - 1) & 1, 128, &abort_sh)) {
+                            // this step's Q is in flight, and not in the drain below
+                            wait(&bar_q[sq], (k / NQ) & 1, 129, &drain_sh);
+                            ok = false;
+                            break;
+                        }
+                        mbar_arrive_expect_tx(&bar_o[so], kTile + kExt);
+                        tma_load_3d(smem + kOffO + so * kTile, &tm_do, &bar_o[so], 0,
+                                    cta.tok0 + i * BR, packed ? hq : bh);
+                        bulk_load(smem + kOffD + so * kExt, p.d_ext + xrow, kExt, &bar_o[so]);
+                        if (++i == cta.i_start + cta.n_i) {
+                            i = cta.i_start;
+                            ++hq;
+                        }
+                    }
+                    if (ok && cta.n_it <= 2) ok = take(then);
+                    cta = then;
+                }
+                if (abort_sh) {   // drain the copies still in flight (bounded)
+                    for (int x = max(0, nb - 2); x < nb; ++x)
+                        wait(&bar_kv[x & 1], (x >> 1) & 1, 129, &drain_sh);
+                    for (int x = max(0, k - NQ); x < k; ++x)
+                        wait(&bar_q[x % NQ], (x / NQ) & 1, 129, &drain_sh);
+                    for (int x = max(0, k - NO); x < k; ++x)
+                        wait(&bar_o[x % NO], (x / NO) & 1, 129, &drain_sh);
+                }
+            }
+        } else if (warp == 17 || warp == 18) {
+            // ------------------------------------------------------ MMAs
+            // The warp stays together and one elected lane issues, by a predicate:
+            // descriptors then travel in uniform registers.
+            constexpr uint32_t id_s = idesc_bf16_f32(128, BR, false, false);
+            constexpr uint32_t id_kv = idesc_bf16_f32(128, D, false, true);
+            constexpr uint32_t id_dq = idesc_bf16_f32(128, D, true, true);
+            const uint32_t base = smem_u32(smem);
+            const uint64_t onesd = sdesc_plain(base + kOffOnes, 128, 256);
+            uint64_t* const q_ready = packed ? bar_qt : bar_q;
+            uint64_t* const o_ready = packed ? bar_ot : bar_o;
+            const bool is_a = warp == 17, leader = elect_one();
+            bool ok = true, done = false;
+            int n = 0, nb = -1, it = 0, n_it = 0;   // items taken, working ones; step of n_it
+            // On to the next step (done at the end); an item's first one waits for its
+            // K_j, V_j.
+            auto next = [&]() -> bool {
+                if (++it < n_it) return true;
+                BwdCta cta;
+                if (!next_item(n++, cta)) {
+                    done = true;
+                    return cta.n_it < 0;             // (0: the wait gave up)
+                }
+                n_it = __shfl_sync(0xffffffffu, cta.n_it, 0);
+                it = 0;
+                ++nb;
+                return wait_warp(&bar_kv_ready[nb & 1], (nb >> 1) & 1, 130, &abort_sh);
+            };
+            auto kv_at = [&](int slot) { return base + kOffKV + (slot & 1) * 2 * kTile; };
+            auto issue_s = [&](uint32_t k) -> bool {   // S^T = K_j Q_i^T - LSE log2(e) / c
+                const int sq = k % NQ;
+                // (dQ(k - 2) lies in this buffer)
+                if (!wait_warp(&q_ready[sq], (k / NQ) & 1, 131, &abort_sh) ||
+                    (k >= 2 && !wait_warp(&bar_dq_free[k & 1], ((k >> 1) - 1) & 1, 132, &abort_sh)))
+                    return false;
+                tc_fence_after();
+                const uint64_t kd = sdesc_sw128(kv_at(nb), 16, 1024);
+                const uint64_t qd = sdesc_sw128(base + kOffQ + sq * kTile, 16, 1024);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    mma_ss_if(leader, tmem + col_s(k), kd + kmajor_step(kk, 0),
+                              qd + kmajor_step(kk, 0), id_s, kk > 0);
+                mma_ss_if(leader, tmem + col_s(k), onesd,
+                          sdesc_plain(base + kOffLse + sq * kExt, 128, 256), id_s, 1u);
+                mma_commit_if(leader, &bar_s[k & 1]);
+                return true;
+            };
+            auto issue_dp = [&](uint32_t k) -> bool {  // dP^T - D = V_j dO_i^T - D
+                const int so = k % NO;
+                if (!wait_warp(&o_ready[so], (k / NO) & 1, 133, &abort_sh)) return false;
+                tc_fence_after();
+                const uint64_t vd = sdesc_sw128(kv_at(nb) + kTile, 16, 1024);
+                const uint64_t od = sdesc_sw128(base + kOffO + so * kTile, 16, 1024);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    mma_ss_if(leader, tmem + kColDP, vd + kmajor_step(kk, 0),
+                              od + kmajor_step(kk, 0), id_s, kk > 0);
+                mma_ss_if(leader, tmem + kColDP, onesd,
+                          sdesc_plain(base + kOffD + so * kExt, 128, 256), id_s, 1u);
+                mma_commit_if(leader, &bar_dp);
+                mma_commit_if(leader, &bar_o_free[so]);      // (the other arrival: dV)
+                return true;
+            };
+            ok = next();
+            if (ok && !done) ok = is_a ? issue_s(0) : issue_dp(0);
+            for (uint32_t k = 0; ok && !done; ++k) {
+                // step k: its item, and whether it is that item's first or last
+                const int at = nb;
+                const bool first = it == 0, last = it + 1 == n_it;
+                if (is_a) {
+                    if (!(ok = next() && (done || issue_s(k + 1)))) break;
+                    // dV += P^T dO_i  (P^T: bf16 pairs in the buffer's first half)
+                    const int so = k % NO;
+                    ok = wait_warp(&bar_p, k & 1, 134, &abort_sh) &&
+                         wait_warp(&o_ready[so], (k / NO) & 1, 135, &abort_sh) &&
+                         (!first || at == 0 ||
+                          wait_warp(&bar_acc_free, (at - 1) & 1, 136, &abort_sh));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t od = sdesc_sw128(base + kOffO + so * kTile, BR * 128, 1024);
+#pragma unroll
+                    for (int kk = 0; kk < BR / 16; ++kk)
+                        mma_ts_if(leader, tmem + kColDV, tmem + col_s(k) + kk * 8,
+                                  od + mnmajor_step(kk), id_kv, (!first || kk > 0) ? 1u : 0u);
+                    mma_commit_if(leader, &bar_o_free[so]);
+                    mma_commit_if(leader && last, &bar_done);
+                    mma_commit_if(leader && last, &bar_kv_free[at & 1]);
+                } else {
+                    ok = next() && wait_warp(&bar_ds, k & 1, 137, &abort_sh) &&
+                         (!first || at == 0 ||
+                          wait_warp(&bar_acc_free, (at - 1) & 1, 138, &abort_sh));
+                    if (!ok) break;
+                    // dK += dS^T Q_i, dQ_i = dS K_j
+                    const int sq = k % NQ;
+                    tc_fence_after();
+                    const uint64_t dsd = sdesc_sw128(base + kOffDS, 16, 1024);
+                    const uint64_t qd = sdesc_sw128(base + kOffQ + sq * kTile, BR * 128, 1024);
+#pragma unroll
+                    for (int kk = 0; kk < BR / 16; ++kk)
+                        mma_ss_if(leader, tmem + kColDK, dsd + kmajor_step(kk, kTile),
+                                  qd + mnmajor_step(kk), id_kv, (!first || kk > 0) ? 1u : 0u);
+                    mma_commit_if(leader, &bar_q_free[sq]);
+                    const uint64_t ad = sdesc_sw128(base + kOffDS, kTile, 1024);
+                    const uint64_t kd = sdesc_sw128(kv_at(at), kTile, 1024);
+#pragma unroll
+                    for (int kk = 0; kk < kBN / 16; ++kk)
+                        mma_ss_if(leader, tmem + col_s(k) + 64, ad + mnmajor_step(kk),
+                                  kd + mnmajor_step(kk), id_dq, kk > 0);
+                    mma_commit_if(leader, &bar_dq[k & 1]);
+                    mma_commit_if(leader && last, &bar_done);
+                    mma_commit_if(leader && last, &bar_kv_free[at & 1]);
+                    ok = done || issue_dp(k + 1);
+                }
+            }
+            if (!ok && leader) {   // no MMA of this thread may still write TMEM at teardown
+                mma_commit(&bar_drain[is_a ? 0 : 1]);
+                wait(&bar_drain[is_a ? 0 : 1], 0, 139, &drain_sh);
+            }
+        } else {
+            // ------------- rows behind the keys, and behind a packed sequence's queries
+            bool ok = true;
+            int k = 0, nb = 0;
+            for (int n = 0; ok; ++n) {
+                BwdCta cta;
+                if (!next_item(n, cta)) break;
+                const int slot = nb & 1;
+                if (!wait_warp(&bar_kv[slot], (nb >> 1) & 1, 140, &abort_sh)) break;
+                if (cta.jblk * kBN + kBN > cta.seq_len) {
+                    uint8_t* const kv = smem + kOffKV + slot * 2 * kTile;
+                    clear_rows(kv, 1, kBN, cta.seq_len - cta.jblk * kBN, lane, 32);
+                    clear_rows(kv + kTile, 1, kBN, cta.seq_len - cta.jblk * kBN, lane, 32);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                if (lane == 0) mbar_arrive(&bar_kv_ready[slot]);
+                ++nb;
+                int i = cta.i_start;
+#pragma unroll 1
+                for (int it = 0; packed && it < cta.n_it; ++it, ++k) {
+                    const int left = cta.q_len - i * BR;
+                    if (++i == cta.i_start + cta.n_i) i = cta.i_start;
+                    const int sq = k % NQ, so = k % NO;
+                    if (!wait_warp(&bar_q[sq], (k / NQ) & 1, 141, &abort_sh)) { ok = false; break; }
+                    if (left < BR) {
+                        clear_rows(smem + kOffQ + sq * kTile, 1, BR, left, lane, 32);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    if (lane == 0) mbar_arrive(&bar_qt[sq]);
+                    if (!wait_warp(&bar_o[so], (k / NO) & 1, 142, &abort_sh)) { ok = false; break; }
+                    if (left < BR) {
+                        clear_rows(smem + kOffO + so * kTile, 1, BR, left, lane, 32);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    if (lane == 0) mbar_arrive(&bar_ot[so]);
+                }
+            }
+        }
+        __syncwarp();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0 && (abort_sh | drain_sh))
+        record_error(p.status, FA_ERR_TIMEOUT, abort_sh ? abort_sh : drain_sh);
+    if (warp == 17) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// dq = bf16(scale * accumulator), sixteen values a thread, the rows inside their sequence;
+// and zeros in dK and dV where the kernel above had no work: the key blocks past a padded
+// sequence's keys and those that no query sees (one block of threads each).  Of 16
+// columns the accumulator has 2 b, 2 b + 1, 8 + 2 b, 9 + 2 b at 4 b.
+__global__ void __launch_bounds__(256)
+fa_bwd_cross64_dq_kernel(__nv_bfloat16* __restrict__ dq, long long n_rows, int dq_blocks,
+                         const BwdParams p) {
+    if ((int)blockIdx.x >= dq_blocks) {
+        const int item = (int)blockIdx.x - dq_blocks, n_kblk = (p.Nk + kBN - 1) / kBN;
+        const BwdCta c = bwd_cta_cross(p, BR, item / n_kblk, item % n_kblk);
+        if (!c.idle && c.n_it > 0) return;
+        zero_grads<D>(p, c, c.jblk * kBN + threadIdx.x / 2, threadIdx.x % 2 * 32,
+                      threadIdx.x % 2 * 32 + 32, true, true);
+        return;
+    }
+    const long long t = (long long)blockIdx.x * 256 + threadIdx.x;
+    const long long r = t / (D / 16);             // of the padded rows
+    const int o = (int)(t % (D / 16)) * 16;
+    if (r >= n_rows) return;
+    const int bh = (int)r / p.Np, i = (int)r - bh * p.Np;      // (rows * D < 2^31)
+    long long to = (long long)bh * p.N + i;
+    int len = p.N;
+    if (p.cu_seqlens) {
+        int t0;
+        const int b = bh / p.H;
+        len = packed_seq(p.cu_seqlens, b, p.N, p.rows, t0);
+        to = (long long)(bh - b * p.H) * p.rows + t0 + i;
+    }
+    if (i >= len) return;
+    const float4* const src = reinterpret_cast<const float4*>(p.dq_acc + r * D + o);
+    uint32_t lo[4], hi[4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        const float4 x = src[b];
+        lo[b] = pack_bf16x2(x.x * p.scale, x.y * p.scale);
+        hi[b] = pack_bf16x2(x.z * p.scale, x.w * p.scale);
+    }
+    uint4* const dst = reinterpret_cast<uint4*>(dq + to * D + o);
+    dst[0] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    dst[1] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+}
+
+}  // namespace
+
+cudaError_t launch_bwd_cross64(const Shape& s, const void* q, const void* k, const void* v,
+                               const void* dout, void* dq, void* dk, void* dv,
+                               const BwdWorkspace& ws, DeviceStatus* status, cudaStream_t stream) {
+    const bool packed = s.cu_seqlens != nullptr;
+    BwdParams p = {};
+    p.H = s.H;
+    p.Hkv = s.Hkv;
+    p.N = s.N;
+    p.Np = padded_rows(s.N);
+    p.G = s.H / s.Hkv;
+    p.causal = s.causal;
+    p.rows = packed ? s.total : s.N;
+    p.cu_seqlens = s.cu_seqlens;
+    p.Nk = s.Nk;
+    p.krows = packed ? s.total_k : s.Nk;
+    p.kv_lens = s.kv_lens;
+    p.cu_k = s.cu_k;
+    p.scale = s.scale;
+    p.scale_log2 = (float)((double)s.scale * 1.4426950408889634);
+    p.lse_ext = ws.lse_ext;
+    p.d_ext = ws.d_ext;
+    p.dq_acc = ws.dq_acc;
+    p.work = ws.work;
+    p.n_bg = s.B * s.Hkv;
+    p.n_items = (s.Nk + kBN - 1) / kBN * p.n_bg;
+    p.dk = static_cast<__nv_bfloat16*>(dk);
+    p.dv = static_cast<__nv_bfloat16*>(dv);
+    p.status = status;
+    const int zq = packed ? s.H : s.B * s.H, zk = packed ? s.Hkv : s.B * s.Hkv;
+    CUtensorMap tq, tk, tv, tdo;
+    if (!make_tmap_bf16_3d(&tq, q, D, p.rows, zq, BR) ||
+        !make_tmap_bf16_3d(&tdo, dout, D, p.rows, zq, BR) ||
+        !make_tmap_bf16_3d(&tk, k, D, p.krows, zk, kBN) ||
+        !make_tmap_bf16_3d(&tv, v, D, p.krows, zk, kBN))
+        return cudaErrorInvalidValue;
+    static int configured_device = -1;   // the attribute is per device; cheap to repeat
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (configured_device != dev) {
+        // The register split must fit in what the launch provides, or the
+        // setmaxnreg.inc of the compute warps would wait forever.
+        cudaFuncAttributes attr;
+        cudaError_t e = cudaFuncGetAttributes(&attr, fa_bwd_cross64_kernel);
+        if (e != cudaSuccess) return e;
+        if (attr.numRegs * kThreads < kRegsNeeded) return cudaErrorInvalidConfiguration;
+        e = cudaFuncSetAttribute(fa_bwd_cross64_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kSmem);
+        if (e != cudaSuccess) return e;
+        configured_device = dev;
+    }
+    const int sms = device_sm_count() > 0 ? device_sm_count() : 148;
+    const int grid = p.n_items < sms ? p.n_items : sms;
+    count_launch();
+    fa_bwd_cross64_kernel<<<grid, kThreads, kSmem, stream>>>(tq, tk, tv, tdo, p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const long long rows = (long long)s.B * s.H * p.Np;
+    const int blocks = (int)((rows * (D / 16) + 255) / 256);  // rows * D < 2^31
+    count_launch();
+    fa_bwd_cross64_dq_kernel<<<(unsigned)blocks + p.n_items, 256, 0, stream>>>(
+        static_cast<__nv_bfloat16*>(dq), rows, blocks, p);
+    return cudaGetLastError();
+}
+
+}  // namespace fa

@@ -203,6 +203,11 @@ cudaError_t launch_fwd_decode_paged(const PagedCache& c, const void* q, void* o,
                                     const int* seqlens, void* workspace, int B, int H, int Nq,
                                     int causal, float scale, DeviceStatus* status,
                                     cudaStream_t stream);
+// The backward at d = 64 with keys of their own, from the preprocess on (fa_bwd_cross.cu):
+// dK/dV and dQ, two launches.
+cudaError_t launch_bwd_cross64(const Shape& s, const void* q, const void* k, const void* v,
+                               const void* dout, void* dq, void* dk, void* dv,
+                               const BwdWorkspace& ws, DeviceStatus* status, cudaStream_t stream);
 // Workspace of a forward with keys of their own (fa_cross.cu).
 size_t cross_fwd_workspace_bytes(const Shape& s);
 // Paged decoding over contiguous K and V [B][Hkv][Nk][d], kv_lens[b] keys a sequence (null: Nk).

@@ -94,6 +94,19 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
+// The same, suspended for at most a microsecond.
+__device__ __forceinline__ bool mbar_try_wait_us(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // Bounded wait for the phase with the given parity to complete.
 __device__ __forceinline__ bool fa_wait(uint64_t* bar, uint32_t parity, int site,
                                         const WaitCtx& ctx,
@@ -194,6 +207,16 @@ __device__ __forceinline__ void bulk_reduce_add_f32(float* dst, const void* src,
         "cp.reduce.async.bulk.global.shared::cta.bulk_group.add.f32 [%0], [%1], %2;"
         ::"l"(reinterpret_cast<uint64_t>(dst)), "r"(smem_u32(src)), "r"(bytes)
         : "memory");
+}
+// Adds from registers; nothing waits for them.
+__device__ __forceinline__ void red_add_f32(float* p, uint32_t x) {
+    asm volatile("red.global.add.f32 [%0], %1;" ::"l"(p), "f"(__uint_as_float(x)) : "memory");
+}
+__device__ __forceinline__ void red_add_f32x4(float* p, uint32_t a, uint32_t b, uint32_t c,
+                                              uint32_t d) {
+    asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(__uint_as_float(a)),
+                 "f"(__uint_as_float(b)), "f"(__uint_as_float(c)), "f"(__uint_as_float(d))
+                 : "memory");
 }
 // Tensor (tiled) reduction shared -> global, add, into the tensor a 2-D map
 // describes (element type from the map); box at coordinates {x, y}.
@@ -383,6 +406,17 @@ __device__ __forceinline__ void mma_ss_f8_if(bool issue, uint32_t d_tmem, uint64
         : "memory");
 }
 
+__device__ __forceinline__ void mma_ts_if(bool issue, uint32_t d_tmem, uint32_t a_tmem,
+                                          uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"((uint32_t)issue)
+        : "memory");
+}
+
 // Arrive (once) on `bar` when every tcgen05.mma issued so far by this thread
 // has completed.
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
@@ -430,6 +464,17 @@ __device__ __forceinline__ void mma_commit_if(bool issue, uint64_t* bar) {
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
+        "%10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, "
+        "%27, %28, %29, %30, %31}, [%32];"
+        : FA_W32(r)
+        : "r"(taddr));
+}
+// 16 lanes (from taddr's, a multiple of 16) x 64 columns: thread 4 a + b holds of lanes a
+// and a + 8 columns 8 c + 2 b and 8 c + 2 b + 1, in r[4 c], r[4 c + 1] and r[4 c + 2],
+// r[4 c + 3].
+__device__ __forceinline__ void tmem_ld16x64(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
         "%10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, "
         "%27, %28, %29, %30, %31}, [%32];"
         : FA_W32(r)
