@@ -54,7 +54,8 @@ fa_status forward(const Shape& s, const void* q, const void* k, const void* v, v
     int dev;
     DeviceStatus* status;
     if ((st = ready_device(&dev, &status)) != FA_OK) return st;
-    return launch_fwd(s, q, k, v, o, lse, false, status, (cudaStream_t)stream) == cudaSuccess
+    return launch_fwd(s, q, k, v, o, lse, false, status, (cudaStream_t)stream, nullptr,
+                      workspace) == cudaSuccess
                ? FA_OK
                : FA_ERR_CUDA;
 }
@@ -122,8 +123,6 @@ fa_status check_decode(int B, int H, int Hkv, int Nq, int Nk, int d) {
 }
 
 }  // namespace
-
-size_t cross_fwd_workspace_bytes(const Shape&) { return 256; }
 
 }  // namespace fa
 

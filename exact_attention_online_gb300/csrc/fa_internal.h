@@ -112,9 +112,11 @@ BwdWorkspace bwd_workspace_carve(void* base, const Shape& s);
 // Launchers (return a cudaError_t from the launch).
 // launch_fwd: train_ws non-null = training forward, which also writes the
 // -LSE table and zeroes the dQ accumulator of that backward workspace.
+// cross_ws: cross_fwd_workspace_bytes() for keys of their own.
 cudaError_t launch_fwd(const Shape& s, const void* q, const void* k, const void* v, void* o,
                        float* lse, bool precise, DeviceStatus* status, cudaStream_t stream,
-                       const BwdWorkspace* train_ws = nullptr);
+                       const BwdWorkspace* train_ws = nullptr, void* cross_ws = nullptr);
+size_t cross_fwd_workspace_bytes(const Shape& s);
 // full = false: only -D (the rest was prepared by the training forward).
 cudaError_t launch_bwd_preprocess(const Shape& s, const void* o, bool o_f32, const void* dout,
                                   const float* lse, const BwdWorkspace& ws,
@@ -208,8 +210,6 @@ cudaError_t launch_fwd_decode_paged(const PagedCache& c, const void* q, void* o,
 cudaError_t launch_bwd_cross64(const Shape& s, const void* q, const void* k, const void* v,
                                const void* dout, void* dq, void* dk, void* dv,
                                const BwdWorkspace& ws, DeviceStatus* status, cudaStream_t stream);
-// Workspace of a forward with keys of their own (fa_cross.cu).
-size_t cross_fwd_workspace_bytes(const Shape& s);
 // Paged decoding over contiguous K and V [B][Hkv][Nk][d], kv_lens[b] keys a sequence (null: Nk).
 cudaError_t launch_fwd_cross_decode(const void* q, const void* k, const void* v, void* o,
                                     float* lse, const int* kv_lens, void* workspace, int B, int H,
