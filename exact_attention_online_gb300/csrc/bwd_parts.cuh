@@ -1,5 +1,5 @@
-// What the dK/dV kernels of the backward share: their parameters, the work items, and the
-// constant operand of the extension MMAs.
+// What the dK/dV kernels of the backward with keys of another length share: their
+// parameters, the work items, and the constant operand of the extension MMAs.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -12,19 +12,13 @@ constexpr int kBwdKeys = 128;   // keys per work item
 
 struct BwdParams {
     int H, Hkv, N, Np, G, causal;
-    int rows;                         // rows per head of q, k, v, dk, dv: N, or the packed total
-    int chunk;                        // key/value heads per key-block-major chunk (causal)
-    // Causal sliding window W: key k is seen by queries k <= i < k + W.
-    // Without a window this holds kNoWindow.
-    int window;
-    // Packed variable-length batches: sequence b is rows cu_seqlens[b] ..
-    // cu_seqlens[b+1] - 1 of every head; N is then the longest sequence and
-    // the workspace keeps N-row (padded) regions per (batch, head).
+    int rows;                         // rows per head of q: N, or the packed total
+    // Packed: sequence b's queries are rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of every
+    // head; N is then the longest sequence and the workspace keeps N-row (padded) regions
+    // per (batch, head).
     const int* cu_seqlens;
-    // Keys of their own (CROSS): N, rows and cu_seqlens are the queries'; at most Nk
-    // keys a sequence, krows rows a head of k, v, dk, dv.  Padded batches: kv_lens[b]
-    // keys, or Nk (null); packed ones: rows cu_k[b] .. cu_k[b+1] - 1.  Otherwise Nk
-    // and krows are N and rows.
+    // At most Nk keys a sequence, krows rows a head of k, v, dk, dv.  Padded batches:
+    // kv_lens[b] keys, or Nk (null); packed ones: rows cu_k[b] .. cu_k[b + 1] - 1.
     int Nk, krows;
     const int* kv_lens;
     const int* cu_k;
@@ -39,29 +33,46 @@ struct BwdParams {
     DeviceStatus* status;
 };
 
-// What one dK/dV work item covers: (batch, kv head, key block j) and the
-// range of query blocks (of br rows) that see some key of the block.  The
-// persistent CTAs take the items in index order from the work counter, so
-// that, as with one CTA per item, the hardware-like first-come order decides
-// which SM runs which item.  Dense causal batches: key-block-major, so that the
-// longest CTAs (small j, every query block after them) start first and the
-// shortest fill the tail (a CPU model of the bench workloads puts the busiest
-// SM within 1-2 % of the mean instead of 7-14 %; measured: dK/dV +2 % to
-// +13 %).  Otherwise head-major: without the mask every CTA costs the same and
-// the CTAs that run at the same time share Q and dO in L2 (key-block-major
-// measured 12 % slower there), and with packed sequences of different lengths
-// j does not rank the cost (measured 12 % slower).  Key-block-major runs over
-// chunks of p.chunk heads at a time, sized so that a chunk's Q, dO and dQ
-// accumulator stay in L2 while its key blocks re-read them.
+inline BwdParams bwd_params(const Shape& s, void* dk, void* dv, const BwdWorkspace& ws,
+                            DeviceStatus* status) {
+    const bool packed = s.cu_seqlens != nullptr;
+    BwdParams p;
+    p.H = s.H;
+    p.Hkv = s.Hkv;
+    p.N = s.N;
+    p.Np = padded_rows(s.N);
+    p.G = s.H / s.Hkv;
+    p.causal = s.causal;
+    p.rows = packed ? s.total : s.N;
+    p.cu_seqlens = s.cu_seqlens;
+    p.Nk = s.Nk;
+    p.krows = packed ? s.total_k : s.Nk;
+    p.kv_lens = s.kv_lens;
+    p.cu_k = s.cu_k;
+    p.scale = s.scale;
+    p.scale_log2 = (float)((double)s.scale * 1.4426950408889634);
+    p.lse_ext = ws.lse_ext;
+    p.d_ext = ws.d_ext;
+    p.dq_acc = ws.dq_acc;
+    p.work = ws.work;
+    p.n_bg = s.B * s.Hkv;
+    p.n_items = (s.Nk + kBwdKeys - 1) / kBwdKeys * p.n_bg;
+    p.dk = static_cast<__nv_bfloat16*>(dk);
+    p.dv = static_cast<__nv_bfloat16*>(dv);
+    p.status = status;
+    return p;
+}
+
+// What one dK/dV work item covers: kv head bg = b * Hkv + g, key block jblk, and the range of
+// query blocks (of br rows) that see some key of the block.
 struct BwdCta {
     int jblk, b, g, bg, z_kv, i_start, n_i, n_it;
     int tok0, q_len;     // first query row of the sequence in its head, and their number
     int ktok0, seq_len;  // the same of its keys
     int off;             // query i sees keys j <= i + off under the causal mask
-    bool idle;   // a key block past its sequence's end: nothing to do
+    bool idle;           // a key block past its sequence's end: nothing to do
 };
-// With keys of their own: kv head bg = b * Hkv + g, key block jblk.
-__device__ __forceinline__ BwdCta bwd_cta_cross(const BwdParams& p, int br, int bg, int jblk) {
+__device__ __forceinline__ BwdCta bwd_cta(const BwdParams& p, int br, int bg, int jblk) {
     BwdCta c;
     const bool packed = p.cu_seqlens != nullptr;
     c.bg = bg;
@@ -80,45 +91,6 @@ __device__ __forceinline__ BwdCta bwd_cta_cross(const BwdParams& p, int br, int 
     c.i_start = p.causal ? max(0, jblk * kBwdKeys - c.off) / br : 0;
     c.n_i = max(0, n_qblk - c.i_start);
     c.n_it = p.G * c.n_i;
-    return c;
-}
-template <bool CAUSAL, bool WINDOW, bool VARLEN, bool CROSS = false>
-__device__ __forceinline__ BwdCta bwd_cta(const BwdParams& p, int br, int item) {
-    BwdCta c;
-    constexpr bool kKeyMajor = CAUSAL && !VARLEN;
-    const int n_kblk = (p.Nk + kBwdKeys - 1) / kBwdKeys;
-    const int n_bg = p.n_bg;                      // B * Hkv
-    if (CROSS) {
-        return bwd_cta_cross(p, br, item / n_kblk, item % n_kblk);
-    } else if (kKeyMajor) {
-        const int chunk = item / (p.chunk * n_kblk), loc = item % (p.chunk * n_kblk);
-        const int width = min(p.chunk, n_bg - chunk * p.chunk);
-        c.jblk = loc / width;
-        c.bg = chunk * p.chunk + loc % width;
-    } else {
-        c.jblk = item % n_kblk;
-        c.bg = item / n_kblk;
-    }
-    c.b = c.bg / p.Hkv;
-    c.g = c.bg % p.Hkv;
-    // The sequence: its first row in the tensors and its length.  Dense
-    // batches address rows of head b*H(kv) + h; packed ones rows tok0 + i of
-    // head h.
-    c.tok0 = 0;
-    c.q_len = VARLEN ? packed_seq(p.cu_seqlens, c.b, p.N, p.rows, c.tok0) : p.N;
-    c.ktok0 = c.tok0;
-    c.seq_len = c.q_len;
-    c.off = 0;
-    c.idle = VARLEN && c.jblk * kBwdKeys >= c.seq_len;
-    c.z_kv = VARLEN ? c.g : c.bg;
-    const int n_qblk = (c.q_len + br - 1) / br;
-    // Query blocks that see some key of the block: rows 128 j .. 128 j + 127
-    // + W - 1 under the causal (windowed) mask.
-    c.i_start = CAUSAL ? (c.jblk * kBwdKeys) / br : 0;
-    const int i_end = WINDOW ? min(n_qblk, (c.jblk * kBwdKeys + kBwdKeys - 1 + (p.window - 1)) / br + 1)
-                             : n_qblk;
-    c.n_i = i_end - c.i_start;
-    c.n_it = p.G * c.n_i;                         // (head in group) x (query block)
     return c;
 }
 

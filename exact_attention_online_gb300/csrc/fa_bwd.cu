@@ -34,12 +34,12 @@
 #include <cuda_runtime.h>
 #include <math_constants.h>
 
-#include "bwd_parts.cuh"
+#include "fa_internal.h"
 
 namespace fa {
 namespace {
 
-constexpr int kBN = kBwdKeys;   // keys per CTA
+constexpr int kBN = 128;   // keys per CTA
 // 16 warps: 0-7 compute (two warpgroups), 8 TMA producer, 9 and 10 MMA
 // issuers, 11 idle, 12-15 dQ read-out.
 constexpr int kThreads = 512;
@@ -99,6 +99,109 @@ struct BwdCfg {
     static constexpr uint32_t kColKT = kColDQ + 64;
     static constexpr bool kKInTmem = (D == 128);
 };
+
+struct BwdParams {
+    int H, Hkv, N, Np, G, causal;
+    int rows;                         // rows per head of q, k, v, dk, dv: N, or the packed total
+    int chunk;                        // key/value heads per key-block-major chunk (causal)
+    // Causal sliding window W: key k is seen by queries k <= i < k + W.
+    // Without a window this holds kNoWindow.
+    int window;
+    // Packed variable-length batches: sequence b is rows cu_seqlens[b] ..
+    // cu_seqlens[b+1] - 1 of every head; N is then the longest sequence and
+    // the workspace keeps N-row (padded) regions per (batch, head).
+    const int* cu_seqlens;
+    float scale, scale_log2;
+    const uint16_t* lse_ext;          // workspace tables (fa_internal.h)
+    const uint16_t* d_ext;
+    float* dq_acc;
+    int* work;                        // next work item (zero on entry, left zero)
+    int n_bg, n_items;                // B * Hkv; work items (B * Hkv * key blocks)
+    __nv_bfloat16* dk;
+    __nv_bfloat16* dv;
+    DeviceStatus* status;
+};
+
+// What one dK/dV work item covers: (batch, kv head, key block j) and the
+// range of query blocks (of br rows) that see some key of the block.  The
+// persistent CTAs take the items in index order from the work counter, so
+// that, as with one CTA per item, the hardware-like first-come order decides
+// which SM runs which item.  Dense causal batches: key-block-major, so that the
+// longest CTAs (small j, every query block after them) start first and the
+// shortest fill the tail (a CPU model of the bench workloads puts the busiest
+// SM within 1-2 % of the mean instead of 7-14 %; measured: dK/dV +2 % to
+// +13 %).  Otherwise head-major: without the mask every CTA costs the same and
+// the CTAs that run at the same time share Q and dO in L2 (key-block-major
+// measured 12 % slower there), and with packed sequences of different lengths
+// j does not rank the cost (measured 12 % slower).  Key-block-major runs over
+// chunks of p.chunk heads at a time, sized so that a chunk's Q, dO and dQ
+// accumulator stay in L2 while its key blocks re-read them.
+struct BwdCta {
+    int jblk, b, g, bg, tok0, seq_len, z_kv, i_start, n_i, n_it;
+    bool idle;   // a key block past its packed sequence's end: nothing to do
+};
+template <bool CAUSAL, bool WINDOW, bool VARLEN>
+__device__ __forceinline__ BwdCta bwd_cta(const BwdParams& p, int br, int item) {
+    BwdCta c;
+    constexpr bool kKeyMajor = CAUSAL && !VARLEN;
+    const int n_kblk = (p.N + kBN - 1) / kBN;
+    const int n_bg = p.n_bg;                      // B * Hkv
+    if (kKeyMajor) {
+        const int chunk = item / (p.chunk * n_kblk), loc = item % (p.chunk * n_kblk);
+        const int width = min(p.chunk, n_bg - chunk * p.chunk);
+        c.jblk = loc / width;
+        c.bg = chunk * p.chunk + loc % width;
+    } else {
+        c.jblk = item % n_kblk;
+        c.bg = item / n_kblk;
+    }
+    c.b = c.bg / p.Hkv;
+    c.g = c.bg % p.Hkv;
+    // The sequence: its first row in the tensors and its length.  Dense
+    // batches address rows of head b*H(kv) + h; packed ones rows tok0 + i of
+    // head h.
+    c.tok0 = 0;
+    c.seq_len = VARLEN ? packed_seq(p.cu_seqlens, c.b, p.N, p.rows, c.tok0) : p.N;
+    c.idle = VARLEN && c.jblk * kBN >= c.seq_len;
+    c.z_kv = VARLEN ? c.g : c.bg;
+    const int n_qblk = (c.seq_len + br - 1) / br;
+    // Query blocks that see some key of the block: rows 128 j .. 128 j + 127
+    // + W - 1 under the causal (windowed) mask.
+    c.i_start = CAUSAL ? (c.jblk * kBN) / br : 0;
+    const int i_end = WINDOW ? min(n_qblk, (c.jblk * kBN + kBN - 1 + (p.window - 1)) / br + 1)
+                             : n_qblk;
+    c.n_i = i_end - c.i_start;
+    c.n_it = p.G * c.n_i;                         // (head in group) x (query block)
+    return c;
+}
+
+// The constant A operand of the extension MMAs, 128 key rows x 16 columns:
+// cols 0-8 hold 1/c as three bf16 terms (h h h m m m l l l), against the B
+// columns (x_h x_m x_l) x 3 of -LSE log2(e), so that the nine products sum to
+// (-LSE log2 e) / c; cols 9-11 hold 1 against the three terms of -D; the rest
+// 0.  One 16-byte piece per thread of the first 256.
+__device__ __forceinline__ void bwd_fill_ones(uint8_t* sOnes, float scale_log2) {
+    if (threadIdx.x < kBN * 32 / 16) {
+        const float inv = 1.0f / scale_log2;
+        const float ih = bf16_round(inv), im = bf16_round(inv - ih),
+                    il = bf16_round(inv - ih - im);
+        const int kc = (threadIdx.x >> 3) & 1;   // K half of this core-matrix row
+        uint4 w;
+        if (kc == 0) {
+            w.x = pack_bf16x2(ih, ih);
+            w.y = pack_bf16x2(ih, im);
+            w.z = pack_bf16x2(im, im);
+            w.w = pack_bf16x2(il, il);
+        } else {
+            w.x = pack_bf16x2(il, 1.0f);
+            w.y = pack_bf16x2(1.0f, 1.0f);
+            w.z = 0u;
+            w.w = 0u;
+        }
+        *reinterpret_cast<uint4*>(sOnes + threadIdx.x * 16) = w;
+        fence_proxy_async_smem();
+    }
+}
 
 // WINDOW (with CAUSAL): the causal sliding window of p.window keys.
 // VARLEN: packed variable-length sequences (p.cu_seqlens).
@@ -835,7 +938,8 @@ __device__ __forceinline__ int seq_row(const int* __restrict__ cu, long long bh,
 // bf16, or fp32 when it comes from the precise forward.  FULL = false (after
 // a training forward, which wrote the -LSE table and zeroed the accumulator):
 // the -D table only.
-template <int D, typename OT, bool FULL>
+// EMPTY: a row may see no key (LSE = -infinity): P = 0 like a padded one's.
+template <int D, typename OT, bool FULL, bool EMPTY = false>
 __global__ void __launch_bounds__(256)
 fa_bwd_pre_kernel(const OT* __restrict__ o, const __nv_bfloat16* __restrict__ dout,
                   const float* __restrict__ lse, uint16_t* __restrict__ lse_ext,
@@ -862,8 +966,7 @@ fa_bwd_pre_kernel(const OT* __restrict__ o, const __nv_bfloat16* __restrict__ do
         const bool used = in && i < (len + kRowPad - 1) / kRowPad * kRowPad;
         float x = -1e30f;
         if (FULL && valid) x = -lse[base + i] * 1.4426950408889634f;
-        // a row that sees no key (LSE = -infinity): P = 0 like a padded one
-        if (x == CUDART_INF_F) x = -1e30f;
+        if (EMPTY && x == CUDART_INF_F) x = -1e30f;
         float acc = 0.0f;
         if (valid) {
             const long long src = (base + i) * D + sl * 8;
@@ -1085,7 +1188,7 @@ struct Bwd2Cfg {
 };
 static_assert(Bwd2Cfg::kSmemAlloc <= 227 * 1024 - 1024, "shared memory of the two-pipeline kernel");
 
-template <bool CAUSAL, bool WINDOW, bool VARLEN, bool CROSS>
+template <bool CAUSAL, bool WINDOW, bool VARLEN>
 __global__ void __launch_bounds__(kThreads, 1)
 fa_bwd_dkdv2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -1105,15 +1208,11 @@ fa_bwd_dkdv2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     __shared__ uint64_t bar_dv_turn, bar_dk_turn;
     __shared__ uint64_t bar_item_full[2], bar_item_empty[2];
     __shared__ int item_sh[2];
-    const int kItemConsumers = kComputeWarps + 4 + 2 + (CROSS && p.cu_seqlens ? 1 : 0);
+    constexpr int kItemConsumers = kComputeWarps + 4 + 2;
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_sh;
     const WaitCtx wc{p.status, &abort_sh};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const bool causal = CAUSAL || (CROSS && p.causal);
-    // as in the kernel above
-    __shared__ uint64_t bar_tail[2 * NS];
-    uint64_t* const bar_ready = CROSS && p.cu_seqlens ? bar_tail : bar_full;
 
     uint8_t* sK = smem + Cfg::kOffK;
     uint8_t* sV = smem + Cfg::kOffV;
@@ -1130,24 +1229,20 @@ fa_bwd_dkdv2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         abort_sh = 0;
         mbar_init(&bar_kv, 1);
         mbar_init(&bar_kv_free, 2);                  // one commit per MMA issuer
-        for (int s = 0; s < 2 * NS; ++s) {
-            mbar_init(&bar_full[s], 1);
-            mbar_init(&bar_tail[s], 1);
-        }
+        for (int s = 0; s < 2 * NS; ++s) mbar_init(&bar_full[s], 1);
         for (int s = 0; s < NS; ++s) mbar_init(&bar_empty[s], 1);   // the step's MMA issuer
         for (int q = 0; q < 2; ++q) {
             mbar_init(&bar_s[q], 1);
             mbar_init(&bar_dp[q], 1);
-            // CROSS: a warp arrives by one lane
-            mbar_init(&bar_p[q], CROSS ? kPipeThreads / 32 : kPipeThreads);
-            mbar_init(&bar_ds[q], CROSS ? kPipeThreads / 32 : kPipeThreads);
+            mbar_init(&bar_p[q], kPipeThreads);
+            mbar_init(&bar_ds[q], kPipeThreads);
             mbar_init(&bar_dq_full[q], 1);
-            mbar_init(&bar_dq_free[q], CROSS ? kReadoutThreads / 32 : kReadoutThreads);
+            mbar_init(&bar_dq_free[q], kReadoutThreads);
             mbar_init(&bar_item_full[q], 1);
             mbar_init(&bar_item_empty[q], kItemConsumers);
         }
         mbar_init(&bar_done, 2);                     // one commit per MMA issuer, per item
-        mbar_init(&bar_acc_free, CROSS ? kComputeWarps : kComputeThreads);   // dK, dV zeroed
+        mbar_init(&bar_acc_free, kComputeThreads);   // dK, dV zeroed for the item
         mbar_init(&bar_dv_turn, 1);
         mbar_init(&bar_dk_turn, 1);
         fence_mbar_init();
@@ -1161,10 +1256,6 @@ fa_bwd_dkdv2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     tc_fence_after();
     const uint32_t tmem = tmem_base_sh;
 
-    auto arrive = [&](uint64_t* bar) {
-        if (CROSS) __syncwarp();
-        if (!CROSS || lane == 0) mbar_arrive(bar);
-    };
     auto next_item_warp = [&](int n, int& item) -> bool {
         const int slot = n & 1;
         if (!fa_wait_warp(&bar_item_full[slot], (n >> 1) & 1, 65, wc)) return false;
@@ -1197,19 +1288,11 @@ fa_bwd_dkdv2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         for (int n = 0; ok; ++n) {
             int item;
             if (!next_item_warp(n, item) || item < 0) break;
-            const BwdCta cta = bwd_cta<CAUSAL, WINDOW, VARLEN, CROSS>(p, BR, item);
-            if (CROSS && (cta.idle || cta.n_it == 0))
-                zero_grads<D>(p, cta, cta.jblk * kBN + rl, 0, D, !cp, cp);
+            const BwdCta cta = bwd_cta<CAUSAL, WINDOW, VARLEN>(p, BR, item);
             if (cta.idle || cta.n_it == 0) continue;
-            const int jblk = cta.jblk, seq_len = cta.seq_len, z_kv = cta.z_kv;
+            const int jblk = cta.jblk, tok0 = cta.tok0, seq_len = cta.seq_len, z_kv = cta.z_kv;
             const int i_start = cta.i_start, n_i = cta.n_i, n_it = cta.n_it;
             const int key = jblk * kBN + rl;
-            if (CROSS && jblk * kBN + kBN > seq_len) {
-                // K_j's (V_j's) rows past the keys: cleared before bar_acc_free
-                if (!fa_wait_warp(&bar_kv, nb & 1, 64, wc)) { ok = false; break; }
-                clear_rows(cp ? sV : sK, D / 64, kBN, seq_len - jblk * kBN, rl, kBN);
-                fence_proxy_async_smem();
-            }
             // dK (pipeline 0's warps) and dV (pipeline 1's) of this item start
             // from zero; the previous item's were read out below
             {
@@ -1221,7 +1304,7 @@ fa_bwd_dkdv2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     tmem_st32(lane_addr + (cp ? Cfg::kColDV : Cfg::kColDK) + c0, z);
                 tmem_st_wait();
                 tc_fence_before();
-                arrive(&bar_acc_free);
+                mbar_arrive(&bar_acc_free);
             }
             for (int it = (gi & 1) == cp ? 0 : 1; ok && it < n_it; it += 2) {
                 const int git = gi + it;
@@ -1230,10 +1313,10 @@ fa_bwd_dkdv2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 if (!fa_wait_warp(&bar_s[cp], k & 1, 61, wc)) { ok = false; break; }
                 tc_fence_after();
                 const int q0 = i * BR;
-                const bool need_mask = (causal && (q0 + cta.off < jblk * kBN + kBN - 1 ||
+                const bool need_mask = (CAUSAL && (q0 < jblk * kBN + kBN - 1 ||
                                                    (WINDOW && q0 + BR - 1 > jblk * kBN + p.window - 1))) ||
                                        (jblk * kBN + kBN > seq_len);
-                const int key_lim = causal ? key - cta.off - q0 : -1;
+                const int key_lim = CAUSAL ? key - q0 : -1;
                 const int key_hi = WINDOW ? key + p.window - 1 - q0 : BR;
                 const bool key_valid = key < seq_len;
                 // P^T = 2^(S'^T c), S'^T = S^T - LSE log2(e) / c from the tensor
@@ -1267,7 +1350,7 @@ fa_bwd_dkdv2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 }
                 tmem_st_wait();
                 tc_fence_before();
-                arrive(&bar_p[cp]);
+                mbar_arrive(&bar_p[cp]);
 
                 // dS^T = P^T o (dP^T - D) -> bf16, swizzled [key][query] tile;
                 // dP^T - D comes from the tensor core.  The pipeline's previous
@@ -1300,14 +1383,13 @@ fa_bwd_dkdv2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 }
                 tc_fence_before();   // the dP^T reads precede the dQ^T MMA over them
                 fence_proxy_async_smem();
-                arrive(&bar_ds[cp]);
+                mbar_arrive(&bar_ds[cp]);
             }
             // ---------------------------------------------------- dK, dV epilogue
             if (ok && fa_wait_warp(&bar_done, nb & 1, 63, wc)) {
                 tc_fence_after();
-                const bool there = key < seq_len;
-                const bool valid = there || (CROSS && !p.cu_seqlens && key < p.Nk);
-                const size_t row = ((size_t)z_kv * p.krows + cta.ktok0 + (valid ? key : 0)) * D;
+                const bool valid = key < seq_len;
+                const size_t row = ((size_t)z_kv * p.rows + tok0 + (valid ? key : 0)) * D;
                 const uint32_t col = cp ? Cfg::kColDV : Cfg::kColDK;
                 const float mul = cp ? 1.0f : p.scale;
                 __nv_bfloat16* dst = (cp ? p.dv : p.dk) + row;
@@ -1316,9 +1398,6 @@ fa_bwd_dkdv2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     uint32_t r[32];
                     tmem_ld32(lane_addr + col + c0, r);
                     tmem_ld_wait(r);
-                    if (CROSS && !there)
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) r[e] = 0u;
                     if (valid) {
                         uint4* d4 = reinterpret_cast<uint4*>(dst + c0);
 #pragma unroll
@@ -1356,7 +1435,7 @@ fa_bwd_dkdv2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         for (int n = 0; ok; ++n) {
             int item;
             if (!next_item_warp(n, item) || item < 0) break;
-            const BwdCta cta = bwd_cta<CAUSAL, WINDOW, VARLEN, CROSS>(p, BR, item);
+            const BwdCta cta = bwd_cta<CAUSAL, WINDOW, VARLEN>(p, BR, item);
             if (cta.idle || cta.n_it == 0) continue;
             const int b = cta.b, g = cta.g, i_start = cta.i_start, n_i = cta.n_i, n_it = cta.n_it;
             for (int it = 0; ok && it < n_it; ++it) {
@@ -1375,35 +1454,23 @@ fa_bwd_dkdv2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 tmem_ld_wait(r0);
                 asm volatile("" : FA_R32(r1) : : "memory");
                 tc_fence_before();
-                arrive(&bar_dq_free[pp]);
-                if constexpr (CROSS) {
-                    // Added from registers, 128 bytes a warp and query: a copy that adds
-                    // takes some 1500 cycles until it has read its tile, and a step's two
-                    // wait for one another (16 packed pairs of sequences, H32 Hkv8: the
-                    // backward 980 us with copies, 936 with these).
-                    float* const to = p.dq_acc + ((size_t)bh * p.Np + (size_t)i * BR) * D + rl;
+                mbar_arrive(&bar_dq_free[pp]);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) red_add_f32(to + e * D, r0[e]);
+                for (int h = 0; h < 2; ++h) {
+                    // the copy that last read the staging tile
+                    if (leader) bulk_wait_group_read<0>();
+                    named_bar_sync(1, kReadoutThreads);
+                    // dQ^T: lane = head-dim index, column = query -> stg[q][dd]
+                    const uint32_t* src = h ? r1 : r0;
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) red_add_f32(to + (32 + e) * D, r1[e]);
-                } else {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        // the copy that last read the staging tile
-                        if (leader) bulk_wait_group_read<0>();
-                        named_bar_sync(1, kReadoutThreads);
-                        // dQ^T: lane = head-dim index, column = query -> stg[q][dd]
-                        const uint32_t* src = h ? r1 : r0;
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) sStage[e * D + rl] = __uint_as_float(src[e]);
-                        fence_proxy_async_smem();
-                        named_bar_sync(1, kReadoutThreads);
-                        if (leader) {
-                            bulk_reduce_add_f32(
-                                p.dq_acc + ((size_t)bh * p.Np + (size_t)i * BR + h * (BR / 2)) * D, sStage,
-                                Cfg::kStageTileBytes);
-                            bulk_commit_group();
-                        }
+                    for (int e = 0; e < 32; ++e) sStage[e * D + rl] = __uint_as_float(src[e]);
+                    fence_proxy_async_smem();
+                    named_bar_sync(1, kReadoutThreads);
+                    if (leader) {
+                        bulk_reduce_add_f32(
+                            p.dq_acc + ((size_t)bh * p.Np + (size_t)i * BR + h * (BR / 2)) * D, sStage,
+                            Cfg::kStageTileBytes);
+                        bulk_commit_group();
                     }
                 }
             }
@@ -1430,7 +1497,7 @@ fa_bwd_dkdv2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     item_sh[slot] = item;
                     mbar_arrive(&bar_item_full[slot]);
                     if (item < 0) break;
-                    const BwdCta cta = bwd_cta<CAUSAL, WINDOW, VARLEN, CROSS>(p, BR, item);
+                    const BwdCta cta = bwd_cta<CAUSAL, WINDOW, VARLEN>(p, BR, item);
                     if (cta.idle || cta.n_it == 0) continue;
                     const int jblk = cta.jblk, b = cta.b, g = cta.g, tok0 = cta.tok0;
                     const int z_kv = cta.z_kv, i_start = cta.i_start, n_i = cta.n_i;
@@ -1439,10 +1506,10 @@ fa_bwd_dkdv2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     if (nb > 0 && !fa_wait(&bar_kv_free, (nb - 1) & 1, 42, wc)) break;
                     mbar_arrive_expect_tx(&bar_kv, 2 * Cfg::kKVBytes);
                     for (int c = 0; c < D / 64; ++c) {
-                        tma_load_3d(sK + c * (kBN * 128), &tm_k, &bar_kv, c * 64,
-                                    cta.ktok0 + jblk * kBN, z_kv);
-                        tma_load_3d(sV + c * (kBN * 128), &tm_v, &bar_kv, c * 64,
-                                    cta.ktok0 + jblk * kBN, z_kv);
+                        tma_load_3d(sK + c * (kBN * 128), &tm_k, &bar_kv, c * 64, tok0 + jblk * kBN,
+                                    z_kv);
+                        tma_load_3d(sV + c * (kBN * 128), &tm_v, &bar_kv, c * 64, tok0 + jblk * kBN,
+                                    z_kv);
                     }
                     ++kv_issued;
                     for (int it = 0; it < n_it; ++it) {
@@ -1455,7 +1522,7 @@ fa_bwd_dkdv2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                         const int hq = g * p.G + it / n_i;
                         const int i = i_start + it % n_i;
                         const int bh = b * p.H + hq;
-                        const int z_q = VARLEN || (CROSS && p.cu_seqlens) ? hq : bh;
+                        const int z_q = VARLEN ? hq : bh;
                         uint64_t* full = &bar_full[git % (2 * NS)];
                         mbar_arrive_expect_tx(full, Cfg::kStepBytes);
                         for (int c = 0; c < D / 64; ++c) {
@@ -1483,26 +1550,7 @@ fa_bwd_dkdv2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             }
             __syncwarp();
         } else if (warp == kMmaWarp || warp == kMma2Warp) {
-            if (CROSS || lane == 0) {
-                // CROSS: the warp stays together and one elected lane issues, by a
-                // predicate, so that descriptors travel in uniform registers.
-                const bool leader = CROSS ? elect_one() : true;
-                auto wait = [&](uint64_t* bar, uint32_t parity, int site) -> bool {
-                    return CROSS ? fa_wait_warp(bar, parity, site, wc)
-                                 : fa_wait(bar, parity, site, wc);
-                };
-                auto ss = [&](uint32_t to, uint64_t x, uint64_t y, uint32_t id, uint32_t add) {
-                    if constexpr (CROSS) mma_ss_if(leader, to, x, y, id, add);
-                    else mma_ss(to, x, y, id, add);
-                };
-                auto ts = [&](uint32_t to, uint32_t x, uint64_t y, uint32_t id, uint32_t add) {
-                    if constexpr (CROSS) mma_ts_if(leader, to, x, y, id, add);
-                    else mma_ts(to, x, y, id, add);
-                };
-                auto commit = [&](uint64_t* bar) {
-                    if constexpr (CROSS) mma_commit_if(leader, bar);
-                    else mma_commit(bar);
-                };
+            if (lane == 0) {
                 // MMA issue for pipeline pp: per step S^T, dP^T (once the
                 // read-out has taken the pipeline's previous dQ^T), dV (once P^T
                 // is in TMEM), dK and dQ^T (once dS^T is in SMEM).
@@ -1523,20 +1571,20 @@ fa_bwd_dkdv2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 int gi = 0, nb = 0;
                 for (int n = 0; ok; ++n) {
                     int item;
-                    if (!(CROSS ? next_item_warp(n, item) : next_item_thread(n, item))) { ok = false; break; }
+                    if (!next_item_thread(n, item)) { ok = false; break; }
                     if (item < 0) break;
-                    const BwdCta cta = bwd_cta<CAUSAL, WINDOW, VARLEN, CROSS>(p, BR, item);
+                    const BwdCta cta = bwd_cta<CAUSAL, WINDOW, VARLEN>(p, BR, item);
                     if (cta.idle || cta.n_it == 0) continue;
                     const int n_it = cta.n_it;
                     // Every per-item phase is waited on by both issuers, whether
                     // or not the item has steps of their parity: K_j, V_j landed
                     // and dK, dV zeroed (a waiter never falls two phases behind).
-                    ok = wait(&bar_kv, nb & 1, 50) && wait(&bar_acc_free, nb & 1, 58);
+                    ok = fa_wait(&bar_kv, nb & 1, 50, wc) && fa_wait(&bar_acc_free, nb & 1, 58, wc);
                     for (int it = (gi & 1) == pp ? 0 : 1; ok && it < n_it; it += 2) {
                         const int git = gi + it;
                         const uint32_t k = (uint32_t)git >> 1;
                         const int st = git % NS;
-                        if (!wait(&bar_ready[git % (2 * NS)], (git / (2 * NS)) & 1, 51)) {
+                        if (!fa_wait(&bar_full[git % (2 * NS)], (git / (2 * NS)) & 1, 51, wc)) {
                             ok = false;
                             break;
                         }
@@ -1547,30 +1595,30 @@ fa_bwd_dkdv2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                             const uint64_t qd = sdesc_sw128(q_, 16, 1024);
 #pragma unroll
                             for (int kk = 0; kk < D / 16; ++kk)
-                                ss(tmem + col_s, kd + kmajor_step(kk, kBN * 128),
+                                mma_ss(tmem + col_s, kd + kmajor_step(kk, kBN * 128),
                                        qd + kmajor_step(kk, BR * 128), id_s, kk > 0);
-                            ss(tmem + col_s, onesd,
+                            mma_ss(tmem + col_s, onesd,
                                    sdesc_plain(sext + 2 * st * Cfg::kExtBytes, 128, 256), id_s, 1u);
-                            commit(&bar_s[pp]);
+                            mma_commit(&bar_s[pp]);
                         }
                         // dP^T - D = V_j dO_i^T - D, over the previous dQ^T
-                        if (k > 0 && !wait(&bar_dq_free[pp], (k - 1) & 1, 53)) { ok = false; break; }
+                        if (k > 0 && !fa_wait(&bar_dq_free[pp], (k - 1) & 1, 53, wc)) { ok = false; break; }
                         tc_fence_after();
                         {
                             const uint64_t dod = sdesc_sw128(do_, 16, 1024);
 #pragma unroll
                             for (int kk = 0; kk < D / 16; ++kk)
-                                ss(tmem + col_dpq, vd + kmajor_step(kk, kBN * 128),
+                                mma_ss(tmem + col_dpq, vd + kmajor_step(kk, kBN * 128),
                                        dod + kmajor_step(kk, BR * 128), id_s, kk > 0);
-                            ss(tmem + col_dpq, onesd,
+                            mma_ss(tmem + col_dpq, onesd,
                                    sdesc_plain(sext + (2 * st + 1) * Cfg::kExtBytes, 128, 256), id_s,
                                    1u);
-                            commit(&bar_dp[pp]);
+                            mma_commit(&bar_dp[pp]);
                         }
                         // dV += P^T dO_i (P^T: bf16 pairs in the first 32 S^T columns),
                         // after step git - 1's dV MMAs
-                        if (!wait(&bar_p[pp], k & 1, 52) ||
-                            (git > 0 && !wait(&bar_dv_turn, (git - 1) & 1, 46))) {
+                        if (!fa_wait(&bar_p[pp], k & 1, 52, wc) ||
+                            (git > 0 && !fa_wait(&bar_dv_turn, (git - 1) & 1, 46, wc))) {
                             ok = false;
                             break;
                         }
@@ -1579,14 +1627,14 @@ fa_bwd_dkdv2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                             const uint64_t dod_mn = sdesc_sw128(do_, BR * 128, 1024);
 #pragma unroll
                             for (int kk = 0; kk < BR / 16; ++kk)
-                                ts(tmem + Cfg::kColDV, tmem + col_s + kk * 8,
+                                mma_ts(tmem + Cfg::kColDV, tmem + col_s + kk * 8,
                                        dod_mn + mnmajor_step(kk), id_kv, 1u);
                         }
                         tc_fence_before();   // the MMAs above precede the turn's arrival
-                        if (leader) mbar_arrive(&bar_dv_turn);
+                        mbar_arrive(&bar_dv_turn);
                         // dK += dS^T Q_i, after step git - 1's dK MMAs
-                        if (!wait(&bar_ds[pp], k & 1, 55) ||
-                            (git > 0 && !wait(&bar_dk_turn, (git - 1) & 1, 47))) {
+                        if (!fa_wait(&bar_ds[pp], k & 1, 55, wc) ||
+                            (git > 0 && !fa_wait(&bar_dk_turn, (git - 1) & 1, 47, wc))) {
                             ok = false;
                             break;
                         }
@@ -1595,28 +1643,28 @@ fa_bwd_dkdv2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                             const uint64_t qd_mn = sdesc_sw128(q_, BR * 128, 1024);
 #pragma unroll
                             for (int kk = 0; kk < BR / 16; ++kk)
-                                ss(tmem + Cfg::kColDK, dsd + kmajor_step(kk, kBN * 128),
+                                mma_ss(tmem + Cfg::kColDK, dsd + kmajor_step(kk, kBN * 128),
                                        qd_mn + mnmajor_step(kk), id_kv, 1u);
                         }
                         tc_fence_before();   // the MMAs above precede the turn's arrival
-                        if (leader) mbar_arrive(&bar_dk_turn);
-                        commit(&bar_empty[st]);      // Q_i, dO_i no longer read
+                        mbar_arrive(&bar_dk_turn);
+                        mma_commit(&bar_empty[st]);      // Q_i, dO_i no longer read
                         // dQ^T partial = K_j^T dS^T (K dimension = the 128 keys),
                         // over dP^T, which the compute warps have read
 #pragma unroll
                         for (int kk = 0; kk < kBN / 16; ++kk)
-                            ss(tmem + col_dpq, kd_mn + mnmajor_step(kk), dsd_mn + mnmajor_step(kk),
+                            mma_ss(tmem + col_dpq, kd_mn + mnmajor_step(kk), dsd_mn + mnmajor_step(kk),
                                    id_dq, kk > 0);
-                        commit(&bar_dq_full[pp]);
+                        mma_commit(&bar_dq_full[pp]);
                     }
                     if (ok) {   // every MMA of the item from this thread (possibly none)
-                        commit(&bar_done);
-                        commit(&bar_kv_free);
+                        mma_commit(&bar_done);
+                        mma_commit(&bar_kv_free);
                     }
                     gi += n_it;
                     ++nb;
                 }
-                if (!ok && leader) {   // no MMA of this thread may still write TMEM at teardown
+                if (!ok) {   // no MMA of this thread may still write TMEM at teardown
                     __shared__ uint64_t bar_drain2[2];
                     mbar_init(&bar_drain2[pp], 1);
                     fence_mbar_init();
@@ -1625,33 +1673,6 @@ fa_bwd_dkdv2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 }
             }
             __syncwarp();
-        } else if (CROSS && warp == 11 && p.cu_seqlens) {
-            // --------------------- Q_i, dO_i rows past a packed sequence's queries
-            bool ok = true;
-            int gi = 0;
-            for (int n = 0; ok; ++n) {
-                int item;
-                if (!next_item_warp(n, item) || item < 0) break;
-                const BwdCta cta = bwd_cta<CAUSAL, WINDOW, VARLEN, CROSS>(p, BR, item);
-                if (cta.idle || cta.n_it == 0) continue;
-                for (int it = 0; it < cta.n_it; ++it) {
-                    const int git = gi + it;
-                    const int st = git % NS;
-                    if (!fa_wait_warp(&bar_full[git % (2 * NS)], (git / (2 * NS)) & 1, 67, wc)) {
-                        ok = false;
-                        break;
-                    }
-                    const int left = cta.q_len - (cta.i_start + it % cta.n_i) * BR;
-                    if (left < BR) {
-                        clear_rows(sQ + st * Cfg::kQBytes, D / 64, BR, left, lane, 32);
-                        clear_rows(sDO + st * Cfg::kQBytes, D / 64, BR, left, lane, 32);
-                        fence_proxy_async_smem();
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar_tail[git % (2 * NS)]);
-                }
-                gi += cta.n_it;
-            }
         }
     }
 
@@ -1663,11 +1684,11 @@ fa_bwd_dkdv2_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     }
 }
 
-template <bool CAUSAL, bool WINDOW = false, bool VARLEN = false, bool CROSS = false>
+template <bool CAUSAL, bool WINDOW = false, bool VARLEN = false>
 cudaError_t launch_dkdv2_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                            const CUtensorMap& tdo, const BwdParams& p, int grid,
                            cudaStream_t stream) {
-    auto kern = fa_bwd_dkdv2_kernel<CAUSAL, WINDOW, VARLEN, CROSS>;
+    auto kern = fa_bwd_dkdv2_kernel<CAUSAL, WINDOW, VARLEN>;
     static int configured_device = -1;
     int dev = 0;
     cudaGetDevice(&dev);
@@ -1704,6 +1725,10 @@ cudaError_t launch_bwd_preprocess(const Shape& s, const void* o, bool o_f32, con
     };
     auto* ob = static_cast<const __nv_bfloat16*>(o);
     auto* of = static_cast<const float*>(o);
+    if (s.Nk > 0)   // keys of another length
+        return o_f32 || !full ? cudaErrorInvalidValue
+               : s.d == 128   ? go(fa_bwd_pre_kernel<128, __nv_bfloat16, true, true>, ob)
+                              : go(fa_bwd_pre_kernel<64, __nv_bfloat16, true, true>, ob);
     if (s.d == 128) {
         if (o_f32)
             return full ? go(fa_bwd_pre_kernel<128, float, true>, of)
@@ -1724,14 +1749,12 @@ cudaError_t launch_bwd_dkdv(const Shape& s, const void* q, const void* k, const 
     const int br = (s.d == 128) ? BwdCfg<128>::kBR : BwdCfg<64>::kBR;
     const bool varlen = s.cu_seqlens != nullptr;
     const int rows = varlen ? s.total : s.N;
-    const bool cross = s.Nk > 0;
-    const int krows = !cross ? rows : varlen ? s.total_k : s.Nk;
     const int zq = varlen ? s.H : s.B * s.H, zkv = varlen ? s.Hkv : s.B * s.Hkv;
     CUtensorMap tq, tk, tv, tdo, tdq;
     if (!make_tmap_bf16_3d(&tq, q, s.d, rows, zq, br) ||
         !make_tmap_bf16_3d(&tdo, dout, s.d, rows, zq, br) ||
-        !make_tmap_bf16_3d(&tk, k, s.d, krows, zkv, kBN) ||
-        !make_tmap_bf16_3d(&tv, v, s.d, krows, zkv, kBN) ||
+        !make_tmap_bf16_3d(&tk, k, s.d, rows, zkv, kBN) ||
+        !make_tmap_bf16_3d(&tv, v, s.d, rows, zkv, kBN) ||
         !make_tmap_f32_2d(&tdq, ws.dq_acc, s.d, (long long)s.B * s.H * padded_rows(s.N), 32, br))
         return cudaErrorInvalidValue;
     BwdParams p;
@@ -1741,10 +1764,6 @@ cudaError_t launch_bwd_dkdv(const Shape& s, const void* q, const void* k, const 
     p.Np = padded_rows(s.N);
     p.rows = rows;
     p.cu_seqlens = s.cu_seqlens;
-    p.Nk = cross ? s.Nk : s.N;
-    p.krows = krows;
-    p.kv_lens = s.kv_lens;
-    p.cu_k = s.cu_k;
     p.G = s.H / s.Hkv;
     // Chunk size: what fits a 64 MB L2 budget of Q, dO (bf16) and dQ
     // accumulator (fp32) rows, 8 G N d bytes per key/value head, but at least
@@ -1772,7 +1791,7 @@ cudaError_t launch_bwd_dkdv(const Shape& s, const void* q, const void* k, const 
     p.dv = static_cast<__nv_bfloat16*>(dv);
     p.status = status;
     p.work = ws.work;
-    const int n_kblk = (p.Nk + kBN - 1) / kBN;
+    const int n_kblk = (s.N + kBN - 1) / kBN;
     p.n_bg = s.B * s.Hkv;
     p.n_items = n_kblk * s.B * s.Hkv;
     // Persistent: one CTA per SM (fewer when there are fewer work items),
@@ -1780,10 +1799,6 @@ cudaError_t launch_bwd_dkdv(const Shape& s, const void* q, const void* k, const 
     const int sms = device_sm_count() > 0 ? device_sm_count() : 148;
     const int grid = p.n_items < sms ? p.n_items : sms;
     count_launch();
-    if (cross) {   // keys of another length (no window; d = 64 has a kernel of its own)
-        if (s.window > 0 || s.d != 128) return cudaErrorInvalidValue;
-        return launch_dkdv2_t<false, false, false, true>(tq, tk, tv, tdo, p, grid, stream);
-    }
     if (varlen) {   // packed variable-length sequences (no window)
         if (s.window > 0) return cudaErrorInvalidValue;
         if (s.d == 128)

@@ -383,7 +383,7 @@ fa_bwd_cross64_kernel(const __grid_constant__ CUtensorMap tm_q,
                 int mine = 0;
 #pragma unroll 1
                 for (int b = b0; b < b1; ++b) {
-                    const BwdCta c = bwd_cta_cross(p, BR, b * p.Hkv, 0);
+                    const BwdCta c = bwd_cta(p, BR, b * p.Hkv, 0);
                     if (c.q_len > 0) mine += (c.seq_len + kBN - 1) / kBN * p.Hkv;
                     list_sh[b + 1] = mine;
                 }
@@ -431,9 +431,9 @@ fa_bwd_cross64_kernel(const __grid_constant__ CUtensorMap tm_q,
                             }
                             const int blocks = (list_sh[lo + 1] - list_sh[lo]) / p.Hkv;
                             const int at = old - list_sh[lo], g = at / blocks;
-                            to = bwd_cta_cross(p, BR, lo * p.Hkv + g, at - g * blocks);
+                            to = bwd_cta(p, BR, lo * p.Hkv + g, at - g * blocks);
                         } else {
-                            to = bwd_cta_cross(p, BR, old / n_kblk, old % n_kblk);
+                            to = bwd_cta(p, BR, old / n_kblk, old % n_kblk);
                         }
                     } while (to.idle || to.n_it == 0);
                     item_sh[nb & 1] = to;
@@ -676,7 +676,7 @@ fa_bwd_cross64_dq_kernel(__nv_bfloat16* __restrict__ dq, long long n_rows, int d
                          const BwdParams p) {
     if ((int)blockIdx.x >= dq_blocks) {
         const int item = (int)blockIdx.x - dq_blocks, n_kblk = (p.Nk + kBN - 1) / kBN;
-        const BwdCta c = bwd_cta_cross(p, BR, item / n_kblk, item % n_kblk);
+        const BwdCta c = bwd_cta(p, BR, item / n_kblk, item % n_kblk);
         if (!c.idle && c.n_it > 0) return;
         zero_grads<D>(p, c, c.jblk * kBN + threadIdx.x / 2, threadIdx.x % 2 * 32,
                       threadIdx.x % 2 * 32 + 32, true, true);
@@ -715,30 +715,7 @@ cudaError_t launch_bwd_cross64(const Shape& s, const void* q, const void* k, con
                                const void* dout, void* dq, void* dk, void* dv,
                                const BwdWorkspace& ws, DeviceStatus* status, cudaStream_t stream) {
     const bool packed = s.cu_seqlens != nullptr;
-    BwdParams p = {};
-    p.H = s.H;
-    p.Hkv = s.Hkv;
-    p.N = s.N;
-    p.Np = padded_rows(s.N);
-    p.G = s.H / s.Hkv;
-    p.causal = s.causal;
-    p.rows = packed ? s.total : s.N;
-    p.cu_seqlens = s.cu_seqlens;
-    p.Nk = s.Nk;
-    p.krows = packed ? s.total_k : s.Nk;
-    p.kv_lens = s.kv_lens;
-    p.cu_k = s.cu_k;
-    p.scale = s.scale;
-    p.scale_log2 = (float)((double)s.scale * 1.4426950408889634);
-    p.lse_ext = ws.lse_ext;
-    p.d_ext = ws.d_ext;
-    p.dq_acc = ws.dq_acc;
-    p.work = ws.work;
-    p.n_bg = s.B * s.Hkv;
-    p.n_items = (s.Nk + kBN - 1) / kBN * p.n_bg;
-    p.dk = static_cast<__nv_bfloat16*>(dk);
-    p.dv = static_cast<__nv_bfloat16*>(dv);
-    p.status = status;
+    const BwdParams p = bwd_params(s, dk, dv, ws, status);
     const int zq = packed ? s.H : s.B * s.H, zk = packed ? s.Hkv : s.B * s.Hkv;
     CUtensorMap tq, tk, tv, tdo;
     if (!make_tmap_bf16_3d(&tq, q, D, p.rows, zq, BR) ||

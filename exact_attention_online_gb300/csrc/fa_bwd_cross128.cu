@@ -1,0 +1,633 @@
+// The dK/dV pass of the backward with keys of another length at d = 128 (fa_bwd_cross.cu has
+// d = 64): the two-pipeline kernel of the dense backward (two query blocks of 64 in flight, each
+// with its own tensor-memory columns and issuing warp; its notes are in fa_bwd.cu), with
+//   - its own work items (key blocks of keys of their own), masks for both lengths, rows of K
+//     and V past a sequence's keys and of Q and dO past its queries cleared, and zeros in the
+//     gradients of keys that no query sees,
+//   - dQ added to its accumulator from registers, a barrier arrival a warp and MMAs issued by a
+//     predicate of a warp that stays together.
+// A kernel of its own because the dense ones lose 1 % when they are compiled from a shared
+// source.  16 packed pairs of sequences, H32 Hkv8, d = 128: the backward 900 us, of which this
+// pass has about 780, 63 % of the bf16 rate.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+
+#include "bwd_parts.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kBN = kBwdKeys;   // keys per CTA
+constexpr int kThreads = 512;
+constexpr int kComputeWarps = 8;
+constexpr int kProducerWarp = 8;
+constexpr int kMmaWarp = 9;      // pipeline 0's MMAs; allocates TMEM
+constexpr int kMma2Warp = 10;    // pipeline 1's
+constexpr int kReadoutWarp0 = 12;
+constexpr int kReadoutThreads = 128;
+// Register split (setmaxnreg) of the launch's 512 x 128.
+constexpr int kRegsCompute = 152;
+constexpr int kRegsReadout = 96;
+constexpr int kRegsControl = 112;
+constexpr int kRegsNeeded = 256 * kRegsCompute + 128 * kRegsReadout + 128 * kRegsControl;
+
+struct Cross2Cfg {
+    static constexpr int D = 128;
+    static constexpr int kBR = 64;
+    static constexpr int kStages = 3;
+    static constexpr int kKVBytes = kBN * D * 2;               // 32 KB
+    static constexpr int kQBytes = kBR * D * 2;                // 16 KB
+    static constexpr int kDSBytes = kBN * kBR * 2;             // 16 KB
+    static constexpr int kOnesBytes = kBN * 32;
+    static constexpr int kExtBytes = kBR * 32;
+    static constexpr int kOffK = 0;
+    static constexpr int kOffV = kOffK + kKVBytes;
+    static constexpr int kOffQ = kOffV + kKVBytes;               // kStages
+    static constexpr int kOffDO = kOffQ + kStages * kQBytes;     // kStages
+    static constexpr int kOffDS = kOffDO + kStages * kQBytes;    // one per pipeline
+    static constexpr int kOffOnes = kOffDS + 2 * kDSBytes;
+    static constexpr int kOffExt = kOffOnes + kOnesBytes;        // [stage][lse, d]
+    static constexpr int kSmemBytes = kOffExt + kStages * 2 * kExtBytes;
+    static constexpr int kSmemAlloc = kSmemBytes + 1024;
+    static constexpr int kStepBytes = 2 * kQBytes + 2 * kExtBytes;
+    static constexpr uint32_t kColDK = 0, kColDV = 128;
+    __host__ __device__ static constexpr uint32_t col_s(int pp) { return 256 + 128 * pp; }
+    __host__ __device__ static constexpr uint32_t col_dpq(int pp) { return 320 + 128 * pp; }
+};
+static_assert(Cross2Cfg::kSmemAlloc <= 227 * 1024 - 1024, "shared memory");
+
+__global__ void __launch_bounds__(kThreads, 1)
+cross_dkdv128_kernel(const __grid_constant__ CUtensorMap tm_q,
+                     const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_v,
+                     const __grid_constant__ CUtensorMap tm_do, const BwdParams p) {
+    using Cfg = Cross2Cfg;
+    constexpr int D = Cfg::D, BR = Cfg::kBR, NS = Cfg::kStages;
+    constexpr int kPipeWarps = 4;                // compute warps of one pipeline
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    // bar_full[git % 6]: step git's Q_i, dO_i and tables landed (stage git % 3)
+    __shared__ uint64_t bar_kv, bar_kv_free, bar_full[2 * NS], bar_empty[NS];
+    __shared__ uint64_t bar_s[2], bar_dp[2], bar_p[2], bar_ds[2], bar_dq_full[2], bar_dq_free[2];
+    __shared__ uint64_t bar_done, bar_acc_free;
+    // bar_dv_turn / bar_dk_turn: phase git completes when step git's dV (dK)
+    // MMAs have been issued
+    __shared__ uint64_t bar_dv_turn, bar_dk_turn;
+    __shared__ uint64_t bar_item_full[2], bar_item_empty[2];
+    __shared__ int item_sh[2];
+    const int kItemConsumers = kComputeWarps + 4 + 2 + (p.cu_seqlens ? 1 : 0);
+    __shared__ uint32_t tmem_base_sh;
+    __shared__ int abort_sh;
+    const WaitCtx wc{p.status, &abort_sh};
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool causal = p.causal;
+    // Packed: warp 11 clears the rows of Q_i and dO_i past a sequence's queries (another
+    // sequence's, or anything), and the issuers wait for it.
+    __shared__ uint64_t bar_tail[2 * NS];
+    uint64_t* const bar_ready = p.cu_seqlens ? bar_tail : bar_full;
+
+    uint8_t* sK = smem + Cfg::kOffK;
+    uint8_t* sV = smem + Cfg::kOffV;
+    uint8_t* sQ = smem + Cfg::kOffQ;
+    uint8_t* sDO = smem + Cfg::kOffDO;
+    uint8_t* sDS = smem + Cfg::kOffDS;
+    uint8_t* sOnes = smem + Cfg::kOffOnes;
+    uint8_t* sExt = smem + Cfg::kOffExt;      // stage st: lse at 2 st, d at 2 st + 1
+
+    const int n_kblk = (p.Nk + kBN - 1) / kBN;
+
+    bwd_fill_ones(sOnes, p.scale_log2);
+
+    if (threadIdx.x == 0) {
+        abort_sh = 0;
+        mbar_init(&bar_kv, 1);
+        mbar_init(&bar_kv_free, 2);                  // one commit per MMA issuer
+        for (int s = 0; s < 2 * NS; ++s) {
+            mbar_init(&bar_full[s], 1);
+            mbar_init(&bar_tail[s], 1);
+        }
+        for (int s = 0; s < NS; ++s) mbar_init(&bar_empty[s], 1);   // the step's MMA issuer
+        for (int q = 0; q < 2; ++q) {
+            mbar_init(&bar_s[q], 1);
+            mbar_init(&bar_dp[q], 1);
+            mbar_init(&bar_p[q], kPipeWarps);        // a warp arrives by one lane
+            mbar_init(&bar_ds[q], kPipeWarps);
+            mbar_init(&bar_dq_full[q], 1);
+            mbar_init(&bar_dq_free[q], kReadoutThreads / 32);
+            mbar_init(&bar_item_full[q], 1);
+            mbar_init(&bar_item_empty[q], kItemConsumers);
+        }
+        mbar_init(&bar_done, 2);                     // one commit per MMA issuer, per item
+        mbar_init(&bar_acc_free, kComputeWarps);     // dK, dV zeroed for the item
+        mbar_init(&bar_dv_turn, 1);
+        mbar_init(&bar_dk_turn, 1);
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&tmem_base_sh, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base_sh;
+
+    auto arrive = [&](uint64_t* bar) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+    };
+    auto next_item = [&](int n, int& item) -> bool {
+        const int slot = n & 1;
+        if (!fa_wait_warp(&bar_item_full[slot], (n >> 1) & 1, 65, wc)) return false;
+        item = item_sh[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_item_empty[slot]);
+        return true;
+    };
+    if (warp < kComputeWarps) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsCompute));
+        // ------------------------------------------------------------ compute
+        // warp w: pipeline w / 4 (the steps of that parity), TMEM lane quarter
+        // w % 4 (= 32 key rows), all 64 query columns of the step.
+        const int cp = warp >> 2, quarter = warp & 3;
+        const int rl = quarter * 32 + lane;          // key row within the block
+        const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
+        const uint32_t col_s = Cfg::col_s(cp), col_dp = Cfg::col_dpq(cp);
+        uint8_t* const sds = sDS + cp * Cfg::kDSBytes;
+        const float c = p.scale_log2;
+        bool ok = true;
+        int gi = 0, nb = 0;   // query-block steps and work items of this CTA so far
+        for (int n = 0; ok; ++n) {
+            int item;
+            if (!next_item(n, item) || item < 0) break;
+            const BwdCta cta = bwd_cta(p, BR, item / n_kblk, item % n_kblk);
+            if (cta.idle || cta.n_it == 0) {
+                zero_grads<D>(p, cta, cta.jblk * kBN + rl, 0, D, !cp, cp);
+                continue;
+            }
+            const int jblk = cta.jblk, seq_len = cta.seq_len, z_kv = cta.z_kv;
+            const int i_start = cta.i_start, n_i = cta.n_i, n_it = cta.n_it;
+            const int key = jblk * kBN + rl;
+            if (jblk * kBN + kBN > seq_len) {
+                // K_j's (V_j's) rows past the keys: cleared before bar_acc_free
+                if (!fa_wait_warp(&bar_kv, nb & 1, 64, wc)) { ok = false; break; }
+                clear_rows(cp ? sV : sK, D / 64, kBN, seq_len - jblk * kBN, rl, kBN);
+                fence_proxy_async_smem();
+            }
+            // dK (pipeline 0's warps) and dV (pipeline 1's) of this item start
+            // from zero; the previous item's were read out below
+            {
+                uint32_t z[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) z[e] = 0u;
+#pragma unroll
+                for (int c0 = 0; c0 < D; c0 += 32)
+                    tmem_st32(lane_addr + (cp ? Cfg::kColDV : Cfg::kColDK) + c0, z);
+                tmem_st_wait();
+                tc_fence_before();
+                arrive(&bar_acc_free);
+            }
+            for (int it = (gi & 1) == cp ? 0 : 1; ok && it < n_it; it += 2) {
+                const int git = gi + it;
+                const uint32_t k = (uint32_t)git >> 1;       // this pipeline's step count
+                const int i = i_start + it % n_i;
+                if (!fa_wait_warp(&bar_s[cp], k & 1, 61, wc)) { ok = false; break; }
+                tc_fence_after();
+                const int q0 = i * BR;
+                const bool need_mask = (causal && q0 + cta.off < jblk * kBN + kBN - 1) ||
+                                       jblk * kBN + kBN > seq_len;
+                // the first query (of the step) that sees this thread's key
+                const int first = key >= seq_len ? BR : causal ? key - cta.off - q0 : 0;
+                // P^T = 2^(S'^T c), S'^T = S^T - LSE log2(e) / c from the tensor
+                // core; fp32 kept for dS, the bf16 pairs written over the first
+                // 32 columns of S^T (already read) for the dV MMA.
+                float pf[BR];
+                const uint64_t c2 = f2(c, c);
+#pragma unroll
+                for (int ch = 0; ch < BR / 32; ++ch) {
+                    uint32_t sr[32];
+                    tmem_ld32(lane_addr + col_s + ch * 32, sr);
+                    tmem_ld_wait(sr);
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int e2 = 0; e2 < 16; ++e2) {
+                        const int qe = ch * 32 + 2 * e2;
+                        float x0, x1;
+                        f2_split(f2_mul(f2(__uint_as_float(sr[2 * e2]), __uint_as_float(sr[2 * e2 + 1])),
+                                        c2),
+                                 x0, x1);
+                        float p0 = ex2(x0), p1 = ex2(x1);
+                        if (need_mask) {
+                            if (qe < first) p0 = 0.0f;
+                            if (qe + 1 < first) p1 = 0.0f;
+                        }
+                        pf[qe] = p0;
+                        pf[qe + 1] = p1;
+                        pk[e2] = pack_bf16x2(p0, p1);
+                    }
+                    tmem_st16(lane_addr + col_s + ch * 16, pk);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                arrive(&bar_p[cp]);
+
+                // dS^T = P^T o (dP^T - D) -> bf16, swizzled [key][query] tile;
+                // dP^T - D comes from the tensor core.  The pipeline's previous
+                // dK and dQ MMAs, which read this tile, were issued before this
+                // dP^T, so its completion frees the tile.
+                if (!fa_wait_warp(&bar_dp[cp], k & 1, 62, wc)) { ok = false; break; }
+                tc_fence_after();
+#pragma unroll
+                for (int ch = 0; ch < BR / 32; ++ch) {
+                    uint32_t dpr[32];
+                    tmem_ld32(lane_addr + col_dp + ch * 32, dpr);
+                    tmem_ld_wait(dpr);
+                    uint32_t dsk[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float d0, d1;
+                        f2_split(f2_mul(f2(pf[ch * 32 + 2 * e], pf[ch * 32 + 2 * e + 1]),
+                                        f2(__uint_as_float(dpr[2 * e]), __uint_as_float(dpr[2 * e + 1]))),
+                                 d0, d1);
+                        dsk[e] = pack_bf16x2(d0, d1);
+                    }
+                    uint8_t* rowp = sds + rl * 128;
+#pragma unroll
+                    for (int u4 = 0; u4 < 4; ++u4) {
+                        const int unit = ch * 4 + u4;
+                        *reinterpret_cast<uint4*>(rowp + ((unit ^ (rl & 7)) * 16)) =
+                            make_uint4(dsk[u4 * 4 + 0], dsk[u4 * 4 + 1], dsk[u4 * 4 + 2],
+                                       dsk[u4 * 4 + 3]);
+                    }
+                }
+                tc_fence_before();   // the dP^T reads precede the dQ^T MMA over them
+                fence_proxy_async_smem();
+                arrive(&bar_ds[cp]);
+            }
+            // ---------------------------------------------------- dK, dV epilogue
+            if (ok && fa_wait_warp(&bar_done, nb & 1, 63, wc)) {
+                tc_fence_after();
+                const bool there = key < seq_len;
+                const bool valid = there || (!p.cu_seqlens && key < p.Nk);
+                const size_t row = ((size_t)z_kv * p.krows + cta.ktok0 + (valid ? key : 0)) * D;
+                const uint32_t col = cp ? Cfg::kColDV : Cfg::kColDK;
+                const float mul = cp ? 1.0f : p.scale;
+                __nv_bfloat16* dst = (cp ? p.dv : p.dk) + row;
+#pragma unroll
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    uint32_t r[32];
+                    tmem_ld32(lane_addr + col + c0, r);
+                    tmem_ld_wait(r);
+                    if (!there)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) r[e] = 0u;
+                    if (valid) {
+                        uint4* d4 = reinterpret_cast<uint4*>(dst + c0);
+#pragma unroll
+                        for (int q4 = 0; q4 < 4; ++q4) {
+                            uint4 w;
+                            w.x = pack_bf16x2(__uint_as_float(r[q4 * 8 + 0]) * mul,
+                                              __uint_as_float(r[q4 * 8 + 1]) * mul);
+                            w.y = pack_bf16x2(__uint_as_float(r[q4 * 8 + 2]) * mul,
+                                              __uint_as_float(r[q4 * 8 + 3]) * mul);
+                            w.z = pack_bf16x2(__uint_as_float(r[q4 * 8 + 4]) * mul,
+                                              __uint_as_float(r[q4 * 8 + 5]) * mul);
+                            w.w = pack_bf16x2(__uint_as_float(r[q4 * 8 + 6]) * mul,
+                                              __uint_as_float(r[q4 * 8 + 7]) * mul);
+                            d4[q4] = w;
+                        }
+                    }
+                }
+            } else {
+                ok = false;
+            }
+            gi += n_it;
+            ++nb;
+        }
+    } else if (warp >= kReadoutWarp0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsReadout));
+        // ----------------------------------------------------- dQ read-out
+        // TMEM (the step's pipeline) -> registers, and added from there, 128 bytes a warp
+        // and query: a bulk copy that adds takes some 1500 cycles until it has read its
+        // tile, and a step's two wait for one another (16 packed pairs of sequences,
+        // H32 Hkv8: the backward 980 us with copies, 936 with these).
+        const int quarter = warp & 3;
+        const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
+        const int rl = quarter * 32 + lane;          // head-dim index
+        bool ok = true;
+        int gi = 0;
+        for (int n = 0; ok; ++n) {
+            int item;
+            if (!next_item(n, item) || item < 0) break;
+            const BwdCta cta = bwd_cta(p, BR, item / n_kblk, item % n_kblk);
+            if (cta.idle || cta.n_it == 0) continue;
+            const int b = cta.b, g = cta.g, i_start = cta.i_start, n_i = cta.n_i, n_it = cta.n_it;
+            for (int it = 0; ok && it < n_it; ++it) {
+                const int git = gi + it;
+                const int pp = git & 1;
+                const uint32_t k = (uint32_t)git >> 1;
+                const int hq = g * p.G + it / n_i;
+                const int i = i_start + it % n_i;
+                const int bh = b * p.H + hq;
+                const bool w_ok = fa_wait_warp(&bar_dq_full[pp], k & 1, 70, wc);
+                if (named_bar_or(1, kReadoutThreads, !w_ok)) { ok = false; break; }
+                tc_fence_after();
+                uint32_t r0[32], r1[32];
+                tmem_ld32(lane_addr + Cfg::col_dpq(pp), r0);
+                tmem_ld32(lane_addr + Cfg::col_dpq(pp) + 32, r1);
+                tmem_ld_wait(r0);
+                asm volatile("" : FA_R32(r1) : : "memory");
+                tc_fence_before();
+                arrive(&bar_dq_free[pp]);
+                float* const to = p.dq_acc + ((size_t)bh * p.Np + (size_t)i * BR) * D + rl;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) red_add_f32(to + e * D, r0[e]);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) red_add_f32(to + (32 + e) * D, r1[e]);
+            }
+            gi += n_it;
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
+        if (warp == kProducerWarp) {
+            if (lane == 0) {
+                tma_prefetch_desc(&tm_q);
+                tma_prefetch_desc(&tm_do);
+                int gi = 0, nb = 0;
+                int issued = 0, kv_issued = 0;
+                bool ok = true;
+                for (int n = 0; ok; ++n) {
+                    const int slot = n & 1;
+                    if (n >= 2 && !fa_wait(&bar_item_empty[slot], ((n >> 1) - 1) & 1, 66, wc)) break;
+                    // Every CTA's last take finds no item; the last of those
+                    // takes leaves the counter zero for the next launch.
+                    const int old = atomicAdd(p.work, 1);
+                    const int item = old < p.n_items ? old : -1;
+                    if (old == p.n_items + (int)gridDim.x - 1) *p.work = 0;
+                    item_sh[slot] = item;
+                    mbar_arrive(&bar_item_full[slot]);
+                    if (item < 0) break;
+                    const BwdCta cta = bwd_cta(p, BR, item / n_kblk, item % n_kblk);
+                    if (cta.idle || cta.n_it == 0) continue;
+                    const int jblk = cta.jblk, b = cta.b, g = cta.g, tok0 = cta.tok0;
+                    const int z_kv = cta.z_kv, i_start = cta.i_start, n_i = cta.n_i;
+                    const int n_it = cta.n_it;
+                    // K_j, V_j over the previous item's, whose MMAs have completed
+                    if (nb > 0 && !fa_wait(&bar_kv_free, (nb - 1) & 1, 42, wc)) break;
+                    mbar_arrive_expect_tx(&bar_kv, 2 * Cfg::kKVBytes);
+                    for (int c = 0; c < D / 64; ++c) {
+                        tma_load_3d(sK + c * (kBN * 128), &tm_k, &bar_kv, c * 64,
+                                    cta.ktok0 + jblk * kBN, z_kv);
+                        tma_load_3d(sV + c * (kBN * 128), &tm_v, &bar_kv, c * 64,
+                                    cta.ktok0 + jblk * kBN, z_kv);
+                    }
+                    ++kv_issued;
+                    for (int it = 0; it < n_it; ++it) {
+                        const int git = gi + it;
+                        const int st = git % NS, u = git / NS;
+                        if (git >= NS && !fa_wait(&bar_empty[st], (u - 1) & 1, 40, wc)) {
+                            ok = false;
+                            break;
+                        }
+                        const int hq = g * p.G + it / n_i;
+                        const int i = i_start + it % n_i;
+                        const int bh = b * p.H + hq;
+                        const int z_q = p.cu_seqlens ? hq : bh;
+                        uint64_t* full = &bar_full[git % (2 * NS)];
+                        mbar_arrive_expect_tx(full, Cfg::kStepBytes);
+                        for (int c = 0; c < D / 64; ++c) {
+                            tma_load_3d(sQ + st * Cfg::kQBytes + c * (BR * 128), &tm_q, full, c * 64,
+                                        tok0 + i * BR, z_q);
+                            tma_load_3d(sDO + st * Cfg::kQBytes + c * (BR * 128), &tm_do, full, c * 64,
+                                        tok0 + i * BR, z_q);
+                        }
+                        const size_t xrow = (size_t)bh * p.Np + (size_t)i * BR;
+                        bulk_load(sExt + (2 * st) * Cfg::kExtBytes, p.lse_ext + xrow * kExtCols,
+                                  Cfg::kExtBytes, full);
+                        bulk_load(sExt + (2 * st + 1) * Cfg::kExtBytes, p.d_ext + xrow * kExtCols,
+                                  Cfg::kExtBytes, full);
+                        issued = git + 1;
+                    }
+                    gi += n_it;
+                    ++nb;
+                }
+                if (abort_sh) {   // drain the copies still in flight (bounded)
+                    const WaitCtx dc{p.status, nullptr};
+                    if (kv_issued > 0) fa_wait(&bar_kv, (kv_issued - 1) & 1, 41, dc);
+                    for (int x = max(0, issued - NS); x < issued; ++x)
+                        fa_wait(&bar_full[x % (2 * NS)], (x / (2 * NS)) & 1, 41, dc);
+                }
+            }
+            __syncwarp();
+        } else if (warp == kMmaWarp || warp == kMma2Warp) {
+            // The warp stays together and one elected lane issues, by a predicate, so
+            // that descriptors travel in uniform registers.
+            const bool leader = elect_one();
+            auto wait = [&](uint64_t* bar, uint32_t parity, int site) -> bool {
+                return fa_wait_warp(bar, parity, site, wc);
+            };
+            auto ss = [&](uint32_t to, uint64_t x, uint64_t y, uint32_t id, uint32_t add) {
+                mma_ss_if(leader, to, x, y, id, add);
+            };
+            auto ts = [&](uint32_t to, uint32_t x, uint64_t y, uint32_t id, uint32_t add) {
+                mma_ts_if(leader, to, x, y, id, add);
+            };
+            auto commit = [&](uint64_t* bar) { mma_commit_if(leader, bar); };
+            // MMA issue for pipeline pp: per step S^T, dP^T (once the
+            // read-out has taken the pipeline's previous dQ^T), dV (once P^T
+            // is in TMEM), dK and dQ^T (once dS^T is in SMEM).
+            const int pp = (warp == kMmaWarp) ? 0 : 1;
+            constexpr uint32_t id_s = idesc_bf16_f32(128, BR, false, false);
+            constexpr uint32_t id_kv = idesc_bf16_f32(128, D, false, true);
+            constexpr uint32_t id_dq = idesc_bf16_f32(128, 64, true, true);
+            const uint32_t sk = smem_u32(sK), sv = smem_u32(sV), sq = smem_u32(sQ),
+                           sdo = smem_u32(sDO), sds = smem_u32(sDS) + pp * Cfg::kDSBytes;
+            const uint64_t kd = sdesc_sw128(sk, 16, 1024), vd = sdesc_sw128(sv, 16, 1024);
+            const uint64_t dsd = sdesc_sw128(sds, 16, 1024);
+            const uint64_t kd_mn = sdesc_sw128(sk, kBN * 128, 1024);
+            const uint64_t dsd_mn = sdesc_sw128(sds, kBN * 128, 1024);
+            const uint32_t sext = smem_u32(sExt);
+            const uint64_t onesd = sdesc_plain(smem_u32(sOnes), 128, 256);
+            const uint32_t col_s = Cfg::col_s(pp), col_dpq = Cfg::col_dpq(pp);
+            bool ok = true;
+            int gi = 0, nb = 0;
+            for (int n = 0; ok; ++n) {
+                int item;
+                if (!next_item(n, item)) { ok = false; break; }
+                if (item < 0) break;
+                const BwdCta cta = bwd_cta(p, BR, item / n_kblk, item % n_kblk);
+                if (cta.idle || cta.n_it == 0) continue;
+                const int n_it = cta.n_it;
+                // Every per-item phase is waited on by both issuers, whether
+                // or not the item has steps of their parity: K_j, V_j landed
+                // and dK, dV zeroed (a waiter never falls two phases behind).
+                ok = wait(&bar_kv, nb & 1, 50) && wait(&bar_acc_free, nb & 1, 58);
+                for (int it = (gi & 1) == pp ? 0 : 1; ok && it < n_it; it += 2) {
+                    const int git = gi + it;
+                    const uint32_t k = (uint32_t)git >> 1;
+                    const int st = git % NS;
+                    if (!wait(&bar_ready[git % (2 * NS)], (git / (2 * NS)) & 1, 51)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t q_ = sq + st * Cfg::kQBytes, do_ = sdo + st * Cfg::kQBytes;
+                    // S^T = K_j Q_i^T - LSE log2(e) / c
+                    {
+                        const uint64_t qd = sdesc_sw128(q_, 16, 1024);
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            ss(tmem + col_s, kd + kmajor_step(kk, kBN * 128),
+                                   qd + kmajor_step(kk, BR * 128), id_s, kk > 0);
+                        ss(tmem + col_s, onesd,
+                               sdesc_plain(sext + 2 * st * Cfg::kExtBytes, 128, 256), id_s, 1u);
+                        commit(&bar_s[pp]);
+                    }
+                    // dP^T - D = V_j dO_i^T - D, over the previous dQ^T
+                    if (k > 0 && !wait(&bar_dq_free[pp], (k - 1) & 1, 53)) { ok = false; break; }
+                    tc_fence_after();
+                    {
+                        const uint64_t dod = sdesc_sw128(do_, 16, 1024);
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            ss(tmem + col_dpq, vd + kmajor_step(kk, kBN * 128),
+                                   dod + kmajor_step(kk, BR * 128), id_s, kk > 0);
+                        ss(tmem + col_dpq, onesd,
+                               sdesc_plain(sext + (2 * st + 1) * Cfg::kExtBytes, 128, 256), id_s,
+                               1u);
+                        commit(&bar_dp[pp]);
+                    }
+                    // dV += P^T dO_i (P^T: bf16 pairs in the first 32 S^T columns),
+                    // after step git - 1's dV MMAs
+                    if (!wait(&bar_p[pp], k & 1, 52) ||
+                        (git > 0 && !wait(&bar_dv_turn, (git - 1) & 1, 46))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    {
+                        const uint64_t dod_mn = sdesc_sw128(do_, BR * 128, 1024);
+#pragma unroll
+                        for (int kk = 0; kk < BR / 16; ++kk)
+                            ts(tmem + Cfg::kColDV, tmem + col_s + kk * 8,
+                                   dod_mn + mnmajor_step(kk), id_kv, 1u);
+                    }
+                    tc_fence_before();   // the MMAs above precede the turn's arrival
+                    if (leader) mbar_arrive(&bar_dv_turn);
+                    // dK += dS^T Q_i, after step git - 1's dK MMAs
+                    if (!wait(&bar_ds[pp], k & 1, 55) ||
+                        (git > 0 && !wait(&bar_dk_turn, (git - 1) & 1, 47))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    {
+                        const uint64_t qd_mn = sdesc_sw128(q_, BR * 128, 1024);
+#pragma unroll
+                        for (int kk = 0; kk < BR / 16; ++kk)
+                            ss(tmem + Cfg::kColDK, dsd + kmajor_step(kk, kBN * 128),
+                                   qd_mn + mnmajor_step(kk), id_kv, 1u);
+                    }
+                    tc_fence_before();   // the MMAs above precede the turn's arrival
+                    if (leader) mbar_arrive(&bar_dk_turn);
+                    commit(&bar_empty[st]);      // Q_i, dO_i no longer read
+                    // dQ^T partial = K_j^T dS^T (K dimension = the 128 keys),
+                    // over dP^T, which the compute warps have read
+#pragma unroll
+                    for (int kk = 0; kk < kBN / 16; ++kk)
+                        ss(tmem + col_dpq, kd_mn + mnmajor_step(kk), dsd_mn + mnmajor_step(kk),
+                               id_dq, kk > 0);
+                    commit(&bar_dq_full[pp]);
+                }
+                if (ok) {   // every MMA of the item from this thread (possibly none)
+                    commit(&bar_done);
+                    commit(&bar_kv_free);
+                }
+                gi += n_it;
+                ++nb;
+            }
+            if (!ok && leader) {   // no MMA of this thread may still write TMEM at teardown
+                __shared__ uint64_t bar_drain2[2];
+                mbar_init(&bar_drain2[pp], 1);
+                fence_mbar_init();
+                mma_commit(&bar_drain2[pp]);
+                fa_wait(&bar_drain2[pp], 0, 59, WaitCtx{p.status, nullptr});
+            }
+            __syncwarp();
+        } else if (warp == 11 && p.cu_seqlens) {
+            // --------------------- Q_i, dO_i rows past a packed sequence's queries
+            bool ok = true;
+            int gi = 0;
+            for (int n = 0; ok; ++n) {
+                int item;
+                if (!next_item(n, item) || item < 0) break;
+                const BwdCta cta = bwd_cta(p, BR, item / n_kblk, item % n_kblk);
+                if (cta.idle || cta.n_it == 0) continue;
+                for (int it = 0; it < cta.n_it; ++it) {
+                    const int git = gi + it;
+                    const int st = git % NS;
+                    if (!fa_wait_warp(&bar_full[git % (2 * NS)], (git / (2 * NS)) & 1, 67, wc)) {
+                        ok = false;
+                        break;
+                    }
+                    const int left = cta.q_len - (cta.i_start + it % cta.n_i) * BR;
+                    if (left < BR) {
+                        clear_rows(sQ + st * Cfg::kQBytes, D / 64, BR, left, lane, 32);
+                        clear_rows(sDO + st * Cfg::kQBytes, D / 64, BR, left, lane, 32);
+                        fence_proxy_async_smem();
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar_tail[git % (2 * NS)]);
+                }
+                gi += cta.n_it;
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_bwd_cross128(const Shape& s, const void* q, const void* k, const void* v,
+                                const void* dout, void* dk, void* dv, const BwdWorkspace& ws,
+                                DeviceStatus* status, cudaStream_t stream) {
+    using Cfg = Cross2Cfg;
+    const bool packed = s.cu_seqlens != nullptr;
+    const BwdParams p = bwd_params(s, dk, dv, ws, status);
+    const int zq = packed ? s.H : s.B * s.H, zkv = packed ? s.Hkv : s.B * s.Hkv;
+    CUtensorMap tq, tk, tv, tdo;
+    if (!make_tmap_bf16_3d(&tq, q, s.d, p.rows, zq, Cfg::kBR) ||
+        !make_tmap_bf16_3d(&tdo, dout, s.d, p.rows, zq, Cfg::kBR) ||
+        !make_tmap_bf16_3d(&tk, k, s.d, p.krows, zkv, kBN) ||
+        !make_tmap_bf16_3d(&tv, v, s.d, p.krows, zkv, kBN))
+        return cudaErrorInvalidValue;
+    static int configured_device = -1;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (configured_device != dev) {
+        cudaFuncAttributes attr;
+        cudaError_t e = cudaFuncGetAttributes(&attr, cross_dkdv128_kernel);
+        if (e != cudaSuccess) return e;
+        if (attr.numRegs * kThreads < kRegsNeeded) return cudaErrorInvalidConfiguration;
+        e = cudaFuncSetAttribute(cross_dkdv128_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 Cfg::kSmemAlloc);
+        if (e != cudaSuccess) return e;
+        configured_device = dev;
+    }
+    // Persistent: one CTA per SM, taking items in order from the work counter.
+    const int sms = device_sm_count() > 0 ? device_sm_count() : 148;
+    const int grid = p.n_items < sms ? p.n_items : sms;
+    count_launch();
+    cross_dkdv128_kernel<<<grid, kThreads, Cfg::kSmemAlloc, stream>>>(tq, tk, tv, tdo, p);
+    return cudaGetLastError();
+}
+
+}  // namespace fa

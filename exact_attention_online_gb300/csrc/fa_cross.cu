@@ -54,8 +54,8 @@ fa_status forward(const Shape& s, const void* q, const void* k, const void* v, v
     int dev;
     DeviceStatus* status;
     if ((st = ready_device(&dev, &status)) != FA_OK) return st;
-    return launch_fwd(s, q, k, v, o, lse, false, status, (cudaStream_t)stream, nullptr,
-                      workspace) == cudaSuccess
+    return launch_fwd_cross(s, q, k, v, o, lse, workspace, status, (cudaStream_t)stream) ==
+                   cudaSuccess
                ? FA_OK
                : FA_ERR_CUDA;
 }
@@ -77,7 +77,7 @@ fa_status backward(const Shape& s, const void* q, const void* k, const void* v, 
     if (e == cudaSuccess && s.d == 64) {
         e = launch_bwd_cross64(s, q, k, v, dout, dq, dk, dv, ws, status, cs);
     } else if (e == cudaSuccess) {
-        e = launch_bwd_dkdv(s, q, k, v, dout, dk, dv, ws, status, cs);
+        e = launch_bwd_cross128(s, q, k, v, dout, dk, dv, ws, status, cs);
         if (e == cudaSuccess) e = launch_bwd_dq_convert(s, ws, dq, cs);
     }
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;

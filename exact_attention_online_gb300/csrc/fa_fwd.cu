@@ -51,8 +51,6 @@
 // moves by at most 2^-11 (sum over block maxima of w |v - O| + sum over the
 // other keys of w |v|) <= 2^-10 max|V|, w = p / l.
 #include <cuda_bf16.h>
-#include <algorithm>
-#include <cmath>
 #include <type_traits>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -113,12 +111,6 @@ struct FwdCfg {
     static constexpr uint32_t kColP0 = 384, kColP1 = 448;
 };
 
-// A place in the list of (item, key block) of a forward with keys of its own: block blk
-// of item it of sequence b.
-struct CrossAt {
-    int b, it, blk, pad;
-};
-
 struct FwdParams {
     int H, Hkv, N, BH, n_mblk, n_items, causal;
     // Causal sliding window W: query i sees keys i - W < j <= i.  Without a
@@ -129,19 +121,6 @@ struct FwdParams {
     // longest sequence.  Dense batches: rows = N, cu_seqlens unused.
     int rows;
     const int* cu_seqlens;
-    // Keys of their own (CROSS): at most Nk of them a sequence, krows rows a head of
-    // k and v.  Padded batches: kv_lens[b] of them, or Nk (null).  Packed ones: rows
-    // cu_k[b] .. cu_k[b+1] - 1.
-    int Nk, krows;
-    const int* kv_lens;
-    const int* cu_k;
-    // CROSS: may key blocks of one item go to several CTAs?  Then the segments' places
-    // in the workspace: [slot][d / 4][256 rows] quarter rows of O (normalised, fp32),
-    // [slot][256] LSEs (base 2), and where each CTA's part begins.
-    int split;
-    float4* part_o;
-    float* part_lse;
-    CrossAt* part_at;
     float scale_log2;                 // scale * log2(e)
     void* o;                          // bf16, or fp32 in the precise variant
     float* lse;
@@ -161,21 +140,9 @@ struct FwdTile {
     int bh, row_base;
     int q_z, kv_z;             // head coordinate of the Q / O and K / V tensor maps
     int tok0, len;             // first row of the sequence in its head, its length
-    int ktok0, klen;           // the same of its keys
-    int off;                   // query i sees keys j <= i + off under the causal mask
     int lo[kTiles];            // first key block each query tile needs
     int n_kv[kTiles];          // one past its last key block
 };
-struct CrossTile : FwdTile {
-    int slot;                  // of a segment of an item, else -1
-};
-
-// The keys of sequence b (CROSS): how many, and the first one's row in its head.
-__device__ __forceinline__ int key_rows(const FwdParams& p, int b, int& ktok0) {
-    if (p.cu_k) return packed_seq(p.cu_k, b, p.Nk, p.krows, ktok0);
-    ktok0 = 0;
-    return p.kv_lens ? min(max(__ldg(p.kv_lens + b), 0), p.Nk) : p.Nk;
-}
 
 __device__ __forceinline__ int fwd_m_blk(int item, const FwdParams& p, bool causal) {
     const int mb_rank = item / p.BH;
@@ -190,7 +157,7 @@ __device__ __forceinline__ int fwd_m_blk(int item, const FwdParams& p, bool caus
 // plain round robin).  With variable lengths the ranks count only the items
 // that have rows (query-block pairs past a sequence's end are passed over):
 // a cursor walks the (level, sequence) list forward, ranks only grow.
-template <bool VARLEN, bool CROSS>
+template <bool VARLEN>
 struct FwdSched {
     int round = 0;
     int mb = 0, b = 0, base = 0;   // cursor: level, sequence, rank of (b, head 0)
@@ -219,237 +186,6 @@ struct FwdSched {
     }
 };
 
-// Keys of another length (CROSS).  The work is a list of (item, key block): sequences in
-// turn, in each the K/V heads, in each the query-block pairs, in each the query heads that
-// share the K/V head, and the item's key blocks.  Each CTA takes an equal share of that
-// list, whole items or segments of them; an item in segments leaves one partial result
-// each in the workspace (a CTA has two at most: its first and its last item), which
-// cross_join_kernel adds up in the order of the keys.  The lengths are on the device, so
-// that each CTA finds its share itself.  Whole items in rounds leave the GPU idle in the
-// last one and are as long as the longest sequence allows: 2 x 32/8 heads, 1024 queries,
-// 17408 keys, d = 128, causal (256 items on 152 SMs): 437 us, in equal shares 390 to 410.
-// Segments pay for the join (a launch, 132 KB written and read each at d = 128): about
-// kJoinCost key blocks, so that cross_ctas() takes them only where an even share is that
-// much shorter; a segment has kMinBlocks blocks at least, and a share that would end
-// within 1/24 of itself of an item's end ends there.  8 heads, 64 queries, d = 128, whole
-// items against segments: 1024 keys 20.6 us / 17.8, 16384 keys 200 / 35; 4 x 32 heads, 256
-// queries (128 items): 2048 keys 40.0 / 48.8, which the rule leaves whole.
-constexpr int kSplitBlocks = 4;   // no segments up to here
-constexpr int kMinBlocks = 2;
-constexpr int kJoinCost = 8;
-constexpr int kItemCost = 3;      // what an item costs besides its key blocks, in those
-constexpr int kMaxCtas = 152;     // the workspace has places for that many
-
-// The items of sequence b, and the key blocks of each.
-struct CrossSeq {
-    int tok0, len, ktok0, klen;
-    int M, n;         // query-block pairs; key blocks
-    int q;            // causal: pair m sees 2 (m + 1) + q of them
-    bool causal;
-
-    __device__ __forceinline__ CrossSeq(const FwdParams& p, int b, bool causal_) {
-        if (p.cu_seqlens) {
-            len = packed_seq(p.cu_seqlens, b, p.N, p.rows, tok0);
-        } else {
-            tok0 = 0;
-            len = p.N;
-        }
-        klen = key_rows(p, b, ktok0);
-        causal = causal_;
-        M = (len + kTiles * kBM - 1) / (kTiles * kBM);
-        n = max(1, (klen + kBN - 1) / kBN);
-        q = (klen - len + kBN - 1) >> 7;   // rounds down for negative ones too
-    }
-    __device__ __forceinline__ int blocks(int m) const {
-        return causal ? min(max(2 * (m + 1) + q, 1), n) : n;
-    }
-    // Cost of pairs 0 .. m - 1, key blocks and kItemCost each: pairs below m1 have one
-    // block, those from m2 on all n.
-    __device__ __forceinline__ long long before(int m) const {
-        if (!causal) return (long long)m * (n + kItemCost);
-        const int m1 = min(max((1 - q) >> 1, 0), m);
-        const int m2 = min(max((n - q) >> 1, m1), m);
-        const long long mid = m2 - m1;
-        return m1 + mid * (m1 + m2 + 1 + q) + (long long)(m - m2) * n + (long long)m * kItemCost;
-    }
-};
-static_assert(kBN == 128 && kBM == 128 && kTiles == 2, "CrossSeq counts in these");
-
-// First block of CTA c's share: block t of the list, which lies in sequence b at o.
-__device__ __forceinline__ CrossAt cross_place(const FwdParams& p, const CrossSeq& sq, int b,
-                                               long long o, bool unit, int snap) {
-    const int G = p.H / p.Hkv;
-    CrossAt at;
-    at.b = b;
-    if (unit) {   // every item counts as one
-        at.it = (int)o;
-        at.blk = 0;
-        return at;
-    }
-    const long long head = G * sq.before(sq.M);
-    const int g = o >> 31 ? (int)(o / head) : (int)((uint32_t)o / (uint32_t)min(head, 0x7fffffffll));
-    o -= g * head;
-    int m = 0;                          // the last pair with G before(m) <= o
-    for (int hi = sq.M; hi - m > 1;) {
-        const int mid = (m + hi) >> 1;
-        if (G * sq.before(mid) <= o) m = mid;
-        else hi = mid;
-    }
-    o -= G * sq.before(m);
-    const int n = sq.blocks(m), cost = n + kItemCost, r = (int)o / cost;
-    at.it = (g * sq.M + m) * G + r;
-    at.blk = max((int)o - r * cost - kItemCost, 0);
-    if (at.blk <= snap && (p.split || 2 * at.blk < n)) {
-        at.blk = 0;
-    } else if (n - at.blk <= snap) {
-        at.blk = 0;
-        if (++at.it == p.H * sq.M) {
-            ++at.b;
-            at.it = 0;
-        }
-    }
-    return at;
-}
-
-// The block's share [at[0], at[1]): every thread counts the blocks of a run of sequences.
-__device__ __forceinline__ void cross_share(const FwdParams& p, bool causal, CrossAt* at,
-                                            long long* warp_sum) {
-    const int B = p.BH / p.H;
-    const int run = (B + kThreads - 1) / kThreads;
-    const int b0 = min(B, (int)threadIdx.x * run), b1 = min(B, b0 + run);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const bool unit = !p.split && p.n_items <= (int)gridDim.x;
-    auto count = [&](const CrossSeq& sq) -> long long {
-        return p.H * (unit ? (long long)sq.M : sq.before(sq.M));
-    };
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += count(CrossSeq(p, b, causal));
-    long long upto = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-        const long long o = __shfl_up_sync(0xffffffffu, upto, d);
-        if (lane >= d) upto += o;
-    }
-    if (lane == 31) warp_sum[warp] = upto;
-    __syncthreads();
-    long long total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
-        if (w == warp) upto += total;
-        total += warp_sum[w];
-    }
-    const long long per = max((total + gridDim.x - 1) / gridDim.x,
-                              (long long)(p.split ? kMinBlocks : 1));
-    // whole items: the nearest item's end
-    const int snap = p.split ? (int)max(1ll, min(per / 24, 1ll << 20)) : 1 << 30;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const long long t = ((long long)blockIdx.x + e) * per;
-        if (t >= total) {
-            if (threadIdx.x == 0) at[e] = CrossAt{B, 0, 0, 0};
-        } else if (t >= upto - mine && t < upto) {
-            long long o = t - (upto - mine);
-            for (int b = b0; b < b1; ++b) {
-                const CrossSeq sq(p, b, causal);
-                const long long n = count(sq);
-                if (o < n) {
-                    at[e] = cross_place(p, sq, b, o, unit, snap);
-                    break;
-                }
-                o -= n;
-            }
-        }
-    }
-}
-
-// The CTA's items and segments.  The K producer, which is ahead of every other role, finds
-// them and leaves them in a ring in shared memory (struct CrossRing): found by each role
-// by itself, with divisions and loads in one thread, an item cost 2 to 4 us more than one
-// of a dense batch (d = 64 to 128).
-struct CrossWalk {
-    const CrossAt* at;   // shared memory: the share's first place and its end
-    int b, it, blk;      // the item, and the first block of it
-    bool begun = false;
-
-    __device__ __forceinline__ explicit CrossWalk(const CrossAt* a)
-        : at(a), b(a[0].b), it(a[0].it), blk(a[0].blk) {}
-
-    __device__ __forceinline__ bool next(const FwdParams& p, bool causal) {
-        if (begun) {
-            ++it;
-            blk = 0;
-        }
-        begun = true;
-        for (;;) {
-            if (b > at[1].b || (b == at[1].b && it > at[1].it)) return false;
-            if (b == at[1].b && it == at[1].it) return at[1].blk > blk;
-            if (it < p.H * CrossSeq(p, b, causal).M) return true;
-            ++b;
-            it = 0;
-        }
-    }
-};
-
-__device__ __forceinline__ CrossTile cross_tile(const CrossWalk& sch, const FwdParams& p,
-                                                bool causal) {
-    const CrossSeq sq(p, sch.b, causal);
-    const int G = p.H / p.Hkv;
-    const int m = sch.it / G % sq.M, kv = sch.it / G / sq.M, h = kv * G + sch.it % G;
-    CrossTile w;
-    w.bh = sch.b * p.H + h;
-    w.tok0 = sq.tok0;
-    w.len = sq.len;
-    w.ktok0 = sq.ktok0;
-    w.klen = sq.klen;
-    w.off = sq.klen - sq.len;
-    w.q_z = p.cu_seqlens ? h : w.bh;
-    w.kv_z = p.cu_seqlens ? kv : sch.b * p.Hkv + kv;
-    w.row_base = m * (kTiles * kBM);
-    const int n = sq.blocks(m);
-    const int lo = sch.blk;
-    const int hi = sch.b == sch.at[1].b && sch.it == sch.at[1].it ? sch.at[1].blk : n;
-    // The first tile's last row sees keys up to its own index + off.  A tile that sees
-    // nothing of the segment keeps one block, which the masks empty.
-    const int n0 = causal ? min(n, max(2 * m + 1 + sq.q, 1)) : n;
-    w.lo[0] = w.lo[1] = lo;
-    w.n_kv[0] = max(lo + 1, min(n0, hi));
-    w.n_kv[1] = hi;
-    // (its first item may lack a beginning, its last one an end)
-    w.slot = lo > 0 ? 2 * (int)blockIdx.x : hi < n ? 2 * (int)blockIdx.x + 1 : -1;
-    return w;
-}
-
-constexpr int kRing = 4;
-constexpr int kRingReaders = 3 + 8;   // V producer, the two issuers, the softmax warps
-
-struct CrossRing {
-    CrossTile tile[kRing];   // n_kv[1] == 0: no more
-    uint64_t full[kRing], empty[kRing];
-};
-
-// A reader's way through the ring, by one thread or (warp) a whole warp.
-template <bool VARLEN>
-struct FwdSched<VARLEN, true> {
-    CrossRing* ring;
-    WaitCtx wc;
-    bool warp;
-    uint32_t i = 0;
-    bool ok = true;
-
-    __device__ __forceinline__ const CrossTile& tile() const { return ring->tile[(i - 1) % kRing]; }
-    // An index below p.n_items (0) while there is one more: tile() is it until the next call.
-    __device__ __forceinline__ int next(const FwdParams& p, bool) {
-        if (i > 0) {
-            if (warp) __syncwarp();
-            if (!warp || (threadIdx.x & 31) == 0) mbar_arrive(&ring->empty[(i - 1) % kRing]);
-        }
-        uint64_t* full = &ring->full[i % kRing];
-        const uint32_t par = (i / kRing) & 1;
-        ok = warp ? fa_wait_warp(full, par, 40, wc) : fa_wait(full, par, 40, wc);
-        ++i;
-        return ok && tile().n_kv[kTiles - 1] > 0 ? 0 : p.n_items;
-    }
-};
-
 template <bool WINDOW, bool VARLEN>
 __device__ __forceinline__ FwdTile fwd_tile(int item, const FwdParams& p, bool causal) {
     FwdTile w;
@@ -466,11 +202,8 @@ __device__ __forceinline__ FwdTile fwd_tile(int item, const FwdParams& p, bool c
         w.q_z = w.bh;
         w.kv_z = b * p.Hkv + h / (p.H / p.Hkv);
     }
-    w.ktok0 = w.tok0;
-    w.klen = w.len;
-    w.off = 0;
     w.row_base = m_blk * (kTiles * kBM);
-    const int n_kv_all = (w.klen + kBN - 1) / kBN;
+    const int n_kv_all = (w.len + kBN - 1) / kBN;
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
         w.n_kv[t] = causal ? min(n_kv_all, 2 * m_blk + t + 1) : n_kv_all;
@@ -511,11 +244,7 @@ __device__ __forceinline__ bool convert_v_half(uint8_t* sV, uint64_t* bar_v, uin
     return true;
 }
 
-// CROSS: queries against keys of another length (p.Nk, p.kv_lens, p.cu_k), padded or
-// packed (p.cu_seqlens), the causal mask by p.causal and counted from the last key.
-// Rows past a sequence's keys may hold anything: their scores are masked, and the
-// softmax of query tile 0 (of tile 1 where only that sees the block) clears V's rows.
-template <int D, bool CAUSAL, bool PRECISE, bool WINDOW, bool VARLEN, bool CROSS>
+template <int D, bool CAUSAL, bool PRECISE, bool WINDOW, bool VARLEN>
 __global__ void __launch_bounds__(kThreads, 1)
 fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
               const __grid_constant__ CUtensorMap tm_v, const FwdParams p) {
@@ -536,21 +265,6 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     __shared__ int abort_sh;
     const WaitCtx wc{p.status, &abort_sh};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const bool causal = CAUSAL || (CROSS && p.causal);
-    __shared__ CrossAt share[2];
-    __shared__ CrossRing ring;
-    auto sched = [&](bool whole_warp) {
-        if constexpr (CROSS) return FwdSched<VARLEN, CROSS>{&ring, wc, whole_warp};
-        else return FwdSched<VARLEN, CROSS>();
-    };
-    auto tile = [&](int item, const FwdSched<VARLEN, CROSS>& sch) {
-        if constexpr (CROSS) return static_cast<FwdTile>(sch.tile());
-        else return fwd_tile<WINDOW, VARLEN>(item, p, causal);
-    };
-    if constexpr (CROSS) {
-        __shared__ long long warp_sum[kThreads / 32];
-        cross_share(p, causal, share, warp_sum);
-    }
 
     if (threadIdx.x == 0) {
         abort_sh = 0;
@@ -572,11 +286,6 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             mbar_init(&bar_s_free[t], 128);
             mbar_init(&bar_pv[t], 1);
         }
-        if constexpr (CROSS)
-            for (int r = 0; r < kRing; ++r) {
-                mbar_init(&ring.full[r], 1);
-                mbar_init(&ring.empty[r], kRingReaders);
-            }
         fence_mbar_init();
     }
     if (warp == kMmaWarp) {
@@ -607,13 +316,12 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         const float c = p.scale_log2;
         uint32_t cs = 0;                         // S_t completions seen so far
         uint32_t cpv = 0;                        // P_t V completions seen (separate P)
-        uint32_t gv = 0;                         // V blocks of the items before (CROSS)
         bool ok = true;
         int lt = 0;
-        FwdSched<VARLEN, CROSS> sch = sched(true);
-        for (int item = sch.next(p, causal); ok && item < p.n_items;
-             item = sch.next(p, causal), ++lt) {
-            const FwdTile wt = tile(item, sch);
+        FwdSched<VARLEN> sch;
+        for (int item = sch.next(p, CAUSAL); ok && item < p.n_items;
+             item = sch.next(p, CAUSAL), ++lt) {
+            const FwdTile wt = fwd_tile<WINDOW, VARLEN>(item, p, CAUSAL);
             const int row0 = wt.row_base + t * kBM;
             const int row = row0 + rl;
             // (selects, not a run-time index: the arrays stay in registers)
@@ -627,22 +335,6 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             // LSE keeps l.
             float lc = 0.0f;
             for (int j = lo; j < n_kv; ++j) {
-                if (CROSS && (j + 1) * kBN > wt.klen && (t == 0 || j >= wt.n_kv[0])) {
-                    // V_j's rows past the keys: a weight of zero would not silence a
-                    // NaN.  Before the scores are waited for (the loads of V_j wait for
-                    // none of this tile's MMAs to come), and by the stage's order no
-                    // other use of the stage comes before this tile's P V.
-                    const uint32_t gj = gv + (uint32_t)(j - lo), vs = gj % SV;
-                    if (!fa_wait_warp(&bar_v[vs], (gj / SV) & 1, 38 + t, wc)) { ok = false; break; }
-                    if (j * kBN + rl >= wt.klen) {
-                        const uint32_t vrow = smem_u32(sV) + vs * Cfg::kTileBytes + rl * 128;
-#pragma unroll
-                        for (int u = 0; u < Cfg::kChunks * 8; ++u)   // (eight lanes, eight banks)
-                            sts_v4(vrow + (u >> 3) * Cfg::kChunkBytes + ((u ^ rl) & 7) * 16,
-                                   make_uint4(0u, 0u, 0u, 0u));
-                    }
-                    fence_proxy_async_smem();
-                }
                 if (!fa_wait_warp(&bar_s[t], cs & 1, 30 + t, wc)) { ok = false; break; }
                 ++cs;
                 tc_fence_after();
@@ -664,23 +356,16 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 for (int e = 0; e < kBN; ++e) sv[e] = __uint_as_float(r[e >> 5][e & 31]);
 
                 const int col0 = j * kBN;
-                const bool need_mask = (causal && (col0 + kBN - 1 > row0 + wt.off ||
+                const bool need_mask = (CAUSAL && (col0 + kBN - 1 > row0 ||
                                                    (WINDOW && col0 < row0 + kBM - p.window))) ||
-                                       (col0 + kBN > wt.klen);
+                                       (col0 + kBN > wt.len);
                 if (need_mask) {
-                    const int lim_causal = causal ? row + wt.off - col0 : kBN;   // keep e <= this
-                    const int lim_n = wt.klen - col0;                    // keep e < N - col0
-                    if (CROSS) {
-                        const int lim = min(lim_causal, lim_n - 1);
+                    const int lim_causal = CAUSAL ? row - col0 : kBN;   // keep e <= row - col0
+                    const int lim_n = wt.len - col0;                     // keep e < N - col0
+                    const int lim_lo = WINDOW ? row - p.window + 1 - col0 : 0;  // keep e >= this
 #pragma unroll
-                        for (int e = 0; e < kBN; ++e)
-                            if (e > lim) sv[e] = -CUDART_INF_F;
-                    } else {
-                        const int lim_lo = WINDOW ? row - p.window + 1 - col0 : 0;  // keep e >= this
-#pragma unroll
-                        for (int e = 0; e < kBN; ++e)
-                            if (e > lim_causal || e >= lim_n || e < lim_lo) sv[e] = -CUDART_INF_F;
-                    }
+                    for (int e = 0; e < kBN; ++e)
+                        if (e > lim_causal || e >= lim_n || e < lim_lo) sv[e] = -CUDART_INF_F;
                 }
                 // Row max: three-input max, eight independent chains.
                 float mx8[8];
@@ -773,7 +458,6 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 mbar_arrive(&bar_p[t]);
             }
             if (!ok) break;
-            if (CROSS) gv += wt.n_kv[kTiles - 1] - lo;
 
             // ------------------------------------------------------- epilogue
             // O row -> registers, release the O columns to the next item's
@@ -794,44 +478,10 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             for (int c0 = 1; c0 < D / 32; ++c0) asm volatile("" : FA_R32(ov[c0]) : : "memory");
             tc_fence_before();
             mbar_arrive(&bar_o_free[t]);
-            // CROSS: where the rows go is read again, not held in registers through the
-            // loop over the keys.
-            FwdTile out = wt;
-            int seg = -1;   // the segment's slot
-            if constexpr (CROSS) {
-                asm volatile("" ::: "memory");
-                out = sch.tile();
-                seg = sch.tile().slot;
-            }
-            const bool valid = row < out.len;
-            // a row that sees no key (the exponentials of the FMA pipe are not quite 0);
-            // scores of NaN, which the maximum passes over, leave l NaN
-            if (CROSS && m2 == -CUDART_INF_F && l == l) {
-                l = 0.0f;
-#pragma unroll
-                for (int c0 = 0; c0 < D / 32; ++c0)
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) ov[c0][e] = 0u;
-            }
+            const bool valid = row < wt.len;
             const float l_o = PRECISE ? l + lc : l;
             const float inv_l = (l_o > 0.0f) ? 1.0f / l_o : 0.0f;
-            if (seg >= 0) {   // a segment: the join makes the rows of it
-                if (valid) {
-                    const int r = t * kBM + rl;
-                    float4* dst = p.part_o + (size_t)seg * (D / 4) * (kTiles * kBM) + r;
-#pragma unroll
-                    for (int c0 = 0; c0 < D / 4; ++c0)
-                        dst[c0 * (kTiles * kBM)] =
-                            make_float4(__uint_as_float(ov[c0 / 8][c0 % 8 * 4 + 0]) * inv_l,
-                                        __uint_as_float(ov[c0 / 8][c0 % 8 * 4 + 1]) * inv_l,
-                                        __uint_as_float(ov[c0 / 8][c0 % 8 * 4 + 2]) * inv_l,
-                                        __uint_as_float(ov[c0 / 8][c0 % 8 * 4 + 3]) * inv_l);
-                    p.part_lse[(size_t)seg * (kTiles * kBM) + r] =
-                        l == 0.0f ? -CUDART_INF_F : m2 + log2f(l);
-                }
-                continue;
-            }
-            const size_t orow = ((size_t)out.q_z * p.rows + out.tok0 + (valid ? row : 0)) * D;
+            const size_t orow = ((size_t)wt.q_z * p.rows + wt.tok0 + (valid ? row : 0)) * D;
             if (valid) {
 #pragma unroll
                 for (int c0 = 0; c0 < D / 32; ++c0) {
@@ -862,8 +512,8 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                         }
                     }
                 }
-                p.lse[(size_t)out.q_z * p.rows + out.tok0 + row] =
-                    (CROSS ? l != 0.0f : l > 0.0f) ? (m2 + log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
+                p.lse[(size_t)wt.q_z * p.rows + wt.tok0 + row] =
+                    (l > 0.0f) ? (m2 + log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
             }
             if (p.lse_ext != nullptr && row0 < p.Np) {
                 // Training forward: this tile's rows of the backward workspace
@@ -890,55 +540,20 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             tma_prefetch_desc(&tm_k);
             uint32_t g = 0;              // K blocks loaded so far (ring position)
             bool ok = true;
-            if constexpr (CROSS) {
-                // The next item goes into the ring once this one's first block is on its way.
-                CrossWalk walk(share);
-                uint32_t n = 0;   // items put into the ring
-                CrossTile nxt;
-                auto put = [&] {
-                    const uint32_t r = n % kRing;
-                    if (n >= (uint32_t)kRing && !fa_wait(&ring.empty[r], (n / kRing - 1) & 1, 41, wc))
-                        return false;
-                    nxt.n_kv[kTiles - 1] = 0;
-                    if (walk.next(p, causal)) nxt = cross_tile(walk, p, causal);
-                    ring.tile[r] = nxt;
-                    mbar_arrive(&ring.full[r]);
-                    ++n;
-                    return true;
-                };
-                ok = put();
-                while (ok && nxt.n_kv[kTiles - 1] > 0) {
-                    const CrossTile wt = nxt;
-                    for (int j = wt.lo[0]; j < wt.n_kv[kTiles - 1]; ++j, ++g) {
-                        const int s = g % SK;
-                        if (g >= (uint32_t)SK &&
-                            !fa_wait(&bar_k_empty[s], ((g / SK) - 1) & 1, 10, wc)) {
-                            ok = false;
-                            break;
-                        }
-                        mbar_arrive_expect_tx(&bar_k[s], Cfg::kTileBytes);
-                        for (int c = 0; c < Cfg::kChunks; ++c)
-                            tma_load_3d(sK + s * Cfg::kTileBytes + c * Cfg::kChunkBytes, &tm_k,
-                                        &bar_k[s], c * 64, wt.ktok0 + j * kBN, wt.kv_z);
-                        if (j == wt.lo[0]) ok = put();
+            FwdSched<VARLEN> sch;
+            for (int item = sch.next(p, CAUSAL); ok && item < p.n_items;
+                 item = sch.next(p, CAUSAL)) {
+                const FwdTile wt = fwd_tile<WINDOW, VARLEN>(item, p, CAUSAL);
+                for (int j = wt.lo[0]; j < wt.n_kv[kTiles - 1]; ++j, ++g) {
+                    const int s = g % SK;
+                    if (g >= (uint32_t)SK && !fa_wait(&bar_k_empty[s], ((g / SK) - 1) & 1, 10, wc)) {
+                        ok = false;
+                        break;
                     }
-                }
-            } else {
-                FwdSched<VARLEN, CROSS> sch = sched(false);
-                for (int item = sch.next(p, causal); ok && item < p.n_items;
-                     item = sch.next(p, causal)) {
-                    const FwdTile wt = tile(item, sch);
-                    for (int j = wt.lo[0]; j < wt.n_kv[kTiles - 1]; ++j, ++g) {
-                        const int s = g % SK;
-                        if (g >= (uint32_t)SK && !fa_wait(&bar_k_empty[s], ((g / SK) - 1) & 1, 10, wc)) {
-                            ok = false;
-                            break;
-                        }
-                        mbar_arrive_expect_tx(&bar_k[s], Cfg::kTileBytes);
-                        for (int c = 0; c < Cfg::kChunks; ++c)
-                            tma_load_3d(sK + s * Cfg::kTileBytes + c * Cfg::kChunkBytes, &tm_k, &bar_k[s],
-                                        c * 64, wt.ktok0 + j * kBN, wt.kv_z);
-                    }
+                    mbar_arrive_expect_tx(&bar_k[s], Cfg::kTileBytes);
+                    for (int c = 0; c < Cfg::kChunks; ++c)
+                        tma_load_3d(sK + s * Cfg::kTileBytes + c * Cfg::kChunkBytes, &tm_k, &bar_k[s],
+                                    c * 64, wt.tok0 + j * kBN, wt.kv_z);
                 }
             }
             if (abort_sh) {   // drain the copies still in flight (bounded)
@@ -955,10 +570,10 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             uint32_t g = 0;
             int lt = 0, q_loaded = -1;
             bool ok = true;
-            FwdSched<VARLEN, CROSS> sch = sched(false);
-            for (int item = sch.next(p, causal); ok && item < p.n_items;
-                 item = sch.next(p, causal), ++lt) {
-                const FwdTile wt = tile(item, sch);
+            FwdSched<VARLEN> sch;
+            for (int item = sch.next(p, CAUSAL); ok && item < p.n_items;
+                 item = sch.next(p, CAUSAL), ++lt) {
+                const FwdTile wt = fwd_tile<WINDOW, VARLEN>(item, p, CAUSAL);
                 for (int t = 0; t < kTiles; ++t) {
                     if (lt > 0 && !fa_wait(&bar_q_free[t], (lt - 1) & 1, 12, wc)) { ok = false; break; }
                     mbar_arrive_expect_tx(&bar_q[t], Cfg::kTileBytes);
@@ -977,7 +592,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                     mbar_arrive_expect_tx(&bar_v[s], Cfg::kTileBytes);
                     for (int c = 0; c < Cfg::kChunks; ++c)
                         tma_load_3d(sV + s * Cfg::kTileBytes + c * Cfg::kChunkBytes, &tm_v, &bar_v[s],
-                                    c * 64, wt.ktok0 + j * kBN, wt.kv_z);
+                                    c * 64, wt.tok0 + j * kBN, wt.kv_z);
                 }
             }
             if (abort_sh) {   // drain the copies still in flight (bounded)
@@ -1002,10 +617,10 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             if (leader) tma_prefetch_desc(&tm_k);
             uint32_t g = 0, gc = 0;      // K blocks loaded (ring position); V halves converted
             bool ok = true;
-            FwdSched<VARLEN, CROSS> sch = sched(false);
-            for (int item = sch.next(p, causal); ok && item < p.n_items;
-                 item = sch.next(p, causal)) {
-                const FwdTile wt = tile(item, sch);
+            FwdSched<VARLEN> sch;
+            for (int item = sch.next(p, CAUSAL); ok && item < p.n_items;
+                 item = sch.next(p, CAUSAL)) {
+                const FwdTile wt = fwd_tile<WINDOW, VARLEN>(item, p, CAUSAL);
                 for (int j = wt.lo[0]; j < wt.n_kv[kTiles - 1]; ++j, ++g) {
                     if (PRECISE && gc + 2 <= g) {
                         if (!convert_v_half<SV, Cfg::kTileBytes>(sV, bar_v, bar_v_cvt, gc, 1, lane, wc)) {
@@ -1053,10 +668,10 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             uint32_t g = 0;   // V blocks issued (and their first halves converted)
             int lt = 0, q_loaded = -1;
             bool ok = true;
-            FwdSched<VARLEN, CROSS> sch = sched(false);
-            for (int item = sch.next(p, causal); ok && item < p.n_items;
-                 item = sch.next(p, causal), ++lt) {
-                const FwdTile wt = tile(item, sch);
+            FwdSched<VARLEN> sch;
+            for (int item = sch.next(p, CAUSAL); ok && item < p.n_items;
+                 item = sch.next(p, CAUSAL), ++lt) {
+                const FwdTile wt = fwd_tile<WINDOW, VARLEN>(item, p, CAUSAL);
                 const int jb = wt.lo[0], je = wt.n_kv[kTiles - 1];
                 auto issue_v = [&](int j) -> bool {   // V_j into the ring
                     const int s = g % SV;
@@ -1129,10 +744,10 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 mma_commit(&bar_pv[T]);
                 return true;
             };
-            FwdSched<VARLEN, CROSS> sch = sched(false);
-            for (int item = sch.next(p, causal); ok && item < p.n_items;
-                 item = sch.next(p, causal), ++lt) {
-                const FwdTile wt = tile(item, sch);
+            FwdSched<VARLEN> sch;
+            for (int item = sch.next(p, CAUSAL); ok && item < p.n_items;
+                 item = sch.next(p, CAUSAL), ++lt) {
+                const FwdTile wt = fwd_tile<WINDOW, VARLEN>(item, p, CAUSAL);
                 // Key blocks [lo0, n0) for tile 0, [lo1, n1) for tile 1, with
                 // lo0 <= lo1 and n0 <= n1; V_j streams for j in [lo0, n1).
                 const int lo0 = wt.lo[0], lo1 = wt.lo[1], n0 = wt.n_kv[0], n1 = wt.n_kv[1];
@@ -1157,7 +772,6 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 }
                 g += n1 - lo0;
             }
-            if constexpr (CROSS) ok = ok && sch.ok;
             if (!ok) {   // no MMA of this thread may still write TMEM at teardown
                 __shared__ uint64_t bar_drain_pv;
                 mbar_init(&bar_drain_pv, 1);
@@ -1195,10 +809,10 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 mma_commit(&bar_s[T]);
                 return true;
             };
-            FwdSched<VARLEN, CROSS> sch = sched(false);
-            for (int item = sch.next(p, causal); ok && item < p.n_items;
-                 item = sch.next(p, causal), ++lt) {
-                const FwdTile wt = tile(item, sch);
+            FwdSched<VARLEN> sch;
+            for (int item = sch.next(p, CAUSAL); ok && item < p.n_items;
+                 item = sch.next(p, CAUSAL), ++lt) {
+                const FwdTile wt = fwd_tile<WINDOW, VARLEN>(item, p, CAUSAL);
                 const int lo0 = wt.lo[0], lo1 = wt.lo[1], n0 = wt.n_kv[0], n1 = wt.n_kv[1];
                 if (!fa_wait(&bar_q[0], lt & 1, 20, wc) || !fa_wait(&bar_q[1], lt & 1, 20, wc)) {
                     ok = false;
@@ -1219,7 +833,6 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 }
                 g += n1 - lo0;
             }
-            if constexpr (CROSS) ok = ok && sch.ok;
             if (!ok) {
                 __shared__ uint64_t bar_drain;
                 mbar_init(&bar_drain, 1);
@@ -1231,7 +844,6 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         __syncwarp();
     }
 
-    if (CROSS && threadIdx.x == 0 && p.split) p.part_at[blockIdx.x] = share[0];
     tc_fence_before();
     __syncthreads();
     if (warp == kMmaWarp) {
@@ -1240,70 +852,11 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     }
 }
 
-// The items that went to several CTAs: O = sum over the segments of 2^(L_s - L) O_s with
-// L = log2 sum 2^L_s, L_s the segment's LSE.  Block (c, y) has the item in whose middle
-// CTA c's share begins, if c is the first such, and 16 columns of O; one row a thread.
-// Bound by the reads of the segments (from L2: they were just written).
-template <int D>
-__global__ void __launch_bounds__(kTiles * kBM)
-cross_join_kernel(const FwdParams p, int ctas) {
-    pdl_wait();
-    const int c = blockIdx.x + 1, r = threadIdx.x;
-    const CrossAt at = p.part_at[c], prev = p.part_at[c - 1];
-    if (at.blk == 0 || (prev.b == at.b && prev.it == at.it && prev.blk > 0)) return;
-    const CrossSeq sq(p, at.b, p.causal);
-    const int G = p.H / p.Hkv;
-    const int h = at.it / G / sq.M * G + at.it % G;
-    const int row = at.it / G % sq.M * (kTiles * kBM) + r;
-    if (row >= sq.len) return;
-    int last = c;
-    while (last + 1 < ctas) {
-        const CrossAt a = p.part_at[last + 1];
-        if (a.b != at.b || a.it != at.it || a.blk == 0) break;
-        ++last;
-    }
-    auto slot = [&](int x) { return (size_t)(2 * x + (x < c ? 1 : 0)); };
-    float top = -CUDART_INF_F;
-    for (int x = c - 1; x <= last; ++x) top = fmaxf(top, p.part_lse[slot(x) * (kTiles * kBM) + r]);
-    const float m = top == -CUDART_INF_F ? 0.0f : top;
-    float sum = 0.0f, acc[16] = {};
-#pragma unroll 2
-    for (int x = c - 1; x <= last; ++x) {
-        const float w = ex2(p.part_lse[slot(x) * (kTiles * kBM) + r] - m);
-        const float4* src =
-            p.part_o + (slot(x) * (D / 4) + blockIdx.y * 4) * (kTiles * kBM) + r;
-        sum += w;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const float4 v = src[u * (kTiles * kBM)];
-            acc[4 * u + 0] = fmaf(w, v.x, acc[4 * u + 0]);
-            acc[4 * u + 1] = fmaf(w, v.y, acc[4 * u + 1]);
-            acc[4 * u + 2] = fmaf(w, v.z, acc[4 * u + 2]);
-            acc[4 * u + 3] = fmaf(w, v.w, acc[4 * u + 3]);
-        }
-    }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const size_t z = p.cu_seqlens ? (size_t)h : (size_t)at.b * p.H + h;
-    const size_t orow = z * p.rows + sq.tok0 + row;
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + orow * D +
-                                          blockIdx.y * 16);
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-        dst[u] = make_uint4(pack_bf16x2(acc[8 * u + 0] * inv, acc[8 * u + 1] * inv),
-                            pack_bf16x2(acc[8 * u + 2] * inv, acc[8 * u + 3] * inv),
-                            pack_bf16x2(acc[8 * u + 4] * inv, acc[8 * u + 5] * inv),
-                            pack_bf16x2(acc[8 * u + 6] * inv, acc[8 * u + 7] * inv));
-    if (blockIdx.y == 0)
-        p.lse[orow] =
-            sum == 0.0f ? -CUDART_INF_F : (m + log2f(sum)) * 0.69314718055994531f;
-}
-
-template <int D, bool CAUSAL, bool PRECISE, bool WINDOW = false, bool VARLEN = false,
-          bool CROSS = false>
+template <int D, bool CAUSAL, bool PRECISE, bool WINDOW = false, bool VARLEN = false>
 cudaError_t launch_fwd_t(const Shape& s, const CUtensorMap& tq, const CUtensorMap& tk,
                          const CUtensorMap& tv, const FwdParams& p, int grid,
                          cudaStream_t stream) {
-    auto kern = fa_fwd_kernel<D, CAUSAL, PRECISE, WINDOW, VARLEN, CROSS>;
+    auto kern = fa_fwd_kernel<D, CAUSAL, PRECISE, WINDOW, VARLEN>;
     static int configured_device = -1;   // attribute is per device; cheap to repeat
     int dev = 0;
     cudaGetDevice(&dev);
@@ -1325,75 +878,19 @@ cudaError_t launch_fwd_t(const Shape& s, const CUtensorMap& tq, const CUtensorMa
 
 }  // namespace
 
-// Keys of another length: the most CTAs that a split call has.
-static long long split_ctas(const Shape& s) {
-    const long long items = (long long)s.B * s.H * ((s.N + kTiles * kBM - 1) / (kTiles * kBM));
-    const long long n = (s.Nk + kBN - 1) / kBN;
-    return n <= kSplitBlocks ? 0 : std::min<long long>(kMaxCtas, (items * n + kMinBlocks - 1) / kMinBlocks);
-}
-
-size_t cross_fwd_workspace_bytes(const Shape& s) {
-    return std::max<size_t>(
-        256, split_ctas(s) * (2 * (kTiles * kBM) * (s.d + 1) * sizeof(float) + sizeof(CrossAt)));
-}
-
-// CTAs, and are there segments?  Only where an even share and the join are shorter than
-// the rounds of whole items; from what the host knows, the sizes (padded sequences
-// counted in full, packed ones as equally long).
-static int cross_ctas(const Shape& s, bool& split) {
-    const int sms = std::min(device_sm_count() > 0 ? device_sm_count() : 148, kMaxCtas);
-    const long long rows = s.cu_seqlens ? s.total / s.B : s.N;
-    const long long keys = s.cu_k ? std::min(s.total_k / s.B, s.Nk) : s.Nk;
-    const long long M = std::max(1ll, (rows + kTiles * kBM - 1) / (kTiles * kBM));
-    const long long n = (keys + kBN - 1) / kBN, q = (s.Nk - s.N) / kBN;
-    double blocks = 0.0;   // of the pairs of one head
-    for (long long m = 0; m < M; ++m)
-        blocks += kItemCost + (s.causal ? std::min(std::max(2 * (m + 1) + q, 1ll), n) : n);
-    const double items = (double)s.B * s.H * M, share = (double)s.B * s.H * blocks / sms;
-    const double longest = (s.Nk + kBN - 1) / kBN + kItemCost;
-    const double whole = std::max(longest, std::ceil(items / sms) * blocks / M);
-    split = split_ctas(s) > 0 && std::max(share, (double)kMinBlocks) + kJoinCost < whole;
-    const long long most = (long long)s.B * s.H * ((s.N + kTiles * kBM - 1) / (kTiles * kBM));
-    return (int)std::min<long long>(sms, split ? split_ctas(s) : most);
-}
-
-static cudaError_t launch_fwd_cross(const Shape& s, const CUtensorMap& tq, const CUtensorMap& tk,
-                                    const CUtensorMap& tv, FwdParams p, void* workspace,
-                                    cudaStream_t stream) {
-    bool split;
-    const int ctas = cross_ctas(s, split);
-    p.split = split;
-    p.part_o = static_cast<float4*>(workspace);
-    p.part_lse = static_cast<float*>(workspace) + (size_t)2 * ctas * (kTiles * kBM) * s.d;
-    p.part_at = reinterpret_cast<CrossAt*>(p.part_lse + (size_t)2 * ctas * (kTiles * kBM));
-    cudaError_t e =
-        s.d == 128
-            ? launch_fwd_t<128, false, false, false, false, true>(s, tq, tk, tv, p, ctas, stream)
-            : launch_fwd_t<64, false, false, false, false, true>(s, tq, tk, tv, p, ctas, stream);
-    if (e != cudaSuccess || !split || ctas < 2) return e;
-    const dim3 grid(ctas - 1, s.d / 16);
-    return s.d == 128 ? launch_pdl(cross_join_kernel<128>, grid, kTiles * kBM, 0, 1, stream, p, ctas)
-                      : launch_pdl(cross_join_kernel<64>, grid, kTiles * kBM, 0, 1, stream, p, ctas);
-}
-
 cudaError_t launch_fwd(const Shape& s, const void* q, const void* k, const void* v, void* o,
                        float* lse, bool precise, DeviceStatus* status, cudaStream_t stream,
-                       const BwdWorkspace* train_ws, void* cross_ws) {
+                       const BwdWorkspace* train_ws) {
     // Dense: maps {d, N, B*H(kv)}.  Packed variable lengths: {d, total, H(kv)},
     // a sequence's rows addressed from its first row.
-    const bool varlen = s.cu_seqlens != nullptr, cross = s.Nk > 0;
+    const bool varlen = s.cu_seqlens != nullptr;
     const int rows = varlen ? s.total : s.N;
-    const int krows = !cross ? rows : varlen ? s.total_k : s.Nk;
     CUtensorMap tq, tk, tv;
     if (!make_tmap_bf16_3d(&tq, q, s.d, rows, varlen ? s.H : s.B * s.H, kBM) ||
-        !make_tmap_bf16_3d(&tk, k, s.d, krows, varlen ? s.Hkv : s.B * s.Hkv, kBN) ||
-        !make_tmap_bf16_3d(&tv, v, s.d, krows, varlen ? s.Hkv : s.B * s.Hkv, kBN))
+        !make_tmap_bf16_3d(&tk, k, s.d, rows, varlen ? s.Hkv : s.B * s.Hkv, kBN) ||
+        !make_tmap_bf16_3d(&tv, v, s.d, rows, varlen ? s.Hkv : s.B * s.Hkv, kBN))
         return cudaErrorInvalidValue;
     FwdParams p;
-    p.Nk = s.Nk;
-    p.krows = krows;
-    p.kv_lens = s.kv_lens;
-    p.cu_k = s.cu_k;
     p.H = s.H;
     p.Hkv = s.Hkv;
     p.N = s.N;
@@ -1422,10 +919,6 @@ cudaError_t launch_fwd(const Shape& s, const void* q, const void* k, const void*
     const int grid = p.n_items < sms ? p.n_items : sms;
     count_launch();
     const bool c = s.causal != 0;
-    if (cross) {   // keys of another length (bf16 output, no window, no training form)
-        if (precise || s.window > 0 || train_ws) return cudaErrorInvalidValue;
-        return launch_fwd_cross(s, tq, tk, tv, p, cross_ws, stream);
-    }
     if (varlen) {   // packed variable-length sequences (bf16 output, no window)
         if (precise || s.window > 0) return cudaErrorInvalidValue;
         if (s.d == 128)

@@ -1,0 +1,1003 @@
+// Forward with keys of another length (Nk a sequence, lengths on the device, padded or
+// packed), causal from the last key or not: the persistent kernel of the dense forward
+// (two 128-row query tiles an item, the same warps, rings and softmax; its notes are in
+// fa_fwd.cu), with a work list of its own, masks for both lengths, rows of V behind the
+// keys cleared, and the causal mask a run-time flag.  A file and a kernel of its own
+// because the dense kernels lose 1 to 2 % when they are compiled from a shared source.
+#include <cuda_bf16.h>
+#include <algorithm>
+#include <cmath>
+#include <type_traits>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+
+#include "fa_internal.h"
+
+namespace fa {
+namespace {
+
+constexpr int kBM = 128;            // query rows per tile
+constexpr int kBN = 128;            // keys per K/V tile
+constexpr int kTiles = 2;           // query tiles per CTA
+constexpr int kItemRows = kTiles * kBM;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kThreads = 12 * 32;   // softmax of tile 0 and of tile 1, control
+constexpr int kProducerWarp = 8;    // K tiles, and the items
+constexpr int kMmaWarp = 9;
+constexpr int kVProducerWarp = 10;  // V and Q tiles
+constexpr int kPvWarp = 11;         // P V MMA issuer
+// Register split (setmaxnreg): 128 x 72 + 256 x 216 = 64512 <= 384 x 168.
+constexpr int kRegsControl = 72;
+constexpr int kRegsSoftmax = 216;
+constexpr int kRegsNeeded = 128 * kRegsControl + 256 * kRegsSoftmax;
+constexpr float kRescaleThreshold = 8.0f;   // log2 units
+
+template <int D>
+struct CrossCfg {
+    static constexpr int kStagesK = D == 128 ? 3 : 4;
+    static constexpr int kStagesV = D == 128 ? 2 : 3;
+    static constexpr int kTileBytes = kBM * D * 2;          // one Q, K or V tile
+    static constexpr int kChunks = D / 64;                  // 128-byte swizzle chunks
+    static constexpr int kChunkBytes = 128 * 128;           // 128 rows x 128 bytes
+    static constexpr int kOffQ = 0;
+    static constexpr int kOffK = kOffQ + kTiles * kTileBytes;
+    static constexpr int kOffV = kOffK + kStagesK * kTileBytes;
+    static constexpr int kSmemBytes = kOffV + kStagesV * kTileBytes;
+    static constexpr int kSmemAlloc = kSmemBytes + 1024;    // alignment slack
+    // TMEM columns; at d = 64 P_t has 64 of its own (SEP), at d = 128 it overwrites S_t
+    static constexpr uint32_t kColS0 = 0, kColS1 = 128, kColO0 = 256, kColO1 = 256 + D;
+    static constexpr uint32_t kColP0 = 384, kColP1 = 448;
+    // d = 128: every eighth pair of exponentials on the FMA pipe; d = 64 has none of its
+    // issue slots to spare
+    static constexpr int kExp2FmaEvery = D == 128 ? 8 : 0;
+};
+
+// A place in the list of (item, key block) of a forward with keys of its own: block blk
+// of item it of sequence b.
+struct CrossAt {
+    int b, it, blk, pad;
+};
+
+struct CrossParams {
+    int H, Hkv, N, BH, n_items, causal;
+    // Padded: rows = N query rows a head.  Packed: sequence b is rows cu_seqlens[b] ..
+    // cu_seqlens[b + 1] - 1 of every head, at most N of them.
+    int rows;
+    const int* cu_seqlens;
+    // At most Nk keys a sequence, krows rows a head of k and v.  Padded batches:
+    // kv_lens[b] keys, or Nk (null).  Packed ones: rows cu_k[b] .. cu_k[b + 1] - 1.
+    int Nk, krows;
+    const int* kv_lens;
+    const int* cu_k;
+    float scale_log2;                 // scale * log2(e)
+    __nv_bfloat16* o;
+    float* lse;
+    DeviceStatus* status;
+    // May key blocks of one item go to several CTAs?  Then the segments' places in the
+    // workspace: [slot][d / 4][256 rows] quarter rows of O (normalised, fp32),
+    // [slot][256] LSEs (base 2), and where each CTA's part begins.
+    int split;
+    float4* part_o;
+    float* part_lse;
+    CrossAt* part_at;
+};
+
+// An item, or a segment of one: the query-block pair and the key blocks.
+struct CrossTile {
+    int row_base;
+    int q_z, kv_z;             // head coordinate of the Q / O and K / V tensor maps
+    int tok0, len;             // first row of the sequence in its head, its length
+    int ktok0, klen;           // the same of its keys
+    int off;                   // query i sees keys j <= i + off under the causal mask
+    int lo;                    // first key block
+    int n_kv[kTiles];          // one past each query tile's last
+    int slot;                  // of a segment, else -1
+};
+
+// The keys of sequence b: how many, and the first one's row in its head.
+__device__ __forceinline__ int key_rows(const CrossParams& p, int b, int& ktok0) {
+    if (p.cu_k) return packed_seq(p.cu_k, b, p.Nk, p.krows, ktok0);
+    ktok0 = 0;
+    return p.kv_lens ? min(max(__ldg(p.kv_lens + b), 0), p.Nk) : p.Nk;
+}
+
+// The work is a list of (item, key block): sequences in
+// turn, in each the K/V heads, in each the query-block pairs, in each the query heads that
+// share the K/V head, and the item's key blocks.  Each CTA takes an equal share of that
+// list, whole items or segments of them; an item in segments leaves one partial result
+// each in the workspace (a CTA has two at most: its first and its last item), which
+// cross_join_kernel adds up in the order of the keys.  The lengths are on the device, so
+// that each CTA finds its share itself.  Whole items in rounds leave the GPU idle in the
+// last one and are as long as the longest sequence allows: 2 x 32/8 heads, 1024 queries,
+// 17408 keys, d = 128, causal (256 items on 152 SMs): 437 us, in equal shares 390 to 410.
+// Segments pay for the join (a launch, 132 KB written and read each at d = 128): about
+// kJoinCost key blocks, so that cross_ctas() takes them only where an even share is that
+// much shorter; a segment has kMinBlocks blocks at least, and a share that would end
+// within 1/24 of itself of an item's end ends there.  8 heads, 64 queries, d = 128, whole
+// items against segments: 1024 keys 20.6 us / 17.8, 16384 keys 200 / 35; 4 x 32 heads, 256
+// queries (128 items): 2048 keys 40.0 / 48.8, which the rule leaves whole.
+constexpr int kSplitBlocks = 4;   // no segments up to here
+constexpr int kMinBlocks = 2;
+constexpr int kJoinCost = 8;
+constexpr int kItemCost = 3;      // what an item costs besides its key blocks, in those
+constexpr int kMaxCtas = 152;     // the workspace has places for that many
+
+// The items of sequence b, and the key blocks of each.
+struct CrossSeq {
+    int tok0, len, ktok0, klen;
+    int M, n;         // query-block pairs; key blocks
+    int q;            // causal: pair m sees 2 (m + 1) + q of them
+    bool causal;
+
+    __device__ __forceinline__ CrossSeq(const CrossParams& p, int b, bool causal_) {
+        if (p.cu_seqlens) {
+            len = packed_seq(p.cu_seqlens, b, p.N, p.rows, tok0);
+        } else {
+            tok0 = 0;
+            len = p.N;
+        }
+        klen = key_rows(p, b, ktok0);
+        causal = causal_;
+        M = (len + kItemRows - 1) / kItemRows;
+        n = max(1, (klen + kBN - 1) / kBN);
+        q = (klen - len + kBN - 1) >> 7;   // rounds down for negative ones too
+    }
+    __device__ __forceinline__ int blocks(int m) const {
+        return causal ? min(max(2 * (m + 1) + q, 1), n) : n;
+    }
+    // Cost of pairs 0 .. m - 1, key blocks and kItemCost each: pairs below m1 have one
+    // block, those from m2 on all n.
+    __device__ __forceinline__ long long before(int m) const {
+        if (!causal) return (long long)m * (n + kItemCost);
+        const int m1 = min(max((1 - q) >> 1, 0), m);
+        const int m2 = min(max((n - q) >> 1, m1), m);
+        const long long mid = m2 - m1;
+        return m1 + mid * (m1 + m2 + 1 + q) + (long long)(m - m2) * n + (long long)m * kItemCost;
+    }
+};
+static_assert(kBN == 128 && kBM == 128 && kTiles == 2, "CrossSeq counts in these");
+
+// First block of CTA c's share: block t of the list, which lies in sequence b at o.
+__device__ __forceinline__ CrossAt cross_place(const CrossParams& p, const CrossSeq& sq, int b,
+                                               long long o, bool unit, int snap) {
+    const int G = p.H / p.Hkv;
+    CrossAt at;
+    at.b = b;
+    if (unit) {   // every item counts as one
+        at.it = (int)o;
+        at.blk = 0;
+        return at;
+    }
+    const long long head = G * sq.before(sq.M);
+    const int g = o >> 31 ? (int)(o / head) : (int)((uint32_t)o / (uint32_t)min(head, 0x7fffffffll));
+    o -= g * head;
+    int m = 0;                          // the last pair with G before(m) <= o
+    for (int hi = sq.M; hi - m > 1;) {
+        const int mid = (m + hi) >> 1;
+        if (G * sq.before(mid) <= o) m = mid;
+        else hi = mid;
+    }
+    o -= G * sq.before(m);
+    const int n = sq.blocks(m), cost = n + kItemCost, r = (int)o / cost;
+    at.it = (g * sq.M + m) * G + r;
+    at.blk = max((int)o - r * cost - kItemCost, 0);
+    if (at.blk <= snap && (p.split || 2 * at.blk < n)) {
+        at.blk = 0;
+    } else if (n - at.blk <= snap) {
+        at.blk = 0;
+        if (++at.it == p.H * sq.M) {
+            ++at.b;
+            at.it = 0;
+        }
+    }
+    return at;
+}
+
+// The block's share [at[0], at[1]): every thread counts the blocks of a run of sequences.
+__device__ __forceinline__ void cross_share(const CrossParams& p, bool causal, CrossAt* at,
+                                            long long* warp_sum) {
+    const int B = p.BH / p.H;
+    const int run = (B + kThreads - 1) / kThreads;
+    const int b0 = min(B, (int)threadIdx.x * run), b1 = min(B, b0 + run);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool unit = !p.split && p.n_items <= (int)gridDim.x;
+    auto count = [&](const CrossSeq& sq) -> long long {
+        return p.H * (unit ? (long long)sq.M : sq.before(sq.M));
+    };
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) mine += count(CrossSeq(p, b, causal));
+    long long upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const long long o = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += o;
+    }
+    if (lane == 31) warp_sum[warp] = upto;
+    __syncthreads();
+    long long total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w == warp) upto += total;
+        total += warp_sum[w];
+    }
+    const long long per = max((total + gridDim.x - 1) / gridDim.x,
+                              (long long)(p.split ? kMinBlocks : 1));
+    // whole items: the nearest item's end
+    const int snap = p.split ? (int)max(1ll, min(per / 24, 1ll << 20)) : 1 << 30;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const long long t = ((long long)blockIdx.x + e) * per;
+        if (t >= total) {
+            if (threadIdx.x == 0) at[e] = CrossAt{B, 0, 0, 0};
+        } else if (t >= upto - mine && t < upto) {
+            long long o = t - (upto - mine);
+            for (int b = b0; b < b1; ++b) {
+                const CrossSeq sq(p, b, causal);
+                const long long n = count(sq);
+                if (o < n) {
+                    at[e] = cross_place(p, sq, b, o, unit, snap);
+                    break;
+                }
+                o -= n;
+            }
+        }
+    }
+}
+
+// The CTA's items and segments.  The K producer, which is ahead of every other role, finds
+// them and leaves them in a ring in shared memory (struct CrossRing): found by each role
+// by itself, with divisions and loads in one thread, an item cost 2 to 4 us more than one
+// of a dense batch (d = 64 to 128).
+struct CrossWalk {
+    const CrossAt* at;   // shared memory: the share's first place and its end
+    int b, it, blk;      // the item, and the first block of it
+    bool begun = false;
+
+    __device__ __forceinline__ explicit CrossWalk(const CrossAt* a)
+        : at(a), b(a[0].b), it(a[0].it), blk(a[0].blk) {}
+
+    __device__ __forceinline__ bool next(const CrossParams& p, bool causal) {
+        if (begun) {
+            ++it;
+            blk = 0;
+        }
+        begun = true;
+        for (;;) {
+            if (b > at[1].b || (b == at[1].b && it > at[1].it)) return false;
+            if (b == at[1].b && it == at[1].it) return at[1].blk > blk;
+            if (it < p.H * CrossSeq(p, b, causal).M) return true;
+            ++b;
+            it = 0;
+        }
+    }
+};
+
+__device__ __forceinline__ CrossTile cross_tile(const CrossWalk& at, const CrossParams& p,
+                                                bool causal) {
+    const CrossSeq sq(p, at.b, causal);
+    const int G = p.H / p.Hkv;
+    const int m = at.it / G % sq.M, kv = at.it / G / sq.M, h = kv * G + at.it % G;
+    CrossTile w;
+    w.tok0 = sq.tok0;
+    w.len = sq.len;
+    w.ktok0 = sq.ktok0;
+    w.klen = sq.klen;
+    w.off = sq.klen - sq.len;
+    w.q_z = p.cu_seqlens ? h : at.b * p.H + h;
+    w.kv_z = p.cu_seqlens ? kv : at.b * p.Hkv + kv;
+    w.row_base = m * kItemRows;
+    const int n = sq.blocks(m);
+    const int lo = at.blk;
+    const int hi = at.b == at.at[1].b && at.it == at.at[1].it ? at.at[1].blk : n;
+    // The first tile's last row sees keys up to its own index + off.  A tile that sees
+    // nothing of the segment keeps one block, which the masks empty.
+    const int n0 = causal ? min(n, max(2 * m + 1 + sq.q, 1)) : n;
+    w.lo = lo;
+    w.n_kv[0] = max(lo + 1, min(n0, hi));
+    w.n_kv[1] = hi;
+    // (its first item may lack a beginning, its last one an end)
+    w.slot = lo > 0 ? 2 * (int)blockIdx.x : hi < n ? 2 * (int)blockIdx.x + 1 : -1;
+    return w;
+}
+
+constexpr int kRing = 4;
+constexpr int kRingReaders = 3 + 8;   // V producer, the two issuers, the softmax warps
+
+struct CrossRing {
+    CrossTile tile[kRing];   // n_kv[1] == 0: no more
+    uint64_t full[kRing], empty[kRing];
+};
+
+// A reader's way through the ring, by one thread or (warp) a whole warp.
+struct RingReader {
+    CrossRing* ring;
+    WaitCtx wc;
+    bool warp;
+    uint32_t i = 0;
+    bool ok = true;   // false: gave up waiting
+
+    // The item, until the next call of next().
+    __device__ __forceinline__ const CrossTile& tile() const { return ring->tile[(i - 1) % kRing]; }
+    __device__ __forceinline__ bool next() {
+        if (i > 0) {
+            if (warp) __syncwarp();
+            if (!warp || (threadIdx.x & 31) == 0) mbar_arrive(&ring->empty[(i - 1) % kRing]);
+        }
+        uint64_t* full = &ring->full[i % kRing];
+        const uint32_t par = (i / kRing) & 1;
+        ok = warp ? fa_wait_warp(full, par, 40, wc) : fa_wait(full, par, 40, wc);
+        ++i;
+        return ok && tile().n_kv[kTiles - 1] > 0;
+    }
+};
+
+// Rows past a sequence's keys may hold anything: their scores are masked, and the softmax
+// of query tile 0 (of tile 1 where only that sees the block) clears V's rows.
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+cross_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                 const __grid_constant__ CUtensorMap tm_v, const CrossParams p) {
+    using Cfg = CrossCfg<D>;
+    constexpr int SK = Cfg::kStagesK, SV = Cfg::kStagesV;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    __shared__ uint64_t bar_k[SK], bar_k_empty[SK], bar_v[SV], bar_v_empty[SV];
+    __shared__ uint64_t bar_q[kTiles], bar_q_free[kTiles];
+    __shared__ uint64_t bar_s[kTiles], bar_p[kTiles], bar_pv[kTiles], bar_o_free[kTiles];
+    __shared__ uint64_t bar_s_free[kTiles];   // SEP only
+    __shared__ CrossAt share[2];
+    __shared__ CrossRing ring;
+    __shared__ long long warp_sum[kThreads / 32];
+    constexpr bool SEP = D == 64;
+    __shared__ uint32_t tmem_base_sh;
+    __shared__ int abort_sh;
+    const WaitCtx wc{p.status, &abort_sh};
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool causal = p.causal;
+    cross_share(p, causal, share, warp_sum);
+
+    if (threadIdx.x == 0) {
+        abort_sh = 0;
+        for (int s = 0; s < SK; ++s) {
+            mbar_init(&bar_k[s], 1);
+            mbar_init(&bar_k_empty[s], 1);
+        }
+        for (int s = 0; s < SV; ++s) {
+            mbar_init(&bar_v[s], 1);
+            mbar_init(&bar_v_empty[s], 1);
+        }
+        for (int t = 0; t < kTiles; ++t) {
+            mbar_init(&bar_q[t], 1);
+            mbar_init(&bar_q_free[t], 1);
+            mbar_init(&bar_s[t], 1);
+            mbar_init(&bar_p[t], 128);
+            mbar_init(&bar_o_free[t], 128);
+            mbar_init(&bar_s_free[t], 128);
+            mbar_init(&bar_pv[t], 1);
+        }
+        for (int r = 0; r < kRing; ++r) {
+            mbar_init(&ring.full[r], 1);
+            mbar_init(&ring.empty[r], kRingReaders);
+        }
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&tmem_base_sh, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base_sh;
+
+    uint8_t* sQ = smem + Cfg::kOffQ;
+    uint8_t* sK = smem + Cfg::kOffK;
+    uint8_t* sV = smem + Cfg::kOffV;
+
+    // One register-budget change per warpgroup, executed by all its warps at
+    // the same instruction; each role's code is dominated by exactly one.
+    if (warp < kSoftmaxWarps) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+        // ------------------------------------------------------------ softmax
+        const int t = warp >> 2;                 // query tile of this group
+        const int quarter = warp & 3;            // TMEM lane quarter
+        const int rl = quarter * 32 + lane;      // row within the tile
+        const uint32_t col_s = t ? Cfg::kColS1 : Cfg::kColS0;
+        const uint32_t col_o = t ? Cfg::kColO1 : Cfg::kColO0;
+        const uint32_t col_p = SEP ? (t ? Cfg::kColP1 : Cfg::kColP0) : col_s;
+        const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
+        const float c = p.scale_log2;
+        uint32_t cs = 0;                         // S_t completions seen so far
+        uint32_t cpv = 0;                        // P_t V completions seen (separate P)
+        uint32_t gv = 0;                         // V blocks of the items before
+        bool ok = true;
+        int lt = 0;
+        RingReader items{&ring, wc, true};
+        for (; ok && items.next(); ++lt) {
+            // (read where it is used: there are no registers to hold it)
+            const CrossTile& wt = items.tile();
+            const int lo = wt.lo, n_kv = wt.n_kv[t];
+            // the last key that this thread's row sees
+            const int last = min(causal ? wt.row_base + t * kBM + rl + wt.off : wt.klen, wt.klen - 1);
+            float m2 = -CUDART_INF_F;   // running max, log2-scaled
+            float l = 0.0f;
+            for (int j = lo; j < n_kv; ++j) {
+                if ((j + 1) * kBN > wt.klen && (t == 0 || j >= wt.n_kv[0])) {
+                    // V_j's rows past the keys: a weight of zero would not silence a
+                    // NaN.  Before the scores are waited for (the loads of V_j wait for
+                    // none of this tile's MMAs to come), and by the stage's order no
+                    // other use of the stage comes before this tile's P V.
+                    const uint32_t gj = gv + (uint32_t)(j - lo), vs = gj % SV;
+                    if (!fa_wait_warp(&bar_v[vs], (gj / SV) & 1, 38 + t, wc)) { ok = false; break; }
+                    if (j * kBN + rl >= wt.klen) {
+                        const uint32_t vrow = smem_u32(sV) + vs * Cfg::kTileBytes + rl * 128;
+#pragma unroll
+                        for (int u = 0; u < Cfg::kChunks * 8; ++u)   // (eight lanes, eight banks)
+                            sts_v4(vrow + (u >> 3) * Cfg::kChunkBytes + ((u ^ rl) & 7) * 16,
+                                   make_uint4(0u, 0u, 0u, 0u));
+                    }
+                    fence_proxy_async_smem();
+                }
+                if (!fa_wait_warp(&bar_s[t], cs & 1, 30 + t, wc)) { ok = false; break; }
+                ++cs;
+                tc_fence_after();
+                uint32_t r[4][32];
+                tmem_ld32(lane_addr + col_s + 0, r[0]);
+                tmem_ld32(lane_addr + col_s + 32, r[1]);
+                tmem_ld32(lane_addr + col_s + 64, r[2]);
+                tmem_ld32(lane_addr + col_s + 96, r[3]);
+                tmem_ld_wait(r[0]);
+                asm volatile("" : FA_R32(r[1]) : : "memory");
+                asm volatile("" : FA_R32(r[2]) : : "memory");
+                asm volatile("" : FA_R32(r[3]) : : "memory");
+                if (SEP) {   // S_t is in registers: the next S_t MMA may overwrite it
+                    tc_fence_before();
+                    mbar_arrive(&bar_s_free[t]);
+                }
+                float sv[kBN];
+#pragma unroll
+                for (int e = 0; e < kBN; ++e) sv[e] = __uint_as_float(r[e >> 5][e & 31]);
+
+                const int col0 = j * kBN;
+                if (last - col0 < kBN - 1) {
+#pragma unroll
+                    for (int e = 0; e < kBN; ++e)
+                        if (e > last - col0) sv[e] = -CUDART_INF_F;
+                }
+                // Row max: three-input max, eight independent chains.
+                float mx8[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) mx8[u] = fmaxf(sv[2 * u], sv[2 * u + 1]);
+#pragma unroll
+                for (int e = 16; e < kBN; e += 16)
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) mx8[u] = fmax3(mx8[u], sv[e + 2 * u], sv[e + 2 * u + 1]);
+                const float mx = fmaxf(fmax3(mx8[0], mx8[1], mx8[2]),
+                                       fmax3(fmax3(mx8[3], mx8[4], mx8[5]), mx8[6], mx8[7]));
+                const float mx2 = mx * c;
+                const bool need = mx2 > m2 + kRescaleThreshold;
+                // O rescale of this block (only when some row raised its max);
+                // the O columns may be touched only after the P V MMA of the
+                // previous block has completed.
+                auto rescale_o = [&](float alpha) {
+#pragma unroll
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        uint32_t ov[32];
+                        tmem_ld32(lane_addr + col_o + c0, ov);
+                        tmem_ld_wait(ov);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                        tmem_st32(lane_addr + col_o + c0, ov);
+                    }
+                };
+                const bool any_need = __any_sync(0xffffffffu, need);
+                float alpha = 1.0f;
+                if (any_need) {
+                    const float m_new = need ? mx2 : m2;
+                    alpha = (m_new == m2) ? 1.0f : ex2(m2 - m_new);
+                    l *= alpha;
+                    if (!SEP && j > lo) rescale_o(alpha);
+                    m2 = m_new;
+                }
+                const float m_use = (m2 == -CUDART_INF_F) ? 0.0f : m2;
+                // p = 2^(s c - m): exponent argument two lanes per instruction,
+                // row sum in four paired accumulators.
+                const uint64_t c2 = f2(c, c), negm2 = f2(-m_use, -m_use);
+                uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};
+                uint32_t pk[2][32];
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+#pragma unroll
+                    for (int e2 = 0; e2 < 32; ++e2) {
+                        const int e = hh * 64 + 2 * e2;
+                        float p0, p1;
+                        if (Cfg::kExp2FmaEvery > 0 &&
+                            e2 % max(Cfg::kExp2FmaEvery, 1) == Cfg::kExp2FmaEvery - 1) {
+                            // this pair on the FMA pipe (exp2_fma2), the rest
+                            // on the exponential unit
+                            f2_split(exp2_fma2(f2_fma(f2(sv[e], sv[e + 1]), c2, negm2)), p0, p1);
+                        } else {
+                            float x0, x1;
+                            f2_split(f2_fma(f2(sv[e], sv[e + 1]), c2, negm2), x0, x1);
+                            p0 = ex2(x0);
+                            p1 = ex2(x1);
+                        }
+                        acc2[e2 & 3] = f2_add(acc2[e2 & 3], f2(p0, p1));
+                        pk[hh][e2] = pack_bf16x2(p0, p1);
+                    }
+                    if (!SEP) tmem_st32(lane_addr + col_s + hh * 32, pk[hh]);
+                }
+                if (SEP) {
+                    // P_t and O_t are free once P_t(j-1) V has completed.
+                    if (j > lo) {
+                        if (!fa_wait_warp(&bar_pv[t], cpv & 1, 34 + t, wc)) { ok = false; break; }
+                        ++cpv;
+                        tc_fence_after();
+                        if (any_need) rescale_o(alpha);
+                    }
+                    tmem_st32(lane_addr + col_p, pk[0]);
+                    tmem_st32(lane_addr + col_p + 32, pk[1]);
+                }
+                {
+                    float a0, a1;
+                    f2_split(f2_add(f2_add(acc2[0], acc2[1]), f2_add(acc2[2], acc2[3])), a0, a1);
+                    l += a0 + a1;
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&bar_p[t]);
+            }
+            if (!ok) break;
+            gv += wt.n_kv[kTiles - 1] - lo;
+
+            // ------------------------------------------------------- epilogue
+            // O row -> registers, release the O columns to the next item's
+            // MMAs, then normalise and store.
+            // The last P_t V MMA of the item has completed.  Without separate
+            // P columns the softmax did not wait for the earlier ones; each S
+            // MMA was issued only after the P V MMA before it had completed,
+            // so those are complete already.
+            if (!SEP) cpv += n_kv - lo - 1;
+            if (!fa_wait_warp(&bar_pv[t], cpv & 1, 34 + t, wc)) { ok = false; break; }
+            ++cpv;
+            tc_fence_after();
+            uint32_t ov[D / 32][32];
+#pragma unroll
+            for (int c0 = 0; c0 < D / 32; ++c0) tmem_ld32(lane_addr + col_o + c0 * 32, ov[c0]);
+            tmem_ld_wait(ov[0]);
+#pragma unroll
+            for (int c0 = 1; c0 < D / 32; ++c0) asm volatile("" : FA_R32(ov[c0]) : : "memory");
+            tc_fence_before();
+            mbar_arrive(&bar_o_free[t]);
+            const int row = wt.row_base + t * kBM + rl, seg = wt.slot;
+            const bool valid = row < wt.len;
+            // a row that sees no key (the exponentials of the FMA pipe are not quite 0);
+            // scores of NaN, which the maximum passes over, leave l NaN
+            if (m2 == -CUDART_INF_F && l == l) {
+                l = 0.0f;
+#pragma unroll
+                for (int c0 = 0; c0 < D / 32; ++c0)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) ov[c0][e] = 0u;
+            }
+            const float inv_l = l > 0.0f ? 1.0f / l : 0.0f;
+            if (seg >= 0) {   // a segment: the join makes the rows of it
+                if (valid) {
+                    const int r = t * kBM + rl;
+                    float4* dst = p.part_o + (size_t)seg * (D / 4) * kItemRows + r;
+#pragma unroll
+                    for (int c0 = 0; c0 < D / 4; ++c0)
+                        dst[c0 * kItemRows] =
+                            make_float4(__uint_as_float(ov[c0 / 8][c0 % 8 * 4 + 0]) * inv_l,
+                                        __uint_as_float(ov[c0 / 8][c0 % 8 * 4 + 1]) * inv_l,
+                                        __uint_as_float(ov[c0 / 8][c0 % 8 * 4 + 2]) * inv_l,
+                                        __uint_as_float(ov[c0 / 8][c0 % 8 * 4 + 3]) * inv_l);
+                    p.part_lse[(size_t)seg * kItemRows + r] =
+                        l == 0.0f ? -CUDART_INF_F : m2 + log2f(l);
+                }
+                continue;
+            }
+            const size_t orow = ((size_t)wt.q_z * p.rows + wt.tok0 + (valid ? row : 0)) * D;
+            if (valid) {
+#pragma unroll
+                for (int c0 = 0; c0 < D / 32; ++c0) {
+                    uint4* dst = reinterpret_cast<uint4*>(
+                        p.o + orow + c0 * 32);
+#pragma unroll
+                    for (int q4 = 0; q4 < 4; ++q4) {
+                        uint4 w;
+                        w.x = pack_bf16x2(__uint_as_float(ov[c0][q4 * 8 + 0]) * inv_l,
+                                          __uint_as_float(ov[c0][q4 * 8 + 1]) * inv_l);
+                        w.y = pack_bf16x2(__uint_as_float(ov[c0][q4 * 8 + 2]) * inv_l,
+                                          __uint_as_float(ov[c0][q4 * 8 + 3]) * inv_l);
+                        w.z = pack_bf16x2(__uint_as_float(ov[c0][q4 * 8 + 4]) * inv_l,
+                                          __uint_as_float(ov[c0][q4 * 8 + 5]) * inv_l);
+                        w.w = pack_bf16x2(__uint_as_float(ov[c0][q4 * 8 + 6]) * inv_l,
+                                          __uint_as_float(ov[c0][q4 * 8 + 7]) * inv_l);
+                        dst[q4] = w;
+                    }
+                }
+                p.lse[(size_t)wt.q_z * p.rows + wt.tok0 + row] =
+                    l != 0.0f ? (m2 + log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
+        if (warp == kProducerWarp && lane == 0) {
+            // ------------------------------------------------- K producer
+            tma_prefetch_desc(&tm_k);
+            uint32_t g = 0;              // K blocks loaded so far (ring position)
+            bool ok = true;
+            // The next item goes into the ring once this one's first block is on its way.
+            CrossWalk walk(share);
+            uint32_t n = 0;   // items put into the ring
+            CrossTile nxt;
+            auto put = [&] {
+                const uint32_t r = n % kRing;
+                if (n >= (uint32_t)kRing && !fa_wait(&ring.empty[r], (n / kRing - 1) & 1, 41, wc))
+                    return false;
+                nxt.n_kv[kTiles - 1] = 0;
+                if (walk.next(p, causal)) nxt = cross_tile(walk, p, causal);
+                ring.tile[r] = nxt;
+                mbar_arrive(&ring.full[r]);
+                ++n;
+                return true;
+            };
+            ok = put();
+            while (ok && nxt.n_kv[kTiles - 1] > 0) {
+                const CrossTile wt = nxt;
+                for (int j = wt.lo; j < wt.n_kv[kTiles - 1]; ++j, ++g) {
+                    const int s = g % SK;
+                    if (g >= (uint32_t)SK &&
+                        !fa_wait(&bar_k_empty[s], ((g / SK) - 1) & 1, 10, wc)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(&bar_k[s], Cfg::kTileBytes);
+                    for (int c = 0; c < Cfg::kChunks; ++c)
+                        tma_load_3d(sK + s * Cfg::kTileBytes + c * Cfg::kChunkBytes, &tm_k,
+                                    &bar_k[s], c * 64, wt.ktok0 + j * kBN, wt.kv_z);
+                    if (j == wt.lo) ok = put();
+                }
+            }
+            if (abort_sh) {   // drain the copies still in flight (bounded)
+                const WaitCtx dc{p.status, nullptr};
+                for (uint32_t x = (g > (uint32_t)SK ? g - SK : 0); x < g; ++x)
+                    fa_wait(&bar_k[x % SK], (x / SK) & 1, 11, dc);
+            }
+        } else if (warp == kVProducerWarp && lane == 0) {
+            // ---------------------------------------------- V and Q producer
+            // The Q tiles of an item are loaded ahead of its V blocks, as soon
+            // as the last S MMAs of the previous item have read the old ones.
+            tma_prefetch_desc(&tm_v);
+            tma_prefetch_desc(&tm_q);
+            uint32_t g = 0;
+            int lt = 0, q_loaded = -1;
+            bool ok = true;
+            RingReader items{&ring, wc, false};
+            for (; ok && items.next(); ++lt) {
+                const CrossTile wt = items.tile();
+                for (int t = 0; t < kTiles; ++t) {
+                    if (lt > 0 && !fa_wait(&bar_q_free[t], (lt - 1) & 1, 12, wc)) { ok = false; break; }
+                    mbar_arrive_expect_tx(&bar_q[t], Cfg::kTileBytes);
+                    for (int c = 0; c < Cfg::kChunks; ++c)
+                        tma_load_3d(sQ + t * Cfg::kTileBytes + c * Cfg::kChunkBytes, &tm_q,
+                                    &bar_q[t], c * 64, wt.tok0 + wt.row_base + t * kBM, wt.q_z);
+                }
+                if (!ok) break;
+                q_loaded = lt;
+                for (int j = wt.lo; j < wt.n_kv[kTiles - 1]; ++j, ++g) {
+                    const int s = g % SV;
+                    if (g >= (uint32_t)SV && !fa_wait(&bar_v_empty[s], ((g / SV) - 1) & 1, 13, wc)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(&bar_v[s], Cfg::kTileBytes);
+                    for (int c = 0; c < Cfg::kChunks; ++c)
+                        tma_load_3d(sV + s * Cfg::kTileBytes + c * Cfg::kChunkBytes, &tm_v, &bar_v[s],
+                                    c * 64, wt.ktok0 + j * kBN, wt.kv_z);
+                }
+            }
+            if (abort_sh) {   // drain the copies still in flight (bounded)
+                const WaitCtx dc{p.status, nullptr};
+                for (uint32_t x = (g > (uint32_t)SV ? g - SV : 0); x < g; ++x)
+                    fa_wait(&bar_v[x % SV], (x / SV) & 1, 14, dc);
+                if (q_loaded >= 0)
+                    for (int t = 0; t < kTiles; ++t) fa_wait(&bar_q[t], q_loaded & 1, 15, dc);
+            }
+        } else if (warp == kPvWarp && lane == 0) {
+            // ------------------------------------------- P V MMA issuer
+            // O_t += P_t V_j, P_t read from TMEM.  A second issuing thread:
+            // while the S issuer waits or commits, this one keeps the tensor
+            // core busy, and the other way round.
+            constexpr uint32_t idesc_o = idesc_bf16_f32(kBM, D, false, true);
+            const uint32_t sv = smem_u32(sV);
+            uint32_t g = 0, cp0 = 0, cp1 = 0;       // V blocks used; P_t arrivals seen
+            bool ok = true;
+            int lt = 0;
+            auto pv = [&](auto tc, uint32_t vstage, bool first, bool wait_o) -> bool {
+                constexpr int T = decltype(tc)::value;
+                constexpr uint32_t col_o = T ? Cfg::kColO1 : Cfg::kColO0;
+                constexpr uint32_t col_s = T ? Cfg::kColS1 : Cfg::kColS0;
+                constexpr uint32_t col_p = SEP ? (T ? Cfg::kColP1 : Cfg::kColP0) : col_s;
+                uint32_t& c = T ? cp1 : cp0;
+                if (!fa_wait(&bar_p[T], c & 1, 24 + T, wc)) return false;
+                ++c;
+                if (wait_o && !fa_wait(&bar_o_free[T], (lt - 1) & 1, 26 + T, wc)) return false;
+                tc_fence_after();
+                const uint64_t vd = sdesc_sw128(sv + vstage * Cfg::kTileBytes, Cfg::kChunkBytes, 1024);
+#pragma unroll
+                for (int kk = 0; kk < kBN / 16; ++kk)
+                    mma_ts(tmem + col_o, tmem + col_p + kk * 8, vd + mnmajor_step(kk), idesc_o,
+                           (!first || kk > 0) ? 1u : 0u);
+                mma_commit(&bar_pv[T]);
+                return true;
+            };
+            RingReader items{&ring, wc, false};
+            for (; ok && items.next(); ++lt) {
+                const CrossTile wt = items.tile();
+                // Key blocks [lo0, n0) for tile 0, [lo1, n1) for tile 1, with
+                // lo0 <= lo1 and n0 <= n1; V_j streams for j in [lo0, n1).
+                const int lo0 = wt.lo, lo1 = wt.lo, n0 = wt.n_kv[0], n1 = wt.n_kv[1];
+                for (int j = lo0; j < n1; ++j) {
+                    const uint32_t gj = g + (j - lo0), vs = gj % SV;
+                    if (!fa_wait(&bar_v[vs], (gj / SV) & 1, 22, wc)) {
+                        ok = false;
+                        break;
+                    }
+                    if (j < n0 && !pv(std::integral_constant<int, 0>{}, vs, j == lo0,
+                                      j == lo0 && lt > 0)) {
+                        ok = false;
+                        break;
+                    }
+                    if (j >= lo1 && !pv(std::integral_constant<int, 1>{}, vs, j == lo1,
+                                        j == lo1 && lt > 0)) {
+                        ok = false;
+                        break;
+                    }
+                    mma_commit(&bar_v_empty[vs]);            // V_j read by both PVs
+                }
+                g += n1 - lo0;
+            }
+            ok = ok && items.ok;
+            if (!ok) {   // no MMA of this thread may still write TMEM at teardown
+                __shared__ uint64_t bar_drain_pv;
+                mbar_init(&bar_drain_pv, 1);
+                fence_mbar_init();
+                mma_commit(&bar_drain_pv);
+                fa_wait(&bar_drain_pv, 0, 29, WaitCtx{p.status, nullptr});
+            }
+        } else if (warp == kMmaWarp && lane == 0) {
+            // ---------------------------------------------- S MMA issuer
+            // S_t(j) = Q_t K_j^T goes out as soon as K_j has landed and the
+            // columns of S_t are free again: loaded by the softmax (P in
+            // columns of its own), or read by the P_t V MMA of the previous
+            // block (P written over S).  The tile index is a compile-time
+            // constant in every MMA, so operand addresses fold into the
+            // instruction stream.
+            constexpr uint32_t idesc_s = idesc_bf16_f32(kBM, kBN, false, false);
+            const uint32_t sq = smem_u32(sQ), sk = smem_u32(sK);
+            uint32_t g = 0, ns0 = 0, ns1 = 0;       // K blocks used; S_t MMAs issued
+            bool ok = true;
+            int lt = 0;
+            auto s_mma = [&](auto tc, uint32_t kstage) -> bool {
+                constexpr int T = decltype(tc)::value;
+                uint32_t& n = T ? ns1 : ns0;
+                if (n > 0 && !fa_wait(SEP ? &bar_s_free[T] : &bar_pv[T], (n - 1) & 1, 36 + T, wc))
+                    return false;
+                ++n;
+                tc_fence_after();
+                const uint64_t qd = sdesc_sw128(sq + T * Cfg::kTileBytes, 16, 1024);
+                const uint64_t kd = sdesc_sw128(sk + kstage * Cfg::kTileBytes, 16, 1024);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    mma_ss(tmem + (T ? Cfg::kColS1 : Cfg::kColS0),
+                           qd + kmajor_step(kk, Cfg::kChunkBytes),
+                           kd + kmajor_step(kk, Cfg::kChunkBytes), idesc_s, kk > 0);
+                mma_commit(&bar_s[T]);
+                return true;
+            };
+            RingReader items{&ring, wc, false};
+            for (; ok && items.next(); ++lt) {
+                const CrossTile wt = items.tile();
+                const int lo0 = wt.lo, lo1 = wt.lo, n0 = wt.n_kv[0], n1 = wt.n_kv[1];
+                if (!fa_wait(&bar_q[0], lt & 1, 20, wc) || !fa_wait(&bar_q[1], lt & 1, 20, wc)) {
+                    ok = false;
+                    break;
+                }
+                for (int j = lo0; j < n1; ++j) {
+                    const uint32_t gj = g + (j - lo0), ks = gj % SK;
+                    if (!fa_wait(&bar_k[ks], (gj / SK) & 1, 21, wc)) { ok = false; break; }
+                    if (j < n0) {
+                        if (!s_mma(std::integral_constant<int, 0>{}, ks)) { ok = false; break; }
+                        if (j + 1 == n0) mma_commit(&bar_q_free[0]);
+                    }
+                    if (j >= lo1) {
+                        if (!s_mma(std::integral_constant<int, 1>{}, ks)) { ok = false; break; }
+                        if (j + 1 == n1) mma_commit(&bar_q_free[1]);
+                    }
+                    mma_commit(&bar_k_empty[ks]);            // K_j read by both S MMAs
+                }
+                g += n1 - lo0;
+            }
+            ok = ok && items.ok;
+            if (!ok) {
+                __shared__ uint64_t bar_drain;
+                mbar_init(&bar_drain, 1);
+                fence_mbar_init();
+                mma_commit(&bar_drain);
+                fa_wait(&bar_drain, 0, 29, WaitCtx{p.status, nullptr});
+            }
+        }
+        __syncwarp();
+    }
+
+    if (threadIdx.x == 0 && p.split) p.part_at[blockIdx.x] = share[0];
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// The items that went to several CTAs: O = sum over the segments of 2^(L_s - L) O_s with
+// L = log2 sum 2^L_s, L_s the segment's LSE.  Block (c, y) has the item in whose middle
+// CTA c's share begins, if c is the first such, and 16 columns of O; one row a thread.
+// Bound by the reads of the segments (from L2: they were just written).
+template <int D>
+__global__ void __launch_bounds__(kItemRows)
+cross_join_kernel(const CrossParams p, int ctas) {
+    pdl_wait();
+    const int c = blockIdx.x + 1, r = threadIdx.x;
+    const CrossAt at = p.part_at[c], prev = p.part_at[c - 1];
+    if (at.blk == 0 || (prev.b == at.b && prev.it == at.it && prev.blk > 0)) return;
+    const CrossSeq sq(p, at.b, p.causal);
+    const int G = p.H / p.Hkv;
+    const int h = at.it / G / sq.M * G + at.it % G;
+    const int row = at.it / G % sq.M * kItemRows + r;
+    if (row >= sq.len) return;
+    int last = c;
+    while (last + 1 < ctas) {
+        const CrossAt a = p.part_at[last + 1];
+        if (a.b != at.b || a.it != at.it || a.blk == 0) break;
+        ++last;
+    }
+    auto slot = [&](int x) { return (size_t)(2 * x + (x < c ? 1 : 0)); };
+    float top = -CUDART_INF_F;
+    for (int x = c - 1; x <= last; ++x) top = fmaxf(top, p.part_lse[slot(x) * kItemRows + r]);
+    const float m = top == -CUDART_INF_F ? 0.0f : top;
+    float sum = 0.0f, acc[16] = {};
+#pragma unroll 2
+    for (int x = c - 1; x <= last; ++x) {
+        const float w = ex2(p.part_lse[slot(x) * kItemRows + r] - m);
+        const float4* src =
+            p.part_o + (slot(x) * (D / 4) + blockIdx.y * 4) * kItemRows + r;
+        sum += w;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const float4 v = src[u * kItemRows];
+            acc[4 * u + 0] = fmaf(w, v.x, acc[4 * u + 0]);
+            acc[4 * u + 1] = fmaf(w, v.y, acc[4 * u + 1]);
+            acc[4 * u + 2] = fmaf(w, v.z, acc[4 * u + 2]);
+            acc[4 * u + 3] = fmaf(w, v.w, acc[4 * u + 3]);
+        }
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const size_t z = p.cu_seqlens ? (size_t)h : (size_t)at.b * p.H + h;
+    const size_t orow = z * p.rows + sq.tok0 + row;
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + orow * D +
+                                          blockIdx.y * 16);
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+        dst[u] = make_uint4(pack_bf16x2(acc[8 * u + 0] * inv, acc[8 * u + 1] * inv),
+                            pack_bf16x2(acc[8 * u + 2] * inv, acc[8 * u + 3] * inv),
+                            pack_bf16x2(acc[8 * u + 4] * inv, acc[8 * u + 5] * inv),
+                            pack_bf16x2(acc[8 * u + 6] * inv, acc[8 * u + 7] * inv));
+    if (blockIdx.y == 0)
+        p.lse[orow] =
+            sum == 0.0f ? -CUDART_INF_F : (m + log2f(sum)) * 0.69314718055994531f;
+}
+
+template <int D>
+cudaError_t launch_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                     const CrossParams& p, int ctas, cudaStream_t stream) {
+    auto kern = cross_fwd_kernel<D>;
+    static int configured_device = -1;   // attribute is per device; cheap to repeat
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (configured_device != dev) {
+        // The register split must fit in what the launch provides, or the
+        // setmaxnreg.inc of the softmax warps would wait forever.
+        cudaFuncAttributes attr;
+        cudaError_t e = cudaFuncGetAttributes(&attr, kern);
+        if (e != cudaSuccess) return e;
+        if (attr.numRegs * kThreads < kRegsNeeded) return cudaErrorInvalidConfiguration;
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 CrossCfg<D>::kSmemAlloc);
+        if (e != cudaSuccess) return e;
+        configured_device = dev;
+    }
+    count_launch();
+    kern<<<ctas, kThreads, CrossCfg<D>::kSmemAlloc, stream>>>(tq, tk, tv, p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || !p.split || ctas < 2) return e;
+    return launch_pdl(cross_join_kernel<D>, dim3(ctas - 1, D / 16), kItemRows, 0, 1, stream, p,
+                      ctas);
+}
+
+// Keys of another length: the most CTAs that a split call has.
+long long split_ctas(const Shape& s) {
+    const long long items = (long long)s.B * s.H * ((s.N + kItemRows - 1) / kItemRows);
+    const long long n = (s.Nk + kBN - 1) / kBN;
+    return n <= kSplitBlocks ? 0 : std::min<long long>(kMaxCtas, (items * n + kMinBlocks - 1) / kMinBlocks);
+}
+
+// CTAs, and are there segments?  Only where an even share and the join are shorter than
+// the rounds of whole items; from what the host knows, the sizes (padded sequences
+// counted in full, packed ones as equally long).
+int cross_ctas(const Shape& s, bool& split) {
+    const int sms = std::min(device_sm_count() > 0 ? device_sm_count() : 148, kMaxCtas);
+    const long long rows = s.cu_seqlens ? s.total / s.B : s.N;
+    const long long keys = s.cu_k ? std::min(s.total_k / s.B, s.Nk) : s.Nk;
+    const long long M = std::max(1ll, (rows + kItemRows - 1) / kItemRows);
+    const long long n = (keys + kBN - 1) / kBN, q = (s.Nk - s.N) / kBN;
+    double blocks = 0.0;   // of the pairs of one head
+    for (long long m = 0; m < M; ++m)
+        blocks += kItemCost + (s.causal ? std::min(std::max(2 * (m + 1) + q, 1ll), n) : n);
+    const double items = (double)s.B * s.H * M, share = (double)s.B * s.H * blocks / sms;
+    const double longest = (s.Nk + kBN - 1) / kBN + kItemCost;
+    const double whole = std::max(longest, std::ceil(items / sms) * blocks / M);
+    split = split_ctas(s) > 0 && std::max(share, (double)kMinBlocks) + kJoinCost < whole;
+    const long long most = (long long)s.B * s.H * ((s.N + kItemRows - 1) / kItemRows);
+    return (int)std::min<long long>(sms, split ? split_ctas(s) : most);
+}
+
+}  // namespace
+
+size_t cross_fwd_workspace_bytes(const Shape& s) {
+    return std::max<size_t>(
+        256, split_ctas(s) * (2 * kItemRows * (s.d + 1) * sizeof(float) + sizeof(CrossAt)));
+}
+
+cudaError_t launch_fwd_cross(const Shape& s, const void* q, const void* k, const void* v, void* o,
+                             float* lse, void* workspace, DeviceStatus* status,
+                             cudaStream_t stream) {
+    // Padded: maps {d, Nq or Nk, B*H(kv)}.  Packed: {d, total, H(kv)}, a sequence's rows
+    // addressed from its first row.
+    const bool packed = s.cu_seqlens != nullptr;
+    const int rows = packed ? s.total : s.N, krows = packed ? s.total_k : s.Nk;
+    CUtensorMap tq, tk, tv;
+    if (!make_tmap_bf16_3d(&tq, q, s.d, rows, packed ? s.H : s.B * s.H, kBM) ||
+        !make_tmap_bf16_3d(&tk, k, s.d, krows, packed ? s.Hkv : s.B * s.Hkv, kBN) ||
+        !make_tmap_bf16_3d(&tv, v, s.d, krows, packed ? s.Hkv : s.B * s.Hkv, kBN))
+        return cudaErrorInvalidValue;
+    bool split;
+    const int ctas = cross_ctas(s, split);
+    CrossParams p;
+    p.H = s.H;
+    p.Hkv = s.Hkv;
+    p.N = s.N;
+    p.BH = s.B * s.H;
+    p.n_items = (s.N + kItemRows - 1) / kItemRows * p.BH;
+    p.causal = s.causal;
+    p.rows = rows;
+    p.cu_seqlens = s.cu_seqlens;
+    p.Nk = s.Nk;
+    p.krows = krows;
+    p.kv_lens = s.kv_lens;
+    p.cu_k = s.cu_k;
+    p.scale_log2 = (float)((double)s.scale * 1.4426950408889634);
+    p.o = static_cast<__nv_bfloat16*>(o);
+    p.lse = lse;
+    p.status = status;
+    p.split = split;
+    p.part_o = static_cast<float4*>(workspace);
+    p.part_lse = static_cast<float*>(workspace) + (size_t)2 * ctas * kItemRows * s.d;
+    p.part_at = reinterpret_cast<CrossAt*>(p.part_lse + (size_t)2 * ctas * kItemRows);
+    return s.d == 128 ? launch_t<128>(tq, tk, tv, p, ctas, stream)
+                      : launch_t<64>(tq, tk, tv, p, ctas, stream);
+}
+
+}  // namespace fa

@@ -112,11 +112,9 @@ BwdWorkspace bwd_workspace_carve(void* base, const Shape& s);
 // Launchers (return a cudaError_t from the launch).
 // launch_fwd: train_ws non-null = training forward, which also writes the
 // -LSE table and zeroes the dQ accumulator of that backward workspace.
-// cross_ws: cross_fwd_workspace_bytes() for keys of their own.
 cudaError_t launch_fwd(const Shape& s, const void* q, const void* k, const void* v, void* o,
                        float* lse, bool precise, DeviceStatus* status, cudaStream_t stream,
-                       const BwdWorkspace* train_ws = nullptr, void* cross_ws = nullptr);
-size_t cross_fwd_workspace_bytes(const Shape& s);
+                       const BwdWorkspace* train_ws = nullptr);
 // full = false: only -D (the rest was prepared by the training forward).
 cudaError_t launch_bwd_preprocess(const Shape& s, const void* o, bool o_f32, const void* dout,
                                   const float* lse, const BwdWorkspace& ws,
@@ -205,11 +203,21 @@ cudaError_t launch_fwd_decode_paged(const PagedCache& c, const void* q, void* o,
                                     const int* seqlens, void* workspace, int B, int H, int Nq,
                                     int causal, float scale, DeviceStatus* status,
                                     cudaStream_t stream);
+// The forward with keys of their own (fa_fwd_cross.cu), and its workspace.
+cudaError_t launch_fwd_cross(const Shape& s, const void* q, const void* k, const void* v, void* o,
+                             float* lse, void* workspace, DeviceStatus* status,
+                             cudaStream_t stream);
+size_t cross_fwd_workspace_bytes(const Shape& s);
 // The backward at d = 64 with keys of their own, from the preprocess on (fa_bwd_cross.cu):
 // dK/dV and dQ, two launches.
 cudaError_t launch_bwd_cross64(const Shape& s, const void* q, const void* k, const void* v,
                                const void* dout, void* dq, void* dk, void* dv,
                                const BwdWorkspace& ws, DeviceStatus* status, cudaStream_t stream);
+// The same at d = 128: dK/dV, and the sum of dQ, which launch_bwd_dq_convert() then
+// writes (fa_bwd_cross128.cu).
+cudaError_t launch_bwd_cross128(const Shape& s, const void* q, const void* k, const void* v,
+                                const void* dout, void* dk, void* dv, const BwdWorkspace& ws,
+                                DeviceStatus* status, cudaStream_t stream);
 // Paged decoding over contiguous K and V [B][Hkv][Nk][d], kv_lens[b] keys a sequence (null: Nk).
 cudaError_t launch_fwd_cross_decode(const void* q, const void* k, const void* v, void* o,
                                     float* lse, const int* kv_lens, void* workspace, int B, int H,
