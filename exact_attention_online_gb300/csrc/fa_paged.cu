@@ -39,8 +39,9 @@
 // order.  A small call (short table, few pairs) takes no list and no second kernel:
 // a cluster of CTAs shares a pair, and joins its parts through their shared memory.
 //
-// A contiguous K and V [B][Hkv][Nk][d] is a pool of one page a sequence without a table,
-// and goes through the same kernels.
+// A contiguous K and V [B][Hkv][Nk][d] is a pool of one page a sequence without a table.
+// fa_cross_decode.cu compiles this file for that (FA_CONTIGUOUS): asked at run time, it cost
+// the paged calls 0.1 us.
 //
 // Warps: 0-3 (and 8-11) softmax, four warps for a group of query rows, which need
 // nothing of one another; 4 loads K, 7 V, 5 issues MMAs, 6 lays out the queries
@@ -52,6 +53,10 @@
 #include <atomic>
 
 #include "fa_internal.h"
+
+#ifndef FA_CONTIGUOUS
+#define FA_CONTIGUOUS 0
+#endif
 
 namespace fa {
 namespace {
@@ -68,18 +73,20 @@ constexpr int kMaxCluster = 8;          // most CTAs that share a pair without a
 struct PagedParams {
     const __nv_bfloat16* q;             // rows i * R .. of pair i = b * Hkv + g
     const float* scales;
-    const int* table;                   // null: page b is sequence b's
-    const int* seqlens;                 // null: all `limit`
+    const int* table;                   // (contiguous: none)
+    const int* seqlens;                 // (contiguous: or null, all `limit`)
     __nv_bfloat16* o;
     float* lse;
     float* part_o;                      // [slots][R][d]
     float* part_lse;                    // [slots][R], log2
     int B, Hkv, Nq, R, n_pages, ps_shift, max_pages, causal;
-    int limit;                          // most keys of a sequence
     int ctas;                           // of the split kernel; in clusters: of a pair
     float scale_log2;
     DeviceStatus* status;
+    int limit;                          // contiguous: keys of a sequence
 };
+
+constexpr bool kContiguous = FA_CONTIGUOUS;
 
 // Sizes of one variant: head dimension, page type, groups of query rows, and how many
 // rows a group works on (of at least eight; the others are zero).
@@ -148,7 +155,8 @@ struct Cfg {
 };
 
 __device__ __forceinline__ int clamped_len(const PagedParams& p, int b) {
-    return p.seqlens ? min(max(p.seqlens[b], 0), p.limit) : p.limit;
+    if (kContiguous) return p.seqlens ? min(max(p.seqlens[b], 0), p.limit) : p.limit;
+    return min(max(p.seqlens[b], 0), p.max_pages << p.ps_shift);
 }
 __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) / kTile; }
 
@@ -435,8 +443,10 @@ fa_decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
     // The page of lane's segment of the cursor's tile (0 where there is none).
     auto page_of = [&](const Cursor& at) {
         const int key = at.t * kTile + lane * seg;
-        if (at.left <= 0 || lane >= n_seg || key >= at.len) return 0;
-        return p.table ? p.table[(long long)at.b * p.max_pages + (key >> p.ps_shift)] : at.b;
+        if (kContiguous) return at.left > 0 ? at.b : 0;
+        return (at.left > 0 && lane < n_seg && key < at.len)
+                   ? p.table[(long long)at.b * p.max_pages + (key >> p.ps_shift)]
+                   : 0;
     };
 
     if (warp == 4 || warp == 7) {
@@ -1091,7 +1101,8 @@ cudaError_t launch_attend(const CUtensorMap& tk, const CUtensorMap& tv, PagedPar
                           cudaStream_t stream) {
     using C = Cfg<D, F8, G, W>;
     static_assert(C::kSmem + C::kStatic <= 227 * 1024, "shared memory of one CTA");
-    const int longest = (p.limit + kTile - 1) / kTile;         // tiles of a pair
+    const int most_keys = kContiguous ? p.limit : p.max_pages << p.ps_shift;
+    const int longest = (most_keys + kTile - 1) / kTile;                      // tiles of a pair
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -1140,10 +1151,12 @@ size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
 
+#if !FA_CONTIGUOUS
 size_t paged_workspace_bytes(int B, int Hkv, int R, int d) {
     const size_t slots = (size_t)kPagedMaxCtas + (size_t)B * Hkv;
     return align256(slots * R * d * 4) + slots * R * 4;
 }
+#endif
 
 namespace {
 
@@ -1167,15 +1180,18 @@ cudaError_t launch_pool(const CUtensorMap& tk, const CUtensorMap& tv, PagedParam
     p.causal = causal;
     p.scale_log2 = scale * kLog2e;
     p.status = status;
-    if (d == 128)
-        return f8 ? launch_rows<128, true>(tk, tv, p, stream)
-                  : launch_rows<128, false>(tk, tv, p, stream);
-    return f8 ? launch_rows<64, true>(tk, tv, p, stream)
-              : launch_rows<64, false>(tk, tv, p, stream);
+    if constexpr (!kContiguous) {
+        if (f8)
+            return d == 128 ? launch_rows<128, true>(tk, tv, p, stream)
+                            : launch_rows<64, true>(tk, tv, p, stream);
+    }
+    return d == 128 ? launch_rows<128, false>(tk, tv, p, stream)
+                    : launch_rows<64, false>(tk, tv, p, stream);
 }
 
 }  // namespace
 
+#if !FA_CONTIGUOUS
 cudaError_t launch_fwd_decode_paged(const PagedCache& c, const void* q, void* o, float* lse,
                                     const int* seqlens, void* workspace, int B, int H, int Nq,
                                     int causal, float scale, DeviceStatus* status,
@@ -1193,11 +1209,11 @@ cudaError_t launch_fwd_decode_paged(const PagedCache& c, const void* q, void* o,
     p.n_pages = c.n_pages;
     p.ps_shift = c.ps_shift;
     p.max_pages = c.max_pages;
-    p.limit = c.max_pages << c.ps_shift;
     return launch_pool(tk, tv, p, f8, c.d, q, o, lse, workspace, B, H, c.Hkv, Nq, causal, scale,
                        status, stream);
 }
 
+#else
 cudaError_t launch_fwd_cross_decode(const void* q, const void* k, const void* v, void* o,
                                     float* lse, const int* kv_lens, void* workspace, int B, int H,
                                     int Hkv, int Nq, int Nk, int d, int causal, float scale,
@@ -1217,5 +1233,6 @@ cudaError_t launch_fwd_cross_decode(const void* q, const void* k, const void* v,
     return launch_pool(tk, tv, p, false, d, q, o, lse, workspace, B, H, Hkv, Nq, causal, scale,
                        status, stream);
 }
+#endif
 
 }  // namespace fa
