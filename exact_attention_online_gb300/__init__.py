@@ -1006,6 +1006,9 @@ def fa_fwd_cross(q, k, v, o, lse, workspace, causal: bool, scale: float, kv_lens
                  stream=None) -> None:
     """q, o: bf16 [B, H, Nq, d]; k, v: bf16 [B, Hkv, Nk, d]; lse: fp32 [B, H, Nq]; kv_lens:
     int32 [B], the keys of each sequence (default: Nk)."""
+    if _done(binding().cross_forward(q, k, v, o, lse, workspace, causal, scale, kv_lens,
+                                     _handle(stream)), "fa_fwd_cross"):
+        return
     qs, ks, ls, sizes, lens = _cross_dims(q, k, kv_lens)
     wp, wb = _ws(workspace)
     _check(lib().fa_fwd_cross(_bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v", ks), _bf16(o, "o", qs),
@@ -1016,6 +1019,9 @@ def fa_fwd_cross(q, k, v, o, lse, workspace, causal: bool, scale: float, kv_lens
 def fa_bwd_cross(q, k, v, o, dout, lse, dq, dk, dv, workspace, causal: bool, scale: float,
                  kv_lens=None, stream=None) -> None:
     """The gradients of fa_fwd_cross."""
+    if _done(binding().cross_backward(q, k, v, o, dout, lse, dq, dk, dv, workspace, causal, scale,
+                                      kv_lens, _handle(stream)), "fa_bwd_cross"):
+        return
     qs, ks, ls, sizes, lens = _cross_dims(q, k, kv_lens)
     wp, wb = _ws(workspace)
     _check(lib().fa_bwd_cross(_bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v", ks), _bf16(o, "o", qs),
@@ -1028,6 +1034,9 @@ def fa_fwd_cross_varlen(q, k, v, o, lse, workspace, cu_q, cu_k, max_q: int, max_
                         causal: bool, scale: float, stream=None) -> None:
     """Packed: q, o [H, total_q, d], k, v [Hkv, total_k, d], lse [H, total_q]; cu_q, cu_k int32
     [B + 1]."""
+    if _done(binding().cross_forward_varlen(q, k, v, o, lse, workspace, causal, scale, cu_q, cu_k,
+                                            max_q, max_k, _handle(stream)), "fa_fwd_cross_varlen"):
+        return
     qs, ks, ls, sizes, cu = _cross_varlen_dims(q, k, cu_q, cu_k, max_q, max_k)
     wp, wb = _ws(workspace)
     _check(lib().fa_fwd_cross_varlen(_bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v", ks),
@@ -1039,6 +1048,10 @@ def fa_fwd_cross_varlen(q, k, v, o, lse, workspace, cu_q, cu_k, max_q: int, max_
 def fa_bwd_cross_varlen(q, k, v, o, dout, lse, dq, dk, dv, workspace, cu_q, cu_k, max_q: int,
                         max_k: int, causal: bool, scale: float, stream=None) -> None:
     """The gradients of fa_fwd_cross_varlen."""
+    if _done(binding().cross_backward_varlen(q, k, v, o, dout, lse, dq, dk, dv, workspace, causal,
+                                             scale, cu_q, cu_k, max_q, max_k, _handle(stream)),
+             "fa_bwd_cross_varlen"):
+        return
     qs, ks, ls, sizes, cu = _cross_varlen_dims(q, k, cu_q, cu_k, max_q, max_k)
     wp, wb = _ws(workspace)
     _check(lib().fa_bwd_cross_varlen(_bf16(q, "q"), _bf16(k, "k"), _bf16(v, "v", ks),

@@ -267,12 +267,119 @@ PyObject* cross_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// Queries and keys of two lengths, padded or (3-D, with cu_q and cu_k) packed: the tensors
+// that all four calls have.
+struct Cross {
+    const at::Tensor &q, &k, &ws;
+    Device dev;
+    bool packed;
+    int B, H, Hkv, Nq, Nk, d, total_q = 0, total_k = 0;
+    const int *cu_q = nullptr, *cu_k = nullptr, *lens = nullptr;
+    // at: the place of cu_q, cu_k, max_q and max_k (packed), of kv_lens (padded)
+    Cross(PyObject* const* a, int workspace, int at, bool packed_)
+        : q(tensor(a[0])), k(tensor(a[1])), ws(tensor(a[workspace])), dev(q), packed(packed_) {
+        const int n = packed ? 3 : 4;
+        need(q.dim() == n && k.dim() == n && k.size(n - 1) == q.size(n - 1));
+        dev.here(ws);
+        need(ws.is_contiguous());
+        d = size_of(q.size(n - 1));
+        H = size_of(q.size(n - 3));
+        Hkv = size_of(k.size(n - 3));
+        Nq = size_of(q.size(n - 2));
+        Nk = size_of(k.size(n - 2));
+        if (packed) {
+            total_q = Nq;
+            total_k = Nk;
+            const at::Tensor &cq = tensor(a[at]), &ck = tensor(a[at + 1]);
+            need(cq.dim() == 1 && cq.size(0) >= 1);
+            cu_q = (const int*)dev.whole(cq, at::kInt, cq.sizes());
+            cu_k = (const int*)dev.whole(ck, at::kInt, cq.sizes());
+            B = size_of(cq.size(0) - 1);
+            Nq = whole_number(a[at + 2]);
+            Nk = whole_number(a[at + 3]);
+        } else {
+            need(k.size(0) == q.size(0));
+            B = size_of(q.size(0));
+            if (a[at] != Py_None) lens = (const int*)dev.whole(a[at], at::kInt, {q.size(0)});
+        }
+    }
+    void* like_q(PyObject* o) const { return dev.whole(o, at::kBFloat16, q.sizes()); }
+    void* like_k(PyObject* o) const { return dev.whole(o, at::kBFloat16, k.sizes()); }
+    float* rows(PyObject* o) const {
+        return (float*)dev.whole(o, at::kFloat, q.sizes().slice(0, q.dim() - 1));
+    }
+};
+
+// (q, k, v, o, lse, workspace, causal, scale, kv_lens | cu_q, cu_k, max_q, max_k, stream)
+PyObject* forward(PyObject* const* a, Py_ssize_t n, bool packed) {
+    return answer(n, packed ? 13 : 10, [&]() -> long {
+        const Cross c(a, 5, 8, packed);
+        const void *q = c.like_q(a[0]), *k = c.like_k(a[1]), *v = c.like_k(a[2]);
+        void* o = c.like_q(a[3]);
+        float* lse = c.rows(a[4]);
+        const bool causal = truth(a[6]);
+        const float scale = number(a[7]);
+        const fa_stream_t st = stream_of(a[n - 1], c.dev);
+        void* const ws = c.ws.data_ptr();
+        const size_t bytes = c.ws.nbytes();
+        return launched([&] {
+            return packed ? fa_fwd_cross_varlen(q, k, v, o, lse, c.cu_q, c.cu_k, ws, bytes, c.B,
+                                                c.Nq, c.Nk, c.total_q, c.total_k, c.H, c.Hkv, c.d,
+                                                causal, scale, st)
+                          : fa_fwd_cross(q, k, v, o, lse, c.lens, ws, bytes, c.B, c.H, c.Hkv, c.Nq,
+                                         c.Nk, c.d, causal, scale, st);
+        });
+    });
+}
+
+// (q, k, v, o, dout, lse, dq, dk, dv, workspace, causal, scale, as above)
+PyObject* backward(PyObject* const* a, Py_ssize_t n, bool packed) {
+    return answer(n, packed ? 17 : 14, [&]() -> long {
+        const Cross c(a, 9, 12, packed);
+        const void *q = c.like_q(a[0]), *k = c.like_k(a[1]), *v = c.like_k(a[2]);
+        const void *o = c.like_q(a[3]), *dout = c.like_q(a[4]);
+        const float* lse = c.rows(a[5]);
+        void *dq = c.like_q(a[6]), *dk = c.like_k(a[7]), *dv = c.like_k(a[8]);
+        const bool causal = truth(a[10]);
+        const float scale = number(a[11]);
+        const fa_stream_t st = stream_of(a[n - 1], c.dev);
+        void* const ws = c.ws.data_ptr();
+        const size_t bytes = c.ws.nbytes();
+        return launched([&] {
+            return packed ? fa_bwd_cross_varlen(q, k, v, o, dout, lse, dq, dk, dv, c.cu_q, c.cu_k,
+                                                ws, bytes, c.B, c.Nq, c.Nk, c.total_q, c.total_k,
+                                                c.H, c.Hkv, c.d, causal, scale, st)
+                          : fa_bwd_cross(q, k, v, o, dout, lse, dq, dk, dv, c.lens, ws, bytes, c.B,
+                                         c.H, c.Hkv, c.Nq, c.Nk, c.d, causal, scale, st);
+        });
+    });
+}
+
+PyObject* cross_forward(PyObject*, PyObject* const* a, Py_ssize_t n) { return forward(a, n, false); }
+PyObject* cross_forward_varlen(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return forward(a, n, true);
+}
+PyObject* cross_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return backward(a, n, false);
+}
+PyObject* cross_backward_varlen(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return backward(a, n, true);
+}
+
 PyMethodDef methods[] = {
     {"kv_reserve", (PyCFunction)(void (*)(void))kv_reserve, METH_FASTCALL, nullptr},
     {"kv_release", (PyCFunction)(void (*)(void))kv_release, METH_FASTCALL, nullptr},
     {"rope", (PyCFunction)(void (*)(void))rope, METH_FASTCALL, nullptr},
     {"rope_append", (PyCFunction)(void (*)(void))rope_append, METH_FASTCALL, nullptr},
     {"cross_decode", (PyCFunction)(void (*)(void))cross_decode, METH_FASTCALL, nullptr},
+    {"cross_forward", (PyCFunction)(void (*)(void))cross_forward, METH_FASTCALL,
+     nullptr},
+    {"cross_forward_varlen", (PyCFunction)(void (*)(void))cross_forward_varlen, METH_FASTCALL,
+     nullptr},
+    {"cross_backward", (PyCFunction)(void (*)(void))cross_backward, METH_FASTCALL,
+     nullptr},
+    {"cross_backward_varlen", (PyCFunction)(void (*)(void))cross_backward_varlen, METH_FASTCALL,
+     nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "fa_binding", nullptr, -1, methods,

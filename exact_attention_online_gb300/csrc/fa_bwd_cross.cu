@@ -20,7 +20,7 @@
 //   - Sixteen compute warps instead of eight, which wait for one another's latencies
 //     less (171 us with eight, 164.5 with sixteen, on the shape above), and arrive on a
 //     barrier by one lane.
-// On that shape the backward takes 157 us, 198 with the kernel of fa_bwd.cu.  A step takes
+// On that shape the backward takes 151 us, 198 with the kernel of fa_bwd.cu.  A step takes
 // about 4000 cycles.  Its MMAs alone take 1710 (an SS MMA of 128 x 64 x 16 reads 6 KB of
 // shared memory and takes 54 cycles, not 32); the rest is the chain dS^T -> dK, dQ -> dP^T ->
 // dS^T, whose first products wait behind S and dV in the tensor pipe's queue.  dP before
@@ -155,6 +155,10 @@ fa_bwd_cross64_kernel(const __grid_constant__ CUtensorMap tm_q,
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base_sh;
+    pdl_wait();                // the tables
+    // The next kernel's blocks may come in where this one's have ended: its zeros need
+    // nothing of it.
+    pdl_launch_dependents();
 
     // The item of rank n, taken apart by the producer, for a converged warp: false if the
     // wait gave up or there is no more work.
@@ -672,17 +676,18 @@ fa_bwd_cross64_kernel(const __grid_constant__ CUtensorMap tm_q,
 // sequence's keys and those that no query sees (one block of threads each).  Of 16
 // columns the accumulator has 2 b, 2 b + 1, 8 + 2 b, 9 + 2 b at 4 b.
 __global__ void __launch_bounds__(256)
-fa_bwd_cross64_dq_kernel(__nv_bfloat16* __restrict__ dq, long long n_rows, int dq_blocks,
+fa_bwd_cross64_dq_kernel(__nv_bfloat16* __restrict__ dq, long long n_rows,
                          const BwdParams p) {
-    if ((int)blockIdx.x >= dq_blocks) {
-        const int item = (int)blockIdx.x - dq_blocks, n_kblk = (p.Nk + kBN - 1) / kBN;
+    if ((int)blockIdx.x < p.n_items) {
+        const int item = (int)blockIdx.x, n_kblk = (p.Nk + kBN - 1) / kBN;
         const BwdCta c = bwd_cta(p, BR, item / n_kblk, item % n_kblk);
         if (!c.idle && c.n_it > 0) return;
         zero_grads<D>(p, c, c.jblk * kBN + threadIdx.x / 2, threadIdx.x % 2 * 32,
                       threadIdx.x % 2 * 32 + 32, true, true);
         return;
     }
-    const long long t = (long long)blockIdx.x * 256 + threadIdx.x;
+    pdl_wait();
+    const long long t = (long long)(blockIdx.x - p.n_items) * 256 + threadIdx.x;
     const long long r = t / (D / 16);             // of the padded rows
     const int o = (int)(t % (D / 16)) * 16;
     if (r >= n_rows) return;
@@ -740,16 +745,13 @@ cudaError_t launch_bwd_cross64(const Shape& s, const void* q, const void* k, con
     }
     const int sms = device_sm_count() > 0 ? device_sm_count() : 148;
     const int grid = p.n_items < sms ? p.n_items : sms;
-    count_launch();
-    fa_bwd_cross64_kernel<<<grid, kThreads, kSmem, stream>>>(tq, tk, tv, tdo, p);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_pdl(fa_bwd_cross64_kernel, dim3(grid), kThreads, kSmem, 1, stream,
+                                     tq, tk, tv, tdo, p);
     if (e != cudaSuccess) return e;
     const long long rows = (long long)s.B * s.H * p.Np;
-    const int blocks = (int)((rows * (D / 16) + 255) / 256);  // rows * D < 2^31
-    count_launch();
-    fa_bwd_cross64_dq_kernel<<<(unsigned)blocks + p.n_items, 256, 0, stream>>>(
-        static_cast<__nv_bfloat16*>(dq), rows, blocks, p);
-    return cudaGetLastError();
+    const unsigned blocks = (unsigned)((rows * (D / 16) + 255) / 256);  // rows * D < 2^31
+    return launch_pdl(fa_bwd_cross64_dq_kernel, dim3(blocks + p.n_items), 256, 0, 1, stream,
+                      static_cast<__nv_bfloat16*>(dq), rows, p);
 }
 
 }  // namespace fa

@@ -7,8 +7,10 @@
 //   - dQ added to its accumulator from registers, a barrier arrival a warp and MMAs issued by a
 //     predicate of a warp that stays together.
 // A kernel of its own because the dense ones lose 1 % when they are compiled from a shared
-// source.  16 packed pairs of sequences, H32 Hkv8, d = 128: the backward 900 us, of which this
-// pass has about 780, 63 % of the bf16 rate.
+// source.  16 packed pairs of sequences (1 to 4096 keys for 128 to 1024 queries), H32 Hkv8:
+// the backward 865 us, of which this pass has 750, its tensor pipe busy half of the time (52 %
+// of the bf16 rate of 1939 TFLOP/s): a step's chain S -> P -> dP -> dS -> dK, dQ is longer than
+// two steps in flight cover, and shared memory and tensor memory have no room for a third.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -133,6 +135,7 @@ cross_dkdv128_kernel(const __grid_constant__ CUtensorMap tm_q,
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base_sh;
+    pdl_wait();                // the tables
 
     auto arrive = [&](uint64_t* bar) {
         __syncwarp();
@@ -625,9 +628,8 @@ cudaError_t launch_bwd_cross128(const Shape& s, const void* q, const void* k, co
     // Persistent: one CTA per SM, taking items in order from the work counter.
     const int sms = device_sm_count() > 0 ? device_sm_count() : 148;
     const int grid = p.n_items < sms ? p.n_items : sms;
-    count_launch();
-    cross_dkdv128_kernel<<<grid, kThreads, Cfg::kSmemAlloc, stream>>>(tq, tk, tv, tdo, p);
-    return cudaGetLastError();
+    return launch_pdl(cross_dkdv128_kernel, dim3(grid), kThreads, Cfg::kSmemAlloc, 1, stream, tq,
+                      tk, tv, tdo, p);
 }
 
 }  // namespace fa

@@ -4,6 +4,11 @@
 // fa_fwd.cu), with a work list of its own, masks for both lengths, rows of V behind the
 // keys cleared, and the causal mask a run-time flag.  A file and a kernel of its own
 // because the dense kernels lose 1 to 2 % when they are compiled from a shared source.
+// What bounds it: d = 128 the tensor pipe; d = 64 (16 x 16 heads, 400 queries, 100 to 1500
+// keys: 57 us) the softmax: a pair of query tiles and 128 keys take 2200 cycles, of which the
+// MMAs 1136 and the exponentials 1024, and an item 3 key blocks' time more.  Sixteen softmax
+// warps there, two threads a row, took 17 % longer: they have to agree on the row's maximum in
+// every block.
 #include <cuda_bf16.h>
 #include <algorithm>
 #include <cmath>
@@ -101,15 +106,16 @@ __device__ __forceinline__ int key_rows(const CrossParams& p, int b, int& ktok0)
     return p.kv_lens ? min(max(__ldg(p.kv_lens + b), 0), p.Nk) : p.Nk;
 }
 
-// The work is a list of (item, key block): sequences in
-// turn, in each the K/V heads, in each the query-block pairs, in each the query heads that
-// share the K/V head, and the item's key blocks.  Each CTA takes an equal share of that
+// The work is a list of (item, key block): sequences in turn, in each the K/V heads, in each
+// the query-block pairs, in each the query heads that share the K/V head, and the item's key
+// blocks.  Each CTA takes an equal share of that
 // list, whole items or segments of them; an item in segments leaves one partial result
 // each in the workspace (a CTA has two at most: its first and its last item), which
 // cross_join_kernel adds up in the order of the keys.  The lengths are on the device, so
 // that each CTA finds its share itself.  Whole items in rounds leave the GPU idle in the
 // last one and are as long as the longest sequence allows: 2 x 32/8 heads, 1024 queries,
-// 17408 keys, d = 128, causal (256 items on 152 SMs): 437 us, in equal shares 390 to 410.
+// 17408 keys, d = 128, causal (256 items on 152 SMs): 437 us, in equal shares 400 to 420
+// (73 % of the bf16 rate of 1939 TFLOP/s, the power limit at work).
 // Segments pay for the join (a launch, 132 KB written and read each at d = 128): about
 // kJoinCost key blocks, so that cross_ctas() takes them only where an even share is that
 // much shorter; a segment has kMinBlocks blocks at least, and a share that would end
@@ -169,7 +175,11 @@ __device__ __forceinline__ CrossAt cross_place(const CrossParams& p, const Cross
         return at;
     }
     const long long head = G * sq.before(sq.M);
-    const int g = o >> 31 ? (int)(o / head) : (int)((uint32_t)o / (uint32_t)min(head, 0x7fffffffll));
+    // (a 64-bit division only where it takes one)
+    auto over = [](long long x, long long y) -> int {
+        return x < y ? 0 : x >> 31 ? (int)(x / y) : (int)((uint32_t)x / (uint32_t)y);
+    };
+    const int g = over(o, head);
     o -= g * head;
     int m = 0;                          // the last pair with G before(m) <= o
     for (int hi = sq.M; hi - m > 1;) {
@@ -178,9 +188,9 @@ __device__ __forceinline__ CrossAt cross_place(const CrossParams& p, const Cross
         else hi = mid;
     }
     o -= G * sq.before(m);
-    const int n = sq.blocks(m), cost = n + kItemCost, r = (int)o / cost;
+    const int n = sq.blocks(m), cost = n + kItemCost, r = over(o, cost);
     at.it = (g * sq.M + m) * G + r;
-    at.blk = max((int)o - r * cost - kItemCost, 0);
+    at.blk = max((int)(o - (long long)r * cost) - kItemCost, 0);
     if (at.blk <= snap && (p.split || 2 * at.blk < n)) {
         at.blk = 0;
     } else if (n - at.blk <= snap) {

@@ -180,3 +180,37 @@ def test_calls_from_several_threads():
         t.join()
     assert not errors, errors
     assert fa.fa_device_status() == 0
+
+
+def test_cross_calls_with_numbers_of_other_types():
+    q, k, v, dout = padded(2, 4, 2, 64, 70, 300, [300, 200], seed=51)
+    n = i32([300, 200])
+    pq, pk, pv, pd, cu_q, cu_k = packed(4, 2, 128, [100, 60], [700, 90], 0)
+    results = []
+    for flag, scale, mq, mk in ((True, 0.125, 100, 700),
+                                (np.bool_(True), np.float32(0.125), np.int32(100), np.int64(700)),
+                                (1, 0.125, 100, np.int64(700))):
+        o, lse = fa.attention_cross(q, k, v, n, causal=flag, scale=scale)
+        _, dk, dv = fa.attention_cross_backward(q, k, v, o, lse, dout, n, causal=flag, scale=scale)
+        po, pl = fa.attention_cross_varlen(pq, pk, pv, cu_q, cu_k, mq, mk, causal=flag, scale=scale)
+        _, pdk, pdv = fa.attention_cross_varlen_backward(pq, pk, pv, po, pl, pd, cu_q, cu_k, mq, mk,
+                                                         causal=flag, scale=scale)
+        results.append([o, lse, dk, dv, po, pl, pdk, pdv])
+    for other in results[1:]:
+        for a, b in zip(results[0], other):
+            assert torch.equal(a, b)
+    with pytest.raises(ValueError):
+        fa.attention_cross(q, k, v, n.long())
+    with pytest.raises(ValueError):
+        fa.attention_cross(q, k.float(), v, n)
+    with pytest.raises(ValueError):
+        fa.attention_cross_varlen(pq, pk, pv, cu_q, cu_k[:2], 100, 700)
+    o, lse = used(q, q[..., 0].float())
+    ws = torch.empty(fa.fa_fwd_cross_workspace_size(2, 4, 2, 70, 300, 64), dtype=torch.uint8,
+                     device="cuda")
+    with pytest.raises(fa.FAError):
+        fa.fa_fwd_cross(q, k, v, o, lse, ws[:16], True, 0.1, kv_lens=n)
+    with pytest.raises(fa.FAError):
+        fa.fa_fwd_cross(q, k, v, o, lse, ws, True, -1.0, kv_lens=n)
+    torch.cuda.synchronize()
+    assert o.isnan().all()
