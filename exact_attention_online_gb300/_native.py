@@ -27,7 +27,7 @@ BINDING_PATH = os.path.join(OUT_DIR, "fa_binding.so")
 SOURCES = ["api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_noalloc.cu", "fa_fp8.cu", "fa_decode.cu",
            "fa_diag.cu", "fa_kvcache.cu", "fa_paged.cu", "fa_tables.cu", "fa_rope.cu",
            "fa_cross.cu", "fa_fwd_cross.cu", "fa_bwd_cross.cu", "fa_bwd_cross128.cu",
-           "fa_cross_decode.cu"]
+           "fa_bwd_cross_rows.cu", "fa_cross_decode.cu"]
 HEADERS = ["sm103_ptx.cuh", "fa_internal.h", "exp2_poly.h", "bwd_parts.cuh",
            "fa_paged.cu"]   # (fa_cross_decode.cu includes it)
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -938,8 +938,7 @@ __device__ __forceinline__ int seq_row(const int* __restrict__ cu, long long bh,
 // bf16, or fp32 when it comes from the precise forward.  FULL = false (after
 // a training forward, which wrote the -LSE table and zeroed the accumulator):
 // the -D table only.
-// EMPTY: a row may see no key (LSE = -infinity): P = 0 like a padded one's.
-template <int D, typename OT, bool FULL, bool EMPTY = false>
+template <int D, typename OT, bool FULL>
 __global__ void __launch_bounds__(256)
 fa_bwd_pre_kernel(const OT* __restrict__ o, const __nv_bfloat16* __restrict__ dout,
                   const float* __restrict__ lse, uint16_t* __restrict__ lse_ext,
@@ -966,7 +965,6 @@ fa_bwd_pre_kernel(const OT* __restrict__ o, const __nv_bfloat16* __restrict__ do
         const bool used = in && i < (len + kRowPad - 1) / kRowPad * kRowPad;
         float x = -1e30f;
         if (FULL && valid) x = -lse[base + i] * 1.4426950408889634f;
-        if (EMPTY && x == CUDART_INF_F) x = -1e30f;
         float acc = 0.0f;
         if (valid) {
             const long long src = (base + i) * D + sl * 8;
@@ -1725,10 +1723,6 @@ cudaError_t launch_bwd_preprocess(const Shape& s, const void* o, bool o_f32, con
     };
     auto* ob = static_cast<const __nv_bfloat16*>(o);
     auto* of = static_cast<const float*>(o);
-    if (s.Nk > 0)   // keys of another length
-        return o_f32 || !full ? cudaErrorInvalidValue
-               : s.d == 128   ? go(fa_bwd_pre_kernel<128, __nv_bfloat16, true, true>, ob)
-                              : go(fa_bwd_pre_kernel<64, __nv_bfloat16, true, true>, ob);
     if (s.d == 128) {
         if (o_f32)
             return full ? go(fa_bwd_pre_kernel<128, float, true>, of)

@@ -73,12 +73,12 @@ fa_status backward(const Shape& s, const void* q, const void* k, const void* v, 
     if ((st = ready_device(&dev, &status)) != FA_OK) return st;
     const BwdWorkspace ws = bwd_workspace_carve(workspace, s);
     cudaStream_t cs = (cudaStream_t)stream;
-    cudaError_t e = launch_bwd_preprocess(s, o, false, dout, lse, ws, status, cs);
+    cudaError_t e = launch_bwd_cross_pre(s, o, dout, lse, ws, cs);
     if (e == cudaSuccess && s.d == 64) {
         e = launch_bwd_cross64(s, q, k, v, dout, dq, dk, dv, ws, status, cs);
     } else if (e == cudaSuccess) {
         e = launch_bwd_cross128(s, q, k, v, dout, dk, dv, ws, status, cs);
-        if (e == cudaSuccess) e = launch_bwd_dq_convert(s, ws, dq, cs);
+        if (e == cudaSuccess) e = launch_bwd_cross_dq128(s, ws, dq, cs);
     }
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
