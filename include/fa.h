@@ -676,12 +676,16 @@ FA_API fa_status fa_rope_append(const void* q, const void* k, const void* v, voi
  * sequence of n keys sees keys j <= i + n - Nq (fa_fwd()'s rule when n = Nq).  A query
  * that sees no key (no keys, or i + n < Nq) gets O = 0, LSE = -infinity and a dQ of 0;
  * a key that no query sees gets dK = dV = 0, and so do the rows behind kv_lens.  A NaN
- * or an infinity among a sequence's keys may reach all of its queries.
+ * or an infinity among a sequence's keys may reach all of its queries; one in a query
+ * reaches that row alone.
  * d in {64, 128}; H % Hkv == 0; B * H * Nq * d, with Nq rounded up to 128, B * Hkv * Nk
  * * d and B * Hkv * Nk rounded up to 128 below 2^31 (FA_ERR_UNSUPPORTED).  Errors
  * otherwise as fa_fwd() and fa_bwd(); workspace: caller-owned, of the size that the
  * function beside each gives, 256-byte aligned, contents on entry of no matter, one for
- * each call that may overlap on the GPU (FA_ERR_WORKSPACE, FA_ERR_ALIGNMENT).
+ * each call that may overlap on the GPU (FA_ERR_WORKSPACE, FA_ERR_ALIGNMENT).  O and
+ * LSE are the same bit for bit on every call.  Lengths are read on the device, so a
+ * captured call may be replayed with others.  One launch, or two where the keys of
+ * few queries are split over the GPU.
  */
 FA_API size_t fa_fwd_cross_workspace_size(int B, int H, int Hkv, int Nq, int Nk, int d);
 FA_API fa_status fa_fwd_cross(const void* q, const void* k, const void* v, void* o, float* lse,
