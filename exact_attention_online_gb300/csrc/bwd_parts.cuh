@@ -10,6 +10,30 @@ namespace fa {
 
 constexpr int kBwdKeys = 128;   // keys per work item
 
+// Few key blocks leave most SMs without work: then the query blocks of one go to `parts` CTAs,
+// each leaves its dK and dV in fp32, and the last kernel adds these in order.  Where at most
+// half of the SMs have a key block and there are steps to share (a head of 3737 queries, GQA 4,
+// to 251 keys, 16 key blocks, d = 128: 292 us with one part, 97 so).
+constexpr int kPartCtas = 152;
+
+inline int bwd_step_rows(const Shape& s) { return s.d == 64 ? 128 : 64; }
+inline long long bwd_key_blocks(const Shape& s) {
+    return (long long)((s.Nk + kBwdKeys - 1) / kBwdKeys) * s.B * s.Hkv;
+}
+inline int bwd_parts(const Shape& s) {
+    const long long base = bwd_key_blocks(s), n = (s.N + bwd_step_rows(s) - 1) / bwd_step_rows(s);
+    if (2 * base > kPartCtas || n * (s.H / s.Hkv) < 8) return 1;
+    return (int)(n < kPartCtas / base ? n : kPartCtas / base);
+}
+// The parts' memory, behind bwd_workspace_bytes(); the most that any call of these sizes takes.
+inline size_t bwd_part_bytes(const Shape& s) {
+    const long long base = bwd_key_blocks(s);
+    if (2 * base > kPartCtas) return 0;
+    const long long n =
+        (long long)(s.N + bwd_step_rows(s) - 1) / bwd_step_rows(s) * (s.H / s.Hkv) * base;
+    return (size_t)(n < kPartCtas ? n : kPartCtas) * 2 * kBwdKeys * s.d * sizeof(float);
+}
+
 struct BwdParams {
     int H, Hkv, N, Np, G, causal;
     int rows;                         // rows per head of q: N, or the packed total
@@ -27,7 +51,9 @@ struct BwdParams {
     const uint16_t* d_ext;
     float* dq_acc;
     int* work;                        // next work item (zero on entry, left zero)
-    int n_bg, n_items;                // B * Hkv; work items (B * Hkv * key blocks)
+    int n_bg, n_base, n_items;        // B * Hkv; key blocks; work items (key blocks * parts)
+    int parts;
+    float* part;                      // [key block][parts][dK, dV][128 keys][d]
     __nv_bfloat16* dk;
     __nv_bfloat16* dv;
     DeviceStatus* status;
@@ -56,7 +82,10 @@ inline BwdParams bwd_params(const Shape& s, void* dk, void* dv, const BwdWorkspa
     p.dq_acc = ws.dq_acc;
     p.work = ws.work;
     p.n_bg = s.B * s.Hkv;
-    p.n_items = (s.Nk + kBwdKeys - 1) / kBwdKeys * p.n_bg;
+    p.n_base = (int)bwd_key_blocks(s);
+    p.parts = bwd_parts(s);
+    p.n_items = p.n_base * p.parts;
+    p.part = reinterpret_cast<float*>(reinterpret_cast<char*>(ws.lse_ext) + bwd_workspace_bytes(s));
     p.dk = static_cast<__nv_bfloat16*>(dk);
     p.dv = static_cast<__nv_bfloat16*>(dv);
     p.status = status;
@@ -64,15 +93,18 @@ inline BwdParams bwd_params(const Shape& s, void* dk, void* dv, const BwdWorkspa
 }
 
 // What one dK/dV work item covers: kv head bg = b * Hkv + g, key block jblk, and the range of
-// query blocks (of br rows) that see some key of the block.
+// query blocks (of br rows) that see some key of the block, or part `part` of that range.
 struct BwdCta {
     int jblk, b, g, bg, z_kv, i_start, n_i, n_it;
     int tok0, q_len;     // first query row of the sequence in its head, and their number
     int ktok0, seq_len;  // the same of its keys
     int off;             // query i sees keys j <= i + off under the causal mask
-    bool idle;           // a key block past its sequence's end: nothing to do
+    int part;
+    bool idle;           // a key block that no query sees, or past its sequence's end
 };
-__device__ __forceinline__ BwdCta bwd_cta(const BwdParams& p, int br, int bg, int jblk) {
+// (PARTS: p.parts > 1.  A switch of the kernels too, which lose 3 to 5 % when asked at run time.)
+template <bool PARTS>
+__device__ __forceinline__ BwdCta bwd_cta(const BwdParams& p, int br, int bg, int jblk, int part) {
     BwdCta c;
     const bool packed = p.cu_seqlens != nullptr;
     c.bg = bg;
@@ -85,13 +117,26 @@ __device__ __forceinline__ BwdCta bwd_cta(const BwdParams& p, int br, int bg, in
                 : p.kv_lens ? min(max(__ldg(p.kv_lens + c.b), 0), p.Nk)
                             : p.Nk;
     c.off = c.seq_len - c.q_len;
-    c.idle = jblk * kBwdKeys >= c.seq_len;
     c.z_kv = packed ? c.g : bg;
     const int n_qblk = (c.q_len + br - 1) / br;
     c.i_start = p.causal ? max(0, jblk * kBwdKeys - c.off) / br : 0;
     c.n_i = max(0, n_qblk - c.i_start);
+    c.idle = jblk * kBwdKeys >= c.seq_len || c.n_i == 0;
+    c.part = part;
+    if (PARTS) {
+        const int from = c.n_i * part / p.parts;
+        c.n_i = c.n_i * (part + 1) / p.parts - from;
+        c.i_start += from;
+    }
     c.n_it = p.G * c.n_i;
     return c;
+}
+
+template <bool PARTS>
+__device__ __forceinline__ BwdCta bwd_item(const BwdParams& p, int br, int item) {
+    const int n_kblk = (p.Nk + kBwdKeys - 1) / kBwdKeys, block = PARTS ? item / p.parts : item;
+    return bwd_cta<PARTS>(p, br, block / n_kblk, block % n_kblk,
+                          PARTS ? item - block * p.parts : 0);
 }
 
 // The constant A operand of the extension MMAs, 128 key rows x 16 columns:
@@ -132,6 +177,47 @@ __device__ __forceinline__ void clear_rows(uint8_t* tile, int chunks, int rows, 
             for (int u = 0; u < 8; ++u)
                 *reinterpret_cast<uint4*>(tile + c * (rows * 128) + r * 128 + u * 16) =
                     make_uint4(0u, 0u, 0u, 0u);
+}
+
+// Where part c.part of a key block leaves dK (which = 0) or dV: [128 keys][d].
+template <int D>
+__device__ __forceinline__ float* part_rows(const BwdParams& p, const BwdCta& c, int which) {
+    const int n_kblk = (p.Nk + kBwdKeys - 1) / kBwdKeys;
+    const size_t slot = ((size_t)c.bg * n_kblk + c.jblk) * p.parts + c.part;
+    return p.part + (slot * 2 + which) * (kBwdKeys * D);
+}
+
+// The parts of four keys of one key block added, in order, by a block of 256 threads; blocks
+// 0 .. kJoinBlocks n_base - 1.
+constexpr int kJoinBlocks = kBwdKeys / 4;
+
+template <int D>
+__device__ __forceinline__ void join_parts(const BwdParams& p, int br, int block) {
+    const int n_kblk = (p.Nk + kBwdKeys - 1) / kBwdKeys, base = block / kJoinBlocks;
+    BwdCta c = bwd_cta<false>(p, br, base / n_kblk, base % n_kblk, 0);
+    if (c.idle || threadIdx.x >= 2 * D) return;   // (idle: zeros, written elsewhere)
+    const int which = threadIdx.x / D, at = threadIdx.x % D;
+    const int row = block % kJoinBlocks * 4 + at / (D / 4), col = at % (D / 4) * 4;
+    const int key = c.jblk * kBwdKeys + row;
+    if (key >= (p.cu_seqlens ? c.seq_len : p.Nk)) return;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (key < c.seq_len) {
+        const float* const from = part_rows<D>(p, c, which) + row * D + col;
+#pragma unroll 8
+        for (int s = 0; s < p.parts; ++s) {
+            // (a range of fewer blocks than parts has empty ones)
+            if (c.n_i < p.parts && c.n_i * s / p.parts == c.n_i * (s + 1) / p.parts) continue;
+            const float4 v =
+                *reinterpret_cast<const float4*>(from + (size_t)s * (2 * kBwdKeys * D));
+            sum.x += v.x;
+            sum.y += v.y;
+            sum.z += v.z;
+            sum.w += v.w;
+        }
+    }
+    const size_t to = ((size_t)c.z_kv * p.krows + c.ktok0 + key) * D + col;
+    *reinterpret_cast<uint2*>((which ? p.dv : p.dk) + to) =
+        make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
 }
 
 // Zeros in dK and dV (columns [c_lo, c_hi) of this thread's key row) of a key block that

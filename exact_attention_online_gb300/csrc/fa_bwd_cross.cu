@@ -90,6 +90,7 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int si
     return __all_sync(0xffffffffu, wait(bar, parity, site, abort));
 }
 
+template <bool PARTS>
 __global__ void __launch_bounds__(kThreads, 1)
 fa_bwd_cross64_kernel(const __grid_constant__ CUtensorMap tm_q,
                       const __grid_constant__ CUtensorMap tm_k,
@@ -204,6 +205,16 @@ fa_bwd_cross64_kernel(const __grid_constant__ CUtensorMap tm_q,
             tmem_ld_wait(r);
             tc_fence_before();
             arrive_warp(&bar_acc_free);
+            if (PARTS) {                     // (rows_of: this warp's, of the part)
+                float4* const to = reinterpret_cast<float4*>(rows_of) + lane * (D / 4) + u0 * 2;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    to[e] = make_float4(__uint_as_float(r[4 * e + 0]) * mul,
+                                        __uint_as_float(r[4 * e + 1]) * mul,
+                                        __uint_as_float(r[4 * e + 2]) * mul,
+                                        __uint_as_float(r[4 * e + 3]) * mul);
+                return true;
+            }
             const bool there = lane < rows_there;
 #pragma unroll
             for (int e = 0; e < 16; ++e)
@@ -215,6 +226,7 @@ fa_bwd_cross64_kernel(const __grid_constant__ CUtensorMap tm_q,
         // Four lanes exchange their rows' 16-byte units, so that they store a row's 64 bytes
         // together (a row a thread took 3200 cycles an item).
         auto store_rows = [&]() {
+            if (PARTS) return;
 #pragma unroll
             for (int x = 1; x < 4; x <<= 1)
 #pragma unroll
@@ -322,6 +334,8 @@ fa_bwd_cross64_kernel(const __grid_constant__ CUtensorMap tm_q,
             rows_in = packed ? rows_there : min(32, p.Nk - key0);
             rows_of = reinterpret_cast<uint4*>(
                 (cg > 1 ? p.dv : p.dk) + ((size_t)cta.z_kv * p.krows + cta.ktok0 + key0) * D);
+            if (PARTS)
+                rows_of = reinterpret_cast<uint4*>(part_rows<D>(p, cta, cg >> 1) + quarter * 32 * D);
             pending = true;
             ++nb;
         }
@@ -379,7 +393,7 @@ fa_bwd_cross64_kernel(const __grid_constant__ CUtensorMap tm_q,
             // Work items: the key blocks that have keys and queries, listed by sequence
             // (in a batch too large for the list, all of them, and the empty ones are
             // passed over).  A CTA asks for the next number an item ahead.
-            const int n_kblk = (p.Nk + kBN - 1) / kBN, B = p.n_bg / p.Hkv;
+            const int B = p.n_bg / p.Hkv;
             const bool listed = B <= kListSeqs;
             int n_work = p.n_items;
             if (listed) {
@@ -387,8 +401,9 @@ fa_bwd_cross64_kernel(const __grid_constant__ CUtensorMap tm_q,
                 int mine = 0;
 #pragma unroll 1
                 for (int b = b0; b < b1; ++b) {
-                    const BwdCta c = bwd_cta(p, BR, b * p.Hkv, 0);
-                    if (c.q_len > 0) mine += (c.seq_len + kBN - 1) / kBN * p.Hkv;
+                    const BwdCta c = bwd_cta<PARTS>(p, BR, b * p.Hkv, 0, 0);
+                    if (c.q_len > 0)
+                        mine += (c.seq_len + kBN - 1) / kBN * p.Hkv * (PARTS ? p.parts : 1);
                     list_sh[b + 1] = mine;
                 }
                 int upto = mine;
@@ -435,9 +450,11 @@ fa_bwd_cross64_kernel(const __grid_constant__ CUtensorMap tm_q,
                             }
                             const int blocks = (list_sh[lo + 1] - list_sh[lo]) / p.Hkv;
                             const int at = old - list_sh[lo], g = at / blocks;
-                            to = bwd_cta(p, BR, lo * p.Hkv + g, at - g * blocks);
+                            const int j = at - g * blocks;
+                            to = PARTS ? bwd_cta<PARTS>(p, BR, lo * p.Hkv + g, j / p.parts, j % p.parts)
+                                       : bwd_cta<PARTS>(p, BR, lo * p.Hkv + g, j, 0);
                         } else {
-                            to = bwd_cta(p, BR, old / n_kblk, old % n_kblk);
+                            to = bwd_item<PARTS>(p, BR, old);
                         }
                     } while (to.idle || to.n_it == 0);
                     item_sh[nb & 1] = to;
@@ -678,16 +695,22 @@ fa_bwd_cross64_kernel(const __grid_constant__ CUtensorMap tm_q,
 __global__ void __launch_bounds__(256)
 fa_bwd_cross64_dq_kernel(__nv_bfloat16* __restrict__ dq, long long n_rows,
                          const BwdParams p) {
-    if ((int)blockIdx.x < p.n_items) {
-        const int item = (int)blockIdx.x, n_kblk = (p.Nk + kBN - 1) / kBN;
-        const BwdCta c = bwd_cta(p, BR, item / n_kblk, item % n_kblk);
-        if (!c.idle && c.n_it > 0) return;
+    if ((int)blockIdx.x < p.n_base) {
+        const int n_kblk = (p.Nk + kBN - 1) / kBN;
+        const BwdCta c =
+            bwd_cta<false>(p, BR, (int)blockIdx.x / n_kblk, (int)blockIdx.x % n_kblk, 0);
+        if (!c.idle) return;
         zero_grads<D>(p, c, c.jblk * kBN + threadIdx.x / 2, threadIdx.x % 2 * 32,
                       threadIdx.x % 2 * 32 + 32, true, true);
         return;
     }
     pdl_wait();
-    const long long t = (long long)(blockIdx.x - p.n_items) * 256 + threadIdx.x;
+    const int joins = p.parts > 1 ? kJoinBlocks * p.n_base : 0, at = (int)blockIdx.x - p.n_base;
+    if (at < joins) {
+        join_parts<D>(p, BR, at);
+        return;
+    }
+    const long long t = (long long)(at - joins) * 256 + threadIdx.x;
     const long long r = t / (D / 16);             // of the padded rows
     const int o = (int)(t % (D / 16)) * 16;
     if (r >= n_rows) return;
@@ -716,6 +739,30 @@ fa_bwd_cross64_dq_kernel(__nv_bfloat16* __restrict__ dq, long long n_rows,
 
 }  // namespace
 
+template <bool PARTS>
+static cudaError_t launch_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                            const CUtensorMap& tdo, const BwdParams& p, cudaStream_t stream) {
+    static int configured_device = -1;   // the attribute is per device; cheap to repeat
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (configured_device != dev) {
+        // The register split must fit in what the launch provides, or the
+        // setmaxnreg.inc of the compute warps would wait forever.
+        cudaFuncAttributes attr;
+        cudaError_t e = cudaFuncGetAttributes(&attr, fa_bwd_cross64_kernel<PARTS>);
+        if (e != cudaSuccess) return e;
+        if (attr.numRegs * kThreads < kRegsNeeded) return cudaErrorInvalidConfiguration;
+        e = cudaFuncSetAttribute(fa_bwd_cross64_kernel<PARTS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kSmem);
+        if (e != cudaSuccess) return e;
+        configured_device = dev;
+    }
+    const int sms = device_sm_count() > 0 ? device_sm_count() : 148;
+    const int grid = p.n_items < sms ? p.n_items : sms;
+    return launch_pdl(fa_bwd_cross64_kernel<PARTS>, dim3(grid), kThreads, kSmem, 1, stream, tq, tk, tv,
+                      tdo, p);
+}
+
 cudaError_t launch_bwd_cross64(const Shape& s, const void* q, const void* k, const void* v,
                                const void* dout, void* dq, void* dk, void* dv,
                                const BwdWorkspace& ws, DeviceStatus* status, cudaStream_t stream) {
@@ -728,29 +775,13 @@ cudaError_t launch_bwd_cross64(const Shape& s, const void* q, const void* k, con
         !make_tmap_bf16_3d(&tk, k, D, p.krows, zk, kBN) ||
         !make_tmap_bf16_3d(&tv, v, D, p.krows, zk, kBN))
         return cudaErrorInvalidValue;
-    static int configured_device = -1;   // the attribute is per device; cheap to repeat
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (configured_device != dev) {
-        // The register split must fit in what the launch provides, or the
-        // setmaxnreg.inc of the compute warps would wait forever.
-        cudaFuncAttributes attr;
-        cudaError_t e = cudaFuncGetAttributes(&attr, fa_bwd_cross64_kernel);
-        if (e != cudaSuccess) return e;
-        if (attr.numRegs * kThreads < kRegsNeeded) return cudaErrorInvalidConfiguration;
-        e = cudaFuncSetAttribute(fa_bwd_cross64_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kSmem);
-        if (e != cudaSuccess) return e;
-        configured_device = dev;
-    }
-    const int sms = device_sm_count() > 0 ? device_sm_count() : 148;
-    const int grid = p.n_items < sms ? p.n_items : sms;
-    const cudaError_t e = launch_pdl(fa_bwd_cross64_kernel, dim3(grid), kThreads, kSmem, 1, stream,
-                                     tq, tk, tv, tdo, p);
+    const cudaError_t e = p.parts > 1 ? launch_t<true>(tq, tk, tv, tdo, p, stream)
+                                      : launch_t<false>(tq, tk, tv, tdo, p, stream);
     if (e != cudaSuccess) return e;
     const long long rows = (long long)s.B * s.H * p.Np;
     const unsigned blocks = (unsigned)((rows * (D / 16) + 255) / 256);  // rows * D < 2^31
-    return launch_pdl(fa_bwd_cross64_dq_kernel, dim3(blocks + p.n_items), 256, 0, 1, stream,
+    return launch_pdl(fa_bwd_cross64_dq_kernel, dim3(blocks + p.n_base * (p.parts > 1 ? 1 + kJoinBlocks : 1)),
+                      256, 0, 1, stream,
                       static_cast<__nv_bfloat16*>(dq), rows, p);
 }
 

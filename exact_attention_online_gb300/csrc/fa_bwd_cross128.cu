@@ -59,6 +59,7 @@ struct Cross2Cfg {
 };
 static_assert(Cross2Cfg::kSmemAlloc <= 227 * 1024 - 1024, "shared memory");
 
+template <bool PARTS>
 __global__ void __launch_bounds__(kThreads, 1)
 cross_dkdv128_kernel(const __grid_constant__ CUtensorMap tm_q,
                      const __grid_constant__ CUtensorMap tm_k,
@@ -97,8 +98,6 @@ cross_dkdv128_kernel(const __grid_constant__ CUtensorMap tm_q,
     uint8_t* sDS = smem + Cfg::kOffDS;
     uint8_t* sOnes = smem + Cfg::kOffOnes;
     uint8_t* sExt = smem + Cfg::kOffExt;      // stage st: lse at 2 st, d at 2 st + 1
-
-    const int n_kblk = (p.Nk + kBN - 1) / kBN;
 
     bwd_fill_ones(sOnes, p.scale_log2);
 
@@ -166,11 +165,10 @@ cross_dkdv128_kernel(const __grid_constant__ CUtensorMap tm_q,
         for (int n = 0; ok; ++n) {
             int item;
             if (!next_item(n, item) || item < 0) break;
-            const BwdCta cta = bwd_cta(p, BR, item / n_kblk, item % n_kblk);
-            if (cta.idle || cta.n_it == 0) {
+            const BwdCta cta = bwd_item<PARTS>(p, BR, item);
+            if (cta.idle && (!PARTS || cta.part == 0))
                 zero_grads<D>(p, cta, cta.jblk * kBN + rl, 0, D, !cp, cp);
-                continue;
-            }
+            if (cta.idle || cta.n_it == 0) continue;
             const int jblk = cta.jblk, seq_len = cta.seq_len, z_kv = cta.z_kv;
             const int i_start = cta.i_start, n_i = cta.n_i, n_it = cta.n_it;
             const int key = jblk * kBN + rl;
@@ -284,6 +282,17 @@ cross_dkdv128_kernel(const __grid_constant__ CUtensorMap tm_q,
                     uint32_t r[32];
                     tmem_ld32(lane_addr + col + c0, r);
                     tmem_ld_wait(r);
+                    if (PARTS) {
+                        float4* const to =
+                            reinterpret_cast<float4*>(part_rows<D>(p, cta, cp) + rl * D + c0);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            to[e] = make_float4(__uint_as_float(r[4 * e + 0]) * mul,
+                                                __uint_as_float(r[4 * e + 1]) * mul,
+                                                __uint_as_float(r[4 * e + 2]) * mul,
+                                                __uint_as_float(r[4 * e + 3]) * mul);
+                        continue;
+                    }
                     if (!there)
 #pragma unroll
                         for (int e = 0; e < 32; ++e) r[e] = 0u;
@@ -325,7 +334,7 @@ cross_dkdv128_kernel(const __grid_constant__ CUtensorMap tm_q,
         for (int n = 0; ok; ++n) {
             int item;
             if (!next_item(n, item) || item < 0) break;
-            const BwdCta cta = bwd_cta(p, BR, item / n_kblk, item % n_kblk);
+            const BwdCta cta = bwd_item<PARTS>(p, BR, item);
             if (cta.idle || cta.n_it == 0) continue;
             const int b = cta.b, g = cta.g, i_start = cta.i_start, n_i = cta.n_i, n_it = cta.n_it;
             for (int it = 0; ok && it < n_it; ++it) {
@@ -373,7 +382,7 @@ cross_dkdv128_kernel(const __grid_constant__ CUtensorMap tm_q,
                     item_sh[slot] = item;
                     mbar_arrive(&bar_item_full[slot]);
                     if (item < 0) break;
-                    const BwdCta cta = bwd_cta(p, BR, item / n_kblk, item % n_kblk);
+                    const BwdCta cta = bwd_item<PARTS>(p, BR, item);
                     if (cta.idle || cta.n_it == 0) continue;
                     const int jblk = cta.jblk, b = cta.b, g = cta.g, tok0 = cta.tok0;
                     const int z_kv = cta.z_kv, i_start = cta.i_start, n_i = cta.n_i;
@@ -461,7 +470,7 @@ cross_dkdv128_kernel(const __grid_constant__ CUtensorMap tm_q,
                 int item;
                 if (!next_item(n, item)) { ok = false; break; }
                 if (item < 0) break;
-                const BwdCta cta = bwd_cta(p, BR, item / n_kblk, item % n_kblk);
+                const BwdCta cta = bwd_item<PARTS>(p, BR, item);
                 if (cta.idle || cta.n_it == 0) continue;
                 const int n_it = cta.n_it;
                 // Every per-item phase is waited on by both issuers, whether
@@ -567,7 +576,7 @@ cross_dkdv128_kernel(const __grid_constant__ CUtensorMap tm_q,
             for (int n = 0; ok; ++n) {
                 int item;
                 if (!next_item(n, item) || item < 0) break;
-                const BwdCta cta = bwd_cta(p, BR, item / n_kblk, item % n_kblk);
+                const BwdCta cta = bwd_item<PARTS>(p, BR, item);
                 if (cta.idle || cta.n_it == 0) continue;
                 for (int it = 0; it < cta.n_it; ++it) {
                     const int git = gi + it;
@@ -600,6 +609,30 @@ cross_dkdv128_kernel(const __grid_constant__ CUtensorMap tm_q,
 
 }  // namespace
 
+template <bool PARTS>
+static cudaError_t launch_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                            const CUtensorMap& tdo, const BwdParams& p, cudaStream_t stream) {
+    using Cfg = Cross2Cfg;
+    static int configured_device = -1;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (configured_device != dev) {
+        cudaFuncAttributes attr;
+        cudaError_t e = cudaFuncGetAttributes(&attr, cross_dkdv128_kernel<PARTS>);
+        if (e != cudaSuccess) return e;
+        if (attr.numRegs * kThreads < kRegsNeeded) return cudaErrorInvalidConfiguration;
+        e = cudaFuncSetAttribute(cross_dkdv128_kernel<PARTS>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmemAlloc);
+        if (e != cudaSuccess) return e;
+        configured_device = dev;
+    }
+    // Persistent: one CTA per SM, taking items in order from the work counter.
+    const int sms = device_sm_count() > 0 ? device_sm_count() : 148;
+    const int grid = p.n_items < sms ? p.n_items : sms;
+    return launch_pdl(cross_dkdv128_kernel<PARTS>, dim3(grid), kThreads, Cfg::kSmemAlloc, 1,
+                      stream, tq, tk, tv, tdo, p);
+}
+
 cudaError_t launch_bwd_cross128(const Shape& s, const void* q, const void* k, const void* v,
                                 const void* dout, void* dk, void* dv, const BwdWorkspace& ws,
                                 DeviceStatus* status, cudaStream_t stream) {
@@ -613,24 +646,8 @@ cudaError_t launch_bwd_cross128(const Shape& s, const void* q, const void* k, co
         !make_tmap_bf16_3d(&tk, k, s.d, p.krows, zkv, kBN) ||
         !make_tmap_bf16_3d(&tv, v, s.d, p.krows, zkv, kBN))
         return cudaErrorInvalidValue;
-    static int configured_device = -1;
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (configured_device != dev) {
-        cudaFuncAttributes attr;
-        cudaError_t e = cudaFuncGetAttributes(&attr, cross_dkdv128_kernel);
-        if (e != cudaSuccess) return e;
-        if (attr.numRegs * kThreads < kRegsNeeded) return cudaErrorInvalidConfiguration;
-        e = cudaFuncSetAttribute(cross_dkdv128_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 Cfg::kSmemAlloc);
-        if (e != cudaSuccess) return e;
-        configured_device = dev;
-    }
-    // Persistent: one CTA per SM, taking items in order from the work counter.
-    const int sms = device_sm_count() > 0 ? device_sm_count() : 148;
-    const int grid = p.n_items < sms ? p.n_items : sms;
-    return launch_pdl(cross_dkdv128_kernel, dim3(grid), kThreads, Cfg::kSmemAlloc, 1, stream, tq,
-                      tk, tv, tdo, p);
+    return p.parts > 1 ? launch_t<true>(tq, tk, tv, tdo, p, stream)
+                       : launch_t<false>(tq, tk, tv, tdo, p, stream);
 }
 
 }  // namespace fa

@@ -93,8 +93,13 @@ __global__ void __launch_bounds__(256)
 cross_dq128_kernel(__nv_bfloat16* __restrict__ dq, const BwdParams p) {
     constexpr int D = 128, kRows = 8 * kPasses;
     pdl_wait();
-    const int n_blk = p.Np / kRows, bh = (int)blockIdx.x / n_blk;
-    const int r0 = ((int)blockIdx.x - bh * n_blk) * kRows;
+    const int joins = p.parts > 1 ? kJoinBlocks * p.n_base : 0;
+    if ((int)blockIdx.x < joins) {
+        join_parts<D>(p, 64, blockIdx.x);
+        return;
+    }
+    const int n_blk = p.Np / kRows, at = (int)blockIdx.x - joins, bh = at / n_blk;
+    const int r0 = (at - bh * n_blk) * kRows;
     long long base;
     const int len = query_rows(p, bh, base);
     const float4* const src =
@@ -115,6 +120,10 @@ cross_dq128_kernel(__nv_bfloat16* __restrict__ dq, const BwdParams p) {
 
 }  // namespace
 
+size_t cross_bwd_workspace_bytes(const Shape& s) {
+    return bwd_workspace_bytes(s) + bwd_part_bytes(s);
+}
+
 cudaError_t launch_bwd_cross_pre(const Shape& s, const void* o, const void* dout, const float* lse,
                                  const BwdWorkspace& ws, cudaStream_t stream) {
     const BwdParams p = bwd_params(s, nullptr, nullptr, ws, nullptr);
@@ -129,10 +138,11 @@ cudaError_t launch_bwd_cross_pre(const Shape& s, const void* o, const void* dout
     return cudaGetLastError();
 }
 
-cudaError_t launch_bwd_cross_dq128(const Shape& s, const BwdWorkspace& ws, void* dq,
-                                   cudaStream_t stream) {
-    const BwdParams p = bwd_params(s, nullptr, nullptr, ws, nullptr);
-    const unsigned grid = (unsigned)((long long)s.B * s.H * p.Np / (8 * kPasses));
+cudaError_t launch_bwd_cross_dq128(const Shape& s, const BwdWorkspace& ws, void* dq, void* dk,
+                                   void* dv, cudaStream_t stream) {
+    const BwdParams p = bwd_params(s, dk, dv, ws, nullptr);
+    const unsigned grid = (unsigned)((long long)s.B * s.H * p.Np / (8 * kPasses)) +
+                          (p.parts > 1 ? kJoinBlocks * p.n_base : 0);
     return launch_pdl(cross_dq128_kernel, dim3(grid), 256, 0, 1, stream,
                       static_cast<__nv_bfloat16*>(dq), p);
 }

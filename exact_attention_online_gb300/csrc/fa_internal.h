@@ -216,8 +216,9 @@ cudaError_t launch_bwd_cross64(const Shape& s, const void* q, const void* k, con
 // Its tables and zeroed accumulator, and at d = 128 the end of dQ (fa_bwd_cross_rows.cu).
 cudaError_t launch_bwd_cross_pre(const Shape& s, const void* o, const void* dout, const float* lse,
                                  const BwdWorkspace& ws, cudaStream_t stream);
-cudaError_t launch_bwd_cross_dq128(const Shape& s, const BwdWorkspace& ws, void* dq,
-                                   cudaStream_t stream);
+cudaError_t launch_bwd_cross_dq128(const Shape& s, const BwdWorkspace& ws, void* dq, void* dk,
+                                   void* dv, cudaStream_t stream);
+size_t cross_bwd_workspace_bytes(const Shape& s);
 // dK/dV and the sum of dQ at d = 128 (fa_bwd_cross128.cu).
 cudaError_t launch_bwd_cross128(const Shape& s, const void* q, const void* k, const void* v,
                                 const void* dout, void* dk, void* dv, const BwdWorkspace& ws,
