@@ -64,7 +64,11 @@ struct CrossAt {
 };
 
 struct CrossParams {
-    int H, Hkv, N, BH, n_items, causal;
+    int H, Hkv, N, n_items, causal;
+    // A query tile has 2^row_log rows of each of `group` neighbouring heads: all 128 of one
+    // head, or, where a group's heads (of short sequences) fit into two tiles, of all of them.
+    int group, row_log;
+    int B, G, heads;                  // G: of group heads each, a K/V head's; heads: all of those
     // Padded: rows = N query rows a head.  Packed: sequence b is rows cu_seqlens[b] ..
     // cu_seqlens[b + 1] - 1 of every head, at most N of them.
     int rows;
@@ -131,9 +135,10 @@ constexpr int kMaxCtas = 152;     // the workspace has places for that many
 // The items of sequence b, and the key blocks of each.
 struct CrossSeq {
     int tok0, len, ktok0, klen;
-    int M, n;         // query-block pairs; key blocks
+    int M, n;         // query-block pairs (one at most with several heads a tile); key blocks
     int q;            // causal: pair m sees 2 (m + 1) + q of them
     bool causal;
+    bool all;         // the one pair's last row is the sequence's, and sees all keys
 
     __device__ __forceinline__ CrossSeq(const CrossParams& p, int b, bool causal_) {
         if (p.cu_seqlens) {
@@ -144,17 +149,18 @@ struct CrossSeq {
         }
         klen = key_rows(p, b, ktok0);
         causal = causal_;
-        M = (len + kItemRows - 1) / kItemRows;
+        M = (len + (2 << p.row_log) - 1) >> (p.row_log + 1);
+        all = p.group > 1;
         n = max(1, (klen + kBN - 1) / kBN);
         q = (klen - len + kBN - 1) >> 7;   // rounds down for negative ones too
     }
     __device__ __forceinline__ int blocks(int m) const {
-        return causal ? min(max(2 * (m + 1) + q, 1), n) : n;
+        return causal && !all ? min(max(2 * (m + 1) + q, 1), n) : n;
     }
     // Cost of pairs 0 .. m - 1, key blocks and kItemCost each: pairs below m1 have one
     // block, those from m2 on all n.
     __device__ __forceinline__ long long before(int m) const {
-        if (!causal) return (long long)m * (n + kItemCost);
+        if (!causal || all) return (long long)m * (n + kItemCost);
         const int m1 = min(max((1 - q) >> 1, 0), m);
         const int m2 = min(max((n - q) >> 1, m1), m);
         const long long mid = m2 - m1;
@@ -166,7 +172,7 @@ static_assert(kBN == 128 && kBM == 128 && kTiles == 2, "CrossSeq counts in these
 // First block of CTA c's share: block t of the list, which lies in sequence b at o.
 __device__ __forceinline__ CrossAt cross_place(const CrossParams& p, const CrossSeq& sq, int b,
                                                long long o, bool unit, int snap) {
-    const int G = p.H / p.Hkv;
+    const int G = p.G;
     CrossAt at;
     at.b = b;
     if (unit) {   // every item counts as one
@@ -195,7 +201,7 @@ __device__ __forceinline__ CrossAt cross_place(const CrossParams& p, const Cross
         at.blk = 0;
     } else if (n - at.blk <= snap) {
         at.blk = 0;
-        if (++at.it == p.H * sq.M) {
+        if (++at.it == p.Hkv * G * sq.M) {
             ++at.b;
             at.it = 0;
         }
@@ -206,13 +212,13 @@ __device__ __forceinline__ CrossAt cross_place(const CrossParams& p, const Cross
 // The block's share [at[0], at[1]): every thread counts the blocks of a run of sequences.
 __device__ __forceinline__ void cross_share(const CrossParams& p, bool causal, CrossAt* at,
                                             long long* warp_sum) {
-    const int B = p.BH / p.H;
+    const int B = p.B;
     const int run = (B + kThreads - 1) / kThreads;
     const int b0 = min(B, (int)threadIdx.x * run), b1 = min(B, b0 + run);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const bool unit = !p.split && p.n_items <= (int)gridDim.x;
     auto count = [&](const CrossSeq& sq) -> long long {
-        return p.H * (unit ? (long long)sq.M : sq.before(sq.M));
+        return p.heads * (unit ? (long long)sq.M : sq.before(sq.M));
     };
     long long mine = 0;
     for (int b = b0; b < b1; ++b) mine += count(CrossSeq(p, b, causal));
@@ -259,33 +265,45 @@ __device__ __forceinline__ void cross_share(const CrossParams& p, bool causal, C
 // of a dense batch (d = 64 to 128).
 struct CrossWalk {
     const CrossAt* at;   // shared memory: the share's first place and its end
+    CrossSeq sq;         // of sequence b
     int b, it, blk;      // the item, and the first block of it
+    int kv, m, g;        // it, taken apart: K/V head, query-block pair, head (or heads) of the group
     bool begun = false;
 
-    __device__ __forceinline__ explicit CrossWalk(const CrossAt* a)
-        : at(a), b(a[0].b), it(a[0].it), blk(a[0].blk) {}
-
+    __device__ __forceinline__ CrossWalk(const CrossParams& p, const CrossAt* a, bool causal)
+        : at(a), sq(p, min(a[0].b, p.B - 1), causal), b(a[0].b), it(a[0].it), blk(a[0].blk) {
+        const int pair = it / p.G;
+        g = it - pair * p.G;
+        kv = sq.M > 0 ? pair / sq.M : 0;
+        m = pair - kv * sq.M;
+    }
     __device__ __forceinline__ bool next(const CrossParams& p, bool causal) {
         if (begun) {
             ++it;
             blk = 0;
+            if (++g == p.G) {
+                g = 0;
+                if (++m == sq.M) {
+                    m = 0;
+                    ++kv;
+                }
+            }
         }
         begun = true;
         for (;;) {
             if (b > at[1].b || (b == at[1].b && it > at[1].it)) return false;
             if (b == at[1].b && it == at[1].it) return at[1].blk > blk;
-            if (it < p.H * CrossSeq(p, b, causal).M) return true;
-            ++b;
-            it = 0;
+            if (sq.M > 0 && kv < p.Hkv) return true;
+            if (++b < p.B) sq = CrossSeq(p, b, causal);
+            it = kv = m = g = 0;
         }
     }
 };
 
 __device__ __forceinline__ CrossTile cross_tile(const CrossWalk& at, const CrossParams& p,
                                                 bool causal) {
-    const CrossSeq sq(p, at.b, causal);
-    const int G = p.H / p.Hkv;
-    const int m = at.it / G % sq.M, kv = at.it / G / sq.M, h = kv * G + at.it % G;
+    const CrossSeq& sq = at.sq;
+    const int m = at.m, h = (at.kv * p.G + at.g) * p.group;
     CrossTile w;
     w.tok0 = sq.tok0;
     w.len = sq.len;
@@ -293,14 +311,16 @@ __device__ __forceinline__ CrossTile cross_tile(const CrossWalk& at, const Cross
     w.klen = sq.klen;
     w.off = sq.klen - sq.len;
     w.q_z = p.cu_seqlens ? h : at.b * p.H + h;
-    w.kv_z = p.cu_seqlens ? kv : at.b * p.Hkv + kv;
-    w.row_base = m * kItemRows;
+    w.kv_z = p.cu_seqlens ? at.kv : at.b * p.Hkv + at.kv;
+    w.row_base = m << (p.row_log + 1);
     const int n = sq.blocks(m);
     const int lo = at.blk;
     const int hi = at.b == at.at[1].b && at.it == at.at[1].it ? at.at[1].blk : n;
     // The first tile's last row sees keys up to its own index + off.  A tile that sees
     // nothing of the segment keeps one block, which the masks empty.
-    const int n0 = causal ? min(n, max(2 * m + 1 + sq.q, 1)) : n;
+    const int n0 = !causal         ? n
+                   : p.group > 1 ? min(n, max(((1 << p.row_log) + w.off + kBN - 1) >> 7, 1))
+                                 : min(n, max(2 * m + 1 + sq.q, 1));
     w.lo = lo;
     w.n_kv[0] = max(lo + 1, min(n0, hi));
     w.n_kv[1] = hi;
@@ -342,7 +362,8 @@ struct RingReader {
 
 // Rows past a sequence's keys may hold anything: their scores are masked, and the softmax
 // of query tile 0 (of tile 1 where only that sees the block) clears V's rows.
-template <int D>
+// GROUP: p.group > 1 (a switch, as d = 64 takes 3 % longer when it is asked at run time).
+template <int D, bool GROUP>
 __global__ void __launch_bounds__(kThreads, 1)
 cross_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const CrossParams p) {
@@ -364,6 +385,7 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const WaitCtx wc{p.status, &abort_sh};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const bool causal = p.causal;
+    const int row_log = GROUP ? p.row_log : 7;
     cross_share(p, causal, share, warp_sum);
 
     if (threadIdx.x == 0) {
@@ -412,6 +434,8 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const int t = warp >> 2;                 // query tile of this group
         const int quarter = warp & 3;            // TMEM lane quarter
         const int rl = quarter * 32 + lane;      // row within the tile
+        // the query after the item's first that this is, and of which of the tile's heads
+        const int query = (t << row_log) + (rl & ((1 << row_log) - 1)), head = rl >> row_log;
         const uint32_t col_s = t ? Cfg::kColS1 : Cfg::kColS0;
         const uint32_t col_o = t ? Cfg::kColO1 : Cfg::kColO0;
         const uint32_t col_p = SEP ? (t ? Cfg::kColP1 : Cfg::kColP0) : col_s;
@@ -428,7 +452,7 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             const CrossTile& wt = items.tile();
             const int lo = wt.lo, n_kv = wt.n_kv[t];
             // the last key that this thread's row sees
-            const int last = min(causal ? wt.row_base + t * kBM + rl + wt.off : wt.klen, wt.klen - 1);
+            const int last = min(causal ? query + wt.row_base + wt.off : wt.klen, wt.klen - 1);
             float m2 = -CUDART_INF_F;   // running max, log2-scaled
             float l = 0.0f;
             for (int j = lo; j < n_kv; ++j) {
@@ -580,7 +604,7 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             for (int c0 = 1; c0 < D / 32; ++c0) asm volatile("" : FA_R32(ov[c0]) : : "memory");
             tc_fence_before();
             mbar_arrive(&bar_o_free[t]);
-            const int row = wt.row_base + t * kBM + rl, seg = wt.slot;
+            const int row = wt.row_base + query, seg = wt.slot;
             const bool valid = row < wt.len;
             // a row that sees no key (the exponentials of the FMA pipe are not quite 0);
             // scores of NaN, which the maximum passes over, leave l NaN
@@ -608,7 +632,7 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 }
                 continue;
             }
-            const size_t orow = ((size_t)wt.q_z * p.rows + wt.tok0 + (valid ? row : 0)) * D;
+            const size_t orow = ((size_t)(wt.q_z + head) * p.rows + wt.tok0 + (valid ? row : 0)) * D;
             if (valid) {
 #pragma unroll
                 for (int c0 = 0; c0 < D / 32; ++c0) {
@@ -628,7 +652,7 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         dst[q4] = w;
                     }
                 }
-                p.lse[(size_t)wt.q_z * p.rows + wt.tok0 + row] =
+                p.lse[(size_t)(wt.q_z + head) * p.rows + wt.tok0 + row] =
                     l != 0.0f ? (m2 + log2f(l)) * 0.69314718055994531f : -CUDART_INF_F;
             }
         }
@@ -640,7 +664,7 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             uint32_t g = 0;              // K blocks loaded so far (ring position)
             bool ok = true;
             // The next item goes into the ring once this one's first block is on its way.
-            CrossWalk walk(share);
+            CrossWalk walk(p, share, causal);
             uint32_t n = 0;   // items put into the ring
             CrossTile nxt;
             auto put = [&] {
@@ -693,7 +717,7 @@ cross_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     mbar_arrive_expect_tx(&bar_q[t], Cfg::kTileBytes);
                     for (int c = 0; c < Cfg::kChunks; ++c)
                         tma_load_3d(sQ + t * Cfg::kTileBytes + c * Cfg::kChunkBytes, &tm_q,
-                                    &bar_q[t], c * 64, wt.tok0 + wt.row_base + t * kBM, wt.q_z);
+                                    &bar_q[t], c * 64, wt.tok0 + wt.row_base + (t << row_log), wt.q_z);
                 }
                 if (!ok) break;
                 q_loaded = lt;
@@ -864,9 +888,9 @@ cross_join_kernel(const CrossParams p, int ctas) {
     const CrossAt at = p.part_at[c], prev = p.part_at[c - 1];
     if (at.blk == 0 || (prev.b == at.b && prev.it == at.it && prev.blk > 0)) return;
     const CrossSeq sq(p, at.b, p.causal);
-    const int G = p.H / p.Hkv;
-    const int h = at.it / G / sq.M * G + at.it % G;
-    const int row = at.it / G % sq.M * kItemRows + r;
+    const int G = p.G, rl = r % kBM, rows = 1 << p.row_log;
+    const int h = (at.it / G / sq.M * G + at.it % G) * p.group + (rl >> p.row_log);
+    const int row = (at.it / G % sq.M * 2 + r / kBM) * rows + (rl & (rows - 1));
     if (row >= sq.len) return;
     int last = c;
     while (last + 1 < ctas) {
@@ -910,10 +934,10 @@ cross_join_kernel(const CrossParams p, int ctas) {
             sum == 0.0f ? -CUDART_INF_F : (m + log2f(sum)) * 0.69314718055994531f;
 }
 
-template <int D>
+template <int D, bool GROUP>
 cudaError_t launch_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                      const CrossParams& p, int ctas, cudaStream_t stream) {
-    auto kern = cross_fwd_kernel<D>;
+    auto kern = cross_fwd_kernel<D, GROUP>;
     static int configured_device = -1;   // attribute is per device; cheap to repeat
     int dev = 0;
     cudaGetDevice(&dev);
@@ -937,6 +961,13 @@ cudaError_t launch_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtenso
                       ctas);
 }
 
+// Query heads a tile: all of a group where their rows fit into two tiles (14 packed sequences
+// of 3 queries to 14092 keys, H16 Hkv2, d = 128: 194 us with a head a tile, 49 so).
+int heads_a_tile(const Shape& s) {
+    const int G = s.H / s.Hkv;
+    return kBM % G == 0 && (long long)G * s.N <= kItemRows ? G : 1;
+}
+
 // Keys of another length: the most CTAs that a split call has.
 long long split_ctas(const Shape& s) {
     const long long items = (long long)s.B * s.H * ((s.N + kItemRows - 1) / kItemRows);
@@ -949,19 +980,22 @@ long long split_ctas(const Shape& s) {
 // counted in full, packed ones as equally long).
 int cross_ctas(const Shape& s, bool& split) {
     const int sms = std::min(device_sm_count() > 0 ? device_sm_count() : 148, kMaxCtas);
+    const int group = heads_a_tile(s), heads = s.H / group, pair = kItemRows / group;
     const long long rows = s.cu_seqlens ? s.total / s.B : s.N;
     const long long keys = s.cu_k ? std::min(s.total_k / s.B, s.Nk) : s.Nk;
-    const long long M = std::max(1ll, (rows + kItemRows - 1) / kItemRows);
+    const long long M = std::max(1ll, (rows + pair - 1) / pair);
     const long long n = (keys + kBN - 1) / kBN, q = (s.Nk - s.N) / kBN;
     double blocks = 0.0;   // of the pairs of one head
     for (long long m = 0; m < M; ++m)
-        blocks += kItemCost + (s.causal ? std::min(std::max(2 * (m + 1) + q, 1ll), n) : n);
-    const double items = (double)s.B * s.H * M, share = (double)s.B * s.H * blocks / sms;
+        blocks += kItemCost + (s.causal && group == 1 ? std::min(std::max(2 * (m + 1) + q, 1ll), n) : n);
+    const double items = (double)s.B * heads * M, share = (double)s.B * heads * blocks / sms;
     const double longest = (s.Nk + kBN - 1) / kBN + kItemCost;
     const double whole = std::max(longest, std::ceil(items / sms) * blocks / M);
     split = split_ctas(s) > 0 && std::max(share, (double)kMinBlocks) + kJoinCost < whole;
-    const long long most = (long long)s.B * s.H * ((s.N + kItemRows - 1) / kItemRows);
-    return (int)std::min<long long>(sms, split ? split_ctas(s) : most);
+    const long long most = (long long)s.B * heads * ((s.N + pair - 1) / pair);
+    const long long keys_most = most * ((s.Nk + kBN - 1) / kBN);
+    return (int)std::min<long long>(
+        sms, split ? std::min(split_ctas(s), (keys_most + kMinBlocks - 1) / kMinBlocks) : most);
 }
 
 }  // namespace
@@ -979,7 +1013,8 @@ cudaError_t launch_fwd_cross(const Shape& s, const void* q, const void* k, const
     const bool packed = s.cu_seqlens != nullptr;
     const int rows = packed ? s.total : s.N, krows = packed ? s.total_k : s.Nk;
     CUtensorMap tq, tk, tv;
-    if (!make_tmap_bf16_3d(&tq, q, s.d, rows, packed ? s.H : s.B * s.H, kBM) ||
+    const int group = heads_a_tile(s);
+    if (!make_tmap_bf16_3d(&tq, q, s.d, rows, packed ? s.H : s.B * s.H, kBM / group, group) ||
         !make_tmap_bf16_3d(&tk, k, s.d, krows, packed ? s.Hkv : s.B * s.Hkv, kBN) ||
         !make_tmap_bf16_3d(&tv, v, s.d, krows, packed ? s.Hkv : s.B * s.Hkv, kBN))
         return cudaErrorInvalidValue;
@@ -989,8 +1024,13 @@ cudaError_t launch_fwd_cross(const Shape& s, const void* q, const void* k, const
     p.H = s.H;
     p.Hkv = s.Hkv;
     p.N = s.N;
-    p.BH = s.B * s.H;
-    p.n_items = (s.N + kItemRows - 1) / kItemRows * p.BH;
+    p.group = group;
+    p.B = s.B;
+    p.G = s.H / s.Hkv / group;
+    p.heads = s.H / group;
+    p.row_log = 7;
+    while (1 << p.row_log > kBM / group) --p.row_log;
+    p.n_items = (s.N + kItemRows / group - 1) / (kItemRows / group) * s.B * p.heads;
     p.causal = s.causal;
     p.rows = rows;
     p.cu_seqlens = s.cu_seqlens;
@@ -1006,8 +1046,11 @@ cudaError_t launch_fwd_cross(const Shape& s, const void* q, const void* k, const
     p.part_o = static_cast<float4*>(workspace);
     p.part_lse = static_cast<float*>(workspace) + (size_t)2 * ctas * kItemRows * s.d;
     p.part_at = reinterpret_cast<CrossAt*>(p.part_lse + (size_t)2 * ctas * kItemRows);
-    return s.d == 128 ? launch_t<128>(tq, tk, tv, p, ctas, stream)
-                      : launch_t<64>(tq, tk, tv, p, ctas, stream);
+    if (s.d == 128)
+        return group > 1 ? launch_t<128, true>(tq, tk, tv, p, ctas, stream)
+                         : launch_t<128, false>(tq, tk, tv, p, ctas, stream);
+    return group > 1 ? launch_t<64, true>(tq, tk, tv, p, ctas, stream)
+                     : launch_t<64, false>(tq, tk, tv, p, ctas, stream);
 }
 
 }  // namespace fa

@@ -134,10 +134,10 @@ cudaError_t launch_exp2_check(const float* x, float* y_fma, float* y_ex2, int n,
 cudaError_t launch_ex2_rate(float* out, int blocks, int iters, cudaStream_t stream);
 
 // Tensor-map encoding through the driver entry point (no libcuda link).
-// Builds a 3-D map over a bf16 tensor [outer][rows][d] with a {64, box_rows, 1}
+// Builds a 3-D map over a bf16 tensor [outer][rows][d] with a {64, box_rows, box_outer}
 // box and 128-byte swizzle.  Returns false on failure.
 bool make_tmap_bf16_3d(CUtensorMap* map, const void* base, int d, int rows, int outer,
-                       int box_rows);
+                       int box_rows, int box_outer = 1);
 
 // 2-D map over an fp32 matrix [rows][inner] with a {box_inner, box_rows} box
 // and 128-byte swizzle (box_inner * 4 <= 128).

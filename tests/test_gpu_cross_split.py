@@ -152,3 +152,38 @@ def test_workspace_too_small():
                         False, 0.1)
     torch.cuda.synchronize()
     assert o.isnan().all()
+
+
+@pytest.mark.parametrize("causal", [False, True], ids=["full", "causal"])
+@pytest.mark.parametrize("H,Hkv,d,nq,nk", [
+    (8, 1, 64, [3, 1, 0, 32], [500, 40, 9, 0]), (8, 2, 128, [5, 64, 33], [300, 9000, 64]),
+    (16, 1, 128, [16, 2, 9], [5000, 1, 130]), (128, 1, 64, [1, 2], [200, 700]),
+    (4, 2, 64, [128, 65, 64, 1], [128, 64, 1000, 0]), (32, 8, 128, [1] * 40, [90 * i for i in range(40)]),
+    (12, 2, 64, [5, 20], [300, 2000]), (256, 1, 64, [1, 1], [300, 2000]), (8, 2, 64, [65, 3], [300, 2000]),
+])
+def test_heads_of_a_group_in_one_tile(H, Hkv, d, nq, nk, causal):
+    """Packed sequences so short that the query heads of a key head fill two tiles together (and
+    some that just do not)."""
+    q, k, v, _, cu_q, cu_k = packed(H, Hkv, d, nq, nk, 2)
+    mq, mk, scale = max(nq), max(nk), d ** -0.5
+    o, lse = used(q, q[..., 0].float())
+    big, ws = fenced(fa.fa_fwd_cross_workspace_size(len(nq), H, Hkv, mq, mk, d))
+    fa.fa_fwd_cross_varlen(q, k, v, o, lse, ws, cu_q, cu_k, mq, mk, causal, scale)
+    assert fa.fa_device_status() == 0
+    assert (big[-4096:] == 0xFF).all()
+    assert o[:, sum(nq):].isnan().all() and lse[:, sum(nq):].isnan().all()
+    for a, b in zip(parts(nq), parts(nk)):
+        want, wl, room, lroom = plain.forward(*(t.double() for t in (q[:, a], k[:, b], v[:, b])),
+                                              causal, scale)
+        plain.inside("o", o[:, a], want, room)
+        plain.inside("lse", lse[:, a], wl, lroom)
+
+
+@pytest.mark.parametrize("B,H,Hkv,d,Nq,Nk,lens", [
+    (2, 8, 1, 128, 32, 3000, [3000, 20]), (3, 16, 4, 64, 7, 200, [200, 3, 0]),
+    (1, 32, 8, 128, 64, 5000, [4999]), (5, 8, 4, 64, 100, 130, [130, 99, 1, 0, 64]),
+])
+def test_heads_of_a_group_in_one_tile_under_the_mask(B, H, Hkv, d, Nq, Nk, lens):
+    q, k, v, _ = padded(B, H, Hkv, d, Nq, Nk, lens, seed=17)
+    o, lse = forward(q, k, v, i32(lens), True, d ** -0.5)
+    check_forward(q, k, v, o, lse, lens, True, d ** -0.5)
