@@ -167,7 +167,7 @@ fa_kv_reserve_kernel(const __grid_constant__ TablesParams p, bool alone) {
     s.n_free = min(max(*p.n_free, 0), p.n_pages);
     if (tid == 0) total_sh = 0;
     const int most = p.max_pages << p.ps_shift;
-    int pages = 0, rows = 0;                      // of the sequences before this round's
+    int pages = 0, rows = 0;                      // of the sequences of the passes before
     for (int base = 0; base < p.B; base += nt) {
         const int b = base + tid;
         int len = 0, n = 0, need = 0;
