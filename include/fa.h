@@ -695,7 +695,8 @@ FA_API fa_status fa_fwd_cross(const void* q, const void* k, const void* v, void*
 
 /*
  * Its gradients, from o and lse as fa_fwd_cross() wrote them.  dk and dv are the same
- * bit for bit on every call, dq as in fa_bwd().  Three launches.
+ * bit for bit on every call, dq as in fa_bwd().  A query's NaN reaches its row of dq and
+ * the dk and dv of the keys that it may see (or of whole blocks of them).  Three launches.
  */
 FA_API size_t fa_bwd_cross_workspace_size(int B, int H, int Hkv, int Nq, int Nk, int d);
 FA_API fa_status fa_bwd_cross(const void* q, const void* k, const void* v, const void* o,

@@ -83,3 +83,26 @@ def test_heads_of_a_group_are_one_without_the_mask(d):
         grads = fa.attention_cross_backward(q, k, v, o, lse, dout, kv_lens)
         check_backward(q, k, v, o, lse, dout, grads, n, False, d ** -0.5)
     assert fa.fa_device_status() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Nq,Nk", [(70, 300), (1500, 100)])
+def test_a_nan_query_spoils_its_row_of_dq_only(d, Nq, Nk):
+    """dQ of the other rows, and dK and dV of the other heads, are as without it."""
+    q, k, v, dout = padded(1, 2, 2, d, Nq, Nk, [Nk], seed=63)
+    grads = []
+    for x in (q, q.clone()):
+        if grads:
+            x[0, 1, 3, 5] = float("nan")
+        o, lse = fa.attention_cross(x, k, v)
+        grads.append(fa.attention_cross_backward(x, k, v, o, lse, dout))
+        if len(grads) == 1:
+            check_backward(x, k, v, o, lse, dout, grads[0], [Nk], False, d ** -0.5)
+    (dq, dk, dv), (dq2, dk2, dv2) = grads
+    assert dq2[0, 1, 3].isnan().all()
+    dq2[0, 1, 3] = dq[0, 1, 3]
+    assert not dq2.isnan().any()
+    # (the same terms added in another order, each row rounded to bf16: 2^-8 of itself, twice)
+    assert torch.allclose(dq2.float(), dq.float(), rtol=2 ** -6, atol=1e-3 * float(dq.abs().max()))
+    assert torch.equal(dk2[0, 0], dk[0, 0]) and torch.equal(dv2[0, 0], dv[0, 0])
+    assert dk2[0, 1].isnan().all() and dv2[0, 1].isnan().all()
