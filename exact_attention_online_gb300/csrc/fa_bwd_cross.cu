@@ -690,8 +690,9 @@ fa_bwd_cross64_kernel(const __grid_constant__ CUtensorMap tm_q,
 
 // dq = bf16(scale * accumulator), sixteen values a thread, the rows inside their sequence;
 // and zeros in dK and dV where the kernel above had no work: the key blocks past a padded
-// sequence's keys and those that no query sees (one block of threads each).  Of 16
-// columns the accumulator has 2 b, 2 b + 1, 8 + 2 b, 9 + 2 b at 4 b.
+// sequence's keys and those that no query sees (one block of threads each); where key blocks
+// went to several CTAs, their parts are added here.  Of 16 columns the accumulator has 2 b,
+// 2 b + 1, 8 + 2 b, 9 + 2 b at 4 b.
 __global__ void __launch_bounds__(256)
 fa_bwd_cross64_dq_kernel(__nv_bfloat16* __restrict__ dq, long long n_rows,
                          const BwdParams p) {
